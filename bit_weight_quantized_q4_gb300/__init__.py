@@ -9,8 +9,10 @@ no CPU fallback: if the library is missing the calls raise.
 Entry points (same names as the C ABI in ``include/q4gemv.h``):
 ``q4_gemv``, ``q4_nrm_gemv``, ``q4_dual_gemv``, ``q4_gus_nrm``,
 ``q4_res_gemv``, ``q4_argmax``, ``q4_group_sums``, ``q4_pack_half``,
-``q4_gemv_half``, ``q4_gemm``, ``q4_decode_step``, ``q4_attn_decode``; plus ``Q4Weight``
-for repacking host weights into the device layout and ``rope_table``.
+``q4_gemv_half``, ``q4_gemm``, ``q4_decode_step``, ``q4_attn_decode``,
+``q4_kv_append``, ``q4_attn_prefill``, ``q4_attn_paged``, ``q4_logprobs``; plus ``Q4Weight``
+for repacking host weights into the device layout, ``KVPages`` (a paged KV cache)
+and ``rope_table``.
 """
 from __future__ import annotations
 
@@ -60,6 +62,13 @@ class _CStepAttention(ctypes.Structure):
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class _CKvPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("nseq", ctypes.c_int32),
+                ("width", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -78,7 +87,7 @@ def lib() -> ctypes.CDLL:
                                "bit_weight_quantized_q4_gb300.build())")
         L = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-        W = ctypes.POINTER(_CWeight)
+        W, KV = ctypes.POINTER(_CWeight), ctypes.POINTER(_CKvPages)
         sig = {
             "q4_packed_bytes": (SZ, [I32, I32, I32]),
             "q4_weight_bytes": (SZ, [I32, I32, I32]),
@@ -116,6 +125,12 @@ def lib() -> ctypes.CDLL:
             "q4_gemm": (I32, [W, P, I32, P, I32, P, SZ, P]),
             "q4_attn_decode": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, F, P, P, P, P, SZ, P]),
             "q4_rope_table": (I32, [I32, I32, ctypes.c_double, P, P]),
+            "q4_kv_append": (I32, [KV, P, P, P, I32, P, P, I32, P, P, I32, P, P]),
+            "q4_attn_prefill_workspace_bytes": (SZ, [KV, I32, I32]),
+            "q4_attn_prefill": (I32, [KV, P, I32, P, P, I32, I32, F, P, P, SZ, P]),
+            "q4_attn_paged_workspace_bytes": (SZ, [KV, I32]),
+            "q4_attn_paged": (I32, [KV, P, P, P, P, I32, I32, F, P, P, I32, P, P, SZ, P]),
+            "q4_logprobs": (I32, [P, I32, I32, P, I32, P, P, P, P, P]),
             "q4_status_str": (ctypes.c_char_p, [I32]),
         }
         for name, (res, args) in sig.items():
@@ -719,3 +734,228 @@ def q4_gemm(W: Q4Weight, x, accumulate: bool = False, out=None, workspace=None):
     _check(lib().q4_gemm(W.cref(), x.data_ptr(), nb, out.data_ptr(), int(bool(accumulate)), workspace.data_ptr(),
                          workspace.numel(), _stream()), "q4_gemm")
     return out
+
+
+# ---------------------------------------------------------------- paged KV cache
+
+def _stream_of(device):
+    """The current stream of the tensors' device (which need not be the
+    current device: the calls below make it current for their launch)."""
+    return _torch().cuda.current_stream(device).cuda_stream
+
+
+def _ints(t, name, numel, device):
+    return _dev_buf(t, name, _torch().int32, (numel,), device).data_ptr()
+
+
+class KVPages:
+    """A paged KV cache that several sequences share: ``k`` and ``v``
+    ``[num_pages, kv_heads, page_size, head_dim]`` CUDA tensors of float32,
+    float16 or bfloat16, ``table`` ``[nseq, width]`` int32: position p of
+    sequence b lies in page ``table[b, p // page_size]``.  The caller owns the
+    tensors and may change the table's values between calls; a contiguous cache
+    ``[kv_heads, max_seq, head_dim]`` is ``KVPages(k[None], v[None], table)``
+    with ``table = [[0]]``.  Keeps the tensors alive."""
+
+    def __init__(self, k, v, table):
+        torch = _torch()
+        kinds = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+        if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dtype not in kinds:
+            raise TypeError("k pages must be a CUDA float32, float16 or bfloat16 tensor")
+        if k.dim() != 4 or 0 in k.shape:
+            raise ValueError("k pages must be [num_pages, kv_heads, page_size, head_dim]")
+        self.k = _dev_buf(k, "k pages", k.dtype, k.shape, k.device)
+        self.v = _dev_buf(v, "v pages", k.dtype, k.shape, k.device)
+        if not isinstance(table, torch.Tensor) or table.dim() != 2 or 0 in table.shape:
+            raise ValueError("table must be an int32 tensor [nseq, width]")
+        self.table = _dev_buf(table, "table", torch.int32, table.shape, k.device)
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = (int(x) for x in k.shape)
+        self.nseq, self.width = int(table.shape[0]), int(table.shape[1])
+        self.dtype, self.device = k.dtype, k.device
+        self._c = _CKvPages(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), kinds[k.dtype],
+                            self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.nseq, self.width)
+
+    def cref(self):
+        return ctypes.byref(self._c)
+
+
+def _pages(pages):
+    if not isinstance(pages, KVPages):
+        raise TypeError("pages must be a KVPages")
+    return pages
+
+
+def _rope_args(rope, head_dim, device):
+    if rope is None:
+        return None, None, 0
+    cos_t, sin_t = rope
+    torch = _torch()
+    if not isinstance(cos_t, torch.Tensor) or cos_t.dim() != 2 or cos_t.shape[1] != head_dim // 2:
+        raise ValueError("rope tables must be [positions, head_dim/2]")
+    n = int(cos_t.shape[0])
+    return (_dev_buf(cos_t, "rope cos", torch.float32, (n, head_dim // 2), device).data_ptr(),
+            _dev_buf(sin_t, "rope sin", torch.float32, (n, head_dim // 2), device).data_ptr(), n)
+
+
+def _heads3(t, name, dtype, head_dim, device):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != head_dim:
+        raise ValueError("%s must be [rows, heads, %d]" % (name, head_dim))
+    return _dev_buf(t, name, dtype, t.shape, device)
+
+
+def _apart(out, others):
+    """out must not share memory with the inputs (it is written while they are read)."""
+    if out.numel() == 0:
+        return
+    a, b = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in others:
+        if t is not None and t.data_ptr() < b and a < t.data_ptr() + t.numel() * t.element_size():
+            raise ValueError("out must not overlap the inputs")
+
+
+def q4_kv_append(k, v, pages: KVPages, cu_rows, start=None, q=None, rope=None, q_out=None):
+    """Write packed rows ``k``, ``v`` ``[rows, kv_heads, D]`` (float32) into the
+    pages of their sequences: rows ``cu_rows[b] .. cu_rows[b+1]`` belong to
+    sequence b, at positions ``start[b] ..`` (``start`` None: zeros); ``rope``
+    an optional (cos, sin) pair of ``[positions, D/2]`` tables that rotate k.
+    With ``q`` ``[rows, H, D]`` (float32) returns it rotated and in the cache's
+    type (``q_out``), the form ``q4_attn_prefill`` takes; else returns None."""
+    torch = _torch()
+    pages = _pages(pages)
+    dev, D = pages.device, pages.head_dim
+    k = _heads3(k, "k", torch.float32, D, dev)
+    rows = int(k.shape[0])
+    _dev_buf(k, "k", torch.float32, (rows, pages.kv_heads, D), dev)
+    _dev_buf(v, "v", torch.float32, (rows, pages.kv_heads, D), dev)
+    cu = _ints(cu_rows, "cu_rows", pages.nseq + 1, dev)
+    st = None if start is None else _ints(start, "start", pages.nseq, dev)
+    cp, sp, rope_rows = _rope_args(rope, D, dev)
+    H = 0
+    if q is not None:
+        q = _heads3(q, "q", torch.float32, D, dev)
+        H = int(q.shape[1])
+        if int(q.shape[0]) != rows:
+            raise ValueError("q has %d rows, k %d" % (int(q.shape[0]), rows))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=pages.dtype, device=dev)
+        _dev_buf(q_out, "q_out", pages.dtype, q.shape, dev)
+        _apart(q_out, (q, k, v))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    with torch.cuda.device(dev):
+        _check(lib().q4_kv_append(pages.cref(), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), rows,
+                                  cu, st, H, cp, sp, rope_rows, None if q is None else q_out.data_ptr(),
+                                  _stream_of(dev)), "q4_kv_append")
+    return q_out
+
+
+def q4_attn_prefill_workspace(pages: KVPages, rows: int, heads: int):
+    """A workspace for ``q4_attn_prefill`` with up to ``rows`` rows (None where
+    the call needs none)."""
+    n = int(lib().q4_attn_prefill_workspace_bytes(_pages(pages).cref(), int(rows), int(heads)))
+    return _torch().empty(n, dtype=_torch().uint8, device=pages.device) if n else None
+
+
+def q4_attn_prefill(q, pages: KVPages, cu_rows, start=None, window: int = 0, scale=None, out=None, workspace=None):
+    """Causal attention of packed prompt rows over the pages of their
+    sequences: ``q`` ``[rows, H, D]`` of the cache's type (``q4_kv_append``
+    returns it), row ``cu_rows[b] + i`` at position ``start[b] + i`` of sequence
+    b, whose keys and values are in the pages already.  Returns ``out``
+    ``[rows, H, D]`` of the same type; ``scale`` defaults to 1/sqrt(D)."""
+    torch = _torch()
+    pages = _pages(pages)
+    dev, D = pages.device, pages.head_dim
+    q = _heads3(q, "q", pages.dtype, D, dev)
+    rows, H = int(q.shape[0]), int(q.shape[1])
+    cu = _ints(cu_rows, "cu_rows", pages.nseq + 1, dev)
+    st = None if start is None else _ints(start, "start", pages.nseq, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    _dev_buf(out, "out", pages.dtype, q.shape, dev)
+    _apart(out, (q, pages.k, pages.v))
+    if workspace is None:
+        workspace = q4_attn_prefill_workspace(pages, rows, H)
+    else:
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=int(
+            lib().q4_attn_prefill_workspace_bytes(pages.cref(), rows, H)))
+    with torch.cuda.device(dev):
+        _check(lib().q4_attn_prefill(pages.cref(), q.data_ptr(), rows, cu, st, H, int(window),
+                                     1.0 / float(D) ** 0.5 if scale is None else float(scale), out.data_ptr(),
+                                     None if workspace is None else workspace.data_ptr(),
+                                     0 if workspace is None else workspace.numel(), _stream_of(dev)),
+               "q4_attn_prefill")
+    return out
+
+
+def q4_attn_paged_workspace(pages: KVPages, heads: int):
+    """A (zero-filled) workspace for ``q4_attn_paged``; calls that may run at
+    the same time, captured ones too, need one each."""
+    n = int(lib().q4_attn_paged_workspace_bytes(_pages(pages).cref(), int(heads)))
+    return _torch().zeros(max(16, n), dtype=_torch().uint8, device=pages.device)
+
+
+def q4_attn_paged(q, k_new, v_new, pages: KVPages, positions, window: int = 0, scale=None, rope=None, out=None,
+                  workspace=None):
+    """Attention of one new token per sequence over its pages: ``q``
+    ``[nseq, H, D]``, ``k_new`` / ``v_new`` ``[nseq, kv_heads, D]`` (float32)
+    at ``positions`` (int32 ``[nseq]``; negative: an idle row, whose out is
+    zero).  RoPE of q and k_new (with ``rope`` tables), append, attention.
+    Returns out ``[nseq, H, D]`` float32; ``scale`` defaults to 1/sqrt(D)."""
+    torch = _torch()
+    pages = _pages(pages)
+    dev, D, n = pages.device, pages.head_dim, pages.nseq
+    q = _heads3(q, "q", torch.float32, D, dev)
+    H = int(q.shape[1])
+    if int(q.shape[0]) != n:
+        raise ValueError("q has %d rows, the table %d sequences" % (int(q.shape[0]), n))
+    _dev_buf(k_new, "k_new", torch.float32, (n, pages.kv_heads, D), dev)
+    _dev_buf(v_new, "v_new", torch.float32, (n, pages.kv_heads, D), dev)
+    pos = _ints(positions, "positions", n, dev)
+    cp, sp, rope_rows = _rope_args(rope, D, dev)
+    if out is None:
+        out = torch.empty((n, H, D), dtype=torch.float32, device=dev)
+    _dev_buf(out, "out", torch.float32, (n, H, D), dev)
+    _apart(out, (q, k_new, v_new, pages.k, pages.v))
+    if workspace is None:  # zero-filled: its counters start at zero
+        workspace = q4_attn_paged_workspace(pages, H)
+    else:
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=int(
+            lib().q4_attn_paged_workspace_bytes(pages.cref(), H)))
+    with torch.cuda.device(dev):
+        _check(lib().q4_attn_paged(pages.cref(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), pos, H, int(window),
+                                   1.0 / float(D) ** 0.5 if scale is None else float(scale), cp, sp, rope_rows,
+                                   out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev)),
+               "q4_attn_paged")
+    return out
+
+
+# ---------------------------------------------------------------- sampling
+
+def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
+    """Log probabilities from logit rows ``[rows, n]`` (float32, as
+    ``q4_argmax(..., want_logits=True)`` returns them).  Returns ``(logprob of
+    tokens int32[rows] or None, entropy [rows] or None, top log probabilities
+    [rows, min(top, n)], their indices int32)``; ties go to the lowest index,
+    a negative token's log probability is 0 (a row that is not scored)."""
+    torch = _torch()
+    logits = _dev_f32(logits, "logits")
+    if logits.dim() != 2 or logits.shape[1] == 0:
+        raise ValueError("logits must be [rows, n]")
+    dev = logits.device
+    rows, n = (int(x) for x in logits.shape)
+    k = min(int(top), n)
+    f32 = dict(dtype=torch.float32, device=dev)
+    lp = tok = ent = None
+    if tokens is not None:
+        tok = _ints(tokens, "tokens", rows, dev)
+        lp = torch.empty(rows, **f32)
+    if entropy:
+        ent = torch.empty(rows, **f32)
+    val = torch.empty((rows, max(0, k)), **f32)
+    idx = torch.empty((rows, max(0, k)), dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().q4_logprobs(logits.data_ptr(), rows, n, tok, k, None if lp is None else lp.data_ptr(),
+                                 None if ent is None else ent.data_ptr(), val.data_ptr() if k > 0 else None,
+                                 idx.data_ptr() if k > 0 else None, _stream_of(dev)), "q4_logprobs")
+    return lp, ent, val, idx

@@ -887,6 +887,222 @@ extern "C" q4_status q4_attn_decode(const float *q, const float *k_new, const fl
     return Q4_OK;
 }
 
+// ---------------------------------------------------------------- paged cache
+
+namespace {
+constexpr int kMaxPagedGroup = 16;  // query heads of one kv head
+constexpr int kMaxPagedCtas = 512;  // bound on the CTAs of a paged attention launch (its workspace slots)
+
+inline bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
+q4_status check_ints(const int32_t *p) {
+    if (!p) return Q4_ERR_NULL;
+    return aligned4(p) ? Q4_OK : Q4_ERR_ALIGN;
+}
+
+// geometry alone (what a workspace size needs), then the pointers
+q4_status check_pages_shape(const q4_kv_pages *c) {
+    if (!c) return Q4_ERR_NULL;
+    if (c->dtype < Q4_T_F32 || c->dtype > Q4_T_BF16 || (c->head_dim != 64 && c->head_dim != 128))
+        return Q4_ERR_UNSUPPORTED;
+    if (c->num_pages < 1 || c->page_size < 1 || c->page_size > (1 << 24) || c->kv_heads < 1 || c->kv_heads > 1024 ||
+        c->nseq < 1 || c->nseq > q4::kMaxSeqs || c->width < 1)
+        return Q4_ERR_SHAPE;
+    if (c->page_size % 16 != 0 && c->width != 1) return Q4_ERR_SHAPE;
+    if ((long long)c->width * c->page_size > (1ll << 30)) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+q4_status check_pages(const q4_kv_pages *c) {
+    Q4_TRY(check_pages_shape(c));
+    Q4_TRY(check_act(c->k));
+    Q4_TRY(check_act(c->v));
+    return check_ints(c->table);
+}
+// query heads: whole groups of 1..16 per kv head
+q4_status check_heads(const q4_kv_pages *c, int32_t H) {
+    if (H < c->kv_heads || H % c->kv_heads != 0) return Q4_ERR_SHAPE;
+    return H / c->kv_heads <= kMaxPagedGroup ? Q4_OK : Q4_ERR_UNSUPPORTED;
+}
+q4_status check_rope(const float *rope_cos, const float *rope_sin, int32_t rope_rows) {
+    if ((rope_cos == nullptr) != (rope_sin == nullptr)) return Q4_ERR_NULL;
+    if (!rope_cos) return Q4_OK;
+    Q4_TRY(check_act(rope_cos));
+    Q4_TRY(check_act(rope_sin));
+    return rope_rows >= 1 ? Q4_OK : Q4_ERR_SHAPE;
+}
+q4::PagedKv paged_view(const q4_kv_pages *c) {
+    return q4::PagedKv{c->k, c->v, c->table, c->num_pages, c->page_size, c->kv_heads, c->nseq, c->width};
+}
+// per (sequence, kv head) counters at the start of the paged workspace
+inline size_t paged_count_bytes(const q4_kv_pages *c) {
+    return ((size_t)c->nseq * c->kv_heads * sizeof(int) + 15) / 16 * 16;
+}
+}  // namespace
+
+extern "C" q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k, const float *v,
+                                  int32_t rows, const int32_t *cu_rows, const int32_t *start, int32_t H,
+                                  const float *rope_cos, const float *rope_sin, int32_t rope_rows, void *q_out,
+                                  cudaStream_t stream) {
+    Q4_TRY(check_pages(pages));
+    if (rows < 0 || rows > (1 << 24)) return Q4_ERR_SHAPE;
+    if (q) Q4_TRY(check_heads(pages, H));
+    Q4_TRY(check_rope(rope_cos, rope_sin, rope_rows));
+    if (rows == 0) return Q4_OK;
+    Q4_TRY(check_act(k));
+    Q4_TRY(check_act(v));
+    if (q) {
+        Q4_TRY(check_act(q));
+        Q4_TRY(check_act(q_out));
+    }
+    Q4_TRY(check_ints(cu_rows));
+    if (start && !aligned4(start)) return Q4_ERR_ALIGN;
+    q4::AppendParams p{};
+    p.kv = paged_view(pages);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.cu = cu_rows;
+    p.start = start;
+    p.rope_cos = rope_cos;
+    p.rope_sin = rope_sin;
+    p.q_out = q_out;
+    p.rows = rows;
+    p.H = H;
+    p.D = pages->head_dim;
+    p.rope_rows = rope_rows;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    cudaGetLastError();
+    if (q4::launch_append(p, pages->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
+extern "C" size_t q4_attn_prefill_workspace_bytes(const q4_kv_pages *pages, int32_t rows, int32_t H) {
+    if (check_pages_shape(pages) != Q4_OK || check_heads(pages, H) != Q4_OK || rows < 0 || rows > (1 << 24)) return 0;
+    return 0;
+}
+
+extern "C" q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows, const int32_t *cu_rows,
+                                     const int32_t *start, int32_t H, int32_t window, float scale, void *out,
+                                     void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    Q4_TRY(check_pages(pages));
+    Q4_TRY(check_heads(pages, H));
+    if (rows < 0 || rows > (1 << 24) || window < 0) return Q4_ERR_SHAPE;
+    if (rows == 0) return Q4_OK;
+    Q4_TRY(check_act(q));
+    Q4_TRY(check_act(out));
+    Q4_TRY(check_ints(cu_rows));
+    if (start && !aligned4(start)) return Q4_ERR_ALIGN;
+    const size_t need = q4_attn_prefill_workspace_bytes(pages, rows, H);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return Q4_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return Q4_ERR_ALIGN;
+    }
+    q4::PrefillParams p{};
+    p.kv = paged_view(pages);
+    p.q = q;
+    p.out = out;
+    p.cu = cu_rows;
+    p.start = start;
+    p.rows = rows;
+    p.H = H;
+    p.D = pages->head_dim;
+    p.window = window;
+    p.scale = scale;
+    p.ws = (uint8_t *)workspace;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    p.wait_cycles = g_wait_cycles;
+    p.extra_tx = g_extra_tx;
+    cudaGetLastError();
+    if (q4::launch_prefill(p, pages->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
+extern "C" size_t q4_attn_paged_workspace_bytes(const q4_kv_pages *pages, int32_t H) {
+    if (check_pages_shape(pages) != Q4_OK || check_heads(pages, H) != Q4_OK) return 0;
+    return paged_count_bytes(pages) + (size_t)kMaxPagedCtas * 2 *
+                                          q4::paged_attn_slot_floats(pages->head_dim, H / pages->kv_heads) *
+                                          sizeof(float);
+}
+
+extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k_new, const float *v_new,
+                                   const int32_t *positions, int32_t H, int32_t window, float scale,
+                                   const float *rope_cos, const float *rope_sin, int32_t rope_rows, float *out,
+                                   void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    Q4_TRY(check_pages(pages));
+    Q4_TRY(check_heads(pages, H));
+    Q4_TRY(check_act(q));
+    Q4_TRY(check_act(k_new));
+    Q4_TRY(check_act(v_new));
+    Q4_TRY(check_ints(positions));
+    Q4_TRY(check_rope(rope_cos, rope_sin, rope_rows));
+    Q4_TRY(check_act(out));
+    if (window < 0) return Q4_ERR_SHAPE;
+    if (!workspace || workspace_bytes < q4_attn_paged_workspace_bytes(pages, H)) return Q4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q4_ERR_ALIGN;
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
+    const int G = H / pages->kv_heads;
+    q4::PagedAttnParams p{};
+    p.kv = paged_view(pages);
+    p.q = q;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.positions = positions;
+    p.rope_cos = rope_cos;
+    p.rope_sin = rope_sin;
+    p.out = out;
+    p.count = (int *)workspace;
+    p.part = (float *)((char *)workspace + paged_count_bytes(pages));
+    p.H = H;
+    p.D = pages->head_dim;
+    p.window = window;
+    p.rope_rows = rope_rows;
+    p.scale = scale;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    // one CTA per slot of the device, no more than there can be units
+    const long long cap = (long long)pages->width * pages->page_size;
+    const long long units = (long long)pages->nseq * pages->kv_heads * ((cap + 127) / 128);
+    const int ctas = (int)std::min<long long>(
+        std::min(q4::paged_attn_ctas(pages->dtype, pages->head_dim, G, sms), kMaxPagedCtas), units);
+    cudaGetLastError();
+    if (q4::launch_paged_attn(p, pages->dtype, ctas, stream) != 0 || cudaGetLastError() != cudaSuccess)
+        return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
+// ---------------------------------------------------------------- sampling
+
+extern "C" q4_status q4_logprobs(const float *logits, int32_t rows, int32_t n, const int32_t *tokens, int32_t top,
+                                 float *logprob, float *entropy, float *top_val, int32_t *top_idx,
+                                 cudaStream_t stream) {
+    if (rows < 0 || rows > (1 << 24) || n < 1 || n > (1 << 24) || top < 0 || top > 32 || top > n) return Q4_ERR_SHAPE;
+    if ((tokens == nullptr) != (logprob == nullptr)) return Q4_ERR_NULL;
+    if (rows == 0) return Q4_OK;
+    Q4_TRY(check_act(logits));
+    if (tokens) Q4_TRY(check_ints(tokens));
+    if (!aligned16(logprob) || !aligned16(entropy)) return Q4_ERR_ALIGN;
+    if (top > 0) {
+        Q4_TRY(check_act(top_val));
+        Q4_TRY(check_act(top_idx));
+    }
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
+    q4::LogprobParams p{};
+    p.logits = logits;
+    p.tokens = tokens;
+    p.logprob = logprob;
+    p.entropy = entropy;
+    p.top_val = top_val;
+    p.top_idx = top_idx;
+    p.rows = rows;
+    p.n = n;
+    p.k = top;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    cudaGetLastError();
+    if (q4::launch_logprobs(p, sms, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
 extern "C" q4_status q4_debug_wait_limits(int64_t barrier_polls, int32_t barrier_extra, int64_t copy_wait_cycles,
                                           int32_t copy_extra_bytes) {
     if (barrier_extra < 0 || barrier_extra > 1 || copy_extra_bytes < 0 || copy_extra_bytes > 4096 ||

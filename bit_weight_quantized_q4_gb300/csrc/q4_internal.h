@@ -400,6 +400,71 @@ size_t gemm_tc_image_bytes(int nb, int C);
 int launch_gemm_tc(const GemmParams &p, int fmt, void *stream);
 constexpr int kGemmTcMinNb = 17;  // up to 16 rows the 16-row mma.sync tile is faster
 
+// ---------------------------------------------------------------- paged cache
+// Device view of a paged KV cache (paged.cuh): pages [hkv][page][D].
+struct PagedKv {
+    void *k, *v;            // [num_pages][hkv][page][D]
+    const int32_t *table;   // [nseq][width] page ids
+    int num_pages, page, hkv, nseq, width;
+};
+constexpr int kMaxSeqs = 1024;  // sequences of one call
+
+// Append (kv_append.cu): packed rows r of sequence b, cu[b] <= r < cu[b + 1],
+// at positions start[b] + r - cu[b].
+struct AppendParams {
+    PagedKv kv;
+    const float *q, *k, *v;            // [rows][H][D] or nullptr, [rows][hkv][D]
+    const int32_t *cu, *start;         // [nseq + 1], [nseq] or nullptr (zeros)
+    const float *rope_cos, *rope_sin;  // [rope_rows][D/2] or nullptr
+    void *q_out;                       // [rows][H][D], the cache's type
+    int *err;
+    int rows, H, D, rope_rows;
+};
+int launch_append(const AppendParams &p, int dtype, void *stream);
+
+// Attention of one new token per sequence (attn_paged.cu).
+struct PagedAttnParams {
+    PagedKv kv;
+    const float *q, *k_new, *v_new;    // [nseq][H][D], [nseq][hkv][D]
+    const int32_t *positions;          // [nseq]; negative: an idle row
+    const float *rope_cos, *rope_sin;  // [rope_rows][D/2] or nullptr
+    float *out;                        // [nseq][H][D]
+    int *count;                        // [nseq * hkv], zero between calls
+    float *part;                       // partial results, 2 slots a CTA
+    int *err;
+    int H, D, window, rope_rows;
+    float scale;
+};
+int paged_attn_ctas(int dtype, int D, int G, int sms);  // CTAs of the largest grid
+size_t paged_attn_slot_floats(int D, int G);
+int launch_paged_attn(const PagedAttnParams &p, int dtype, int ctas, void *stream);
+
+// Attention of packed prompt rows (attn_prefill.cu).
+struct PrefillParams {
+    PagedKv kv;
+    const void *q;              // [rows][H][D], the cache's type
+    void *out;                  // [rows][H][D]
+    const int32_t *cu, *start;  // as in AppendParams
+    int *err;
+    long long wait_cycles;
+    int extra_tx;
+    int rows, H, D, window;
+    float scale;
+    uint8_t *ws;
+};
+int launch_prefill(const PrefillParams &p, int dtype, void *stream);
+
+// Token log probabilities (logprobs.cu).
+struct LogprobParams {
+    const float *logits;    // [rows][n]
+    const int32_t *tokens;  // [rows] or nullptr
+    float *logprob, *entropy, *top_val;
+    int32_t *top_idx;
+    int *err;
+    int rows, n, k;
+};
+int launch_logprobs(const LogprobParams &p, int sms, void *stream);
+
 int launch_gemv_q4_0(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_affine(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_q8_0(const GemvParams &p, const Plan &plan, void *stream);

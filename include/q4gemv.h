@@ -326,9 +326,10 @@ q4_status q4_decode_check(const void *workspace, cudaStream_t stream);
 /* Synchronises `stream` and reports whether any GEMV-family kernel of this
  * library on the current device (q4_gemv, q4_nrm_gemv, q4_dual_gemv,
  * q4_gus_nrm, q4_res_gemv, q4_argmax, q4_argmax_noalloc, q4_gemm,
- * q4_attn_decode) gave up waiting for its weight (or K/V) copies since the
- * last check (Q4_ERR_CUDA; the flag is then
- * cleared) or not (Q4_OK).  Each kernel bounds every such wait (about a
+ * q4_attn_decode, q4_attn_prefill) gave up waiting for its weight (or K/V)
+ * copies since the last check, or a kernel of the paged cache or of
+ * q4_logprobs met a position, page or token out of range (Q4_ERR_CUDA; the
+ * flag is then cleared) or not (Q4_OK).  Each kernel bounds every such wait (about a
  * second); a kernel that gives up records it in a per-device word of the
  * library, stops streaming, waits (bounded) for its copies in flight and
  * returns, leaving its outputs undefined.  The word's address is resolved
@@ -440,6 +441,95 @@ q4_status q4_attn_decode(const float *q, const float *k_new, const float *v_new,
  * the angle pos / rope_theta^(2j/D) (honeycrisp/mod.rs, attn_state).  D even,
  * rope_theta > 0, 1 <= max_seq <= 2^24, else Q4_ERR_SHAPE. */
 q4_status q4_rope_table(int32_t max_seq, int32_t D, double rope_theta, float *host_cos, float *host_sin);
+
+/* ---------------------------------------------------------------- paged KV cache
+ * A KV cache that several sequences share (library-specific layout; the
+ * operations are those of honeycrisp/mod.rs, gpu_attention and the fused RoPE +
+ * KV-append + SDPA dispatch of forward_decode_fused_layers, over a batch).
+ * k and v: [num_pages][kv_heads][page_size][head_dim] of `dtype`.  Position p
+ * of sequence b lies in page table[b * width + p / page_size], slot p %
+ * page_size; table: [nseq][width] device int32.  A contiguous cache
+ * [kv_heads][max_seq][head_dim] is one page of max_seq positions (width 1).
+ * Limits: head_dim 64 or 128; page_size a multiple of 16 up to 2^24, or any
+ * size up to 2^24 with width 1; width * page_size <= 2^30; 1 <= nseq <= 1024;
+ * kv_heads <= 1024.
+ * The int32 arrays of these calls (table, cu_rows, start, positions, tokens)
+ * are device memory with 4-byte alignment; everything else is 16-byte aligned.
+ * They are read by the kernels, so a captured launch follows their values.  A
+ * position or page id out of range is never followed: the kernel leaves that
+ * row (append) or those positions (attention) out and records it, and
+ * q4_device_check then returns Q4_ERR_CUDA. */
+typedef enum { Q4_T_F32 = 0, Q4_T_F16 = 1, Q4_T_BF16 = 2 } q4_dtype;
+typedef struct {
+    void *k, *v;
+    const int32_t *table;
+    int32_t dtype, num_pages, page_size, kv_heads, head_dim, nseq, width;
+} q4_kv_pages;
+
+/* New rows into the pages.  Packed rows r of sequence b, cu_rows[b] <= r <
+ * cu_rows[b + 1], have positions start[b] + r - cu_rows[b] (start NULL: zeros).
+ * k (rotated by the tables' row of its position, as q4_attn_decode rotates) and
+ * v are rounded to the cache's type (nearest even) and written to their pages;
+ * with q not NULL, q [rows][H][D] is rotated and rounded likewise into q_out
+ * [rows][H][D] of the cache's type, the form q4_attn_prefill takes.  k, v:
+ * [rows][kv_heads][D] fp32; cu_rows: [nseq + 1], non-decreasing, cu_rows[0] =
+ * 0; sequences may have no rows; rows from cu_rows[nseq] on are left alone (in
+ * q_out too).  rope_cos, rope_sin: [rope_rows][D/2] or both NULL.  Two rows
+ * must not share a position of a page.  rows = 0 launches nothing. */
+q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k, const float *v, int32_t rows,
+                       const int32_t *cu_rows, const int32_t *start, int32_t H, const float *rope_cos,
+                       const float *rope_sin, int32_t rope_rows, void *q_out, cudaStream_t stream);
+
+/* Causal attention of packed prompt rows (rows and positions as in
+ * q4_kv_append; their keys and values, and those of the cached positions before
+ * them, are already in the pages): row r at position p of its sequence gets
+ * out[r][h] = sum_j w_j v_j over the positions j <= p (j > p - window for
+ * window > 0), w = softmax_j(scale q[r][h] . k_j), query head h reading kv head
+ * h / (H / kv_heads).  q, out: [rows][H][D] of the cache's type, not
+ * overlapping; out rows from cu_rows[nseq] on are left alone.  H / kv_heads in
+ * 1..16.  What masked positions hold (infinities, NaN) does not reach out.
+ * Numerics: fp32 sums and softmax statistics; with a 16-bit type the softmax
+ * weights enter the products rounded once to it.
+ * workspace: q4_attn_prefill_workspace_bytes bytes (may be 0: then NULL), no
+ * initialisation needed. */
+size_t q4_attn_prefill_workspace_bytes(const q4_kv_pages *pages, int32_t rows, int32_t H);
+q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows, const int32_t *cu_rows,
+                          const int32_t *start, int32_t H, int32_t window, float scale, void *out, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* Attention of one new token per sequence: for each sequence b with
+ * positions[b] = p >= 0, q4_attn_decode's operation (RoPE of q and k_new,
+ * append, attention over (p - window, p]) over the pages; the new row is
+ * attended as the cache stores it.  A negative position marks an idle row (a
+ * padded batch): nothing is appended and its out row is zeros.  q, out:
+ * [nseq][H][D] fp32; k_new, v_new: [nseq][kv_heads][D] fp32; positions: [nseq].
+ * H / kv_heads in 1..16.  Two sequences must not append to one page slot.
+ * workspace: q4_attn_paged_workspace_bytes bytes, zero-filled by the caller
+ * before its first use (every call leaves its counters zero); calls (and
+ * captured graphs) that share one must not run at the same time.  Results do
+ * not depend on scheduling. */
+size_t q4_attn_paged_workspace_bytes(const q4_kv_pages *pages, int32_t H);
+q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k_new, const float *v_new,
+                        const int32_t *positions, int32_t H, int32_t window, float scale, const float *rope_cos,
+                        const float *rope_sin, int32_t rope_rows, float *out, void *workspace,
+                        size_t workspace_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- sampling
+ * Log probabilities from logit rows (Module gpu, module sampling: what a
+ * sampler reads beside the greedy argmax).  logits: [rows][n] fp32, as
+ * q4_argmax writes them; with lse = log sum_i exp(x_i) and p = exp(x - lse):
+ *   logprob[r] = x[tokens[r]] - lse (0 for a negative token: a row not scored;
+ *     NaN, and recorded for q4_device_check, for a token >= n);
+ *   entropy[r] = -sum_i p_i log p_i;
+ *   top_val[r][j], top_idx[r][j], j < top: the largest log probabilities in
+ *     descending order and their indices, ties to the lowest index.
+ * Logits of -inf are forbidden tokens (p = 0); a row of nothing else has
+ * log probabilities -inf and entropy 0.  A NaN or +inf logit makes the row's
+ * values NaN (in top_idx a NaN ranks below every number).  tokens and logprob:
+ * [rows] or both NULL; entropy: [rows] or NULL; top_val, top_idx: [rows][top],
+ * 0 <= top <= min(32, n) (NULL for top = 0).  1 <= n <= 2^24. */
+q4_status q4_logprobs(const float *logits, int32_t rows, int32_t n, const int32_t *tokens, int32_t top,
+                      float *logprob, float *entropy, float *top_val, int32_t *top_idx, cudaStream_t stream);
 
 /* Launch plan the library uses for a GEMV-shaped call (host-only; exposed
  * for tests and tuning).  tiles: 16-row tiles of the launch, chunks: 128-k
