@@ -1,10 +1,433 @@
 // attn_prefill.cu -- causal attention of packed prompt rows over the pages of
-// their sequences (honeycrisp/mod.rs, gpu_attention, for a prompt): a warp per
-// row and head.
+// their sequences (honeycrisp/mod.rs, gpu_attention, for a prompt).
+//
+// 16-bit caches (q4attn_prefill_tc_kernel): a CTA takes two tiles of up to 128
+// rows of one kv head's group -- floor(128 / G) consecutive tokens by G query
+// heads, so the group shares every K and V tile -- and walks the key tiles of
+// 128 positions with a running softmax:
+//   S = Q K^T          tcgen05.mma, 128 x 128 fp32 in tensor memory
+//   P = 2^(c S - m)    a thread a row; P (16-bit) over S's columns
+//   O += P V           tcgen05.mma with P as the tensor-memory operand
+// Q, K and V tiles come by tensor-map copies (TMA, 128-byte swizzle) straight
+// from the packed rows and the pages; V is the MN-major operand, so nothing is
+// transposed.  Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8
+// issues the MMAs, warp 9 the copies.  While one tile's softmax runs, the
+// tensor core works on the other's products.  O is rescaled in tensor memory
+// only when a row's maximum grew by more than 2^8 (the sums stay exact: the
+// reference maximum is the row's own, and its factor cancels).
+//
+// Masked positions: scores are replaced before the maximum; V rows behind the
+// sequence's end are zeroed in shared memory.  A non-finite value at a position
+// that some rows of a tile see and others do not would still enter as 0 * NaN:
+// a row whose result is not finite is therefore taken again by the definition
+// (attn_row), which never touches what it does not attend.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "attn_prefill_row.cuh"
+#include "gemv_launch.cuh"
+#include "tc_common.cuh"
 
 namespace q4 {
 namespace dev {
+
+constexpr int kPfKeys = 128;                // positions of a key tile
+constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values
+constexpr int kPfThreads = 32 * 10;
+constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
+
+template <int D>
+struct PfCfg {
+    static constexpr int NB = D / 64;                  // 64-value blocks of a row
+    static constexpr int Tile = NB * kPfBlk;           // a Q, K or V tile
+    static constexpr int NS = D == 128 ? 5 : 6;        // ring stages (K and V tiles in turn)
+    static constexpr int OffQ = 0, OffRing = 2 * Tile, OffBar = OffRing + NS * Tile;
+    static constexpr int Smem = OffBar + 512 + 1024;   // + slack to align to 1024
+    static constexpr int ColO = 256;                   // tensor memory: S0 0, S1 128, O0, O1
+    static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
+};
+
+__device__ __forceinline__ void pf_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// The CTA's tile: sequence, its first token (row of the packed batch and
+// position) and its tokens.  Tiles of a sequence are numbered from its end:
+// the longest first.
+struct PfTile {
+    int seq, row0, pos0, tokens;
+};
+// Called by one warp; seq = -1 when there is no such tile.
+__device__ __forceinline__ PfTile pf_find(const PrefillParams &p, int idx, int tpc, int lane) {
+    PfTile t = {-1, 0, 0, 0};
+    long long before = 0;
+    for (int b0 = 0; b0 < p.kv.nseq; b0 += 32) {
+        const int b = b0 + lane;
+        int begin = 0, rows = 0;
+        if (b < p.kv.nseq) {
+            begin = min(max(p.cu[b], 0), p.rows);
+            rows = max(min(p.cu[b + 1], p.rows) - begin, 0);
+        }
+        const int first = b < p.kv.nseq && p.start ? p.start[b] : 0;
+        const long long cap = (long long)p.kv.width * p.kv.page;
+        if (rows > 0 && (first < 0 || (long long)first + rows > cap)) {
+            atomicExch(p.err, kErrPaged);
+            rows = first < 0 || first >= cap ? 0 : (int)(cap - first);
+        }
+        const int n = (rows + tpc - 1) / tpc;
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > idx);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            const int nb = __shfl_sync(0xffffffffu, n, l);
+            const int at = (int)(idx - (before + __shfl_sync(0xffffffffu, inc, l) - nb));  // 0: the last tile
+            const int tok = (nb - 1 - at) * tpc;
+            t.seq = b0 + l;
+            t.row0 = __shfl_sync(0xffffffffu, begin, l) + tok;
+            t.pos0 = __shfl_sync(0xffffffffu, first, l) + tok;
+            t.tokens = min(tpc, __shfl_sync(0xffffffffu, rows, l) - tok);
+            return t;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return t;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPfThreads, 1)
+    q4attn_prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mq,
+                             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                             const int box_rows) {
+    using Cf = PfCfg<D>;
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    constexpr int NB = Cf::NB, NS = Cf::NS;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t *sm = smem_raw + (sb - raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t bars = sb + Cf::OffBar;
+    const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 16, b_p = b_s + 16,
+                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 256);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 260);
+    PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 272);
+    const long long lim = p.wait_cycles;
+    const int G = p.H / p.kv.hkv, TQ = 128 / G;
+    const int hk = (int)(blockIdx.x % p.kv.hkv), idx = (int)(blockIdx.x / p.kv.hkv);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(b_full + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(b_q + 8 * i, 1);
+            mbar_init(b_s + 8 * i, 1);
+            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_o + 8 * i, 1);
+        }
+        mbar_init(b_fix, 1);
+        mbar_init(b_drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        tc::tmem_alloc(smem_u32(tslot), 512);
+        tc::tmem_relinquish();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 9) {
+        const PfTile t = pf_find(p, idx, 2 * TQ, lane);
+        if (lane == 0) *tile_s = t;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t taddr = *tslot;
+    const PfTile t = *tile_s;
+    if (t.seq < 0) {  // no tile of this number
+        __syncthreads();
+        if (warp == 8) tc::tmem_dealloc(taddr, 512);
+        return;
+    }
+    const int nt = t.tokens > TQ ? 2 : 1;  // row tiles in use
+    const int key_end = t.pos0 + t.tokens;
+    const int key_lo = p.window > 0 && t.pos0 + 1 > p.window ? t.pos0 + 1 - p.window : 0;
+    const int k_first = key_lo & ~(kPfKeys - 1);
+    const int nk = (key_end - k_first + kPfKeys - 1) / kPfKeys;
+    const int tail = key_end - (k_first + (nk - 1) * kPfKeys);  // positions of the last key tile
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicExch(p.err, 6);
+    };
+
+    int issued = 0;      // ring tiles issued (warp 9)
+    bool mma_any = false;  // MMAs issued (warp 8 lane 0)
+    if (warp == 9) {
+        // ------------------------------------------------------------ copies
+        if (lane == 0) {
+            const uint32_t qbytes = (uint32_t)NB * 128u * (uint32_t)(G * TQ);
+            for (int i = 0; i < nt; ++i) {
+                mbar_expect_tx(b_q + 8 * i, qbytes + (i == 0 ? (uint32_t)p.extra_tx : 0u));
+                for (int b = 0; b < NB; ++b)
+                    tma3(sb + Cf::OffQ + i * Cf::Tile + b * kPfBlk, &mq, 64 * b, hk * G, t.row0 + i * TQ, b_q + 8 * i);
+            }
+        }
+        const int boxes = kPfKeys / box_rows;
+        for (int n = 0; n < 2 * nk; ++n) {
+            const int st = n % NS;
+            const bool ok = n < NS || mbar_wait(b_empty + 8 * st, (uint32_t)(n / NS - 1) & 1u, lim);
+            if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
+                if (lane == 0 && !*abort_flag) fail();
+                break;
+            }
+            const int k0 = k_first + (n >> 1) * kPfKeys;
+            const int live = min(boxes, (key_end - k0 + box_rows - 1) / box_rows);  // boxes with attended positions
+            if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
+            __syncwarp();
+            const uint32_t dst = sb + Cf::OffRing + st * Cf::Tile;
+            for (int x = lane; x < live * NB; x += 32) {
+                const int b = x / live, r = x - b * live;
+                const int key = k0 + r * box_rows, col = key / p.kv.page;
+                // a page out of range is copied as zeros (its coordinate is
+                // out of the map's range); below the window it may be gone
+                const int page = page_at(p.kv, t.seq, col);
+                if (page < 0 && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
+                tma4(dst + b * kPfBlk + r * box_rows * 128, (n & 1) ? &mv : &mk, 64 * b, key - col * p.kv.page, hk, page,
+                     b_full + 8 * st);
+            }
+            __syncwarp();
+            issued = n + 1;
+        }
+        if (issued == 2 * nk && tail < kPfKeys) {
+            // V rows behind the last position: zeros, whatever the page holds
+            const int n = 2 * nk - 1, st = n % NS;
+            const bool ok = mbar_wait(b_full + 8 * st, (uint32_t)(n / NS) & 1u, lim);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) fail();
+            } else {
+                uint8_t *v = sm + Cf::OffRing + st * Cf::Tile;
+                for (int x = tail * 8 + lane; x < kPfKeys * 8; x += 32)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        *reinterpret_cast<uint4 *>(v + b * kPfBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) pf_arrive(b_fix);
+            }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
+            const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
+            const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
+            const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
+            auto scores = [&](int i, int n) {  // S_i = Q_i K^T of ring tile n
+                const uint64_t qd = q0 + (uint64_t)((i * Cf::Tile) >> 4);
+                const uint64_t kd = k0 + (uint64_t)(((n % NS) * Cf::Tile) >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
+                    tc::mma_f16(taddr + 128u * i, qd + off, kd + off, id_s, ks != 0);
+                }
+                mma_any = true;
+                tc::commit(b_s + 8 * i);
+            };
+            auto full = [&](int n) { return mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, lim); };
+            bool ok = full(0);
+            for (int i = 0; ok && i < nt; ++i) {
+                ok = mbar_wait(b_q + 8 * i, 0u, lim);
+                if (!ok) break;
+                tc::fence_after_sync();
+                scores(i, 0);
+                if (i == nt - 1) tc::commit(b_empty);
+            }
+            for (int j = 0; ok && j < nk; ++j) {
+                for (int i = 0; i < nt; ++i) {
+                    ok = mbar_wait(b_p + 8 * i, (uint32_t)j & 1u, lim);
+                    if (ok && i == 0) {
+                        ok = full(2 * j + 1);
+                        if (ok && j == nk - 1 && tail < kPfKeys) ok = mbar_wait(b_fix, 0u, lim);
+                    }
+                    if (!ok || *abort_flag) break;
+                    tc::fence_after_sync();
+                    const uint64_t vd = v0 + (uint64_t)((((2 * j + 1) % NS) * Cf::Tile) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < kPfKeys / 16; ++ks)
+                        tc::mma_f16_ta(taddr + Cf::ColO + D * i, taddr + 128u * i + 8u * ks,
+                                       vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
+                    if (i == nt - 1) tc::commit(b_empty + 8 * ((2 * j + 1) % NS));
+                    if (j + 1 < nk) {
+                        if (i == 0) ok = full(2 * j + 2);
+                        if (!ok) break;
+                        scores(i, 2 * j + 2);
+                        if (i == nt - 1) tc::commit(b_empty + 8 * ((2 * j + 2) % NS));
+                    } else {
+                        tc::commit(b_o + 8 * i);
+                    }
+                }
+                if (*abort_flag) break;
+            }
+            if (!ok) fail();
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int i = warp >> 2, r = 32 * (warp & 3) + lane;  // row tile, row
+        if (i < nt) {
+            const int tok = i * TQ + r / G, g = r % G;
+            const bool live = r < G * TQ && tok < t.tokens;
+            const int pos = t.pos0 + (live ? tok : min(i * TQ, t.tokens - 1));
+            const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
+            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t ts = taddr + lanes + 128u * i, to = taddr + lanes + Cf::ColO + D * i;
+            const float c = p.scale * 1.4426950408889634f;
+            float m = -INFINITY, l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < nk; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_s + 8 * i, (uint32_t)j & 1u, lim));
+                if (!ok || *abort_flag) break;
+                tc::fence_after_sync();
+                uint32_t s[128];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc::ld32(ts + 32 * q, s + 32 * q);
+                tc::wait_ld();
+                const int k0 = k_first + j * kPfKeys;
+                if (k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
+                    const int hi = pos - k0, lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
+#pragma unroll
+                    for (int e = 0; e < 128; ++e)
+                        if (e > hi || e < lo) s[e] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(s[q]);
+#pragma unroll
+                for (int e = 4; e < 128; e += 4)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[e + q]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float mn = fmaxf(m, top);
+                        // S of this key tile is complete, so the products before it are too
+                        const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+                        l *= alpha;
+                        m = mn;
+#pragma unroll
+                        for (int q = 0; q < D / 32; ++q) {
+                            uint32_t o[32];
+                            tc::ld32(to + 32 * q, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::st32(to + 32 * q, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * c;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = ex2(fmaf(__uint_as_float(s[32 * q + 2 * e]), c, -mc));
+                        const float b = ex2(fmaf(__uint_as_float(s[32 * q + 2 * e + 1]), c, -mc));
+                        sum[e & 3] += a + b;
+                        w[e] = pack2<T>(a, b);
+                    }
+                    tc::st16(ts + 16 * q, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pf_arrive(b_p + 8 * i);
+            }
+            if (!ok && lane == 0) fail();
+            ok = ok && !*abort_flag;
+            if (ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, 0u, lim));
+                if (!ok && lane == 0) fail();
+            }
+            if (ok) {
+                tc::fence_after_sync();
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int row = t.row0 + tok, head = hk * G + g;
+                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D;
+                bool fine = true;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tc::ld32(to + 32 * q, o);
+                    tc::wait_ld();
+                    uint4 w[4];
+                    uint32_t *ww = reinterpret_cast<uint32_t *>(w);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
+                        fine = fine && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+                        ww[e] = pack2<T>(a, b);
+                    }
+                    if (live)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * e) = w[e];
+                }
+                // rows that are not finite: by the definition
+                unsigned again = __ballot_sync(0xffffffffu, live && !fine);
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    attn_row<T, D>(p, __shfl_sync(0xffffffffu, row, src), __shfl_sync(0xffffffffu, head, src), t.seq,
+                                   __shfl_sync(0xffffffffu, pos, src), lane);
+                }
+            }
+        }
+    }
+    // what is in flight lands before the CTA ends (it has, unless a wait gave up)
+    if (warp == 9 && lane == 0) {
+        for (int n = max(0, issued - NS); n < issued; ++n)
+            mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, kWaitCycles);
+        if (*abort_flag)
+            for (int i = 0; i < nt; ++i) mbar_wait(b_q + 8 * i, 0u, kWaitCycles);
+    }
+    if (warp == 8 && lane == 0 && mma_any) {
+        tc::commit(b_drain);
+        mbar_wait(b_drain, 0u, kWaitCycles);
+    }
+    __syncwarp();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 8) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(taddr, 512);
+    }
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) q4attn_prefill_rows_kernel(const __grid_constant__ PrefillParams p) {
@@ -19,26 +442,98 @@ __global__ void __launch_bounds__(256) q4attn_prefill_rows_kernel(const __grid_c
 
 }  // namespace dev
 
-template <typename T, int D>
-static int launch_rows(const PrefillParams &p, cudaStream_t stream) {
+namespace {
+
+// cuTensorMapEncodeTiled, resolved once (the library links the runtime only)
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static std::atomic<void *> cached{nullptr};
+    void *f = cached.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult res;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res) !=
+                cudaSuccess ||
+            res != cudaDriverEntryPointSuccess)
+            return nullptr;
+        cached.store(f, std::memory_order_release);
+    }
+    return (EncodeTiled)f;
+}
+
+// A row-major map of 16-bit values with boxes of 64 values (128 bytes) by
+// box[1 ..] rows, 128-byte swizzled; dims innermost first.
+bool make_map(CUtensorMap *m, bool bf16, void *base, int rank, const cuuint64_t *dims, const cuuint32_t *box) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    cuuint64_t strides[4];
+    cuuint64_t s = 2;
+    for (int i = 0; i + 1 < rank; ++i) {
+        s *= dims[i];
+        strides[i] = s;
+    }
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, base,
+               dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaLaunchConfig_t pdl_config(unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                              cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.rows, 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_rows_kernel<T, D>, p) == cudaSuccess ? 0 : -1;
+    return cfg;
+}
+
+}  // namespace
+
+template <int D>
+static int launch_rows(const PrefillParams &p, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)p.rows, 256, 0, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_rows_kernel<float, D>, p) == cudaSuccess ? 0 : -1;
+}
+
+template <typename T, int D>
+static int launch_tc(const PrefillParams &p, cudaStream_t stream) {
+    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    const int G = p.H / p.kv.hkv, TQ = 128 / G;
+    // positions a copy box takes: a power of two that divides the page, so
+    // that no box crosses a page's end (one page alone: whole key tiles)
+    int box_rows = 128;
+    while (p.kv.width > 1 && p.kv.page % box_rows != 0) box_rows /= 2;
+    CUtensorMap mq, mk, mv;
+    const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)p.H, (cuuint64_t)p.rows};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
+    const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)p.kv.page, (cuuint64_t)p.kv.hkv, (cuuint64_t)p.kv.num_pages};
+    const cuuint32_t kb[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    if (!make_map(&mq, BF, const_cast<void *>(p.q), 3, qd, qb) || !make_map(&mk, BF, p.kv.k, 4, kd, kb) ||
+        !make_map(&mv, BF, p.kv.v, 4, kd, kb))
+        return -1;
+    auto kern = dev::q4attn_prefill_tc_kernel<T, D>;
+    static size_t smem_set[64] = {0};
+    if (!raise_smem(kern, (size_t)dev::PfCfg<D>::Smem, smem_set)) return -1;
+    // at most one part-filled tile a sequence
+    const long long tiles = (long long)p.rows / (2 * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows);
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(tiles * p.kv.hkv), dev::kPfThreads, dev::PfCfg<D>::Smem, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows) == cudaSuccess ? 0 : -1;
 }
 
 int launch_prefill(const PrefillParams &p, int dtype, void *stream_) {
     cudaStream_t s = (cudaStream_t)stream_;
     switch (dtype) {
-        case 0: return p.D == 64 ? launch_rows<float, 64>(p, s) : launch_rows<float, 128>(p, s);
-        case 1: return p.D == 64 ? launch_rows<__half, 64>(p, s) : launch_rows<__half, 128>(p, s);
-        case 2: return p.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, s) : launch_rows<__nv_bfloat16, 128>(p, s);
+        case 0: return p.D == 64 ? launch_rows<64>(p, s) : launch_rows<128>(p, s);
+        case 1: return p.D == 64 ? launch_tc<__half, 64>(p, s) : launch_tc<__half, 128>(p, s);
+        case 2: return p.D == 64 ? launch_tc<__nv_bfloat16, 64>(p, s) : launch_tc<__nv_bfloat16, 128>(p, s);
     }
     return -1;
 }
