@@ -309,24 +309,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(b_s + 8 * i, (uint32_t)j & 1u, lim));
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
-                uint32_t s[128];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::ld32(ts + 32 * q, s + 32 * q);
-                tc::wait_ld();
+                // the scores are read twice, 32 columns at a time with the next 32 in
+                // flight: all 128 at once would take the registers of both passes
                 const int k0 = k_first + j * kPfKeys;
-                if (k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
-                    const int hi = pos - k0, lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
+                const bool edge = k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window);
+                const int hi = pos - k0, lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
+                auto mask = [&](uint32_t (&v)[32], int q) {
 #pragma unroll
-                    for (int e = 0; e < 128; ++e)
-                        if (e > hi || e < lo) s[e] = 0xff800000u;
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * q + e > hi || 32 * q + e < lo) v[e] = 0xff800000u;
+                };
+                uint32_t s[2][32];
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tc::ld32(ts, s[0]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tc::wait_ld32(s[q & 1]);
+                    tc::ld32(ts + 32 * ((q + 1) & 3), s[(q + 1) & 1]);  // at last the first 32 again
+                    if (edge) mask(s[q & 1], q);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[q & 1][e]));
                 }
-                float mx[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(s[q]);
-#pragma unroll
-                for (int e = 4; e < 128; e += 4)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[e + q]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if (j == 0) {
                     m = top;
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         for (int q = 0; q < D / 32; ++q) {
                             uint32_t o[32];
                             tc::ld32(to + 32 * q, o);
-                            tc::wait_ld();
+                            tc::wait_ld32(o);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                             tc::st32(to + 32 * q, o);
@@ -353,11 +356,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
+                    tc::wait_ld32(s[q & 1]);
+                    if (q < 3) tc::ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
+                    uint32_t(&v)[32] = s[q & 1];
+                    if (edge) mask(v, q);
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = ex2(fmaf(__uint_as_float(s[32 * q + 2 * e]), c, -mc));
-                        const float b = ex2(fmaf(__uint_as_float(s[32 * q + 2 * e + 1]), c, -mc));
+                        const float a = ex2(fmaf(__uint_as_float(v[2 * e]), c, -mc));
+                        const float b = ex2(fmaf(__uint_as_float(v[2 * e + 1]), c, -mc));
                         sum[e & 3] += a + b;
                         w[e] = pack2<T>(a, b);
                     }
@@ -385,7 +392,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t o[32];
                     tc::ld32(to + 32 * q, o);
-                    tc::wait_ld();
+                    tc::wait_ld32(o);
                     uint4 w[4];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
