@@ -34,7 +34,9 @@ namespace dev {
 
 constexpr int kPfKeys = 128;                // positions of a key tile
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values
-constexpr int kPfThreads = 32 * 10;
+constexpr int kPfSoft = 16;                 // softmax warps: 2 row tiles x 2 column halves x 4 row quarters
+constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 1;
+constexpr int kPfThreads = 32 * (kPfSoft + 2);
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
 template <int D>
@@ -43,7 +45,8 @@ struct PfCfg {
     static constexpr int Tile = NB * kPfBlk;           // a Q, K or V tile
     static constexpr int NS = D == 128 ? 5 : 6;        // ring stages (K and V tiles in turn)
     static constexpr int OffQ = 0, OffRing = 2 * Tile, OffBar = OffRing + NS * Tile;
-    static constexpr int Smem = OffBar + 512 + 1024;   // + slack to align to 1024
+    static constexpr int OffX = OffBar + 512;          // maxima the column halves exchange [tile][half][row]
+    static constexpr int Smem = OffX + 2 * 2 * 128 * 4;
     static constexpr int ColO = 256;                   // tensor memory: S0 0, S1 128, O0, O1
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
 };
@@ -64,6 +67,28 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
         "[%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
+}
+
+// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
+    return pair_u32(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ float lo_f32(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_f32(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // The CTA's tile: sequence, its first token (row of the packed batch and
@@ -121,14 +146,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     using Cf = PfCfg<D>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     constexpr int NB = Cf::NB, NS = Cf::NS;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t sb = (raw + 1023u) & ~1023u;
-    uint8_t *sm = smem_raw + (sb - raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = sb + Cf::OffBar;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 16, b_p = b_s + 16,
-                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8;
+                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 8;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 256);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 260);
     PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 272);
@@ -144,20 +167,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 4);
+            mbar_init(b_p + 8 * i, 8);
             mbar_init(b_o + 8 * i, 1);
         }
+        for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
         mbar_init(b_fix, 1);
         mbar_init(b_drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 8) {
+    if (warp == kPfMma) {
         tc::tmem_alloc(smem_u32(tslot), 512);
         tc::tmem_relinquish();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == 9) {
+    if (warp == kPfCopy) {
         const PfTile t = pf_find(p, idx, 2 * TQ, lane);
         if (lane == 0) *tile_s = t;
     }
@@ -168,7 +192,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const PfTile t = *tile_s;
     if (t.seq < 0) {  // no tile of this number
         __syncthreads();
-        if (warp == 8) tc::tmem_dealloc(taddr, 512);
+        if (warp == kPfMma) tc::tmem_dealloc(taddr, 512);
         return;
     }
     const int nt = t.tokens > TQ ? 2 : 1;  // row tiles in use
@@ -182,9 +206,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         atomicExch(p.err, 6);
     };
 
-    int issued = 0;      // ring tiles issued (warp 9)
-    bool mma_any = false;  // MMAs issued (warp 8 lane 0)
-    if (warp == 9) {
+    int issued = 0;      // ring tiles issued (the copy warp)
+    bool mma_any = false;  // MMAs issued (the MMA warp)
+    if (warp == kPfCopy) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
             const uint32_t qbytes = (uint32_t)NB * 128u * (uint32_t)(G * TQ);
@@ -237,64 +261,84 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) pf_arrive(b_fix);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == kPfMma) {
         // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
-            const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
-            const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
-            const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
-            auto scores = [&](int i, int n) {  // S_i = Q_i K^T of ring tile n
-                const uint64_t qd = q0 + (uint64_t)((i * Cf::Tile) >> 4);
-                const uint64_t kd = k0 + (uint64_t)(((n % NS) * Cf::Tile) >> 4);
+        const bool leader = tc::elect_one();
+        const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
+        const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
+        const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
+        const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)); };
+        // S_i = Q_i K^T of ring stage st, which `last` frees
+        auto scores = [&](int i, int st, bool last) {
+            const uint64_t qd = q0 + (uint64_t)((i * Cf::Tile) >> 4), kd = k0 + (uint64_t)((st * Cf::Tile) >> 4);
+            if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
                     tc::mma_f16(taddr + 128u * i, qd + off, kd + off, id_s, ks != 0);
                 }
-                mma_any = true;
                 tc::commit(b_s + 8 * i);
-            };
-            auto full = [&](int n) { return mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, lim); };
-            bool ok = full(0);
-            for (int i = 0; ok && i < nt; ++i) {
-                ok = mbar_wait(b_q + 8 * i, 0u, lim);
-                if (!ok) break;
-                tc::fence_after_sync();
-                scores(i, 0);
-                if (i == nt - 1) tc::commit(b_empty);
+                if (last) tc::commit(b_empty + 8 * st);
             }
-            for (int j = 0; ok && j < nk; ++j) {
-                for (int i = 0; i < nt; ++i) {
-                    ok = mbar_wait(b_p + 8 * i, (uint32_t)j & 1u, lim);
-                    if (ok && i == 0) {
-                        ok = full(2 * j + 1);
-                        if (ok && j == nk - 1 && tail < kPfKeys) ok = mbar_wait(b_fix, 0u, lim);
-                    }
-                    if (!ok || *abort_flag) break;
-                    tc::fence_after_sync();
-                    const uint64_t vd = v0 + (uint64_t)((((2 * j + 1) % NS) * Cf::Tile) >> 4);
+            __syncwarp();
+        };
+        // the ring: K of key tile j is tile 2 j, V tile 2 j + 1
+        int st = 0;
+        uint32_t ph = 0;
+        auto full = [&]() { return wait(b_full + 8 * st, ph); };
+        auto next = [&]() {
+            if (++st == NS) {
+                st = 0;
+                ph ^= 1;
+            }
+        };
+        bool ok = full();
+        for (int i = 0; ok && i < nt; ++i) {
+            ok = wait(b_q + 8 * i, 0u);
+            if (!ok) break;
+            tc::fence_after_sync();
+            mma_any = true;
+            scores(i, 0, i == nt - 1);
+        }
+        for (int j = 0; ok && j < nk; ++j) {
+            next();
+            const int sv = st;  // V's stage
+            const uint32_t phv = ph;
+            next();  // the next K's
+            for (int i = 0; i < nt; ++i) {
+                ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
+                if (ok && i == 0) {
+                    ok = wait(b_full + 8 * sv, phv);
+                    if (ok && j == nk - 1 && tail < kPfKeys) ok = wait(b_fix, 0u);
+                    if (ok && j + 1 < nk) ok = full();
+                }
+                if (!ok || *abort_flag) break;
+                tc::fence_after_sync();
+                const uint64_t vd = v0 + (uint64_t)((sv * Cf::Tile) >> 4);
+                if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < kPfKeys / 16; ++ks)
                         tc::mma_f16_ta(taddr + Cf::ColO + D * i, taddr + 128u * i + 8u * ks,
                                        vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
-                    if (i == nt - 1) tc::commit(b_empty + 8 * ((2 * j + 1) % NS));
-                    if (j + 1 < nk) {
-                        if (i == 0) ok = full(2 * j + 2);
-                        if (!ok) break;
-                        scores(i, 2 * j + 2);
-                        if (i == nt - 1) tc::commit(b_empty + 8 * ((2 * j + 2) % NS));
-                    } else {
-                        tc::commit(b_o + 8 * i);
-                    }
+                    if (i == nt - 1) tc::commit(b_empty + 8 * sv);
+                    if (j + 1 == nk) tc::commit(b_o + 8 * i);
                 }
-                if (*abort_flag) break;
+                __syncwarp();
+                if (j + 1 < nk) scores(i, st, i == nt - 1);
             }
-            if (!ok) fail();
+            if (*abort_flag) break;
         }
+        if (!ok && leader) fail();
+        if (leader && mma_any) {  // nothing is in flight when the CTA ends
+            tc::commit(b_drain);
+            mbar_wait(b_drain, 0u, kWaitCycles);
+        }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
-        const int i = warp >> 2, r = 32 * (warp & 3) + lane;  // row tile, row
+        // tile i, column half hf of every key tile, row r
+        const int i = warp >> 3, hf = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
         if (i < nt) {
             const int tok = i * TQ + r / G, g = r % G;
             const bool live = r < G * TQ && tok < t.tokens;
@@ -302,135 +346,146 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t ts = taddr + lanes + 128u * i, to = taddr + lanes + Cf::ColO + D * i;
+            const uint32_t bx = b_x + 8 * (4 * i + (warp & 3));
+            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
             const float c = p.scale * 1.4426950408889634f;
+            // a row's value of the other column half, exchange number n: its warp
+            // has read the one before from `buf` by the time it is written again
+            // (S of the next key tile, and the end of O, come after every warp's P)
+            auto other = [&](float mine, int n, float *buf, bool &ok) {
+                buf[hf * 128 + r] = mine;
+                __syncwarp();
+                if (lane == 0) pf_arrive(bx);
+                ok = __all_sync(0xffffffffu, mbar_wait(bx, (uint32_t)n & 1u, lim));
+                return buf[(hf ^ 1) * 128 + r];
+            };
             float m = -INFINITY, l = 0.f;
             bool ok = true;
             for (int j = 0; j < nk; ++j) {
                 ok = __all_sync(0xffffffffu, mbar_wait(b_s + 8 * i, (uint32_t)j & 1u, lim));
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
-                // the scores are read twice, 32 columns at a time with the next 32 in
-                // flight: all 128 at once would take the registers of both passes
+                uint32_t s[64];
+                tc::ld32(ts + 64 * hf, s);
+                tc::ld32(ts + 64 * hf + 32, s + 32);
+                tc::wait_ld32(s);
+                tc::wait_ld32(s + 32);
                 const int k0 = k_first + j * kPfKeys;
-                const bool edge = k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window);
-                const int hi = pos - k0, lo = p.window > 0 ? pos - p.window + 1 - k0 : -1;
-                auto mask = [&](uint32_t (&v)[32], int q) {
+                if (k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
+                    const int hi = pos - k0 - 64 * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - 64 * hf : -1;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * q + e > hi || 32 * q + e < lo) v[e] = 0xff800000u;
-                };
-                uint32_t s[2][32];
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                tc::ld32(ts, s[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tc::wait_ld32(s[q & 1]);
-                    tc::ld32(ts + 32 * ((q + 1) & 3), s[(q + 1) & 1]);  // at last the first 32 again
-                    if (edge) mask(s[q & 1], q);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[q & 1][e]));
+                    for (int e = 0; e < 64; ++e)
+                        if (e > hi || e < lo) s[e] = 0xff800000u;
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
+#pragma unroll
+                for (int e = 8; e < 64; e += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                top = fmaxf(top, other(top, j, xs, ok));
+                if (!ok) break;
                 if (j == 0) {
                     m = top;
                 } else {
                     const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
-                    if (__any_sync(0xffffffffu, grew)) {
+                    if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
                         const float mn = fmaxf(m, top);
                         // S of this key tile is complete, so the products before it are too
                         const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                         l *= alpha;
                         m = mn;
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[32];
-                            tc::ld32(to + 32 * q, o);
-                            tc::wait_ld32(o);
+                            uint32_t o[16];
+                            const uint32_t at = to + (D / 2) * hf + 16 * q;
+                            tc::ld16(at, o);
+                            tc::wait_ld16(o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tc::st32(to + 32 * q, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::st16(at, o);
                         }
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float mc = m == -INFINITY ? 0.f : -m * c;
+                const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
+                uint64_t sum[2] = {0ull, 0ull};
+                // P over S's columns 0..63: both halves have read theirs (the exchange)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tc::wait_ld32(s[q & 1]);
-                    if (q < 3) tc::ld32(ts + 32 * (q + 1), s[(q + 1) & 1]);
-                    uint32_t(&v)[32] = s[q & 1];
-                    if (edge) mask(v, q);
+                for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float a = ex2(fmaf(__uint_as_float(v[2 * e]), c, -mc));
-                        const float b = ex2(fmaf(__uint_as_float(v[2 * e + 1]), c, -mc));
-                        sum[e & 3] += a + b;
+                        const uint64_t x = fma_f32x2(pair_u32(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mc2);
+                        const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
+                        sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
                         w[e] = pack2<T>(a, b);
                     }
-                    tc::st16(ts + 16 * q, w);
+                    tc::st16(ts + 32 * hf + 16 * q, w);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const uint64_t s2 = add_f32x2(sum[0], sum[1]);
+                l += lo_f32(s2) + hi_f32(s2);
                 tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
-            if (!ok && lane == 0) fail();
-            ok = ok && !*abort_flag;
-            if (ok) {
+            if (ok && !*abort_flag) {
                 ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, 0u, lim));
-                if (!ok && lane == 0) fail();
+                if (ok) l += other(l, nk, xs, ok);
             }
-            if (ok) {
+            if (!ok && lane == 0) fail();
+            if (ok && !*abort_flag) {
                 tc::fence_after_sync();
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int row = t.row0 + tok, head = hk * G + g;
-                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D;
-                bool fine = true;
+                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / 2) * hf;
+                float worst = 0.f;  // NaN or infinite where a value is
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
+                for (int q = 0; q < D / 64; ++q) {
                     uint32_t o[32];
-                    tc::ld32(to + 32 * q, o);
+                    tc::ld32(to + (D / 2) * hf + 32 * q, o);
                     tc::wait_ld32(o);
                     uint4 w[4];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
-                        fine = fine && fabsf(a) < INFINITY && fabsf(b) < INFINITY;
+                        worst = fmaf(a, 0.f, fmaf(b, 0.f, worst));
                         ww[e] = pack2<T>(a, b);
                     }
                     if (live)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * e) = w[e];
                 }
-                // rows that are not finite: by the definition
-                unsigned again = __ballot_sync(0xffffffffu, live && !fine);
+                // rows that are not finite: by the definition (whole rows, after
+                // both halves have stored theirs); Q's tile is free by now
+                worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::Tile), ok);
+                unsigned again = __ballot_sync(0xffffffffu, ok && live && hf == 0 && worst != 0.f);
                 while (again) {
                     const int src = __ffs(again) - 1;
                     again &= again - 1;
                     attn_row<T, D>(p, __shfl_sync(0xffffffffu, row, src), __shfl_sync(0xffffffffu, head, src), t.seq,
                                    __shfl_sync(0xffffffffu, pos, src), lane);
                 }
+                if (!ok && lane == 0) fail();
             }
         }
     }
     // what is in flight lands before the CTA ends (it has, unless a wait gave up)
-    if (warp == 9 && lane == 0) {
+    if (warp == kPfCopy && lane == 0) {
         for (int n = max(0, issued - NS); n < issued; ++n)
             mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, kWaitCycles);
         if (*abort_flag)
             for (int i = 0; i < nt; ++i) mbar_wait(b_q + 8 * i, 0u, kWaitCycles);
     }
-    if (warp == 8 && lane == 0 && mma_any) {
-        tc::commit(b_drain);
-        mbar_wait(b_drain, 0u, kWaitCycles);
-    }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kPfMma) {
         tc::fence_after_sync();
         tc::tmem_dealloc(taddr, 512);
     }
