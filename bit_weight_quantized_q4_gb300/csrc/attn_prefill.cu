@@ -45,9 +45,14 @@ struct PfCfg {
     static constexpr int Tile = NB * kPfBlk;           // a Q, K or V tile
     static constexpr int NS = D == 128 ? 5 : 6;        // ring stages (K and V tiles in turn)
     static constexpr int OffQ = 0, OffRing = 2 * Tile, OffBar = OffRing + NS * Tile;
-    static constexpr int OffX = OffBar + 512;          // maxima the column halves exchange [tile][half][row]
-    static constexpr int Smem = OffX + 2 * 2 * 128 * 4;
-    static constexpr int ColO = 256;                   // tensor memory: S0 0, S1 128, O0, O1
+    // tensor memory columns: S0 0, S1 128, O0 and O1 from 256; at D = 64 P has
+    // columns of its own, so the next scores start as soon as these are read;
+    // at D = 128 it lies over its S
+    static constexpr bool Sep = D == 64;
+    static constexpr int ColO = 256, ColP = Sep ? 256 + 2 * D : 0, PStep = Sep ? 64 : 128;
+    static constexpr int XBuf = Sep ? 2 : 1;           // exchange buffers
+    static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][buffer][half][row]
+    static constexpr int Smem = OffX + XBuf * 2 * 2 * 128 * 4;
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
 };
 
@@ -151,7 +156,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = sb + Cf::OffBar;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 16, b_p = b_s + 16,
-                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 8;
+                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 8, b_sf = b_x + 64;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 256);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 260);
     PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 272);
@@ -169,6 +174,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_p + 8 * i, 8);
             mbar_init(b_o + 8 * i, 1);
+            mbar_init(b_sf + 8 * i, 8);
         }
         for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
         mbar_init(b_fix, 1);
@@ -218,31 +224,45 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     tma3(sb + Cf::OffQ + i * Cf::Tile + b * kPfBlk, &mq, 64 * b, hk * G, t.row0 + i * TQ, b_q + 8 * i);
             }
         }
-        const int boxes = kPfKeys / box_rows;
-        for (int n = 0; n < 2 * nk; ++n) {
-            const int st = n % NS;
-            const bool ok = n < NS || mbar_wait(b_empty + 8 * st, (uint32_t)(n / NS - 1) & 1u, lim);
-            if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
-                if (lane == 0 && !*abort_flag) fail();
-                break;
+        // lane = 64-value block bl, box r of a tile (at most 16 boxes); the next key
+        // tile's pages are looked up while this one's copies go out: looked up in
+        // place they held the ring back (a tile every 1400 cycles)
+        const int boxes = kPfKeys / box_rows, bl = lane / boxes, r = lane - bl * boxes;
+        auto lookup = [&](int j, int &page, int &slot) {
+            const int key = k_first + j * kPfKeys + r * box_rows, col = key / p.kv.page;
+            slot = key - col * p.kv.page;
+            page = bl < NB && key < key_end ? page_at(p.kv, t.seq, col) : -1;
+            // a page out of range is copied as zeros (its coordinate is out of
+            // the map's range); below the window it may be gone
+            if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
+        };
+        int page1, slot1;
+        lookup(0, page1, slot1);
+        bool ok = true;
+        int st = 0;
+        uint32_t ph = 1;  // an empty slot's phase: the first pass finds them free
+        for (int j = 0; ok && j < nk; ++j) {
+            const int page = page1, slot = slot1;
+            const int live = min(boxes, (key_end - k_first - j * kPfKeys + box_rows - 1) / box_rows);  // boxes with attended positions
+            if (j + 1 < nk) lookup(j + 1, page1, slot1);
+            for (int kv = 0; kv < 2; ++kv) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * st, ph, lim));
+                if (!ok || *abort_flag) {
+                    if (lane == 0 && !ok) fail();
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
+                __syncwarp();
+                if (bl < NB && r < live)
+                    tma4(sb + Cf::OffRing + st * Cf::Tile + bl * kPfBlk + r * box_rows * 128, kv ? &mv : &mk, 64 * bl,
+                         slot, hk, page, b_full + 8 * st);
+                ++issued;
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
-            const int k0 = k_first + (n >> 1) * kPfKeys;
-            const int live = min(boxes, (key_end - k0 + box_rows - 1) / box_rows);  // boxes with attended positions
-            if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
-            __syncwarp();
-            const uint32_t dst = sb + Cf::OffRing + st * Cf::Tile;
-            for (int x = lane; x < live * NB; x += 32) {
-                const int b = x / live, r = x - b * live;
-                const int key = k0 + r * box_rows, col = key / p.kv.page;
-                // a page out of range is copied as zeros (its coordinate is
-                // out of the map's range); below the window it may be gone
-                const int page = page_at(p.kv, t.seq, col);
-                if (page < 0 && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
-                tma4(dst + b * kPfBlk + r * box_rows * 128, (n & 1) ? &mv : &mk, 64 * b, key - col * p.kv.page, hk, page,
-                     b_full + 8 * st);
-            }
-            __syncwarp();
-            issued = n + 1;
         }
         if (issued == 2 * nk && tail < kPfKeys) {
             // V rows behind the last position: zeros, whatever the page holds
@@ -306,26 +326,37 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int sv = st;  // V's stage
             const uint32_t phv = ph;
             next();  // the next K's
-            for (int i = 0; i < nt; ++i) {
-                ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
-                if (ok && i == 0) {
-                    ok = wait(b_full + 8 * sv, phv);
-                    if (ok && j == nk - 1 && tail < kPfKeys) ok = wait(b_fix, 0u);
-                    if (ok && j + 1 < nk) ok = full();
-                }
-                if (!ok || *abort_flag) break;
-                tc::fence_after_sync();
+            auto out = [&](int i) {  // O_i += P_i V
                 const uint64_t vd = v0 + (uint64_t)((sv * Cf::Tile) >> 4);
                 if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < kPfKeys / 16; ++ks)
-                        tc::mma_f16_ta(taddr + Cf::ColO + D * i, taddr + 128u * i + 8u * ks,
+                        tc::mma_f16_ta(taddr + Cf::ColO + D * i, taddr + Cf::ColP + Cf::PStep * i + 8 * ks,
                                        vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
+                    if (Cf::Sep || j + 1 == nk) tc::commit(b_o + 8 * i);
                     if (i == nt - 1) tc::commit(b_empty + 8 * sv);
-                    if (j + 1 == nk) tc::commit(b_o + 8 * i);
                 }
                 __syncwarp();
-                if (j + 1 < nk) scores(i, st, i == nt - 1);
+            };
+            if (Cf::Sep && j + 1 < nk) {  // the next scores, while the softmax of these runs
+                ok = full();
+                for (int i = 0; ok && i < nt; ++i) {
+                    ok = wait(b_sf + 8 * i, (uint32_t)j & 1u);
+                    tc::fence_after_sync();
+                    if (ok) scores(i, st, i == nt - 1);
+                }
+            }
+            for (int i = 0; ok && i < nt; ++i) {
+                ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
+                if (ok && i == 0) {
+                    ok = wait(b_full + 8 * sv, phv);
+                    if (ok && j == nk - 1 && tail < kPfKeys) ok = wait(b_fix, 0u);
+                    if (ok && !Cf::Sep && j + 1 < nk) ok = full();
+                }
+                if (!ok || *abort_flag) break;
+                tc::fence_after_sync();
+                out(i);
+                if (!Cf::Sep && j + 1 < nk) scores(i, st, i == nt - 1);
             }
             if (*abort_flag) break;
         }
@@ -346,13 +377,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t ts = taddr + lanes + 128u * i, to = taddr + lanes + Cf::ColO + D * i;
+            const uint32_t tp = taddr + lanes + Cf::ColP + Cf::PStep * i;
             const uint32_t bx = b_x + 8 * (4 * i + (warp & 3));
-            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
+            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * Cf::XBuf * i;  // [buffer][half][row]
             const float c = p.scale * 1.4426950408889634f;
             // a row's value of the other column half, exchange number n: its warp
             // has read the one before from `buf` by the time it is written again
-            // (S of the next key tile, and the end of O, come after every warp's P)
+            // (two buffers, or S of the next key tile comes after every warp's P)
             auto other = [&](float mine, int n, float *buf, bool &ok) {
+                if (Cf::XBuf == 2) buf += 256 * (n & 1);
                 buf[hf * 128 + r] = mine;
                 __syncwarp();
                 if (lane == 0) pf_arrive(bx);
@@ -370,6 +403,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 tc::ld32(ts + 64 * hf + 32, s + 32);
                 tc::wait_ld32(s);
                 tc::wait_ld32(s + 32);
+                if (Cf::Sep) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) pf_arrive(b_sf + 8 * i);
+                }
                 const int k0 = k_first + j * kPfKeys;
                 if (k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
                     const int hi = pos - k0 - 64 * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - 64 * hf : -1;
@@ -387,14 +425,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 top = fmaxf(top, other(top, j, xs, ok));
+                // the products of the key tile before have read P, and O holds them
+                // (with P over S, S itself came after them)
+                if (ok && Cf::Sep && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, (uint32_t)(j - 1) & 1u, lim));
                 if (!ok) break;
+                if (Cf::Sep) tc::fence_after_sync();
                 if (j == 0) {
                     m = top;
                 } else {
                     const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
                     if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
                         const float mn = fmaxf(m, top);
-                        // S of this key tile is complete, so the products before it are too
                         const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                         l *= alpha;
                         m = mn;
@@ -413,7 +454,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 const float mc = m == -INFINITY ? 0.f : -m * c;
                 const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
                 uint64_t sum[2] = {0ull, 0ull};
-                // P over S's columns 0..63: both halves have read theirs (the exchange)
+                // (P over S's columns 0..63: both halves have read theirs, the exchange)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
@@ -424,7 +465,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
                         w[e] = pack2<T>(a, b);
                     }
-                    tc::st16(ts + 32 * hf + 16 * q, w);
+                    tc::st16(tp + 32 * hf + 16 * q, w);
                 }
                 const uint64_t s2 = add_f32x2(sum[0], sum[1]);
                 l += lo_f32(s2) + hi_f32(s2);
@@ -434,7 +475,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
             if (ok && !*abort_flag) {
-                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, 0u, lim));
+                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, Cf::Sep ? (uint32_t)(nk - 1) & 1u : 0u, lim));
                 if (ok) l += other(l, nk, xs, ok);
             }
             if (!ok && lane == 0) fail();
