@@ -35,8 +35,8 @@ namespace dev {
 constexpr int kPfKeys = 128;                // positions of a key tile
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values
 constexpr int kPfSoft = 16;                 // softmax warps: 2 row tiles x 2 column halves x 4 row quarters
-constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 1;
-constexpr int kPfThreads = 32 * (kPfSoft + 2);
+constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // an MMA warp for each row tile, the copy warp
+constexpr int kPfThreads = 32 * (kPfSoft + 3);
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
 template <int D>
@@ -54,6 +54,7 @@ struct PfCfg {
     static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][buffer][half][row]
     static constexpr int Smem = OffX + XBuf * 2 * 2 * 128 * 4;
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
+    static_assert(16 * NS + 168 <= 448, "barriers before the tensor-memory address");
 };
 
 __device__ __forceinline__ void pf_arrive(uint32_t bar) {
@@ -156,10 +157,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = sb + Cf::OffBar;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 16, b_p = b_s + 16,
-                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 8, b_sf = b_x + 64;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 256);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 260);
-    PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 272);
+                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 16, b_sf = b_x + 64;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 448);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 452);
+    PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 464);
     const long long lim = p.wait_cycles;
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
     const int hk = (int)(blockIdx.x % p.kv.hkv), idx = (int)(blockIdx.x / p.kv.hkv);
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 1);
+            mbar_init(b_empty + 8 * i, 2);  // one for each MMA warp
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(b_q + 8 * i, 1);
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
         mbar_init(b_fix, 1);
-        mbar_init(b_drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(b_drain + 8 * i, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -213,7 +214,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     };
 
     int issued = 0;      // ring tiles issued (the copy warp)
-    bool mma_any = false;  // MMAs issued (the MMA warp)
     if (warp == kPfCopy) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
@@ -281,91 +281,85 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) pf_arrive(b_fix);
             }
         }
-    } else if (warp == kPfMma) {
+    } else if (warp == kPfMma || warp == kPfMma + 1) {
         // ------------------------------------------------------------ MMA issue
+        // one warp a row tile, so that neither waits for the other's softmax
+        // (one warp for both: 315 us against 277 at 8192 rows, head size 64)
+        const int i = warp - kPfMma;
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
-        const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
+        const uint64_t qd = tc::smem_desc_sw128(sb + Cf::OffQ + i * Cf::Tile, 16, 1024);
         const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
         const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
+        const uint32_t ts = taddr + 128u * i, to = taddr + Cf::ColO + D * i, tp = taddr + Cf::ColP + Cf::PStep * i;
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)); };
-        // S_i = Q_i K^T of ring stage st, which `last` frees
-        auto scores = [&](int i, int st, bool last) {
-            const uint64_t qd = q0 + (uint64_t)((i * Cf::Tile) >> 4), kd = k0 + (uint64_t)((st * Cf::Tile) >> 4);
+        // both row tiles free a ring stage; a tile alone does it twice
+        auto release = [&](int st) {
+            tc::commit(b_empty + 8 * st);
+            if (nt == 1) tc::commit(b_empty + 8 * st);
+        };
+        auto scores = [&](int st) {  // S = Q K^T of ring stage st
+            const uint64_t kd = k0 + (uint64_t)((st * Cf::Tile) >> 4);
             if (leader) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks) {
                     const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
-                    tc::mma_f16(taddr + 128u * i, qd + off, kd + off, id_s, ks != 0);
+                    tc::mma_f16(ts, qd + off, kd + off, id_s, ks != 0);
                 }
                 tc::commit(b_s + 8 * i);
-                if (last) tc::commit(b_empty + 8 * st);
+                release(st);
             }
             __syncwarp();
         };
         // the ring: K of key tile j is tile 2 j, V tile 2 j + 1
         int st = 0;
         uint32_t ph = 0;
-        auto full = [&]() { return wait(b_full + 8 * st, ph); };
         auto next = [&]() {
             if (++st == NS) {
                 st = 0;
                 ph ^= 1;
             }
         };
-        bool ok = full();
-        for (int i = 0; ok && i < nt; ++i) {
-            ok = wait(b_q + 8 * i, 0u);
-            if (!ok) break;
-            tc::fence_after_sync();
-            mma_any = true;
-            scores(i, 0, i == nt - 1);
-        }
-        for (int j = 0; ok && j < nk; ++j) {
-            next();
-            const int sv = st;  // V's stage
-            const uint32_t phv = ph;
-            next();  // the next K's
-            auto out = [&](int i) {  // O_i += P_i V
-                const uint64_t vd = v0 + (uint64_t)((sv * Cf::Tile) >> 4);
-                if (leader) {
-#pragma unroll
-                    for (int ks = 0; ks < kPfKeys / 16; ++ks)
-                        tc::mma_f16_ta(taddr + Cf::ColO + D * i, taddr + Cf::ColP + Cf::PStep * i + 8 * ks,
-                                       vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
-                    if (Cf::Sep || j + 1 == nk) tc::commit(b_o + 8 * i);
-                    if (i == nt - 1) tc::commit(b_empty + 8 * sv);
-                }
-                __syncwarp();
-            };
-            if (Cf::Sep && j + 1 < nk) {  // the next scores, while the softmax of these runs
-                ok = full();
-                for (int i = 0; ok && i < nt; ++i) {
-                    ok = wait(b_sf + 8 * i, (uint32_t)j & 1u);
-                    tc::fence_after_sync();
-                    if (ok) scores(i, st, i == nt - 1);
-                }
+        if (i < nt) {
+            bool ok = wait(b_q + 8 * i, 0u) && wait(b_full, 0u);
+            if (ok) {
+                tc::fence_after_sync();
+                scores(0);
             }
-            for (int i = 0; ok && i < nt; ++i) {
-                ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
-                if (ok && i == 0) {
-                    ok = wait(b_full + 8 * sv, phv);
-                    if (ok && j == nk - 1 && tail < kPfKeys) ok = wait(b_fix, 0u);
-                    if (ok && !Cf::Sep && j + 1 < nk) ok = full();
+            for (int j = 0; ok && j < nk; ++j) {
+                next();
+                const int sv = st;  // V's stage
+                const uint32_t phv = ph;
+                next();  // the next K's
+                if (j + 1 < nk) ok = wait(b_full + 8 * st, ph);
+                if (Cf::Sep && j + 1 < nk) {  // the next scores, while the softmax of these runs
+                    ok = ok && wait(b_sf + 8 * i, (uint32_t)j & 1u);
+                    tc::fence_after_sync();
+                    if (ok) scores(st);
                 }
+                ok = ok && wait(b_full + 8 * sv, phv);
+                if (j == nk - 1 && tail < kPfKeys) ok = ok && wait(b_fix, 0u);
+                ok = ok && wait(b_p + 8 * i, (uint32_t)j & 1u);
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
-                out(i);
-                if (!Cf::Sep && j + 1 < nk) scores(i, st, i == nt - 1);
+                const uint64_t vd = v0 + (uint64_t)((sv * Cf::Tile) >> 4);
+                if (leader) {  // O += P V
+#pragma unroll
+                    for (int ks = 0; ks < kPfKeys / 16; ++ks)
+                        tc::mma_f16_ta(to, tp + 8 * ks, vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
+                    if (Cf::Sep || j + 1 == nk) tc::commit(b_o + 8 * i);
+                    release(sv);
+                }
+                __syncwarp();
+                if (!Cf::Sep && j + 1 < nk) scores(st);
             }
-            if (*abort_flag) break;
+            if (!ok && leader) fail();
+            if (leader) {  // nothing is in flight when the CTA ends
+                tc::commit(b_drain + 8 * i);
+                mbar_wait(b_drain + 8 * i, 0u, kWaitCycles);
+            }
+            __syncwarp();
         }
-        if (!ok && leader) fail();
-        if (leader && mma_any) {  // nothing is in flight when the CTA ends
-            tc::commit(b_drain);
-            mbar_wait(b_drain, 0u, kWaitCycles);
-        }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax
         // tile i, column half hf of every key tile, row r
