@@ -39,39 +39,65 @@ constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // an MMA warp for each 
 constexpr int kPfThreads = 32 * (kPfSoft + 3);
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
-template <int D>
+// What enters the products of a cache type: 16-bit values as they are (one
+// part); fp32 values as two f16 parts hi + lo (22 bits) after a power-of-two
+// scale, three products each (lo lo, of 2^-22, is left out).
+template <typename T>
+struct PfT {
+    using M = T;
+    static constexpr int Parts = 1;
+    static constexpr float PExp = 0.f;
+};
+template <>
+struct PfT<float> {
+    using M = __half;
+    static constexpr int Parts = 2;
+    static constexpr float PExp = 6.f;  // weights reach 2^(6 + kPfGrow): their low parts stay normal f16
+};
+
+template <int D, int Parts>
 struct PfCfg {
     static constexpr int NB = D / 64;                  // 64-value blocks of a row
-    static constexpr int Tile = NB * kPfBlk;           // a Q, K or V tile
-    static constexpr int NS = D == 128 ? 5 : 6;        // ring stages (K and V tiles in turn)
-    static constexpr int OffQ = 0, OffRing = 2 * Tile, OffBar = OffRing + NS * Tile;
-    // tensor memory columns: S0 0, S1 128, O0 and O1 from 256; at D = 64 P has
-    // columns of its own, so the next scores start as soon as these are read;
-    // at D = 128 it lies over its S
-    static constexpr bool Sep = D == 64;
+    static constexpr int Tile = NB * kPfBlk;           // one part of a Q, K or V tile
+    static constexpr int NT = D * Parts == 256 ? 1 : 2;  // row tiles of a CTA
+    static constexpr int QTile = Parts * Tile;
+    static constexpr int NS = D == 128 || Parts == 2 ? 5 : 6;  // ring stages: per key tile K's parts, then V's
+    static constexpr int OffQ = 0, OffRing = NT * QTile, OffBar = OffRing + NS * Tile;
+    // tensor memory columns: S0 0, S1 128, O0 and O1 from 256.  One part at D =
+    // 64: P has columns of its own, so the next scores start as soon as these
+    // are read; else it lies over its S (two parts: each column half's parts
+    // over that half's columns, 16 columns of hi and 16 of lo per 32 positions)
+    static constexpr bool Sep = D == 64 && Parts == 1;
     static constexpr int ColO = 256, ColP = Sep ? 256 + 2 * D : 0, PStep = Sep ? 64 : 128;
     static constexpr int XBuf = Sep ? 2 : 1;           // exchange buffers
     static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][buffer][half][row]
     static constexpr int Smem = OffX + XBuf * 2 * 2 * 128 * 4;
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
     static_assert(16 * NS + 168 <= 448, "barriers before the tensor-memory address");
+    // P's column of 16 positions (step ks), part 0
+    static constexpr int p_col(int ks) {
+        return Parts == 1 ? 8 * ks : 64 * (ks / 4) + 32 * ((ks % 4) / 2) + 8 * (ks % 2);
+    }
 };
 
+// The inverse of the power of two for a largest magnitude given as fp32 bits.
+__device__ __forceinline__ float pf_back(uint32_t bits);
 __device__ __forceinline__ void pf_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-            dst),
-        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
 }
 __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
         "[%2];" ::"r"(dst),
         "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, int v,
+                                     uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+        "[%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
         : "memory");
 }
 
@@ -149,8 +175,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     q4attn_prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mq,
                              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                              const int box_rows) {
-    using Cf = PfCfg<D>;
-    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    using M = typename PfT<T>::M;
+    constexpr int NP = PfT<T>::Parts;
+    using Cf = PfCfg<D, NP>;
+    constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
     constexpr int NB = Cf::NB, NS = Cf::NS;
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const uint32_t sb = smem_u32(sm);
@@ -189,7 +217,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kPfCopy) {
-        const PfTile t = pf_find(p, idx, 2 * TQ, lane);
+        const PfTile t = pf_find(p, idx, Cf::NT * TQ, lane);
         if (lane == 0) *tile_s = t;
     }
     tc::fence_before_sync();
@@ -217,11 +245,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     if (warp == kPfCopy) {
         // ------------------------------------------------------------ copies
         if (lane == 0) {
-            const uint32_t qbytes = (uint32_t)NB * 128u * (uint32_t)(G * TQ);
+            const uint32_t qbytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
             for (int i = 0; i < nt; ++i) {
                 mbar_expect_tx(b_q + 8 * i, qbytes + (i == 0 ? (uint32_t)p.extra_tx : 0u));
-                for (int b = 0; b < NB; ++b)
-                    tma3(sb + Cf::OffQ + i * Cf::Tile + b * kPfBlk, &mq, 64 * b, hk * G, t.row0 + i * TQ, b_q + 8 * i);
+                for (int b = 0; b < NP * NB; ++b)
+                    tma4(sb + Cf::OffQ + i * Cf::QTile + b * kPfBlk, &mq, 64 * (b % NB), hk * G, t.row0 + i * TQ, b / NB,
+                         b_q + 8 * i);
             }
         }
         // lane = 64-value block bl, box r of a tile (at most 16 boxes); the next key
@@ -245,7 +274,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int page = page1, slot = slot1;
             const int live = min(boxes, (key_end - k_first - j * kPfKeys + box_rows - 1) / box_rows);  // boxes with attended positions
             if (j + 1 < nk) lookup(j + 1, page1, slot1);
-            for (int kv = 0; kv < 2; ++kv) {
+            for (int kv = 0; kv < 2 * NP; ++kv) {  // K's parts, V's parts
                 ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * st, ph, lim));
                 if (!ok || *abort_flag) {
                     if (lane == 0 && !ok) fail();
@@ -255,8 +284,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
                 __syncwarp();
                 if (bl < NB && r < live)
-                    tma4(sb + Cf::OffRing + st * Cf::Tile + bl * kPfBlk + r * box_rows * 128, kv ? &mv : &mk, 64 * bl,
-                         slot, hk, page, b_full + 8 * st);
+                    tma5(sb + Cf::OffRing + st * Cf::Tile + bl * kPfBlk + r * box_rows * 128, kv >= NP ? &mv : &mk,
+                         64 * bl, slot, hk, page, kv % NP, b_full + 8 * st);
                 ++issued;
                 if (++st == NS) {
                     st = 0;
@@ -264,21 +293,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
             }
         }
-        if (issued == 2 * nk && tail < kPfKeys) {
+        if (issued == 2 * NP * nk && tail < kPfKeys) {
             // V rows behind the last position: zeros, whatever the page holds
-            const int n = 2 * nk - 1, st = n % NS;
-            const bool ok = mbar_wait(b_full + 8 * st, (uint32_t)(n / NS) & 1u, lim);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) fail();
-            } else {
-                uint8_t *v = sm + Cf::OffRing + st * Cf::Tile;
-                for (int x = tail * 8 + lane; x < kPfKeys * 8; x += 32)
+            for (int n = issued - NP; ok && n < issued; ++n) {
+                const int sv = n % NS;
+                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * sv, (uint32_t)(n / NS) & 1u, lim));
+                uint8_t *v = sm + Cf::OffRing + sv * Cf::Tile;
+                for (int x = tail * 8 + lane; ok && x < kPfKeys * 8; x += 32)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
                         *reinterpret_cast<uint4 *>(v + b * kPfBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) pf_arrive(b_fix);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (ok)
+                    pf_arrive(b_fix);
+                else
+                    fail();
             }
         }
     } else if (warp == kPfMma || warp == kPfMma + 1) {
@@ -288,7 +320,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int i = warp - kPfMma;
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
-        const uint64_t qd = tc::smem_desc_sw128(sb + Cf::OffQ + i * Cf::Tile, 16, 1024);
+        const uint64_t qd = tc::smem_desc_sw128(sb + Cf::OffQ + i * Cf::QTile, 16, 1024);
         const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
         const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
         const uint32_t ts = taddr + 128u * i, to = taddr + Cf::ColO + D * i, tp = taddr + Cf::ColP + Cf::PStep * i;
@@ -298,20 +330,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             tc::commit(b_empty + 8 * st);
             if (nt == 1) tc::commit(b_empty + 8 * st);
         };
-        auto scores = [&](int st) {  // S = Q K^T of ring stage st
-            const uint64_t kd = k0 + (uint64_t)((st * Cf::Tile) >> 4);
-            if (leader) {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
-                    tc::mma_f16(ts, qd + off, kd + off, id_s, ks != 0);
-                }
-                tc::commit(b_s + 8 * i);
-                release(st);
-            }
-            __syncwarp();
-        };
-        // the ring: K of key tile j is tile 2 j, V tile 2 j + 1
+        // the ring: key tile j's K parts, then its V parts
         int st = 0;
         uint32_t ph = 0;
         auto next = [&]() {
@@ -320,38 +339,78 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ph ^= 1;
             }
         };
+        // S = Q K^T of the NP ring stages from st on, which have landed
+        auto scores = [&](int st) {
+            if (leader) {
+#pragma unroll
+                for (int y = 0; y < NP; ++y) {
+                    const int sk = st + y < NS ? st + y : st + y - NS;
+                    const uint64_t kd = k0 + (uint64_t)((sk * Cf::Tile) >> 4);
+#pragma unroll
+                    for (int x = 0; x < NP - y; ++x)  // Q's part x by K's part y
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
+                            tc::mma_f16(ts, qd + (uint64_t)((x * Cf::Tile) >> 4) + off, kd + off, id_s, (x | y | ks) != 0);
+                        }
+                    if (y == NP - 1) tc::commit(b_s + 8 * i);
+                    release(sk);
+                }
+            }
+            __syncwarp();
+        };
         if (i < nt) {
-            bool ok = wait(b_q + 8 * i, 0u) && wait(b_full, 0u);
+            bool ok = wait(b_q + 8 * i, 0u);
+            for (int y = 0; y < NP; ++y) ok = ok && wait(b_full + 8 * y, 0u);
             if (ok) {
                 tc::fence_after_sync();
                 scores(0);
             }
+            for (int y = 0; y < NP; ++y) next();
             for (int j = 0; ok && j < nk; ++j) {
-                next();
-                const int sv = st;  // V's stage
+                const int sv = st;  // V's stages
                 const uint32_t phv = ph;
-                next();  // the next K's
-                if (j + 1 < nk) ok = wait(b_full + 8 * st, ph);
+                for (int y = 0; y < NP; ++y) next();
+                const int sk = st;  // the next K's
+                const uint32_t phk = ph;
+                for (int y = 0; y < NP; ++y) next();
+                auto landed = [&](int s0, uint32_t p0) {
+                    bool all = true;
+#pragma unroll
+                    for (int y = 0; y < NP; ++y) {
+                        const int at = s0 + y < NS ? s0 + y : s0 + y - NS;
+                        all = all && wait(b_full + 8 * at, s0 + y < NS ? p0 : p0 ^ 1u);
+                    }
+                    return all;
+                };
+                ok = landed(sv, phv);
+                if (j + 1 < nk) ok = ok && landed(sk, phk);
                 if (Cf::Sep && j + 1 < nk) {  // the next scores, while the softmax of these runs
                     ok = ok && wait(b_sf + 8 * i, (uint32_t)j & 1u);
                     tc::fence_after_sync();
-                    if (ok) scores(st);
+                    if (ok) scores(sk);
                 }
-                ok = ok && wait(b_full + 8 * sv, phv);
                 if (j == nk - 1 && tail < kPfKeys) ok = ok && wait(b_fix, 0u);
                 ok = ok && wait(b_p + 8 * i, (uint32_t)j & 1u);
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
-                const uint64_t vd = v0 + (uint64_t)((sv * Cf::Tile) >> 4);
                 if (leader) {  // O += P V
 #pragma unroll
-                    for (int ks = 0; ks < kPfKeys / 16; ++ks)
-                        tc::mma_f16_ta(to, tp + 8 * ks, vd + (uint64_t)((ks * 2048) >> 4), id_o, (j | ks) != 0);
-                    if (Cf::Sep || j + 1 == nk) tc::commit(b_o + 8 * i);
-                    release(sv);
+                    for (int y = 0; y < NP; ++y) {
+                        const int at = sv + y < NS ? sv + y : sv + y - NS;
+                        const uint64_t vd = v0 + (uint64_t)((at * Cf::Tile) >> 4);
+#pragma unroll
+                        for (int x = 0; x < NP - y; ++x)  // P's part x by V's part y
+#pragma unroll
+                            for (int ks = 0; ks < kPfKeys / 16; ++ks)
+                                tc::mma_f16_ta(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint64_t)((ks * 2048) >> 4), id_o,
+                                               (j | x | y | ks) != 0);
+                        if (y == NP - 1 && (Cf::Sep || j + 1 == nk)) tc::commit(b_o + 8 * i);
+                        release(at);
+                    }
                 }
                 __syncwarp();
-                if (!Cf::Sep && j + 1 < nk) scores(st);
+                if (!Cf::Sep && j + 1 < nk) scores(sk);
             }
             if (!ok && leader) fail();
             if (leader) {  // nothing is in flight when the CTA ends
@@ -374,7 +433,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const uint32_t tp = taddr + lanes + Cf::ColP + Cf::PStep * i;
             const uint32_t bx = b_x + 8 * (4 * i + (warp & 3));
             float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * Cf::XBuf * i;  // [buffer][half][row]
-            const float c = p.scale * 1.4426950408889634f;
+            float c = p.scale * 1.4426950408889634f, vback = 1.f;
+            if constexpr (NP == 2) {  // the powers of two of Q's row, K and V back
+                c *= pf_back(p.maxima[hk]) * (live ? p.qback[(size_t)(t.row0 + tok) * p.H + hk * G + g] : 0.f);
+                vback = pf_back(p.maxima[p.kv.hkv + hk]);
+            }
             // a row's value of the other column half, exchange number n: its warp
             // has read the one before from `buf` by the time it is written again
             // (two buffers, or S of the next key tile comes after every warp's P)
@@ -445,10 +508,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         }
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : -m * c;
+                const float mc = (m == -INFINITY ? 0.f : -m * c) + PfT<T>::PExp;
                 const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
                 uint64_t sum[2] = {0ull, 0ull};
-                // (P over S's columns 0..63: both halves have read theirs, the exchange)
+                // (one part over S's columns 0..63: both halves have read theirs, the exchange)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
@@ -457,9 +520,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         const uint64_t x = fma_f32x2(pair_u32(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mc2);
                         const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
                         sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
-                        w[e] = pack2<T>(a, b);
+                        w[e] = pack2<M>(a, b);
+                        if constexpr (NP == 2) {  // what the high part leaves
+                            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                            s[32 * q + e] = pack2<M>(a - h.x, b - h.y);
+                        }
                     }
-                    tc::st16(tp + 32 * hf + 16 * q, w);
+                    tc::st16(tp + (NP == 2 ? 64 * hf + 32 * q : 32 * hf + 16 * q), w);
+                    if constexpr (NP == 2) tc::st16(tp + 64 * hf + 32 * q + 16, s + 32 * q);
                 }
                 const uint64_t s2 = add_f32x2(sum[0], sum[1]);
                 l += lo_f32(s2) + hi_f32(s2);
@@ -475,7 +543,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (!ok && lane == 0) fail();
             if (ok && !*abort_flag) {
                 tc::fence_after_sync();
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = (l == 0.f ? 0.f : 1.f / l) * vback;
                 const int row = t.row0 + tok, head = hk * G + g;
                 T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / 2) * hf;
                 float worst = 0.f;  // NaN or infinite where a value is
@@ -484,21 +552,27 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     uint32_t o[32];
                     tc::ld32(to + (D / 2) * hf + 32 * q, o);
                     tc::wait_ld32(o);
-                    uint4 w[4];
+                    uint4 w[sizeof(T) * 2];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
                         worst = fmaf(a, 0.f, fmaf(b, 0.f, worst));
-                        ww[e] = pack2<T>(a, b);
+                        if constexpr (sizeof(T) == 4) {
+                            ww[2 * e] = __float_as_uint(a);
+                            ww[2 * e + 1] = __float_as_uint(b);
+                        } else {
+                            ww[e] = pack2<T>(a, b);
+                        }
                     }
                     if (live)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4 *>(dst + 32 * q + 8 * e) = w[e];
+                        for (int e = 0; e < (int)sizeof(T) * 2; ++e)
+                            *(reinterpret_cast<uint4 *>(dst + 32 * q) + e) = w[e];
                 }
                 // rows that are not finite: by the definition (whole rows, after
                 // both halves have stored theirs); Q's tile is free by now
-                worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::Tile), ok);
+                worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::QTile), ok);
                 unsigned again = __ballot_sync(0xffffffffu, ok && live && hf == 0 && worst != 0.f);
                 while (again) {
                     const int src = __ffs(again) - 1;
@@ -526,15 +600,175 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) q4attn_prefill_rows_kernel(const __grid_constant__ PrefillParams p) {
+// ---------------------------------------------------------------- fp32 caches
+// q4attn_prefill_scale_kernel finds the largest finite |k| and |v| of each kv
+// head over the positions the call attends, and writes Q's two f16 parts (a
+// power of two per row and head puts its largest value in [2^13, 2^14)) with
+// the factors back; q4attn_prefill_split_kernel then writes the attended
+// positions' K and V parts, scaled by their head's power of two, into images
+// laid out like the pages ([part][page][kv head][slot][D]), so that the tensor
+// maps of a 16-bit cache fit.  Shared pages get the same values from every
+// sequence.  Values 2^16 below their head's largest and more lose relative
+// precision (the parts' step is 2^-40 of the largest value).
+
+constexpr int kPfChunk = 64;  // positions of a staging item
+
+// The power of two for a largest magnitude given as fp32 bits, and its inverse.
+__device__ __forceinline__ int pf_exp(uint32_t bits) {
+    const float mx = __uint_as_float(bits);
+    if (!(mx > 0.f)) return 0;
+    int e;
+    frexpf(mx, &e);
+    return min(max(14 - e, -126), 126);
+}
+
+__device__ __forceinline__ float pf_back(uint32_t bits) { return ldexpf(1.f, -pf_exp(bits)); }
+
+// hi and lo parts of four scaled values
+__device__ __forceinline__ void pf_split4(float4 v, float f, uint2 &hi, uint2 &lo) {
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    hi = make_uint2(pack2<__half>(v.x, v.y), pack2<__half>(v.z, v.w));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&hi.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi.y));
+    lo = make_uint2(pack2<__half>(v.x - a.x, v.y - a.y), pack2<__half>(v.z - b.x, v.w - b.y));
+}
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a < INFINITY ? a : 0.f;
+}
+
+// fn(sequence, kv head, first position, end) for this CTA's items: the chunks
+// of every sequence's attended positions (from a key tile's start) by kv heads.
+template <class F>
+__device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
+    __shared__ long long prefix[kMaxSeqs + 1];
+    __shared__ long long wsum[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto range = [&](int b, int &lo, int &end) {
+        const int begin = min(max(p.cu[b], 0), p.rows), rows = max(min(p.cu[b + 1], p.rows) - begin, 0);
+        const int first = p.start ? p.start[b] : 0;
+        lo = end = 0;
+        if (rows == 0 || first < 0 || first >= (long long)p.kv.width * p.kv.page) return;
+        end = (int)min((long long)first + rows, (long long)p.kv.width * p.kv.page);
+        lo = (p.window > 0 && first + 1 > p.window ? first + 1 - p.window : 0) & ~(kPfKeys - 1);
+    };
+    long long n[4], own = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int b = 4 * tid + i;
+        int lo = 0, end = 0;
+        if (b < p.kv.nseq) range(b, lo, end);
+        n[i] = (end - lo + kPfChunk - 1) / kPfChunk;
+        own += n[i];
+    }
+    long long inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long base = inc - own;
+    for (int w = 0; w < warp; ++w) base += wsum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (4 * tid + i <= p.kv.nseq) prefix[4 * tid + i] = base;
+        base += n[i];
+    }
+    if (tid == 255 && p.kv.nseq == kMaxSeqs) prefix[kMaxSeqs] = base;
+    __syncthreads();
+    const long long total = prefix[p.kv.nseq] * p.kv.hkv;
+    for (long long it = blockIdx.x; it < total; it += gridDim.x) {
+        const long long c = it / p.kv.hkv;
+        const int hk = (int)(it - c * p.kv.hkv);
+        int b = 0, hi = p.kv.nseq;
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (prefix[mid] <= c)
+                b = mid;
+            else
+                hi = mid;
+        }
+        int lo, end;
+        range(b, lo, end);
+        const int at = lo + (int)(c - prefix[b]) * kPfChunk;
+        fn(b, hk, at, min(end, at + kPfChunk));
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_constant__ PrefillParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x;
-    int seq, pos;
-    if (!locate_row(p, row, lane, seq, pos)) return;
-    for (int h = threadIdx.x >> 5; h < p.H; h += 8) attn_row<T, D>(p, row, h, seq, pos, lane);
+    constexpr int L = D / 4;  // lanes of a row
+    const int tid = threadIdx.x, lane = tid & 31, j = 4 * (tid % L);
+    pf_items(p, [&](int b, int hk, int at, int end) {
+        float mk = 0.f, mv = 0.f;
+#pragma unroll 4
+        for (int pos = at + tid / L; pos < end; pos += 256 / L) {
+            const int col = pos / p.kv.page, page = page_at(p.kv, b, col);
+            if (page < 0) continue;
+            const size_t off = row_off(p.kv, page, hk, pos - col * p.kv.page, D) + j;
+            const float4 k = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off);
+            const float4 v = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off);
+            mk = fmaxf(fmaxf(mk, fmaxf(finite_abs(k.x), finite_abs(k.y))), fmaxf(finite_abs(k.z), finite_abs(k.w)));
+            mv = fmaxf(fmaxf(mv, fmaxf(finite_abs(v.x), finite_abs(v.y))), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+        }
+        if (lane == 0) {  // non-negative floats order like their bits
+            atomicMax(p.maxima + hk, __float_as_uint(mk));
+            atomicMax(p.maxima + p.kv.hkv + hk, __float_as_uint(mv));
+        }
+    });
+    const size_t units = (size_t)p.rows * p.H, part = units * D;
+    for (size_t u0 = (size_t)blockIdx.x * (256 / L); u0 < units; u0 += (size_t)gridDim.x * (256 / L)) {
+        const size_t u = u0 + tid / L;
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (u < units) q = *reinterpret_cast<const float4 *>((const float *)p.q + u * D + j);
+        float m = fmaxf(fmaxf(finite_abs(q.x), finite_abs(q.y)), fmaxf(finite_abs(q.z), finite_abs(q.w)));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = pf_exp(__float_as_uint(m));
+        if (u < units) {
+            uint2 hi, lo;
+            pf_split4(q, ldexpf(1.f, e), hi, lo);
+            *reinterpret_cast<uint2 *>(p.qimg + u * D + j) = hi;
+            *reinterpret_cast<uint2 *>(p.qimg + part + u * D + j) = lo;
+            if (j == 0) p.qback[u] = ldexpf(1.f, -e);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) q4attn_prefill_split_kernel(const __grid_constant__ PrefillParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int L = D / 4;
+    const int tid = threadIdx.x, j = 4 * (tid % L);
+    const size_t part = (size_t)p.kv.num_pages * p.kv.hkv * p.kv.page * D;
+    pf_items(p, [&](int b, int hk, int at, int end) {
+        const float fk = ldexpf(1.f, pf_exp(p.maxima[hk])), fv = ldexpf(1.f, pf_exp(p.maxima[p.kv.hkv + hk]));
+#pragma unroll 4
+        for (int pos = at + tid / L; pos < end; pos += 256 / L) {
+            const int col = pos / p.kv.page, page = page_at(p.kv, b, col);
+            if (page < 0) continue;
+            const size_t off = row_off(p.kv, page, hk, pos - col * p.kv.page, D) + j;
+            const float4 k = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off);
+            const float4 v = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off);
+            uint2 hi, lo;
+            pf_split4(k, fk, hi, lo);
+            *reinterpret_cast<uint2 *>(p.kimg + off) = hi;
+            *reinterpret_cast<uint2 *>(p.kimg + part + off) = lo;
+            pf_split4(v, fv, hi, lo);
+            *reinterpret_cast<uint2 *>(p.vimg + off) = hi;
+            *reinterpret_cast<uint2 *>(p.vimg + part + off) = lo;
+        }
+    });
 }
 
 }  // namespace dev
@@ -561,17 +795,17 @@ EncodeTiled encode_tiled() {
 
 // A row-major map of 16-bit values with boxes of 64 values (128 bytes) by
 // box[1 ..] rows, 128-byte swizzled; dims innermost first.
-bool make_map(CUtensorMap *m, bool bf16, void *base, int rank, const cuuint64_t *dims, const cuuint32_t *box) {
+bool make_map(CUtensorMap *m, bool bf16, const void *base, int rank, const cuuint64_t *dims, const cuuint32_t *box) {
     EncodeTiled enc = encode_tiled();
     if (!enc) return false;
-    cuuint64_t strides[4];
+    cuuint64_t strides[5];
     cuuint64_t s = 2;
     for (int i = 0; i + 1 < rank; ++i) {
         s *= dims[i];
         strides[i] = s;
     }
     const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, base,
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
                dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -592,45 +826,69 @@ cudaLaunchConfig_t pdl_config(unsigned grid, unsigned block, size_t smem, cudaSt
 
 }  // namespace
 
-template <int D>
-static int launch_rows(const PrefillParams &p, cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)p.rows, 256, 0, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_rows_kernel<float, D>, p) == cudaSuccess ? 0 : -1;
+// The fp32 form's workspace: the heads' maxima, Q's factors back and parts,
+// K's and V's parts.
+size_t prefill_workspace(PrefillParams &p, int num_pages, int page, uint8_t *ws) {
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t q = (size_t)p.rows * p.H, kv = (size_t)num_pages * p.kv.hkv * page * p.D;
+    size_t at = 0;
+    p.maxima = (uint32_t *)(ws + at);
+    at += up(2 * sizeof(uint32_t) * p.kv.hkv);
+    p.qback = (float *)(ws + at);
+    at += up(q * sizeof(float));
+    p.qimg = (uint16_t *)(ws + at);
+    at += up(2 * q * p.D * sizeof(uint16_t));
+    p.kimg = (uint16_t *)(ws + at);
+    at += up(2 * kv * sizeof(uint16_t));
+    p.vimg = (uint16_t *)(ws + at);
+    return at + up(2 * kv * sizeof(uint16_t));
 }
 
 template <typename T, int D>
-static int launch_tc(const PrefillParams &p, cudaStream_t stream) {
+static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
+    constexpr int NP = dev::PfT<T>::Parts;
+    using Cf = dev::PfCfg<D, NP>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
     // positions a copy box takes: a power of two that divides the page, so
     // that no box crosses a page's end (one page alone: whole key tiles)
     int box_rows = 128;
     while (p.kv.width > 1 && p.kv.page % box_rows != 0) box_rows /= 2;
+    const void *q = p.q, *k = p.kv.k, *v = p.kv.v;
+    cudaLaunchAttribute attr;
+    if (NP == 2) {  // the parts of Q, K and V
+        q = p.qimg;
+        k = p.kimg;
+        v = p.vimg;
+        if (cudaMemsetAsync(p.maxima, 0, 2 * sizeof(uint32_t) * p.kv.hkv, stream) != cudaSuccess) return -1;
+        cudaLaunchConfig_t cfg = pdl_config(4u * sms, 256, 0, stream, &attr);
+        if (cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_scale_kernel<D>, p) != cudaSuccess ||
+            cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_split_kernel<D>, p) != cudaSuccess)
+            return -1;
+    }
     CUtensorMap mq, mk, mv;
-    const cuuint64_t qd[3] = {(cuuint64_t)D, (cuuint64_t)p.H, (cuuint64_t)p.rows};
-    const cuuint32_t qb[3] = {64, (cuuint32_t)G, (cuuint32_t)TQ};
-    const cuuint64_t kd[4] = {(cuuint64_t)D, (cuuint64_t)p.kv.page, (cuuint64_t)p.kv.hkv, (cuuint64_t)p.kv.num_pages};
-    const cuuint32_t kb[4] = {64, (cuuint32_t)box_rows, 1, 1};
-    if (!make_map(&mq, BF, const_cast<void *>(p.q), 3, qd, qb) || !make_map(&mk, BF, p.kv.k, 4, kd, kb) ||
-        !make_map(&mv, BF, p.kv.v, 4, kd, kb))
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)p.H, (cuuint64_t)p.rows, (cuuint64_t)NP};
+    const cuuint32_t qb[4] = {64, (cuuint32_t)G, (cuuint32_t)TQ, 1};
+    const cuuint64_t kd[5] = {(cuuint64_t)D, (cuuint64_t)p.kv.page, (cuuint64_t)p.kv.hkv, (cuuint64_t)p.kv.num_pages,
+                              (cuuint64_t)NP};
+    const cuuint32_t kb[5] = {64, (cuuint32_t)box_rows, 1, 1, 1};
+    if (!make_map(&mq, BF, q, 4, qd, qb) || !make_map(&mk, BF, k, 5, kd, kb) || !make_map(&mv, BF, v, 5, kd, kb))
         return -1;
     auto kern = dev::q4attn_prefill_tc_kernel<T, D>;
     static size_t smem_set[64] = {0};
-    if (!raise_smem(kern, (size_t)dev::PfCfg<D>::Smem, smem_set)) return -1;
+    if (!raise_smem(kern, (size_t)Cf::Smem, smem_set)) return -1;
     // at most one part-filled tile a sequence
-    const long long tiles = (long long)p.rows / (2 * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows);
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(tiles * p.kv.hkv), dev::kPfThreads, dev::PfCfg<D>::Smem, stream, &attr);
+    const long long tiles = (long long)p.rows / (Cf::NT * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows);
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(tiles * p.kv.hkv), dev::kPfThreads, Cf::Smem, stream, &attr);
     return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows) == cudaSuccess ? 0 : -1;
 }
 
-int launch_prefill(const PrefillParams &p, int dtype, void *stream_) {
+int launch_prefill(const PrefillParams &p, int dtype, int sms, void *stream_) {
     cudaStream_t s = (cudaStream_t)stream_;
     switch (dtype) {
-        case 0: return p.D == 64 ? launch_rows<64>(p, s) : launch_rows<128>(p, s);
-        case 1: return p.D == 64 ? launch_tc<__half, 64>(p, s) : launch_tc<__half, 128>(p, s);
-        case 2: return p.D == 64 ? launch_tc<__nv_bfloat16, 64>(p, s) : launch_tc<__nv_bfloat16, 128>(p, s);
+        case 0: return p.D == 64 ? launch_tc<float, 64>(p, sms, s) : launch_tc<float, 128>(p, sms, s);
+        case 1: return p.D == 64 ? launch_tc<__half, 64>(p, sms, s) : launch_tc<__half, 128>(p, sms, s);
+        case 2: return p.D == 64 ? launch_tc<__nv_bfloat16, 64>(p, sms, s) : launch_tc<__nv_bfloat16, 128>(p, sms, s);
     }
     return -1;
 }

@@ -978,7 +978,13 @@ extern "C" q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, cons
 
 extern "C" size_t q4_attn_prefill_workspace_bytes(const q4_kv_pages *pages, int32_t rows, int32_t H) {
     if (check_pages_shape(pages) != Q4_OK || check_heads(pages, H) != Q4_OK || rows < 0 || rows > (1 << 24)) return 0;
-    return 0;
+    if (pages->dtype != Q4_T_F32 || rows == 0) return 0;  // the 16-bit forms need none
+    q4::PrefillParams p{};
+    p.rows = rows;
+    p.H = H;
+    p.D = pages->head_dim;
+    p.kv.hkv = pages->kv_heads;
+    return q4::prefill_workspace(p, pages->num_pages, pages->page_size, nullptr);
 }
 
 extern "C" q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows, const int32_t *cu_rows,
@@ -1008,12 +1014,14 @@ extern "C" q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, in
     p.D = pages->head_dim;
     p.window = window;
     p.scale = scale;
-    p.ws = (uint8_t *)workspace;
+    if (need > 0) q4::prefill_workspace(p, pages->num_pages, pages->page_size, (uint8_t *)workspace);
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
     Q4_TRY(kernel_err_ptr(&p.err));
     p.wait_cycles = g_wait_cycles;
     p.extra_tx = g_extra_tx;
     cudaGetLastError();
-    if (q4::launch_prefill(p, pages->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    if (q4::launch_prefill(p, pages->dtype, sms, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
     return Q4_OK;
 }
 

@@ -450,9 +450,16 @@ struct PrefillParams {
     int extra_tx;
     int rows, H, D, window;
     float scale;
-    uint8_t *ws;
+    // fp32 caches, in the workspace: largest |k| and |v| per kv head as bits
+    // [2][hkv], Q's factors back [rows][H], the f16 parts [2][...] of Q, K, V
+    uint32_t *maxima;
+    float *qback;
+    uint16_t *qimg, *kimg, *vimg;
 };
-int launch_prefill(const PrefillParams &p, int dtype, void *stream);
+// Sets the workspace pointers of the fp32 form from `ws` (rows, H, D and
+// kv.hkv of p given) and returns its size.
+size_t prefill_workspace(PrefillParams &p, int num_pages, int page, uint8_t *ws);
+int launch_prefill(const PrefillParams &p, int dtype, int sms, void *stream);
 
 // Token log probabilities (logprobs.cu).
 struct LogprobParams {
