@@ -738,14 +738,26 @@ def q4_gemm(W: Q4Weight, x, accumulate: bool = False, out=None, workspace=None):
 
 # ---------------------------------------------------------------- paged KV cache
 
-def _stream_of(device):
-    """The current stream of the tensors' device (which need not be the
-    current device: the calls below make it current for their launch)."""
-    return _torch().cuda.current_stream(device).cuda_stream
+def _launch(device, fn, *args):
+    """Call `fn` with the raw handle of the current stream of the tensors'
+    device appended, that device being current (it need not be the caller's)."""
+    torch = _torch()
+    index = device.index
+    if torch.cuda.current_device() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
-def _ints(t, name, numel, device):
-    return _dev_buf(t, name, _torch().int32, (numel,), device).data_ptr()
+def _ptr(t, name, dtype, shape, device):
+    """Address of a contiguous `dtype` tensor of exactly `shape` on `device`;
+    anything else raises (_dev_buf says what is wrong)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev_buf(t, name, dtype, shape, device).data_ptr()
 
 
 class KVPages:
@@ -774,9 +786,26 @@ class KVPages:
         self.dtype, self.device = k.dtype, k.device
         self._c = _CKvPages(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), kinds[k.dtype],
                             self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.nseq, self.width)
+        self._ref = ctypes.byref(self._c)
+        self.itemsize = self.k.element_size()
+        self.nbytes = self.k.numel() * self.itemsize  # of the k pages, and of the v pages
+        self._paged_ws = {}
 
     def cref(self):
-        return ctypes.byref(self._c)
+        return self._ref
+
+
+    def workspace_bytes(self, call: str, heads: int, rows: int = 0) -> int:
+        """Workspace bytes of ``q4_attn_paged`` ("paged") or of
+        ``q4_attn_prefill`` ("prefill") with ``heads`` query heads."""
+        if call == "paged":
+            n = self._paged_ws.get(heads)  # by the shapes alone
+            if n is None:
+                n = self._paged_ws[heads] = int(lib().q4_attn_paged_workspace_bytes(self._ref, heads))
+            return n
+        if self._c.dtype != 0 and rows >= 0:
+            return 0
+        return int(lib().q4_attn_prefill_workspace_bytes(self._ref, rows, heads))
 
 
 def _pages(pages):
@@ -792,25 +821,24 @@ def _rope_args(rope, head_dim, device):
     torch = _torch()
     if not isinstance(cos_t, torch.Tensor) or cos_t.dim() != 2 or cos_t.shape[1] != head_dim // 2:
         raise ValueError("rope tables must be [positions, head_dim/2]")
-    n = int(cos_t.shape[0])
-    return (_dev_buf(cos_t, "rope cos", torch.float32, (n, head_dim // 2), device).data_ptr(),
-            _dev_buf(sin_t, "rope sin", torch.float32, (n, head_dim // 2), device).data_ptr(), n)
+    shape = cos_t.shape
+    return (_ptr(cos_t, "rope cos", torch.float32, shape, device),
+            _ptr(sin_t, "rope sin", torch.float32, shape, device), shape[0])
 
 
-def _heads3(t, name, dtype, head_dim, device):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != head_dim:
+def _heads3(t, name, head_dim):
+    """(rows, heads) of a [rows, heads, head_dim] tensor."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != 3 or t.shape[2] != head_dim:
         raise ValueError("%s must be [rows, heads, %d]" % (name, head_dim))
-    return _dev_buf(t, name, dtype, t.shape, device)
+    return t.shape[0], t.shape[1]
 
 
-def _apart(out, others):
-    """out must not share memory with the inputs (it is written while they are read)."""
-    if out.numel() == 0:
-        return
-    a, b = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
-    for t in others:
-        if t is not None and t.data_ptr() < b and a < t.data_ptr() + t.numel() * t.element_size():
+def _apart(out, nbytes, *others):
+    """The output at address `out` must not share memory with the inputs
+    (address, bytes): it is written while they are read."""
+    end = out + nbytes
+    for ptr, n in others:
+        if ptr < end and out < ptr + n:
             raise ValueError("out must not overlap the inputs")
 
 
@@ -823,37 +851,37 @@ def q4_kv_append(k, v, pages: KVPages, cu_rows, start=None, q=None, rope=None, q
     type (``q_out``), the form ``q4_attn_prefill`` takes; else returns None."""
     torch = _torch()
     pages = _pages(pages)
-    dev, D = pages.device, pages.head_dim
-    k = _heads3(k, "k", torch.float32, D, dev)
-    rows = int(k.shape[0])
-    _dev_buf(k, "k", torch.float32, (rows, pages.kv_heads, D), dev)
-    _dev_buf(v, "v", torch.float32, (rows, pages.kv_heads, D), dev)
-    cu = _ints(cu_rows, "cu_rows", pages.nseq + 1, dev)
-    st = None if start is None else _ints(start, "start", pages.nseq, dev)
+    dev, D, i32, f32 = pages.device, pages.head_dim, torch.int32, torch.float32
+    rows, _ = _heads3(k, "k", D)
+    kp = _ptr(k, "k", f32, (rows, pages.kv_heads, D), dev)
+    vp = _ptr(v, "v", f32, (rows, pages.kv_heads, D), dev)
+    cu = _ptr(cu_rows, "cu_rows", i32, (pages.nseq + 1,), dev)
+    st = None if start is None else _ptr(start, "start", i32, (pages.nseq,), dev)
     cp, sp, rope_rows = _rope_args(rope, D, dev)
-    H = 0
+    H, qp, op = 0, None, None
     if q is not None:
-        q = _heads3(q, "q", torch.float32, D, dev)
-        H = int(q.shape[1])
-        if int(q.shape[0]) != rows:
-            raise ValueError("q has %d rows, k %d" % (int(q.shape[0]), rows))
+        n, H = _heads3(q, "q", D)
+        if n != rows:
+            raise ValueError("q has %d rows, k %d" % (n, rows))
+        shape = (rows, H, D)
+        qp = _ptr(q, "q", f32, shape, dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=pages.dtype, device=dev)
-        _dev_buf(q_out, "q_out", pages.dtype, q.shape, dev)
-        _apart(q_out, (q, k, v))
+            q_out = torch.empty(shape, dtype=pages.dtype, device=dev)
+        op = _ptr(q_out, "q_out", pages.dtype, shape, dev)
+        if rows:
+            nb = 4 * rows * D
+            _apart(op, rows * H * D * pages.itemsize, (qp, nb * H), (kp, nb * pages.kv_heads), (vp, nb * pages.kv_heads))
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    with torch.cuda.device(dev):
-        _check(lib().q4_kv_append(pages.cref(), None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), rows,
-                                  cu, st, H, cp, sp, rope_rows, None if q is None else q_out.data_ptr(),
-                                  _stream_of(dev)), "q4_kv_append")
+    _check(_launch(dev, lib().q4_kv_append, pages._ref, qp, kp, vp, rows, cu, st, H, cp, sp, rope_rows, op),
+           "q4_kv_append")
     return q_out
 
 
 def q4_attn_prefill_workspace(pages: KVPages, rows: int, heads: int):
     """A workspace for ``q4_attn_prefill`` with up to ``rows`` rows (None where
-    the call needs none)."""
-    n = int(lib().q4_attn_prefill_workspace_bytes(_pages(pages).cref(), int(rows), int(heads)))
+    the call needs none: the 16-bit caches)."""
+    n = _pages(pages).workspace_bytes("prefill", int(heads), int(rows))
     return _torch().empty(n, dtype=_torch().uint8, device=pages.device) if n else None
 
 
@@ -865,33 +893,34 @@ def q4_attn_prefill(q, pages: KVPages, cu_rows, start=None, window: int = 0, sca
     ``[rows, H, D]`` of the same type; ``scale`` defaults to 1/sqrt(D)."""
     torch = _torch()
     pages = _pages(pages)
-    dev, D = pages.device, pages.head_dim
-    q = _heads3(q, "q", pages.dtype, D, dev)
-    rows, H = int(q.shape[0]), int(q.shape[1])
-    cu = _ints(cu_rows, "cu_rows", pages.nseq + 1, dev)
-    st = None if start is None else _ints(start, "start", pages.nseq, dev)
+    dev, D, i32 = pages.device, pages.head_dim, torch.int32
+    rows, H = _heads3(q, "q", D)
+    shape = (rows, H, D)
+    qp = _ptr(q, "q", pages.dtype, shape, dev)
+    cu = _ptr(cu_rows, "cu_rows", i32, (pages.nseq + 1,), dev)
+    st = None if start is None else _ptr(start, "start", i32, (pages.nseq,), dev)
     if out is None:
-        out = torch.empty_like(q)
-    _dev_buf(out, "out", pages.dtype, q.shape, dev)
-    _apart(out, (q, pages.k, pages.v))
+        out = torch.empty(shape, dtype=pages.dtype, device=dev)
+    op = _ptr(out, "out", pages.dtype, shape, dev)
+    if rows:
+        nb = rows * H * D * pages.itemsize
+        _apart(op, nb, (qp, nb), (pages._c.k, pages.nbytes), (pages._c.v, pages.nbytes))
+    wp, wn = None, 0
     if workspace is None:
         workspace = q4_attn_prefill_workspace(pages, rows, H)
     else:
-        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=int(
-            lib().q4_attn_prefill_workspace_bytes(pages.cref(), rows, H)))
-    with torch.cuda.device(dev):
-        _check(lib().q4_attn_prefill(pages.cref(), q.data_ptr(), rows, cu, st, H, int(window),
-                                     1.0 / float(D) ** 0.5 if scale is None else float(scale), out.data_ptr(),
-                                     None if workspace is None else workspace.data_ptr(),
-                                     0 if workspace is None else workspace.numel(), _stream_of(dev)),
-               "q4_attn_prefill")
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=pages.workspace_bytes("prefill", H, rows))
+    if workspace is not None:
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _check(_launch(dev, lib().q4_attn_prefill, pages._ref, qp, rows, cu, st, H, int(window),
+                   1.0 / float(D) ** 0.5 if scale is None else float(scale), op, wp, wn), "q4_attn_prefill")
     return out
 
 
 def q4_attn_paged_workspace(pages: KVPages, heads: int):
     """A (zero-filled) workspace for ``q4_attn_paged``; calls that may run at
     the same time, captured ones too, need one each."""
-    n = int(lib().q4_attn_paged_workspace_bytes(_pages(pages).cref(), int(heads)))
+    n = _pages(pages).workspace_bytes("paged", int(heads))
     return _torch().zeros(max(16, n), dtype=_torch().uint8, device=pages.device)
 
 
@@ -904,29 +933,29 @@ def q4_attn_paged(q, k_new, v_new, pages: KVPages, positions, window: int = 0, s
     Returns out ``[nseq, H, D]`` float32; ``scale`` defaults to 1/sqrt(D)."""
     torch = _torch()
     pages = _pages(pages)
-    dev, D, n = pages.device, pages.head_dim, pages.nseq
-    q = _heads3(q, "q", torch.float32, D, dev)
-    H = int(q.shape[1])
-    if int(q.shape[0]) != n:
-        raise ValueError("q has %d rows, the table %d sequences" % (int(q.shape[0]), n))
-    _dev_buf(k_new, "k_new", torch.float32, (n, pages.kv_heads, D), dev)
-    _dev_buf(v_new, "v_new", torch.float32, (n, pages.kv_heads, D), dev)
-    pos = _ints(positions, "positions", n, dev)
+    dev, D, n, f32 = pages.device, pages.head_dim, pages.nseq, torch.float32
+    got, H = _heads3(q, "q", D)
+    if got != n:
+        raise ValueError("q has %d rows, the table %d sequences" % (got, n))
+    shape, kv_shape = (n, H, D), (n, pages.kv_heads, D)
+    qp = _ptr(q, "q", f32, shape, dev)
+    kp = _ptr(k_new, "k_new", f32, kv_shape, dev)
+    vp = _ptr(v_new, "v_new", f32, kv_shape, dev)
+    pos = _ptr(positions, "positions", torch.int32, (n,), dev)
     cp, sp, rope_rows = _rope_args(rope, D, dev)
     if out is None:
-        out = torch.empty((n, H, D), dtype=torch.float32, device=dev)
-    _dev_buf(out, "out", torch.float32, (n, H, D), dev)
-    _apart(out, (q, k_new, v_new, pages.k, pages.v))
+        out = torch.empty(shape, dtype=f32, device=dev)
+    op = _ptr(out, "out", f32, shape, dev)
+    nb = 4 * n * D
+    _apart(op, nb * H, (qp, nb * H), (kp, nb * pages.kv_heads), (vp, nb * pages.kv_heads),
+           (pages._c.k, pages.nbytes), (pages._c.v, pages.nbytes))
     if workspace is None:  # zero-filled: its counters start at zero
         workspace = q4_attn_paged_workspace(pages, H)
     else:
-        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=int(
-            lib().q4_attn_paged_workspace_bytes(pages.cref(), H)))
-    with torch.cuda.device(dev):
-        _check(lib().q4_attn_paged(pages.cref(), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), pos, H, int(window),
-                                   1.0 / float(D) ** 0.5 if scale is None else float(scale), cp, sp, rope_rows,
-                                   out.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(dev)),
-               "q4_attn_paged")
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=pages.workspace_bytes("paged", H))
+    _check(_launch(dev, lib().q4_attn_paged, pages._ref, qp, kp, vp, pos, H, int(window),
+                   1.0 / float(D) ** 0.5 if scale is None else float(scale), cp, sp, rope_rows, op,
+                   workspace.data_ptr(), workspace.numel()), "q4_attn_paged")
     return out
 
 
@@ -943,19 +972,19 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
     if logits.dim() != 2 or logits.shape[1] == 0:
         raise ValueError("logits must be [rows, n]")
     dev = logits.device
-    rows, n = (int(x) for x in logits.shape)
+    rows, n = logits.shape
     k = min(int(top), n)
-    f32 = dict(dtype=torch.float32, device=dev)
-    lp = tok = ent = None
+    f32, i32 = torch.float32, torch.int32
+    lp = tok = ent = lpp = entp = None
     if tokens is not None:
-        tok = _ints(tokens, "tokens", rows, dev)
-        lp = torch.empty(rows, **f32)
+        tok = _ptr(tokens, "tokens", i32, (rows,), dev)
+        lp = torch.empty(rows, dtype=f32, device=dev)
+        lpp = lp.data_ptr()
     if entropy:
-        ent = torch.empty(rows, **f32)
-    val = torch.empty((rows, max(0, k)), **f32)
-    idx = torch.empty((rows, max(0, k)), dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().q4_logprobs(logits.data_ptr(), rows, n, tok, k, None if lp is None else lp.data_ptr(),
-                                 None if ent is None else ent.data_ptr(), val.data_ptr() if k > 0 else None,
-                                 idx.data_ptr() if k > 0 else None, _stream_of(dev)), "q4_logprobs")
+        ent = torch.empty(rows, dtype=f32, device=dev)
+        entp = ent.data_ptr()
+    val = torch.empty((rows, max(0, k)), dtype=f32, device=dev)
+    idx = torch.empty((rows, max(0, k)), dtype=i32, device=dev)
+    _check(_launch(dev, lib().q4_logprobs, logits.data_ptr(), rows, n, tok, k, lpp, entp,
+                   val.data_ptr() if k > 0 else None, idx.data_ptr() if k > 0 else None), "q4_logprobs")
     return lp, ent, val, idx

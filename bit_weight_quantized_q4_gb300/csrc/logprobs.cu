@@ -41,12 +41,14 @@ __device__ __forceinline__ unsigned long long lp_pair(uint32_t key, int i) {
     return ((unsigned long long)key << 32) | (0xFFFFFFFFu - (uint32_t)i);
 }
 
-// fn(value, index) for the elements [i0, i1) of row x: scalars up to a 16-byte
-// boundary, then four 16-byte loads in flight a thread, then scalars.
-template <class F>
-__device__ __forceinline__ void lp_each(const float *x, int i0, int i1, int tid, F fn) {
+// The elements [i0, i1) of row x: one(value, index) for those before a 16-byte
+// boundary and after the last whole float4, and batch(float4 x 4, index of the
+// first, step) for four float4 in flight a thread (their elements start at
+// index + q * step); what is left of the vectors goes through one().
+template <class One, class Batch>
+__device__ __forceinline__ void lp_each(const float *x, int i0, int i1, int tid, One one, Batch batch) {
     const int head = min(i1 - i0, (int)((4u - (((uintptr_t)(x + i0) >> 2) & 3u)) & 3u));
-    if (tid < head) fn(x[i0 + tid], i0 + tid);
+    if (tid < head) one(x[i0 + tid], i0 + tid);
     const int v0 = i0 + head, nv = (i1 - v0) >> 2;
     const float4 *xv = reinterpret_cast<const float4 *>(x + v0);
     int j = tid;
@@ -54,26 +56,20 @@ __device__ __forceinline__ void lp_each(const float *x, int i0, int i1, int tid,
         float4 v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = xv[j + q * kLpThreads];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int i = v0 + 4 * (j + q * kLpThreads);
-            fn(v[q].x, i);
-            fn(v[q].y, i + 1);
-            fn(v[q].z, i + 2);
-            fn(v[q].w, i + 3);
-        }
+        batch(v, v0 + 4 * j, 4 * kLpThreads);
     }
     for (; j < nv; j += kLpThreads) {
         const float4 v = xv[j];
         const int i = v0 + 4 * j;
-        fn(v.x, i);
-        fn(v.y, i + 1);
-        fn(v.z, i + 2);
-        fn(v.w, i + 3);
+        one(v.x, i);
+        one(v.y, i + 1);
+        one(v.z, i + 2);
+        one(v.w, i + 3);
     }
     const int tail = v0 + 4 * nv + tid;
-    if (tail < i1) fn(x[tail], tail);
+    if (tail < i1) one(x[tail], tail);
 }
+__device__ __forceinline__ float lp_at(const float4 &v, int e) { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
 
 struct LpSums {
     float m, s, t;
@@ -88,16 +84,35 @@ __device__ __forceinline__ LpSums lp_join(const LpSums &a, const LpSums &b) {
     return {m, a.s * fa + b.s * fb, fa * fmaf(da, a.s, a.t) + fb * fmaf(db, b.s, b.t)};
 }
 
+constexpr int kLpMaxCluster = 8;
+
 struct LpShared {
-    LpSums sums;                       // the CTA's, read by rank 0
-    unsigned long long top[kLpTop];    // the CTA's k best pairs (0: none)
+    // rank 0 of a cluster receives every CTA's sums and k best pairs (0: none)
+    LpSums sums[kLpMaxCluster];
+    unsigned long long top[kLpMaxCluster * kLpTop];
+    unsigned long long mine[kLpTop];   // this CTA's
     unsigned long long cand[kLpCand];
     LpSums warp[kLpThreads / 32];
-    uint32_t quad[kLpQuads];
+    __align__(16) uint32_t quad[kLpQuads];
     unsigned long long best[kLpThreads / 32];
     uint32_t bound;
     int ncand;
 };
+
+// v added to the running sums: a new maximum m rescales what came before.
+__device__ __forceinline__ void lp_raise(LpSums &a, float m) {
+    if (m > a.m) {
+        const float d = fmaxf(a.m - m, -200.f), f = __expf(d);  // from -inf: the sums are zero
+        a.t = f * fmaf(d, a.s, a.t);
+        a.s *= f;
+        a.m = m;
+    }
+}
+__device__ __forceinline__ void lp_add(LpSums &a, float v, float mu) {
+    const float d = v - mu, e = __expf(d);  // NaN stays; -inf: e = 0, and its term of t is 0
+    a.s += e;
+    a.t = fmaf(e, fmaxf(d, -200.f), a.t);
+}
 
 __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_constant__ LogprobParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -109,25 +124,41 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
     const int i0 = min(p.n, rank * per), i1 = min(p.n, i0 + per);
     const float *x = p.logits + (size_t)row * p.n;
     const int k = p.k;
+    // this CTA runs: the matching wait comes before the writes to rank 0
+    if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (tid == 0) sh.ncand = 0;
-    if (tid < kLpTop) sh.top[tid] = 0ull;
+    if (tid < kLpTop) sh.mine[tid] = 0ull;
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     LpSums a = {-INFINITY, 0.f, 0.f};
     uint32_t kmax = 0u;
-    lp_each(x, i0, i1, tid, [&](float v, int) {
-        kmax = max(kmax, lp_key(v));
-        if (v > a.m) {  // a new maximum: rescale what came before
-            const float d = a.m == -INFINITY ? 0.f : fmaxf(a.m - v, -200.f), f = __expf(d);
-            a.t = f * fmaf(d, a.s, a.t);
-            a.s *= f;
-            a.m = v;
-        }
-        const float d = a.m == -INFINITY && v == -INFINITY ? -200.f : fmaxf(v - a.m, -200.f);
-        const float e = v != v ? v : __expf(d);
-        a.s += e;
-        a.t = fmaf(e, d, a.t);
-    });
+    lp_each(
+        x, i0, i1, tid,
+        [&](float v, int) {
+            kmax = max(kmax, lp_key(v));
+            lp_raise(a, v);
+            lp_add(a, v, a.m == -INFINITY ? 0.f : a.m);
+        },
+        [&](const float4 (&v)[4], int, int) {
+            float m = fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w));  // numbers before NaN
+#pragma unroll
+            for (int q = 1; q < 4; ++q) m = fmaxf(m, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
+            kmax = max(kmax, lp_key(m));
+            lp_raise(a, m);
+            const float mu = a.m == -INFINITY ? 0.f : a.m;
+            LpSums c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                c[q] = {0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) lp_add(c[q], lp_at(v[q], e), mu);
+            }
+            a.s += (c[0].s + c[1].s) + (c[2].s + c[3].s);
+            a.t += (c[0].t + c[1].t) + (c[2].t + c[3].t);
+        });
+    uint32_t kq = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
+    kq = max(kq, __shfl_xor_sync(0xffffffffu, kq, 2));
+    if ((lane & 3) == 0) sh.quad[tid >> 2] = kq;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         const LpSums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
@@ -135,12 +166,23 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
         // the lower lane's share first: both lanes get the same sum
         a = (lane & o) ? lp_join(b, a) : lp_join(a, b);
     }
-    uint32_t kq = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
-    kq = max(kq, __shfl_xor_sync(0xffffffffu, kq, 2));
-    if ((lane & 3) == 0) sh.quad[tid >> 2] = kq;
     if (lane == 0) sh.warp[warp] = a;
     __syncthreads();
-    if (warp == 0) {
+    if (k > 0) {
+        if (tid >= 32 && tid < 32 + kLpQuads) {  // warps 1..4: the k-th largest of the quads' maxima
+            const int q = tid - 32;
+            const uint32_t mine = sh.quad[q];
+            int r = 0;
+#pragma unroll 8
+            for (int j = 0; j < kLpQuads; j += 4) {
+                const uint4 o = *reinterpret_cast<const uint4 *>(sh.quad + j);
+                r += (o.x > mine || (o.x == mine && j < q)) + (o.y > mine || (o.y == mine && j + 1 < q)) +
+                     (o.z > mine || (o.z == mine && j + 2 < q)) + (o.w > mine || (o.w == mine && j + 3 < q));
+            }
+            if (r == k - 1) sh.bound = mine;
+        }
+    }
+    if (warp == 0) {  // meanwhile warp 0 joins the warps' sums
         a = lane < kLpThreads / 32 ? sh.warp[lane] : LpSums{-INFINITY, 0.f, 0.f};
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) {
@@ -148,22 +190,25 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
                               __shfl_xor_sync(0xffffffffu, a.t, o)};
             a = (lane & o) ? lp_join(b, a) : lp_join(a, b);
         }
-        if (lane == 0) sh.sums = a;
     }
     if (k > 0) {
-        if (tid < kLpQuads) {  // the k-th largest of the quads' maxima
-            const uint32_t mine = sh.quad[tid];
-            int r = 0;
-            for (int j = 0; j < kLpQuads; ++j) r += sh.quad[j] > mine || (sh.quad[j] == mine && j < tid);
-            if (r == k - 1) sh.bound = mine;
-        }
         __syncthreads();
         const uint32_t bound = sh.bound;
-        lp_each(x, i0, i1, tid, [&](float v, int i) {
-            const uint32_t key = lp_key(v);
-            if (key >= bound) {
+        const float bv = bound ? lp_value(bound) : 0.f;  // key 0: everything is a candidate
+        auto take = [&](float v, int i) {
+            if (v >= bv || bound == 0u) {
                 const int at = atomicAdd(&sh.ncand, 1);
-                if (at < kLpCand) sh.cand[at] = lp_pair(key, i);
+                if (at < kLpCand) sh.cand[at] = lp_pair(lp_key(v), i);
+            }
+        };
+        lp_each(x, i0, i1, tid, take, [&](const float4 (&v)[4], int i, int step) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float m = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
+                if (m >= bv || bound == 0u) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) take(lp_at(v[q], e), i + q * step + e);
+                }
             }
         });
         __syncthreads();
@@ -172,16 +217,23 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
             for (int c = tid; c < nc; c += kLpThreads) {
                 const unsigned long long mine = sh.cand[c];
                 int r = 0;
+#pragma unroll 8
                 for (int j = 0; j < nc; ++j) r += sh.cand[j] > mine;
-                if (r < k) sh.top[r] = mine;
+                if (r < k) sh.mine[r] = mine;
             }
         } else {  // one by one: the best pair below the last one
             unsigned long long last = ~0ull;
             for (int q = 0; q < k; ++q) {
                 unsigned long long best = 0ull;
-                lp_each(x, i0, i1, tid, [&](float v, int i) {
+                auto look = [&](float v, int i) {
                     const unsigned long long c = lp_pair(lp_key(v), i);
                     if (c < last && c > best) best = c;
+                };
+                lp_each(x, i0, i1, tid, look, [&](const float4 (&v)[4], int i, int step) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) look(lp_at(v[z], e), i + z * step + e);
                 });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
@@ -193,58 +245,54 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
                 best = sh.best[0];
 #pragma unroll
                 for (int w = 1; w < kLpThreads / 32; ++w) best = sh.best[w] > best ? sh.best[w] : best;
-                if (tid == 0) sh.top[q] = best;
+                if (tid == 0) sh.mine[q] = best;
                 last = best;
                 __syncthreads();
             }
         }
     }
+    __syncthreads();
+    // the sums and the best pairs to rank 0
+    if (S > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    LpShared *root = cl.map_shared_rank(&sh, 0);
+    if (tid == 0) root->sums[rank] = a;
+    if (tid < k) root->top[rank * k + tid] = sh.mine[tid];
     if (S > 1)
-        cl.sync();  // every CTA's sums and best pairs are there
+        cl.sync();
     else
         __syncthreads();
-    if (rank == 0) {
-        LpSums all = sh.sums;
-        for (int r = 1; r < S; ++r) all = lp_join(all, *cl.map_shared_rank(&sh.sums, r));
-        // a row whose logits are all -inf allows nothing: log probability
-        // -inf for every token, entropy 0
-        const bool empty = all.m == -INFINITY && all.s == 0.f;
-        const float lse = empty ? 0.f : all.m + logf(all.s);
-        if (tid == 0) {
-            if (p.entropy) p.entropy[row] = empty ? 0.f : logf(all.s) - all.t / all.s;
-            if (p.logprob) {
-                const int tok = p.tokens[row];
-                float lp = 0.f;  // a negative token: a row that is not scored
-                if (tok >= p.n) {
-                    lp = __uint_as_float(0x7fffffffu);
-                    atomicExch(p.err, kErrPaged);
-                } else if (tok >= 0) {
-                    lp = x[tok] - lse;
-                }
-                p.logprob[row] = lp;
+    if (rank != 0) return;
+    LpSums all = sh.sums[0];
+    for (int r = 1; r < S; ++r) all = lp_join(all, sh.sums[r]);
+    // a row whose logits are all -inf allows nothing: log probability -inf for
+    // every token, entropy 0
+    const bool empty = all.m == -INFINITY && all.s == 0.f;
+    const float lse = empty ? 0.f : all.m + logf(all.s);
+    if (tid == 0) {
+        if (p.entropy) p.entropy[row] = empty ? 0.f : logf(all.s) - all.t / all.s;
+        if (p.logprob) {
+            const int tok = p.tokens[row];
+            float lp = 0.f;  // a negative token: a row that is not scored
+            if (tok >= p.n) {
+                lp = __uint_as_float(0x7fffffffu);
+                atomicExch(p.err, kErrPaged);
+            } else if (tok >= 0) {
+                lp = x[tok] - lse;
             }
-        }
-        // merge the CTAs' lists by rank: S * k pairs, all different
-        if (k > 0 && tid < S * kLpTop && (tid & (kLpTop - 1)) < k) {
-            const int r = tid / kLpTop, j = tid & (kLpTop - 1);
-            const unsigned long long mine = cl.map_shared_rank(&sh, r)->top[j];
-            if (mine != 0ull) {
-                int at = j;
-                for (int r2 = 0; r2 < S; ++r2) {
-                    if (r2 == r) continue;
-                    const unsigned long long *o = cl.map_shared_rank(&sh, r2)->top;
-                    int c = 0;  // the lists are sorted: count the larger ones
-                    while (c < k && o[c] > mine) ++c;
-                    at += c;
-                }
-                if (at < k) {
-                    p.top_val[(size_t)row * k + at] = lp_value((uint32_t)(mine >> 32)) - lse;
-                    p.top_idx[(size_t)row * k + at] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-                }
-            }
+            p.logprob[row] = lp;
         }
     }
-    if (S > 1) cl.sync();  // no CTA leaves while rank 0 reads it
+    // the k best of the CTAs' lists, by rank (the pairs are all different)
+    if (tid < S * k) {
+        const unsigned long long mine = sh.top[tid];
+        int at = 0;
+#pragma unroll 8
+        for (int j = 0; j < S * k; ++j) at += sh.top[j] > mine;
+        if (mine != 0ull && at < k) {
+            p.top_val[(size_t)row * k + at] = lp_value((uint32_t)(mine >> 32)) - lse;
+            p.top_idx[(size_t)row * k + at] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
+        }
+    }
 }
 
 }  // namespace dev
