@@ -31,12 +31,14 @@
 
 #include "gemv_launch.cuh"
 #include "paged.cuh"
+#include "tensor_map.h"
 
 namespace q4 {
 namespace dev {
 
-constexpr int kPagedWarps = 8;
-constexpr int kPagedUnit = 16 * kPagedWarps;  // positions of one unit
+constexpr int kPagedWarps = 4;
+constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kPagedOcc = 2;  // CTAs of an SM: eight warps with up to 255 registers each
 
 template <typename T>
 struct PagedT;
@@ -99,14 +101,51 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
+// Four 8 x 8 matrices of 16-bit values from shared memory (lane l gives a row's
+// address), as A fragments; and transposed.
+__device__ __forceinline__ void ldsm4(uint32_t (&a)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&a)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(dst),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
 __device__ __forceinline__ float f_of(const uint4 &v, int i) {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
 }
 __device__ __forceinline__ uint32_t w_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// A warp's step and its ring.  A step takes MT tiles of 16 positions (two share
+// each Q fragment; one where two would leave no room to look ahead), so a unit
+// of the split is 64 MT positions.  A ring item is the K, or the V, of one step;
+// the rings hold about 190 KB of an SM.
+template <typename T, int D>
+struct PagedCfg {
+    static constexpr int Tile = 16 * D * (int)sizeof(T);
+    static constexpr int MT = Tile <= 4096 ? 2 : 1;
+    static constexpr int Step = 16 * MT, Unit = Step * kPagedWarps;
+    static constexpr int Item = MT * Tile;
+    static constexpr int NI = 24 * 1024 / Item;
+    static_assert(NI >= 3, "two items in flight while one is read");
+};
+
 // Shared memory of a CTA: the prefix of units over the sequences, Q's
-// fragments and factors, the warps' maxima and sums, the fold's sums, a flag,
-// then the warps' outputs [warps][G][D] (also the fold's weights).
+// fragments (more than 8 heads: else they live in registers after their
+// preparation) and factors, the warps' maxima and sums, the fold's sums, a
+// flag, then the rings; over them, when a segment's loop is done, the warps'
+// outputs [warps][G][D] and the fold's weights.
 template <typename T, int D, int NT>
 struct PagedSmem {
     static constexpr int Prefix = 0;
@@ -116,27 +155,41 @@ struct PagedSmem {
     static constexpr int Wl = Wm + 4 * kPagedWarps * 8 * NT;
     static constexpr int Fl = Wl + 4 * kPagedWarps * 8 * NT;  // [8 NT] fold sums
     static constexpr int Flag = Fl + 4 * 8 * NT;
-    static constexpr int Red = (Flag + 16 + 15) / 16 * 16;
+    static constexpr int New = (Flag + 16 + 15) / 16 * 16;    // the new k and v in the cache's type [2][D]
+    static constexpr int Bars = New + 2 * D * (int)sizeof(T);
+    static constexpr int Red = (Bars + 8 * kPagedWarps * PagedCfg<T, D>::NI + 1023) / 1024 * 1024;
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128) || NT == 2 ? 1 : 2)
-    q4attn_paged_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
+    q4attn_paged_kernel(const __grid_constant__ PagedAttnParams p, const __grid_constant__ CUtensorMap mk,
+                        const __grid_constant__ CUtensorMap mv) {
     using C = PagedT<T>;
     using M = typename C::M;
     using S = PagedSmem<T, D, NT>;
-    constexpr int KP = C::KP, QP = C::QP, NW = kPagedWarps, KS = D / 16, KB = D / 32, VB = D / 64;
-    constexpr int LV = sizeof(T) == 4 ? 2 : 1;  // 16-byte loads per 8 values
-    extern __shared__ __align__(16) uint8_t smem[];
+    using Cfg = PagedCfg<T, D>;
+    constexpr int KP = C::KP, QP = C::QP, NW = kPagedWarps, KS = D / 16, VB = D / 64;
+    constexpr bool H16 = sizeof(T) == 2;
+    constexpr int MT = Cfg::MT, Step = Cfg::Step, NI = Cfg::NI, Item = Cfg::Item, Tile = Cfg::Tile;
+    constexpr bool QReg = NT == 1;
+    extern __shared__ __align__(1024) uint8_t psm[];  // the swizzle's pattern repeats every 1024 bytes
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int hkv = p.kv.hkv, G = p.H / hkv, nseq = p.kv.nseq;
-    long long *prefix = reinterpret_cast<long long *>(smem + S::Prefix);
-    uint2 *qf = reinterpret_cast<uint2 *>(smem + S::Qf);
-    float *qs = reinterpret_cast<float *>(smem + S::Qs);
-    float *wm = reinterpret_cast<float *>(smem + S::Wm), *wl = reinterpret_cast<float *>(smem + S::Wl);
-    float *fl = reinterpret_cast<float *>(smem + S::Fl);
-    int *flag = reinterpret_cast<int *>(smem + S::Flag);
-    float *red = reinterpret_cast<float *>(smem + S::Red);
+    long long *prefix = reinterpret_cast<long long *>(psm + S::Prefix);
+    uint2 *qf = reinterpret_cast<uint2 *>(psm + S::Qf);
+    float *qs = reinterpret_cast<float *>(psm + S::Qs);
+    float *wm = reinterpret_cast<float *>(psm + S::Wm), *wl = reinterpret_cast<float *>(psm + S::Wl);
+    float *fl = reinterpret_cast<float *>(psm + S::Fl);
+    int *flag = reinterpret_cast<int *>(psm + S::Flag);
+    float *red = reinterpret_cast<float *>(psm + S::Red);
+    T *fresh = reinterpret_cast<T *>(psm + S::New);
+    const uint32_t bars = smem_u32(psm + S::Bars) + 8 * NI * warp;
+    const uint32_t ring = smem_u32(red) + (uint32_t)(warp * NI * Item);
+    uint8_t *ring_p = reinterpret_cast<uint8_t *>(red) + warp * NI * Item;
+    if (lane == 0) {
+        for (int i = 0; i < NI; ++i) mbar_init(bars + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
@@ -147,48 +200,39 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
     auto units_of = [&](int pos) -> int {
         if (pos < 0 || pos >= cap || (p.rope_cos && pos >= p.rope_rows)) return 0;
         const int lo = lo_of(pos) & ~15;
-        return (pos - lo) / kPagedUnit + 1;
+        return (pos - lo) / Cfg::Unit + 1;
     };
-    {  // prefix[b] = units of sequences before b (all kv heads): four sequences a thread
-        int pos[4];
-        long long n[4], own = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = 4 * tid + i;
-            pos[i] = b < nseq ? p.positions[b] : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            n[i] = (long long)units_of(pos[i]) * hkv;
-            own += n[i];
-        }
-        long long inc = own;
+    // prefix[b] = units of sequences before b (all kv heads), a sequence a thread
+    long long W = 0;
+    for (int b0 = 0; b0 < nseq; b0 += kPagedThreads) {
+        const int b = b0 + tid;
+        const long long n = b < nseq ? (long long)units_of(p.positions[b]) * hkv : 0;
+        long long inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        long long *wsum = reinterpret_cast<long long *>(red);
+        long long *wsum = reinterpret_cast<long long *>(red) + ((b0 / kPagedThreads) & 1) * NW;
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
-        long long base = inc - own;
-        for (int w = 0; w < warp; ++w) base += wsum[w];
+        long long before = W;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int b = 4 * tid + i;
-            if (b <= nseq) prefix[b] = base;
-            base += n[i];
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += wsum[w];
+            W += wsum[w];
         }
-        if (tid == 255 && nseq == kMaxSeqs) prefix[nseq] = base;
-        __syncthreads();
+        if (b < nseq) prefix[b + 1] = before + inc;
     }
+    if (tid == 0) prefix[0] = 0;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's room is the rings'
+    __syncthreads();
     // idle rows: zeros
     for (int b = blockIdx.x; b < nseq; b += gridDim.x)
         if (prefix[b + 1] == prefix[b]) {
-            for (int i = tid; i < p.H * D; i += 32 * NW) p.out[(size_t)b * p.H * D + i] = 0.f;
+            for (int i = tid; i < p.H * D; i += kPagedThreads) p.out[(size_t)b * p.H * D + i] = 0.f;
             if (tid == 0 && p.positions[b] >= 0) atomicExch(p.err, kErrPaged);
         }
-    const long long W = prefix[nseq];
     // CTAs with work: never more than units, so that none of a pair's CTAs is
     // without a share (each adds to the pair's count)
     const int N = W < gridDim.x ? (int)W : (int)gridDim.x, cta = blockIdx.x;
@@ -207,6 +251,14 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
     }
     const float qscale = p.scale * 1.4426950408889634f;
     const size_t slot_floats = (size_t)G * (D + 2);
+    // the ring's state, carried over the segments: the slot (and its phase) of
+    // the next item to issue and to read
+    int fill_slot = 0, slot = 0;
+    uint32_t phase = 0;
+    int out = 0;                     // items in flight
+    bool ok = true;                  // no wait of this warp gave up
+    const uint64_t pol = evict_first_policy();
+    uint32_t extra = p.extra_tx;     // testing the give-up path only
 
     for (long long u = u0; u < u1;) {
         while (prefix[b + 1] <= u) ++b;
@@ -220,6 +272,122 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
         const bool owner = ue == s1;  // this segment ends with the new token
         const float *cosr = p.rope_cos ? p.rope_cos + (size_t)pos * (D / 2) : nullptr;
         const float *sinr = p.rope_cos ? p.rope_sin + (size_t)pos * (D / 2) : nullptr;
+
+        // this warp's steps: first + warp, first + warp + NW, .. below last.  Their
+        // K and V tiles come through the warp's own ring in shared memory by TMA
+        // (16-bit: 16 rows x 64 values a box, swizzled; fp32: whole rows), each
+        // slot on its mbarrier: item 2 i is the K of its i-th step, 2 i + 1 the V.
+        // (16-byte copies by the lanes themselves measured the same 4.5 TB/s as
+        // loads into registers: the load path, not the room, was full.)
+        const int new_step = (pos - base16) / Step;  // the step of the new token, the last of all
+        const int first = st * NW + warp, last = min((st + n_units) * NW, new_step + 1);
+        const int count = first < last ? (last - first + NW - 1) / NW : 0;
+        int fill_n = 0;                    // items issued
+        uint32_t bad = 0;                  // bit (i MT + m) % 32: that tile's page is out of range
+        int page_next[MT], page[MT], slot0[MT];  // table entries of the next step to issue, loaded ahead; this one's
+        auto pages_of = [&](int i) {       // load the i-th step's
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int key = base16 + Step * (first + NW * i) + 16 * m;
+                page_next[m] = i < count && key <= pos ? page_raw(p.kv, b, page_col(p.kv, key)) : -1;
+            }
+        };
+        auto issue = [&]() {
+            const int i = fill_n >> 1;
+            if (i >= count || !ok) return;
+            const int key0 = base16 + Step * (first + NW * i);
+            if ((fill_n & 1) == 0) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int key = key0 + 16 * m;
+                    const uint32_t bit = 1u << ((i * MT + m) & 31);
+                    page[m] = page_ok(p.kv, page_next[m]);
+                    slot0[m] = key - page_col(p.kv, key) * p.kv.page;
+                    bad = page[m] < 0 ? bad | bit : bad & ~bit;
+                    if (page[m] < 0 && key <= pos && lane == 0) atomicExch(p.err, kErrPaged);
+                }
+                pages_of(i + 1);
+            }
+            const bool isv = (fill_n & 1) != 0;
+            const uint32_t dst = ring + (uint32_t)(fill_slot * Item), bar = bars + 8 * fill_slot;
+            __syncwarp();  // every lane has read what the slot held
+            if constexpr (H16) {
+                if (lane == 0) mbar_expect_tx(bar, Item + extra);
+                __syncwarp();
+                if (lane < MT * VB) {  // box: tile m, 64-value block; a page out of range is copied as zeros
+                    const int m = lane / VB, blk = lane - m * VB;
+                    int pg = page[0], sl = slot0[0];
+#pragma unroll
+                    for (int x = 1; x < MT; ++x)
+                        if (m == x) {
+                            pg = page[x];
+                            sl = slot0[x];
+                        }
+                    tma_page(dst + m * Tile + blk * 2048, isv ? &mv : &mk, 64 * blk, sl, hk, pg, bar);
+                }
+            } else if (lane == 0) {  // the attended rows of each tile
+                uint32_t bytes = 0;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int key = key0 + 16 * m, r0 = max(lo - key, 0), r1 = page[m] < 0 ? 0 : min(pos - key + 1, 16);
+                    if (r1 > r0) bytes += (uint32_t)(r1 - r0) * D * 4;
+                }
+                mbar_expect_tx(bar, bytes + extra);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const int key = key0 + 16 * m, r0 = max(lo - key, 0), r1 = page[m] < 0 ? 0 : min(pos - key + 1, 16);
+                    if (r1 > r0)
+                        bulk_g2s(dst + m * Tile + r0 * D * 4,
+                                 (const T *)(isv ? p.kv.v : p.kv.k) + row_off(p.kv, page[m], hk, slot0[m] + r0, D),
+                                 (uint32_t)(r1 - r0) * D * 4, bar, pol);
+                }
+            }
+            extra = 0;
+            ++out;
+            ++fill_n;
+            fill_slot = fill_slot + 1 == NI ? 0 : fill_slot + 1;
+        };
+        // the next item has landed (false: a wait gave up)
+        auto landed = [&]() {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, phase, p.wait_cycles))) {
+                ok = false;
+                if (lane == 0) atomicExch(p.err, 7);
+            }
+            return ok;
+        };
+        auto advance = [&]() {
+            --out;
+            if (++slot == NI) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        // byte offset of 16 bytes of a tile row (dims 16 / size x ..)
+        auto at_of = [&](int m, int r, int x) {
+            if constexpr (H16) return m * Tile + (x >> 3) * 2048 + r * 128 + (((x & 7) ^ (r & 7)) << 4);
+            return m * Tile + r * D * 4 + x * 16;
+        };
+        // a step at an end of the range: the new token's row (its copy may have
+        // come before the append), zeros in V's rows that are not attended
+        auto mend = [&](int i, bool isv) {
+            const int key0 = base16 + Step * (first + NW * i);
+            constexpr int XR = D * (int)sizeof(T) / 16;  // 16-byte parts of a row
+            uint8_t *it = ring_p + slot * Item;
+            for (int y = lane; y < Step * XR; y += 32) {
+                const int r = y / XR, x = y - r * XR, key = key0 + r, m = r >> 4;
+                uint4 *dst = reinterpret_cast<uint4 *>(it + at_of(m, r & 15, x));
+                const bool none = (bad >> ((i * MT + m) & 31)) & 1u;
+                if (key == pos && !none)
+                    *dst = *(reinterpret_cast<const uint4 *>(fresh + (isv ? D : 0)) + x);
+                else if (isv && (key < lo || key > pos || none))
+                    *dst = make_uint4(0u, 0u, 0u, 0u);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the slot's next copy
+            __syncwarp();
+        };
+        pages_of(0);
+        // the first items now, under Q's preparation
+        for (int i = 0; i < NI - 1; ++i) issue();
 
         // the group's query heads: rotated, scaled (log2 units), in parts, as
         // B fragments; lane j < D / 8 holds dims 4j.. and D/2 + 4j..
@@ -256,18 +424,30 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const float4 v = half ? c : a;
-                    const int d = 4 * lane + half * (D / 2), kb = d >> 5, r = d & 31;
-                    const int ks = 2 * kb + ((r >> 2) & 1), ln = gg * 4 + (r >> 3);
+                    const int d = 4 * lane + half * (D / 2);
                     uint32_t w0[QP], w1[QP];
                     split2<M, QP>(v.x * f, v.y * f, w0);
                     split2<M, QP>(v.z * f, v.w * f, w1);
+                    if constexpr (H16) {
+                        // k16 step d / 16: word (d % 16) / 8 of lanes t = (d % 8) / 2 and t + 1
+                        const int ks = d >> 4, ln = gg * 4 + ((d & 7) >> 1), wd = (d >> 3) & 1;
 #pragma unroll
-                    for (int i = 0; i < QP; ++i) qf[((i * NT + nt) * KS + ks) * 32 + ln] = make_uint2(w0[i], w1[i]);
+                        for (int i = 0; i < QP; ++i) {
+                            uint32_t *at = reinterpret_cast<uint32_t *>(qf + ((i * NT + nt) * KS + ks) * 32 + ln) + wd;
+                            at[0] = w0[i];
+                            at[2] = w1[i];
+                        }
+                    } else {
+                        // fp32: a lane's 32 bytes of a row are its k pairs of two steps
+                        const int kb = d >> 5, r = d & 31, ks = 2 * kb + ((r >> 2) & 1), ln = gg * 4 + (r >> 3);
+#pragma unroll
+                        for (int i = 0; i < QP; ++i) qf[((i * NT + nt) * KS + ks) * 32 + ln] = make_uint2(w0[i], w1[i]);
+                    }
                 }
             }
         }
         if (owner && warp < 2) {  // append: warp 0 the new k (rotated), warp 1 the new v
-            const int page = page_at(p.kv, b, pos / p.kv.page);
+            const int col = page_col(p.kv, pos), page = page_at(p.kv, b, col);
             if (page < 0) {
                 if (lane == 0) atomicExch(p.err, kErrPaged);
             } else if (lane < D / 8) {
@@ -276,12 +456,14 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
                 if (warp == 0 && cosr)
                     rotate4(a, c, *reinterpret_cast<const float4 *>(cosr + 4 * lane),
                             *reinterpret_cast<const float4 *>(sinr + 4 * lane));
-                T *dst = (T *)(warp == 0 ? p.kv.k : p.kv.v) + row_off(p.kv, page, hk, pos % p.kv.page, D) + 4 * lane;
+                T *dst = (T *)(warp == 0 ? p.kv.k : p.kv.v) + row_off(p.kv, page, hk, pos - col * p.kv.page, D) + 4 * lane;
                 store4(dst, a);
                 store4(dst + D / 2, c);
+                store4(fresh + warp * D + 4 * lane, a);
+                store4(fresh + warp * D + 4 * lane + D / 2, c);
             }
         }
-        __syncthreads();  // Q's fragments; the appended rows, for this CTA's loads
+        __syncthreads();  // Q's fragments, the new row
 
         float m[NT][2], l[NT][2], qi[NT][2], acc[NT][KS][4];
 #pragma unroll
@@ -298,180 +480,192 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
             for (int j = 0; j < KS; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[nt][j][i] = 0.f;
+        uint2 qr[QReg ? QP * KS : 1];
+        if constexpr (QReg)
+#pragma unroll
+            for (int x = 0; x < QP * KS; ++x) qr[x] = qf[x * 32 + lane];
 
-        uint4 kr[KB][2][LV], vr[VB][4][LV];
-        const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
-        // a step's first position, its first row's element offset (or none)
-        // and the attended rows [r0, r1) of its 16
-        struct Step {
-            size_t off;
-            int r0, r1;
-        };
-        auto step_of = [&](int s) {
-            Step x;
-            const int key0 = base16 + 16 * s;
-            x.r0 = max(lo - key0, 0);
-            x.r1 = min(pos - key0 + 1, 16);
-            x.off = 0;
-            if (x.r1 > x.r0) {
-                const int col = key0 / p.kv.page, page = page_at(p.kv, b, col);
-                if (page < 0) {
-                    x.r1 = 0;
-                    if (lane == 0) atomicExch(p.err, kErrPaged);
-                } else {
-                    x.off = row_off(p.kv, page, hk, key0 - col * p.kv.page, D);
+        for (int i = 0; i < count; ++i) {
+            const int key0 = base16 + Step * (first + NW * i);
+            const bool whole_step = key0 >= lo && key0 + Step - 1 < pos && ((bad >> ((i * MT) & 31)) & ((1u << MT) - 1u)) == 0;
+            if (!landed()) break;
+            if (!whole_step) mend(i, false);
+            // scores: rows g and g + 8 of tile mt, heads 2t and 2t + 1, a sum for each part of Q
+            float sc[MT][NT][QP][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < QP; ++x)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[mt][nt][x][e] = 0.f;
+            const uint32_t kt = ring + slot * Item;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                uint32_t a[MT][KP][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    if constexpr (H16) {
+                        // matrices: rows 0-7 and 8-15, k 0-7 then 8-15
+                        ldsm4(a[mt][0], kt + at_of(mt, lane & 15, 2 * ks + (lane >> 4)));
+                    } else {
+                        // the lane's k pairs of this step: four of its eight values of a 32-value block
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const uint4 v = lds128_at<0>(kt + at_of(mt, g + 8 * rr, 8 * (ks >> 1) + 2 * t + (ks & 1)));
+                            uint32_t w0[KP], w1[KP];
+                            split2<M, KP>(f_of(v, 0), f_of(v, 1), w0);
+                            split2<M, KP>(f_of(v, 2), f_of(v, 3), w1);
+#pragma unroll
+                            for (int y = 0; y < KP; ++y) {
+                                a[mt][y][rr] = w0[y];
+                                a[mt][y][2 + rr] = w1[y];
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < QP; ++x) {
+                        const int at = (x * NT + nt) * KS + ks;
+                        const uint2 bq = QReg ? qr[QReg ? at : 0] : qf[at * 32 + lane];
+#pragma unroll
+                        for (int y = 0; y < KP; ++y)
+                            if (x + y < QP)
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) mma16816<M>(sc[mt][nt][x], a[mt][y], bq.x, bq.y);
+                    }
+            }
+            advance();
+            issue();  // into the slot of the item read before this one
+            uint32_t pw[MT][NT][2][QP];  // P as B fragments: positions 2t.. and 2t + 8.., head g
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float x[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = sc[mt][nt][QP - 1][e];
+#pragma unroll
+                        for (int y = QP - 2; y >= 0; --y) v += sc[mt][nt][y][e];
+                        x[mt][e] = v * qi[nt][e & 1];
+                    }
+                if (!whole_step) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const bool none = (bad >> ((i * MT + mt) & 31)) & 1u;
+                        const int key = key0 + 16 * mt;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = key + g + 8 * (e >> 1);
+                            if (none || at < lo || at > pos) x[mt][e] = -INFINITY;
+                        }
+                    }
+                }
+                float alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float mx = fmaxf(x[0][h], x[0][2 + h]);
+#pragma unroll
+                    for (int mt = 1; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(x[mt][h], x[mt][2 + h]));
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float mn = fmaxf(m[nt][h], mx);
+                    const float mu = mn == -INFINITY ? 0.f : mn;  // nothing attended yet
+                    alpha[h] = ex2(m[nt][h] - mu);
+                    m[nt][h] = mn;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        x[mt][h] = ex2(x[mt][h] - mu + C::PEXP);
+                        x[mt][2 + h] = ex2(x[mt][2 + h] - mu + C::PEXP);
+                        sum += x[mt][h] + x[mt][2 + h];
+                    }
+                    l[nt][h] = fmaf(l[nt][h], alpha[h], sum);
+                }
+                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][j][e] *= alpha[e & 1];
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint32_t w0[QP], w1[QP];
+                    split2<M, QP>(x[mt][0], x[mt][1], w0);
+                    split2<M, QP>(x[mt][2], x[mt][3], w1);
+#pragma unroll
+                    for (int y = 0; y < QP; ++y) {
+                        pw[mt][nt][0][y] = transpose8x8(w0[y]);
+                        pw[mt][nt][1][y] = transpose8x8(w1[y]);
+                    }
                 }
             }
-            return x;
-        };
-        auto load_k = [&](const Step &x) {
-            const T *base = (const T *)p.kv.k + x.off;
+            if (!landed()) break;
+            if (!whole_step) mend(i, true);
+            const uint32_t vt = ring + slot * Item;
+            // outputs: 16-bit, m tile j: dims 16 j + g and + 8; fp32, m tile 4 vb + j:
+            // dims 64 vb + 8 g + j and + 4 (a lane's 32 bytes of a V row are rows of its own tiles)
+            if constexpr (H16) {
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) {
-                const int r = g + 8 * rr;
-                const bool ok = r >= x.r0 && r < x.r1;
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
+                    for (int j = 0; j < KS; ++j) {
+                        uint32_t a[4];
+                        // matrices: dims 0-7 and 8-15 of positions 0-7, then of 8-15
+                        ldsm4t(a, vt + at_of(mt, (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
 #pragma unroll
-                    for (int i = 0; i < LV; ++i)
-                        kr[kb][rr][i] =
-                            ok ? __ldcg(reinterpret_cast<const uint4 *>(base + (size_t)r * D + 32 * kb + 8 * t) + i)
-                               : zero4;
-            }
-        };
-        auto load_v = [&](const Step &x) {
-            const T *base = (const T *)p.kv.v + x.off;
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const int r = 2 * t + (kk & 1) + 8 * (kk >> 1);
-                const bool ok = r >= x.r0 && r < x.r1;
+                            for (int x = QP - 1; x >= 0; --x) mma16816<M>(acc[nt][j], a, pw[mt][nt][0][x], pw[mt][nt][1][x]);
+                    }
+            } else {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
 #pragma unroll
-                    for (int i = 0; i < LV; ++i)
-                        vr[vb][kk][i] =
-                            ok ? __ldcg(reinterpret_cast<const uint4 *>(base + (size_t)r * D + 64 * vb + 8 * g) + i)
-                               : zero4;
+                    for (int mt = 0; mt < MT; ++mt) {
+                        uint4 vr[4][2];
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                vr[kk][x] = lds128_at<0>(vt + at_of(mt, 2 * t + (kk & 1) + 8 * (kk >> 1), 16 * vb + 2 * g + x));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t a[KP][4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {  // e & 1: + 4 dims; e >> 1: + 8 positions
+                                uint32_t w[KP];
+                                split2<M, KP>(f_of(vr[2 * (e >> 1)][e & 1], j), f_of(vr[2 * (e >> 1) + 1][e & 1], j), w);
+#pragma unroll
+                                for (int y = 0; y < KP; ++y) a[y][e] = w[y];
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int x = QP - 1; x >= 0; --x)
+#pragma unroll
+                                    for (int y = KP - 1; y >= 0; --y)
+                                        if (x + y < QP)
+                                            mma16816<M>(acc[nt][4 * vb + j], a[y], pw[mt][nt][0][x], pw[mt][nt][1][x]);
+                        }
+                    }
             }
-        };
-
-        const int first = st * NW, last = (st + n_units) * NW;  // 16-position steps of this segment
-        Step cur = step_of(first + warp);
-        load_k(cur);
-        for (int s = first + warp; s < last; s += NW) {
-            load_v(cur);
-            Step nxt = cur;
-            if (s + NW < last) nxt = step_of(s + NW);
-            // scores: rows g and g + 8, heads 2t and 2t + 1
-            float sc[NT][QP][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < QP; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][i][e] = 0.f;
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                for (int hs = 0; hs < 2; ++hs) {
-                    uint32_t a[KP][4];
-                    if constexpr (KP == 1) {
-                        a[0][0] = w_of(kr[kb][0][0], 2 * hs);
-                        a[0][1] = w_of(kr[kb][1][0], 2 * hs);
-                        a[0][2] = w_of(kr[kb][0][0], 2 * hs + 1);
-                        a[0][3] = w_of(kr[kb][1][0], 2 * hs + 1);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 &x = kr[kb][e & 1][LV == 2 ? hs : 0];
-                            uint32_t w[KP];
-                            split2<M, KP>(f_of(x, 2 * (e >> 1)), f_of(x, 2 * (e >> 1) + 1), w);
-#pragma unroll
-                            for (int i = 0; i < KP; ++i) a[i][e] = w[i];
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < QP; ++i) {
-                            const uint2 bq = qf[((i * NT + nt) * KS + 2 * kb + hs) * 32 + lane];
-#pragma unroll
-                            for (int j = 0; j < KP; ++j)
-                                if (i + j < QP) mma16816<M>(sc[nt][i], a[j], bq.x, bq.y);
-                        }
-                }
-            if (s + NW < last) load_k(nxt);
-            const bool ok0 = g >= cur.r0 && g < cur.r1, ok1 = g + 8 >= cur.r0 && g + 8 < cur.r1;
-            uint32_t pw[NT][2][QP];  // P as B fragments: positions 2t.. and 2t + 8.., head g
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = sc[nt][QP - 1][e];
-#pragma unroll
-                    for (int i = QP - 2; i >= 0; --i) v += sc[nt][i][e];
-                    x[e] = (e < 2 ? ok0 : ok1) ? v * qi[nt][e & 1] : -INFINITY;
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(x[i], x[2 + i]);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float mn = fmaxf(m[nt][i], mx);
-                    const float mu = mn == -INFINITY ? 0.f : mn;  // nothing attended yet
-                    const float alpha = ex2(m[nt][i] - mu);
-                    m[nt][i] = mn;
-                    x[i] = ex2(x[i] - mu + C::PEXP);
-                    x[2 + i] = ex2(x[2 + i] - mu + C::PEXP);
-                    l[nt][i] = fmaf(l[nt][i], alpha, x[i] + x[2 + i]);
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        acc[nt][j][i] *= alpha;
-                        acc[nt][j][2 + i] *= alpha;
-                    }
-                }
-                uint32_t w0[QP], w1[QP];
-                split2<M, QP>(x[0], x[1], w0);
-                split2<M, QP>(x[2], x[3], w1);
-#pragma unroll
-                for (int i = 0; i < QP; ++i) {
-                    pw[nt][0][i] = transpose8x8(w0[i]);
-                    pw[nt][1][i] = transpose8x8(w1[i]);
-                }
-            }
-            // outputs: m tile (vb, j) has rows dim 64 vb + 8 g + j and + 4
-#pragma unroll
-            for (int vb = 0; vb < VB; ++vb)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t a[KP][4];
-                    if constexpr (KP == 1) {
-                        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)  // e & 1: + 4 dims; e >> 1: + 8 positions
-                            a[0][e] = __byte_perm(w_of(vr[vb][2 * (e >> 1)][0], (j >> 1) + 2 * (e & 1)),
-                                                  w_of(vr[vb][2 * (e >> 1) + 1][0], (j >> 1) + 2 * (e & 1)), sel);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w[KP];
-                            split2<M, KP>(f_of(vr[vb][2 * (e >> 1)][LV == 2 ? (e & 1) : 0], j),
-                                          f_of(vr[vb][2 * (e >> 1) + 1][LV == 2 ? (e & 1) : 0], j), w);
-#pragma unroll
-                            for (int i = 0; i < KP; ++i) a[i][e] = w[i];
-                        }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = QP - 1; i >= 0; --i)
-#pragma unroll
-                            for (int jj = KP - 1; jj >= 0; --jj)
-                                if (i + jj < QP) mma16816<M>(acc[nt][4 * vb + j], a[jj], pw[nt][0][i], pw[nt][1][i]);
-                }
-            cur = nxt;
+            advance();
+            issue();
         }
+        // a wait gave up: what is in flight lands before the room is used again
+        for (; out > 0; --out) {
+            mbar_wait(bars + 8 * slot, phase, kWaitCycles);
+            if (++slot == NI) {
+                slot = 0;
+                phase ^= 1;
+            }
+        }
+        __syncthreads();  // the rings are done: their room holds the merge
 
         // merge the warps in warp order: M = max_w m_w, l = sum l_w 2^(m_w - M), ...
 #pragma unroll
@@ -487,21 +681,30 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
                     wl[warp * 8 * NT + h] = s;
                 }
                 if (h < G) {
-                    float *dst = red + ((size_t)warp * G + h) * D + 8 * g;
+                    float *dst = red + ((size_t)warp * G + h) * D;
+                    if constexpr (H16) {
 #pragma unroll
-                    for (int vb = 0; vb < VB; ++vb) {
-                        *reinterpret_cast<float4 *>(dst + 64 * vb) = make_float4(
-                            acc[nt][4 * vb][i], acc[nt][4 * vb + 1][i], acc[nt][4 * vb + 2][i], acc[nt][4 * vb + 3][i]);
-                        *reinterpret_cast<float4 *>(dst + 64 * vb + 4) =
-                            make_float4(acc[nt][4 * vb][2 + i], acc[nt][4 * vb + 1][2 + i], acc[nt][4 * vb + 2][2 + i],
-                                        acc[nt][4 * vb + 3][2 + i]);
+                        for (int j = 0; j < KS; ++j) {
+                            dst[16 * j + g] = acc[nt][j][i];
+                            dst[16 * j + 8 + g] = acc[nt][j][2 + i];
+                        }
+                    } else {
+#pragma unroll
+                        for (int vb = 0; vb < VB; ++vb) {
+                            *reinterpret_cast<float4 *>(dst + 64 * vb + 8 * g) =
+                                make_float4(acc[nt][4 * vb][i], acc[nt][4 * vb + 1][i], acc[nt][4 * vb + 2][i],
+                                            acc[nt][4 * vb + 3][i]);
+                            *reinterpret_cast<float4 *>(dst + 64 * vb + 8 * g + 4) =
+                                make_float4(acc[nt][4 * vb][2 + i], acc[nt][4 * vb + 1][2 + i], acc[nt][4 * vb + 2][2 + i],
+                                            acc[nt][4 * vb + 3][2 + i]);
+                        }
                     }
                 }
             }
         __syncthreads();
         const bool whole = u == s0 && ue == s1;
         float *mine = p.part + ((size_t)cta * 2 + (u == u0 ? 0 : 1)) * slot_floats;
-        for (int idx = tid; idx < G * D; idx += 32 * NW) {
+        for (int idx = tid; idx < G * D; idx += kPagedThreads) {
             const int h = idx / D;
             float Mx = -INFINITY;
 #pragma unroll
@@ -536,10 +739,9 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
                 __threadfence();
                 // CTA c0 + i's slot: its first segment, except a first CTA whose
                 // range starts before the pair
-                auto slot_of = [&](int i) {
-                    const int sl = i == 0 && W * c0 / N != s0 ? 1 : 0;
-                    return p.part + ((size_t)(c0 + i) * 2 + sl) * slot_floats;
-                };
+                const float *part0 = p.part + ((size_t)c0 * 2 + (W * c0 / N != s0 ? 1 : 0)) * slot_floats;
+                const float *part1 = p.part + (size_t)c0 * 2 * slot_floats;
+                auto slot_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * slot_floats; };
                 float *wts = red;  // [nc][G]
                 for (int h = warp; h < G; h += NW) {
                     float Mx = -INFINITY;
@@ -558,16 +760,23 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
                     if (lane == 0) fl[h] = L;
                 }
                 __syncthreads();
-                for (int idx = tid; idx < G * D; idx += 32 * NW) {
+                for (int idx = 2 * tid; idx < G * D; idx += 2 * kPagedThreads) {
                     const int h = idx / D;
-                    float o = 0.f;
-#pragma unroll 8
-                    for (int i = 0; i < nc; ++i) o = fmaf(__ldcg(slot_of(i) + idx), wts[i * G + h], o);
-                    p.out[((size_t)b * p.H + hk * G) * D + idx] = fl[h] == 0.f ? 0.f : o / fl[h];
+                    float2 o = make_float2(0.f, 0.f);
+#pragma unroll 16
+                    for (int i = 0; i < nc; ++i) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + idx));
+                        const float f = wts[i * G + h];
+                        o.x = fmaf(v.x, f, o.x);
+                        o.y = fmaf(v.y, f, o.y);
+                    }
+                    const float L = fl[h], inv = L == 0.f ? 0.f : 1.f / L;
+                    *reinterpret_cast<float2 *>(p.out + ((size_t)b * p.H + hk * G) * D + idx) = make_float2(o.x * inv, o.y * inv);
                 }
                 if (tid == 0) p.count[(size_t)b * hkv + hk] = 0;  // zero again for the next call
             }
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge's writes, before the next copies
         __syncthreads();  // the shared memory is free for the next segment
         u = ue;
     }
@@ -575,12 +784,8 @@ __global__ void __launch_bounds__(32 * kPagedWarps, (sizeof(T) == 4 && D == 128)
 
 }  // namespace dev
 
-namespace {
-// grid slots of one SM: two CTAs, one where the registers allow no more
-int paged_occ(int dtype, int D, int G) { return (dtype == 0 && D == 128) || G > 8 ? 1 : 2; }
-}  // namespace
-
-int paged_attn_ctas(int dtype, int D, int G, int sms) { return paged_occ(dtype, D, G) * sms; }
+// above 8 heads a kv head Q's fragments leave room for one CTA of an SM
+int paged_attn_ctas(int G, int sms) { return (G > 8 ? 1 : dev::kPagedOcc) * sms; }
 size_t paged_attn_slot_floats(int D, int G) { return (size_t)G * (D + 2); }
 
 template <typename T, int D, int NT>
@@ -588,21 +793,21 @@ static int launch_paged_t(const PagedAttnParams &p, int ctas, cudaStream_t strea
     auto kern = dev::q4attn_paged_kernel<T, D, NT>;
     static size_t smem_set[64] = {0};
     const int G = p.H / p.kv.hkv;
-    // the merge area also holds the fold's weights, one per CTA and head
+    using Cfg = dev::PagedCfg<T, D>;
+    // the rings; over them the merge, and the fold's weights, one per CTA and head
     const size_t merge = sizeof(float) * G * (size_t)std::max(dev::kPagedWarps * D, ctas);
-    const size_t smem = dev::PagedSmem<T, D, NT>::Red + merge;
+    const size_t smem = dev::PagedSmem<T, D, NT>::Red + std::max(merge, (size_t)dev::kPagedWarps * Cfg::NI * Cfg::Item);
     if (!raise_smem(kern, smem, smem_set)) return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-    cfg.blockDim = dim3(32 * dev::kPagedWarps, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
+    CUtensorMap mk{}, mv{};
+    if (sizeof(T) == 2) {
+        const bool bf = std::is_same<T, __nv_bfloat16>::value;
+        const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.kv.page, (cuuint64_t)p.kv.hkv, (cuuint64_t)p.kv.num_pages};
+        const cuuint32_t box[4] = {64, 16, 1, 1};
+        if (!make_map(&mk, bf, p.kv.k, 4, dims, box) || !make_map(&mv, bf, p.kv.v, 4, dims, box)) return -1;
+    }
     cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kPagedThreads, smem, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, kern, p, mk, mv) == cudaSuccess ? 0 : -1;
 }
 
 template <typename T>

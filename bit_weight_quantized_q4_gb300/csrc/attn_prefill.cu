@@ -21,13 +21,10 @@
 // that some rows of a tile see and others do not would still enter as 0 * NaN:
 // a row whose result is not finite is therefore taken again by the definition
 // (attn_row), which never touches what it does not attend.
-#include <cuda.h>
-
-#include <atomic>
-
 #include "attn_prefill_row.cuh"
 #include "gemv_launch.cuh"
 #include "tc_common.cuh"
+#include "tensor_map.h"
 
 namespace q4 {
 namespace dev {
@@ -258,12 +255,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // place they held the ring back (a tile every 1400 cycles)
         const int boxes = kPfKeys / box_rows, bl = lane / boxes, r = lane - bl * boxes;
         auto lookup = [&](int j, int &page, int &slot) {
-            const int key = k_first + j * kPfKeys + r * box_rows, col = key / p.kv.page;
+            const int key = k_first + j * kPfKeys + r * box_rows, col = page_col(p.kv, key);
             slot = key - col * p.kv.page;
-            page = bl < NB && key < key_end ? page_at(p.kv, t.seq, col) : -1;
-            // a page out of range is copied as zeros (its coordinate is out of
-            // the map's range); below the window it may be gone
-            if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
+            page = bl < NB && key < key_end ? page_raw(p.kv, t.seq, col) : -1;
         };
         int page1, slot1;
         lookup(0, page1, slot1);
@@ -271,7 +265,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         int st = 0;
         uint32_t ph = 1;  // an empty slot's phase: the first pass finds them free
         for (int j = 0; ok && j < nk; ++j) {
-            const int page = page1, slot = slot1;
+            const int page = page_ok(p.kv, page1), slot = slot1;
+            // a page out of range is copied as zeros (its coordinate is out of
+            // the map's range); below the window it may be gone
+            const int key = k_first + j * kPfKeys + r * box_rows;
+            if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
             const int live = min(boxes, (key_end - k_first - j * kPfKeys + box_rows - 1) / box_rows);  // boxes with attended positions
             if (j + 1 < nk) lookup(j + 1, page1, slot1);
             for (int kv = 0; kv < 2 * NP; ++kv) {  // K's parts, V's parts
@@ -772,59 +770,6 @@ __global__ void __launch_bounds__(256) q4attn_prefill_split_kernel(const __grid_
 }
 
 }  // namespace dev
-
-namespace {
-
-// cuTensorMapEncodeTiled, resolved once (the library links the runtime only)
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-    static std::atomic<void *> cached{nullptr};
-    void *f = cached.load(std::memory_order_acquire);
-    if (!f) {
-        cudaDriverEntryPointQueryResult res;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res) !=
-                cudaSuccess ||
-            res != cudaDriverEntryPointSuccess)
-            return nullptr;
-        cached.store(f, std::memory_order_release);
-    }
-    return (EncodeTiled)f;
-}
-
-// A row-major map of 16-bit values with boxes of 64 values (128 bytes) by
-// box[1 ..] rows, 128-byte swizzled; dims innermost first.
-bool make_map(CUtensorMap *m, bool bf16, const void *base, int rank, const cuuint64_t *dims, const cuuint32_t *box) {
-    EncodeTiled enc = encode_tiled();
-    if (!enc) return false;
-    cuuint64_t strides[5];
-    cuuint64_t s = 2;
-    for (int i = 0; i + 1 < rank; ++i) {
-        s *= dims[i];
-        strides[i] = s;
-    }
-    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, const_cast<void *>(base),
-               dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-cudaLaunchConfig_t pdl_config(unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                              cudaLaunchAttribute *attr) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(block, 1, 1);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr->val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cfg;
-}
-
-}  // namespace
 
 // The fp32 form's workspace: the heads' maxima, Q's factors back and parts,
 // K's and V's parts.

@@ -931,7 +931,14 @@ q4_status check_rope(const float *rope_cos, const float *rope_sin, int32_t rope_
     return rope_rows >= 1 ? Q4_OK : Q4_ERR_SHAPE;
 }
 q4::PagedKv paged_view(const q4_kv_pages *c) {
-    return q4::PagedKv{c->k, c->v, c->table, c->num_pages, c->page_size, c->kv_heads, c->nseq, c->width};
+    // s = ceil(log2 page), mul = floor(2^(31 + s) / page) + 1: with p < 2^31 the
+    // quotient umulhi(p, mul) >> (s - 1) is exact (the error p / 2^(31 + s) is
+    // below 1 / page)
+    int s = 0;
+    while ((1ll << s) < c->page_size) ++s;
+    const uint32_t mul = c->page_size > 1 ? (uint32_t)((1ull << (31 + s)) / c->page_size + 1) : 0;
+    return q4::PagedKv{c->k,     c->v,   c->table, c->num_pages, c->page_size, c->kv_heads, c->nseq,
+                       c->width, mul,    s - 1};
 }
 // per (sequence, kv head) counters at the start of the paged workspace
 inline size_t paged_count_bytes(const q4_kv_pages *c) {
@@ -1049,7 +1056,6 @@ extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, con
     if (!aligned16(workspace)) return Q4_ERR_ALIGN;
     const int sms = num_sms();
     if (sms <= 0) return Q4_ERR_CUDA;
-    const int G = H / pages->kv_heads;
     q4::PagedAttnParams p{};
     p.kv = paged_view(pages);
     p.q = q;
@@ -1067,11 +1073,12 @@ extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, con
     p.rope_rows = rope_rows;
     p.scale = scale;
     Q4_TRY(kernel_err_ptr(&p.err));
+    p.wait_cycles = g_wait_cycles;
+    p.extra_tx = g_extra_tx;
     // one CTA per slot of the device, no more than there can be units
     const long long cap = (long long)pages->width * pages->page_size;
-    const long long units = (long long)pages->nseq * pages->kv_heads * ((cap + 127) / 128);
-    const int ctas = (int)std::min<long long>(
-        std::min(q4::paged_attn_ctas(pages->dtype, pages->head_dim, G, sms), kMaxPagedCtas), units);
+    const long long units = (long long)pages->nseq * pages->kv_heads * ((cap + 63) / 64);
+    const int ctas = (int)std::min<long long>(std::min(q4::paged_attn_ctas(H / pages->kv_heads, sms), kMaxPagedCtas), units);
     cudaGetLastError();
     if (q4::launch_paged_attn(p, pages->dtype, ctas, stream) != 0 || cudaGetLastError() != cudaSuccess)
         return Q4_ERR_CUDA;

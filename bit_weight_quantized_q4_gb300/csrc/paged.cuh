@@ -20,11 +20,23 @@ namespace dev {
 
 constexpr int kErrPaged = 5;  // error word: a position, page or token out of range
 
+// Table column of position p (p / page), without a division.
+__device__ __forceinline__ int page_col(const PagedKv &kv, int p) {
+    return kv.page == 1 ? p : (int)(__umulhi((unsigned)p, kv.page_mul) >> kv.page_shift);
+}
 // Page id of table column `i` of sequence b, or -1 where the table's entry
 // (or the column) is out of range.
 __device__ __forceinline__ int page_at(const PagedKv &kv, int b, int i) {
     if ((unsigned)i >= (unsigned)kv.width) return -1;
     const int id = kv.table[(size_t)b * kv.width + i];
+    return (unsigned)id < (unsigned)kv.num_pages ? id : -1;
+}
+// The same in two steps, for a lookup ahead of its use: the raw entry (a load
+// whose result nothing needs yet), and its check.
+__device__ __forceinline__ int page_raw(const PagedKv &kv, int b, int i) {
+    return (unsigned)i < (unsigned)kv.width ? kv.table[(size_t)b * kv.width + i] : -1;
+}
+__device__ __forceinline__ int page_ok(const PagedKv &kv, int id) {
     return (unsigned)id < (unsigned)kv.num_pages ? id : -1;
 }
 // Element offset of (page, kv head, slot, dim 0).

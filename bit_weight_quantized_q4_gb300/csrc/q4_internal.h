@@ -406,6 +406,8 @@ struct PagedKv {
     void *k, *v;            // [num_pages][hkv][page][D]
     const int32_t *table;   // [nseq][width] page ids
     int num_pages, page, hkv, nseq, width;
+    uint32_t page_mul;      // p / page = umulhi(p, page_mul) >> page_shift for 0 <= p < 2^31, page > 1
+    int page_shift;
 };
 constexpr int kMaxSeqs = 1024;  // sequences of one call
 
@@ -432,10 +434,12 @@ struct PagedAttnParams {
     int *count;                        // [nseq * hkv], zero between calls
     float *part;                       // partial results, 2 slots a CTA
     int *err;
+    long long wait_cycles;
+    int extra_tx;
     int H, D, window, rope_rows;
     float scale;
 };
-int paged_attn_ctas(int dtype, int D, int G, int sms);  // CTAs of the largest grid
+int paged_attn_ctas(int G, int sms);  // CTAs of the largest grid
 size_t paged_attn_slot_floats(int D, int G);
 int launch_paged_attn(const PagedAttnParams &p, int dtype, int ctas, void *stream);
 
