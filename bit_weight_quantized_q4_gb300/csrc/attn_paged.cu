@@ -141,7 +141,8 @@ struct PagedCfg {
     static_assert(NI >= 3, "two items in flight while one is read");
 };
 
-// Shared memory of a CTA: the prefix of units over the sequences, Q's
+// Shared memory of a CTA: the prefix of units over the sequences (per kv
+// head) and their positions, Q's
 // fragments (more than 8 heads: else they live in registers after their
 // preparation) and factors, the warps' maxima and sums, the fold's sums, a
 // flag, then the rings; over them, when a segment's loop is done, the warps'
@@ -149,7 +150,8 @@ struct PagedCfg {
 template <typename T, int D, int NT>
 struct PagedSmem {
     static constexpr int Prefix = 0;
-    static constexpr int Qf = Prefix + 8 * (kMaxSeqs + 2);
+    static constexpr int Pos = Prefix + 4 * (kMaxSeqs + 4);
+    static constexpr int Qf = Pos + 4 * kMaxSeqs;
     static constexpr int Qs = Qf + PagedT<T>::QP * NT * (D / 16) * 32 * 8;
     static constexpr int Wm = Qs + 4 * 8 * NT;
     static constexpr int Wl = Wm + 4 * kPagedWarps * 8 * NT;
@@ -159,6 +161,9 @@ struct PagedSmem {
     static constexpr int Bars = New + 2 * D * (int)sizeof(T);
     static constexpr int Red = (Bars + 8 * kPagedWarps * PagedCfg<T, D>::NI + 1023) / 1024 * 1024;
 };
+
+// A partial result: G outputs of D, G maxima, G sums, in whole 16 bytes.
+Q4_HD constexpr size_t paged_slot_floats(int G, int D) { return ((size_t)G * (D + 2) + 3) / 4 * 4; }
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
     extern __shared__ __align__(1024) uint8_t psm[];  // the swizzle's pattern repeats every 1024 bytes
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int hkv = p.kv.hkv, G = p.H / hkv, nseq = p.kv.nseq;
-    long long *prefix = reinterpret_cast<long long *>(psm + S::Prefix);
+    int *prefix = reinterpret_cast<int *>(psm + S::Prefix), *pos_s = reinterpret_cast<int *>(psm + S::Pos);
     uint2 *qf = reinterpret_cast<uint2 *>(psm + S::Qf);
     float *qs = reinterpret_cast<float *>(psm + S::Qs);
     float *wm = reinterpret_cast<float *>(psm + S::Wm), *wl = reinterpret_cast<float *>(psm + S::Wl);
@@ -202,39 +207,45 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         const int lo = lo_of(pos) & ~15;
         return (pos - lo) / Cfg::Unit + 1;
     };
-    // prefix[b] = units of sequences before b (all kv heads), a sequence a thread
-    long long W = 0;
+    // prefix[b] = units of a kv head of the sequences before b (the host bounds
+    // the sum to 31 bits), a sequence a thread
+    int Wh = 0;
     for (int b0 = 0; b0 < nseq; b0 += kPagedThreads) {
         const int b = b0 + tid;
-        const long long n = b < nseq ? (long long)units_of(p.positions[b]) * hkv : 0;
-        long long inc = n;
+        const int pos = b < nseq ? p.positions[b] : -1;
+        int inc = units_of(pos);
+        const int n = inc;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        long long *wsum = reinterpret_cast<long long *>(red) + ((b0 / kPagedThreads) & 1) * NW;
+        int *wsum = reinterpret_cast<int *>(red) + ((b0 / kPagedThreads) & 1) * NW;
         if (lane == 31) wsum[warp] = inc;
         __syncthreads();
-        long long before = W;
+        int before = Wh;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             if (w < warp) before += wsum[w];
-            W += wsum[w];
+            Wh += wsum[w];
         }
-        if (b < nseq) prefix[b + 1] = before + inc;
+        if (b < nseq) {
+            prefix[b] = before + inc - n;
+            pos_s[b] = pos;
+        }
     }
-    if (tid == 0) prefix[0] = 0;
+    if (tid == 0) prefix[nseq] = Wh;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's room is the rings'
     __syncthreads();
     // idle rows: zeros
     for (int b = blockIdx.x; b < nseq; b += gridDim.x)
         if (prefix[b + 1] == prefix[b]) {
             for (int i = tid; i < p.H * D; i += kPagedThreads) p.out[(size_t)b * p.H * D + i] = 0.f;
-            if (tid == 0 && p.positions[b] >= 0) atomicExch(p.err, kErrPaged);
+            if (tid == 0 && pos_s[b] >= 0) atomicExch(p.err, kErrPaged);
         }
     // CTAs with work: never more than units, so that none of a pair's CTAs is
     // without a share (each adds to the pair's count)
+    const long long W = (long long)Wh * hkv;
     const int N = W < gridDim.x ? (int)W : (int)gridDim.x, cta = blockIdx.x;
     if (cta >= N) return;
     const long long u0 = W * cta / N, u1 = W * (cta + 1) / N;
@@ -243,14 +254,14 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         int hi = nseq;
         while (hi - b > 1) {
             const int mid = (b + hi) >> 1;
-            if (prefix[mid] <= u0)
+            if ((long long)prefix[mid] * hkv <= u0)
                 b = mid;
             else
                 hi = mid;
         }
     }
     const float qscale = p.scale * 1.4426950408889634f;
-    const size_t slot_floats = (size_t)G * (D + 2);
+    const size_t slot_floats = paged_slot_floats(G, D);
     // the ring's state, carried over the segments: the slot (and its phase) of
     // the next item to issue and to read
     int fill_slot = 0, slot = 0;
@@ -261,17 +272,41 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
     uint32_t extra = p.extra_tx;     // testing the give-up path only
 
     for (long long u = u0; u < u1;) {
-        while (prefix[b + 1] <= u) ++b;
-        const int pos = p.positions[b], lo = lo_of(pos), base16 = lo & ~15;
+        while ((long long)prefix[b + 1] * hkv <= u) ++b;
+        const int pos = pos_s[b], lo = lo_of(pos), base16 = lo & ~15;
         const int cs = units_of(pos);
-        const long long rem = u - prefix[b];
+        const long long sb = (long long)prefix[b] * hkv, rem = u - sb;
         const int hk = (int)(rem / cs), st = (int)(rem - (long long)hk * cs);
-        const long long s0 = prefix[b] + (long long)hk * cs, s1 = s0 + cs;  // the pair's units
+        const long long s0 = sb + (long long)hk * cs, s1 = s0 + cs;  // the pair's units
         const long long ue = s1 < u1 ? s1 : u1;
         const int n_units = (int)(ue - u);
         const bool owner = ue == s1;  // this segment ends with the new token
-        const float *cosr = p.rope_cos ? p.rope_cos + (size_t)pos * (D / 2) : nullptr;
-        const float *sinr = p.rope_cos ? p.rope_sin + (size_t)pos * (D / 2) : nullptr;
+
+        // Q's heads (warp, warp + NW, ..; lane j < D / 8 holds dims 4 j .. and D / 2 +
+        // 4 j ..) and the position's rotation, loaded before the copies go out
+        constexpr int HW = 8 * NT / NW;
+        const bool ql = lane < D / 8;
+        float4 qa[HW], qb[HW], cr = make_float4(1.f, 1.f, 1.f, 1.f), sr = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < HW; ++x) {
+            const int h = warp + NW * x;
+            qa[x] = qb[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h < G && ql) {
+                const float *src = p.q + ((size_t)b * p.H + hk * G + h) * D + 4 * lane;
+                qa[x] = *reinterpret_cast<const float4 *>(src);
+                qb[x] = *reinterpret_cast<const float4 *>(src + D / 2);
+            }
+        }
+        if (p.rope_cos && ql) {
+            cr = *reinterpret_cast<const float4 *>(p.rope_cos + (size_t)pos * (D / 2) + 4 * lane);
+            sr = *reinterpret_cast<const float4 *>(p.rope_sin + (size_t)pos * (D / 2) + 4 * lane);
+        }
+        float4 na = make_float4(0.f, 0.f, 0.f, 0.f), nb = na;  // warp 0: the new k, warp 1: the new v
+        if (owner && warp < 2 && ql) {
+            const float *src = (warp == 0 ? p.k_new : p.v_new) + ((size_t)b * hkv + hk) * D + 4 * lane;
+            na = *reinterpret_cast<const float4 *>(src);
+            nb = *reinterpret_cast<const float4 *>(src + D / 2);
+        }
 
         // this warp's steps: first + warp, first + warp + NW, .. below last.  Their
         // K and V tiles come through the warp's own ring in shared memory by TMA
@@ -390,17 +425,12 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         for (int i = 0; i < NI - 1; ++i) issue();
 
         // the group's query heads: rotated, scaled (log2 units), in parts, as
-        // B fragments; lane j < D / 8 holds dims 4j.. and D/2 + 4j..
-        for (int h = warp; h < 8 * NT; h += NW) {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
-            if (h < G && lane < D / 8) {
-                const float *src = p.q + ((size_t)b * p.H + hk * G + h) * D + 4 * lane;
-                a = *reinterpret_cast<const float4 *>(src);
-                c = *reinterpret_cast<const float4 *>(src + D / 2);
-                if (cosr)
-                    rotate4(a, c, *reinterpret_cast<const float4 *>(cosr + 4 * lane),
-                            *reinterpret_cast<const float4 *>(sinr + 4 * lane));
-            }
+        // B fragments
+#pragma unroll
+        for (int y = 0; y < HW; ++y) {
+            const int h = warp + NW * y;
+            float4 a = qa[y], c = qb[y];
+            if (p.rope_cos) rotate4(a, c, cr, sr);
             float f = qscale;
             if constexpr (C::SCALED) {
                 float mx = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
@@ -419,7 +449,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                 }
                 if (lane == 0) qs[h] = back;
             }
-            if (lane < D / 8) {
+            if (ql) {
                 const int nt = h >> 3, gg = h & 7;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -450,12 +480,9 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             const int col = page_col(p.kv, pos), page = page_at(p.kv, b, col);
             if (page < 0) {
                 if (lane == 0) atomicExch(p.err, kErrPaged);
-            } else if (lane < D / 8) {
-                const float *src = (warp == 0 ? p.k_new : p.v_new) + ((size_t)b * hkv + hk) * D + 4 * lane;
-                float4 a = *reinterpret_cast<const float4 *>(src), c = *reinterpret_cast<const float4 *>(src + D / 2);
-                if (warp == 0 && cosr)
-                    rotate4(a, c, *reinterpret_cast<const float4 *>(cosr + 4 * lane),
-                            *reinterpret_cast<const float4 *>(sinr + 4 * lane));
+            } else if (ql) {
+                float4 a = na, c = nb;
+                if (warp == 0 && p.rope_cos) rotate4(a, c, cr, sr);
                 T *dst = (T *)(warp == 0 ? p.kv.k : p.kv.v) + row_off(p.kv, page, hk, pos - col * p.kv.page, D) + 4 * lane;
                 store4(dst, a);
                 store4(dst + D / 2, c);
@@ -731,47 +758,65 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             // the last of the pair's CTAs to finish folds their shares in CTA order
             const long long c0 = ((s0 + 1) * N - 1) / W, c1 = (s1 * N - 1) / W;  // first and last CTA
             const int nc = (int)(c1 - c0) + 1;
-            __threadfence();
             __syncthreads();
-            if (tid == 0) *flag = atomicAdd(p.count + (size_t)b * hkv + hk, 1) == nc - 1;
+            if (tid == 0) {
+                __threadfence();  // the CTA's share (the barrier orders it before), then the count
+                *flag = atomicAdd(p.count + (size_t)b * hkv + hk, 1) == nc - 1;
+                __threadfence();
+            }
             __syncthreads();
             if (*flag) {
-                __threadfence();
                 // CTA c0 + i's slot: its first segment, except a first CTA whose
                 // range starts before the pair
                 const float *part0 = p.part + ((size_t)c0 * 2 + (W * c0 / N != s0 ? 1 : 0)) * slot_floats;
                 const float *part1 = p.part + (size_t)c0 * 2 * slot_floats;
                 auto slot_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * slot_floats; };
-                float *wts = red;  // [nc][G]
+                // weights 2^(m_i - M) and the sum, a warp a head
+                float *wts = red, *part = red + (size_t)((nc * G + 31) & ~31);  // [nc][G], then [NW][G D]
                 for (int h = warp; h < G; h += NW) {
-                    float Mx = -INFINITY;
-                    for (int i = lane; i < nc; i += 32) Mx = fmaxf(Mx, __ldcg(slot_of(i) + G * D + h));
+                    float Mx = -INFINITY, mi = -INFINITY, li = 0.f;
+                    for (int i = lane; i < nc; i += 32) {
+                        mi = __ldcg(slot_of(i) + G * D + h);
+                        li = __ldcg(slot_of(i) + G * D + G + h);
+                        Mx = fmaxf(Mx, mi);
+                        wts[i * G + h] = mi;
+                    }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
                     const float mu = Mx == -INFINITY ? 0.f : Mx;
                     float L = 0.f;
                     for (int i = lane; i < nc; i += 32) {
-                        const float f = ex2(__ldcg(slot_of(i) + G * D + h) - mu);
+                        const float f = ex2(wts[i * G + h] - mu);
                         wts[i * G + h] = f;
-                        L = fmaf(__ldcg(slot_of(i) + G * D + G + h), f, L);
+                        L = fmaf(nc <= 32 ? li : __ldcg(slot_of(i) + G * D + G + h), f, L);
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
                     if (lane == 0) fl[h] = L;
                 }
                 __syncthreads();
-                for (int idx = 2 * tid; idx < G * D; idx += 2 * kPagedThreads) {
-                    const int h = idx / D;
-                    float2 o = make_float2(0.f, 0.f);
-#pragma unroll 16
-                    for (int i = 0; i < nc; ++i) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + idx));
-                        const float f = wts[i * G + h];
-                        o.x = fmaf(v.x, f, o.x);
-                        o.y = fmaf(v.y, f, o.y);
+                // warp w adds the shares w, w + NW, .. of 128 outputs at a time, then
+                // the warps' sums are added in warp order
+                for (int e0 = 0; e0 < G * D; e0 += 128) {
+                    const int idx = e0 + 4 * lane, h = idx / D;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (idx < G * D) {
+#pragma unroll 4
+                        for (int i = warp; i < nc; i += NW) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot_of(i) + idx));
+                            const float f = wts[i * G + h];
+                            o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+                        }
+                        *reinterpret_cast<float4 *>(part + (size_t)warp * G * D + idx) = o;
                     }
-                    const float L = fl[h], inv = L == 0.f ? 0.f : 1.f / L;
-                    *reinterpret_cast<float2 *>(p.out + ((size_t)b * p.H + hk * G) * D + idx) = make_float2(o.x * inv, o.y * inv);
+                }
+                __syncthreads();
+                for (int idx = tid; idx < G * D; idx += kPagedThreads) {
+                    float o = 0.f;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) o += part[(size_t)w * G * D + idx];
+                    const float L = fl[idx / D];
+                    p.out[((size_t)b * p.H + hk * G) * D + idx] = L == 0.f ? 0.f : o / L;
                 }
                 if (tid == 0) p.count[(size_t)b * hkv + hk] = 0;  // zero again for the next call
             }
@@ -786,7 +831,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
 
 // above 8 heads a kv head Q's fragments leave room for one CTA of an SM
 int paged_attn_ctas(int G, int sms) { return (G > 8 ? 1 : dev::kPagedOcc) * sms; }
-size_t paged_attn_slot_floats(int D, int G) { return (size_t)G * (D + 2); }
+size_t paged_attn_slot_floats(int D, int G) { return dev::paged_slot_floats(G, D); }
 
 template <typename T, int D, int NT>
 static int launch_paged_t(const PagedAttnParams &p, int ctas, cudaStream_t stream) {
@@ -794,8 +839,8 @@ static int launch_paged_t(const PagedAttnParams &p, int ctas, cudaStream_t strea
     static size_t smem_set[64] = {0};
     const int G = p.H / p.kv.hkv;
     using Cfg = dev::PagedCfg<T, D>;
-    // the rings; over them the merge, and the fold's weights, one per CTA and head
-    const size_t merge = sizeof(float) * G * (size_t)std::max(dev::kPagedWarps * D, ctas);
+    // the rings; over them the merge, or the fold's weights (one per CTA and head) and sums
+    const size_t merge = sizeof(float) * ((size_t)G * (dev::kPagedWarps * D + ctas) + 32);
     const size_t smem = dev::PagedSmem<T, D, NT>::Red + std::max(merge, (size_t)dev::kPagedWarps * Cfg::NI * Cfg::Item);
     if (!raise_smem(kern, smem, smem_set)) return -1;
     CUtensorMap mk{}, mv{};
