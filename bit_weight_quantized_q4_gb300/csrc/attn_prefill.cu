@@ -98,28 +98,6 @@ __device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, 
         : "memory");
 }
 
-// Two fp32 values in one 64-bit register, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_f32(float a, float b) {
-    return pair_u32(__float_as_uint(a), __float_as_uint(b));
-}
-__device__ __forceinline__ float lo_f32(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float hi_f32(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // The CTA's tile: sequence, its first token (row of the packed batch and
 // position) and its tokens.  Tiles of a sequence are numbered from its end:
 // the longest first.

@@ -5,11 +5,15 @@
 //   logprob = x[token] - lse,   entropy = lse - sum p x = log s - t / s,
 //   t = sum e^(x - m) (x - m)   (terms of x = -inf count as 0)
 //   top: the k largest (ties to the lowest index), as x - lse.
-// One pass for (m, s, t) and each thread's largest value; then the k-th
-// largest of the 128 quads' maxima bounds the k-th largest logit from below,
-// and a second pass over the row (in L2 by then) collects the few values at or
-// above that bound, which are ranked by counting.  Where a bound lets too many
-// through (long ties, masked rows) the k largest are found one by one.
+// One pass for the sums and each thread's largest value; then the k-th largest
+// of the 128 quads' maxima bounds the k-th largest logit from below, and a
+// second pass over the row (in L2 by then; in registers where a slice is one
+// batch) keeps the few values at or above that bound, which are ranked by
+// counting.  Where a bound lets too many through (long ties, masked rows) the k
+// largest are found one by one.  (Keeping candidates during the first pass, from
+// the bound of its first batch, costs more instructions than the second read:
+// 46 us for 512 rows of 65536 against 34.5; slices staged in shared memory took
+// 71.)
 // HBM-bound on the row: a CTA a row when the rows fill the device; for fewer
 // rows a cluster of up to 8 CTAs splits each row and joins through distributed
 // shared memory, in one launch.
@@ -24,7 +28,6 @@ namespace dev {
 namespace cg = cooperative_groups;
 
 constexpr int kLpThreads = 512;
-constexpr int kLpQuads = kLpThreads / 4;
 constexpr int kLpCand = 1024;  // candidates a CTA holds
 constexpr int kLpTop = 32;     // largest k
 
@@ -41,88 +44,95 @@ __device__ __forceinline__ unsigned long long lp_pair(uint32_t key, int i) {
     return ((unsigned long long)key << 32) | (0xFFFFFFFFu - (uint32_t)i);
 }
 
-// The elements [i0, i1) of row x: one(value, index) for those before a 16-byte
-// boundary and after the last whole float4, and batch(float4 x 4, index of the
-// first, step) for four float4 in flight a thread (their elements start at
-// index + q * step); what is left of the vectors goes through one().
-template <class One, class Batch>
-__device__ __forceinline__ void lp_each(const float *x, int i0, int i1, int tid, One one, Batch batch) {
-    const int head = min(i1 - i0, (int)((4u - (((uintptr_t)(x + i0) >> 2) & 3u)) & 3u));
-    if (tid < head) one(x[i0 + tid], i0 + tid);
-    const int v0 = i0 + head, nv = (i1 - v0) >> 2;
-    const float4 *xv = reinterpret_cast<const float4 *>(x + v0);
-    int j = tid;
-    for (; j + 3 * kLpThreads < nv; j += 4 * kLpThreads) {
-        float4 v[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = xv[j + q * kLpThreads];
-        batch(v, v0 + 4 * j, 4 * kLpThreads);
-    }
-    for (; j < nv; j += kLpThreads) {
-        const float4 v = xv[j];
-        const int i = v0 + 4 * j;
-        one(v.x, i);
-        one(v.y, i + 1);
-        one(v.z, i + 2);
-        one(v.w, i + 3);
-    }
-    const int tail = v0 + 4 * nv + tid;
-    if (tail < i1) one(x[tail], tail);
-}
 __device__ __forceinline__ float lp_at(const float4 &v, int e) { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
 
 struct LpSums {
     float m, s, t;
 };
-__device__ __forceinline__ LpSums lp_join(const LpSums &a, const LpSums &b) {
-    const float m = fmaxf(a.m, b.m), mu = m == -INFINITY ? 0.f : m;
+// Joins the shares of a warp's lanes (of lanes l and l ^ o for o = width / 2, ..,
+// 1; each lane ends with the same): the largest maximum first, then the sums
+// scaled to it once and added, lower lanes first.
+__device__ __forceinline__ LpSums lp_join(const LpSums &a, int width, int lane) {
+    float m = a.m;
+    for (int o = width / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     // a share without a finite maximum has nothing to scale; a difference below
     // -200 scales by e^-200 = 0 in fp32, and stays finite (0 * -inf is NaN)
-    const float da = a.m == -INFINITY ? 0.f : fmaxf(a.m - mu, -200.f);
-    const float db = b.m == -INFINITY ? 0.f : fmaxf(b.m - mu, -200.f);
-    const float fa = __expf(da), fb = __expf(db);
-    return {m, a.s * fa + b.s * fb, fa * fmaf(da, a.s, a.t) + fb * fmaf(db, b.s, b.t)};
+    const float d = a.m == -INFINITY ? 0.f : fmaxf(a.m - m, -200.f), f = __expf(d);
+    float s = a.s * f, t = f * fmaf(d, a.s, a.t);
+    for (int o = width / 2; o > 0; o >>= 1) {
+        const float s2 = __shfl_xor_sync(0xffffffffu, s, o), t2 = __shfl_xor_sync(0xffffffffu, t, o);
+        s = (lane & o) ? s2 + s : s + s2;
+        t = (lane & o) ? t2 + t : t + t2;
+    }
+    return {m, s, t};
 }
 
 constexpr int kLpMaxCluster = 8;
 
 struct LpShared {
+    static constexpr int Quads = kLpThreads / 4, Quarter = Quads / 4;
     // rank 0 of a cluster receives every CTA's sums and k best pairs (0: none)
     LpSums sums[kLpMaxCluster];
     unsigned long long top[kLpMaxCluster * kLpTop];
     unsigned long long mine[kLpTop];   // this CTA's
     unsigned long long cand[kLpCand];
     LpSums warp[kLpThreads / 32];
-    __align__(16) uint32_t quad[kLpQuads];
+    __align__(16) uint32_t quad[Quads + 12];  // quarters of it 4 words apart: their readers meet no bank twice
     unsigned long long best[kLpThreads / 32];
     uint32_t bound;
     int ncand;
+    __device__ __forceinline__ uint32_t *quad_at(int q) { return quad + q + 4 * (q / Quarter); }
 };
 
-// v added to the running sums: a new maximum m rescales what came before.
+// The sums' reference m: raised (and what came before rescaled) when a logit is
+// more than kLpSlack above it, so that few logits do, and at once from -inf.
+constexpr float kLpSlack = 8.f;
 __device__ __forceinline__ void lp_raise(LpSums &a, float m) {
-    if (m > a.m) {
+    if (m > a.m + kLpSlack) {
         const float d = fmaxf(a.m - m, -200.f), f = __expf(d);  // from -inf: the sums are zero
         a.t = f * fmaf(d, a.s, a.t);
         a.s *= f;
         a.m = m;
     }
 }
-__device__ __forceinline__ void lp_add(LpSums &a, float v, float mu) {
-    const float d = v - mu, e = __expf(d);  // NaN stays; -inf: e = 0, and its term of t is 0
-    a.s += e;
-    a.t = fmaf(e, fmaxf(d, -200.f), a.t);
+// Two logits into sums in log2 units, two at a time (mu: minus the reference):
+// e = 2^y, y = (v - m) log2 e; NaN stays; -inf: e = 0, and its term of t is 0
+__device__ __forceinline__ void lp_add2(uint64_t &s, uint64_t &t, float v0, float v1, uint64_t mu) {
+    const uint64_t y = mul_f32x2(add_f32x2(pair_f32(v0, v1), mu), pair_f32(1.4426950408889634f, 1.4426950408889634f));
+    const float y0 = lo_f32(y), y1 = hi_f32(y);
+    const uint64_t e = pair_f32(ex2(y0), ex2(y1));
+    s = add_f32x2(s, e);
+    t = fma_f32x2(e, pair_f32(fmaxf(y0, -300.f), fmaxf(y1, -300.f)), t);
+}
+
+// The first n of v's values (at index i ..) whose key reaches the bound become
+// candidates.  Not inlined: few values get here, and the kernel's own code,
+// which a row runs through once, stays short (inlined it took 11.7 us for one
+// row of 65536 against 7.5).
+__device__ __noinline__ void lp_take(LpShared &sh, float4 v, int i, int n, uint32_t bound) {
+    for (int e = 0; e < n; ++e) {
+        const uint32_t key = lp_key(v.x);
+        if (key >= bound) {
+            const int at = atomicAdd(&sh.ncand, 1);
+            if (at < kLpCand) sh.cand[at] = lp_pair(key, i + e);
+        }
+        v = make_float4(v.y, v.z, v.w, v.x);
+    }
 }
 
 __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_constant__ LogprobParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int Batch = 16 * kLpThreads;  // logits: four float4 in flight a thread
     __shared__ LpShared sh;
     cg::cluster_group cl = cg::this_cluster();
     const int S = (int)cl.num_blocks(), rank = (int)cl.block_rank(), row = blockIdx.x / S;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per = ((p.n + S - 1) / S + 3) & ~3;
-    const int i0 = min(p.n, rank * per), i1 = min(p.n, i0 + per);
     const float *x = p.logits + (size_t)row * p.n;
+    // this CTA's logits [i0, i1), whole batches of them from v0, a 16-byte boundary
+    const int i0 = min(p.n, rank * per), i1 = min(p.n, i0 + per);
+    const int v0 = min(i1, i0 + (int)((4u - (((uintptr_t)(x + i0) >> 2) & 3u)) & 3u));
+    const int v1 = v0 + (i1 - v0) / Batch * Batch;
     const int k = p.k;
     // this CTA runs: the matching wait comes before the writes to rank 0
     if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -132,108 +142,124 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
 
     LpSums a = {-INFINITY, 0.f, 0.f};
     uint32_t kmax = 0u;
-    lp_each(
-        x, i0, i1, tid,
-        [&](float v, int) {
-            kmax = max(kmax, lp_key(v));
-            lp_raise(a, v);
-            lp_add(a, v, a.m == -INFINITY ? 0.f : a.m);
-        },
-        [&](const float4 (&v)[4], int, int) {
-            float m = fmaxf(fmaxf(v[0].x, v[0].y), fmaxf(v[0].z, v[0].w));  // numbers before NaN
+    auto add2 = [&](float v0, float v1) {
+        const float mu = a.m == -INFINITY ? 0.f : -a.m;
+        uint64_t s2 = 0ull, t2 = 0ull;
+        lp_add2(s2, t2, v0, v1, pair_f32(mu, mu));
+        a.s += lo_f32(s2) + hi_f32(s2);
+        a.t = fmaf(lo_f32(t2) + hi_f32(t2), 0.69314718055994531f, a.t);
+    };
+    auto add4 = [&](const float4 (&v)[4]) {
+        const float mu = a.m == -INFINITY ? 0.f : -a.m;
+        uint64_t s2[2] = {0ull, 0ull}, t2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int q = 1; q < 4; ++q) m = fmaxf(m, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
-            kmax = max(kmax, lp_key(m));
-            lp_raise(a, m);
-            const float mu = a.m == -INFINITY ? 0.f : a.m;
-            LpSums c[4];
+        for (int q = 0; q < 4; ++q) {
+            lp_add2(s2[0], t2[0], v[q].x, v[q].y, pair_f32(mu, mu));
+            lp_add2(s2[1], t2[1], v[q].z, v[q].w, pair_f32(mu, mu));
+        }
+        s2[0] = add_f32x2(s2[0], s2[1]);
+        t2[0] = add_f32x2(t2[0], t2[1]);
+        a.s += lo_f32(s2[0]) + hi_f32(s2[0]);
+        a.t = fmaf(lo_f32(t2[0]) + hi_f32(t2[0]), 0.69314718055994531f, a.t);
+    };
+    // The k-th largest of the quads' maxima (all threads; k > 0): the value
+    // with fewer than k above it and at least k not below it, four threads a quad
+    auto bound_of = [&]() {
+        uint32_t kq = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
+        kq = max(kq, __shfl_xor_sync(0xffffffffu, kq, 2));
+        if ((lane & 3) == 0) *sh.quad_at(tid >> 2) = kq;
+        if (tid == 0) sh.ncand = 0;
+        __syncthreads();
+        const uint32_t mine = *sh.quad_at(tid >> 2);
+        int above = 0, below = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                c[q] = {0.f, 0.f, 0.f};
+        for (int j = 0; j < LpShared::Quarter; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(sh.quad_at((tid & 3) * LpShared::Quarter) + j);
+            above += (int)(o.x > mine) + (int)(o.y > mine) + (int)(o.z > mine) + (int)(o.w > mine);
+            below += (int)(o.x < mine) + (int)(o.y < mine) + (int)(o.z < mine) + (int)(o.w < mine);
+        }
+        int both = above | below << 16;
+        both += __shfl_xor_sync(0xffffffffu, both, 1);
+        both += __shfl_xor_sync(0xffffffffu, both, 2);
+        if ((both & 0xffff) < k && LpShared::Quads - (both >> 16) >= k) sh.bound = mine;  // equal ones write the same
+        __syncthreads();
+    };
+    // fn(value, index) for the logits [j0, j1), rolled: the ends, and slow paths
+    auto each = [&](int j0, int j1, auto fn) {
+#pragma unroll 4
+        for (int i = j0 + tid; i < j1; i += kLpThreads) fn(x[i], i);
+    };
+    float4 v[4];
+    float m[4];
+    auto load = [&](int j) {
+        const float4 *xv = reinterpret_cast<const float4 *>(x + j) + tid;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) lp_add(c[q], lp_at(v[q], e), mu);
-            }
-            a.s += (c[0].s + c[1].s) + (c[2].s + c[3].s);
-            a.t += (c[0].t + c[1].t) + (c[2].t + c[3].t);
-        });
-    uint32_t kq = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, 1));
-    kq = max(kq, __shfl_xor_sync(0xffffffffu, kq, 2));
-    if ((lane & 3) == 0) sh.quad[tid >> 2] = kq;
+        for (int q = 0; q < 4; ++q) v[q] = xv[q * kLpThreads];
+    };
+    auto tops = [&]() {  // numbers before NaN
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const LpSums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                          __shfl_xor_sync(0xffffffffu, a.t, o)};
-        // the lower lane's share first: both lanes get the same sum
-        a = (lane & o) ? lp_join(b, a) : lp_join(a, b);
+        for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
+    };
+#pragma unroll 2
+    for (int j = v0; j < v1; j += Batch) {
+        load(j);
+        tops();
+        const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        kmax = max(kmax, lp_key(top));
+        lp_raise(a, top);
+        add4(v);
     }
+    auto end = [&](float x1, int) {
+        kmax = max(kmax, lp_key(x1));
+        lp_raise(a, x1);
+        add2(x1, -INFINITY);
+    };
+    each(i0, v0, end);
+    each(v1, i1, end);
+    a = lp_join(a, 32, lane);
     if (lane == 0) sh.warp[warp] = a;
     __syncthreads();
-    if (k > 0) {
-        if (tid >= 32 && tid < 32 + kLpQuads) {  // warps 1..4: the k-th largest of the quads' maxima
-            const int q = tid - 32;
-            const uint32_t mine = sh.quad[q];
-            int r = 0;
-#pragma unroll 8
-            for (int j = 0; j < kLpQuads; j += 4) {
-                const uint4 o = *reinterpret_cast<const uint4 *>(sh.quad + j);
-                r += (o.x > mine || (o.x == mine && j < q)) + (o.y > mine || (o.y == mine && j + 1 < q)) +
-                     (o.z > mine || (o.z == mine && j + 2 < q)) + (o.w > mine || (o.w == mine && j + 3 < q));
-            }
-            if (r == k - 1) sh.bound = mine;
-        }
-    }
-    if (warp == 0) {  // meanwhile warp 0 joins the warps' sums
+    if (warp == 0) {
         a = lane < kLpThreads / 32 ? sh.warp[lane] : LpSums{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            const LpSums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o),
-                              __shfl_xor_sync(0xffffffffu, a.t, o)};
-            a = (lane & o) ? lp_join(b, a) : lp_join(a, b);
-        }
+        a = lp_join(a, 32, lane);
     }
     if (k > 0) {
-        __syncthreads();
+        bound_of();
         const uint32_t bound = sh.bound;
-        const float bv = bound ? lp_value(bound) : 0.f;  // key 0: everything is a candidate
-        auto take = [&](float v, int i) {
-            if (v >= bv || bound == 0u) {
-                const int at = atomicAdd(&sh.ncand, 1);
-                if (at < kLpCand) sh.cand[at] = lp_pair(lp_key(v), i);
+        const float bv = bound ? lp_value(bound) : -INFINITY;  // key 0: everything is a candidate
+        for (int j = v0; j < v1; j += Batch) {
+            if (v1 - v0 > Batch) {  // one batch is still in registers
+                load(j);
+                tops();
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (m[q] >= bv || bound == 0u) lp_take(sh, v[q], j + 4 * (tid + q * kLpThreads), 4, bound);
+        }
+        auto take = [&](float x1, int i) {
+            if (lp_key(x1) >= bound) lp_take(sh, make_float4(x1, 0.f, 0.f, 0.f), i, 1, bound);
         };
-        lp_each(x, i0, i1, tid, take, [&](const float4 (&v)[4], int i, int step) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float m = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
-                if (m >= bv || bound == 0u) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) take(lp_at(v[q], e), i + q * step + e);
-                }
-            }
-        });
+        each(i0, v0, take);
+        each(v1, i1, take);
         __syncthreads();
         const int nc = sh.ncand;
         if (nc <= kLpCand) {
-            for (int c = tid; c < nc; c += kLpThreads) {
+            for (int c = tid >> 1; c < nc; c += kLpThreads / 2) {  // two threads a candidate
                 const unsigned long long mine = sh.cand[c];
+                const int half = (nc + 1) / 2, j0 = (tid & 1) * half, j1 = min(nc, j0 + half);
                 int r = 0;
 #pragma unroll 8
-                for (int j = 0; j < nc; ++j) r += sh.cand[j] > mine;
-                if (r < k) sh.mine[r] = mine;
+                for (int j = j0; j < j1; ++j) r += sh.cand[j] > mine;
+                r += __shfl_xor_sync(3u << (lane & ~1), r, 1);
+                if ((tid & 1) == 0 && r < k) sh.mine[r] = mine;
             }
         } else {  // one by one: the best pair below the last one
             unsigned long long last = ~0ull;
             for (int q = 0; q < k; ++q) {
                 unsigned long long best = 0ull;
-                auto look = [&](float v, int i) {
+                each(i0, i1, [&](float v, int i) {
                     const unsigned long long c = lp_pair(lp_key(v), i);
                     if (c < last && c > best) best = c;
-                };
-                lp_each(x, i0, i1, tid, look, [&](const float4 (&v)[4], int i, int step) {
-#pragma unroll
-                    for (int z = 0; z < 4; ++z)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) look(lp_at(v[z], e), i + z * step + e);
                 });
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) {
@@ -262,8 +288,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
     else
         __syncthreads();
     if (rank != 0) return;
-    LpSums all = sh.sums[0];
-    for (int r = 1; r < S; ++r) all = lp_join(all, sh.sums[r]);
+    const LpSums all =
+        S > 1 ? lp_join(lane < S ? sh.sums[lane] : LpSums{-INFINITY, 0.f, 0.f}, 32, lane) : sh.sums[0];
     // a row whose logits are all -inf allows nothing: log probability -inf for
     // every token, entropy 0
     const bool empty = all.m == -INFINITY && all.s == 0.f;
@@ -283,12 +309,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
         }
     }
     // the k best of the CTAs' lists, by rank (the pairs are all different)
-    if (tid < S * k) {
-        const unsigned long long mine = sh.top[tid];
+    if ((tid >> 1) < S * k) {  // two threads a pair, each half of the pairs
+        const unsigned long long mine = sh.top[tid >> 1];
+        const int half = (S * k + 1) / 2, j0 = (tid & 1) * half, j1 = min(S * k, j0 + half);
         int at = 0;
 #pragma unroll 8
-        for (int j = 0; j < S * k; ++j) at += sh.top[j] > mine;
-        if (mine != 0ull && at < k) {
+        for (int j = j0; j < j1; ++j) at += sh.top[j] > mine;
+        at += __shfl_xor_sync(3u << (lane & ~1), at, 1);
+        if ((tid & 1) == 0 && mine != 0ull && at < k) {
             p.top_val[(size_t)row * k + at] = lp_value((uint32_t)(mine >> 32)) - lse;
             p.top_idx[(size_t)row * k + at] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
         }
@@ -298,13 +326,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
 }  // namespace dev
 
 int launch_logprobs(const LogprobParams &p, int sms, void *stream_) {
-    cudaStream_t stream = (cudaStream_t)stream_;
+    // a CTA a row, or a cluster for each row while those do not fill the device
+    // (512 rows of 65536 by clusters of two: 48 us against 34.5)
     int S = 1;
-    while (S < 8 && (long long)p.rows * S * 2 <= 2 * sms && p.n / (2 * S) >= 2 * dev::kLpThreads) S *= 2;
+    while (S < dev::kLpMaxCluster && (long long)p.rows * S * 2 <= 2 * sms && p.n / (2 * S) >= 2 * dev::kLpThreads) S *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.rows * S), 1, 1);
     cfg.blockDim = dim3(dev::kLpThreads, 1, 1);
-    cfg.stream = stream;
+    cfg.stream = (cudaStream_t)stream_;
     cudaLaunchAttribute attrs[2];
     attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attrs[0].val.programmaticStreamSerializationAllowed = 1;
