@@ -1,20 +1,29 @@
 // attn_prefill.cu -- causal attention of packed prompt rows over the pages of
 // their sequences (honeycrisp/mod.rs, gpu_attention, for a prompt).
 //
-// 16-bit caches (q4attn_prefill_tc_kernel): a CTA takes two tiles of up to 128
-// rows of one kv head's group -- floor(128 / G) consecutive tokens by G query
-// heads, so the group shares every K and V tile -- and walks the key tiles of
-// 128 positions with a running softmax:
-//   S = Q K^T          tcgen05.mma, 128 x 128 fp32 in tensor memory
-//   P = 2^(c S - m)    a thread a row; P (16-bit) over S's columns
+// A CTA (q4attn_prefill_tc_kernel) takes up to NT tiles of up to 128 rows of one
+// kv head's group -- floor(128 / G) consecutive tokens by G query heads, so the
+// group shares every K and V tile -- and walks the key tiles of KT positions with
+// a running softmax:
+//   S = Q K^T          tcgen05.mma, 128 x KT fp32 in tensor memory
+//   P = 2^(c S - m)    64 columns a thread; P (16-bit) over S's columns
 //   O += P V           tcgen05.mma with P as the tensor-memory operand
 // Q, K and V tiles come by tensor-map copies (TMA, 128-byte swizzle) straight
 // from the packed rows and the pages; V is the MN-major operand, so nothing is
-// transposed.  Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, warp 8
-// issues the MMAs, warp 9 the copies.  While one tile's softmax runs, the
-// tensor core works on the other's products.  O is rescaled in tensor memory
-// only when a row's maximum grew by more than 2^8 (the sums stay exact: the
-// reference maximum is the row's own, and its factor cancels).
+// transposed.  Sixteen softmax warps, two that issue MMAs, one that copies.
+// While some tiles' softmax runs, the tensor core works on the others'
+// products: a tile's own chain (scores, weights, product) takes several times
+// its tensor work.  16-bit at head size 64: four tiles, key tiles of 64 positions
+// (4 x (S 64 + O 64) columns fill the tensor memory), a thread a row.  Else two
+// tiles (one for fp32 at head size 128, whose parts fill the shared memory), key
+// tiles of 128 positions, two warps a row that exchange its maximum.
+// An MMA of 128 rows takes about 60 cycles per K = 16 at N = 64 as at N = 128
+// (measured by its issue), so at head size 64 the product runs at half the
+// tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
+// positions, P beside S and S a key tile ahead, and 277 with four of 64.
+// O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
+// (the sums stay exact: the reference maximum is the row's own, and its factor
+// cancels).
 //
 // Masked positions: scores are replaced before the maximum; V rows behind the
 // sequence's end are zeroed in shared memory.  A non-finite value at a position
@@ -29,10 +38,9 @@
 namespace q4 {
 namespace dev {
 
-constexpr int kPfKeys = 128;                // positions of a key tile
-constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values
-constexpr int kPfSoft = 16;                 // softmax warps: 2 row tiles x 2 column halves x 4 row quarters
-constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // an MMA warp for each row tile, the copy warp
+constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values (a block of a Q tile)
+constexpr int kPfSoft = 16;                 // softmax warps: row tiles x column halves x 4 row quarters
+constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // two MMA warps, the copy warp
 constexpr int kPfThreads = 32 * (kPfSoft + 3);
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
@@ -54,23 +62,26 @@ struct PfT<float> {
 
 template <int D, int Parts>
 struct PfCfg {
+    static constexpr int KT = D == 64 && Parts == 1 ? 64 : 128;  // positions of a key tile
+    static constexpr int HF = KT / 64;                 // warps (columns of 64) that share a row
+    static constexpr int NT = KT == 64 ? 4 : D * Parts == 256 ? 1 : 2;  // row tiles of a CTA at most
     static constexpr int NB = D / 64;                  // 64-value blocks of a row
-    static constexpr int Tile = NB * kPfBlk;           // one part of a Q, K or V tile
-    static constexpr int NT = D * Parts == 256 ? 1 : 2;  // row tiles of a CTA
-    static constexpr int QTile = Parts * Tile;
-    static constexpr int NS = D == 128 || Parts == 2 ? 5 : 6;  // ring stages: per key tile K's parts, then V's
+    static constexpr int KBlk = KT * 128;              // a block of a K or V tile
+    static constexpr int Tile = NB * KBlk;             // one part of a K or V tile
+    static constexpr int QPart = NB * kPfBlk, QTile = Parts * QPart;
+    // ring stages: per key tile K's parts, then V's
+    static constexpr int NS = KT == 64 ? 12 : D == 64 ? 9 : 5;
     static constexpr int OffQ = 0, OffRing = NT * QTile, OffBar = OffRing + NS * Tile;
-    // tensor memory columns: S0 0, S1 128, O0 and O1 from 256.  One part at D =
-    // 64: P has columns of its own, so the next scores start as soon as these
-    // are read; else it lies over its S (two parts: each column half's parts
-    // over that half's columns, 16 columns of hi and 16 of lo per 32 positions)
-    static constexpr bool Sep = D == 64 && Parts == 1;
-    static constexpr int ColO = 256, ColP = Sep ? 256 + 2 * D : 0, PStep = Sep ? 64 : 128;
-    static constexpr int XBuf = Sep ? 2 : 1;           // exchange buffers
-    static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][buffer][half][row]
-    static constexpr int Smem = OffX + XBuf * 2 * 2 * 128 * 4;
+    // tensor memory columns: S of tile i from KT i, O of tile i from ColO + D i; P
+    // lies over its S (two parts: each column half's over its own, 16 columns of hi
+    // and 16 of lo per 32 positions)
+    static constexpr int ColO = NT * KT;
+    static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][half][row]
+    static constexpr int Smem = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
-    static_assert(16 * NS + 168 <= 448, "barriers before the tensor-memory address");
+    static_assert(ColO + NT * D <= 512, "tensor memory");
+    static_assert(4 * HF * NT <= kPfSoft, "softmax warps");
+    static_assert(16 * NS + 32 * NT + 88 <= 448, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
     static constexpr int p_col(int ks) {
         return Parts == 1 ? 8 * ks : 64 * (ks / 4) + 32 * ((ks % 4) / 2) + 8 * (ks % 2);
@@ -149,18 +160,19 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPfThreads, 1)
     q4attn_prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mq,
                              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                             const int box_rows) {
+                             const int box_rows, const int row_tiles) {
     using M = typename PfT<T>::M;
     constexpr int NP = PfT<T>::Parts;
     using Cf = PfCfg<D, NP>;
     constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
-    constexpr int NB = Cf::NB, NS = Cf::NS;
+    constexpr int NB = Cf::NB, NS = Cf::NS, NT = Cf::NT, KT = Cf::KT, HF = Cf::HF;
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const uint32_t bars = sb + Cf::OffBar;
-    const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 16, b_p = b_s + 16,
-                   b_o = b_p + 16, b_fix = b_o + 16, b_drain = b_fix + 8, b_x = b_drain + 16, b_sf = b_x + 64;
+    const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 8 * NT,
+                   b_p = b_s + 8 * NT, b_o = b_p + 8 * NT, b_fix = b_o + 8 * NT, b_drain = b_fix + 8,
+                   b_x = b_drain + 16;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 448);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 452);
     PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 464);
@@ -173,12 +185,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mbar_init(b_full + 8 * i, 1);
             mbar_init(b_empty + 8 * i, 2);  // one for each MMA warp
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NT; ++i) {
             mbar_init(b_q + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 8);
+            mbar_init(b_p + 8 * i, 4 * HF);
             mbar_init(b_o + 8 * i, 1);
-            mbar_init(b_sf + 8 * i, 8);
         }
         for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
         mbar_init(b_fix, 1);
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kPfCopy) {
-        const PfTile t = pf_find(p, idx, Cf::NT * TQ, lane);
+        const PfTile t = pf_find(p, idx, row_tiles * TQ, lane);
         if (lane == 0) *tile_s = t;
     }
     tc::fence_before_sync();
@@ -205,12 +216,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (warp == kPfMma) tc::tmem_dealloc(taddr, 512);
         return;
     }
-    const int nt = t.tokens > TQ ? 2 : 1;  // row tiles in use
+    const int nt = (t.tokens + TQ - 1) / TQ;  // row tiles in use
     const int key_end = t.pos0 + t.tokens;
     const int key_lo = p.window > 0 && t.pos0 + 1 > p.window ? t.pos0 + 1 - p.window : 0;
-    const int k_first = key_lo & ~(kPfKeys - 1);
-    const int nk = (key_end - k_first + kPfKeys - 1) / kPfKeys;
-    const int tail = key_end - (k_first + (nk - 1) * kPfKeys);  // positions of the last key tile
+    const int k_first = key_lo & ~(KT - 1);
+    const int nk = (key_end - k_first + KT - 1) / KT;
+    const int tail = key_end - (k_first + (nk - 1) * KT);  // positions of the last key tile
     auto fail = [&]() {
         *abort_flag = 1;
         atomicExch(p.err, 6);
@@ -231,9 +242,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // lane = 64-value block bl, box r of a tile (at most 16 boxes); the next key
         // tile's pages are looked up while this one's copies go out: looked up in
         // place they held the ring back (a tile every 1400 cycles)
-        const int boxes = kPfKeys / box_rows, bl = lane / boxes, r = lane - bl * boxes;
+        const int boxes = KT / box_rows, bl = lane / boxes, r = lane - bl * boxes;
         auto lookup = [&](int j, int &page, int &slot) {
-            const int key = k_first + j * kPfKeys + r * box_rows, col = page_col(p.kv, key);
+            const int key = k_first + j * KT + r * box_rows, col = page_col(p.kv, key);
             slot = key - col * p.kv.page;
             page = bl < NB && key < key_end ? page_raw(p.kv, t.seq, col) : -1;
         };
@@ -246,9 +257,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int page = page_ok(p.kv, page1), slot = slot1;
             // a page out of range is copied as zeros (its coordinate is out of
             // the map's range); below the window it may be gone
-            const int key = k_first + j * kPfKeys + r * box_rows;
+            const int key = k_first + j * KT + r * box_rows;
             if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
-            const int live = min(boxes, (key_end - k_first - j * kPfKeys + box_rows - 1) / box_rows);  // boxes with attended positions
+            const int live = min(boxes, (key_end - k_first - j * KT + box_rows - 1) / box_rows);  // boxes with attended positions
             if (j + 1 < nk) lookup(j + 1, page1, slot1);
             for (int kv = 0; kv < 2 * NP; ++kv) {  // K's parts, V's parts
                 ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * st, ph, lim));
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
                 __syncwarp();
                 if (bl < NB && r < live)
-                    tma5(sb + Cf::OffRing + st * Cf::Tile + bl * kPfBlk + r * box_rows * 128, kv >= NP ? &mv : &mk,
+                    tma5(sb + Cf::OffRing + st * Cf::Tile + bl * Cf::KBlk + r * box_rows * 128, kv >= NP ? &mv : &mk,
                          64 * bl, slot, hk, page, kv % NP, b_full + 8 * st);
                 ++issued;
                 if (++st == NS) {
@@ -269,16 +280,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
             }
         }
-        if (issued == 2 * NP * nk && tail < kPfKeys) {
+        if (issued == 2 * NP * nk && tail < KT) {
             // V rows behind the last position: zeros, whatever the page holds
             for (int n = issued - NP; ok && n < issued; ++n) {
                 const int sv = n % NS;
                 ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * sv, (uint32_t)(n / NS) & 1u, lim));
                 uint8_t *v = sm + Cf::OffRing + sv * Cf::Tile;
-                for (int x = tail * 8 + lane; ok && x < kPfKeys * 8; x += 32)
+                for (int x = tail * 8 + lane; ok && x < KT * 8; x += 32)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<uint4 *>(v + b * kPfBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(v + b * Cf::KBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -291,17 +302,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
     } else if (warp == kPfMma || warp == kPfMma + 1) {
         // ------------------------------------------------------------ MMA issue
-        // one warp a row tile, so that neither waits for the other's softmax
-        // (one warp for both: 315 us against 277 at 8192 rows, head size 64)
-        const int i = warp - kPfMma;
+        // warp w: row tiles w and w + 2, so that tiles seldom wait for each other's
+        // softmax (one warp for two tiles: 315 us against 277 at 8192 rows, head
+        // size 64, two tiles a CTA)
+        const int w = warp - kPfMma;
+        const int last = w + 2 < nt ? w + 2 : w;  // this warp's last tile
         const bool leader = tc::elect_one();
-        const uint32_t id_s = tc::idesc_16(128, 128, BF, false), id_o = tc::idesc_16(128, D, BF, true);
-        const uint64_t qd = tc::smem_desc_sw128(sb + Cf::OffQ + i * Cf::QTile, 16, 1024);
+        const uint32_t id_s = tc::idesc_16(128, KT, BF, false), id_o = tc::idesc_16(128, D, BF, true);
+        const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
         const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
-        const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, kPfBlk, 1024);
-        const uint32_t ts = taddr + 128u * i, to = taddr + Cf::ColO + D * i, tp = taddr + Cf::ColP + Cf::PStep * i;
+        const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, Cf::KBlk, 1024);
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)); };
-        // both row tiles free a ring stage; a tile alone does it twice
+        // both warps free a ring stage after their last tile; a warp alone does it twice
         auto release = [&](int st) {
             tc::commit(b_empty + 8 * st);
             if (nt == 1) tc::commit(b_empty + 8 * st);
@@ -315,9 +327,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ph ^= 1;
             }
         };
-        // S = Q K^T of the NP ring stages from st on, which have landed
-        auto scores = [&](int st) {
+        auto landed = [&](int s0, uint32_t p0) {  // the NP stages from s0 on
+            bool all = true;
+#pragma unroll
+            for (int y = 0; y < NP; ++y) {
+                const int at = s0 + y < NS ? s0 + y : s0 + y - NS;
+                all = all && wait(b_full + 8 * at, s0 + y < NS ? p0 : p0 ^ 1u);
+            }
+            return all;
+        };
+        // S_i = Q_i K^T of the NP ring stages from st on, which have landed
+        auto scores = [&](int i, int st) {
             if (leader) {
+                const uint32_t ts = taddr + (uint32_t)(KT * i);
+                const uint64_t qd = q0 + (uint64_t)((i * Cf::QTile) >> 4);
 #pragma unroll
                 for (int y = 0; y < NP; ++y) {
                     const int sk = st + y < NS ? st + y : st + y - NS;
@@ -325,22 +348,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                     for (int x = 0; x < NP - y; ++x)  // Q's part x by K's part y
 #pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint64_t off = (uint64_t)(((ks / 4) * kPfBlk + (ks % 4) * 32) >> 4);
-                            tc::mma_f16(ts, qd + (uint64_t)((x * Cf::Tile) >> 4) + off, kd + off, id_s, (x | y | ks) != 0);
-                        }
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            tc::mma_f16(ts, qd + (uint64_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
+                                        kd + (uint64_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
+                                        (x | y | ks) != 0);
                     if (y == NP - 1) tc::commit(b_s + 8 * i);
-                    release(sk);
+                    if (i == last) release(sk);
                 }
             }
             __syncwarp();
         };
-        if (i < nt) {
-            bool ok = wait(b_q + 8 * i, 0u);
-            for (int y = 0; y < NP; ++y) ok = ok && wait(b_full + 8 * y, 0u);
-            if (ok) {
+        if (w < nt) {
+            bool ok = landed(0, 0u);
+            for (int i = w; ok && i < nt; i += 2) {
+                ok = wait(b_q + 8 * i, 0u);
                 tc::fence_after_sync();
-                scores(0);
+                if (ok) scores(i, 0);
             }
             for (int y = 0; y < NP; ++y) next();
             for (int j = 0; ok && j < nk; ++j) {
@@ -350,65 +373,54 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 const int sk = st;  // the next K's
                 const uint32_t phk = ph;
                 for (int y = 0; y < NP; ++y) next();
-                auto landed = [&](int s0, uint32_t p0) {
-                    bool all = true;
-#pragma unroll
-                    for (int y = 0; y < NP; ++y) {
-                        const int at = s0 + y < NS ? s0 + y : s0 + y - NS;
-                        all = all && wait(b_full + 8 * at, s0 + y < NS ? p0 : p0 ^ 1u);
-                    }
-                    return all;
-                };
                 ok = landed(sv, phv);
                 if (j + 1 < nk) ok = ok && landed(sk, phk);
-                if (Cf::Sep && j + 1 < nk) {  // the next scores, while the softmax of these runs
-                    ok = ok && wait(b_sf + 8 * i, (uint32_t)j & 1u);
+                if (j == nk - 1 && tail < KT) ok = ok && wait(b_fix, 0u);
+                for (int i = w; ok && i < nt; i += 2) {
+                    ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
+                    if (!ok || *abort_flag) break;
                     tc::fence_after_sync();
-                    if (ok) scores(sk);
-                }
-                if (j == nk - 1 && tail < kPfKeys) ok = ok && wait(b_fix, 0u);
-                ok = ok && wait(b_p + 8 * i, (uint32_t)j & 1u);
-                if (!ok || *abort_flag) break;
-                tc::fence_after_sync();
-                if (leader) {  // O += P V
+                    if (leader) {  // O_i += P_i V
+                        const uint32_t to = taddr + (uint32_t)(Cf::ColO + D * i), tp = taddr + (uint32_t)(KT * i);
 #pragma unroll
-                    for (int y = 0; y < NP; ++y) {
-                        const int at = sv + y < NS ? sv + y : sv + y - NS;
-                        const uint64_t vd = v0 + (uint64_t)((at * Cf::Tile) >> 4);
+                        for (int y = 0; y < NP; ++y) {
+                            const int at = sv + y < NS ? sv + y : sv + y - NS;
+                            const uint64_t vd = v0 + (uint64_t)((at * Cf::Tile) >> 4);
 #pragma unroll
-                        for (int x = 0; x < NP - y; ++x)  // P's part x by V's part y
+                            for (int x = 0; x < NP - y; ++x)  // P's part x by V's part y
 #pragma unroll
-                            for (int ks = 0; ks < kPfKeys / 16; ++ks)
-                                tc::mma_f16_ta(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint64_t)((ks * 2048) >> 4), id_o,
-                                               (j | x | y | ks) != 0);
-                        if (y == NP - 1 && (Cf::Sep || j + 1 == nk)) tc::commit(b_o + 8 * i);
-                        release(at);
+                                for (int ks = 0; ks < KT / 16; ++ks)
+                                    tc::mma_f16_ta(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint64_t)((ks * 2048) >> 4),
+                                                   id_o, (j | x | y | ks) != 0);
+                            if (y == NP - 1 && j + 1 == nk) tc::commit(b_o + 8 * i);
+                            if (i == last) release(at);
+                        }
                     }
+                    __syncwarp();
+                    if (j + 1 < nk) scores(i, sk);
                 }
-                __syncwarp();
-                if (!Cf::Sep && j + 1 < nk) scores(sk);
+                if (*abort_flag) break;
             }
             if (!ok && leader) fail();
             if (leader) {  // nothing is in flight when the CTA ends
-                tc::commit(b_drain + 8 * i);
-                mbar_wait(b_drain + 8 * i, 0u, kWaitCycles);
+                tc::commit(b_drain + 8 * w);
+                mbar_wait(b_drain + 8 * w, 0u, kWaitCycles);
             }
             __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ softmax
-        // tile i, column half hf of every key tile, row r
-        const int i = warp >> 3, hf = (warp >> 2) & 1, r = 32 * (warp & 3) + lane;
+        // tile i, columns 64 hf .. of every key tile, row r
+        const int i = (warp >> 2) / HF, hf = (warp >> 2) % HF, r = 32 * (warp & 3) + lane;
         if (i < nt) {
             const int tok = i * TQ + r / G, g = r % G;
             const bool live = r < G * TQ && tok < t.tokens;
             const int pos = t.pos0 + (live ? tok : min(i * TQ, t.tokens - 1));
             const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t ts = taddr + lanes + 128u * i, to = taddr + lanes + Cf::ColO + D * i;
-            const uint32_t tp = taddr + lanes + Cf::ColP + Cf::PStep * i;
-            const uint32_t bx = b_x + 8 * (4 * i + (warp & 3));
-            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * Cf::XBuf * i;  // [buffer][half][row]
+            const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
+            const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
+            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
             float c = p.scale * 1.4426950408889634f, vback = 1.f;
             if constexpr (NP == 2) {  // the powers of two of Q's row, K and V back
                 c *= pf_back(p.maxima[hk]) * (live ? p.qback[(size_t)(t.row0 + tok) * p.H + hk * G + g] : 0.f);
@@ -416,9 +428,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             // a row's value of the other column half, exchange number n: its warp
             // has read the one before from `buf` by the time it is written again
-            // (two buffers, or S of the next key tile comes after every warp's P)
+            // (S of the next key tile comes after every warp's P)
             auto other = [&](float mine, int n, float *buf, bool &ok) {
-                if (Cf::XBuf == 2) buf += 256 * (n & 1);
                 buf[hf * 128 + r] = mine;
                 __syncwarp();
                 if (lane == 0) pf_arrive(bx);
@@ -436,13 +447,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 tc::ld32(ts + 64 * hf + 32, s + 32);
                 tc::wait_ld32(s);
                 tc::wait_ld32(s + 32);
-                if (Cf::Sep) {
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) pf_arrive(b_sf + 8 * i);
-                }
-                const int k0 = k_first + j * kPfKeys;
-                if (k0 + kPfKeys - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
+                const int k0 = k_first + j * KT;
+                if (k0 + KT - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
                     const int hi = pos - k0 - 64 * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - 64 * hf : -1;
 #pragma unroll
                     for (int e = 0; e < 64; ++e)
@@ -457,25 +463,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     for (int q = 0; q < 4; ++q)
                         mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                top = fmaxf(top, other(top, j, xs, ok));
-                // the products of the key tile before have read P, and O holds them
-                // (with P over S, S itself came after them)
-                if (ok && Cf::Sep && j > 0) ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, (uint32_t)(j - 1) & 1u, lim));
-                if (!ok) break;
-                if (Cf::Sep) tc::fence_after_sync();
+                if constexpr (HF == 2) {
+                    top = fmaxf(top, other(top, j, xs, ok));
+                    if (!ok) break;
+                }
                 if (j == 0) {
                     m = top;
                 } else {
                     const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
                     if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
+                        // (S came after the product before it: O is complete)
                         const float mn = fmaxf(m, top);
                         const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                         l *= alpha;
                         m = mn;
 #pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
+                        for (int q = 0; q < D / (16 * HF); ++q) {
                             uint32_t o[16];
-                            const uint32_t at = to + (D / 2) * hf + 16 * q;
+                            const uint32_t at = to + (D / HF) * hf + 16 * q;
                             tc::ld16(at, o);
                             tc::wait_ld16(o);
 #pragma unroll
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 const float mc = (m == -INFINITY ? 0.f : -m * c) + PfT<T>::PExp;
                 const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
                 uint64_t sum[2] = {0ull, 0ull};
-                // (one part over S's columns 0..63: both halves have read theirs, the exchange)
+                // (over S's columns: the row's warps have read them)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
@@ -502,8 +507,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             s[32 * q + e] = pack2<M>(a - h.x, b - h.y);
                         }
                     }
-                    tc::st16(tp + (NP == 2 ? 64 * hf + 32 * q : 32 * hf + 16 * q), w);
-                    if constexpr (NP == 2) tc::st16(tp + 64 * hf + 32 * q + 16, s + 32 * q);
+                    tc::st16(ts + (NP == 2 ? 64 * hf + 32 * q : 32 * hf + 16 * q), w);
+                    if constexpr (NP == 2) tc::st16(ts + 64 * hf + 32 * q + 16, s + 32 * q);
                 }
                 const uint64_t s2 = add_f32x2(sum[0], sum[1]);
                 l += lo_f32(s2) + hi_f32(s2);
@@ -513,20 +518,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
             if (ok && !*abort_flag) {
-                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, Cf::Sep ? (uint32_t)(nk - 1) & 1u : 0u, lim));
-                if (ok) l += other(l, nk, xs, ok);
+                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, 0u, lim));
+                if constexpr (HF == 2)
+                    if (ok) l += other(l, nk, xs, ok);
             }
             if (!ok && lane == 0) fail();
             if (ok && !*abort_flag) {
                 tc::fence_after_sync();
                 const float inv = (l == 0.f ? 0.f : 1.f / l) * vback;
                 const int row = t.row0 + tok, head = hk * G + g;
-                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / 2) * hf;
+                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / HF) * hf;
                 float worst = 0.f;  // NaN or infinite where a value is
 #pragma unroll
-                for (int q = 0; q < D / 64; ++q) {
+                for (int q = 0; q < D / (32 * HF); ++q) {
                     uint32_t o[32];
-                    tc::ld32(to + (D / 2) * hf + 32 * q, o);
+                    tc::ld32(to + (D / HF) * hf + 32 * q, o);
                     tc::wait_ld32(o);
                     uint4 w[sizeof(T) * 2];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
@@ -548,7 +554,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 }
                 // rows that are not finite: by the definition (whole rows, after
                 // both halves have stored theirs); Q's tile is free by now
-                worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::QTile), ok);
+                if constexpr (HF == 2)
+                    worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::QTile), ok);
+                __syncwarp();
                 unsigned again = __ballot_sync(0xffffffffu, ok && live && hf == 0 && worst != 0.f);
                 while (again) {
                     const int src = __ffs(again) - 1;
@@ -614,7 +622,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // fn(sequence, kv head, first position, end) for this CTA's items: the chunks
-// of every sequence's attended positions (from a key tile's start) by kv heads.
+// of every sequence's attended positions (from a key tile's start: a multiple of 64) by kv heads.
 template <class F>
 __device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
     __shared__ long long prefix[kMaxSeqs + 1];
@@ -626,7 +634,7 @@ __device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
         lo = end = 0;
         if (rows == 0 || first < 0 || first >= (long long)p.kv.width * p.kv.page) return;
         end = (int)min((long long)first + rows, (long long)p.kv.width * p.kv.page);
-        lo = (p.window > 0 && first + 1 > p.window ? first + 1 - p.window : 0) & ~(kPfKeys - 1);
+        lo = (p.window > 0 && first + 1 > p.window ? first + 1 - p.window : 0) & ~127;
     };
     long long n[4], own = 0;
 #pragma unroll
@@ -775,7 +783,7 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
     // positions a copy box takes: a power of two that divides the page, so
     // that no box crosses a page's end (one page alone: whole key tiles)
-    int box_rows = 128;
+    int box_rows = Cf::KT;
     while (p.kv.width > 1 && p.kv.page % box_rows != 0) box_rows /= 2;
     const void *q = p.q, *k = p.kv.k, *v = p.kv.v;
     cudaLaunchAttribute attr;
@@ -800,10 +808,15 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
     auto kern = dev::q4attn_prefill_tc_kernel<T, D>;
     static size_t smem_set[64] = {0};
     if (!raise_smem(kern, (size_t)Cf::Smem, smem_set)) return -1;
-    // at most one part-filled tile a sequence
-    const long long tiles = (long long)p.rows / (Cf::NT * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows);
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(tiles * p.kv.hkv), dev::kPfThreads, Cf::Smem, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows) == cudaSuccess ? 0 : -1;
+    // row tiles a CTA: NT, fewer while that leaves the device without a CTA and a
+    // half an SM; at most one part-filled CTA a sequence
+    int row_tiles = Cf::NT;
+    auto ctas = [&](int n) {
+        return ((long long)p.rows / (n * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows)) * p.kv.hkv;
+    };
+    while (row_tiles > 1 && 2 * ctas(row_tiles) < 3 * sms) row_tiles /= 2;
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas(row_tiles), dev::kPfThreads, Cf::Smem, stream, &attr);
+    return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows, row_tiles) == cudaSuccess ? 0 : -1;
 }
 
 int launch_prefill(const PrefillParams &p, int dtype, int sms, void *stream_) {
