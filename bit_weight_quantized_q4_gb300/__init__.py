@@ -870,7 +870,8 @@ def q4_kv_append(k, v, pages: KVPages, cu_rows, start=None, q=None, rope=None, q
         op = _ptr(q_out, "q_out", pages.dtype, shape, dev)
         if rows:
             nb = 4 * rows * D
-            _apart(op, rows * H * D * pages.itemsize, (qp, nb * H), (kp, nb * pages.kv_heads), (vp, nb * pages.kv_heads))
+            _apart(op, rows * H * D * pages.itemsize, (qp, nb * H), (kp, nb * pages.kv_heads),
+                   (vp, nb * pages.kv_heads), (pages._c.k, pages.nbytes), (pages._c.v, pages.nbytes))
     elif q_out is not None:
         raise ValueError("q_out needs q")
     _check(_launch(dev, lib().q4_kv_append, pages._ref, qp, kp, vp, rows, cu, st, H, cp, sp, rope_rows, op),
@@ -968,11 +969,12 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
     [rows, min(top, n)], their indices int32)``; ties go to the lowest index,
     a negative token's log probability is 0 (a row that is not scored)."""
     torch = _torch()
-    logits = _dev_f32(logits, "logits")
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA float32 tensor")
     if logits.dim() != 2 or logits.shape[1] == 0:
         raise ValueError("logits must be [rows, n]")
-    dev = logits.device
-    rows, n = logits.shape
+    dev, (rows, n) = logits.device, logits.shape
+    x = _ptr(logits, "logits", torch.float32, (rows, n), dev)
     k = min(int(top), n)
     f32, i32 = torch.float32, torch.int32
     lp = tok = ent = lpp = entp = None
@@ -985,6 +987,6 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
         entp = ent.data_ptr()
     val = torch.empty((rows, max(0, k)), dtype=f32, device=dev)
     idx = torch.empty((rows, max(0, k)), dtype=i32, device=dev)
-    _check(_launch(dev, lib().q4_logprobs, logits.data_ptr(), rows, n, tok, k, lpp, entp,
+    _check(_launch(dev, lib().q4_logprobs, x, rows, n, tok, k, lpp, entp,
                    val.data_ptr() if k > 0 else None, idx.data_ptr() if k > 0 else None), "q4_logprobs")
     return lp, ent, val, idx

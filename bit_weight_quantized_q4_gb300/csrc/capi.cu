@@ -942,10 +942,13 @@ q4::PagedKv paged_view(const q4_kv_pages *c) {
     return q4::PagedKv{c->k,     c->v,   c->table, c->num_pages, c->page_size, c->kv_heads, c->nseq,
                        c->width, mul,    s - 1};
 }
-// per (sequence, kv head) counters at the start of the paged workspace
-inline size_t paged_count_bytes(const q4_kv_pages *c) {
-    return ((size_t)c->nseq * c->kv_heads * sizeof(int) + 15) / 16 * 16;
-}
+// The (sequence, kv head) counters at the start of the paged workspace: room
+// for every geometry, so that calls of different ones can share a workspace
+// (none's partial results lie where another's counters do).
+constexpr int kMaxPagedPairs = 1 << 16;
+constexpr size_t kPagedCountBytes = kMaxPagedPairs * sizeof(int);
+
+bool scale_ok(float scale) { return scale >= 0.f && std::isfinite(scale); }
 }  // namespace
 
 extern "C" q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k, const float *v,
@@ -1001,7 +1004,7 @@ extern "C" q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, in
                                      void *workspace, size_t workspace_bytes, cudaStream_t stream) {
     Q4_TRY(check_pages(pages));
     Q4_TRY(check_heads(pages, H));
-    if (rows < 0 || rows > (1 << 24) || window < 0) return Q4_ERR_SHAPE;
+    if (rows < 0 || rows > (1 << 24) || window < 0 || !scale_ok(scale)) return Q4_ERR_SHAPE;
     if (rows == 0) return Q4_OK;
     Q4_TRY(check_act(q));
     Q4_TRY(check_act(out));
@@ -1036,9 +1039,9 @@ extern "C" q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, in
 
 extern "C" size_t q4_attn_paged_workspace_bytes(const q4_kv_pages *pages, int32_t H) {
     if (check_pages_shape(pages) != Q4_OK || check_heads(pages, H) != Q4_OK) return 0;
-    return paged_count_bytes(pages) + (size_t)kMaxPagedCtas * 2 *
-                                          q4::paged_attn_slot_floats(pages->head_dim, H / pages->kv_heads) *
-                                          sizeof(float);
+    if ((long long)pages->nseq * pages->kv_heads > kMaxPagedPairs) return 0;
+    return kPagedCountBytes + (size_t)kMaxPagedCtas * 2 *
+                                  q4::paged_attn_slot_floats(pages->head_dim, H / pages->kv_heads) * sizeof(float);
 }
 
 extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k_new, const float *v_new,
@@ -1053,7 +1056,7 @@ extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, con
     Q4_TRY(check_ints(positions));
     Q4_TRY(check_rope(rope_cos, rope_sin, rope_rows));
     Q4_TRY(check_act(out));
-    if (window < 0) return Q4_ERR_SHAPE;
+    if (window < 0 || !scale_ok(scale) || (long long)pages->nseq * pages->kv_heads > kMaxPagedPairs) return Q4_ERR_SHAPE;
     if (!workspace || workspace_bytes < q4_attn_paged_workspace_bytes(pages, H)) return Q4_ERR_WORKSPACE;
     if (!aligned16(workspace)) return Q4_ERR_ALIGN;
     const int sms = num_sms();
@@ -1068,7 +1071,7 @@ extern "C" q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, con
     p.rope_sin = rope_sin;
     p.out = out;
     p.count = (int *)workspace;
-    p.part = (float *)((char *)workspace + paged_count_bytes(pages));
+    p.part = (float *)((char *)workspace + kPagedCountBytes);
     p.H = H;
     p.D = pages->head_dim;
     p.window = window;

@@ -326,7 +326,7 @@ q4_status q4_decode_check(const void *workspace, cudaStream_t stream);
 /* Synchronises `stream` and reports whether any GEMV-family kernel of this
  * library on the current device (q4_gemv, q4_nrm_gemv, q4_dual_gemv,
  * q4_gus_nrm, q4_res_gemv, q4_argmax, q4_argmax_noalloc, q4_gemm,
- * q4_attn_decode, q4_attn_prefill) gave up waiting for its weight (or K/V)
+ * q4_attn_decode, q4_attn_prefill, q4_attn_paged) gave up waiting for its weight (or K/V)
  * copies since the last check, or a kernel of the paged cache or of
  * q4_logprobs met a position, page or token out of range (Q4_ERR_CUDA; the
  * flag is then cleared) or not (Q4_OK).  Each kernel bounds every such wait (about a
@@ -345,7 +345,8 @@ q4_status q4_device_check(cudaStream_t stream);
  * before a wait for a weight-copy stage gives up (<= 0: the default, 2^31,
  * about a second); copy_extra_bytes (0..4096, a multiple of 16), bytes each
  * weight-copy stage of the GEMV kernels expects beyond its copies (the first
- * stage only for q4_gemm and for each CTA of q4_attn_decode).  A non-zero extra makes every
+ * stage only for q4_gemm, for each CTA of q4_attn_decode and q4_attn_prefill
+ * and for each warp of q4_attn_paged).  A non-zero extra makes every
  * such wait run out: the kernel then records the failure (q4_decode_check,
  * q4_device_check), waits for its copies in flight (always bounded by the
  * default second) and returns with its outputs undefined; nothing faults or
@@ -457,8 +458,9 @@ q4_status q4_rope_table(int32_t max_seq, int32_t D, double rope_theta, float *ho
  * are device memory with 4-byte alignment; everything else is 16-byte aligned.
  * They are read by the kernels, so a captured launch follows their values.  A
  * position or page id out of range is never followed: the kernel leaves that
- * row (append) or those positions (attention) out and records it, and
- * q4_device_check then returns Q4_ERR_CUDA. */
+ * row (append) or those positions (attention) out, or lets them count as zeros
+ * (q4_attn_prefill: that sequence's rows are then undefined), and records it,
+ * and q4_device_check then returns Q4_ERR_CUDA. */
 typedef enum { Q4_T_F32 = 0, Q4_T_F16 = 1, Q4_T_BF16 = 2 } q4_dtype;
 typedef struct {
     void *k, *v;
@@ -488,10 +490,15 @@ q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k,
  * h / (H / kv_heads).  q, out: [rows][H][D] of the cache's type, not
  * overlapping; out rows from cu_rows[nseq] on are left alone.  H / kv_heads in
  * 1..16.  What masked positions hold (infinities, NaN) does not reach out.
+ * scale: finite, not negative (as q4_attn_paged's).  A row with no attended
+ * position (every page out of range) is zeros.
  * Numerics: fp32 sums and softmax statistics; with a 16-bit type the softmax
- * weights enter the products rounded once to it.
- * workspace: q4_attn_prefill_workspace_bytes bytes (may be 0: then NULL), no
- * initialisation needed. */
+ * weights enter the products rounded once to it; with fp32, q, k and the weights
+ * enter with about 22 bits, k and v relative to their kv head's largest value
+ * over the attended positions (2^-40 of it at least).
+ * workspace: q4_attn_prefill_workspace_bytes bytes, no initialisation needed,
+ * not shared by calls that run at the same time: 0 (NULL will do) for the 16-bit
+ * types; for fp32 the operands' parts, as large as the cache itself and q. */
 size_t q4_attn_prefill_workspace_bytes(const q4_kv_pages *pages, int32_t rows, int32_t H);
 q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows, const int32_t *cu_rows,
                           const int32_t *start, int32_t H, int32_t window, float scale, void *out, void *workspace,
@@ -505,9 +512,12 @@ q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows,
  * [nseq][H][D] fp32; k_new, v_new: [nseq][kv_heads][D] fp32; positions: [nseq].
  * H / kv_heads in 1..16.  Two sequences must not append to one page slot.
  * workspace: q4_attn_paged_workspace_bytes bytes, zero-filled by the caller
- * before its first use (every call leaves its counters zero); calls (and
- * captured graphs) that share one must not run at the same time.  Results do
- * not depend on scheduling. */
+ * before its first use (every call leaves its counters zero, so calls of
+ * different shapes can share one that is large enough); calls (and captured
+ * graphs) that share one must not run at the same time.  nseq * kv_heads <=
+ * 65536.  Results do not depend on scheduling.
+ * Numerics: q and the softmax weights enter with 22 bits or more, the cache's
+ * values exactly; fp32 sums and softmax statistics. */
 size_t q4_attn_paged_workspace_bytes(const q4_kv_pages *pages, int32_t H);
 q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k_new, const float *v_new,
                         const int32_t *positions, int32_t H, int32_t window, float scale, const float *rope_cos,

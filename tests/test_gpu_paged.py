@@ -408,6 +408,55 @@ def test_captured_calls_follow_their_positions(q4):
     q4.q4_device_check()
 
 
+def test_one_workspace_for_calls_of_several_shapes(q4):
+    # the counters of a wide batch lie where a narrow one has none
+    ws = None
+    for H, Hkv, D, positions in ((16, 1, 128, [5000]), (8, 2, 64, [700] * 40), (16, 1, 128, [4000, 100]), (4, 4, 64, [900])):
+        rng = np.random.default_rng(len(positions) + D)
+        pool = Pool(rng, [p + 1 for p in positions], Hkv, 64, D, torch.bfloat16)
+        for b, p in enumerate(positions):
+            pool.put(b, np.arange(p), *rng.standard_normal((2, p, Hkv, D)))
+        dev = pool.device(q4)
+        if ws is None:
+            ws = q4.q4_attn_paged_workspace(dev, H)
+        q, kn, vn = (T(rng.standard_normal((len(positions), h, D)).astype(np.float32)) for h in (H, Hkv, Hkv))
+        want = q4.q4_attn_paged(q, kn, vn, dev, I(positions))
+        assert torch.equal(q4.q4_attn_paged(q, kn, vn, dev, I(positions), workspace=ws), want)
+        assert int(ws[:1 << 18].view(torch.int32).abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_copy_waits_give_up_and_the_next_call_is_unchanged(q4, dtype):
+    rng = np.random.default_rng(65)
+    H, Hkv, D = 8, 2, 64
+    pool = Pool(rng, [300, 200], Hkv, 32, D, DTYPES[dtype])
+    for b, n in enumerate((300, 200)):
+        pool.put(b, np.arange(n), *rng.standard_normal((2, n, Hkv, D)))
+    dev = pool.device(q4)
+    q, kn, vn = (T(rng.standard_normal((2, h, D)).astype(np.float32)) for h in (H, Hkv, Hkv))
+    qp = T(rng.standard_normal((90, H, D)).astype(np.float32)).to(DTYPES[dtype])
+    ws = q4.q4_attn_paged_workspace(dev, H)
+
+    def calls():
+        return (q4.q4_attn_paged(q, kn, vn, dev, I([250, 100]), workspace=ws),
+                q4.q4_attn_prefill(qp, dev, I([0, 50, 90]), I([100, 30])))
+
+    want = calls()
+    q4.q4_device_check()
+    for which in range(2):
+        q4.q4_debug_wait_limits(copy_wait_cycles=200000, copy_extra_bytes=16)
+        try:
+            calls()[which]
+            with pytest.raises(q4.Q4Error) as e:
+                q4.q4_device_check()
+            assert e.value.status == 6
+        finally:
+            q4.q4_debug_wait_limits()
+        for a, b in zip(want, calls()):
+            assert torch.equal(a, b)
+        q4.q4_device_check()
+
+
 def test_two_streams_with_a_workspace_each(q4):
     rng = np.random.default_rng(62)
     H, Hkv, D = 8, 2, 128

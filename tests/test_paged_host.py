@@ -19,7 +19,8 @@ def pages(k=0x1000, v=0x2000, table=0x3000, dtype=1, num_pages=10, page=16, hkv=
 BAD_PAGES = [(dict(k=None), 1), (dict(v=0), 1), (dict(table=None), 1), (dict(k=0x1008), 3), (dict(table=0x3002), 3),
              (dict(dtype=3), 4), (dict(dtype=-1), 4), (dict(D=96), 4), (dict(num_pages=0), 2), (dict(page=0), 2),
              (dict(page=24), 2), (dict(page=(1 << 24) + 16), 2), (dict(hkv=0), 2), (dict(nseq=0), 2),
-             (dict(nseq=1025), 2), (dict(width=0), 2), (dict(page=1 << 24, width=65), 2)]
+             (dict(nseq=1025), 2), (dict(width=0), 2), (dict(page=1 << 24, width=65), 2),
+             (dict(nseq=1024, page=1 << 24, width=8), 2)]
 
 
 def _calls(c):
@@ -32,10 +33,10 @@ def _calls(c):
                                              o.get("cu", A), o.get("start", A), o.get("H", 4), o.get("cos", A),
                                              o.get("sin", A), o.get("rope_rows", 64), o.get("out", A), None),
         "prefill": lambda **o: L.q4_attn_prefill(r, o.get("q", A), o.get("rows", 5), o.get("cu", A),
-                                                 o.get("start", A), o.get("H", 4), o.get("window", 0), 0.125,
-                                                 o.get("out", A), o.get("ws", A), o.get("wsb", 1 << 40), None),
+                                                 o.get("start", A), o.get("H", 4), o.get("window", 0),
+                                                 o.get("scale", 0.125), o.get("out", A), o.get("ws", A), o.get("wsb", 1 << 40), None),
         "paged": lambda **o: L.q4_attn_paged(r, o.get("q", A), o.get("k", A), o.get("v", A), o.get("positions", A),
-                                             o.get("H", 4), o.get("window", 0), 0.125, o.get("cos", A),
+                                             o.get("H", 4), o.get("window", 0), o.get("scale", 0.125), o.get("cos", A),
                                              o.get("sin", A), o.get("rope_rows", 64), o.get("out", A),
                                              o.get("ws", A), o.get("wsb", 1 << 40), None),
     }
@@ -60,7 +61,8 @@ def test_no_pages(call):
     ("append", dict(cos=0x4004), 3), ("append", dict(rope_rows=0), 2),
     ("prefill", dict(rows=-1), 2), ("prefill", dict(q=None), 1), ("prefill", dict(out=0x4004), 3),
     ("prefill", dict(cu=None), 1), ("prefill", dict(start=0x4002), 3), ("prefill", dict(H=3), 2),
-    ("prefill", dict(H=34), 4), ("prefill", dict(window=-1), 2),
+    ("prefill", dict(H=34), 4), ("prefill", dict(window=-1), 2), ("prefill", dict(scale=-0.1), 2),
+    ("prefill", dict(scale=float("nan")), 2), ("paged", dict(scale=float("inf")), 2), ("paged", dict(scale=-1.0), 2),
     ("paged", dict(q=None), 1), ("paged", dict(k=0x4004), 3), ("paged", dict(v=None), 1),
     ("paged", dict(positions=None), 1), ("paged", dict(positions=0x4002), 3), ("paged", dict(H=1), 2),
     ("paged", dict(H=64), 4), ("paged", dict(window=-3), 2), ("paged", dict(out=None), 1),
@@ -83,6 +85,17 @@ def test_workspace_bytes():
     # sized by the heads, not by the cache's length
     big = pages(width=1000)
     assert L.q4_attn_paged_workspace_bytes(ctypes.byref(big), 4) == L.q4_attn_paged_workspace_bytes(ctypes.byref(c), 4)
+    # and its counters do not move with the geometry: calls of several shapes share one
+    assert L.q4_attn_paged_workspace_bytes(ctypes.byref(pages(nseq=9, hkv=1)), 2) == L.q4_attn_paged_workspace_bytes(ctypes.byref(c), 4)
+    assert L.q4_attn_paged_workspace_bytes(ctypes.byref(pages(nseq=1024, hkv=128)), 128) == 0  # too many pairs
+    assert _calls(pages(nseq=1024, hkv=128))["paged"](H=128) == 2
+    # the fp32 prompt attention: the parts of the cache and of q
+    f = pages(dtype=0, num_pages=10, page=16, hkv=2, D=64)
+    kv = 10 * 16 * 2 * 64
+    assert L.q4_attn_prefill_workspace_bytes(ctypes.byref(f), 5, 4) >= 2 * 2 * 2 * kv + 5 * 4 * (4 + 2 * 2 * 64)
+    assert L.q4_attn_prefill_workspace_bytes(ctypes.byref(f), 0, 4) == 0
+    assert L.q4_attn_prefill_workspace_bytes(ctypes.byref(c), 5, 4) == 0
+    assert _calls(f)["prefill"](ws=None) == 5 and _calls(f)["prefill"](wsb=100) == 5 and _calls(f)["prefill"](ws=0x4008) == 3
     for bad in (pages(D=32), pages(nseq=0)):
         assert L.q4_attn_paged_workspace_bytes(ctypes.byref(bad), 4) == 0
         assert L.q4_attn_prefill_workspace_bytes(ctypes.byref(bad), 10, 4) == 0
