@@ -568,6 +568,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             advance();
             issue();  // into the slot of the item read before this one
             uint32_t pw[MT][NT][2][QP];  // P as B fragments: positions 2t.. and 2t + 8.., head g
+            float alpha[NT][2];          // what the outputs so far are rescaled by
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float x[MT][4];
@@ -592,7 +593,6 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                         }
                     }
                 }
-                float alpha[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float mx = fmaxf(x[0][h], x[0][2 + h]);
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float mn = fmaxf(m[nt][h], mx);
                     const float mu = mn == -INFINITY ? 0.f : mn;  // nothing attended yet
-                    alpha[h] = ex2(m[nt][h] - mu);
+                    alpha[nt][h] = ex2(m[nt][h] - mu);
                     m[nt][h] = mn;
                     float sum = 0.f;
 #pragma unroll
@@ -611,13 +611,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                         x[mt][2 + h] = ex2(x[mt][2 + h] - mu + C::PEXP);
                         sum += x[mt][h] + x[mt][2 + h];
                     }
-                    l[nt][h] = fmaf(l[nt][h], alpha[h], sum);
-                }
-                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-                    for (int j = 0; j < KS; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[nt][j][e] *= alpha[e & 1];
+                    l[nt][h] = fmaf(l[nt][h], alpha[nt][h], sum);
                 }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
@@ -636,19 +630,28 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             const uint32_t vt = ring + slot * Item;
             // outputs: 16-bit, m tile j: dims 16 j + g and + 8; fp32, m tile 4 vb + j:
             // dims 64 vb + 8 g + j and + 4 (a lane's 32 bytes of a V row are rows of its own tiles)
+            // Each step's products are summed by themselves and added to the outputs
+            // in fp32: the tensor core's own accumulation truncates, and over a long
+            // context that bias would show (2e-6 after 1000 positions a warp).
             if constexpr (H16) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                for (int j = 0; j < KS; ++j) {
+                    float d[NT][4] = {};
 #pragma unroll
-                    for (int j = 0; j < KS; ++j) {
+                    for (int mt = 0; mt < MT; ++mt) {
                         uint32_t a[4];
                         // matrices: dims 0-7 and 8-15 of positions 0-7, then of 8-15
                         ldsm4t(a, vt + at_of(mt, (lane & 7) + 8 * (lane >> 4), 2 * j + ((lane >> 3) & 1)));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int x = QP - 1; x >= 0; --x) mma16816<M>(acc[nt][j], a, pw[mt][nt][0][x], pw[mt][nt][1][x]);
+                            for (int x = QP - 1; x >= 0; --x) mma16816<M>(d[nt], a, pw[mt][nt][0][x], pw[mt][nt][1][x]);
                     }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][j][e] = fmaf(acc[nt][j][e], alpha[nt][e & 1], d[nt][e]);
+                }
             } else {
 #pragma unroll
                 for (int vb = 0; vb < VB; ++vb)
@@ -671,13 +674,16 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                                 for (int y = 0; y < KP; ++y) a[y][e] = w[y];
                             }
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float d[4] = {};
 #pragma unroll
-                                for (int x = QP - 1; x >= 0; --x)
+                                for (int s = QP - 1; s >= 0; --s)  // the smallest products first
 #pragma unroll
-                                    for (int y = KP - 1; y >= 0; --y)
-                                        if (x + y < QP)
-                                            mma16816<M>(acc[nt][4 * vb + j], a[y], pw[mt][nt][0][x], pw[mt][nt][1][x]);
+                                    for (int x = 0; x <= s; ++x) mma16816<M>(d, a[s - x], pw[mt][nt][0][x], pw[mt][nt][1][x]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc[nt][4 * vb + j][e] = fmaf(acc[nt][4 * vb + j][e], mt == 0 ? alpha[nt][e & 1] : 1.f, d[e]);
+                            }
                         }
                     }
             }

@@ -42,6 +42,10 @@ constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit val
 constexpr int kPfSoft = 16;                 // softmax warps: row tiles x column halves x 4 row quarters
 constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // two MMA warps, the copy warp
 constexpr int kPfThreads = 32 * (kPfSoft + 3);
+// fp32: the tensor core's accumulation truncates, which over a long chain of
+// products shows (3e-6 of the output after 2048 positions); every kPfFlush key
+// tiles O is added to a sum beside it, and starts again
+constexpr int kPfFlush = 2;
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
 // What enters the products of a cache type: 16-bit values as they are (one
@@ -75,11 +79,11 @@ struct PfCfg {
     // tensor memory columns: S of tile i from KT i, O of tile i from ColO + D i; P
     // lies over its S (two parts: each column half's over its own, 16 columns of hi
     // and 16 of lo per 32 positions)
-    static constexpr int ColO = NT * KT;
+    static constexpr int ColO = NT * KT, ColSum = ColO + NT * D;
     static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][half][row]
     static constexpr int Smem = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
-    static_assert(ColO + NT * D <= 512, "tensor memory");
+    static_assert(ColO + NT * D * Parts <= 512, "tensor memory");
     static_assert(4 * HF * NT <= kPfSoft, "softmax warps");
     static_assert(16 * NS + 32 * NT + 88 <= 448, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
@@ -342,17 +346,17 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 const uint32_t ts = taddr + (uint32_t)(KT * i);
                 const uint64_t qd = q0 + (uint64_t)((i * Cf::QTile) >> 4);
 #pragma unroll
-                for (int y = 0; y < NP; ++y) {
+                for (int y = NP - 1; y >= 0; --y) {  // the small products first
                     const int sk = st + y < NS ? st + y : st + y - NS;
                     const uint64_t kd = k0 + (uint64_t)((sk * Cf::Tile) >> 4);
 #pragma unroll
-                    for (int x = 0; x < NP - y; ++x)  // Q's part x by K's part y
+                    for (int x = NP - 1 - y; x >= 0; --x)  // Q's part x by K's part y
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
                             tc::mma_f16(ts, qd + (uint64_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
                                         kd + (uint64_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
-                                        (x | y | ks) != 0);
-                    if (y == NP - 1) tc::commit(b_s + 8 * i);
+                                        !(y == NP - 1 && x == 0 && ks == 0));
+                    if (y == 0) tc::commit(b_s + 8 * i);
                     if (i == last) release(sk);
                 }
             }
@@ -382,17 +386,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     tc::fence_after_sync();
                     if (leader) {  // O_i += P_i V
                         const uint32_t to = taddr + (uint32_t)(Cf::ColO + D * i), tp = taddr + (uint32_t)(KT * i);
+                        const bool fresh = NP == 2 ? j % kPfFlush == 0 : j == 0;
 #pragma unroll
-                        for (int y = 0; y < NP; ++y) {
+                        for (int y = NP - 1; y >= 0; --y) {
                             const int at = sv + y < NS ? sv + y : sv + y - NS;
                             const uint64_t vd = v0 + (uint64_t)((at * Cf::Tile) >> 4);
 #pragma unroll
-                            for (int x = 0; x < NP - y; ++x)  // P's part x by V's part y
+                            for (int x = NP - 1 - y; x >= 0; --x)  // P's part x by V's part y
 #pragma unroll
                                 for (int ks = 0; ks < KT / 16; ++ks)
                                     tc::mma_f16_ta(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint64_t)((ks * 2048) >> 4),
-                                                   id_o, (j | x | y | ks) != 0);
-                            if (y == NP - 1 && j + 1 == nk) tc::commit(b_o + 8 * i);
+                                                   id_o, !(fresh && y == NP - 1 && x == 0 && ks == 0));
+                            if (y == 0 && j + 1 == nk) tc::commit(b_o + 8 * i);
                             if (i == last) release(at);
                         }
                     }
@@ -419,6 +424,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
             const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
+            const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of flushed O
+            constexpr int QO = D / (16 * HF), QS = NP * QO;             // 16-column parts of O, and with the sum
             const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
             float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
             float c = p.scale * 1.4426950408889634f, vback = 1.f;
@@ -442,6 +449,24 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait(b_s + 8 * i, (uint32_t)j & 1u, lim));
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
+                const bool flush = NP == 2 && j > 0 && j % kPfFlush == 0;
+                if (flush) {  // S came after the product before it: O is complete
+#pragma unroll 1
+                    for (int q = 0; q < D / (16 * HF); ++q) {
+                        uint32_t o[16], a[16];
+                        const uint32_t at = (D / HF) * hf + 16 * q;
+                        tc::ld16(to + at, o);
+                        if (j > kPfFlush) {
+                            tc::ld16(tsum + at, a);
+                            tc::wait_ld16(a);
+                        }
+                        tc::wait_ld16(o);
+                        if (j > kPfFlush)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+                        tc::st16(tsum + at, o);
+                    }
+                }
                 uint32_t s[64];
                 tc::ld32(ts + 64 * hf, s);
                 tc::ld32(ts + 64 * hf + 32, s + 32);
@@ -472,15 +497,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 } else {
                     const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
                     if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
-                        // (S came after the product before it: O is complete)
                         const float mn = fmaxf(m, top);
                         const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                         l *= alpha;
                         m = mn;
 #pragma unroll 1
-                        for (int q = 0; q < D / (16 * HF); ++q) {
+                        for (int q = flush ? QO : 0; q < (j >= kPfFlush ? QS : QO); ++q) {  // O (if it holds any), then its sum
                             uint32_t o[16];
-                            const uint32_t at = to + (D / HF) * hf + 16 * q;
+                            const uint32_t at = (q < QO ? to + 16 * q : tsum + 16 * (q - QO)) + (D / HF) * hf;
                             tc::ld16(at, o);
                             tc::wait_ld16(o);
 #pragma unroll
@@ -534,6 +558,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     uint32_t o[32];
                     tc::ld32(to + (D / HF) * hf + 32 * q, o);
                     tc::wait_ld32(o);
+                    if (NP == 2 && nk > kPfFlush) {
+                        uint32_t a[32];
+                        tc::ld32(tsum + (D / HF) * hf + 32 * q, a);
+                        tc::wait_ld32(a);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+                    }
                     uint4 w[sizeof(T) * 2];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
