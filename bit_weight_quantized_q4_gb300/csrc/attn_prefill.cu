@@ -313,9 +313,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int last = w + 2 < nt ? w + 2 : w;  // this warp's last tile
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, KT, BF, false), id_o = tc::idesc_16(128, D, BF, true);
-        const uint64_t q0 = tc::smem_desc_sw128(sb + Cf::OffQ, 16, 1024);
-        const uint64_t k0 = tc::smem_desc_sw128(sb + Cf::OffRing, 16, 1024);
-        const uint64_t v0 = tc::smem_desc_sw128(sb + Cf::OffRing, Cf::KBlk, 1024);
+        const uint32_t q0 = tc::desc_sw128(sb + Cf::OffQ, 16), k0 = tc::desc_sw128(sb + Cf::OffRing, 16);
+        const uint32_t v0 = tc::desc_sw128(sb + Cf::OffRing, Cf::KBlk);
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)); };
         // both warps free a ring stage after their last tile; a warp alone does it twice
         auto release = [&](int st) {
@@ -344,18 +343,18 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         auto scores = [&](int i, int st) {
             if (leader) {
                 const uint32_t ts = taddr + (uint32_t)(KT * i);
-                const uint64_t qd = q0 + (uint64_t)((i * Cf::QTile) >> 4);
+                const uint32_t qd = q0 + (uint32_t)((i * Cf::QTile) >> 4);
 #pragma unroll
                 for (int y = NP - 1; y >= 0; --y) {  // the small products first
                     const int sk = st + y < NS ? st + y : st + y - NS;
-                    const uint64_t kd = k0 + (uint64_t)((sk * Cf::Tile) >> 4);
+                    const uint32_t kd = k0 + (uint32_t)((sk * Cf::Tile) >> 4);
 #pragma unroll
                     for (int x = NP - 1 - y; x >= 0; --x)  // Q's part x by K's part y
 #pragma unroll
                         for (int ks = 0; ks < D / 16; ++ks)
-                            tc::mma_f16(ts, qd + (uint64_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
-                                        kd + (uint64_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
-                                        !(y == NP - 1 && x == 0 && ks == 0));
+                            tc::mma_sw128(ts, qd + (uint32_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
+                                          kd + (uint32_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
+                                          !(y == NP - 1 && x == 0 && ks == 0));
                     if (y == 0) tc::commit(b_s + 8 * i);
                     if (i == last) release(sk);
                 }
@@ -390,13 +389,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
                         for (int y = NP - 1; y >= 0; --y) {
                             const int at = sv + y < NS ? sv + y : sv + y - NS;
-                            const uint64_t vd = v0 + (uint64_t)((at * Cf::Tile) >> 4);
+                            const uint32_t vd = v0 + (uint32_t)((at * Cf::Tile) >> 4);
 #pragma unroll
                             for (int x = NP - 1 - y; x >= 0; --x)  // P's part x by V's part y
 #pragma unroll
                                 for (int ks = 0; ks < KT / 16; ++ks)
-                                    tc::mma_f16_ta(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint64_t)((ks * 2048) >> 4),
-                                                   id_o, !(fresh && y == NP - 1 && x == 0 && ks == 0));
+                                    tc::mma_ta_sw128(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint32_t)((ks * 2048) >> 4),
+                                                     id_o, !(fresh && y == NP - 1 && x == 0 && ks == 0));
                             if (y == 0 && j + 1 == nk) tc::commit(b_o + 8 * i);
                             if (i == last) release(at);
                         }
@@ -554,21 +553,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / HF) * hf;
                 float worst = 0.f;  // NaN or infinite where a value is
 #pragma unroll
-                for (int q = 0; q < D / (32 * HF); ++q) {
-                    uint32_t o[32];
-                    tc::ld32(to + (D / HF) * hf + 32 * q, o);
-                    tc::wait_ld32(o);
+                for (int q = 0; q < QO; ++q) {
+                    uint32_t o[16];
+                    tc::ld16(to + (D / HF) * hf + 16 * q, o);
+                    tc::wait_ld16(o);
                     if (NP == 2 && nk > kPfFlush) {
-                        uint32_t a[32];
-                        tc::ld32(tsum + (D / HF) * hf + 32 * q, a);
-                        tc::wait_ld32(a);
+                        uint32_t a[16];
+                        tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
+                        tc::wait_ld16(a);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
                     }
-                    uint4 w[sizeof(T) * 2];
+                    uint4 w[sizeof(T)];
                     uint32_t *ww = reinterpret_cast<uint32_t *>(w);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
                         worst = fmaf(a, 0.f, fmaf(b, 0.f, worst));
                         if constexpr (sizeof(T) == 4) {
@@ -580,8 +579,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     }
                     if (live)
 #pragma unroll
-                        for (int e = 0; e < (int)sizeof(T) * 2; ++e)
-                            *(reinterpret_cast<uint4 *>(dst + 32 * q) + e) = w[e];
+                        for (int e = 0; e < (int)sizeof(T); ++e) *(reinterpret_cast<uint4 *>(dst + 16 * q) + e) = w[e];
                 }
                 // rows that are not finite: by the definition (whole rows, after
                 // both halves have stored theirs); Q's tile is free by now

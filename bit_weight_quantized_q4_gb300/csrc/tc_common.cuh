@@ -63,25 +63,35 @@ __device__ __forceinline__ void commit(uint32_t bar) {
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]: the A operand's rows are TMEM lanes, 16-bit
-// values two to a 32-bit column.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t acc) {
+// Shared-memory descriptors of operands in the 128-byte swizzle (layout type 2
+// in bits 61-63): 8-row groups of 128-byte rows, as a tensor-map copy with
+// CU_TENSOR_MAP_SWIZZLE_128B writes them, 1024 bytes apart (the stride offset).
+// The upper word is the same for all; the lower one holds the address and the
+// leading offset.  K-major: the rows are M (or N), `lbo` is unused, and a step of
+// 16 along K advances the address by 32 bytes.  MN-major: the rows are K, `lbo`
+// is the distance of consecutive 64-value blocks along MN.
+constexpr uint32_t kSw128Hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_sw128(uint32_t saddr, uint32_t lbo) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+// D[tmem] (+)= A[smem] * B[smem]^T with such descriptors (their lower words).
+__device__ __forceinline__ void mma_sw128(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kSw128Hi)
         : "memory");
 }
-// Shared-memory descriptor of an operand in the 128-byte swizzle (layout type
-// 2 in bits 61-63): 8-row groups of 128-byte rows, as a tensor-map copy with
-// CU_TENSOR_MAP_SWIZZLE_128B writes them.  K-major: the rows are M (or N) and
-// `sbo` is the distance of consecutive 8-row groups (`lbo` unused); a step of
-// 16 along K advances the address by 32 bytes.  MN-major: the rows are K, `sbo`
-// the distance of consecutive 8-row groups along K, `lbo` that of consecutive
-// 64-value blocks along MN.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return smem_desc(saddr, lbo, sbo) | (2ull << 61);
+// D[tmem] (+)= A[tmem] * B[smem]: the A operand's rows are TMEM lanes, 16-bit
+// values two to a 32-bit column.
+__device__ __forceinline__ void mma_ta_sw128(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc,
+                                             uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(acc), "n"(kSw128Hi)
+        : "memory");
 }
 // kind::f16 with either 16-bit type (bits 7-9, 10-12: 0 f16, 1 bf16) and
 // optionally an MN-major B (bit 16).
