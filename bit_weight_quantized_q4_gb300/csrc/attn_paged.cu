@@ -208,9 +208,26 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         return (pos - lo) / Cfg::Unit + 1;
     };
     // prefix[b] = units of a kv head of the sequences before b (the host bounds
-    // the sum to 31 bits), a sequence a thread
+    // the sum over all heads to 31 bits).  Up to 32 sequences: every warp scans
+    // them for itself and writes the same words, no barrier; else a thread each.
     int Wh = 0;
-    for (int b0 = 0; b0 < nseq; b0 += kPagedThreads) {
+    if (nseq <= 32) {
+        const int pos = lane < nseq ? p.positions[lane] : -1, n = units_of(pos);
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        Wh = __shfl_sync(0xffffffffu, inc, 31);
+        if (lane < nseq) {
+            prefix[lane] = inc - n;
+            pos_s[lane] = pos;
+        }
+        if (lane == 0) prefix[nseq] = Wh;
+        __syncwarp();
+    }
+    for (int b0 = 0; nseq > 32 && b0 < nseq; b0 += kPagedThreads) {
         const int b = b0 + tid;
         const int pos = b < nseq ? p.positions[b] : -1;
         int inc = units_of(pos);
@@ -234,9 +251,11 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             pos_s[b] = pos;
         }
     }
-    if (tid == 0) prefix[nseq] = Wh;
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's room is the rings'
-    __syncthreads();
+    if (nseq > 32) {
+        if (tid == 0) prefix[nseq] = Wh;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's room is the rings'
+        __syncthreads();
+    }
     // idle rows: zeros
     for (int b = blockIdx.x; b < nseq; b += gridDim.x)
         if (prefix[b + 1] == prefix[b]) {
@@ -245,16 +264,26 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         }
     // CTAs with work: never more than units, so that none of a pair's CTAs is
     // without a share (each adds to the pair's count)
-    const long long W = (long long)Wh * hkv;
-    const int N = W < gridDim.x ? (int)W : (int)gridDim.x, cta = blockIdx.x;
+    const int W = Wh * hkv, N = min(W, (int)gridDim.x), cta = blockIdx.x;
     if (cta >= N) return;
-    const long long u0 = W * cta / N, u1 = W * (cta + 1) / N;
+    // CTA c's units start at floor(W c / N), the larger shares spread over the
+    // CTAs (all in front, the SMs that get two of them end last: 34 -> 38 us for
+    // one context of 32768)
+    const int each = W / N, more = W - each * N;
+    auto start_of = [&](int c) { return each * c + more * c / N; };
+    auto cta_of = [&](int u) {  // the CTA of unit u: an estimate, then the exact one
+        int c = min(N - 1, (int)((float)u * ((float)N / (float)W)));
+        while (start_of(c) > u) --c;
+        while (start_of(c + 1) <= u) ++c;
+        return c;
+    };
+    const int u0 = start_of(cta), u1 = start_of(cta + 1);
     int b = 0;
     {  // the last b with prefix[b] <= u0 that has units
         int hi = nseq;
         while (hi - b > 1) {
             const int mid = (b + hi) >> 1;
-            if ((long long)prefix[mid] * hkv <= u0)
+            if (prefix[mid] * hkv <= u0)
                 b = mid;
             else
                 hi = mid;
@@ -271,15 +300,14 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
     const uint64_t pol = evict_first_policy();
     uint32_t extra = p.extra_tx;     // testing the give-up path only
 
-    for (long long u = u0; u < u1;) {
-        while ((long long)prefix[b + 1] * hkv <= u) ++b;
+    for (int u = u0; u < u1;) {
+        while (prefix[b + 1] * hkv <= u) ++b;
         const int pos = pos_s[b], lo = lo_of(pos), base16 = lo & ~15;
         const int cs = units_of(pos);
-        const long long sb = (long long)prefix[b] * hkv, rem = u - sb;
-        const int hk = (int)(rem / cs), st = (int)(rem - (long long)hk * cs);
-        const long long s0 = sb + (long long)hk * cs, s1 = s0 + cs;  // the pair's units
-        const long long ue = s1 < u1 ? s1 : u1;
-        const int n_units = (int)(ue - u);
+        const int sb = prefix[b] * hkv, hk = (u - sb) / cs, st = u - sb - hk * cs;
+        const int s0 = sb + hk * cs, s1 = s0 + cs;  // the pair's units
+        const int ue = min(s1, u1);
+        const int n_units = ue - u;
         const bool owner = ue == s1;  // this segment ends with the new token
 
         // Q's heads (warp, warp + NW, ..; lane j < D / 8 holds dims 4 j .. and D / 2 +
@@ -762,8 +790,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
         }
         if (!whole) {
             // the last of the pair's CTAs to finish folds their shares in CTA order
-            const long long c0 = ((s0 + 1) * N - 1) / W, c1 = (s1 * N - 1) / W;  // first and last CTA
-            const int nc = (int)(c1 - c0) + 1;
+            const int c0 = cta_of(s0), nc = cta_of(s1 - 1) - c0 + 1;  // first CTA, CTAs
             __syncthreads();
             if (tid == 0) {
                 __threadfence();  // the CTA's share (the barrier orders it before), then the count
@@ -774,7 +801,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             if (*flag) {
                 // CTA c0 + i's slot: its first segment, except a first CTA whose
                 // range starts before the pair
-                const float *part0 = p.part + ((size_t)c0 * 2 + (W * c0 / N != s0 ? 1 : 0)) * slot_floats;
+                const float *part0 = p.part + ((size_t)c0 * 2 + (start_of(c0) != s0 ? 1 : 0)) * slot_floats;
                 const float *part1 = p.part + (size_t)c0 * 2 * slot_floats;
                 auto slot_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * slot_floats; };
                 // weights 2^(m_i - M) and the sum, a warp a head

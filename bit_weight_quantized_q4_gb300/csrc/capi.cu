@@ -910,7 +910,7 @@ q4_status check_pages_shape(const q4_kv_pages *c) {
         return Q4_ERR_SHAPE;
     if (c->page_size % 16 != 0 && c->width != 1) return Q4_ERR_SHAPE;
     if ((long long)c->width * c->page_size > (1ll << 30) ||
-        (long long)c->nseq * c->width * c->page_size > (1ll << 36))
+        (long long)c->nseq * c->width * c->page_size > (1ll << 36) / c->kv_heads)
         return Q4_ERR_SHAPE;
     return Q4_OK;
 }

@@ -452,8 +452,8 @@ q4_status q4_rope_table(int32_t max_seq, int32_t D, double rope_theta, float *ho
  * page_size; table: [nseq][width] device int32.  A contiguous cache
  * [kv_heads][max_seq][head_dim] is one page of max_seq positions (width 1).
  * Limits: head_dim 64 or 128; page_size a multiple of 16 up to 2^24, or any
- * size up to 2^24 with width 1; width * page_size <= 2^30 and nseq times that
- * <= 2^36; 1 <= nseq <= 1024; kv_heads <= 1024.
+ * size up to 2^24 with width 1; width * page_size <= 2^30 and nseq *
+ * kv_heads times that <= 2^36; 1 <= nseq <= 1024; kv_heads <= 1024.
  * The int32 arrays of these calls (table, cu_rows, start, positions, tokens)
  * are device memory with 4-byte alignment; everything else is 16-byte aligned.
  * They are read by the kernels, so a captured launch follows their values.  A
