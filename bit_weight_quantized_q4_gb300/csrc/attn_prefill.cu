@@ -20,7 +20,10 @@
 // An MMA of 128 rows takes about 60 cycles per K = 16 at N = 64 as at N = 128
 // (measured by its issue), so at head size 64 the product runs at half the
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
-// positions, P beside S and S a key tile ahead, and 277 with four of 64.
+// positions, P beside S and S a key tile ahead, and 277 with four of 64 (272 now:
+// 1010 TFLOP/s, 83 % of what the half rate leaves).  At head size 128 the tensor
+// core is busy 64 % of the time (115 us for ten ragged prompts, 93 GFLOP): two row
+// tiles fill the tensor memory, and the softmax of one does not cover the other's.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
 // (the sums stay exact: the reference maximum is the row's own, and its factor
 // cancels).
@@ -56,6 +59,12 @@ struct PfT {
     using M = T;
     static constexpr int Parts = 1;
     static constexpr float PExp = 0.f;
+};
+template <>
+struct PfT<__half> {
+    using M = __half;
+    static constexpr int Parts = 1;
+    static constexpr float PExp = 6.f;  // weights reach 2^(6 + kPfGrow), and stay normal down to 2^-20 of the largest
 };
 template <>
 struct PfT<float> {
@@ -637,9 +646,14 @@ __device__ __forceinline__ int pf_exp(uint32_t bits) {
 
 __device__ __forceinline__ float pf_back(uint32_t bits) { return ldexpf(1.f, -pf_exp(bits)); }
 
+// A scaled value: finite ones stay finite (beyond f16's range only at positions
+// nothing attends, where a weight of 0 meets them)
+__device__ __forceinline__ float pf_scaled(float x, float f) {
+    return fabsf(x) < INFINITY ? fminf(fmaxf(x * f, -65504.f), 65504.f) : x;
+}
 // hi and lo parts of four scaled values
 __device__ __forceinline__ void pf_split4(float4 v, float f, uint2 &hi, uint2 &lo) {
-    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    v = make_float4(pf_scaled(v.x, f), pf_scaled(v.y, f), pf_scaled(v.z, f), pf_scaled(v.w, f));
     hi = make_uint2(pack2<__half>(v.x, v.y), pack2<__half>(v.z, v.w));
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&hi.x));
     const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi.y));
@@ -651,8 +665,9 @@ __device__ __forceinline__ float finite_abs(float x) {
 }
 
 // fn(sequence, kv head, first position, end) for this CTA's items: the chunks
-// of every sequence's attended positions (from a key tile's start: a multiple of 64) by kv heads.
-template <class F>
+// of every sequence's attended positions (rounded down to a multiple of `Align`)
+// by kv heads.
+template <int Align, class F>
 __device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
     __shared__ long long prefix[kMaxSeqs + 1];
     __shared__ long long wsum[8];
@@ -663,7 +678,7 @@ __device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
         lo = end = 0;
         if (rows == 0 || first < 0 || first >= (long long)p.kv.width * p.kv.page) return;
         end = (int)min((long long)first + rows, (long long)p.kv.width * p.kv.page);
-        lo = (p.window > 0 && first + 1 > p.window ? first + 1 - p.window : 0) & ~127;
+        lo = (p.window > 0 && first + 1 > p.window ? first + 1 - p.window : 0) & ~(Align - 1);
     };
     long long n[4], own = 0;
 #pragma unroll
@@ -716,7 +731,7 @@ __global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int L = D / 4;  // lanes of a row
     const int tid = threadIdx.x, lane = tid & 31, j = 4 * (tid % L);
-    pf_items(p, [&](int b, int hk, int at, int end) {
+    pf_items<1>(p, [&](int b, int hk, int at, int end) {
         float mk = 0.f, mv = 0.f;
 #pragma unroll 4
         for (int pos = at + tid / L; pos < end; pos += 256 / L) {
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(256) q4attn_prefill_split_kernel(const __grid_
     constexpr int L = D / 4;
     const int tid = threadIdx.x, j = 4 * (tid % L);
     const size_t part = (size_t)p.kv.num_pages * p.kv.hkv * p.kv.page * D;
-    pf_items(p, [&](int b, int hk, int at, int end) {
+    pf_items<128>(p, [&](int b, int hk, int at, int end) {  // from a key tile's start
         const float fk = ldexpf(1.f, pf_exp(p.maxima[hk])), fv = ldexpf(1.f, pf_exp(p.maxima[p.kv.hkv + hk]));
 #pragma unroll 4
         for (int pos = at + tid / L; pos < end; pos += 256 / L) {

@@ -294,6 +294,58 @@ def test_prefill_scales(q4, dtype, qmul):
     _prefill_case(q4, DTYPES[dtype], 4, 2, 64, 64, [290], [0], 0, 45, qmul=qmul)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_stale_values_below_the_window_change_nothing(q4, dtype, D):
+    # finite but huge values at positions before every row's window, some of them
+    # in the window's own key tile: not a bit of the result may follow them
+    rng = np.random.default_rng(case_seed("stale", dtype, D))
+    t = DTYPES[dtype]
+    start, rows, window, page = 200, 50, 40, 32
+    lo, n = start + 1 - window, start + rows
+    outs = []
+    q = torch.from_numpy(rng.standard_normal((rows, 4, D)).astype(np.float32)).to(t).cuda()
+    kv = torch.from_numpy(rng.standard_normal((2, 8, 2, page, D)).astype(np.float32)).to(t)
+    table = I([list(range(8))])
+    for big in (None, 3e4):
+        k, v = kv[0].cuda(), kv[1].cuda()
+        if big is not None:
+            for x in (k, v):
+                flat = x.transpose(1, 2).reshape(8 * page, 2, D).clone()
+                flat[:lo] = -big if t == torch.float16 else -big * 1e25
+                x.copy_(flat.reshape(8, page, 2, D).transpose(1, 2))
+        pages = q4.KVPages(k, v, table)
+        outs.append(q4.q4_attn_prefill(q, pages, I([0, rows]), I([start]), window=window))
+    q4.q4_device_check()
+    assert n <= 8 * page and torch.isfinite(outs[0]).all()
+    assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_prefill_many_small_weights(q4, dtype):
+    # one position of weight 1 whose value is zero, 4095 of weight w = 0.7 * 2^-22:
+    # f16 and fp32 weights are held to 2^-31 of the largest, bf16 ones to half a
+    # step; the output is rounded once; (n / 4 + 64) 2^-24 for the sums, 1e-5 for
+    # the scores' fp32 (ln w = -15.6 times 2^-24, twice) and the exponential
+    t, D, n, w = DTYPES[dtype], 64, 4096, 0.7 * 2.0 ** -22
+    k, v = torch.zeros(1, 1, n, D), torch.ones(1, 1, n, D)
+    k[0, 0, 0, 0] = 16.0
+    v[0, 0, 0] = 0.0
+    q = torch.zeros(1, 1, D)
+    q[0, 0, 0] = 1.0
+    pages = q4.KVPages(k.to(t).cuda(), v.to(t).cuda(), I([[0]]))
+    out = f64(q4.q4_attn_prefill(q.to(t).cuda(), pages, I([0, 1]), I([n - 1]), scale=float(-np.log(w) / 16)))
+    ref = w * (n - 1) / (1 + w * (n - 1))
+    tol = 1e-5 + (n / 4 + 64) * U32 + (2 * half_step(t) if t == torch.bfloat16 else 2.0 ** -31 / w + half_step(t))
+    assert (np.abs(out - ref) <= tol * ref).all(), (out.min(), out.max(), ref)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_prefill_scale_zero_is_the_mean(q4, dtype):
+    # every weight is equal, whatever the scores
+    _prefill_case(q4, DTYPES[dtype], 4, 2, 64, 32, [150], [20], 0, 51, scale=0.0)
+
+
 def test_prefill_contiguous_cache_as_one_page(q4):
     _prefill_case(q4, torch.float32, 8, 2, 64, 333, [300], [33], 0, 46)
     _prefill_case(q4, torch.float16, 8, 2, 64, 201, [200], [1], 0, 47)
