@@ -6,24 +6,28 @@
 //
 // The work is HBM-bound on the cache rows, whatever the cache's type: a kv
 // head's G query heads share each row, so the arithmetic runs on the tensor
-// cores (mma.sync m16n8k16: the batch of 8 columns is the group's heads) and
-// costs a fraction of the row's load time.  A warp takes 16 positions per
-// step, entirely in registers:
-//   S^T [16 positions][heads] = K Q^T   A = K rows as loaded (16 bytes of a row
-//        per lane; the k order inside a 32-dim block is permuted, and Q's
-//        fragments carry the same permutation),
-//   O^T [dims][heads] += V^T P^T        A = V rows, pairs of positions packed,
-//        rows of the m tiles permuted so that a lane's 16 bytes of a V row are
-//        rows of its own tiles; P goes through movmatrix.
-// Nothing goes through shared memory but Q's fragments and the final merge.
+// cores (mma.sync m16n8k16: the 8 columns are the group's heads; a wider
+// instruction would leave most of its rows empty) and costs a fraction of the
+// row's load time.  Each of a CTA's four warps brings its own tiles of 16
+// positions by TMA into a ring of its own and waits for nobody else:
+//   S^T [16 positions][heads] = K Q^T   A = K rows (16-bit: ldmatrix of swizzled
+//        rows; fp32: 16 bytes of a row per lane, the k order inside a 32-dim
+//        block permuted, and Q's fragments with it),
+//   O^T [dims][heads] += V^T P^T        A = V rows (16-bit: transposing ldmatrix;
+//        fp32: pairs of positions packed, rows of the m tiles permuted so that a
+//        lane's 32 bytes of a V row are rows of its own tiles); P goes through
+//        movmatrix.
+// 64 ragged bf16 contexts up to 8191 (1.03 GB): 178 us, 5.8 TB/s; one of 32768
+// (134 MB): 34.6 us, of which the loop runs at the memory's rate and about 6 us
+// are the scan, Q, the warps' merge and the joining of the CTAs' shares.
 //
 // Precision: q and p stay fp32-like.  f16 caches: q (scaled per head by a
 // power of two) and p enter as two f16 parts (22 bits); bf16 caches: as three
 // bf16 parts (24 bits); f32 caches: K and V as three bf16 parts too, with the
 // six products of order >= 2^-16.  The cache's values themselves are exact.
 //
-// Split: the 128-position units of all (sequence, kv head) pairs form one
-// line that the CTAs divide evenly, whatever the lengths; lengths are read on
+// Split: the units (64 or 128 positions) of all (sequence, kv head) pairs form
+// one line that the CTAs (two an SM) divide evenly, whatever the lengths; lengths are read on
 // the device, so a captured launch follows them.  A pair cut by a boundary is
 // joined by the last of its CTAs to finish, in CTA order: the result does not
 // depend on scheduling.
@@ -141,11 +145,10 @@ struct PagedCfg {
     static_assert(NI >= 3, "two items in flight while one is read");
 };
 
-// Shared memory of a CTA: the prefix of units over the sequences (per kv
-// head) and their positions, Q's
-// fragments (more than 8 heads: else they live in registers after their
-// preparation) and factors, the warps' maxima and sums, the fold's sums, a
-// flag, then the rings; over them, when a segment's loop is done, the warps'
+// Shared memory of a CTA: the prefix of units over the sequences (per kv head)
+// and their positions, Q's fragments (more than 8 heads: else they live in
+// registers after their preparation) and factors, the warps' maxima and sums,
+// the fold's sums, a flag, then the rings; over them, when a segment's loop is done, the warps'
 // outputs [warps][G][D] and the fold's weights.
 template <typename T, int D, int NT>
 struct PagedSmem {

@@ -6,26 +6,6 @@
 namespace q4 {
 namespace dev {
 
-// The sequence of packed row `row` and its position; false for a row behind
-// the last sequence, or one whose position the table does not have.  Called
-// by whole warps.
-__device__ __forceinline__ bool locate_row(const PrefillParams &p, int row, int lane, int &seq, int &pos) {
-    seq = 0;
-    for (int b0 = 0; b0 < p.kv.nseq; b0 += 32) {
-        const int b = b0 + lane;
-        seq += __popc(__ballot_sync(0xffffffffu, b < p.kv.nseq && p.cu[b + 1] <= row));
-    }
-    if (seq >= p.kv.nseq) return false;
-    const int begin = p.cu[seq], first = p.start ? p.start[seq] : 0;
-    const long long at = (long long)first + row - begin;
-    if (begin < 0 || begin > row || first < 0 || at >= (long long)p.kv.width * p.kv.page) {
-        if (lane == 0) atomicExch(p.err, kErrPaged);
-        return false;
-    }
-    pos = (int)at;
-    return true;
-}
-
 // out = sum_j p_j v_j over j in (pos - window, pos], p = softmax of scale q . k_j;
 // lane l holds dims l, l + 32, ...; positions on pages out of range are skipped.
 template <typename T, int D>

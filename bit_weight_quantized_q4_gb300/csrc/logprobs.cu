@@ -44,8 +44,6 @@ __device__ __forceinline__ unsigned long long lp_pair(uint32_t key, int i) {
     return ((unsigned long long)key << 32) | (0xFFFFFFFFu - (uint32_t)i);
 }
 
-__device__ __forceinline__ float lp_at(const float4 &v, int e) { return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w; }
-
 struct LpSums {
     float m, s, t;
 };
@@ -107,8 +105,7 @@ __device__ __forceinline__ void lp_add2(uint64_t &s, uint64_t &t, float v0, floa
 
 // The first n of v's values (at index i ..) whose key reaches the bound become
 // candidates.  Not inlined: few values get here, and the kernel's own code,
-// which a row runs through once, stays short (inlined it took 11.7 us for one
-// row of 65536 against 7.5).
+// which a row runs through once, stays short.
 __device__ __noinline__ void lp_take(LpShared &sh, float4 v, int i, int n, uint32_t bound) {
     for (int e = 0; e < n; ++e) {
         const uint32_t key = lp_key(v.x);
