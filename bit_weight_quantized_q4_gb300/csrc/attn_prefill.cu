@@ -44,7 +44,9 @@ namespace dev {
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values (a block of a Q tile)
 constexpr int kPfSoft = 16;                 // softmax warps: row tiles x column halves x 4 row quarters
 constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // two MMA warps, the copy warp
-constexpr int kPfThreads = 32 * (kPfSoft + 3);
+constexpr int kPfRows = kPfSoft + 3;        // the warp of the rows taken by the definition
+constexpr int kPfThreads = 32 * (kPfSoft + 4);
+constexpr int kPfItems = 4;                 // work items of a CTA that are known and not done
 // fp32: the tensor core's accumulation truncates, which over a long chain of
 // products shows (3e-6 of the output after 2048 positions); every kPfFlush key
 // tiles O is added to a sum beside it, and starts again
@@ -89,12 +91,12 @@ struct PfCfg {
     // lies over its S (two parts: each column half's over its own, 16 columns of hi
     // and 16 of lo per 32 positions)
     static constexpr int ColO = NT * KT, ColSum = ColO + NT * D;
-    static constexpr int OffX = OffBar + 512;          // values the column halves exchange [tile][half][row]
+    static constexpr int OffX = OffBar + 608 + (20 + 4 * kPfSoft) * kPfItems;          // values the column halves exchange [tile][half][row]
     static constexpr int Smem = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
     static_assert(ColO + NT * D * Parts <= 512, "tensor memory");
     static_assert(4 * HF * NT <= kPfSoft, "softmax warps");
-    static_assert(16 * NS + 32 * NT + 88 <= 448, "barriers before the tensor-memory address");
+    static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 <= 576, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
     static constexpr int p_col(int ks) {
         return Parts == 1 ? 8 * ks : 64 * (ks / 4) + 32 * ((ks % 4) / 2) + 8 * (ks % 2);
@@ -122,15 +124,36 @@ __device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, 
         : "memory");
 }
 
-// The CTA's tile: sequence, its first token (row of the packed batch and
-// position) and its tokens.  Tiles of a sequence are numbered from its end:
-// the longest first.
+// Transposes 16-byte parts among eight lanes: lane l's part x becomes lane x's part l.
+__device__ __forceinline__ void pf_transpose8(uint32_t (&w)[8][4], int lane) {
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) {
+        const bool up = (lane & k) != 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if ((x & k) == 0)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[x][e] : w[x | k][e], k);
+                    if (up)
+                        w[x][e] = got;
+                    else
+                        w[x | k][e] = got;
+                }
+    }
+}
+
+// A work item: sequence, its first token (row of the packed batch and position),
+// its tokens, and the kv head.  Tiles of a sequence are numbered from its end: the
+// longest first.
 struct PfTile {
-    int seq, row0, pos0, tokens;
+    int seq, row0, pos0, tokens, hk;
 };
-// Called by one warp; seq = -1 when there is no such tile.
-__device__ __forceinline__ PfTile pf_find(const PrefillParams &p, int idx, int tpc, int lane) {
-    PfTile t = {-1, 0, 0, 0};
+// Item number `item` of tiles of tpc tokens; called by one warp.  seq = -1 when
+// there is no such item (nor one of a higher number).
+__device__ __forceinline__ PfTile pf_find(const PrefillParams &p, int item, int tpc, int lane) {
+    const int idx = item / p.kv.hkv;
+    PfTile t = {-1, 0, 0, 0, item - idx * p.kv.hkv};
     long long before = 0;
     for (int b0 = 0; b0 < p.kv.nseq; b0 += 32) {
         const int b = b0 + lane;
@@ -169,11 +192,37 @@ __device__ __forceinline__ PfTile pf_find(const PrefillParams &p, int idx, int t
     return t;
 }
 
+// Work items (a kv head's tiles of one CTA) are CTAs of the grid; a CTA that has
+// one goes on with the next that has not been launched yet (it cancels that
+// launch and takes its number), so the copies and first scores of an item run
+// under the softmax and the epilogue of the one before it: a CTA an item took
+// 11 us beside its key tiles (8192 rows: 272 us, nine ragged prompts: 117).
+// Asks for the next item: the answer comes to `resp` (16 bytes) on `bar`.
+__device__ __forceinline__ void pf_ask_next(uint32_t resp, uint32_t bar) {
+    mbar_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(resp),
+        "r"(bar)
+        : "memory");
+}
+// The answer: a CTA's number, or -1 when there is none (and none may be asked for).
+__device__ __forceinline__ int pf_next(uint32_t resp) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tmov.b32 %0, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(x)
+        : "r"(resp)
+        : "memory");
+    return x;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPfThreads, 1)
     q4attn_prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mq,
                              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                             const int box_rows, const int row_tiles) {
+                             const int box_rows, const int row_tiles, const bool more) {
     using M = typename PfT<T>::M;
     constexpr int NP = PfT<T>::Parts;
     using Cf = PfCfg<D, NP>;
@@ -182,16 +231,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    // barriers.  Of the ring: a stage's copies have landed, both MMA warps are
+    // done with it.  Of row tile i: Q has landed, Q is free, a key tile's S is
+    // complete, its P is written, O is complete, O is free.  Of the work items:
+    // slot's tile is known, every warp has read it, the answer to pf_ask_next.
     const uint32_t bars = sb + Cf::OffBar;
-    const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_s = b_q + 8 * NT,
-                   b_p = b_s + 8 * NT, b_o = b_p + 8 * NT, b_fix = b_o + 8 * NT, b_drain = b_fix + 8,
-                   b_x = b_drain + 16;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 448);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 452);
-    PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 464);
+    const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_qe = b_q + 8 * NT,
+                   b_s = b_qe + 8 * NT, b_p = b_s + 8 * NT, b_o = b_p + 8 * NT, b_oe = b_o + 8 * NT,
+                   b_known = b_oe + 8 * NT, b_read = b_known + 8 * kPfItems, b_mask = b_read + 8 * kPfItems,
+                   b_next = b_mask + 8 * kPfItems, b_drain = b_next + 8, b_x = b_drain + 16;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 576);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 580);
+    volatile int *slow = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 584);  // a row is being taken by the definition
+    const uint32_t resp = bars + 592;
+    PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 608);  // [kPfItems]
+    unsigned *mask_s = reinterpret_cast<unsigned *>(sm + Cf::OffBar + 608 + 20 * kPfItems);  // [kPfItems][kPfSoft]: rows to take again
     const long long lim = p.wait_cycles;
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
-    const int hk = (int)(blockIdx.x % p.kv.hkv), idx = (int)(blockIdx.x / p.kv.hkv);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -200,14 +256,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         for (int i = 0; i < NT; ++i) {
             mbar_init(b_q + 8 * i, 1);
+            mbar_init(b_qe + 8 * i, 1);
             mbar_init(b_s + 8 * i, 1);
             mbar_init(b_p + 8 * i, 4 * HF);
             mbar_init(b_o + 8 * i, 1);
+            mbar_init(b_oe + 8 * i, 4 * HF);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
-        mbar_init(b_fix, 1);
+        for (int i = 0; i < kPfItems; ++i) {
+            mbar_init(b_known + 8 * i, 1);
+            mbar_init(b_read + 8 * i, kPfSoft + 3);
+            mbar_init(b_mask + 8 * i, kPfSoft);
+        }
         for (int i = 0; i < 2; ++i) mbar_init(b_drain + 8 * i, 1);
+        mbar_init(b_next, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
         *abort_flag = 0;
+        *slow = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPfMma) {
@@ -216,123 +280,166 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == kPfCopy) {
-        const PfTile t = pf_find(p, idx, row_tiles * TQ, lane);
-        if (lane == 0) *tile_s = t;
+        const PfTile t = pf_find(p, (int)blockIdx.x, row_tiles * TQ, lane);
+        if (lane == 0) tile_s[0] = t;
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t taddr = *tslot;
-    const PfTile t = *tile_s;
-    if (t.seq < 0) {  // no tile of this number
+    if (tile_s[0].seq < 0) {  // no item of this number
         __syncthreads();
         if (warp == kPfMma) tc::tmem_dealloc(taddr, 512);
         return;
     }
-    const int nt = (t.tokens + TQ - 1) / TQ;  // row tiles in use
-    const int key_end = t.pos0 + t.tokens;
-    const int key_lo = p.window > 0 && t.pos0 + 1 > p.window ? t.pos0 + 1 - p.window : 0;
-    const int k_first = key_lo & ~(KT - 1);
-    const int nk = (key_end - k_first + KT - 1) / KT;
-    const int tail = key_end - (k_first + (nk - 1) * KT);  // positions of the last key tile
     auto fail = [&]() {
         *abort_flag = 1;
         atomicExch(p.err, 6);
     };
+    // A wait of a whole warp
+    auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)) != 0; };
+    // and one for a warp that may be at rows by the definition, which ends, but may
+    // take longer than the limit
+    auto wait_rows = [&](uint32_t bar, uint32_t parity) {
+        while (!wait(bar, parity)) {
+            const int busy = *slow;
+            if (!__any_sync(0xffffffffu, busy != 0) || *abort_flag) return false;
+        }
+        return true;
+    };
+    // key tiles of an item: the first position, how many, the last one's positions
+    auto keys_of = [&](const PfTile &t, int &k_first, int &nk, int &tail) {
+        const int key_end = t.pos0 + t.tokens;
+        const int key_lo = p.window > 0 && t.pos0 + 1 > p.window ? t.pos0 + 1 - p.window : 0;
+        k_first = key_lo & ~(KT - 1);
+        nk = (key_end - k_first + KT - 1) / KT;
+        tail = key_end - (k_first + (nk - 1) * KT);
+        return key_lo;
+    };
+    // item n, as the copy warp published it (seq < 0: no more)
+    auto tile_of = [&](int n, PfTile &t) {
+        const bool ok = wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
+        t = tile_s[n % kPfItems];
+        return ok;
+    };
+    auto tile_read = [&](int n) {
+        __syncwarp();
+        if (lane == 0) pf_arrive(b_read + 8 * (n % kPfItems));
+    };
 
-    int issued = 0;      // ring tiles issued (the copy warp)
     if (warp == kPfCopy) {
         // ------------------------------------------------------------ copies
-        if (lane == 0) {
-            const uint32_t qbytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
-            for (int i = 0; i < nt; ++i) {
-                mbar_expect_tx(b_q + 8 * i, qbytes + (i == 0 ? (uint32_t)p.extra_tx : 0u));
-                for (int b = 0; b < NP * NB; ++b)
-                    tma4(sb + Cf::OffQ + i * Cf::QTile + b * kPfBlk, &mq, 64 * (b % NB), hk * G, t.row0 + i * TQ, b / NB,
-                         b_q + 8 * i);
-            }
-        }
-        // lane = 64-value block bl, box r of a tile (at most 16 boxes); the next key
-        // tile's pages are looked up while this one's copies go out: looked up in
-        // place they held the ring back (a tile every 1400 cycles)
+        // lane = 64-value block bl, box r of a tile (at most 16 boxes)
         const int boxes = KT / box_rows, bl = lane / boxes, r = lane - bl * boxes;
-        auto lookup = [&](int j, int &page, int &slot) {
-            const int key = k_first + j * KT + r * box_rows, col = page_col(p.kv, key);
-            slot = key - col * p.kv.page;
-            page = bl < NB && key < key_end ? page_raw(p.kv, t.seq, col) : -1;
-        };
-        int page1, slot1;
-        lookup(0, page1, slot1);
-        bool ok = true;
-        int st = 0;
-        uint32_t ph = 1;  // an empty slot's phase: the first pass finds them free
-        for (int j = 0; ok && j < nk; ++j) {
-            const int page = page_ok(p.kv, page1), slot = slot1;
-            // a page out of range is copied as zeros (its coordinate is out of
-            // the map's range); below the window it may be gone
-            const int key = k_first + j * KT + r * box_rows;
-            if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
-            const int live = min(boxes, (key_end - k_first - j * KT + box_rows - 1) / box_rows);  // boxes with attended positions
-            if (j + 1 < nk) lookup(j + 1, page1, slot1);
-            for (int kv = 0; kv < 2 * NP; ++kv) {  // K's parts, V's parts
-                ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * st, ph, lim));
-                if (!ok || *abort_flag) {
-                    if (lane == 0 && !ok) fail();
-                    ok = false;
-                    break;
+        bool ok = true, asked = false;  // asked: an answer is outstanding, in this phase
+        uint32_t asked_phase = 0;
+        int issued = 0, st = 0;  // ring tiles issued, the next one's stage
+        uint32_t ph = 1;         // an empty slot's phase: the first pass finds them free
+        uint32_t qph = ~0u, q_out = 0;  // bit i: the phase of tile i's free Q; Q copies issued and perhaps in flight
+        PfTile t = tile_s[0];
+        if (lane == 0) pf_arrive(b_known);
+        for (int n = 0; ok && t.seq >= 0; ++n) {
+            int k_first, nk, tail;
+            const int key_lo = keys_of(t, k_first, nk, tail), key_end = t.pos0 + t.tokens;
+            const int nt = (t.tokens + TQ - 1) / TQ;
+            PfTile next = {-1, 0, 0, 0, 0};
+            // the next key tile's pages are looked up while this one's copies go out:
+            // looked up in place they held the ring back (a tile every 1400 cycles)
+            auto lookup = [&](int j, int &page, int &slot) {
+                const int key = k_first + j * KT + r * box_rows, col = page_col(p.kv, key);
+                slot = key - col * p.kv.page;
+                page = bl < NB && key < key_end ? page_raw(p.kv, t.seq, col) : -1;
+            };
+            int page1, slot1;
+            lookup(0, page1, slot1);
+            for (int j = 0; ok && j < nk; ++j) {
+                const int page = page_ok(p.kv, page1), slot = slot1;
+                // a page out of range is copied as zeros (its coordinate is out of
+                // the map's range); below the window it may be gone
+                const int key = k_first + j * KT + r * box_rows;
+                if (page < 0 && bl < NB && key < key_end && key + box_rows > key_lo) atomicExch(p.err, kErrPaged);
+                const int live = min(boxes, (key_end - k_first - j * KT + box_rows - 1) / box_rows);  // boxes with attended positions
+                if (j + 1 < nk) {
+                    lookup(j + 1, page1, slot1);
+                } else if (more) {  // no sooner, or the CTAs with the longest items would have all the others too
+                    if (lane == 0) pf_ask_next(resp, b_next);
+                    asked = true;
+                    asked_phase = (uint32_t)n & 1u;
                 }
-                if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
-                __syncwarp();
-                if (bl < NB && r < live)
-                    tma5(sb + Cf::OffRing + st * Cf::Tile + bl * Cf::KBlk + r * box_rows * 128, kv >= NP ? &mv : &mk,
-                         64 * bl, slot, hk, page, kv % NP, b_full + 8 * st);
-                ++issued;
-                if (++st == NS) {
-                    st = 0;
-                    ph ^= 1;
+                for (int kv = 0; ok && kv < 2 * NP; ++kv) {  // K's parts, V's parts
+                    if (j == 0 && kv == NP)
+                        for (int i = 0; ok && i < nt; ++i) {
+                            ok = wait(b_qe + 8 * i, (qph >> i) & 1u) && !*abort_flag;
+                            if (ok) {
+                                if (lane == 0) {
+                                    const uint32_t bytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
+                                    mbar_expect_tx(b_q + 8 * i, bytes + (n == 0 && i == 0 ? (uint32_t)p.extra_tx : 0u));
+                                    for (int b = 0; b < NP * NB; ++b)
+                                        tma4(sb + Cf::OffQ + i * Cf::QTile + b * kPfBlk, &mq, 64 * (b % NB), t.hk * G,
+                                             t.row0 + i * TQ, b / NB, b_q + 8 * i);
+                                }
+                                __syncwarp();
+                                qph ^= 1u << i;
+                                q_out |= 1u << i;
+                            }
+                        }
+                    ok = ok && wait(b_empty + 8 * st, ph) && !*abort_flag;
+                    if (!ok) break;
+                    if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
+                    __syncwarp();
+                    if (bl < NB && r < live)
+                        tma5(sb + Cf::OffRing + st * Cf::Tile + bl * Cf::KBlk + r * box_rows * 128, kv >= NP ? &mv : &mk,
+                             64 * bl, slot, t.hk, page, kv % NP, b_full + 8 * st);
+                    ++issued;
+                    if (++st == NS) {
+                        st = 0;
+                        ph ^= 1;
+                    }
                 }
+                if (ok && j + 1 == nk) {  // the ring is full: time to find the next item
+                    if (asked) ok = wait(b_next, asked_phase);
+                    if (ok) {
+                        const int at = asked ? pf_next(resp) : -1;
+                        asked = false;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next answer
+                        __syncwarp();
+                        if (at >= 0) next = pf_find(p, at, row_tiles * TQ, lane);
+                        ok = wait_rows(b_read + 8 * ((n + 1) % kPfItems), ((uint32_t)((n + 1) / kPfItems) & 1u) ^ 1u);
+                    }
+                    if (ok && lane == 0) {
+                        tile_s[(n + 1) % kPfItems] = next;
+                        pf_arrive(b_known + 8 * ((n + 1) % kPfItems));
+                    }
+                    __syncwarp();
+                }
+            }
+            if (ok) t = next;
+        }
+        if (!ok && lane == 0) fail();
+        // what is in flight lands before the CTA ends (it has, unless a wait gave up)
+        if (lane == 0) {
+            for (int n = max(0, issued - NS); n < issued; ++n)
+                mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, kWaitCycles);
+            if (!ok) {
+                for (int i = 0; i < NT; ++i)
+                    if ((q_out >> i) & 1u) mbar_wait(b_q + 8 * i, (qph >> i) & 1u, kWaitCycles);
+                if (asked) mbar_wait(b_next, asked_phase, kWaitCycles);
             }
         }
-        if (issued == 2 * NP * nk && tail < KT) {
-            // V rows behind the last position: zeros, whatever the page holds
-            for (int n = issued - NP; ok && n < issued; ++n) {
-                const int sv = n % NS;
-                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * sv, (uint32_t)(n / NS) & 1u, lim));
-                uint8_t *v = sm + Cf::OffRing + sv * Cf::Tile;
-                for (int x = tail * 8 + lane; ok && x < KT * 8; x += 32)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        *reinterpret_cast<uint4 *>(v + b * Cf::KBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                if (ok)
-                    pf_arrive(b_fix);
-                else
-                    fail();
-            }
-        }
+        __syncwarp();
     } else if (warp == kPfMma || warp == kPfMma + 1) {
         // ------------------------------------------------------------ MMA issue
         // warp w: row tiles w and w + 2, so that tiles seldom wait for each other's
         // softmax (one warp for two tiles: 315 us against 277 at 8192 rows, head
         // size 64, two tiles a CTA)
         const int w = warp - kPfMma;
-        const int last = w + 2 < nt ? w + 2 : w;  // this warp's last tile
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, KT, BF, false), id_o = tc::idesc_16(128, D, BF, true);
         const uint32_t q0 = tc::desc_sw128(sb + Cf::OffQ, 16), k0 = tc::desc_sw128(sb + Cf::OffRing, 16);
         const uint32_t v0 = tc::desc_sw128(sb + Cf::OffRing, Cf::KBlk);
-        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)); };
-        // both warps free a ring stage after their last tile; a warp alone does it twice
-        auto release = [&](int st) {
-            tc::commit(b_empty + 8 * st);
-            if (nt == 1) tc::commit(b_empty + 8 * st);
-        };
-        // the ring: key tile j's K parts, then its V parts
-        int st = 0;
+        int st = 0;  // the ring: key tile j's K parts, then its V parts
         uint32_t ph = 0;
+        uint32_t qph = 0, pph = 0, oph = ~0u;  // bit i: phases of tile i's Q, P and free O
         auto next = [&]() {
             if (++st == NS) {
                 st = 0;
@@ -348,34 +455,55 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
             return all;
         };
-        // S_i = Q_i K^T of the NP ring stages from st on, which have landed
-        auto scores = [&](int i, int st) {
-            if (leader) {
-                const uint32_t ts = taddr + (uint32_t)(KT * i);
-                const uint32_t qd = q0 + (uint32_t)((i * Cf::QTile) >> 4);
-#pragma unroll
-                for (int y = NP - 1; y >= 0; --y) {  // the small products first
-                    const int sk = st + y < NS ? st + y : st + y - NS;
-                    const uint32_t kd = k0 + (uint32_t)((sk * Cf::Tile) >> 4);
-#pragma unroll
-                    for (int x = NP - 1 - y; x >= 0; --x)  // Q's part x by K's part y
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks)
-                            tc::mma_sw128(ts, qd + (uint32_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
-                                          kd + (uint32_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
-                                          !(y == NP - 1 && x == 0 && ks == 0));
-                    if (y == 0) tc::commit(b_s + 8 * i);
-                    if (i == last) release(sk);
-                }
+        bool ok = true;
+        PfTile t;
+        for (int n = 0; ok; ++n) {
+            ok = tile_of(n, t);
+            if (!ok || t.seq < 0) break;
+            tile_read(n);
+            int k_first, nk, tail;
+            keys_of(t, k_first, nk, tail);
+            const int nt = (t.tokens + TQ - 1) / TQ;
+            if (w >= nt) {  // the other warp frees the stages
+                for (int x = 0; x < 2 * NP * nk; ++x) next();
+                continue;
             }
-            __syncwarp();
-        };
-        if (w < nt) {
-            bool ok = landed(0, 0u);
+            const int last = w + 2 < nt ? w + 2 : w;  // this warp's last tile
+            // both warps free a ring stage after their last tile; a warp alone does it twice
+            auto release = [&](int s) {
+                tc::commit(b_empty + 8 * s);
+                if (nt == 1) tc::commit(b_empty + 8 * s);
+            };
+            // S_i = Q_i K^T of the NP ring stages from s0 on, which have landed
+            auto scores = [&](int i, int s0, bool final) {
+                if (leader) {
+                    const uint32_t ts = taddr + (uint32_t)(KT * i);
+                    const uint32_t qd = q0 + (uint32_t)((i * Cf::QTile) >> 4);
+#pragma unroll
+                    for (int y = NP - 1; y >= 0; --y) {  // the small products first
+                        const int sk = s0 + y < NS ? s0 + y : s0 + y - NS;
+                        const uint32_t kd = k0 + (uint32_t)((sk * Cf::Tile) >> 4);
+#pragma unroll
+                        for (int x = NP - 1 - y; x >= 0; --x)  // Q's part x by K's part y
+#pragma unroll
+                            for (int ks = 0; ks < D / 16; ++ks)
+                                tc::mma_sw128(ts,
+                                              qd + (uint32_t)((x * Cf::QPart + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
+                                              kd + (uint32_t)(((ks / 4) * Cf::KBlk + (ks % 4) * 32) >> 4), id_s,
+                                              !(y == NP - 1 && x == 0 && ks == 0));
+                        if (y == 0) tc::commit(b_s + 8 * i);
+                        if (y == 0 && final) tc::commit(b_qe + 8 * i);
+                        if (i == last) release(sk);
+                    }
+                }
+                __syncwarp();
+            };
+            ok = landed(st, ph);
             for (int i = w; ok && i < nt; i += 2) {
-                ok = wait(b_q + 8 * i, 0u);
+                ok = wait(b_q + 8 * i, (qph >> i) & 1u) && !*abort_flag;
+                qph ^= 1u << i;
                 tc::fence_after_sync();
-                if (ok) scores(i, 0);
+                if (ok) scores(i, st, nk == 1);
             }
             for (int y = 0; y < NP; ++y) next();
             for (int j = 0; ok && j < nk; ++j) {
@@ -384,13 +512,33 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 for (int y = 0; y < NP; ++y) next();
                 const int sk = st;  // the next K's
                 const uint32_t phk = ph;
-                for (int y = 0; y < NP; ++y) next();
                 ok = landed(sv, phv);
-                if (j + 1 < nk) ok = ok && landed(sk, phk);
-                if (j == nk - 1 && tail < KT) ok = ok && wait(b_fix, 0u);
+                if (j + 1 < nk) {
+                    for (int y = 0; y < NP; ++y) next();
+                    ok = ok && landed(sk, phk);
+                } else if (ok && tail < KT) {
+                    // V rows behind the last position: zeros, whatever the page holds
+                    // (each MMA warp writes them: nobody waits)
+#pragma unroll
+                    for (int y = 0; y < NP; ++y) {
+                        uint8_t *v = sm + Cf::OffRing + (sv + y < NS ? sv + y : sv + y - NS) * Cf::Tile;
+                        for (int x = tail * 8 + lane; x < KT * 8; x += 32)
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+                                *reinterpret_cast<uint4 *>(v + b * Cf::KBlk + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
                 for (int i = w; ok && i < nt; i += 2) {
-                    ok = wait(b_p + 8 * i, (uint32_t)j & 1u);
-                    if (!ok || *abort_flag) break;
+                    ok = wait(b_p + 8 * i, (pph >> i) & 1u);
+                    pph ^= 1u << i;
+                    if (j == 0) {  // the item before has left O
+                        ok = ok && wait(b_oe + 8 * i, (oph >> i) & 1u);
+                        oph ^= 1u << i;
+                    }
+                    ok = ok && !*abort_flag;
+                    if (!ok) break;
                     tc::fence_after_sync();
                     if (leader) {  // O_i += P_i V
                         const uint32_t to = taddr + (uint32_t)(Cf::ColO + D * i), tp = taddr + (uint32_t)(KT * i);
@@ -410,51 +558,95 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (j + 1 < nk) scores(i, sk);
+                    if (j + 1 < nk) scores(i, sk, j + 2 == nk);
                 }
-                if (*abort_flag) break;
             }
-            if (!ok && leader) fail();
-            if (leader) {  // nothing is in flight when the CTA ends
-                tc::commit(b_drain + 8 * w);
-                mbar_wait(b_drain + 8 * w, 0u, kWaitCycles);
-            }
-            __syncwarp();
         }
+        if (!ok && leader) fail();
+        if (leader) {  // nothing is in flight when the CTA ends
+            tc::commit(b_drain + 8 * w);
+            mbar_wait(b_drain + 8 * w, 0u, kWaitCycles);
+        }
+        __syncwarp();
+    } else if (warp == kPfRows) {
+        // ------------------------------------------------------------ rows by the definition
+        bool ok = true;
+        PfTile t;
+        for (int n = 0; ok; ++n) {
+            ok = tile_of(n, t);
+            if (!ok || t.seq < 0) break;
+            ok = wait(b_mask + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u) && !*abort_flag;
+            if (!ok) break;
+            const unsigned rows = lane < kPfSoft ? mask_s[(n % kPfItems) * kPfSoft + lane] : 0u;
+            unsigned warps = __ballot_sync(0xffffffffu, rows != 0u);
+            if (warps) {
+                if (lane == 0) *slow = 1;
+                for (; warps; warps &= warps - 1) {
+                    const int w = __ffs(warps) - 1;
+                    for (unsigned left = __shfl_sync(0xffffffffu, rows, w); left; left &= left - 1) {
+                        const int r = 32 * (w & 3) + __ffs(left) - 1, tok = (w >> 2) / HF * TQ + r / G;
+                        attn_row<T, D>(p, t.row0 + tok, t.hk * G + r % G, t.seq, t.pos0 + tok, lane);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) *slow = 0;
+            }
+            tile_read(n);
+        }
+        if (!ok && lane == 0) fail();
     } else {
         // ------------------------------------------------------------ softmax
         // tile i, columns 64 hf .. of every key tile, row r
         const int i = (warp >> 2) / HF, hf = (warp >> 2) % HF, r = 32 * (warp & 3) + lane;
-        if (i < nt) {
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
+        const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of flushed O
+        constexpr int QO = D / (16 * HF), QS = NP * QO;             // 16-column parts of O, and with the sum
+        const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
+        float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
+        uint32_t sph = 0, oph = 0, xph = 0;  // phases of S, O and the exchange
+        // a row's value of the other column half: its warp has read the one before
+        // by the time it is written again (S of the next key tile comes after every
+        // warp's P)
+        auto other = [&](float mine, bool &ok) {
+            xs[hf * 128 + r] = mine;
+            __syncwarp();
+            if (lane == 0) pf_arrive(bx);
+            ok = wait(bx, xph);
+            xph ^= 1u;
+            return xs[(hf ^ 1) * 128 + r];
+        };
+        bool ok = true;
+        PfTile t;
+        for (int n = 0; ok; ++n) {
+            ok = tile_of(n, t);
+            if (!ok || t.seq < 0) break;
+            tile_read(n);
+            // rows that are not finite are left to the warp that takes them again
+            auto post = [&](unsigned rows) {
+                if (lane == 0) {
+                    mask_s[(n % kPfItems) * kPfSoft + warp] = rows;
+                    pf_arrive(b_mask + 8 * (n % kPfItems));
+                }
+            };
+            if (i >= (t.tokens + TQ - 1) / TQ) {
+                post(0u);
+                continue;
+            }
+            int k_first, nk, tail;
+            keys_of(t, k_first, nk, tail);
             const int tok = i * TQ + r / G, g = r % G;
             const bool live = r < G * TQ && tok < t.tokens;
             const int pos = t.pos0 + (live ? tok : min(i * TQ, t.tokens - 1));
             const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
-            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
-            const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of flushed O
-            constexpr int QO = D / (16 * HF), QS = NP * QO;             // 16-column parts of O, and with the sum
-            const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
-            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
-            float c = p.scale * 1.4426950408889634f, vback = 1.f;
-            if constexpr (NP == 2) {  // the powers of two of Q's row, K and V back
-                c *= pf_back(p.maxima[hk]) * (live ? p.qback[(size_t)(t.row0 + tok) * p.H + hk * G + g] : 0.f);
-                vback = pf_back(p.maxima[p.kv.hkv + hk]);
-            }
-            // a row's value of the other column half, exchange number n: its warp
-            // has read the one before from `buf` by the time it is written again
-            // (S of the next key tile comes after every warp's P)
-            auto other = [&](float mine, int n, float *buf, bool &ok) {
-                buf[hf * 128 + r] = mine;
-                __syncwarp();
-                if (lane == 0) pf_arrive(bx);
-                ok = __all_sync(0xffffffffu, mbar_wait(bx, (uint32_t)n & 1u, lim));
-                return buf[(hf ^ 1) * 128 + r];
-            };
+            const int row = t.row0 + tok, head = t.hk * G + g;
+            float c = p.scale * 1.4426950408889634f;
+            if constexpr (NP == 2)  // the powers of two of Q's row and K back
+                c *= pf_back(p.maxima[t.hk]) * (live ? p.qback[(size_t)row * p.H + head] : 0.f);
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
             for (int j = 0; j < nk; ++j) {
-                ok = __all_sync(0xffffffffu, mbar_wait(b_s + 8 * i, (uint32_t)j & 1u, lim));
+                ok = wait(b_s + 8 * i, sph);
+                sph ^= 1u;
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
                 const bool flush = NP == 2 && j > 0 && j % kPfFlush == 0;
@@ -497,7 +689,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
                 float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 if constexpr (HF == 2) {
-                    top = fmaxf(top, other(top, j, xs, ok));
+                    top = fmaxf(top, other(top, ok));
                     if (!ok) break;
                 }
                 if (j == 0) {
@@ -549,69 +741,75 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 __syncwarp();
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
-            if (ok && !*abort_flag) {
-                ok = __all_sync(0xffffffffu, mbar_wait(b_o + 8 * i, 0u, lim));
-                if constexpr (HF == 2)
-                    if (ok) l += other(l, nk, xs, ok);
+            if (ok && !*abort_flag) ok = wait(b_o + 8 * i, oph);
+            oph ^= 1u;
+            ok = ok && !*abort_flag;
+            if (!ok) break;
+            tc::fence_after_sync();
+            uint32_t o[16 * QO];
+            float worst = 0.f;  // NaN where a value is not finite
+#pragma unroll
+            for (int q = 0; q < QO; ++q) {
+                tc::ld16(to + (D / HF) * hf + 16 * q, o + 16 * q);
+                if (NP == 2 && nk > kPfFlush) {
+                    uint32_t a[16];
+                    tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
+                    tc::wait_ld16(a);
+                    tc::wait_ld16(o + 16 * q);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        o[16 * q + e] = __float_as_uint(__uint_as_float(o[16 * q + e]) + __uint_as_float(a[e]));
+                }
             }
-            if (!ok && lane == 0) fail();
-            if (ok && !*abort_flag) {
-                tc::fence_after_sync();
-                const float inv = (l == 0.f ? 0.f : 1.f / l) * vback;
-                const int row = t.row0 + tok, head = hk * G + g;
-                T *dst = (T *)p.out + ((size_t)row * p.H + head) * D + (D / HF) * hf;
-                float worst = 0.f;  // NaN or infinite where a value is
 #pragma unroll
-                for (int q = 0; q < QO; ++q) {
-                    uint32_t o[16];
-                    tc::ld16(to + (D / HF) * hf + 16 * q, o);
-                    tc::wait_ld16(o);
-                    if (NP == 2 && nk > kPfFlush) {
-                        uint32_t a[16];
-                        tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
-                        tc::wait_ld16(a);
+            for (int q = 0; q < QO; ++q) tc::wait_ld16(o + 16 * q);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) pf_arrive(b_oe + 8 * i);  // the next item's product may begin
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
-                    }
-                    uint4 w[sizeof(T)];
-                    uint32_t *ww = reinterpret_cast<uint32_t *>(w);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float a = __uint_as_float(o[2 * e]) * inv, b = __uint_as_float(o[2 * e + 1]) * inv;
-                        worst = fmaf(a, 0.f, fmaf(b, 0.f, worst));
-                        if constexpr (sizeof(T) == 4) {
-                            ww[2 * e] = __float_as_uint(a);
-                            ww[2 * e + 1] = __float_as_uint(b);
-                        } else {
-                            ww[e] = pack2<T>(a, b);
-                        }
-                    }
-                    if (live)
-#pragma unroll
-                        for (int e = 0; e < (int)sizeof(T); ++e) *(reinterpret_cast<uint4 *>(dst + 16 * q) + e) = w[e];
-                }
-                // rows that are not finite: by the definition (whole rows, after
-                // both halves have stored theirs); Q's tile is free by now
-                if constexpr (HF == 2)
-                    worst += other(worst, nk + 1, reinterpret_cast<float *>(sm + Cf::OffQ + i * Cf::QTile), ok);
+            for (int e = 0; e < 16 * QO; ++e) worst = fmaf(__uint_as_float(o[e]), 0.f, worst);
+            l += worst;
+            if constexpr (HF == 2) {
+                l += other(l, ok);
+                if (!ok) break;
                 __syncwarp();
-                unsigned again = __ballot_sync(0xffffffffu, ok && live && hf == 0 && worst != 0.f);
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    attn_row<T, D>(p, __shfl_sync(0xffffffffu, row, src), __shfl_sync(0xffffffffu, head, src), t.seq,
-                                   __shfl_sync(0xffffffffu, pos, src), lane);
+                if (lane == 0) pf_arrive(bx);  // read: may be written again
+            }
+            // (both halves' warps see the same l)
+            const bool finite = fabsf(l) < INFINITY;
+            float inv = l == 0.f ? 0.f : 1.f / l;
+            if constexpr (NP == 2) inv *= pf_back(p.maxima[p.kv.hkv + t.hk]);
+            // 128 bytes of a row at a time: eight lanes exchange theirs, so that a store
+            // fills whole lines (each lane its own row: 7000 cycles an item, not 2000)
+            const size_t at = ((size_t)row * p.H + head) * D + (D / HF) * hf;
+            const unsigned good = __ballot_sync(0xffffffffu, live && finite);
+#pragma unroll
+            for (int q = 0; q < D * (int)sizeof(T) / (128 * HF); ++q) {
+                uint32_t w[8][4];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    if constexpr (sizeof(T) == 4)
+                        w[e / 4][e % 4] = __float_as_uint(__uint_as_float(o[32 * q + e]) * inv);
+                    else
+                        w[e / 4][e % 4] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
                 }
-                if (!ok && lane == 0) fail();
+                pf_transpose8(w, lane);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int src = (lane & 24) + x;
+                    const size_t a = __shfl_sync(0xffffffffu, at, src);
+                    if ((good >> src) & 1u)
+                        *reinterpret_cast<uint4 *>((uint8_t *)((T *)p.out + a) + 128 * q + 16 * (lane & 7)) =
+                            make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                }
+            }
+            post(__ballot_sync(0xffffffffu, live && hf == 0 && !finite));
+            if constexpr (HF == 2) {
+                ok = wait(bx, xph);
+                xph ^= 1u;
             }
         }
-    }
-    // what is in flight lands before the CTA ends (it has, unless a wait gave up)
-    if (warp == kPfCopy && lane == 0) {
-        for (int n = max(0, issued - NS); n < issued; ++n)
-            mbar_wait(b_full + 8 * (n % NS), (uint32_t)(n / NS) & 1u, kWaitCycles);
-        if (*abort_flag)
-            for (int i = 0; i < nt; ++i) mbar_wait(b_q + 8 * i, 0u, kWaitCycles);
+        if (!ok && lane == 0) fail();
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -860,7 +1058,8 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
     };
     while (row_tiles > 1 && 2 * ctas(row_tiles) < 3 * sms) row_tiles /= 2;
     const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas(row_tiles), dev::kPfThreads, Cf::Smem, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows, row_tiles) == cudaSuccess ? 0 : -1;
+    const bool more = ctas(row_tiles) > sms;  // than run at once
+    return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows, row_tiles, more) == cudaSuccess ? 0 : -1;
 }
 
 int launch_prefill(const PrefillParams &p, int dtype, int sms, void *stream_) {
