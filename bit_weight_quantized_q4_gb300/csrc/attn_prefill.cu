@@ -33,6 +33,8 @@
 // that some rows of a tile see and others do not would still enter as 0 * NaN:
 // a row whose result is not finite is therefore taken again by the definition
 // (attn_row), which never touches what it does not attend.
+#include <algorithm>
+
 #include "attn_prefill_row.cuh"
 #include "gemv_launch.cuh"
 #include "tc_common.cuh"
@@ -249,29 +251,25 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const long long lim = p.wait_cycles;
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tid == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(b_full + 8 * i, 1);
-            mbar_init(b_empty + 8 * i, 2);  // one for each MMA warp
+    if (warp == 0) {
+        auto init = [&](uint32_t bar, int n, uint32_t count) {  // n consecutive barriers, one a lane
+            if (lane < n) mbar_init(bar + 8 * lane, count);
+        };
+        init(b_full, NS, 1);
+        init(b_empty, NS, 2);  // one for each MMA warp
+        init(b_q, 3 * NT, 1);  // Q, free Q, S
+        init(b_p, NT, 4 * HF);
+        init(b_o, NT, 1);
+        init(b_oe, NT, 4 * HF);
+        init(b_known, kPfItems, 1);
+        init(b_read, kPfItems, kPfSoft + 3);
+        init(b_mask, kPfItems, kPfSoft);
+        init(b_next, 3, 1);  // and b_drain
+        init(b_x, 8, 2);
+        if (lane == 0) {
+            *abort_flag = 0;
+            *slow = 0;
         }
-        for (int i = 0; i < NT; ++i) {
-            mbar_init(b_q + 8 * i, 1);
-            mbar_init(b_qe + 8 * i, 1);
-            mbar_init(b_s + 8 * i, 1);
-            mbar_init(b_p + 8 * i, 4 * HF);
-            mbar_init(b_o + 8 * i, 1);
-            mbar_init(b_oe + 8 * i, 4 * HF);
-        }
-        for (int i = 0; i < kPfItems; ++i) {
-            mbar_init(b_known + 8 * i, 1);
-            mbar_init(b_read + 8 * i, kPfSoft + 3);
-            mbar_init(b_mask + 8 * i, kPfSoft);
-        }
-        for (int i = 0; i < 2; ++i) mbar_init(b_drain + 8 * i, 1);
-        mbar_init(b_next, 1);
-        for (int i = 0; i < 8; ++i) mbar_init(b_x + 8 * i, 2);
-        *abort_flag = 0;
-        *slow = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kPfMma) {
@@ -318,7 +316,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     };
     // item n, as the copy warp published it (seq < 0: no more)
     auto tile_of = [&](int n, PfTile &t) {
-        const bool ok = wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
+        const bool ok = n == 0 || wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
         t = tile_s[n % kPfItems];
         return ok;
     };
@@ -332,7 +330,22 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         // lane = 64-value block bl, box r of a tile (at most 16 boxes)
         const int boxes = KT / box_rows, bl = lane / boxes, r = lane - bl * boxes;
         bool ok = true, asked = false;  // asked: an answer is outstanding, in this phase
-        uint32_t asked_phase = 0;
+        uint32_t nph = 0;
+        auto ask = [&]() {
+            if (lane == 0) pf_ask_next(resp, b_next);
+            asked = true;
+        };
+        auto answer = [&]() {  // the next item's number, -1: none
+            if (!asked) return -1;
+            ok = wait(b_next, nph);
+            if (!ok) return -1;
+            asked = false;
+            nph ^= 1u;
+            const int at = pf_next(resp);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next answer
+            __syncwarp();
+            return at;
+        };
         int issued = 0, st = 0;  // ring tiles issued, the next one's stage
         uint32_t ph = 1;         // an empty slot's phase: the first pass finds them free
         uint32_t qph = ~0u, q_out = 0;  // bit i: the phase of tile i's free Q; Q copies issued and perhaps in flight
@@ -362,9 +375,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 if (j + 1 < nk) {
                     lookup(j + 1, page1, slot1);
                 } else if (more) {  // no sooner, or the CTAs with the longest items would have all the others too
-                    if (lane == 0) pf_ask_next(resp, b_next);
-                    asked = true;
-                    asked_phase = (uint32_t)n & 1u;
+                    ask();
                 }
                 for (int kv = 0; ok && kv < 2 * NP; ++kv) {  // K's parts, V's parts
                     if (j == 0 && kv == NP)
@@ -397,15 +408,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     }
                 }
                 if (ok && j + 1 == nk) {  // the ring is full: time to find the next item
-                    if (asked) ok = wait(b_next, asked_phase);
-                    if (ok) {
-                        const int at = asked ? pf_next(resp) : -1;
-                        asked = false;
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next answer
-                        __syncwarp();
-                        if (at >= 0) next = pf_find(p, at, row_tiles * TQ, lane);
-                        ok = wait_rows(b_read + 8 * ((n + 1) % kPfItems), ((uint32_t)((n + 1) / kPfItems) & 1u) ^ 1u);
+                    int at = answer();
+                    if (at >= 0) next = pf_find(p, at, row_tiles * TQ, lane);
+                    while (ok && at >= 0 && next.seq < 0) {  // the numbers behind it have no item either: nothing launches them
+                        ask();
+                        at = answer();
                     }
+                    if (ok) ok = wait_rows(b_read + 8 * ((n + 1) % kPfItems), ((uint32_t)((n + 1) / kPfItems) & 1u) ^ 1u);
                     if (ok && lane == 0) {
                         tile_s[(n + 1) % kPfItems] = next;
                         pf_arrive(b_known + 8 * ((n + 1) % kPfItems));
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (!ok) {
                 for (int i = 0; i < NT; ++i)
                     if ((q_out >> i) & 1u) mbar_wait(b_q + 8 * i, (qph >> i) & 1u, kWaitCycles);
-                if (asked) mbar_wait(b_next, asked_phase, kWaitCycles);
+                if (asked) mbar_wait(b_next, nph, kWaitCycles);
             }
         }
         __syncwarp();
@@ -923,23 +932,52 @@ __device__ __forceinline__ void pf_items(const PrefillParams &p, F fn) {
     }
 }
 
+// The K and V values of a staging item that a thread handles: dims 4 (tid % L) ..
+// of every 256 / L-th position, all loads at once (ok: bit i, position i is
+// attended and its page in range).
+template <int D>
+struct PfRows {
+    static constexpr int L = D / 4, N = kPfChunk * L / 256;
+    float4 k[N], v[N];
+    size_t off[N];
+    unsigned ok = 0;
+    __device__ __forceinline__ PfRows(const PrefillParams &p, int b, int hk, int at, int end) {
+        const int tid = threadIdx.x;
+        int page[N], slot[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int pos = at + tid / L + i * (256 / L), col = page_col(p.kv, pos);
+            page[i] = pos < end ? page_at(p.kv, b, col) : -1;
+            slot[i] = pos - col * p.kv.page;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (page[i] < 0) continue;
+            ok |= 1u << i;
+            off[i] = row_off(p.kv, page[i], hk, slot[i], D) + 4 * (tid % L);
+            k[i] = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off[i]);
+            v[i] = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off[i]);
+        }
+    }
+};
+__device__ __forceinline__ float finite_max(float m, float4 v) {
+    return fmaxf(fmaxf(m, fmaxf(finite_abs(v.x), finite_abs(v.y))), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_constant__ PrefillParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int L = D / 4;  // lanes of a row
+    constexpr int L = D / 4, U = 4;  // lanes of a row, rows of Q at once
     const int tid = threadIdx.x, lane = tid & 31, j = 4 * (tid % L);
     pf_items<1>(p, [&](int b, int hk, int at, int end) {
+        const PfRows<D> x(p, b, hk, at, end);
         float mk = 0.f, mv = 0.f;
-#pragma unroll 4
-        for (int pos = at + tid / L; pos < end; pos += 256 / L) {
-            const int col = pos / p.kv.page, page = page_at(p.kv, b, col);
-            if (page < 0) continue;
-            const size_t off = row_off(p.kv, page, hk, pos - col * p.kv.page, D) + j;
-            const float4 k = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off);
-            const float4 v = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off);
-            mk = fmaxf(fmaxf(mk, fmaxf(finite_abs(k.x), finite_abs(k.y))), fmaxf(finite_abs(k.z), finite_abs(k.w)));
-            mv = fmaxf(fmaxf(mv, fmaxf(finite_abs(v.x), finite_abs(v.y))), fmaxf(finite_abs(v.z), finite_abs(v.w)));
+#pragma unroll
+        for (int i = 0; i < PfRows<D>::N; ++i) {
+            mk = finite_max(mk, x.k[i]);
+            mv = finite_max(mv, x.v[i]);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -952,17 +990,28 @@ __global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_
         }
     });
     const size_t units = (size_t)p.rows * p.H, part = units * D;
-    for (size_t u0 = (size_t)blockIdx.x * (256 / L); u0 < units; u0 += (size_t)gridDim.x * (256 / L)) {
-        const size_t u = u0 + tid / L;
-        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (u < units) q = *reinterpret_cast<const float4 *>((const float *)p.q + u * D + j);
-        float m = fmaxf(fmaxf(finite_abs(q.x), finite_abs(q.y)), fmaxf(finite_abs(q.z), finite_abs(q.w)));
+    for (size_t u0 = (size_t)blockIdx.x * (U * 256 / L); u0 < units; u0 += (size_t)gridDim.x * (U * 256 / L)) {
+        float4 q[U];
+        float m[U];
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = pf_exp(__float_as_uint(m));
-        if (u < units) {
+        for (int i = 0; i < U; ++i) {
+            const size_t u = u0 + tid / L + i * (256 / L);
+            q[i] = u < units ? *reinterpret_cast<const float4 *>((const float *)p.q + u * D + j)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) m[i] = finite_max(0.f, q[i]);
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < U; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const size_t u = u0 + tid / L + i * (256 / L);
+            if (u >= units) continue;
+            const int e = pf_exp(__float_as_uint(m[i]));
             uint2 hi, lo;
-            pf_split4(q, ldexpf(1.f, e), hi, lo);
+            pf_split4(q[i], ldexpf(1.f, e), hi, lo);
             *reinterpret_cast<uint2 *>(p.qimg + u * D + j) = hi;
             *reinterpret_cast<uint2 *>(p.qimg + part + u * D + j) = lo;
             if (j == 0) p.qback[u] = ldexpf(1.f, -e);
@@ -974,25 +1023,20 @@ template <int D>
 __global__ void __launch_bounds__(256) q4attn_prefill_split_kernel(const __grid_constant__ PrefillParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    constexpr int L = D / 4;
-    const int tid = threadIdx.x, j = 4 * (tid % L);
     const size_t part = (size_t)p.kv.num_pages * p.kv.hkv * p.kv.page * D;
     pf_items<128>(p, [&](int b, int hk, int at, int end) {  // from a key tile's start
+        const PfRows<D> x(p, b, hk, at, end);
         const float fk = ldexpf(1.f, pf_exp(p.maxima[hk])), fv = ldexpf(1.f, pf_exp(p.maxima[p.kv.hkv + hk]));
-#pragma unroll 4
-        for (int pos = at + tid / L; pos < end; pos += 256 / L) {
-            const int col = pos / p.kv.page, page = page_at(p.kv, b, col);
-            if (page < 0) continue;
-            const size_t off = row_off(p.kv, page, hk, pos - col * p.kv.page, D) + j;
-            const float4 k = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off);
-            const float4 v = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off);
+#pragma unroll
+        for (int i = 0; i < PfRows<D>::N; ++i) {
+            if (((x.ok >> i) & 1u) == 0) continue;
             uint2 hi, lo;
-            pf_split4(k, fk, hi, lo);
-            *reinterpret_cast<uint2 *>(p.kimg + off) = hi;
-            *reinterpret_cast<uint2 *>(p.kimg + part + off) = lo;
-            pf_split4(v, fv, hi, lo);
-            *reinterpret_cast<uint2 *>(p.vimg + off) = hi;
-            *reinterpret_cast<uint2 *>(p.vimg + part + off) = lo;
+            pf_split4(x.k[i], fk, hi, lo);
+            *reinterpret_cast<uint2 *>(p.kimg + x.off[i]) = hi;
+            *reinterpret_cast<uint2 *>(p.kimg + part + x.off[i]) = lo;
+            pf_split4(x.v[i], fv, hi, lo);
+            *reinterpret_cast<uint2 *>(p.vimg + x.off[i]) = hi;
+            *reinterpret_cast<uint2 *>(p.vimg + part + x.off[i]) = lo;
         }
     });
 }
@@ -1051,10 +1095,10 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
     static size_t smem_set[64] = {0};
     if (!raise_smem(kern, (size_t)Cf::Smem, smem_set)) return -1;
     // row tiles a CTA: NT, fewer while that leaves the device without a CTA and a
-    // half an SM; at most one part-filled CTA a sequence
+    // half an SM; at most one part-filled item a sequence
     int row_tiles = Cf::NT;
     auto ctas = [&](int n) {
-        return ((long long)p.rows / (n * TQ) + (p.kv.nseq < p.rows ? p.kv.nseq : p.rows)) * p.kv.hkv;
+        return (p.rows + std::min<long long>(p.kv.nseq, p.rows) * (n * TQ - 1)) / (n * TQ) * p.kv.hkv;
     };
     while (row_tiles > 1 && 2 * ctas(row_tiles) < 3 * sms) row_tiles /= 2;
     const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas(row_tiles), dev::kPfThreads, Cf::Smem, stream, &attr);
