@@ -44,10 +44,6 @@ namespace q4 {
 namespace dev {
 
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values (a block of a Q tile)
-constexpr int kPfSoft = 16;                 // softmax warps: row tiles x column halves x 4 row quarters
-constexpr int kPfMma = kPfSoft, kPfCopy = kPfSoft + 2;  // two MMA warps, the copy warp
-constexpr int kPfRows = kPfSoft + 3;        // the warp of the rows taken by the definition
-constexpr int kPfThreads = 32 * (kPfSoft + 4);
 constexpr int kPfItems = 4;                 // work items of a CTA that are known and not done
 // fp32: the tensor core's accumulation truncates, which over a long chain of
 // products shows (3e-6 of the output after 2048 positions); every kPfFlush key
@@ -80,8 +76,14 @@ struct PfT<float> {
 template <int D, int Parts>
 struct PfCfg {
     static constexpr int KT = D == 64 && Parts == 1 ? 64 : 128;  // positions of a key tile
-    static constexpr int HF = KT / 64;                 // warps (columns of 64) that share a row
+    // warps that share a row, CW columns each (head size 128 with a warp a row and
+    // 168 registers: 98 us against 91 for nine ragged prompts)
+    static constexpr int HF = KT / 64;
+    static constexpr int CW = KT / HF;
     static constexpr int NT = KT == 64 ? 4 : D * Parts == 256 ? 1 : 2;  // row tiles of a CTA at most
+    // softmax warps (row tiles x columns x 4 row quarters), two that issue MMAs, the
+    // copy warp, the warp of the rows taken by the definition
+    static constexpr int Soft = 4 * HF * NT, Mma = Soft, Copy = Soft + 2, Rows = Soft + 3, Threads = 32 * (Soft + 4);
     static constexpr int NB = D / 64;                  // 64-value blocks of a row
     static constexpr int KBlk = KT * 128;              // a block of a K or V tile
     static constexpr int Tile = NB * KBlk;             // one part of a K or V tile
@@ -93,11 +95,11 @@ struct PfCfg {
     // lies over its S (two parts: each column half's over its own, 16 columns of hi
     // and 16 of lo per 32 positions)
     static constexpr int ColO = NT * KT, ColSum = ColO + NT * D;
-    static constexpr int OffX = OffBar + 608 + (20 + 4 * kPfSoft) * kPfItems;          // values the column halves exchange [tile][half][row]
+    static constexpr int OffX = OffBar + 608 + (20 + 4 * 16) * kPfItems;  // values the column halves exchange [tile][half][row]
     static constexpr int Smem = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
     static_assert(ColO + NT * D * Parts <= 512, "tensor memory");
-    static_assert(4 * HF * NT <= kPfSoft, "softmax warps");
+    static_assert(Soft <= 16, "a barrier of the exchange for each pair of warps; masks");
     static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 <= 576, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
     static constexpr int p_col(int ks) {
@@ -221,7 +223,7 @@ __device__ __forceinline__ int pf_next(uint32_t resp) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPfThreads, 1)
+__global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     q4attn_prefill_tc_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap mq,
                              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                              const int box_rows, const int row_tiles, const bool more) {
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     constexpr int NP = PfT<T>::Parts;
     using Cf = PfCfg<D, NP>;
     constexpr bool BF = std::is_same<M, __nv_bfloat16>::value;
-    constexpr int NB = Cf::NB, NS = Cf::NS, NT = Cf::NT, KT = Cf::KT, HF = Cf::HF;
+    constexpr int NB = Cf::NB, NS = Cf::NS, NT = Cf::NT, KT = Cf::KT, HF = Cf::HF, CW = Cf::CW;
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     volatile int *slow = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 584);  // a row is being taken by the definition
     const uint32_t resp = bars + 592;
     PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 608);  // [kPfItems]
-    unsigned *mask_s = reinterpret_cast<unsigned *>(sm + Cf::OffBar + 608 + 20 * kPfItems);  // [kPfItems][kPfSoft]: rows to take again
+    unsigned *mask_s = reinterpret_cast<unsigned *>(sm + Cf::OffBar + 608 + 20 * kPfItems);  // [kPfItems][Cf::Soft]: rows to take again
     const long long lim = p.wait_cycles;
     const int G = p.H / p.kv.hkv, TQ = 128 / G;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         init(b_o, NT, 1);
         init(b_oe, NT, 4 * HF);
         init(b_known, kPfItems, 1);
-        init(b_read, kPfItems, kPfSoft + 3);
-        init(b_mask, kPfItems, kPfSoft);
+        init(b_read, kPfItems, Cf::Soft + 3);
+        init(b_mask, kPfItems, Cf::Soft);
         init(b_next, 3, 1);  // and b_drain
         init(b_x, 8, 2);
         if (lane == 0) {
@@ -272,12 +274,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kPfMma) {
+    if (warp == Cf::Mma) {
         tc::tmem_alloc(smem_u32(tslot), 512);
         tc::tmem_relinquish();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (warp == kPfCopy) {
+    if (warp == Cf::Copy) {
         const PfTile t = pf_find(p, (int)blockIdx.x, row_tiles * TQ, lane);
         if (lane == 0) tile_s[0] = t;
     }
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const uint32_t taddr = *tslot;
     if (tile_s[0].seq < 0) {  // no item of this number
         __syncthreads();
-        if (warp == kPfMma) tc::tmem_dealloc(taddr, 512);
+        if (warp == Cf::Mma) tc::tmem_dealloc(taddr, 512);
         return;
     }
     auto fail = [&]() {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     };
     // item n, as the copy warp published it (seq < 0: no more)
     auto tile_of = [&](int n, PfTile &t) {
-        const bool ok = n == 0 || wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
+        const bool ok = wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
         t = tile_s[n % kPfItems];
         return ok;
     };
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (lane == 0) pf_arrive(b_read + 8 * (n % kPfItems));
     };
 
-    if (warp == kPfCopy) {
+    if (warp == Cf::Copy) {
         // ------------------------------------------------------------ copies
         // lane = 64-value block bl, box r of a tile (at most 16 boxes)
         const int boxes = KT / box_rows, bl = lane / boxes, r = lane - bl * boxes;
@@ -436,12 +438,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == kPfMma || warp == kPfMma + 1) {
+    } else if (warp == Cf::Mma || warp == Cf::Mma + 1) {
         // ------------------------------------------------------------ MMA issue
         // warp w: row tiles w and w + 2, so that tiles seldom wait for each other's
         // softmax (one warp for two tiles: 315 us against 277 at 8192 rows, head
         // size 64, two tiles a CTA)
-        const int w = warp - kPfMma;
+        const int w = warp - Cf::Mma;
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, KT, BF, false), id_o = tc::idesc_16(128, D, BF, true);
         const uint32_t q0 = tc::desc_sw128(sb + Cf::OffQ, 16), k0 = tc::desc_sw128(sb + Cf::OffRing, 16);
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             mbar_wait(b_drain + 8 * w, 0u, kWaitCycles);
         }
         __syncwarp();
-    } else if (warp == kPfRows) {
+    } else if (warp == Cf::Rows) {
         // ------------------------------------------------------------ rows by the definition
         bool ok = true;
         PfTile t;
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             if (!ok || t.seq < 0) break;
             ok = wait(b_mask + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u) && !*abort_flag;
             if (!ok) break;
-            const unsigned rows = lane < kPfSoft ? mask_s[(n % kPfItems) * kPfSoft + lane] : 0u;
+            const unsigned rows = lane < Cf::Soft ? mask_s[(n % kPfItems) * Cf::Soft + lane] : 0u;
             unsigned warps = __ballot_sync(0xffffffffu, rows != 0u);
             if (warps) {
                 if (lane == 0) *slow = 1;
@@ -634,7 +636,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             // rows that are not finite are left to the warp that takes them again
             auto post = [&](unsigned rows) {
                 if (lane == 0) {
-                    mask_s[(n % kPfItems) * kPfSoft + warp] = rows;
+                    mask_s[(n % kPfItems) * Cf::Soft + warp] = rows;
                     pf_arrive(b_mask + 8 * (n % kPfItems));
                 }
             };
@@ -676,23 +678,23 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                         tc::st16(tsum + at, o);
                     }
                 }
-                uint32_t s[64];
-                tc::ld32(ts + 64 * hf, s);
-                tc::ld32(ts + 64 * hf + 32, s + 32);
-                tc::wait_ld32(s);
-                tc::wait_ld32(s + 32);
+                uint32_t s[CW];
+#pragma unroll
+                for (int q = 0; q < CW / 32; ++q) tc::ld32(ts + CW * hf + 32 * q, s + 32 * q);
+#pragma unroll
+                for (int q = 0; q < CW / 32; ++q) tc::wait_ld32(s + 32 * q);
                 const int k0 = k_first + j * KT;
                 if (k0 + KT - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
-                    const int hi = pos - k0 - 64 * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - 64 * hf : -1;
+                    const int hi = pos - k0 - CW * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - CW * hf : -1;
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
+                    for (int e = 0; e < CW; ++e)
                         if (e > hi || e < lo) s[e] = 0xff800000u;
                 }
                 float mx[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
 #pragma unroll
-                for (int e = 8; e < 64; e += 8)
+                for (int e = 8; e < CW; e += 8)
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                 uint64_t sum[2] = {0ull, 0ull};
                 // (over S's columns: the row's warps have read them)
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < CW / 32; ++q) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -740,8 +742,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                             s[32 * q + e] = pack2<M>(a - h.x, b - h.y);
                         }
                     }
-                    tc::st16(ts + (NP == 2 ? 64 * hf + 32 * q : 32 * hf + 16 * q), w);
-                    if constexpr (NP == 2) tc::st16(ts + 64 * hf + 32 * q + 16, s + 32 * q);
+                    tc::st16(ts + (NP == 2 ? CW * hf + 32 * q : CW / 2 * hf + 16 * q), w);
+                    if constexpr (NP == 2) tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
                 }
                 const uint64_t s2 = add_f32x2(sum[0], sum[1]);
                 l += lo_f32(s2) + hi_f32(s2);
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     if constexpr (sizeof(T) == 4)
                         w[e / 4][e % 4] = __float_as_uint(__uint_as_float(o[32 * q + e]) * inv);
                     else
-                        w[e / 4][e % 4] = pack2<T>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                        w[e / 4][e % 4] = pack2<T>(__uint_as_float(o[64 * q + 2 * e]) * inv, __uint_as_float(o[64 * q + 2 * e + 1]) * inv);
                 }
                 pf_transpose8(w, lane);
 #pragma unroll
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kPfMma) {
+    if (warp == Cf::Mma) {
         tc::fence_after_sync();
         tc::tmem_dealloc(taddr, 512);
     }
@@ -1101,7 +1103,7 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
         return (p.rows + std::min<long long>(p.kv.nseq, p.rows) * (n * TQ - 1)) / (n * TQ) * p.kv.hkv;
     };
     while (row_tiles > 1 && 2 * ctas(row_tiles) < 3 * sms) row_tiles /= 2;
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas(row_tiles), dev::kPfThreads, Cf::Smem, stream, &attr);
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas(row_tiles), Cf::Threads, Cf::Smem, stream, &attr);
     const bool more = ctas(row_tiles) > sms;  // than run at once
     return cudaLaunchKernelEx(&cfg, kern, p, mq, mk, mv, box_rows, row_tiles, more) == cudaSuccess ? 0 : -1;
 }
