@@ -10,7 +10,8 @@
 //   O += P V           tcgen05.mma with P as the tensor-memory operand
 // Q, K and V tiles come by tensor-map copies (TMA, 128-byte swizzle) straight
 // from the packed rows and the pages; V is the MN-major operand, so nothing is
-// transposed.  Sixteen softmax warps, two that issue MMAs, one that copies.
+// transposed.  Up to sixteen softmax warps, two that issue MMAs, one that copies,
+// one for rows taken by the definition (below).
 // While some tiles' softmax runs, the tensor core works on the others'
 // products: a tile's own chain (scores, weights, product) takes several times
 // its tensor work.  16-bit at head size 64: four tiles, key tiles of 64 positions
@@ -20,10 +21,13 @@
 // An MMA of 128 rows takes about 60 cycles per K = 16 at N = 64 as at N = 128
 // (measured by its issue), so at head size 64 the product runs at half the
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
-// positions, P beside S and S a key tile ahead, and 277 with four of 64 (272 now:
-// 1010 TFLOP/s, 83 % of what the half rate leaves).  At head size 128 the tensor
-// core is busy 64 % of the time (115 us for ten ragged prompts, 93 GFLOP): two row
-// tiles fill the tensor memory, and the softmax of one does not cover the other's.
+// positions, P beside S and S a key tile ahead, and 277 with four of 64 (259 now:
+// 1060 TFLOP/s, the tensor core busy 92 % of the loop).  At head size 128 (nine
+// ragged prompts, 93 GFLOP: 91 us, 1020 TFLOP/s) a key tile takes 3100 cycles of
+// which the tensor core works 1900: two row tiles fill the tensor memory, and the
+// softmax of one does not cover all of the other's.  fp32 (2048 rows: 77 us): three
+// products each at 4500 cycles a key tile, 4300 of them tensor work, and about 17 us
+// to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
 // (the sums stay exact: the reference maximum is the row's own, and its factor
 // cancels).

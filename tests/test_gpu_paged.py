@@ -346,6 +346,17 @@ def test_prefill_scale_zero_is_the_mean(q4, dtype):
     _prefill_case(q4, DTYPES[dtype], 4, 2, 64, 32, [150], [20], 0, 51, scale=0.0)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_more_work_than_runs_at_once(q4, dtype, D):
+    # several hundred tiles of all sizes, so that a CTA goes from one to the next
+    # (other sequences, other row tiles, partly filled key tiles), some of their rows
+    # not finite; the second call inside must give the same bits
+    _prefill_case(q4, DTYPES[dtype], 32, 8, D, 48, [310, 1, 700, 0, 64, 33, 129, 500, 2, 257, 96, 31],
+                  [0, 900, 0, 5, 64, 31, 17, 300, 1000, 3, 200, 1], 0, case_seed("work", dtype, D), poison=40)
+    _prefill_case(q4, DTYPES[dtype], 16, 16, D, 16, [400, 90, 222], [0, 400, 7], 100, case_seed("work1", dtype, D))
+
+
 def test_prefill_contiguous_cache_as_one_page(q4):
     _prefill_case(q4, torch.float32, 8, 2, 64, 333, [300], [33], 0, 46)
     _prefill_case(q4, torch.float16, 8, 2, 64, 201, [200], [1], 0, 47)
