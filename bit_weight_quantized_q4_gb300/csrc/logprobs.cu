@@ -7,13 +7,13 @@
 //   top: the k largest (ties to the lowest index), as x - lse.
 // One pass for the sums and each thread's largest value; then the k-th largest
 // of the 128 quads' maxima bounds the k-th largest logit from below, and a
-// second pass over the row (in L2 by then; in registers where a slice is one
-// batch) keeps the few values at or above that bound, which are ranked by
-// counting.  Where a bound lets too many through (long ties, masked rows) the k
-// largest are found one by one.  (Keeping candidates during the first pass, from
-// the bound of its first batch, costs more instructions than the second read:
-// 46 us for 512 rows of 65536 against 34.5; slices staged in shared memory took
-// 71.)
+// second look keeps the few values at or above that bound, which are ranked by
+// counting.  The first pass leaves the largest value of every 16 in shared memory,
+// so that the second reads again (from L2) only the 16s that reach the bound.
+// Where a bound lets too many through (long ties, masked rows) the k largest are
+// found one by one.  (512 rows of 65536: 31 us; 34.5 with the whole row read again,
+// 46 with candidates kept during the first pass from the bound of its first batch,
+// 71 with slices staged in shared memory; 23.7 without the top.)
 // HBM-bound on the row: a CTA a row when the rows fill the device; for fewer
 // rows a cluster of up to 8 CTAs splits each row and joins through distributed
 // shared memory, in one launch.
@@ -30,6 +30,7 @@ namespace cg = cooperative_groups;
 constexpr int kLpThreads = 512;
 constexpr int kLpCand = 1024;  // candidates a CTA holds
 constexpr int kLpTop = 32;     // largest k
+constexpr int kLpSlots = 16;   // batches whose largest values are held apart
 
 // Order-preserving key of a logit: NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t lp_key(float x) {
@@ -77,6 +78,7 @@ struct LpShared {
     LpSums warp[kLpThreads / 32];
     __align__(16) uint32_t quad[Quads + 12];  // quarters of it 4 words apart: their readers meet no bank twice
     unsigned long long best[kLpThreads / 32];
+    float tops[kLpSlots][kLpThreads];  // a thread's largest value of each batch (of batches kLpSlots apart)
     uint32_t bound;
     int ncand;
     __device__ __forceinline__ uint32_t *quad_at(int q) { return quad + q + 4 * (q / Quarter); }
@@ -197,11 +199,14 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
 #pragma unroll
         for (int q = 0; q < 4; ++q) m[q] = fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w));
     };
+    const int nbatch = (v1 - v0) / Batch;
 #pragma unroll 2
-    for (int j = v0; j < v1; j += Batch) {
-        load(j);
+    for (int b = 0; b < nbatch; ++b) {
+        load(v0 + b * Batch);
         tops();
         const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        float &slot = sh.tops[b % kLpSlots][tid];
+        slot = b < kLpSlots ? top : fmaxf(top, slot);
         kmax = max(kmax, lp_key(top));
         lp_raise(a, top);
         add4(v);
@@ -224,14 +229,23 @@ __global__ void __launch_bounds__(kLpThreads, 2) q4logprobs_kernel(const __grid_
         bound_of();
         const uint32_t bound = sh.bound;
         const float bv = bound ? lp_value(bound) : -INFINITY;  // key 0: everything is a candidate
-        for (int j = v0; j < v1; j += Batch) {
-            if (v1 - v0 > Batch) {  // one batch is still in registers
-                load(j);
-                tops();
-            }
+        auto take4 = [&](int j) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
                 if (m[q] >= bv || bound == 0u) lp_take(sh, v[q], j + 4 * (tid + q * kLpThreads), 4, bound);
+        };
+        if (nbatch == 1) {  // still in registers
+            take4(v0);
+        } else {
+            unsigned hit = 0;
+            for (int c = 0; c < min(nbatch, kLpSlots); ++c)
+                if (sh.tops[c][tid] >= bv || bound == 0u) hit |= 1u << c;
+            for (; hit; hit &= hit - 1)
+                for (int b = __ffs(hit) - 1; b < nbatch; b += kLpSlots) {
+                    load(v0 + b * Batch);
+                    tops();
+                    take4(v0 + b * Batch);
+                }
         }
         auto take = [&](float x1, int i) {
             if (lp_key(x1) >= bound) lp_take(sh, make_float4(x1, 0.f, 0.f, 0.f), i, 1, bound);
