@@ -11,7 +11,8 @@
 // dependent loads).  A thread takes four rotation pairs (j .. j + 3 with j +
 // D/2 ..), so every load is 16 bytes and every store 8 or 16; the first loads go
 // out before the row's place is known, so the two latencies overlap.  8191 rows
-// of 48 heads of 128 (306 MB): 51.7 us, 5.9 TB/s (53.6 with the loads after).
+// of 48 heads of 128 (306 MB): 45.8 us, 6.7 TB/s (51.7 with the head size an
+// argument, whose divisions were half the instructions; 53.6 with the loads after).
 #include "paged.cuh"
 #include "tensor_map.h"
 
@@ -21,17 +22,17 @@ namespace dev {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendAhead = 3;  // units a thread loads ahead
 
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kAppendThreads) q4kv_append_kernel(const __grid_constant__ AppendParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int row = blockIdx.x, tid = threadIdx.x;
-    const int D = p.D, half = D / 2, UH = D / 8;
+    constexpr int half = D / 2, UH = D / 8;
     const int Hq = p.q ? p.H : 0, Hkv = p.kv.hkv;
     const int units = (Hq + 2 * Hkv) * UH;
     // unit u: head u / UH of q, then k, then v, values j .. and half + j ..
-    auto load = [&](int u, float4 &a, float4 &b) {
-        const int hs = u / UH, j = 4 * (u - hs * UH);
+    auto load = [&](unsigned u, float4 &a, float4 &b) {
+        const int hs = u / UH, j = 4 * (u % UH);
         const float *src = hs < Hq         ? p.q + ((size_t)row * p.H + hs) * D
                            : hs < Hq + Hkv ? p.k + ((size_t)row * Hkv + hs - Hq) * D
                                            : p.v + ((size_t)row * Hkv + hs - Hq - Hkv) * D;
@@ -53,16 +54,16 @@ __global__ void __launch_bounds__(kAppendThreads) q4kv_append_kernel(const __gri
     const bool in_range = begin >= 0 && begin <= row && first >= 0 &&
                           pos64 < (long long)p.kv.width * p.kv.page && (!p.rope_cos || pos64 < p.rope_rows);
     const int pos = in_range ? (int)pos64 : 0;
-    const int page = in_range ? page_at(p.kv, seq, pos / p.kv.page) : -1;
+    const int col = page_col(p.kv, pos), page = in_range ? page_at(p.kv, seq, col) : -1;
     if (page < 0) {  // recorded, nothing of this row is written
         if (tid == 0) atomicExch(p.err, kErrPaged);
         return;
     }
-    const int slot = pos % p.kv.page;
+    const int slot = pos - col * p.kv.page;
     const float *cosr = p.rope_cos ? p.rope_cos + (size_t)pos * half : nullptr;
     const float *sinr = p.rope_cos ? p.rope_sin + (size_t)pos * half : nullptr;
-    auto store = [&](int u, float4 x, float4 y) {
-        const int hs = u / UH, j = 4 * (u - hs * UH);
+    auto store = [&](unsigned u, float4 x, float4 y) {
+        const int hs = u / UH, j = 4 * (u % UH);
         const bool isq = hs < Hq, isv = hs >= Hq + Hkv;
         if (cosr && !isv)
             rotate4(x, y, *reinterpret_cast<const float4 *>(cosr + j), *reinterpret_cast<const float4 *>(sinr + j));
@@ -86,7 +87,10 @@ template <typename T>
 static int launch_append_t(const AppendParams &p, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = pdl_config((unsigned)p.rows, dev::kAppendThreads, 0, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, dev::q4kv_append_kernel<T>, p) == cudaSuccess ? 0 : -1;
+    return cudaLaunchKernelEx(&cfg, p.D == 64 ? dev::q4kv_append_kernel<T, 64> : dev::q4kv_append_kernel<T, 128>, p) ==
+                   cudaSuccess
+               ? 0
+               : -1;
 }
 
 int launch_append(const AppendParams &p, int dtype, void *stream_) {

@@ -77,6 +77,17 @@ def test_logprobs(q4, n, rows):
         _check(q4, x, rng.integers(0, n, rows), top)
 
 
+@pytest.mark.parametrize("rows,n", [(1, 1200003), (2, 140001), (170, 139264)])
+def test_rows_longer_than_the_batches_held_apart(q4, rows, n):
+    # the largest values 8192 apart and so a thread's own, beside ordinary ones
+    rng = np.random.default_rng(n)
+    x = (2 * rng.standard_normal((rows, n))).astype(np.float32)
+    for r in range(min(rows, 3)):
+        at = np.arange(17 + 4 * r, n, 8192)
+        x[r, at] = 20 + rng.standard_normal(len(at)).astype(np.float32)
+    _check(q4, x, rng.integers(0, n, rows), 32)
+
+
 def test_more_rows_than_the_device_holds(q4):
     rng = np.random.default_rng(1)
     x = (3 * rng.standard_normal((700, 5001))).astype(np.float32)
