@@ -49,10 +49,6 @@ namespace dev {
 
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values (a block of a Q tile)
 constexpr int kPfItems = 4;                 // work items of a CTA that are known and not done
-// fp32: the tensor core's accumulation truncates, which over a long chain of
-// products shows (3e-6 of the output after 2048 positions); every kPfFlush key
-// tiles O is added to a sum beside it, and starts again
-constexpr int kPfFlush = 2;
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
 // What enters the products of a cache type: 16-bit values as they are (one
@@ -557,7 +553,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                     tc::fence_after_sync();
                     if (leader) {  // O_i += P_i V
                         const uint32_t to = taddr + (uint32_t)(Cf::ColO + D * i), tp = taddr + (uint32_t)(KT * i);
-                        const bool fresh = NP == 2 ? j % kPfFlush == 0 : j == 0;
+                        const bool fresh = NP == 2 || j == 0;
 #pragma unroll
                         for (int y = NP - 1; y >= 0; --y) {
                             const int at = sv + y < NS ? sv + y : sv + y - NS;
@@ -615,8 +611,8 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         const int i = (warp >> 2) / HF, hf = (warp >> 2) % HF, r = 32 * (warp & 3) + lane;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
-        const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of flushed O
-        constexpr int QO = D / (16 * HF), QS = NP * QO;             // 16-column parts of O, and with the sum
+        const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of the O before
+        constexpr int QO = D / (16 * HF);  // 16-column parts of O
         const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
         float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
         uint32_t sph = 0, oph = 0, xph = 0;  // phases of S, O and the exchange
@@ -664,19 +660,22 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 sph ^= 1u;
                 if (!ok || *abort_flag) break;
                 tc::fence_after_sync();
-                const bool flush = NP == 2 && j > 0 && j % kPfFlush == 0;
-                if (flush) {  // S came after the product before it: O is complete
+                // fp32: the tensor core's accumulation truncates, which over a long chain
+                // of products shows (3e-6 of the output after 2048 positions, 8e-7 with
+                // two key tiles in a chain, 4e-7 so): each key tile's O is added to a
+                // sum beside it.  S came after the product before it: O is complete
+                if (NP == 2 && j > 0) {
 #pragma unroll 1
                     for (int q = 0; q < D / (16 * HF); ++q) {
                         uint32_t o[16], a[16];
                         const uint32_t at = (D / HF) * hf + 16 * q;
                         tc::ld16(to + at, o);
-                        if (j > kPfFlush) {
+                        if (j > 1) {
                             tc::ld16(tsum + at, a);
                             tc::wait_ld16(a);
                         }
                         tc::wait_ld16(o);
-                        if (j > kPfFlush)
+                        if (j > 1)
 #pragma unroll
                             for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
                         tc::st16(tsum + at, o);
@@ -717,9 +716,9 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         l *= alpha;
                         m = mn;
 #pragma unroll 1
-                        for (int q = flush ? QO : 0; q < (j >= kPfFlush ? QS : QO); ++q) {  // O (if it holds any), then its sum
+                        for (int q = 0; q < QO; ++q) {
                             uint32_t o[16];
-                            const uint32_t at = (q < QO ? to + 16 * q : tsum + 16 * (q - QO)) + (D / HF) * hf;
+                            const uint32_t at = (NP == 2 ? tsum : to) + 16 * q + (D / HF) * hf;
                             tc::ld16(at, o);
                             tc::wait_ld16(o);
 #pragma unroll
@@ -766,7 +765,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
 #pragma unroll
             for (int q = 0; q < QO; ++q) {
                 tc::ld16(to + (D / HF) * hf + 16 * q, o + 16 * q);
-                if (NP == 2 && nk > kPfFlush) {
+                if (NP == 2 && nk > 1) {
                     uint32_t a[16];
                     tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
                     tc::wait_ld16(a);
