@@ -21,11 +21,11 @@
 // An MMA of 128 rows takes about 60 cycles per K = 16 at N = 64 as at N = 128
 // (measured by its issue), so at head size 64 the product runs at half the
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
-// positions, P beside S and S a key tile ahead, and 277 with four of 64 (259 now:
-// 1060 TFLOP/s, the tensor core busy 92 % of the loop).  At head size 128 (nine
-// ragged prompts, 93 GFLOP: 91 us, 1020 TFLOP/s) a key tile takes 3100 cycles of
+// positions, P beside S and S a key tile ahead, and 277 with four of 64 (247 now:
+// 1110 TFLOP/s, the tensor core busy over 90 % of the loop).  At head size 128 (nine
+// ragged prompts, 93 GFLOP: 90 us, 1030 TFLOP/s) a key tile takes 3000 cycles of
 // which the tensor core works 1900: two row tiles fill the tensor memory, and the
-// softmax of one does not cover all of the other's.  fp32 (2048 rows: 77 us): three
+// softmax of one does not cover all of the other's.  fp32 (2048 rows: 74 us): three
 // products each at 4500 cycles a key tile, 4300 of them tensor work, and about 17 us
 // to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 576);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 580);
     volatile int *slow = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 584);  // a row is being taken by the definition
+    volatile int *progress = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 588);  // key tiles copied
     const uint32_t resp = bars + 592;
     PfTile *tile_s = reinterpret_cast<PfTile *>(sm + Cf::OffBar + 608);  // [kPfItems]
     unsigned *mask_s = reinterpret_cast<unsigned *>(sm + Cf::OffBar + 608 + 20 * kPfItems);  // [kPfItems][Cf::Soft]: rows to take again
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         if (lane == 0) {
             *abort_flag = 0;
             *slow = 0;
+            *progress = 0;
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -298,12 +300,19 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     };
     // A wait of a whole warp
     auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim)) != 0; };
-    // and one for a warp that may be at rows by the definition, which ends, but may
-    // take longer than the limit
-    auto wait_rows = [&](uint32_t bar, uint32_t parity) {
+    // one that ends too when another warp has given up (of the copies, so that none
+    // follow; the others run dry and end by themselves)
+    auto wait_go = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim) && *abort_flag == 0) != 0;
+    };
+    // and one that may last a whole item: it gives up when, for the limit, no copy
+    // has gone out and no row was being taken by the definition
+    auto wait_item = [&](uint32_t bar, uint32_t parity) {
+        int seen = __shfl_sync(0xffffffffu, *progress, 0);
         while (!wait(bar, parity)) {
-            const int busy = *slow;
-            if (!__any_sync(0xffffffffu, busy != 0) || *abort_flag) return false;
+            const int now = __shfl_sync(0xffffffffu, *progress, 0);
+            if (!__any_sync(0xffffffffu, now != seen || *slow != 0) || __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            seen = now;
         }
         return true;
     };
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     };
     // item n, as the copy warp published it (seq < 0: no more)
     auto tile_of = [&](int n, PfTile &t) {
-        const bool ok = wait_rows(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
+        const bool ok = wait_item(b_known + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
         t = tile_s[n % kPfItems];
         return ok;
     };
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 for (int kv = 0; ok && kv < 2 * NP; ++kv) {  // K's parts, V's parts
                     if (j == 0 && kv == NP)
                         for (int i = 0; ok && i < nt; ++i) {
-                            ok = wait(b_qe + 8 * i, (qph >> i) & 1u) && !*abort_flag;
+                            ok = wait_go(b_qe + 8 * i, (qph >> i) & 1u);
                             if (ok) {
                                 if (lane == 0) {
                                     const uint32_t bytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
@@ -396,7 +405,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                                 q_out |= 1u << i;
                             }
                         }
-                    ok = ok && wait(b_empty + 8 * st, ph) && !*abort_flag;
+                    ok = ok && wait_go(b_empty + 8 * st, ph);
                     if (!ok) break;
                     if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
                     __syncwarp();
@@ -409,6 +418,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         ph ^= 1;
                     }
                 }
+                if (lane == 0) *progress = issued;
                 if (ok && j + 1 == nk) {  // the ring is full: time to find the next item
                     int at = answer();
                     if (at >= 0) next = pf_find(p, at, row_tiles * TQ, lane);
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         ask();
                         at = answer();
                     }
-                    if (ok) ok = wait_rows(b_read + 8 * ((n + 1) % kPfItems), ((uint32_t)((n + 1) / kPfItems) & 1u) ^ 1u);
+                    if (ok) ok = wait_item(b_read + 8 * ((n + 1) % kPfItems), ((uint32_t)((n + 1) / kPfItems) & 1u) ^ 1u);
                     if (ok && lane == 0) {
                         tile_s[(n + 1) % kPfItems] = next;
                         pf_arrive(b_known + 8 * ((n + 1) % kPfItems));
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             };
             ok = landed(st, ph);
             for (int i = w; ok && i < nt; i += 2) {
-                ok = wait(b_q + 8 * i, (qph >> i) & 1u) && !*abort_flag;
+                ok = wait(b_q + 8 * i, (qph >> i) & 1u);
                 qph ^= 1u << i;
                 tc::fence_after_sync();
                 if (ok) scores(i, st, nk == 1);
@@ -548,7 +558,6 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         ok = ok && wait(b_oe + 8 * i, (oph >> i) & 1u);
                         oph ^= 1u << i;
                     }
-                    ok = ok && !*abort_flag;
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (leader) {  // O_i += P_i V
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         for (int n = 0; ok; ++n) {
             ok = tile_of(n, t);
             if (!ok || t.seq < 0) break;
-            ok = wait(b_mask + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u) && !*abort_flag;
+            ok = wait_item(b_mask + 8 * (n % kPfItems), (uint32_t)(n / kPfItems) & 1u);
             if (!ok) break;
             const unsigned rows = lane < Cf::Soft ? mask_s[(n % kPfItems) * Cf::Soft + lane] : 0u;
             unsigned warps = __ballot_sync(0xffffffffu, rows != 0u);
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             for (int j = 0; j < nk; ++j) {
                 ok = wait(b_s + 8 * i, sph);
                 sph ^= 1u;
-                if (!ok || *abort_flag) break;
+                if (!ok) break;
                 tc::fence_after_sync();
                 // fp32: the tensor core's accumulation truncates, which over a long chain
                 // of products shows (3e-6 of the output after 2048 positions, 8e-7 with
@@ -755,9 +764,8 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 __syncwarp();
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
-            if (ok && !*abort_flag) ok = wait(b_o + 8 * i, oph);
+            ok = ok && wait(b_o + 8 * i, oph);
             oph ^= 1u;
-            ok = ok && !*abort_flag;
             if (!ok) break;
             tc::fence_after_sync();
             uint32_t o[16 * QO];
