@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             const bool whole_step = key0 >= lo && key0 + Step - 1 < pos && ((bad >> ((i * MT) & 31)) & ((1u << MT) - 1u)) == 0;
             if (!landed()) break;
             if (!whole_step) mend(i, false);
-            // scores: rows g and g + 8 of tile mt, heads 2t and 2t + 1, a sum for each part of Q
+            // scores: rows g and g + 8 of tile mt, heads 2t and 2t + 1, a sum for the
+            // products of each order (parts x of Q and y of K: x + y), so that the
+            // accumulation's truncation meets the largest ones D / 16 times only
             float sc[MT][NT][QP][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                         for (int y = 0; y < KP; ++y)
                             if (x + y < QP)
 #pragma unroll
-                                for (int mt = 0; mt < MT; ++mt) mma16816<M>(sc[mt][nt][x], a[mt][y], bq.x, bq.y);
+                                for (int mt = 0; mt < MT; ++mt) mma16816<M>(sc[mt][nt][x + y], a[mt][y], bq.x, bq.y);
                     }
             }
             advance();
