@@ -42,6 +42,7 @@ namespace dev {
 
 constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kPagedBatch = 16;  // shares a joining thread has in flight
 constexpr int kPagedOcc = 2;  // CTAs of an SM: eight warps with up to 255 registers each
 
 template <typename T>
@@ -147,9 +148,9 @@ struct PagedCfg {
 
 // Shared memory of a CTA: the prefix of units over the sequences (per kv head)
 // and their positions, Q's fragments (more than 8 heads: else they live in
-// registers after their preparation) and factors, the warps' maxima and sums,
-// the fold's sums, a flag, then the rings; over them, when a segment's loop is done, the warps'
-// outputs [warps][G][D] and the fold's weights.
+// registers after their preparation) and factors, the warps' maxima and sums, a
+// flag, then the rings; over them, when a segment's loop is done, the warps'
+// outputs [warps][G][D], or the joining's.
 template <typename T, int D, int NT>
 struct PagedSmem {
     static constexpr int Prefix = 0;
@@ -158,8 +159,7 @@ struct PagedSmem {
     static constexpr int Qs = Qf + PagedT<T>::QP * NT * (D / 16) * 32 * 8;
     static constexpr int Wm = Qs + 4 * 8 * NT;
     static constexpr int Wl = Wm + 4 * kPagedWarps * 8 * NT;
-    static constexpr int Fl = Wl + 4 * kPagedWarps * 8 * NT;  // [8 NT] fold sums
-    static constexpr int Flag = Fl + 4 * 8 * NT;
+    static constexpr int Flag = Wl + 4 * kPagedWarps * 8 * NT;
     static constexpr int New = (Flag + 16 + 15) / 16 * 16;    // the new k and v in the cache's type [2][D]
     static constexpr int Bars = New + 2 * D * (int)sizeof(T);
     static constexpr int Red = (Bars + 8 * kPagedWarps * PagedCfg<T, D>::NI + 1023) / 1024 * 1024;
@@ -187,7 +187,6 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
     uint2 *qf = reinterpret_cast<uint2 *>(psm + S::Qf);
     float *qs = reinterpret_cast<float *>(psm + S::Qs);
     float *wm = reinterpret_cast<float *>(psm + S::Wm), *wl = reinterpret_cast<float *>(psm + S::Wl);
-    float *fl = reinterpret_cast<float *>(psm + S::Fl);
     int *flag = reinterpret_cast<int *>(psm + S::Flag);
     float *red = reinterpret_cast<float *>(psm + S::Red);
     T *fresh = reinterpret_cast<T *>(psm + S::New);
@@ -809,52 +808,74 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                 const float *part0 = p.part + ((size_t)c0 * 2 + (start_of(c0) != s0 ? 1 : 0)) * slot_floats;
                 const float *part1 = p.part + (size_t)c0 * 2 * slot_floats;
                 auto slot_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * slot_floats; };
-                // weights 2^(m_i - M) and the sum, a warp a head
-                float *wts = red, *part = red + (size_t)((nc * G + 31) & ~31);  // [nc][G], then [NW][G D]
-                for (int h = warp; h < G; h += NW) {
-                    float Mx = -INFINITY, mi = -INFINITY, li = 0.f;
-                    for (int i = lane; i < nc; i += 32) {
-                        mi = __ldcg(slot_of(i) + G * D + h);
-                        li = __ldcg(slot_of(i) + G * D + G + h);
-                        Mx = fmaxf(Mx, mi);
-                        wts[i * G + h] = mi;
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) Mx = fmaxf(Mx, __shfl_xor_sync(0xffffffffu, Mx, o));
-                    const float mu = Mx == -INFINITY ? 0.f : Mx;
-                    float L = 0.f;
-                    for (int i = lane; i < nc; i += 32) {
-                        const float f = ex2(wts[i * G + h] - mu);
-                        wts[i * G + h] = f;
-                        L = fmaf(nc <= 32 ? li : __ldcg(slot_of(i) + G * D + G + h), f, L);
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-                    if (lane == 0) fl[h] = L;
-                }
-                __syncthreads();
-                // warp w adds the shares w, w + NW, .. of 128 outputs at a time, then
-                // the warps' sums are added in warp order
-                for (int e0 = 0; e0 < G * D; e0 += 128) {
-                    const int idx = e0 + 4 * lane, h = idx / D;
+                // A thread a float4 of the outputs (with threads to spare, groups of them
+                // that take every NG-th share): kPagedBatch shares at once, so that their
+                // latencies overlap, joined like the softmax's own steps.  (A warp's lanes
+                // on 128 outputs, one pass for the weights and another for the sums, took
+                // the last CTA of 38 9 us.)
+                const int T4 = G * D / 4, NG = T4 < kPagedThreads ? kPagedThreads / T4 : 1;
+                const int grp = NG > 1 ? tid / T4 : 0;
+                float *dst = p.out + ((size_t)b * p.H + hk * G) * D;
+                for (int e = tid - grp * T4; grp < NG && e < T4; e += kPagedThreads) {
+                    const int idx = 4 * e, h = idx / D;
+                    float Mx = -INFINITY, L = 0.f;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (idx < G * D) {
-#pragma unroll 4
-                        for (int i = warp; i < nc; i += NW) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot_of(i) + idx));
-                            const float f = wts[i * G + h];
-                            o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+                    for (int i0 = grp; i0 < nc; i0 += NG * kPagedBatch) {
+                        float4 v[kPagedBatch];
+                        float mi[kPagedBatch], li[kPagedBatch];
+#pragma unroll
+                        for (int y = 0; y < kPagedBatch; ++y) {
+                            const int i = i0 + NG * y;
+                            mi[y] = -INFINITY;
+                            li[y] = 0.f;
+                            v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (i < nc) {
+                                const float *sl = slot_of(i);
+                                v[y] = __ldcg(reinterpret_cast<const float4 *>(sl + idx));
+                                mi[y] = __ldcg(sl + G * D + h);
+                                li[y] = __ldcg(sl + G * D + G + h);
+                            }
                         }
-                        *reinterpret_cast<float4 *>(part + (size_t)warp * G * D + idx) = o;
+                        float mn = Mx;
+#pragma unroll
+                        for (int y = 0; y < kPagedBatch; ++y) mn = fmaxf(mn, mi[y]);
+                        const float mu = mn == -INFINITY ? 0.f : mn, a = ex2(Mx - mu);
+                        o = make_float4(o.x * a, o.y * a, o.z * a, o.w * a);
+                        L *= a;
+#pragma unroll
+                        for (int y = 0; y < kPagedBatch; ++y) {
+                            const float f = ex2(mi[y] - mu);
+                            o = make_float4(fmaf(v[y].x, f, o.x), fmaf(v[y].y, f, o.y), fmaf(v[y].z, f, o.z),
+                                            fmaf(v[y].w, f, o.w));
+                            L = fmaf(li[y], f, L);
+                        }
+                        Mx = mn;
+                    }
+                    if (NG == 1) {
+                        const float r = L == 0.f ? 0.f : 1.f / L;
+                        *reinterpret_cast<float4 *>(dst + idx) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+                    } else {
+                        *reinterpret_cast<float4 *>(red + (size_t)grp * G * D + idx) = o;
+                        if (idx == h * D) {
+                            wm[grp * G + h] = Mx;
+                            wl[grp * G + h] = L;
+                        }
                     }
                 }
-                __syncthreads();
-                for (int idx = tid; idx < G * D; idx += kPagedThreads) {
-                    float o = 0.f;
-#pragma unroll
-                    for (int w = 0; w < NW; ++w) o += part[(size_t)w * G * D + idx];
-                    const float L = fl[idx / D];
-                    p.out[((size_t)b * p.H + hk * G) * D + idx] = L == 0.f ? 0.f : o / L;
+                if (NG > 1) {
+                    __syncthreads();
+                    for (int idx = tid; idx < G * D; idx += kPagedThreads) {
+                        const int h = idx / D;
+                        float Mx = -INFINITY, o = 0.f, L = 0.f;
+                        for (int y = 0; y < NG; ++y) Mx = fmaxf(Mx, wm[y * G + h]);
+                        const float mu = Mx == -INFINITY ? 0.f : Mx;
+                        for (int y = 0; y < NG; ++y) {
+                            const float f = ex2(wm[y * G + h] - mu);
+                            o = fmaf(red[(size_t)y * G * D + idx], f, o);
+                            L = fmaf(wl[y * G + h], f, L);
+                        }
+                        dst[idx] = L == 0.f ? 0.f : o / L;
+                    }
                 }
                 if (tid == 0) p.count[(size_t)b * hkv + hk] = 0;  // zero again for the next call
             }
@@ -877,8 +898,8 @@ static int launch_paged_t(const PagedAttnParams &p, int ctas, cudaStream_t strea
     static size_t smem_set[64] = {0};
     const int G = p.H / p.kv.hkv;
     using Cfg = dev::PagedCfg<T, D>;
-    // the rings; over them the merge, or the fold's weights (one per CTA and head) and sums
-    const size_t merge = sizeof(float) * ((size_t)G * (dev::kPagedWarps * D + ctas) + 32);
+    // the rings; over them the merge (or the joining, of 512 floats at most)
+    const size_t merge = sizeof(float) * std::max(G * dev::kPagedWarps * D, 512);
     const size_t smem = dev::PagedSmem<T, D, NT>::Red + std::max(merge, (size_t)dev::kPagedWarps * Cfg::NI * Cfg::Item);
     if (!raise_smem(kern, smem, smem_set)) return -1;
     CUtensorMap mk{}, mv{};
