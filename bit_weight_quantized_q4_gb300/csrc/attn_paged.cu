@@ -796,10 +796,13 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             // the last of the pair's CTAs to finish folds their shares in CTA order
             const int c0 = cta_of(s0), nc = cta_of(s1 - 1) - c0 + 1;  // first CTA, CTAs
             __syncthreads();
-            if (tid == 0) {
-                __threadfence();  // the CTA's share (the barrier orders it before), then the count
-                *flag = atomicAdd(p.count + (size_t)b * hkv + hk, 1) == nc - 1;
-                __threadfence();
+            if (tid == 0) {  // the CTA's share (the barrier orders it before), then the count; the others' after it
+                int before;
+                asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                             : "=r"(before)
+                             : "l"(p.count + (size_t)b * hkv + hk)
+                             : "memory");
+                *flag = before == nc - 1;
             }
             __syncthreads();
             if (*flag) {
