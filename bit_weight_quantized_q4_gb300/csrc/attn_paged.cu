@@ -17,8 +17,8 @@
 //        fp32: pairs of positions packed, rows of the m tiles permuted so that a
 //        lane's 32 bytes of a V row are rows of its own tiles); P goes through
 //        movmatrix.
-// 64 ragged bf16 contexts up to 8191 (1.03 GB): 178 us, 5.8 TB/s; one of 32768
-// (134 MB): 34.6 us, of which the loop runs at the memory's rate and about 6 us
+// 64 ragged bf16 contexts up to 8191 (1.03 GB): 173 us, 5.9 TB/s; one of 32768
+// (134 MB): 30.5 us, of which the loop runs at the memory's rate and about 5 us
 // are the scan, Q, the warps' merge and the joining of the CTAs' shares.
 //
 // Precision: q and p stay fp32-like.  f16 caches: q (scaled per head by a
@@ -42,7 +42,7 @@ namespace dev {
 
 constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
-constexpr int kPagedBatch = 16;  // shares a joining thread has in flight
+constexpr int kPagedBatch = 8;  // shares a joining thread has in flight
 constexpr int kPagedOcc = 2;  // CTAs of an SM: eight warps with up to 255 registers each
 
 template <typename T>
@@ -272,9 +272,14 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
     // CTAs (all in front, the SMs that get two of them end last: 34 -> 38 us for
     // one context of 32768)
     const int each = W / N, more = W - each * N;
-    auto start_of = [&](int c) { return each * c + more * c / N; };
+    // (more c < 2^17 is exact in fp32, and the quotient's estimate off by one at most)
+    const float per_n = 1.f / (float)N, per_w = (float)N / (float)W;
+    auto start_of = [&](int c) {
+        const int x = more * c, q = (int)((float)x * per_n), r = x - q * N;
+        return each * c + q + (r >= N) - (r < 0);
+    };
     auto cta_of = [&](int u) {  // the CTA of unit u: an estimate, then the exact one
-        int c = min(N - 1, (int)((float)u * ((float)N / (float)W)));
+        int c = min(N - 1, (int)((float)u * per_w));
         while (start_of(c) > u) --c;
         while (start_of(c + 1) <= u) ++c;
         return c;
@@ -812,8 +817,8 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                 const float *part1 = p.part + (size_t)c0 * 2 * slot_floats;
                 auto slot_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * slot_floats; };
                 // A thread a float4 of the outputs (with threads to spare, groups of them
-                // that take every NG-th share): kPagedBatch shares at once, so that their
-                // latencies overlap, joined like the softmax's own steps.  (A warp's lanes
+                // that take every NG-th share): eight shares at once, so that their latencies
+                // overlap, joined like the softmax's own steps.  (A warp's lanes
                 // on 128 outputs, one pass for the weights and another for the sums, took
                 // the last CTA of 38 9 us.)
                 const int T4 = G * D / 4, NG = T4 < kPagedThreads ? kPagedThreads / T4 : 1;
