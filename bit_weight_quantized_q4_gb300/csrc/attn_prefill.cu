@@ -88,9 +88,13 @@ struct PfCfg {
     static constexpr int KBlk = KT * 128;              // a block of a K or V tile
     static constexpr int Tile = NB * KBlk;             // one part of a K or V tile
     static constexpr int QPart = NB * kPfBlk, QTile = Parts * QPart;
-    // ring stages: per key tile K's parts, then V's
-    static constexpr int NS = KT == 64 ? 12 : D == 64 ? 9 : 5;
-    static constexpr int OffQ = 0, OffRing = NT * QTile, OffBar = OffRing + NS * Tile;
+    // P in shared memory (blocks like Q's) instead of over its S: S is free as soon as
+    // it is in registers, and the next key tile's can be under way
+    static constexpr bool PS = D == 128 && Parts == 1;
+    // ring stages: per key tile K's parts, then V's (P in shared memory: K a tile ahead)
+    static constexpr int NS = KT == 64 ? 12 : D == 64 ? 9 : PS ? 3 : 5;
+    static constexpr int OffQ = 0, OffP = NT * QTile, PTile = PS ? (KT / 64) * kPfBlk : 0;
+    static constexpr int OffRing = OffP + NT * PTile, OffBar = OffRing + NS * Tile;
     // tensor memory columns: S of tile i from KT i, O of tile i from ColO + D i; P
     // lies over its S (two parts: each column half's over its own, 16 columns of hi
     // and 16 of lo per 32 positions)
@@ -100,7 +104,7 @@ struct PfCfg {
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
     static_assert(ColO + NT * D * Parts <= 512, "tensor memory");
     static_assert(Soft <= 16, "a barrier of the exchange for each pair of warps; masks");
-    static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 <= 576, "barriers before the tensor-memory address");
+    static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 + (PS ? 16 * NT : 0) <= 576, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
     static constexpr int p_col(int ks) {
         return Parts == 1 ? 8 * ks : 64 * (ks / 4) + 32 * ((ks % 4) / 2) + 8 * (ks % 2);
@@ -237,13 +241,15 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // barriers.  Of the ring: a stage's copies have landed, both MMA warps are
     // done with it.  Of row tile i: Q has landed, Q is free, a key tile's S is
-    // complete, its P is written, O is complete, O is free.  Of the work items:
+    // complete, its P is written, O is complete, O is free (P in shared memory: S has
+    // been read, P has been used).  Of the work items:
     // slot's tile is known, every warp has read it, the answer to pf_ask_next.
     const uint32_t bars = sb + Cf::OffBar;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_qe = b_q + 8 * NT,
                    b_s = b_qe + 8 * NT, b_p = b_s + 8 * NT, b_o = b_p + 8 * NT, b_oe = b_o + 8 * NT,
                    b_known = b_oe + 8 * NT, b_read = b_known + 8 * kPfItems, b_mask = b_read + 8 * kPfItems,
-                   b_next = b_mask + 8 * kPfItems, b_drain = b_next + 8, b_x = b_drain + 16;
+                   b_next = b_mask + 8 * kPfItems, b_drain = b_next + 8, b_x = b_drain + 16,
+                   b_sr = b_x + 64, b_pe = b_sr + 8 * NT;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 576);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 580);
     volatile int *slow = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 584);  // a row is being taken by the definition
@@ -269,6 +275,10 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         init(b_mask, kPfItems, Cf::Soft);
         init(b_next, 3, 1);  // and b_drain
         init(b_x, 8, 2);
+        if constexpr (Cf::PS) {
+            init(b_sr, NT, 4 * HF);
+            init(b_pe, NT, 1);
+        }
         if (lane == 0) {
             *abort_flag = 0;
             *slow = 0;
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 slot = key - col * p.kv.page;
                 page = bl < NB && key < key_end ? page_raw(p.kv, t.seq, col) : -1;
             };
-            int page1, slot1;
+            int page1, slot1, v_live = 0, v_page = -1, v_slot = 0;
             lookup(0, page1, slot1);
             for (int j = 0; ok && j < nk; ++j) {
                 const int page = page_ok(p.kv, page1), slot = slot1;
@@ -388,25 +398,9 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 } else if (more) {  // no sooner, or the CTAs with the longest items would have all the others too
                     ask();
                 }
-                for (int kv = 0; ok && kv < 2 * NP; ++kv) {  // K's parts, V's parts
-                    if (j == 0 && kv == NP)
-                        for (int i = 0; ok && i < nt; ++i) {
-                            ok = wait_go(b_qe + 8 * i, (qph >> i) & 1u);
-                            if (ok) {
-                                if (lane == 0) {
-                                    const uint32_t bytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
-                                    mbar_expect_tx(b_q + 8 * i, bytes + (n == 0 && i == 0 ? (uint32_t)p.extra_tx : 0u));
-                                    for (int b = 0; b < NP * NB; ++b)
-                                        tma4(sb + Cf::OffQ + i * Cf::QTile + b * kPfBlk, &mq, 64 * (b % NB), t.hk * G,
-                                             t.row0 + i * TQ, b / NB, b_q + 8 * i);
-                                }
-                                __syncwarp();
-                                qph ^= 1u << i;
-                                q_out |= 1u << i;
-                            }
-                        }
+                auto put = [&](int kv, int live, int page, int slot) {  // K's parts (kv < NP), V's parts
                     ok = ok && wait_go(b_empty + 8 * st, ph);
-                    if (!ok) break;
+                    if (!ok) return;
                     if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
                     __syncwarp();
                     if (bl < NB && r < live)
@@ -417,6 +411,32 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         st = 0;
                         ph ^= 1;
                     }
+                };
+                for (int kv = 0; kv < NP; ++kv) put(kv, live, page, slot);
+                if (j == 0)
+                    for (int i = 0; ok && i < nt; ++i) {
+                        ok = wait_go(b_qe + 8 * i, (qph >> i) & 1u);
+                        if (ok) {
+                            if (lane == 0) {
+                                const uint32_t bytes = (uint32_t)(NP * NB) * 128u * (uint32_t)(G * TQ);
+                                mbar_expect_tx(b_q + 8 * i, bytes + (n == 0 && i == 0 ? (uint32_t)p.extra_tx : 0u));
+                                for (int b = 0; b < NP * NB; ++b)
+                                    tma4(sb + Cf::OffQ + i * Cf::QTile + b * kPfBlk, &mq, 64 * (b % NB), t.hk * G,
+                                         t.row0 + i * TQ, b / NB, b_q + 8 * i);
+                            }
+                            __syncwarp();
+                            qph ^= 1u << i;
+                            q_out |= 1u << i;
+                        }
+                    }
+                if constexpr (Cf::PS) {  // V follows the next key tile's K
+                    if (j > 0) put(NP, v_live, v_page, v_slot);
+                    v_live = live;
+                    v_page = page;
+                    v_slot = slot;
+                    if (j + 1 == nk) put(NP, live, page, slot);
+                } else {
+                    for (int kv = NP; kv < 2 * NP; ++kv) put(kv, live, page, slot);
                 }
                 if (lane == 0) *progress = issued;
                 if (ok && j + 1 == nk) {  // the ring is full: time to find the next item
@@ -457,10 +477,10 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         const bool leader = tc::elect_one();
         const uint32_t id_s = tc::idesc_16(128, KT, BF, false), id_o = tc::idesc_16(128, D, BF, true);
         const uint32_t q0 = tc::desc_sw128(sb + Cf::OffQ, 16), k0 = tc::desc_sw128(sb + Cf::OffRing, 16);
-        const uint32_t v0 = tc::desc_sw128(sb + Cf::OffRing, Cf::KBlk);
+        const uint32_t v0 = tc::desc_sw128(sb + Cf::OffRing, Cf::KBlk), p0 = tc::desc_sw128(sb + Cf::OffP, 16);
         int st = 0;  // the ring: key tile j's K parts, then its V parts
         uint32_t ph = 0;
-        uint32_t qph = 0, pph = 0, oph = ~0u;  // bit i: phases of tile i's Q, P and free O
+        uint32_t qph = 0, pph = 0, oph = ~0u, rph = ~0u;  // bit i: phases of tile i's Q, P, free O and read S
         auto next = [&]() {
             if (++st == NS) {
                 st = 0;
@@ -519,24 +539,41 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 }
                 __syncwarp();
             };
+            auto s_read = [&](int i) {  // the tile's S before has been read
+                if constexpr (Cf::PS) {
+                    ok = ok && wait(b_sr + 8 * i, (rph >> i) & 1u);
+                    rph ^= 1u << i;
+                }
+            };
             ok = landed(st, ph);
             for (int i = w; ok && i < nt; i += 2) {
                 ok = wait(b_q + 8 * i, (qph >> i) & 1u);
                 qph ^= 1u << i;
+                s_read(i);
                 tc::fence_after_sync();
                 if (ok) scores(i, st, nk == 1);
             }
             for (int y = 0; y < NP; ++y) next();
             for (int j = 0; ok && j < nk; ++j) {
+                if constexpr (Cf::PS)
+                    if (j + 1 < nk) {  // the next scores, as soon as S has been read
+                        ok = landed(st, ph);
+                        s_read(w);
+                        tc::fence_after_sync();
+                        if (ok) scores(w, st, j + 2 == nk);
+                        next();
+                    }
                 const int sv = st;  // V's stages
                 const uint32_t phv = ph;
                 for (int y = 0; y < NP; ++y) next();
                 const int sk = st;  // the next K's
                 const uint32_t phk = ph;
-                ok = landed(sv, phv);
+                ok = ok && landed(sv, phv);
                 if (j + 1 < nk) {
-                    for (int y = 0; y < NP; ++y) next();
-                    ok = ok && landed(sk, phk);
+                    if constexpr (!Cf::PS) {
+                        for (int y = 0; y < NP; ++y) next();
+                        ok = ok && landed(sk, phk);
+                    }
                 } else if (ok && tail < KT) {
                     // V rows behind the last position: zeros, whatever the page holds
                     // (each MMA warp writes them: nobody waits)
@@ -571,14 +608,21 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             for (int x = NP - 1 - y; x >= 0; --x)  // P's part x by V's part y
 #pragma unroll
                                 for (int ks = 0; ks < KT / 16; ++ks)
-                                    tc::mma_ta_sw128(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint32_t)((ks * 2048) >> 4),
+                                    if constexpr (Cf::PS)
+                                        tc::mma_sw128(to,
+                                                      p0 + (uint32_t)((i * Cf::PTile + (ks / 4) * kPfBlk + (ks % 4) * 32) >> 4),
+                                                      vd + (uint32_t)((ks * 2048) >> 4), id_o, !(fresh && ks == 0));
+                                    else
+                                        tc::mma_ta_sw128(to, tp + Cf::p_col(ks) + 16 * x, vd + (uint32_t)((ks * 2048) >> 4),
                                                      id_o, !(fresh && y == NP - 1 && x == 0 && ks == 0));
                             if (y == 0 && j + 1 == nk) tc::commit(b_o + 8 * i);
+                            if (Cf::PS) tc::commit(b_pe + 8 * i);
                             if (i == last) release(at);
                         }
                     }
                     __syncwarp();
-                    if (j + 1 < nk) scores(i, sk, j + 2 == nk);
+                    if constexpr (!Cf::PS)
+                        if (j + 1 < nk) scores(i, sk, j + 2 == nk);
                 }
             }
         }
@@ -624,7 +668,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         constexpr int QO = D / (16 * HF);  // 16-column parts of O
         const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
         float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
-        uint32_t sph = 0, oph = 0, xph = 0;  // phases of S, O and the exchange
+        uint32_t sph = 0, oph = 0, xph = 0, uph = 1;  // phases of S, O, the exchange and the used P
         // a row's value of the other column half: its warp has read the one before
         // by the time it is written again (S of the next key tile comes after every
         // warp's P)
@@ -715,6 +759,20 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                     top = fmaxf(top, other(top, ok));
                     if (!ok) break;
                 }
+                bool used = !Cf::PS;  // the product before this key tile's is complete
+                auto wait_used = [&]() {
+                    if (!used) {
+                        ok = wait(b_pe + 8 * i, uph);
+                        uph ^= 1u;
+                        tc::fence_after_sync();
+                        used = true;
+                    }
+                };
+                if constexpr (Cf::PS) {  // S (and the other half's maximum) has been read
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) pf_arrive(b_sr + 8 * i);
+                }
                 if (j == 0) {
                     m = top;
                 } else {
@@ -724,6 +782,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
                         l *= alpha;
                         m = mn;
+                        wait_used();
 #pragma unroll 1
                         for (int q = 0; q < QO; ++q) {
                             uint32_t o[16];
@@ -754,13 +813,24 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             s[32 * q + e] = pack2<M>(a - h.x, b - h.y);
                         }
                     }
-                    tc::st16(ts + (NP == 2 ? CW * hf + 32 * q : CW / 2 * hf + 16 * q), w);
+                    if constexpr (Cf::PS) {
+                        wait_used();
+                        uint8_t *dst = sm + Cf::OffP + i * Cf::PTile + hf * kPfBlk + r * 128;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            *reinterpret_cast<uint4 *>(dst + (((4 * q + x) ^ (r & 7)) << 4)) =
+                                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                    } else {
+                        tc::st16(ts + (NP == 2 ? CW * hf + 32 * q : CW / 2 * hf + 16 * q), w);
+                    }
                     if constexpr (NP == 2) tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
                 }
                 const uint64_t s2 = add_f32x2(sum[0], sum[1]);
                 l += lo_f32(s2) + hi_f32(s2);
+                if (!ok) break;
                 tc::wait_st();
                 tc::fence_before_sync();
+                if constexpr (Cf::PS) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) pf_arrive(b_p + 8 * i);
             }
