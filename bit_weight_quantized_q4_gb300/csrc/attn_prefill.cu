@@ -6,8 +6,9 @@
 // group shares every K and V tile -- and walks the key tiles of KT positions with
 // a running softmax:
 //   S = Q K^T          tcgen05.mma, 128 x KT fp32 in tensor memory
-//   P = 2^(c S - m)    64 columns a thread; P (16-bit) over S's columns
-//   O += P V           tcgen05.mma with P as the tensor-memory operand
+//   P = 2^(c S - m)    64 columns a thread; P (16-bit) over S's columns, or in
+//                      shared memory
+//   O += P V           tcgen05.mma
 // Q, K and V tiles come by tensor-map copies (TMA, 128-byte swizzle) straight
 // from the packed rows and the pages; V is the MN-major operand, so nothing is
 // transposed.  Up to sixteen softmax warps, two that issue MMAs, one that copies,
@@ -23,9 +24,10 @@
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
 // positions, P beside S and S a key tile ahead, and 277 with four of 64 (247 now:
 // 1110 TFLOP/s, the tensor core busy over 90 % of the loop).  At head size 128 (nine
-// ragged prompts, 93 GFLOP: 90 us, 1030 TFLOP/s) a key tile takes 3000 cycles of
-// which the tensor core works 1900: two row tiles fill the tensor memory, and the
-// softmax of one does not cover all of the other's.  fp32 (2048 rows: 74 us): three
+// ragged prompts, 93 GFLOP: 86 us, 1080 TFLOP/s) a key tile takes 2900 cycles of
+// which the tensor core works 1900: two row tiles fill the tensor memory, and their
+// softmax takes 2400 (the halves' maxima joined a key tile late, with bf16's
+// exponents, changed nothing: 87 us).  fp32 (2048 rows: 74 us): three
 // products each at 4500 cycles a key tile, 4300 of them tensor work, and about 17 us
 // to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8

@@ -357,6 +357,32 @@ def test_prefill_more_work_than_runs_at_once(q4, dtype, D):
     _prefill_case(q4, DTYPES[dtype], 16, 16, D, 16, [400, 90, 222], [0, 400, 7], 100, case_seed("work1", dtype, D))
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("step", [3.0, 60.0, 2000.0])
+def test_prefill_scores_that_grow_along_the_sequence(q4, dtype, D, step):
+    # the maximum grows by `step` (in units of the exponent) every 64 positions, so
+    # each key tile outweighs all before it; and by three steps in a descending one.
+    # Exact scores (powers of two and small integers), so the plain form's softmax
+    # decides the same: one tile counts, its 64 equal weights are 1/64 each
+    t, n = DTYPES[dtype], 520
+    for sign in (1.0, -1.0):
+        k = torch.zeros(1, 1, n, D)
+        k[0, 0, :, 0] = (torch.arange(n) // 64).float() * sign
+        v = torch.from_numpy(np.random.default_rng(7).standard_normal((1, 1, n, D)).astype(np.float32))
+        q = torch.zeros(n, 1, D)
+        q[:, 0, 0] = 1.0
+        k, v, q = k.to(t), v.to(t), q.to(t)
+        pages = q4.KVPages(k.cuda(), v.cuda(), I([[0]]))
+        out = f64(q4.q4_attn_prefill(q.cuda(), pages, I([0, n]), I([0]), scale=step))[:, 0]
+        q4.q4_device_check()
+        K, V = k[0, 0].double().numpy(), v[0, 0].double().numpy()
+        for p in (0, 1, 63, 64, 65, 127, 128, 129, 200, 256, 300, 383, 384, 447, 448, 500, 519):
+            ref, bound = attend(q[p, 0].double().numpy(), K[:p + 1], V[:p + 1], step, None if t == torch.float32 else t)
+            eps = half_step(t)
+            check(out[p], ref, bound * (1 + eps) + eps * np.abs(ref) + 2.0 ** -25, "growing %g at %d" % (sign * step, p))
+
+
 def test_prefill_contiguous_cache_as_one_page(q4):
     _prefill_case(q4, torch.float32, 8, 2, 64, 333, [300], [33], 0, 46)
     _prefill_case(q4, torch.float16, 8, 2, 64, 201, [200], [1], 0, 47)
