@@ -24,10 +24,12 @@
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
 // positions, P beside S and S a key tile ahead, and 277 with four of 64 (247 now:
 // 1110 TFLOP/s, the tensor core busy over 90 % of the loop).  At head size 128 (nine
-// ragged prompts, 93 GFLOP: 86 us, 1080 TFLOP/s) a key tile takes 2900 cycles of
-// which the tensor core works 1900: two row tiles fill the tensor memory, and their
-// softmax takes 2400 (the halves' maxima joined a key tile late, with bf16's
-// exponents, changed nothing: 87 us).  fp32 (2048 rows: 74 us): three
+// ragged prompts, 93 GFLOP: 86 us, 1080 TFLOP/s) a key tile takes 2900 cycles, the
+// time in which shared memory moves what it has to at 128 bytes a cycle: 128 KB of
+// operands for the scores of two row tiles, 128 for their products, 64 of copies, 64
+// of weights written.  (P over its S spares 128 KB of that, but the next scores then
+// wait for the product: 89 us.  The halves' maxima joined a key tile late, with
+// bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 74 us): three
 // products each at 4500 cycles a key tile, 4300 of them tensor work, and about 17 us
 // to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
@@ -78,8 +80,7 @@ struct PfT<float> {
 template <int D, int Parts>
 struct PfCfg {
     static constexpr int KT = D == 64 && Parts == 1 ? 64 : 128;  // positions of a key tile
-    // warps that share a row, CW columns each (head size 128 with a warp a row and
-    // 168 registers: 98 us against 91 for nine ragged prompts)
+    // warps that share a row, CW columns each
     static constexpr int HF = KT / 64;
     static constexpr int CW = KT / HF;
     static constexpr int NT = KT == 64 ? 4 : D * Parts == 256 ? 1 : 2;  // row tiles of a CTA at most
