@@ -742,11 +742,11 @@ def _launch(device, fn, *args):
     """Call `fn` with the raw handle of the current stream of the tensors'
     device appended, that device being current (it need not be the caller's)."""
     torch = _torch()
-    index = device.index
-    if torch.cuda.current_device() == index:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    index, c = device.index, torch._C
+    if c._cuda_getDevice() == index:
+        return fn(*args, c._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        return fn(*args, c._cuda_getCurrentRawStream(index))
 
 
 def _ptr(t, name, dtype, shape, device):
