@@ -567,6 +567,48 @@ def test_two_streams_with_a_workspace_each(q4):
         assert torch.equal(o, wants[i % 2])
 
 
+def test_prompts_on_two_streams_and_replayed(q4):
+    # two prompts, each more work than runs at once, on two streams at the same time
+    # and replayed from a graph while the other runs: the bits of each alone
+    cases = []
+    for seed, t, D, rows in ((1, torch.float16, 64, [1500, 700]), (2, torch.bfloat16, 128, [900, 1100])):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        n, H, Hkv, page = sum(rows), 32, 8, 64
+        width = -(-max(rows) // page)
+        k, v = (torch.randn(2 * width, Hkv, page, D, device="cuda", generator=g).to(t) for _ in range(2))
+        pages = q4.KVPages(k, v, I(np.arange(2 * width).reshape(2, width).tolist()))
+        q = torch.randn(n, H, D, device="cuda", generator=g).to(t)
+        cases.append((q, pages, I([0, rows[0], n])))
+    alone = [q4.q4_attn_prefill(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.empty_like(x) for x in alone]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for c, s, o in zip(cases, streams, outs):
+            with torch.cuda.stream(s):
+                o.zero_()
+                q4.q4_attn_prefill(*c, out=o)
+    torch.cuda.synchronize()
+    for x, o in zip(alone, outs):
+        assert torch.equal(x, o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            q4.q4_attn_prefill(*cases[0], out=outs[0])
+    outs[0].zero_()
+    outs[1].zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            q4.q4_attn_prefill(*cases[1], out=outs[1])
+    torch.cuda.synchronize()
+    for x, o in zip(alone, outs):
+        assert torch.equal(x, o)
+    q4.q4_device_check()
+
+
 @pytest.mark.parametrize("dtype", list(DTYPES))
 def test_request_prompt_then_tokens(q4, dtype):
     """Two requests through quantised projections: the prompts at once (q4_gemm,
