@@ -786,6 +786,9 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         l *= alpha;
                         m = mn;
                         wait_used();
+                        // the sum's columns were stored above: a load is not ordered after
+                        // a store of the same columns until the store's wait
+                        if constexpr (NP == 2) tc::wait_st();
 #pragma unroll 1
                         for (int q = 0; q < QO; ++q) {
                             uint32_t o[16];

@@ -698,3 +698,39 @@ def test_device_refusals(q4):
         q4.q4_kv_append(f(3, 2, 64), f(3, 2, 64), dev, I([0, 3]), q_out=h(3, 4, 64))
     with pytest.raises(TypeError):
         q4.KVPages(torch.zeros((1, 1, 16, 64), dtype=torch.int8, device="cuda"), f(1, 1, 16, 64), I([[0]]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("step", [6.0, 40.0])
+def test_prefill_sums_rescaled_in_every_key_tile(q4, D, step):
+    # fp32: each key tile's product is added to the sum beside it, and the maximum
+    # grows by `step` (log units; e^6 > 2^8) a key tile of 128, so that sum is rescaled
+    # right after it was stored, in every row tile of several sequences.  At step 6 the
+    # key tile before has a weight of 128 e^-6 = 0.3 in a key tile's first row and
+    # 0.0025 in its last, a hundred and five times the bound: a lost one shows
+    rng = np.random.default_rng(case_seed("rescaled", D, step))
+    H, Hkv, page, rows, starts = 4, 2, 64, [700, 300, 515], [0, 400, 5]
+    lens = [s + r for s, r in zip(starts, rows)]
+    pool = Pool(rng, lens, Hkv, page, D, torch.float32)
+    for b, n in enumerate(lens):
+        kv = rng.standard_normal((2, n, Hkv, D)).astype(np.float32)
+        kv[0] = 0.0
+        kv[0, :, :, 0] = (np.arange(n) // 128)[:, None]
+        pool.put(b, np.arange(n), *kv)
+    dev = pool.device(q4)
+    q = np.zeros((sum(rows), H, D), np.float32)
+    q[:, :, 0] = 1.0
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    outs = [q4.q4_attn_prefill(T(q), dev, I(cu), I(starts), scale=step) for _ in range(4)]
+    q4.q4_device_check()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    got = f64(outs[0])
+    for b, r in enumerate(rows):
+        K, V = (pool.get(x, b, np.arange(lens[b])) for x in (pool.k, pool.v))
+        for i in sorted({0, r - 1, *(x for e in range(128, 900, 128) for x in (e - 1 - starts[b], e - starts[b], e + 1 - starts[b])
+                                     if 0 <= x < r), *rng.integers(0, r, 20).tolist()}):
+            p = starts[b] + i
+            for h in range(H):
+                ref, bound = attend(q[cu[b] + i, h].astype(np.float64), K[:p + 1, h // 2], V[:p + 1, h // 2], step)
+                check(got[cu[b] + i, h], ref, bound + 2.0 ** -25, "rescaled b=%d p=%d h=%d" % (b, p, h))
