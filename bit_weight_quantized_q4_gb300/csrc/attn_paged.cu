@@ -130,7 +130,6 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *m, int
 __device__ __forceinline__ float f_of(const uint4 &v, int i) {
     return __uint_as_float(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w);
 }
-__device__ __forceinline__ uint32_t w_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // A warp's step and its ring.  A step takes MT tiles of 16 positions (two share
 // each Q fragment; one where two would leave no room to look ahead), so a unit

@@ -30,7 +30,7 @@
 // of weights written.  (P over its S spares 128 KB of that, but the next scores then
 // wait for the product: 89 us.  The halves' maxima joined a key tile late, with
 // bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 74 us): three
-// products each at 4500 cycles a key tile, 4300 of them tensor work, and about 17 us
+// products each at 4500 cycles a key tile, 4300 of them tensor work, and about 14 us
 // to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
 // (the sums stay exact: the reference maximum is the row's own, and its factor
@@ -53,11 +53,26 @@ namespace dev {
 
 constexpr int kPfBlk = 128 * 128;           // bytes of 128 rows x 64 16-bit values (a block of a Q tile)
 constexpr int kPfItems = 4;                 // work items of a CTA that are known and not done
+constexpr float kPfUsual = 0.0078125f;      // the usual factor back of a position of K or V, 2^-7
 constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that rescales O
 
 // What enters the products of a cache type: 16-bit values as they are (one
 // part); fp32 values as two f16 parts hi + lo (22 bits) after a power-of-two
-// scale, three products each (lo lo, of 2^-22, is left out).
+// scale, three products each (lo lo, of 2^-22, is left out).  The 16-bit types'
+// weights are rounded to the type too: a second part for them would be another P V,
+// half of the tensor work again, against an error of 1.3 times the output's own rounding.
+//
+// The scales of fp32: every row of Q and every position of K and of V has its own,
+// so that no value's bits depend on another's size -- another sequence's, a later
+// token's, or a stale one's.  A position's factors back (K's and V's, powers of two)
+// multiply its column of S, and its weight: a row's scaled weights are brought to
+// f16's range by one more power of two a key tile, found from their own largest, which
+// goes into the sum beside O.  That costs twice the time, so the scales of K and V
+// are steps of 2^12: a key tile whose positions have the same ones takes them as one
+// factor, and a call whose attended positions all have the usual one (rows whose
+// largest value is in [2^-5, 2^7), or zeros) never looks at them (2048 rows: 74 us; 89
+// where a position of the call has another one, 160 where every key tile mixes them).
+// A row's bits are the same by each way.
 template <typename T>
 struct PfT {
     using M = T;
@@ -103,19 +118,26 @@ struct PfCfg {
     // and 16 of lo per 32 positions)
     static constexpr int ColO = NT * KT, ColSum = ColO + NT * D;
     static constexpr int OffX = OffBar + 608 + (20 + 4 * 16) * kPfItems;  // values the column halves exchange [tile][half][row]
-    static constexpr int Smem = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
+    // fp32: the factors back of a key tile's positions (bf16, K's in the upper half),
+    // and the one that all share, if so; of as many key tiles as the ring can be ahead of
+    // the weights: the slot that a key tile's first copy waits for held V of the tile NF
+    // before, whose weights are written
+    static constexpr int NF = Parts == 2 ? (NS + 2 * Parts - 1) / (2 * Parts) : 0;
+    static constexpr int OffF = OffX + (HF == 2 ? NT * 2 * 128 * 4 : 0);
+    static constexpr int FacBytes = KT * 4 + 16;
+    static constexpr int OffWide = OffF + NF * FacBytes;  // fp32: whether factors are looked at at all
+    static constexpr int Smem = OffWide + (Parts == 2 ? 16 : 0);
+    static_assert(Parts == 1 || (NS % (2 * Parts) == 1 && HF == 2), "NF; the weights' exchange");
     static_assert(Smem <= (int)kSmemMax, "prefill shared memory");
     static_assert(ColO + NT * D * Parts <= 512, "tensor memory");
     static_assert(Soft <= 16, "a barrier of the exchange for each pair of warps; masks");
-    static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 + (PS ? 16 * NT : 0) <= 576, "barriers before the tensor-memory address");
+    static_assert(16 * NS + 48 * NT + 24 * kPfItems + 88 + (PS ? 16 * NT : 0) + 8 * NF <= 576, "barriers before the tensor-memory address");
     // P's column of 16 positions (step ks), part 0
     static constexpr int p_col(int ks) {
         return Parts == 1 ? 8 * ks : 64 * (ks / 4) + 32 * ((ks % 4) / 2) + 8 * (ks % 2);
     }
 };
 
-// The inverse of the power of two for a largest magnitude given as fp32 bits.
-__device__ __forceinline__ float pf_back(uint32_t bits);
 __device__ __forceinline__ void pf_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -245,14 +267,14 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
     // barriers.  Of the ring: a stage's copies have landed, both MMA warps are
     // done with it.  Of row tile i: Q has landed, Q is free, a key tile's S is
     // complete, its P is written, O is complete, O is free (P in shared memory: S has
-    // been read, P has been used).  Of the work items:
-    // slot's tile is known, every warp has read it, the answer to pf_ask_next.
+    // been read, P has been used).  Of the factors (fp32): a key tile's are written.  Of
+    // the work items: slot's tile is known, every warp has read it, the answer to pf_ask_next.
     const uint32_t bars = sb + Cf::OffBar;
     const uint32_t b_full = bars, b_empty = b_full + 8 * NS, b_q = b_empty + 8 * NS, b_qe = b_q + 8 * NT,
                    b_s = b_qe + 8 * NT, b_p = b_s + 8 * NT, b_o = b_p + 8 * NT, b_oe = b_o + 8 * NT,
                    b_known = b_oe + 8 * NT, b_read = b_known + 8 * kPfItems, b_mask = b_read + 8 * kPfItems,
                    b_next = b_mask + 8 * kPfItems, b_drain = b_next + 8, b_x = b_drain + 16,
-                   b_sr = b_x + 64, b_pe = b_sr + 8 * NT;
+                   b_sr = b_x + 64, b_pe = b_sr + 8 * NT, b_f = b_sr + (Cf::PS ? 16 * NT : 0);
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 576);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 580);
     volatile int *slow = reinterpret_cast<volatile int *>(sm + Cf::OffBar + 584);  // a row is being taken by the definition
@@ -282,6 +304,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             init(b_sr, NT, 4 * HF);
             init(b_pe, NT, 1);
         }
+        if constexpr (NP == 2) init(b_f, Cf::NF, 1);
         if (lane == 0) {
             *abort_flag = 0;
             *slow = 0;
@@ -298,10 +321,18 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         const PfTile t = pf_find(p, (int)blockIdx.x, row_tiles * TQ, lane);
         if (lane == 0) tile_s[0] = t;
     }
+    if (NP == 2 && warp == Cf::Rows) {  // a CTA of the staging met another factor than the usual one
+        uint32_t met = 0u;
+        for (int x = lane; x < p.nmet; x += 32) met |= __ldcg(p.met + x);
+        met = __reduce_or_sync(0xffffffffu, met);
+        if (lane == 0) *reinterpret_cast<uint32_t *>(sm + Cf::OffWide) = met;
+    }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t taddr = *tslot;
+    bool wide = false;
+    if constexpr (NP == 2) wide = *reinterpret_cast<const uint32_t *>(sm + Cf::OffWide) != 0u;
     if (tile_s[0].seq < 0) {  // no item of this number
         __syncthreads();
         if (warp == Cf::Mma) tc::tmem_dealloc(taddr, 512);
@@ -371,6 +402,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             return at;
         };
         int issued = 0, st = 0;  // ring tiles issued, the next one's stage
+        int n_tile = 0;          // key tiles
         uint32_t ph = 1;         // an empty slot's phase: the first pass finds them free
         uint32_t qph = ~0u, q_out = 0;  // bit i: the phase of tile i's free Q; Q copies issued and perhaps in flight
         PfTile t = tile_s[0];
@@ -389,6 +421,24 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             };
             int page1, slot1, v_live = 0, v_page = -1, v_slot = 0;
             lookup(0, page1, slot1);
+            // the factors of a key tile, four positions a lane (0 where nothing is attended)
+            auto factors = [&](int j) {
+                uint4 f = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (NP == 2) {
+                    const int box = 4 * lane / box_rows, left = key_end - (k_first + j * KT + 4 * lane);
+                    const int page = page_ok(p.kv, __shfl_sync(0xffffffffu, page1, box));
+                    const int slot = __shfl_sync(0xffffffffu, slot1, box) + 4 * lane - box * box_rows;
+                    if (page >= 0 && left > 0)
+                        f = __ldcg(reinterpret_cast<const uint4 *>(
+                            p.fac + ((size_t)page * p.kv.hkv + t.hk) * p.fac_stride + slot));
+                    if (left < 4) f.w = 0u;
+                    if (left < 3) f.z = 0u;
+                    if (left < 2) f.y = 0u;
+                }
+                return f;
+            };
+            uint4 fac = make_uint4(0u, 0u, 0u, 0u);
+            if (wide) fac = factors(0);
             for (int j = 0; ok && j < nk; ++j) {
                 const int page = page_ok(p.kv, page1), slot = slot1;
                 // a page out of range is copied as zeros (its coordinate is out of
@@ -404,6 +454,30 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 auto put = [&](int kv, int live, int page, int slot) {  // K's parts (kv < NP), V's parts
                     ok = ok && wait_go(b_empty + 8 * st, ph);
                     if (!ok) return;
+                    if constexpr (NP == 2)
+                        if (wide && kv == 0) {
+                            uint8_t *at = sm + Cf::OffF + (n_tile % Cf::NF) * Cf::FacBytes;
+                            *reinterpret_cast<uint4 *>(at + 16 * lane) = fac;
+                            // the largest and the smallest of each half (0, of a row of zeros, goes with any)
+                            uint32_t k1 = 0u, k0 = 0xffffu, v1 = 0u, v0 = 0xffffu;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t k = w_of(fac, x) >> 16, v = w_of(fac, x) & 0xffffu;
+                                k1 = max(k1, k);
+                                v1 = max(v1, v);
+                                k0 = min(k0, k ? k : 0xffffu);
+                                v0 = min(v0, v ? v : 0xffffu);
+                            }
+                            k1 = __reduce_max_sync(0xffffffffu, k1);
+                            v1 = __reduce_max_sync(0xffffffffu, v1);
+                            k0 = __reduce_min_sync(0xffffffffu, k0);
+                            v0 = __reduce_min_sync(0xffffffffu, v0);
+                            if (lane == 0)
+                                *reinterpret_cast<uint2 *>(at + 4 * KT) =
+                                    make_uint2(k1 << 16 | v1, (k1 == k0 || k1 == 0u) && (v1 == v0 || v1 == 0u));
+                            __syncwarp();
+                            if (lane == 0) pf_arrive(b_f + 8 * (n_tile % Cf::NF));
+                        }
                     if (lane == 0) mbar_expect_tx(b_full + 8 * st, (uint32_t)(live * box_rows) * 128u * NB);
                     __syncwarp();
                     if (bl < NB && r < live)
@@ -442,6 +516,8 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                     for (int kv = NP; kv < 2 * NP; ++kv) put(kv, live, page, slot);
                 }
                 if (lane == 0) *progress = issued;
+                ++n_tile;
+                if (wide && j + 1 < nk) fac = factors(j + 1);  // the lookup has come back by now
                 if (ok && j + 1 == nk) {  // the ring is full: time to find the next item
                     int at = answer();
                     if (at >= 0) next = pf_find(p, at, row_tiles * TQ, lane);
@@ -663,251 +739,482 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         if (!ok && lane == 0) fail();
     } else {
         // ------------------------------------------------------------ softmax
-        // tile i, columns 64 hf .. of every key tile, row r
-        const int i = (warp >> 2) / HF, hf = (warp >> 2) % HF, r = 32 * (warp & 3) + lane;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
-        const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of the O before
-        constexpr int QO = D / (16 * HF);  // 16-column parts of O
-        const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
-        float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
-        uint32_t sph = 0, oph = 0, xph = 0, uph = 1;  // phases of S, O, the exchange and the used P
-        // a row's value of the other column half: its warp has read the one before
-        // by the time it is written again (S of the next key tile comes after every
-        // warp's P)
-        auto other = [&](float mine, bool &ok) {
-            xs[hf * 128 + r] = mine;
-            __syncwarp();
-            if (lane == 0) pf_arrive(bx);
-            ok = wait(bx, xph);
-            xph ^= 1u;
-            return xs[(hf ^ 1) * 128 + r];
-        };
-        bool ok = true;
-        PfTile t;
-        for (int n = 0; ok; ++n) {
-            ok = tile_of(n, t);
-            if (!ok || t.seq < 0) break;
-            tile_read(n);
-            // rows that are not finite are left to the warp that takes them again
-            auto post = [&](unsigned rows) {
-                if (lane == 0) {
-                    mask_s[(n % kPfItems) * Cf::Soft + warp] = rows;
-                    pf_arrive(b_mask + 8 * (n % kPfItems));
-                }
-            };
-            if (i >= (t.tokens + TQ - 1) / TQ) {
-                post(0u);
-                continue;
-            }
-            int k_first, nk, tail;
-            keys_of(t, k_first, nk, tail);
-            const int tok = i * TQ + r / G, g = r % G;
-            const bool live = r < G * TQ && tok < t.tokens;
-            const int pos = t.pos0 + (live ? tok : min(i * TQ, t.tokens - 1));
-            const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
-            const int row = t.row0 + tok, head = t.hk * G + g;
-            float c = p.scale * 1.4426950408889634f;
-            if constexpr (NP == 2)  // the powers of two of Q's row and K back
-                c *= pf_back(p.maxima[t.hk]) * (live ? p.qback[(size_t)row * p.H + head] : 0.f);
-            float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < nk; ++j) {
-                ok = wait(b_s + 8 * i, sph);
-                sph ^= 1u;
-                if (!ok) break;
-                tc::fence_after_sync();
-                // fp32: the tensor core's accumulation truncates, which over a long chain
-                // of products shows (3e-6 of the output after 2048 positions, 8e-7 with
-                // two key tiles in a chain, 4e-7 so): each key tile's O is added to a
-                // sum beside it.  S came after the product before it: O is complete
-                if (NP == 2 && j > 0) {
-#pragma unroll 1
-                    for (int q = 0; q < D / (16 * HF); ++q) {
-                        uint32_t o[16], a[16];
-                        const uint32_t at = (D / HF) * hf + 16 * q;
-                        tc::ld16(to + at, o);
-                        if (j > 1) {
-                            tc::ld16(tsum + at, a);
-                            tc::wait_ld16(a);
-                        }
-                        tc::wait_ld16(o);
-                        if (j > 1)
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
-                        tc::st16(tsum + at, o);
-                    }
-                }
-                uint32_t s[CW];
-#pragma unroll
-                for (int q = 0; q < CW / 32; ++q) tc::ld32(ts + CW * hf + 32 * q, s + 32 * q);
-#pragma unroll
-                for (int q = 0; q < CW / 32; ++q) tc::wait_ld32(s + 32 * q);
-                const int k0 = k_first + j * KT;
-                if (k0 + KT - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
-                    const int hi = pos - k0 - CW * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - CW * hf : -1;
-#pragma unroll
-                    for (int e = 0; e < CW; ++e)
-                        if (e > hi || e < lo) s[e] = 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
-#pragma unroll
-                for (int e = 8; e < CW; e += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if constexpr (HF == 2) {
-                    top = fmaxf(top, other(top, ok));
-                    if (!ok) break;
-                }
-                bool used = !Cf::PS;  // the product before this key tile's is complete
-                auto wait_used = [&]() {
-                    if (!used) {
-                        ok = wait(b_pe + 8 * i, uph);
-                        uph ^= 1u;
-                        tc::fence_after_sync();
-                        used = true;
-                    }
-                };
-                if constexpr (Cf::PS) {  // S (and the other half's maximum) has been read
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) pf_arrive(b_sr + 8 * i);
-                }
-                if (j == 0) {
-                    m = top;
-                } else {
-                    const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
-                    if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
-                        const float mn = fmaxf(m, top);
-                        const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
-                        l *= alpha;
-                        m = mn;
-                        wait_used();
-                        // the sum's columns were stored above: a load is not ordered after
-                        // a store of the same columns until the store's wait
-                        if constexpr (NP == 2) tc::wait_st();
-#pragma unroll 1
-                        for (int q = 0; q < QO; ++q) {
-                            uint32_t o[16];
-                            const uint32_t at = (NP == 2 ? tsum : to) + 16 * q + (D / HF) * hf;
-                            tc::ld16(at, o);
-                            tc::wait_ld16(o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tc::st16(at, o);
-                        }
-                    }
-                }
-                const float mc = (m == -INFINITY ? 0.f : -m * c) + PfT<T>::PExp;
-                const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
-                uint64_t sum[2] = {0ull, 0ull};
-                // (over S's columns: the row's warps have read them)
-#pragma unroll
-                for (int q = 0; q < CW / 32; ++q) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint64_t x = fma_f32x2(pair_u32(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mc2);
-                        const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
-                        sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
-                        w[e] = pack2<M>(a, b);
-                        if constexpr (NP == 2) {  // what the high part leaves
-                            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-                            s[32 * q + e] = pack2<M>(a - h.x, b - h.y);
-                        }
-                    }
-                    if constexpr (Cf::PS) {
-                        wait_used();
-                        uint8_t *dst = sm + Cf::OffP + i * Cf::PTile + hf * kPfBlk + r * 128;
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            *reinterpret_cast<uint4 *>(dst + (((4 * q + x) ^ (r & 7)) << 4)) =
-                                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-                    } else {
-                        tc::st16(ts + (NP == 2 ? CW * hf + 32 * q : CW / 2 * hf + 16 * q), w);
-                    }
-                    if constexpr (NP == 2) tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
-                }
-                const uint64_t s2 = add_f32x2(sum[0], sum[1]);
-                l += lo_f32(s2) + hi_f32(s2);
-                if (!ok) break;
-                tc::wait_st();
-                tc::fence_before_sync();
-                if constexpr (Cf::PS) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        auto softmax = [&](auto wide_t) {
+            constexpr bool Wide = decltype(wide_t)::value;
+            // tile i, columns 64 hf .. of every key tile, row r
+            const int i = (warp >> 2) / HF, hf = (warp >> 2) % HF, r = 32 * (warp & 3) + lane;
+            const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+            const uint32_t ts = taddr + lanes + KT * i, to = taddr + lanes + Cf::ColO + D * i;
+            const uint32_t tsum = taddr + lanes + Cf::ColSum + D * i;  // fp32: the sum of the O before
+            constexpr int QO = D / (16 * HF);  // 16-column parts of O
+            const uint32_t bx = b_x + 8 * (4 * (i & 1) + (warp & 3));
+            float *xs = reinterpret_cast<float *>(sm + Cf::OffX) + 256 * i;  // [half][row]
+            uint32_t sph = 0, oph = 0, xph = 0, uph = 1;  // phases of S, O, the exchange and the used P
+            // a row's value of the other column half: its warp has read the one before
+            // by the time it is written again (S of the next key tile comes after every
+            // warp's P; where a key tile has several, a thread writes where it has itself
+            // read last)
+            int xw = hf;
+            auto other = [&](float mine, bool &ok) {
+                xs[xw * 128 + r] = mine;
                 __syncwarp();
-                if (lane == 0) pf_arrive(b_p + 8 * i);
-            }
-            ok = ok && wait(b_o + 8 * i, oph);
-            oph ^= 1u;
-            if (!ok) break;
-            tc::fence_after_sync();
-            uint32_t o[16 * QO];
-            float worst = 0.f;  // NaN where a value is not finite
-#pragma unroll
-            for (int q = 0; q < QO; ++q) {
-                tc::ld16(to + (D / HF) * hf + 16 * q, o + 16 * q);
-                if (NP == 2 && nk > 1) {
-                    uint32_t a[16];
-                    tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
-                    tc::wait_ld16(a);
-                    tc::wait_ld16(o + 16 * q);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        o[16 * q + e] = __float_as_uint(__uint_as_float(o[16 * q + e]) + __uint_as_float(a[e]));
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < QO; ++q) tc::wait_ld16(o + 16 * q);
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) pf_arrive(b_oe + 8 * i);  // the next item's product may begin
-#pragma unroll
-            for (int e = 0; e < 16 * QO; ++e) worst = fmaf(__uint_as_float(o[e]), 0.f, worst);
-            l += worst;
-            if constexpr (HF == 2) {
-                l += other(l, ok);
-                if (!ok) break;
-                __syncwarp();
-                if (lane == 0) pf_arrive(bx);  // read: may be written again
-            }
-            // (both halves' warps see the same l)
-            const bool finite = fabsf(l) < INFINITY;
-            float inv = l == 0.f ? 0.f : 1.f / l;
-            if constexpr (NP == 2) inv *= pf_back(p.maxima[p.kv.hkv + t.hk]);
-            // 128 bytes of a row at a time: eight lanes exchange theirs, so that a store
-            // fills whole lines (each lane its own row: 7000 cycles an item, not 2000)
-            const size_t at = ((size_t)row * p.H + head) * D + (D / HF) * hf;
-            const unsigned good = __ballot_sync(0xffffffffu, live && finite);
-#pragma unroll
-            for (int q = 0; q < D * (int)sizeof(T) / (128 * HF); ++q) {
-                uint32_t w[8][4];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    if constexpr (sizeof(T) == 4)
-                        w[e / 4][e % 4] = __float_as_uint(__uint_as_float(o[32 * q + e]) * inv);
-                    else
-                        w[e / 4][e % 4] = pack2<T>(__uint_as_float(o[64 * q + 2 * e]) * inv, __uint_as_float(o[64 * q + 2 * e + 1]) * inv);
-                }
-                pf_transpose8(w, lane);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const int src = (lane & 24) + x;
-                    const size_t a = __shfl_sync(0xffffffffu, at, src);
-                    if ((good >> src) & 1u)
-                        *reinterpret_cast<uint4 *>((uint8_t *)((T *)p.out + a) + 128 * q + 16 * (lane & 7)) =
-                            make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
-                }
-            }
-            post(__ballot_sync(0xffffffffu, live && hf == 0 && !finite));
-            if constexpr (HF == 2) {
+                if (lane == 0) pf_arrive(bx);
                 ok = wait(bx, xph);
                 xph ^= 1u;
+                const float got = xs[(xw ^ 1) * 128 + r];
+                if constexpr (Wide) xw ^= 1;
+                return got;
+            };
+            int n_tile = 0;  // Wide: key tiles of the items before
+            // 32 weights as two f16 parts: the high ones in w, what those leave in place
+            auto parts = [](uint32_t *x, uint32_t (&w)[16]) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float a = __uint_as_float(x[2 * e]), b = __uint_as_float(x[2 * e + 1]);
+                    w[e] = pack2<M>(a, b);
+                    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                    x[e] = pack2<M>(a - h.x, b - h.y);
+                }
+            };
+            bool ok = true;
+            PfTile t;
+            for (int n = 0; ok; ++n) {
+                ok = tile_of(n, t);
+                if (!ok || t.seq < 0) break;
+                tile_read(n);
+                // rows that are not finite are left to the warp that takes them again
+                auto post = [&](unsigned rows) {
+                    if (lane == 0) {
+                        mask_s[(n % kPfItems) * Cf::Soft + warp] = rows;
+                        pf_arrive(b_mask + 8 * (n % kPfItems));
+                    }
+                };
+                int k_first, nk, tail, f_tile = 0;
+                if constexpr (Wide) {
+                    keys_of(t, k_first, nk, tail);
+                    f_tile = n_tile;
+                    n_tile += nk;
+                }
+                if (i >= (t.tokens + TQ - 1) / TQ) {
+                    post(0u);
+                    continue;
+                }
+                if constexpr (!Wide) keys_of(t, k_first, nk, tail);
+                const int tok = i * TQ + r / G, g = r % G;
+                const bool live = r < G * TQ && tok < t.tokens;
+                const int pos = t.pos0 + (live ? tok : min(i * TQ, t.tokens - 1));
+                const int pmin = t.pos0 + i * TQ, pmax = t.pos0 + min((i + 1) * TQ, t.tokens) - 1;
+                const int row = t.row0 + tok, head = t.hk * G + g;
+                // what brings S to log2 units: in the exponential's own product (c), fp32 when
+                // S is read (cq, with K's factor)
+                const float c = NP == 2 ? 1.f : p.scale * 1.4426950408889634f;
+                float cq = 1.f;
+                if constexpr (NP == 2)
+                    cq = p.scale * 1.4426950408889634f * (Wide ? 1.f : kPfUsual) * (live ? p.qback[(size_t)row * p.H + head] : 0.f);
+                float m = -INFINITY, l = 0.f;
+                float back = 1.f;  // Wide: what the last key tile's O is in the sum's units
+                for (int j = 0; j < nk; ++j) {
+                    ok = wait(b_s + 8 * i, sph);
+                    sph ^= 1u;
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    // fp32: the tensor core's accumulation truncates, which over a long chain
+                    // of products shows (3e-6 of the output after 2048 positions, 8e-7 with
+                    // two key tiles in a chain, 4e-7 so): each key tile's O is added to a
+                    // sum beside it.  S came after the product before it: O is complete
+                    if (NP == 2 && j > 0) {
+#pragma unroll 1
+                        for (int q = 0; q < D / (16 * HF); ++q) {
+                            uint32_t o[16], a[16];
+                            const uint32_t at = (D / HF) * hf + 16 * q;
+                            tc::ld16(to + at, o);
+                            if (j > 1) {
+                                tc::ld16(tsum + at, a);
+                                tc::wait_ld16(a);
+                            }
+                            tc::wait_ld16(o);
+                            if constexpr (Wide) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), back, j > 1 ? __uint_as_float(a[e]) : 0.f));
+                            } else if (j > 1) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+                            }
+                            tc::st16(tsum + at, o);
+                        }
+                    }
+                    if constexpr (Wide) {
+                        const int k0 = k_first + j * KT;
+                        const bool masked = k0 + KT - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window);
+                        const int hi = pos - k0 - CW * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - CW * hf : -1;
+                        // the positions' factors, and whether all have the same
+                        const int at = f_tile + j;
+                        ok = wait(b_f + 8 * (at % Cf::NF), (uint32_t)(at / Cf::NF) & 1u);
+                        if (!ok) break;
+                        const uint32_t f0 = Cf::OffF + (at % Cf::NF) * Cf::FacBytes, fac = sb + f0 + CW * 4 * hf;
+                        const uint2 same = *reinterpret_cast<const uint2 *>(sm + f0 + 4 * KT);
+                        // each position with its own factor: the scores of 32 columns from q on,
+                        // in log2 units (read again in every pass over them: registers for all of
+                        // them beside the other path's were not to be had)
+                        auto own_scores = [&](int q, uint32_t (&x)[32]) {
+                            tc::ld32(ts + CW * hf + q, x);
+                            tc::wait_ld32(x);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const uint4 f = lds128_at<0>(fac + 4 * (q + e));
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    x[e + y] = __float_as_uint(__uint_as_float(x[e + y]) * (__uint_as_float(w_of(f, y) & 0xffff0000u) * cq));
+                                    if (masked && (q + e + y > hi || q + e + y < lo)) x[e + y] = 0xff800000u;
+                                }
+                            }
+                        };
+                        uint64_t sum[2] = {0ull, 0ull}, mc2 = 0ull;
+                        float top = -INFINITY, mc = 0.f;
+                        // the row's maximum with this key tile's, and the sums so far to it
+                        auto raise = [&]() {
+                            top = fmaxf(top, other(top, ok));
+                            if (!ok) return;
+                            if (j == 0) {
+                                m = top;
+                            } else {
+                                const bool grew = top > m && (m == -INFINITY || top - m > kPfGrow);
+                                if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
+                                    const float mn = grew ? fmaxf(m, top) : m;
+                                    const float alpha = m == -INFINITY ? 0.f : ex2(m - mn);
+                                    l *= alpha;
+                                    m = mn;
+                                    tc::wait_st();  // the sum's columns were stored above
+#pragma unroll 1
+                                    for (int q = 0; q < QO; ++q) {
+                                        uint32_t o[16];
+                                        const uint32_t at = tsum + 16 * q + (D / HF) * hf;
+                                        tc::ld16(at, o);
+                                        tc::wait_ld16(o);
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                        tc::st16(at, o);
+                                    }
+                                }
+                            }
+                            mc = (m == -INFINITY ? 0.f : -m) + PfT<T>::PExp;
+                            mc2 = pair_f32(mc, mc);
+                        };
+                        if (same.y != 0u) {
+                            uint32_t s[CW];
+#pragma unroll
+                            for (int q = 0; q < CW / 32; ++q) tc::ld32(ts + CW * hf + 32 * q, s + 32 * q);
+#pragma unroll
+                            for (int q = 0; q < CW / 32; ++q) tc::wait_ld32(s + 32 * q);
+                            const float cs = cq * __uint_as_float(same.x & 0xffff0000u);
+                            const uint64_t cs2 = pair_f32(cs, cs);
+#pragma unroll
+                            for (int e = 0; e < CW; e += 2) {
+                                const uint64_t y = mul_f32x2(pair_u32(s[e], s[e + 1]), cs2);
+                                s[e] = (uint32_t)y;
+                                s[e + 1] = (uint32_t)(y >> 32);
+                            }
+                            if (masked) {
+#pragma unroll
+                                for (int e = 0; e < CW; ++e)
+                                    if (e > hi || e < lo) s[e] = 0xff800000u;
+                            }
+                            float mx[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
+#pragma unroll
+                            for (int e = 8; e < CW; e += 8)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
+                            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                            raise();
+                            if (!ok) break;
+                            back = __uint_as_float(same.x << 16);
+#pragma unroll
+                        for (int e = 0; e < CW; e += 2) {
+                            const uint64_t x = add_f32x2(pair_u32(s[e], s[e + 1]), mc2);
+                            const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
+                            sum[e / 2 & 1] = add_f32x2(sum[e / 2 & 1], pair_f32(a, b));
+                            s[e] = __float_as_uint(a);
+                            s[e + 1] = __float_as_uint(b);
+                        }
+#pragma unroll
+                        for (int q = 0; q < CW / 32; ++q) {
+                            uint32_t w[16];
+                            parts(s + 32 * q, w);
+                            tc::st16(ts + CW * hf + 32 * q, w);
+                            tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
+                        }
+                    } else {
+#pragma unroll 1
+                            for (int q = 0; q < CW; q += 32) {
+                                uint32_t x[32];
+                                own_scores(q, x);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(x[e]));
+                            }
+                            raise();
+                            if (!ok) break;
+                            // the largest of the attended factors of V, of the weights of values that
+                            // are not zero, and of their products
+                            float big = 0.f, big_v = 0.f, big_w = 0.f;
+#pragma unroll 1
+                            for (int q = 0; q < CW; q += 32) {
+                                uint32_t x[32];
+                                own_scores(q, x);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    float v;
+                                    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(fac + 4 * (q + e)) : "memory");
+                                    v = __uint_as_float(__float_as_uint(v) << 16);
+                                    if (__uint_as_float(x[e]) > -INFINITY && v > 0.f) {
+                                        const float w = ex2(__uint_as_float(x[e]) + mc);
+                                        big = fmaxf(big, w * v);
+                                        big_v = fmaxf(big_v, v);
+                                        big_w = fmaxf(big_w, w);
+                                    }
+                                }
+                            }
+                            big = fmaxf(big, other(big, ok));
+                            if (!ok) break;
+                            big_v = fmaxf(big_v, other(big_v, ok));
+                            if (!ok) break;
+                            big_w = fmaxf(big_w, other(big_w, ok));
+                            if (!ok) break;
+                            // The largest factor becomes the one of all, as long as the largest
+                            // product is within 2^6 of that weight at it (it is when the attended
+                            // factors are the same: the bits are then those of a key tile with one);
+                            // else the largest product goes to [2^13, 2^14).  Powers of two, back and
+                            // forth below 2^127
+                            const uint32_t e_big = __float_as_uint(big) >> 23, e_v = __float_as_uint(big_v) >> 23;
+                            const uint32_t ex = min(big < big_w * big_v * 0.015625f ? 267u - e_big : 254u - e_v, 253u);
+                            const float up = __uint_as_float(ex << 23);
+                            back = __uint_as_float((254u - ex) << 23);
+#pragma unroll 1
+                            for (int q = 0; q < CW; q += 32) {
+                                uint32_t x[32], w[16];
+                                own_scores(q, x);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    float v0, v1;
+                                    asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v0), "=f"(v1) : "r"(fac + 4 * (q + 2 * e)) : "memory");
+                                    const uint64_t y = add_f32x2(pair_u32(x[2 * e], x[2 * e + 1]), mc2);
+                                    const float a = ex2(lo_f32(y)), b = ex2(hi_f32(y));
+                                    sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
+                                    x[2 * e] = __float_as_uint(a * (__uint_as_float(__float_as_uint(v0) << 16) * up));
+                                x[2 * e + 1] = __float_as_uint(b * (__uint_as_float(__float_as_uint(v1) << 16) * up));
+                            }
+                            parts(x, w);
+                            tc::st16(ts + CW * hf + q, w);
+                                tc::st16(ts + CW * hf + q + 16, x);
+                            }
+                        }
+                        const uint64_t s2 = add_f32x2(sum[0], sum[1]);
+                        l += lo_f32(s2) + hi_f32(s2);
+                    } else {
+                        uint32_t s[CW];
+#pragma unroll
+                        for (int q = 0; q < CW / 32; ++q) tc::ld32(ts + CW * hf + 32 * q, s + 32 * q);
+#pragma unroll
+                        for (int q = 0; q < CW / 32; ++q) tc::wait_ld32(s + 32 * q);
+                        if constexpr (NP == 2) {
+                            const uint64_t cq2 = pair_f32(cq, cq);
+#pragma unroll
+                            for (int e = 0; e < CW; e += 2) {
+                                const uint64_t y = mul_f32x2(pair_u32(s[e], s[e + 1]), cq2);
+                                s[e] = (uint32_t)y;
+                                s[e + 1] = (uint32_t)(y >> 32);
+                            }
+                        }
+                        const int k0 = k_first + j * KT;
+                        if (k0 + KT - 1 > pmin || (p.window > 0 && k0 <= pmax - p.window)) {
+                            const int hi = pos - k0 - CW * hf, lo = p.window > 0 ? pos - p.window + 1 - k0 - CW * hf : -1;
+#pragma unroll
+                            for (int e = 0; e < CW; ++e)
+                                if (e > hi || e < lo) s[e] = 0xff800000u;
+                        }
+                        float mx[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(s[q]), __uint_as_float(s[4 + q]));
+#pragma unroll
+                        for (int e = 8; e < CW; e += 8)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[e + q])), __uint_as_float(s[e + 4 + q]));
+                        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        if constexpr (HF == 2) {
+                            top = fmaxf(top, other(top, ok));
+                            if (!ok) break;
+                        }
+                        bool used = !Cf::PS;  // the product before this key tile's is complete
+                        auto wait_used = [&]() {
+                            if (!used) {
+                                ok = wait(b_pe + 8 * i, uph);
+                                uph ^= 1u;
+                                tc::fence_after_sync();
+                                used = true;
+                            }
+                        };
+                        if constexpr (Cf::PS) {  // S (and the other half's maximum) has been read
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) pf_arrive(b_sr + 8 * i);
+                        }
+                        if (j == 0) {
+                            m = top;
+                        } else {
+                            const bool grew = top > m && (m == -INFINITY || (top - m) * c > kPfGrow);
+                            if (__any_sync(0xffffffffu, grew)) {  // the same answer in both halves' warps
+                                // (fp32: only the rows that grew, so that none follows its neighbours)
+                                const float mn = NP == 1 || grew ? fmaxf(m, top) : m;
+                                const float alpha = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+                                l *= alpha;
+                                m = mn;
+                                wait_used();
+                                // the sum's columns were stored above: a load is not ordered after
+                                // a store of the same columns until the store's wait
+                                if constexpr (NP == 2) tc::wait_st();
+#pragma unroll 1
+                                for (int q = 0; q < QO; ++q) {
+                                    uint32_t o[16];
+                                    const uint32_t at = (NP == 2 ? tsum : to) + 16 * q + (D / HF) * hf;
+                                    tc::ld16(at, o);
+                                    tc::wait_ld16(o);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tc::st16(at, o);
+                                }
+                            }
+                        }
+                        const float mc = (m == -INFINITY ? 0.f : -m * c) + PfT<T>::PExp;
+                        const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
+                        uint64_t sum[2] = {0ull, 0ull};
+                        if constexpr (NP == 2) {  // (all, then their parts: 75 us, pair by pair 81)
+#pragma unroll
+                            for (int e = 0; e < CW; e += 2) {
+                                const uint64_t x = add_f32x2(pair_u32(s[e], s[e + 1]), mc2);
+                                const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
+                                sum[e / 2 & 1] = add_f32x2(sum[e / 2 & 1], pair_f32(a, b));
+                                s[e] = __float_as_uint(a);
+                                s[e + 1] = __float_as_uint(b);
+                            }
+                        }
+                        // (over S's columns: the row's warps have read them)
+#pragma unroll
+                        for (int q = 0; q < CW / 32; ++q) {
+                            uint32_t w[16];
+                            if constexpr (NP == 2) {
+                                parts(s + 32 * q, w);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const uint64_t x = fma_f32x2(pair_u32(s[32 * q + 2 * e], s[32 * q + 2 * e + 1]), c2, mc2);
+                                    const float a = ex2(lo_f32(x)), b = ex2(hi_f32(x));
+                                    sum[e & 1] = add_f32x2(sum[e & 1], pair_f32(a, b));
+                                    w[e] = pack2<M>(a, b);
+                                }
+                            }
+                            if constexpr (Cf::PS) {
+                                wait_used();
+                                uint8_t *dst = sm + Cf::OffP + i * Cf::PTile + hf * kPfBlk + r * 128;
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    *reinterpret_cast<uint4 *>(dst + (((4 * q + x) ^ (r & 7)) << 4)) =
+                                        make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                            } else {
+                                tc::st16(ts + (NP == 2 ? CW * hf + 32 * q : CW / 2 * hf + 16 * q), w);
+                            }
+                            if constexpr (NP == 2) tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
+                        }
+                        const uint64_t s2 = add_f32x2(sum[0], sum[1]);
+                        l += lo_f32(s2) + hi_f32(s2);
+                    }
+                    if (!ok) break;
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                    if constexpr (Cf::PS) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) pf_arrive(b_p + 8 * i);
+                }
+                ok = ok && wait(b_o + 8 * i, oph);
+                oph ^= 1u;
+                if (!ok) break;
+                tc::fence_after_sync();
+                uint32_t o[16 * QO];
+                float worst = 0.f;  // NaN where a value is not finite
+#pragma unroll
+                for (int q = 0; q < QO; ++q) {
+                    tc::ld16(to + (D / HF) * hf + 16 * q, o + 16 * q);
+                    if (NP == 2 && nk > 1) {
+                        uint32_t a[16];
+                        tc::ld16(tsum + (D / HF) * hf + 16 * q, a);
+                        tc::wait_ld16(a);
+                        tc::wait_ld16(o + 16 * q);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[16 * q + e] = __float_as_uint(Wide ? fmaf(__uint_as_float(o[16 * q + e]), back, __uint_as_float(a[e]))
+                                                                 : __uint_as_float(o[16 * q + e]) + __uint_as_float(a[e]));
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < QO; ++q) tc::wait_ld16(o + 16 * q);
+                if (Wide && nk == 1)
+#pragma unroll
+                    for (int e = 0; e < 16 * QO; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) pf_arrive(b_oe + 8 * i);  // the next item's product may begin
+#pragma unroll
+                for (int e = 0; e < 16 * QO; ++e) worst = fmaf(__uint_as_float(o[e]), 0.f, worst);
+                l += worst;
+                if constexpr (HF == 2) {
+                    l += other(l, ok);
+                    if (!ok) break;
+                    __syncwarp();
+                    if (lane == 0) pf_arrive(bx);  // read: may be written again
+                }
+                // (both halves' warps see the same l)
+                const bool finite = fabsf(l) < INFINITY;
+                float inv = l == 0.f ? 0.f : 1.f / l;
+                if constexpr (NP == 2 && !Wide) inv *= kPfUsual;
+                // 128 bytes of a row at a time: eight lanes exchange theirs, so that a store
+                // fills whole lines (each lane its own row: 7000 cycles an item, not 2000)
+                const size_t at = ((size_t)row * p.H + head) * D + (D / HF) * hf;
+                const unsigned good = __ballot_sync(0xffffffffu, live && finite);
+#pragma unroll
+                for (int q = 0; q < D * (int)sizeof(T) / (128 * HF); ++q) {
+                    uint32_t w[8][4];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if constexpr (sizeof(T) == 4)
+                            w[e / 4][e % 4] = __float_as_uint(__uint_as_float(o[32 * q + e]) * inv);
+                        else
+                            w[e / 4][e % 4] = pack2<T>(__uint_as_float(o[64 * q + 2 * e]) * inv, __uint_as_float(o[64 * q + 2 * e + 1]) * inv);
+                    }
+                    pf_transpose8(w, lane);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int src = (lane & 24) + x;
+                        const size_t a = __shfl_sync(0xffffffffu, at, src);
+                        if ((good >> src) & 1u)
+                            *reinterpret_cast<uint4 *>((uint8_t *)((T *)p.out + a) + 128 * q + 16 * (lane & 7)) =
+                                make_uint4(w[x][0], w[x][1], w[x][2], w[x][3]);
+                    }
+                }
+                post(__ballot_sync(0xffffffffu, live && hf == 0 && !finite));
+                if constexpr (HF == 2) {
+                    ok = wait(bx, xph);
+                    xph ^= 1u;
+                }
             }
-        }
-        if (!ok && lane == 0) fail();
+            if (!ok && lane == 0) fail();
+        };
+        if (wide)
+            softmax(std::integral_constant<bool, NP == 2>());
+        else
+            softmax(std::false_type());
     }
     __syncwarp();
     tc::fence_before_sync();
@@ -919,37 +1226,36 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
 }
 
 // ---------------------------------------------------------------- fp32 caches
-// q4attn_prefill_scale_kernel finds the largest finite |k| and |v| of each kv
-// head over the positions the call attends, and writes Q's two f16 parts (a
-// power of two per row and head puts its largest value in [2^13, 2^14)) with
-// the factors back; q4attn_prefill_split_kernel then writes the attended
-// positions' K and V parts, scaled by their head's power of two, into images
-// laid out like the pages ([part][page][kv head][slot][D]), so that the tensor
-// maps of a 16-bit cache fit.  Shared pages get the same values from every
-// sequence.  Values 2^16 below their head's largest and more lose relative
-// precision (the parts' step is 2^-40 of the largest value).
+// q4attn_prefill_split_kernel writes the two f16 parts of Q's rows, and of the
+// attended positions' K and V into images laid out like the pages ([part][page]
+// [kv head][slot][D]), so that the tensor maps of a 16-bit cache fit.  A power of
+// two a row puts its largest finite value below 2^14 (of Q, per head, in [2^13,
+// 2^14); of K and V, per position and kv head, in steps of 2^12: in [2^2, 2^14)); its
+// inverses lie beside (Q's fp32; K's and V's as one word of bf16 halves, laid out like
+// the pages).  They follow from the row alone: pages that sequences share get the
+// same values from each.  A part's rounding is 2^-25 at least, so a value of K or V
+// enters with 22 bits or to 2^-27 of its row's largest.
 
 constexpr int kPfChunk = 64;  // positions of a staging item
 
-// The power of two for a largest magnitude given as fp32 bits, and its inverse.
-__device__ __forceinline__ int pf_exp(uint32_t bits) {
-    const float mx = __uint_as_float(bits);
+// The power of two for a largest magnitude.
+__device__ __forceinline__ int pf_exp(float mx) {
     if (!(mx > 0.f)) return 0;
     int e;
     frexpf(mx, &e);
-    return min(max(14 - e, -126), 126);
+    return min(14 - e, 126);  // at least -114
+}
+// The same in steps of 12: values of 2^-5 .. 2^7, a cache's usual ones, in one step
+__device__ __forceinline__ int pf_exp12(float mx) {
+    if (!(mx > 0.f)) return 0;
+    int e;
+    frexpf(mx, &e);
+    return min(7 - ((e + 4 + 156) / 12 - 13) * 12, 126);  // at least -125
 }
 
-__device__ __forceinline__ float pf_back(uint32_t bits) { return ldexpf(1.f, -pf_exp(bits)); }
-
-// A scaled value: finite ones stay finite (beyond f16's range only at positions
-// nothing attends, where a weight of 0 meets them)
-__device__ __forceinline__ float pf_scaled(float x, float f) {
-    return fabsf(x) < INFINITY ? fminf(fmaxf(x * f, -65504.f), 65504.f) : x;
-}
-// hi and lo parts of four scaled values
+// hi and lo parts of four values times f
 __device__ __forceinline__ void pf_split4(float4 v, float f, uint2 &hi, uint2 &lo) {
-    v = make_float4(pf_scaled(v.x, f), pf_scaled(v.y, f), pf_scaled(v.z, f), pf_scaled(v.w, f));
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
     hi = make_uint2(pack2<__half>(v.x, v.y), pack2<__half>(v.z, v.w));
     const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&hi.x));
     const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi.y));
@@ -1028,7 +1334,7 @@ template <int D>
 struct PfRows {
     static constexpr int L = D / 4, N = kPfChunk * L / 256;
     float4 k[N], v[N];
-    size_t off[N];
+    size_t off[N], place[N];  // element of (position, this thread's dims); of the position's factors
     unsigned ok = 0;
     __device__ __forceinline__ PfRows(const PrefillParams &p, int b, int hk, int at, int end) {
         const int tid = threadIdx.x;
@@ -1045,6 +1351,7 @@ struct PfRows {
             if (page[i] < 0) continue;
             ok |= 1u << i;
             off[i] = row_off(p.kv, page[i], hk, slot[i], D) + 4 * (tid % L);
+            place[i] = ((size_t)page[i] * p.kv.hkv + hk) * p.fac_stride + slot[i];
             k[i] = *reinterpret_cast<const float4 *>((const float *)p.kv.k + off[i]);
             v[i] = *reinterpret_cast<const float4 *>((const float *)p.kv.v + off[i]);
         }
@@ -1054,31 +1361,54 @@ __device__ __forceinline__ float finite_max(float m, float4 v) {
     return fmaxf(fmaxf(m, fmaxf(finite_abs(v.x), finite_abs(v.y))), fmaxf(finite_abs(v.z), finite_abs(v.w)));
 }
 
+// The largest of m[0 .. N) over the D / 4 lanes of a row.
+template <int D, int N>
+__device__ __forceinline__ void row_max(float (&m)[N]) {
+#pragma unroll
+    for (int o = D / 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(256, 2) q4attn_prefill_split_kernel(const __grid_constant__ PrefillParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int L = D / 4, U = 4;  // lanes of a row, rows of Q at once
-    const int tid = threadIdx.x, lane = tid & 31, j = 4 * (tid % L);
-    pf_items<1>(p, [&](int b, int hk, int at, int end) {
+    const int tid = threadIdx.x, j = 4 * (tid % L);
+    const size_t part = (size_t)p.kv.num_pages * p.kv.hkv * p.kv.page * D;
+    bool met = false;  // a factor that is not the usual one
+    pf_items<128>(p, [&](int b, int hk, int at, int end) {  // from a key tile's start
+        constexpr int N = PfRows<D>::N;
         const PfRows<D> x(p, b, hk, at, end);
-        float mk = 0.f, mv = 0.f;
+        float mk[N], mv[N];
 #pragma unroll
-        for (int i = 0; i < PfRows<D>::N; ++i) {
-            mk = finite_max(mk, x.k[i]);
-            mv = finite_max(mv, x.v[i]);
+        for (int i = 0; i < N; ++i) {
+            mk[i] = finite_max(0.f, x.k[i]);
+            mv[i] = finite_max(0.f, x.v[i]);
         }
+        row_max<D>(mk);
+        row_max<D>(mv);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-        }
-        if (lane == 0) {  // non-negative floats order like their bits
-            atomicMax(p.maxima + hk, __float_as_uint(mk));
-            atomicMax(p.maxima + p.kv.hkv + hk, __float_as_uint(mv));
+        for (int i = 0; i < N; ++i) {
+            if (((x.ok >> i) & 1u) == 0) continue;
+            const int ek = pf_exp12(mk[i]), ev = pf_exp12(mv[i]);
+            uint2 hi, lo;
+            pf_split4(x.k[i], ldexpf(1.f, ek), hi, lo);
+            *reinterpret_cast<uint2 *>(p.kimg + x.off[i]) = hi;
+            *reinterpret_cast<uint2 *>(p.kimg + part + x.off[i]) = lo;
+            pf_split4(x.v[i], ldexpf(1.f, ev), hi, lo);
+            *reinterpret_cast<uint2 *>(p.vimg + x.off[i]) = hi;
+            *reinterpret_cast<uint2 *>(p.vimg + part + x.off[i]) = lo;
+            // zeros: 0, so that their weight does not set the others' step
+            met = met || (mk[i] > 0.f && ek != 7) || (mv[i] > 0.f && ev != 7);
+            if (j == 0)
+                p.fac[x.place[i]] = (mk[i] > 0.f ? __float_as_uint(ldexpf(1.f, -ek)) : 0u) |
+                                    (mv[i] > 0.f ? __float_as_uint(ldexpf(1.f, -ev)) >> 16 : 0u);
         }
     });
-    const size_t units = (size_t)p.rows * p.H, part = units * D;
+    if (const int any = __syncthreads_or(met); tid == 0) p.met[blockIdx.x] = any;
+    const size_t units = (size_t)p.rows * p.H, qpart = units * D;
     for (size_t u0 = (size_t)blockIdx.x * (U * 256 / L); u0 < units; u0 += (size_t)gridDim.x * (U * 256 / L)) {
         float4 q[U];
         float m[U];
@@ -1090,56 +1420,36 @@ __global__ void __launch_bounds__(256) q4attn_prefill_scale_kernel(const __grid_
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) m[i] = finite_max(0.f, q[i]);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < U; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+        row_max<D>(m);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const size_t u = u0 + tid / L + i * (256 / L);
             if (u >= units) continue;
-            const int e = pf_exp(__float_as_uint(m[i]));
+            const int e = pf_exp(m[i]);
             uint2 hi, lo;
             pf_split4(q[i], ldexpf(1.f, e), hi, lo);
             *reinterpret_cast<uint2 *>(p.qimg + u * D + j) = hi;
-            *reinterpret_cast<uint2 *>(p.qimg + part + u * D + j) = lo;
+            *reinterpret_cast<uint2 *>(p.qimg + qpart + u * D + j) = lo;
             if (j == 0) p.qback[u] = ldexpf(1.f, -e);
         }
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) q4attn_prefill_split_kernel(const __grid_constant__ PrefillParams p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const size_t part = (size_t)p.kv.num_pages * p.kv.hkv * p.kv.page * D;
-    pf_items<128>(p, [&](int b, int hk, int at, int end) {  // from a key tile's start
-        const PfRows<D> x(p, b, hk, at, end);
-        const float fk = ldexpf(1.f, pf_exp(p.maxima[hk])), fv = ldexpf(1.f, pf_exp(p.maxima[p.kv.hkv + hk]));
-#pragma unroll
-        for (int i = 0; i < PfRows<D>::N; ++i) {
-            if (((x.ok >> i) & 1u) == 0) continue;
-            uint2 hi, lo;
-            pf_split4(x.k[i], fk, hi, lo);
-            *reinterpret_cast<uint2 *>(p.kimg + x.off[i]) = hi;
-            *reinterpret_cast<uint2 *>(p.kimg + part + x.off[i]) = lo;
-            pf_split4(x.v[i], fv, hi, lo);
-            *reinterpret_cast<uint2 *>(p.vimg + x.off[i]) = hi;
-            *reinterpret_cast<uint2 *>(p.vimg + part + x.off[i]) = lo;
-        }
-    });
-}
-
 }  // namespace dev
 
-// The fp32 form's workspace: the heads' maxima, Q's factors back and parts,
-// K's and V's parts.
+constexpr int kPfStaging = 1024;  // CTAs of the staging at most
+
+// The fp32 form's workspace: the staging CTAs' words, K's and V's factors back, Q's,
+// Q's parts, K's and V's.
 size_t prefill_workspace(PrefillParams &p, int num_pages, int page, uint8_t *ws) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     const size_t q = (size_t)p.rows * p.H, kv = (size_t)num_pages * p.kv.hkv * page * p.D;
     size_t at = 0;
-    p.maxima = (uint32_t *)(ws + at);
-    at += up(2 * sizeof(uint32_t) * p.kv.hkv);
+    p.met = (uint32_t *)(ws + at);
+    at += up(sizeof(uint32_t) * kPfStaging);
+    p.fac = (uint32_t *)(ws + at);
+    p.fac_stride = (page + 3) / 4 * 4;  // four positions a load
+    at += up(sizeof(uint32_t) * num_pages * p.kv.hkv * p.fac_stride);
     p.qback = (float *)(ws + at);
     at += up(q * sizeof(float));
     p.qimg = (uint16_t *)(ws + at);
@@ -1151,7 +1461,7 @@ size_t prefill_workspace(PrefillParams &p, int num_pages, int page, uint8_t *ws)
 }
 
 template <typename T, int D>
-static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
+static int launch_tc(PrefillParams p, int sms, cudaStream_t stream) {
     constexpr int NP = dev::PfT<T>::Parts;
     using Cf = dev::PfCfg<D, NP>;
     constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
@@ -1166,11 +1476,9 @@ static int launch_tc(const PrefillParams &p, int sms, cudaStream_t stream) {
         q = p.qimg;
         k = p.kimg;
         v = p.vimg;
-        if (cudaMemsetAsync(p.maxima, 0, 2 * sizeof(uint32_t) * p.kv.hkv, stream) != cudaSuccess) return -1;
-        cudaLaunchConfig_t cfg = pdl_config(4u * sms, 256, 0, stream, &attr);
-        if (cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_scale_kernel<D>, p) != cudaSuccess ||
-            cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_split_kernel<D>, p) != cudaSuccess)
-            return -1;
+        p.nmet = std::min(4 * sms, kPfStaging);
+        const cudaLaunchConfig_t cfg = pdl_config((unsigned)p.nmet, 256, 0, stream, &attr);
+        if (cudaLaunchKernelEx(&cfg, dev::q4attn_prefill_split_kernel<D>, p) != cudaSuccess) return -1;
     }
     CUtensorMap mq, mk, mv;
     const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)p.H, (cuuint64_t)p.rows, (cuuint64_t)NP};

@@ -97,6 +97,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Word i of four, i a constant after unrolling.
+__device__ __forceinline__ uint32_t w_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
 // Two fp32 values in one 64-bit register, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t pair_u32(uint32_t a, uint32_t b) {
     uint64_t r;

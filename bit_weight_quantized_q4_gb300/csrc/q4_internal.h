@@ -454,9 +454,13 @@ struct PrefillParams {
     int extra_tx;
     int rows, H, D, window;
     float scale;
-    // fp32 caches, in the workspace: largest |k| and |v| per kv head as bits
-    // [2][hkv], Q's factors back [rows][H], the f16 parts [2][...] of Q, K, V
-    uint32_t *maxima;
+    // fp32 caches, in the workspace: K's and V's factors back (a word of two bf16
+    // halves, K's the upper) [num_pages][hkv][fac_stride], Q's [rows][H], the f16
+    // parts [2][...] of Q, K, V
+    uint32_t *met;  // a word a staging CTA: it has met a factor that is not the usual one
+    int nmet;
+    uint32_t *fac;
+    int fac_stride;
     float *qback;
     uint16_t *qimg, *kimg, *vimg;
 };

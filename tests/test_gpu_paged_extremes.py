@@ -1,0 +1,150 @@
+"""GPU tests of the paged cache's attention at values of very different sizes: what one
+sequence, or a later token, holds must not reach another row's bits."""
+import numpy as np
+import pytest
+
+from paged_ref import attend, check
+from parity import case_seed
+from test_gpu_paged import I, T, f64, q4  # noqa: F401  (q4: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def _prefill(q4, k, v, table, q, cu, starts, **kw):  # noqa: F811
+    """k, v: float32 [pages][Hkv][page][D] arrays; also checks the error word."""
+    out = q4.q4_attn_prefill(T(q), q4.KVPages(T(k), T(v), I(table)), I(cu), I(starts), **kw)
+    q4.q4_device_check()
+    return out
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("big_k,big_v", [(2.0 ** 30, 2.0 ** 30), (1.0, 2.0 ** 45), (2.0 ** 60, 1.0), (2.0 ** -60, 2.0 ** -60)])
+def test_sequences_do_not_share_precision(q4, D, big_k, big_v):  # noqa: F811
+    # fp32: two sequences in one call, one with far larger (or smaller) values: the
+    # other's output is that of the sequence alone, bit for bit
+    rng = np.random.default_rng(case_seed("share", D, big_v))
+    H, Hkv, page, n = 8, 2, 32, [300, 300]
+    npg = 10
+    k, v = (rng.standard_normal((2 * npg, Hkv, page, D)).astype(np.float32) for _ in range(2))
+    k[:npg] *= big_k
+    v[:npg] *= big_v
+    q = rng.standard_normal((400, H, D)).astype(np.float32)
+    q[:200] /= big_k
+    table = np.arange(2 * npg).reshape(2, npg).tolist()
+    both = _prefill(q4, k, v, table, q, [0, 200, 400], [100, 100])
+    alone = _prefill(q4, k, v, table[1:], q[200:], [0, 200], [100])
+    assert torch.equal(both[200:], alone)
+    # and it is the formula's
+    ks, vs, got = (x.astype(np.float64) for x in (k, v, f64(both)))
+    for b in range(2):
+        K, V = (x[npg * b:npg * (b + 1)].transpose(0, 2, 1, 3).reshape(-1, Hkv, D) for x in (ks, vs))
+        for i in (0, 1, 27, 28, 29, 130, 199):
+            for h in (0, 3, 7):
+                p = 100 + i
+                ref, bound = attend(q[200 * b + i, h].astype(np.float64), K[:p + 1, h // 4], V[:p + 1, h // 4], D ** -0.5)
+                check(got[200 * b + i, h], ref, bound + 1e-38, "b=%d i=%d h=%d" % (b, i, h))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_pages_attended_to_different_lengths(q4, D):  # noqa: F811
+    # fp32: two sequences over the same pages, one reaching far larger values behind
+    # the other's end (in the same page): the shorter one's bits are its own
+    rng = np.random.default_rng(case_seed("lengths", D))
+    k, v = (rng.standard_normal((4, 1, 64, D)).astype(np.float32) for _ in range(2))
+    for x in (k, v):
+        x[2, 0, 10:] *= 2.0 ** 40
+    q = rng.standard_normal((90, 4, D)).astype(np.float32)
+    table = [[0, 1, 2, 3], [0, 1, 2, 3]]
+    both = _prefill(q4, k, v, table, q, [0, 40, 90], [98, 150])
+    alone = _prefill(q4, k, v, table[:1], q[:40], [0, 40], [98])
+    assert torch.equal(both[:40], alone)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 45, 2.0 ** -45])
+def test_rows_do_not_follow_later_tokens(q4, D, factor):  # noqa: F811
+    # fp32, one prompt: later positions (of the same key tiles, and of later ones)
+    # become far larger; no earlier row changes a bit
+    rng = np.random.default_rng(case_seed("later", D, factor))
+    rows, first = 330, 150
+    k, v = (rng.standard_normal((1, 2, 384, D)).astype(np.float32) for _ in range(2))
+    q = rng.standard_normal((rows, 4, D)).astype(np.float32)
+    outs = []
+    for f in (1.0, factor):
+        k2, v2 = k.copy(), v.copy()
+        k2[:, :, first:] *= f
+        v2[:, :, first:] *= f
+        outs.append(_prefill(q4, k2, v2, [[0]], q, [0, rows], [0]))
+    assert torch.equal(outs[0][:first], outs[1][:first])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ln_w,big", [(-30.0, 2.0 ** 40), (-60.0, 2.0 ** 80), (-60.0, 2.0 ** 90), (-20.0, 2.0 ** 60),
+                                      (0.0, 2.0 ** -60)])
+def test_large_values_of_small_weight(q4, D, ln_w, big):  # noqa: F811
+    # fp32: some positions' values are `big` times the others' at e^ln_w times their
+    # weight, in the same key tile and in another.  The values enter with 22 bits or to
+    # 2^-27 of their row's largest, R_j, which is scaled into [2^2, 2^14).  The weights
+    # times the rows' scales enter with 22 bits or to 2^-25 when the largest of them is
+    # 2^13: off by 2^-38 of it, by a value below 2^14, over a row's scale of R_j / 2^2 at
+    # most: 2^-26 of max_j w_j R_j a position
+    rng = np.random.default_rng(case_seed("small weight", D, ln_w, big))
+    n, at = 300, np.array([5, 70, 131, 250])
+    k = np.zeros((1, 1, n, D), np.float32)
+    k[0, 0, at, 0] = 1.0
+    v = rng.standard_normal((1, 1, n, D)).astype(np.float32)
+    v[0, 0, at] *= big
+    q = np.zeros((1, 1, D), np.float32)
+    q[0, 0, 0] = -1.0  # the scale is not negative
+    got = f64(_prefill(q4, k, v, [[0]], q, [0, 1], [n - 1], scale=abs(ln_w)))[0, 0]
+    K, V = k[0, 0].astype(np.float64), v[0, 0].astype(np.float64)
+    ref, bound = attend(q[0, 0].astype(np.float64), K, V, -ln_w)
+    s = -ln_w * (K @ q[0, 0])
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    rowmax = np.abs(V).max(1)
+    bound = bound + 3 * 2.0 ** -22 * (w @ np.abs(V)) + 2.0 ** -27 * (w @ rowmax) + n * 2.0 ** -26 * (w * rowmax).max()
+    check(got, ref, bound, "small weights")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("eq,ek,ev", [(100, -96, 0), (-108, 108, 96), (0, 0, -84), (-80, -84, 0), (100, -100, 0),
+                                      (-100, 100, 100), (0, 0, -90), (7, -5, 11)])
+def test_powers_of_two_change_nothing(q4, D, eq, ek, ev):  # noqa: F811
+    # fp32: q, k and v times powers of two.  Of q any, of k and v the scales' steps of
+    # 2^12: the same bits, scaled; others: the formula's.  (Scores that leave fp32's
+    # range at the bottom: the mean of the attended values.)
+    rng = np.random.default_rng(case_seed("powers", D))
+    rows, f = 140, [np.float32(2.0 ** e) for e in (eq, ek, ev)]
+    k, v = (rng.standard_normal((1, 1, rows, D)).astype(np.float32) for _ in range(2))
+    q = rng.standard_normal((rows, 2, D)).astype(np.float32)
+    gone = eq + ek < -140
+    got = _prefill(q4, k * f[1], v * f[2], [[0]], q * f[0], [0, rows], [0], scale=D ** -0.5 / (1.0 if gone else 2.0 ** (eq + ek)))
+    if ek % 12 == 0 and ev % 12 == 0:
+        want = _prefill(q4, k, v, [[0]], q, [0, rows], [0], scale=0.0 if gone else D ** -0.5)
+        assert torch.equal(want * float(f[2]), got)
+    K, V, got = k[0, 0].astype(np.float64), v[0, 0].astype(np.float64), f64(got) / float(f[2])
+    for i in range(0, rows, 3):
+        for h in range(2):
+            ref, bound = attend(q[i, h].astype(np.float64), K[:i + 1], V[:i + 1], 0.0 if gone else D ** -0.5)
+            check(got[i, h], ref, bound, "i=%d h=%d" % (i, h))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_of_zero_and_a_page_of_zeros(q4, D):  # noqa: F811
+    rng = np.random.default_rng(case_seed("zeros", D))
+    rows = 200
+    k, v = (rng.standard_normal((1, 1, rows, D)).astype(np.float32) for _ in range(2))
+    v[0, 0, :150:2] = 0.0
+    k[0, 0, 40:60] = 0.0
+    q = rng.standard_normal((rows, 2, D)).astype(np.float32)
+    q[7] = 0.0
+    got = f64(_prefill(q4, k, v, [[0]], q, [0, rows], [0]))
+    K, V = k[0, 0].astype(np.float64), v[0, 0].astype(np.float64)
+    for i in range(0, rows, 3):
+        for h in range(2):
+            ref, bound = attend(q[i, h].astype(np.float64), K[:i + 1], V[:i + 1], D ** -0.5)
+            check(got[i, h], ref, bound + 1e-30, "zeros %d" % i)
+    assert not f64(_prefill(q4, k, v * 0, [[0]], q, [0, rows], [0])).any()
