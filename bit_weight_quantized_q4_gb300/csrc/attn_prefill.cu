@@ -40,7 +40,8 @@
 // sequence's end are zeroed in shared memory.  A non-finite value at a position
 // that some rows of a tile see and others do not would still enter as 0 * NaN:
 // a row whose result is not finite is therefore taken again by the definition
-// (attn_row), which never touches what it does not attend.
+// (attn_row), which never touches what it does not attend; and so is one whose weights
+// are all zero.
 #include <algorithm>
 
 #include "attn_prefill_row.cuh"
@@ -1176,8 +1177,8 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                     if (lane == 0) pf_arrive(bx);  // read: may be written again
                 }
                 // (both halves' warps see the same l)
-                const bool finite = fabsf(l) < INFINITY;
-                float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool finite = l > 0.f && l < INFINITY;  // (0: every score is -inf)
+                float inv = 1.f / l;
                 if constexpr (NP == 2 && !Wide) inv *= kPfUsual;
                 // 128 bytes of a row at a time: eight lanes exchange theirs, so that a store
                 // fills whole lines (each lane its own row: 7000 cycles an item, not 2000)

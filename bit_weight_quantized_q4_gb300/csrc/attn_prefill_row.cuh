@@ -7,7 +7,8 @@ namespace q4 {
 namespace dev {
 
 // out = sum_j p_j v_j over j in (pos - window, pos], p = softmax of scale q . k_j;
-// lane l holds dims l, l + 32, ...; positions on pages out of range are skipped.
+// lane l holds dims l, l + 32, ...; positions on pages out of range are skipped (all
+// of them: zeros).  Scores that are all -inf are 0 / 0.
 template <typename T, int D>
 __device__ __noinline__ void attn_row(const PrefillParams &p, int row, int head, int seq, int pos, int lane) {
     constexpr int DL = D / 32;
@@ -22,6 +23,7 @@ __device__ __noinline__ void attn_row(const PrefillParams &p, int row, int head,
     float m = -INFINITY, l = 0.f;
     const int lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
     int page = -1, col = -1;
+    bool seen = false;
     for (int j = lo; j <= pos; ++j) {
         if (j / p.kv.page != col) {
             col = j / p.kv.page;
@@ -29,6 +31,7 @@ __device__ __noinline__ void attn_row(const PrefillParams &p, int row, int head,
             if (page < 0 && lane == 0) atomicExch(p.err, kErrPaged);
         }
         if (page < 0) continue;
+        seen = true;
         const size_t off = row_off(p.kv, page, hk, j - col * p.kv.page, D);
         float s = 0.f;
 #pragma unroll
@@ -44,7 +47,7 @@ __device__ __noinline__ void attn_row(const PrefillParams &p, int row, int head,
     }
     T *out = (T *)p.out + ((size_t)row * p.H + head) * D;
 #pragma unroll
-    for (int i = 0; i < DL; ++i) out[lane + 32 * i] = from_f32<T>(l == 0.f ? 0.f : acc[i] / l);
+    for (int i = 0; i < DL; ++i) out[lane + 32 * i] = from_f32<T>(seen ? acc[i] / l : 0.f);
 }
 
 }  // namespace dev

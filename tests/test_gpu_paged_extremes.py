@@ -1,11 +1,12 @@
 """GPU tests of the paged cache's attention at values of very different sizes: what one
-sequence, or a later token, holds must not reach another row's bits."""
+sequence, or a later token, holds must not reach another row's bits; and at infinities
+that are attended, which give what the formula gives."""
 import numpy as np
 import pytest
 
 from paged_ref import attend, check
 from parity import case_seed
-from test_gpu_paged import I, T, f64, q4  # noqa: F401  (q4: the fixture)
+from test_gpu_paged import DTYPES, I, T, f64, q4  # noqa: F401  (q4: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +149,80 @@ def test_values_of_zero_and_a_page_of_zeros(q4, D):  # noqa: F811
             ref, bound = attend(q[i, h].astype(np.float64), K[:i + 1], V[:i + 1], D ** -0.5)
             check(got[i, h], ref, bound + 1e-30, "zeros %d" % i)
     assert not f64(_prefill(q4, k, v * 0, [[0]], q, [0, rows], [0])).any()
+
+
+# ------------------------------------------------------------------ infinities
+
+def _formula(q, K, V, scale):
+    """The definition in 64 bits with IEEE rules: weights of +inf scores are NaN, of
+    -inf scores 0 (all of them -inf: NaN), an attended infinity is one."""
+    with np.errstate(all="ignore"):
+        s = scale * (K @ q)
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        return w @ V
+
+
+def _same(got, ref, tol, what):
+    """NaN and infinities where the formula has them, the rest within tol (below: scores
+    off by 2 (D + 16) 2^-24 A, A = scale sum |q k| < 8 for q of 0.5, so 2^-12 of the
+    values' scale, 1 here, covers it with the sums and the exponential)."""
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), what
+    inf = np.isinf(ref)
+    assert np.array_equal(got[inf], ref[inf]) and np.isfinite(got[~inf & ~np.isnan(ref)]).all(), what
+    fin = np.isfinite(ref)
+    assert (np.abs(got[fin] - ref[fin]) <= tol * (1 + np.abs(ref[fin]))).all(), what
+
+
+INF = float("inf")
+# (which of k and v, position from the end, dim, value)
+INFS = {"v": [("v", 3, 5, INF)], "v both": [("v", 3, 5, INF), ("v", 40, 6, -INF)],
+        "v cancels": [("v", 3, 5, INF), ("v", 2, 5, -INF)], "v nan": [("v", 7, 9, float("nan"))],
+        "k": [("k", 11, 2, INF)], "new": [("v", 0, 1, -INF)], "k new": [("k", 0, 1, INF)],
+        "far": [("v", 299, 63, INF), ("k", 290, 0, -INF)]}
+
+
+def _with_infs(rng, n, Hkv, D, t, infs):
+    """k, v [n][Hkv][D] in the cache's type, the infinities in kv head 1."""
+    k, v = (torch.from_numpy(rng.standard_normal((n, Hkv, D)).astype(np.float32)).to(t) for _ in range(2))
+    for which, back, dim, x in infs:
+        (k if which == "k" else v)[n - 1 - back, 1, dim] = x
+    return k, v
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("case", list(INFS))
+def test_prefill_attended_infinities(q4, dtype, D, case):  # noqa: F811
+    t, H, Hkv, n, rows = DTYPES[dtype], 6, 2, 300, 40
+    rng = np.random.default_rng(case_seed("inf prompt", dtype, D))
+    k, v = _with_infs(rng, n, Hkv, D, t, INFS[case])
+    q = torch.from_numpy((0.5 * rng.standard_normal((rows, H, D))).astype(np.float32)).to(t)
+    pages = q4.KVPages(*(x.transpose(0, 1)[None].contiguous().cuda() for x in (k, v)), I([[0]]))
+    got = f64(q4.q4_attn_prefill(q.cuda(), pages, I([0, rows]), I([n - rows])))
+    q4.q4_device_check()
+    K, V, Q = k.double().numpy(), v.double().numpy(), q.double().numpy()
+    for i in range(rows):
+        p = n - rows + i
+        for h in range(H):
+            ref = _formula(Q[i, h], K[:p + 1, h // 3], V[:p + 1, h // 3], D ** -0.5)
+            # three roundings of the 16-bit types (q is given): weights, output, and a margin of one
+            _same(got[i, h], ref, 2.0 ** -12 + 3 * float(torch.finfo(t).eps) / 2, "%s i=%d h=%d" % (case, i, h))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_scores_all_minus_infinity(q4, dtype, D):  # noqa: F811
+    # every attended key is -inf against a positive q: 0 / 0, as the formula has it (the
+    # other head's q is negative: +inf, NaN too); the other sequence is untouched
+    t = DTYPES[dtype]
+    k = torch.full((2, 1, 160, D), 0.25, dtype=t, device="cuda")
+    k[0, 0, :, 3] = -INF
+    pages = q4.KVPages(k, torch.ones_like(k), I([[0], [1]]))
+    q = torch.ones(40, 2, D, device="cuda", dtype=t)
+    q[:, 1] = -1.0
+    got = q4.q4_attn_prefill(q, pages, I([0, 20, 40]), I([100, 100])).float()
+    q4.q4_device_check()
+    # the others' values are ones: weights that add up to one, rounded once
+    assert torch.isnan(got[:20]).all()
+    assert float((got[20:] - 1).abs().max()) <= float(torch.finfo(t).eps) + 2.0 ** -17
