@@ -226,3 +226,33 @@ def test_prefill_scores_all_minus_infinity(q4, dtype, D):  # noqa: F811
     # the others' values are ones: weights that add up to one, rounded once
     assert torch.isnan(got[:20]).all()
     assert float((got[20:] - 1).abs().max()) <= float(torch.finfo(t).eps) + 2.0 ** -17
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_scale_zero_takes_the_same_path(q4, dtype, D):  # noqa: F811
+    # masked scores must not become -inf * 0: rows of NaN weights are taken one by one,
+    # a hundred times as long and more.  The values are multiples of 1/8, so their sums
+    # are exact, and the mean is off by its division and the output's rounding
+    t, rows = DTYPES[dtype], 1024
+    v = torch.from_numpy(np.random.default_rng(5).integers(-8, 9, (1, 2, rows, D)).astype(np.float32) / 8)
+    k = torch.from_numpy(np.random.default_rng(6).standard_normal((1, 2, rows, D)).astype(np.float32))
+    q = torch.from_numpy(np.random.default_rng(7).standard_normal((rows, 8, D)).astype(np.float32)).to(t).cuda()
+    pages = q4.KVPages(k.to(t).cuda(), v.to(t).cuda(), I([[0]]))
+    args, ws = (q, pages, I([0, rows]), I([0])), q4.q4_attn_prefill_workspace(pages, rows, 8)
+    out = torch.empty_like(q)
+    took = []
+    for scale in (None, 0.0):
+        q4.q4_attn_prefill(*args, scale=scale, out=out, workspace=ws)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(3):
+            q4.q4_attn_prefill(*args, scale=scale, out=out, workspace=ws)
+        b.record()
+        torch.cuda.synchronize()
+        took.append(a.elapsed_time(b))
+    assert took[1] < 10 * took[0], took
+    mean = v[0].double().cumsum(1) / torch.arange(1, rows + 1).double()[:, None]
+    got = out.double().cpu().view(rows, 2, 4, D).permute(1, 2, 0, 3)
+    err = (got - mean[:, None]).abs()
+    assert bool((err <= (2.0 ** -18 + float(torch.finfo(t).eps) / 2 * mean.abs()[:, None])).all()), float(err.max())
