@@ -45,7 +45,7 @@
 #include <algorithm>
 #include <limits>
 
-#include "attn_prefill_row.cuh"
+#include "attn_row.cuh"
 #include "gemv_launch.cuh"
 #include "tc_common.cuh"
 #include "tensor_map.h"

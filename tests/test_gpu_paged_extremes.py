@@ -256,3 +256,30 @@ def test_prefill_scale_zero_takes_the_same_path(q4, dtype, D):  # noqa: F811
     got = out.double().cpu().view(rows, 2, 4, D).permute(1, 2, 0, 3)
     err = (got - mean[:, None]).abs()
     assert bool((err <= (2.0 ** -18 + float(torch.finfo(t).eps) / 2 * mean.abs()[:, None])).all()), float(err.max())
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_of_nan_ends_soon(q4, dtype, D):  # noqa: F811
+    # a prompt whose q is NaN is NaN, and whose rows all are: each is taken by the
+    # definition, which must not walk on once its weights are NaN (75 ms against 0.04)
+    t, rows = DTYPES[dtype], 1024
+    k, v = (torch.randn(1, 2, rows, D, device="cuda").to(t) for _ in range(2))
+    q = torch.randn(rows, 8, D, device="cuda").to(t)
+    pages = q4.KVPages(k, v, I([[0]]))
+    ws = q4.q4_attn_prefill_workspace(pages, rows, 8)
+    took = []
+    for bad in (False, True):
+        if bad:
+            q[:, :, 3] = float("nan")
+        out = q4.q4_attn_prefill(q, pages, I([0, rows]), I([0]), workspace=ws)
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        cu, st = I([0, rows]), I([0])
+        a.record()
+        for _ in range(3):
+            q4.q4_attn_prefill(q, pages, cu, st, out=out, workspace=ws)
+        b.record()
+        torch.cuda.synchronize()
+        took.append(a.elapsed_time(b))
+        assert bool(torch.isnan(out).all()) == bad and bool(torch.isfinite(out).all()) != bad
+    assert took[1] < 200 * took[0], took
