@@ -24,7 +24,8 @@
 // Precision: q and p stay fp32-like.  f16 caches: q (scaled per head by a
 // power of two) and p enter as two f16 parts (22 bits); bf16 caches: as three
 // bf16 parts (24 bits); f32 caches: K and V as three bf16 parts too, with the
-// six products of order >= 2^-16.  The cache's values themselves are exact.
+// six products of order >= 2^-16.  The cache's values themselves are exact.  Outputs
+// that are not finite are taken again by the definition (paged_again).
 //
 // Split: the units (64 or 128 positions) of all (sequence, kv head) pairs form
 // one line that the CTAs (two an SM) divide evenly, whatever the lengths; lengths are read on
@@ -33,8 +34,8 @@
 // depend on scheduling.
 #include <algorithm>
 
+#include "attn_row.cuh"
 #include "gemv_launch.cuh"
-#include "paged.cuh"
 #include "tensor_map.h"
 
 namespace q4 {
@@ -166,6 +167,65 @@ struct PagedSmem {
 
 // A partial result: G outputs of D, G maxima, G sums, in whole 16 bytes.
 Q4_HD constexpr size_t paged_slot_floats(int G, int D) { return ((size_t)G * (D + 2) + 3) / 4 * 4; }
+
+// The heads of (sequence b, kv head hk) whose outputs are not finite, again by the
+// definition, by the whole CTA: a product's parts (of p, and of fp32 values) can be
+// zero or negative, so an attended infinity comes out as NaN.  The outputs, and the new
+// token's row of the pages, are visible to this CTA.  room: kPagedWarps (D + 3) floats.
+template <typename T, int D>
+__device__ __noinline__ void paged_again(const PagedAttnParams &p, int b, int hk, int pos, float *room) {
+    constexpr int DL = D / 32;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, G = p.H / p.kv.hkv;
+    const int lo = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
+    float *stat = room + kPagedWarps * D;  // per warp: maximum, sum, whether a position had a page
+    for (int h = 0; h < G; ++h) {
+        const size_t at = ((size_t)b * p.H + hk * G + h) * D;
+        bool bad = false;
+        for (int d = tid; d < D; d += kPagedThreads) bad = bad || !(fabsf(p.out[at + d]) < INFINITY);
+        if (!__syncthreads_or(bad)) continue;  // (and the room is free again)
+        float q[DL];
+#pragma unroll
+        for (int i = 0; i < DL; ++i) q[i] = p.q[at + lane + 32 * i];
+#pragma unroll
+        for (int i = 0; i < DL / 2; ++i) {
+            const float x = q[i], y = q[i + DL / 2];
+            const float c = p.rope_cos ? p.rope_cos[(size_t)pos * (D / 2) + lane + 32 * i] : 1.f;
+            const float s = p.rope_cos ? p.rope_sin[(size_t)pos * (D / 2) + lane + 32 * i] : 0.f;
+            if (p.rope_cos) {
+                q[i] = x * c - y * s;
+                q[i + DL / 2] = y * c + x * s;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < DL; ++i) q[i] *= p.scale * 1.4426950408889634f;
+        RowSum<D> a;
+        for (int k0 = lo + 32 * warp; k0 <= pos && !all_nan(a); k0 += 32 * kPagedWarps)
+            attn_span<T, D>(a, p.kv, q, b, hk, k0, pos, lane, p.err);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a.l += __shfl_xor_sync(0xffffffffu, a.l, o);
+#pragma unroll
+        for (int i = 0; i < DL; ++i) room[warp * D + lane + 32 * i] = a.acc[i];
+        if (lane == 0) {
+            stat[3 * warp] = a.m;
+            stat[3 * warp + 1] = a.l;
+            stat[3 * warp + 2] = a.seen ? 1.f : 0.f;
+        }
+        __syncthreads();
+        for (int d = tid; d < D; d += kPagedThreads) {
+            float M = -INFINITY, o = 0.f, L = 0.f, seen = 0.f;
+            for (int w = 0; w < kPagedWarps; ++w) M = fmaxf(M, stat[3 * w]);
+            const float mu = M == -INFINITY ? 0.f : M;
+            for (int w = 0; w < kPagedWarps; ++w) {
+                const float f = ex2(stat[3 * w] - mu);
+                if (stat[3 * w + 2] == 0.f) continue;
+                o = fmaf(room[w * D + d], f, o);
+                L = fmaf(stat[3 * w + 1], f, L);
+                seen = 1.f;
+            }
+            p.out[at + d] = seen == 0.f ? 0.f : o / L;
+        }
+    }
+}
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
@@ -772,6 +832,13 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
             }
         __syncthreads();
         const bool whole = u == s0 && ue == s1;
+        // an output that is not finite (or without a weight: 0 / 0 here) is looked at again
+        bool again = false;
+        auto result = [&](float o, float L) {
+            const float x = o / L;
+            again = again || !(fabsf(x) < INFINITY);
+            return x;
+        };
         float *mine = p.part + ((size_t)cta * 2 + (u == u0 ? 0 : 1)) * slot_floats;
         for (int idx = tid; idx < G * D; idx += kPagedThreads) {
             const int h = idx / D;
@@ -787,7 +854,7 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                 L = fmaf(wl[w * 8 * NT + h], f, L);
             }
             if (whole) {
-                p.out[((size_t)b * p.H + hk * G) * D + idx] = L == 0.f ? 0.f : o / L;
+                p.out[((size_t)b * p.H + hk * G) * D + idx] = result(o, L);
             } else {
                 mine[idx] = o;
                 if (idx - h * D == 0) {
@@ -859,8 +926,11 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                         Mx = mn;
                     }
                     if (NG == 1) {
-                        const float r = L == 0.f ? 0.f : 1.f / L;
-                        *reinterpret_cast<float4 *>(dst + idx) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+                        const float r = 1.f / L;
+                        const float4 x = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+                        again = again || !(fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY &&
+                                           fabsf(x.w) < INFINITY);
+                        *reinterpret_cast<float4 *>(dst + idx) = x;
                     } else {
                         *reinterpret_cast<float4 *>(red + (size_t)grp * G * D + idx) = o;
                         if (idx == h * D) {
@@ -881,14 +951,18 @@ __global__ void __launch_bounds__(kPagedThreads, kPagedOcc)
                             o = fmaf(red[(size_t)y * G * D + idx], f, o);
                             L = fmaf(wl[y * G + h], f, L);
                         }
-                        dst[idx] = L == 0.f ? 0.f : o / L;
+                        dst[idx] = result(o, L);
                     }
                 }
                 if (tid == 0) p.count[(size_t)b * hkv + hk] = 0;  // zero again for the next call
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the merge's writes, before the next copies
-        __syncthreads();  // the shared memory is free for the next segment
+        if (__syncthreads_or(again)) {  // the shared memory is free for the next segment
+            paged_again<T, D>(p, b, hk, pos, red);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncthreads();
+        }
         u = ue;
     }
 }

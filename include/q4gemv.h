@@ -489,7 +489,9 @@ q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k,
  * window > 0), w = softmax_j(scale q[r][h] . k_j), query head h reading kv head
  * h / (H / kv_heads).  q, out: [rows][H][D] of the cache's type, not
  * overlapping; out rows from cu_rows[nseq] on are left alone.  H / kv_heads in
- * 1..16.  What masked positions hold (infinities, NaN) does not reach out.
+ * 1..16.  What masked positions hold (infinities, NaN) does not reach out;
+ * attended ones give what the formula gives (an infinity, or NaN; scores that are
+ * all -inf: NaN), and rows that are not finite take far longer.
  * scale: finite, not negative (as q4_attn_paged's).  A row with no attended
  * position (every page out of range) is zeros.
  * Numerics: fp32 sums and softmax statistics; with a 16-bit type the softmax
@@ -520,7 +522,8 @@ q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows,
  * graphs) that share one must not run at the same time.  nseq * kv_heads <=
  * 65536.  Results do not depend on scheduling.
  * Numerics: q and the softmax weights enter with 22 bits or more, the cache's
- * values exactly; fp32 sums and softmax statistics. */
+ * values exactly; fp32 sums and softmax statistics.  Masked and attended infinities
+ * and NaN as q4_attn_prefill has them. */
 size_t q4_attn_paged_workspace_bytes(const q4_kv_pages *pages, int32_t H);
 q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k_new, const float *v_new,
                         const int32_t *positions, int32_t H, int32_t window, float scale, const float *rope_cos,

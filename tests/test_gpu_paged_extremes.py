@@ -283,3 +283,78 @@ def test_prefill_of_nan_ends_soon(q4, dtype, D):  # noqa: F811
         took.append(a.elapsed_time(b))
         assert bool(torch.isnan(out).all()) == bad and bool(torch.isfinite(out).all()) != bad
     assert took[1] < 200 * took[0], took
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("H,D,n", [(8, 64, 300), (24, 128, 300), (8, 64, 9000), (2, 128, 300)])
+@pytest.mark.parametrize("case", list(INFS))
+def test_paged_attended_infinities(q4, dtype, H, D, n, case):  # noqa: F811
+    # whole in one CTA's share or joined from many; q, k, v of order one: no weight is
+    # zero, so an infinity is attended wherever its position is
+    t, Hkv = DTYPES[dtype], 2
+    rng = np.random.default_rng(case_seed("inf", dtype, H, D, n))
+    k, v = _with_infs(rng, n, Hkv, D, t, INFS[case])
+    q = (0.5 * rng.standard_normal((2, H, D))).astype(np.float32)
+    # sequence 1 is finite: a part of the same positions
+    page, npg = 128, -(-n // 128)
+    pool = torch.full((2, 2 * npg, Hkv, page, D), float("nan"), dtype=t)
+    for i, x in enumerate((k, v)):
+        flat = pool[i].transpose(1, 2).reshape(2 * npg * page, Hkv, D)
+        flat[:n - 1] = x[:n - 1]
+        flat[npg * page:npg * page + 200] = torch.nan_to_num(x[:200].float(), 0.5, 0.5, 0.5).to(t)
+        pool[i] = flat.reshape(2 * npg, page, Hkv, D).transpose(1, 2)
+    pages = q4.KVPages(pool[0].cuda(), pool[1].cuda(), I(np.arange(2 * npg).reshape(2, npg).tolist()))
+    new = [torch.stack([x[n - 1].float(), torch.ones(Hkv, D)]).cuda() for x in (k, v)]
+    got = q4.q4_attn_paged(T(q), *new, pages, I([n - 1, 200]))
+    assert torch.equal(got.view(torch.int32), q4.q4_attn_paged(T(q), *new, pages, I([n - 1, 200])).view(torch.int32))
+    q4.q4_device_check()
+    got = f64(got)
+    K, V = k.double().numpy(), v.double().numpy()
+    assert np.isfinite(got[1]).all()
+    for h in range(H):
+        hk = h // (H // Hkv)
+        ref = _formula(q[0, h].astype(np.float64), K[:, hk], V[:, hk], D ** -0.5)
+        _same(got[0, h], ref, 2.0 ** -12, "%s h=%d" % (case, h))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_paged_values_that_overflow_the_cache(q4, D):  # noqa: F811
+    # f16: a new value beyond 65504 is stored as infinity, and attended as one
+    n = 30
+    pages = q4.KVPages(torch.zeros(1, 1, 32, D, device="cuda", dtype=torch.float16),
+                       torch.ones(1, 1, 32, D, device="cuda", dtype=torch.float16), I([[0]]))
+    f = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    v = f(1, 1, D)
+    v[0, 0, 7], v[0, 0, 8] = 1e5, -1e5
+    got = f64(q4.q4_attn_paged(f(1, 4, D) + 1, f(1, 1, D), v, pages, I([n - 1])))[0]
+    ref = np.full(D, (n - 1) / n)
+    ref[7], ref[8] = INF, -INF
+    for h in range(4):
+        _same(got[h], ref, 2.0 ** -20, "overflow")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [150, 9000])
+def test_paged_scores_all_minus_infinity(q4, dtype, D, n):  # noqa: F811
+    t = DTYPES[dtype]
+    k = torch.full((2, 1, n + 10, D), 0.25, dtype=t, device="cuda")
+    k[0, 0, :, 3] = -INF
+    pages = q4.KVPages(k, torch.ones_like(k), I([[0], [1]]))
+    q = torch.ones(2, 2, D, device="cuda")
+    q[:, 1] = -1.0
+    kn = torch.stack([k[0, :, 0].float(), k[1, :, 0].float()])
+    got = q4.q4_attn_paged(q, kn, torch.ones_like(kn), pages, I([n - 1, n - 1]))
+    q4.q4_device_check()
+    assert torch.isnan(got[0]).all() and float((got[1] - 1).abs().max()) <= (n / 4 + 64) * 2.0 ** -24 + 2.0 ** -20
+
+
+def test_paged_pages_that_are_all_gone(q4):  # noqa: F811
+    # no attended position has a page: zeros, and recorded
+    pages = q4.KVPages(torch.ones(2, 1, 16, 64, device="cuda"), torch.ones(2, 1, 16, 64, device="cuda"), I([[7, -1], [0, 1]]))
+    x = torch.ones(2, 3, 64, device="cuda")
+    new = torch.ones(2, 1, 64, device="cuda")
+    got = q4.q4_attn_paged(x, new, new, pages, I([20, 20]))
+    with pytest.raises(q4.Q4Error):
+        q4.q4_device_check()
+    assert not got[0].any() and float((got[1] - 1).abs().max()) <= 2.0 ** -18
