@@ -734,3 +734,35 @@ def test_prefill_sums_rescaled_in_every_key_tile(q4, D, step):
             for h in range(H):
                 ref, bound = attend(q[cu[b] + i, h].astype(np.float64), K[:p + 1, h // 2], V[:p + 1, h // 2], step)
                 check(got[cu[b] + i, h], ref, bound + 2.0 ** -25, "rescaled b=%d p=%d h=%d" % (b, p, h))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("H,Hkv,D", [(32, 8, 64), (4, 4, 128), (6, 2, 64), (7, 1, 128), (16, 1, 128), (2, 1, 64)])
+@pytest.mark.parametrize("rows,starts,window,page", [([1], [0], 0, 16), ([33, 0, 1, 130], [0, 4, 77, 0], 0, 48),
+                                                     ([257, 64], [100, 0], 70, 64), ([5], [400], 0, 128),
+                                                     ([300], [0], 1, 256), ([900, 1200], [0, 300], 0, 64)])
+def test_prefill_repeats_its_bits(q4, dtype, H, Hkv, D, rows, starts, window, page):
+    # the rows that a call writes are the same bits every time, with rows behind the
+    # last sequence (left alone) too, and on workspaces with other contents
+    t, rng = DTYPES[dtype], np.random.default_rng(case_seed("repeat", dtype, H, D, rows))
+    lens = [s + r for s, r in zip(starts, rows)]
+    pool = Pool(rng, [max(1, x) for x in lens], Hkv, page, D, t)
+    for b, n in enumerate(lens):
+        if n:
+            pool.put(b, np.arange(n), *rng.standard_normal((2, n, Hkv, D)))
+    dev = pool.device(q4)
+    used = sum(rows)
+    q = torch.from_numpy(rng.standard_normal((used + 3, H, D)).astype(np.float32)).to(t).cuda()
+    cu, st = I(np.concatenate([[0], np.cumsum(rows)]).tolist()), I(starts)
+    ws = q4.q4_attn_prefill_workspace(dev, used + 3, H)
+    outs = []
+    for fill in (0, 255, 63, 127):
+        if ws is not None:
+            ws.fill_(fill)
+        out = torch.full_like(q, 9.0)
+        q4.q4_attn_prefill(q, dev, cu, st, window=window, out=out, workspace=ws)
+        assert bool((out[used:] == 9.0).all()) and bool(torch.isfinite(out).all())
+        outs.append(out[:used].contiguous().view(torch.uint8))
+    for o in outs[1:]:
+        assert torch.equal(outs[0], o)
+    q4.q4_device_check()
