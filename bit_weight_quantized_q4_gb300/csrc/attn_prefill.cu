@@ -352,12 +352,13 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim) && *abort_flag == 0) != 0;
     };
     // and one that may last a whole item: it gives up when, for the limit, no copy
-    // has gone out and no row was being taken by the definition
+    // has gone out and no rows were being taken by the definition, nor had been since
+    // (slow: odd while they are, so that the moment between two items' is seen)
     auto wait_item = [&](uint32_t bar, uint32_t parity) {
-        int seen = __shfl_sync(0xffffffffu, *progress, 0);
+        int seen = __shfl_sync(0xffffffffu, *progress + *slow, 0);
         while (!wait(bar, parity)) {
-            const int now = __shfl_sync(0xffffffffu, *progress, 0);
-            if (!__any_sync(0xffffffffu, now != seen || *slow != 0) || __any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            const int was = __shfl_sync(0xffffffffu, *slow, 0), now = __shfl_sync(0xffffffffu, *progress, 0) + was;
+            if ((now == seen && (was & 1) == 0) || __any_sync(0xffffffffu, *abort_flag != 0)) return false;
             seen = now;
         }
         return true;
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
             const unsigned rows = lane < Cf::Soft ? mask_s[(n % kPfItems) * Cf::Soft + lane] : 0u;
             unsigned warps = __ballot_sync(0xffffffffu, rows != 0u);
             if (warps) {
-                if (lane == 0) *slow = 1;
+                if (lane == 0) *slow = *slow + 1;
                 for (; warps; warps &= warps - 1) {
                     const int w = __ffs(warps) - 1;
                     for (unsigned left = __shfl_sync(0xffffffffu, rows, w); left; left &= left - 1) {
@@ -734,7 +735,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) *slow = 0;
+                if (lane == 0) *slow = *slow + 1;
             }
             tile_read(n);
         }
