@@ -32,14 +32,19 @@ __device__ __forceinline__ void attn_span(RowSum<D> &a, const PagedKv &kv, const
     const unsigned have = __ballot_sync(0xffffffffu, page >= 0);
     a.seen = a.seen || have != 0u;
     float s = 0.f;
+    // (two loads at a time: as many registers as the loads of a whole row make the
+    // kernels that call this spill around the call)
 #pragma unroll
-    for (int x = 0; x < D; x += V) {
-        T k[V];
-        *reinterpret_cast<uint4 *>(k) = page < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                                 : __ldcg(reinterpret_cast<const uint4 *>((const T *)kv.k + off + x));
+    for (int i = 0; i < DL; ++i)
+#pragma unroll 2
+        for (int x = 0; x < 32; x += V) {
+            T k[V];
+            *reinterpret_cast<uint4 *>(k) =
+                page < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                         : __ldcg(reinterpret_cast<const uint4 *>((const T *)kv.k + off + 32 * i + x));
 #pragma unroll
-        for (int e = 0; e < V; ++e) s = fmaf(__shfl_sync(0xffffffffu, q[(x + e) / 32], (x + e) % 32), to_f32(k[e]), s);
-    }
+            for (int e = 0; e < V; ++e) s = fmaf(__shfl_sync(0xffffffffu, q[i], x + e), to_f32(k[e]), s);
+        }
     if (page < 0) s = -INFINITY;
     float mx = s;
 #pragma unroll

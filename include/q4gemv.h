@@ -515,7 +515,8 @@ q4_status q4_attn_prefill(const q4_kv_pages *pages, const void *q, int32_t rows,
  * attended as the cache stores it.  A negative position marks an idle row (a
  * padded batch): nothing is appended and its out row is zeros.  q, out:
  * [nseq][H][D] fp32; k_new, v_new: [nseq][kv_heads][D] fp32; positions: [nseq].
- * H / kv_heads in 1..16.  Two sequences must not append to one page slot.
+ * H / kv_heads in 1..16.  Two sequences must not append to one page slot, nor may
+ * one attend a slot that another appends to in the same call.
  * workspace: q4_attn_paged_workspace_bytes bytes, zero-filled by the caller
  * before its first use (every call leaves its counters zero, so calls of
  * different shapes can share one that is large enough); calls (and captured
