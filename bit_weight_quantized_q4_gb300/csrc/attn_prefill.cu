@@ -29,7 +29,7 @@
 // operands for the scores of two row tiles, 128 for their products, 64 of copies, 64
 // of weights written.  (P over its S spares 128 KB of that, but the next scores then
 // wait for the product: 89 us.  The halves' maxima joined a key tile late, with
-// bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 74 us): three
+// bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 76 us): three
 // products each at 4500 cycles a key tile, 4300 of them tensor work, and about 14 us
 // to write the operands' parts.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
@@ -69,12 +69,15 @@ constexpr float kPfGrow = 8.f;              // log2 growth of a maximum that res
 // token's, or a stale one's.  A position's factors back (K's and V's, powers of two)
 // multiply its column of S, and its weight: a row's scaled weights are brought to
 // f16's range by one more power of two a key tile, found from their own largest, which
-// goes into the sum beside O.  That costs twice the time, so the scales of K and V
-// are steps of 2^12: a key tile whose positions have the same ones takes them as one
-// factor, and a call whose attended positions all have the usual one (rows whose
-// largest value is in [2^-5, 2^7), or zeros) never looks at them (2048 rows: 74 us; 89
-// where a position of the call has another one, 160 where every key tile mixes them).
-// A row's bits are the same by each way.
+// goes into the sum beside O.  So does the reference of a key tile's weights, its own
+// maximum: the row's so far would leave the weights of a later key tile few bits, which
+// large values there would show.
+// Factors of their own cost twice the time, so the scales of K and V are steps of 2^12:
+// a key tile whose positions have the same ones takes them as one factor, and a call
+// whose attended positions all have the usual one (rows whose largest value is in
+// [2^-5, 2^7), or zeros) never looks at them (2048 rows: 76 us; 84 where a position of
+// the call has another one, 165 where every key tile mixes them).  A row's bits are the
+// same by each way.
 template <typename T>
 struct PfT {
     using M = T;
@@ -91,7 +94,7 @@ template <>
 struct PfT<float> {
     using M = __half;
     static constexpr int Parts = 2;
-    static constexpr float PExp = 6.f;  // weights reach 2^(6 + kPfGrow): their low parts stay normal f16
+    static constexpr float PExp = 13.f;  // weights reach 2^13 in each key tile: its own maximum is their reference
 };
 
 template <int D, int Parts>
@@ -769,6 +772,11 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 return got;
             };
             int n_tile = 0;  // Wide: key tiles of the items before
+            // fp32: weights from a key tile's own maximum `top` (2^PExp there) in the units of
+            // the sums, whose reference is m
+            auto own_down = [](float top, float m) {
+                return top == -INFINITY ? 0.f : ex2(top - m - PfT<T>::PExp);
+            };
             // 32 weights as two f16 parts: the high ones in w, what those leave in place
             auto parts = [](uint32_t *x, uint32_t (&w)[16]) {
 #pragma unroll
@@ -815,7 +823,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                 if constexpr (NP == 2)
                     cq = p.scale * 1.4426950408889634f * (Wide ? 1.f : kPfUsual) * (live ? p.qback[(size_t)row * p.H + head] : 0.f);
                 float m = -INFINITY, l = 0.f;
-                float back = 1.f;  // Wide: what the last key tile's O is in the sum's units
+                float back = 1.f;  // fp32: what the last key tile's O (and sum of weights) is in the sums' units
                 for (int j = 0; j < nk; ++j) {
                     ok = wait(b_s + 8 * i, sph);
                     sph ^= 1u;
@@ -836,13 +844,12 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                                 tc::wait_ld16(a);
                             }
                             tc::wait_ld16(o);
-                            if constexpr (Wide) {
+                            const uint64_t b2 = pair_f32(back, back);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), back, j > 1 ? __uint_as_float(a[e]) : 0.f));
-                            } else if (j > 1) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(a[e]));
+                            for (int e = 0; e < 16; e += 2) {
+                                const uint64_t y = fma_f32x2(pair_u32(o[e], o[e + 1]), b2, j > 1 ? pair_u32(a[e], a[e + 1]) : 0ull);
+                                o[e] = (uint32_t)y;
+                                o[e + 1] = (uint32_t)(y >> 32);
                             }
                             tc::st16(tsum + at, o);
                         }
@@ -874,7 +881,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             }
                         };
                         uint64_t sum[2] = {0ull, 0ull}, mc2 = 0ull;
-                        float top = -INFINITY, mc = 0.f;
+                        float top = -INFINITY, mc = 0.f, down = 0.f;
                         // the row's maximum with this key tile's, and the sums so far to it
                         auto raise = [&]() {
                             top = fmaxf(top, other(top, ok));
@@ -901,8 +908,9 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                                     }
                                 }
                             }
-                            mc = (m == -INFINITY ? 0.f : -m) + PfT<T>::PExp;
+                            mc = (top == -INFINITY ? 0.f : -top) + PfT<T>::PExp;
                             mc2 = pair_f32(mc, mc);
+                            down = own_down(top, m);
                         };
                         if (same.y != 0u) {
                             uint32_t s[CW];
@@ -934,7 +942,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                             raise();
                             if (!ok) break;
-                            back = __uint_as_float(same.x << 16);
+                            back = down * __uint_as_float(same.x << 16);
 #pragma unroll
                         for (int e = 0; e < CW; e += 2) {
                             const uint64_t x = add_f32x2(pair_u32(s[e], s[e + 1]), mc2);
@@ -994,7 +1002,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             const uint32_t e_big = __float_as_uint(big) >> 23, e_v = __float_as_uint(big_v) >> 23;
                             const uint32_t ex = min(big < big_w * big_v * 0.015625f ? 267u - e_big : 254u - e_v, 253u);
                             const float up = __uint_as_float(ex << 23);
-                            back = __uint_as_float((254u - ex) << 23);
+                            back = down * __uint_as_float((254u - ex) << 23);
 #pragma unroll 1
                             for (int q = 0; q < CW; q += 32) {
                                 uint32_t x[32], w[16];
@@ -1015,7 +1023,7 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             }
                         }
                         const uint64_t s2 = add_f32x2(sum[0], sum[1]);
-                        l += lo_f32(s2) + hi_f32(s2);
+                        l = fmaf(lo_f32(s2) + hi_f32(s2), down, l);
                     } else {
                         uint32_t s[CW];
 #pragma unroll
@@ -1091,10 +1099,12 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                                 }
                             }
                         }
-                        const float mc = (m == -INFINITY ? 0.f : -m * c) + PfT<T>::PExp;
+                        // (fp32: from the key tile's own maximum)
+                        const float ref = NP == 2 ? top : m;
+                        const float mc = (ref == -INFINITY ? 0.f : -ref * c) + PfT<T>::PExp;
                         const uint64_t c2 = pair_f32(c, c), mc2 = pair_f32(mc, mc);
                         uint64_t sum[2] = {0ull, 0ull};
-                        if constexpr (NP == 2) {  // (all, then their parts: 75 us, pair by pair 81)
+                        if constexpr (NP == 2) {  // (all, then their parts: 74 us, pair by pair 81)
 #pragma unroll
                             for (int e = 0; e < CW; e += 2) {
                                 const uint64_t x = add_f32x2(pair_u32(s[e], s[e + 1]), mc2);
@@ -1132,7 +1142,12 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                             if constexpr (NP == 2) tc::st16(ts + CW * hf + 32 * q + 16, s + 32 * q);
                         }
                         const uint64_t s2 = add_f32x2(sum[0], sum[1]);
-                        l += lo_f32(s2) + hi_f32(s2);
+                        if constexpr (NP == 2) {
+                            back = own_down(top, m);
+                            l = fmaf(lo_f32(s2) + hi_f32(s2), back, l);
+                        }
+                        else
+                            l += lo_f32(s2) + hi_f32(s2);
                     }
                     if (!ok) break;
                     tc::wait_st();
@@ -1157,13 +1172,12 @@ __global__ void __launch_bounds__(PfCfg<D, PfT<T>::Parts>::Threads, 1)
                         tc::wait_ld16(o + 16 * q);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            o[16 * q + e] = __float_as_uint(Wide ? fmaf(__uint_as_float(o[16 * q + e]), back, __uint_as_float(a[e]))
-                                                                 : __uint_as_float(o[16 * q + e]) + __uint_as_float(a[e]));
+                            o[16 * q + e] = __float_as_uint(fmaf(__uint_as_float(o[16 * q + e]), back, __uint_as_float(a[e])));
                     }
                 }
 #pragma unroll
                 for (int q = 0; q < QO; ++q) tc::wait_ld16(o + 16 * q);
-                if (Wide && nk == 1)
+                if (NP == 2 && nk == 1)
 #pragma unroll
                     for (int e = 0; e < 16 * QO; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * back);
                 tc::fence_before_sync();

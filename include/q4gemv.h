@@ -497,10 +497,9 @@ q4_status q4_kv_append(const q4_kv_pages *pages, const float *q, const float *k,
  * Numerics: fp32 sums and softmax statistics; with a 16-bit type the softmax
  * weights enter the products rounded once to it (f16: to 2^-31 of the row's
  * largest at least); with fp32, q, k, v and the weights enter with about 22 bits,
- * a position's k and v to 2^-27 of its own largest value at least, the weights to
- * 2^-31 of the row's largest (where a key tile mixes values of very different sizes,
- * each weight times its v's largest to 2^-26 of the largest such product).  A row's
- * bits follow from q's row and the positions it attends alone.
+ * a position's k and v to 2^-27 of its own largest value at least, each weight times
+ * its v's largest value to 2^-26 of the largest such product.  A row's bits follow
+ * from q's row and the positions it attends alone.
  * workspace: q4_attn_prefill_workspace_bytes bytes, no initialisation needed,
  * not shared by calls that run at the same time: 0 (NULL will do) for the 16-bit
  * types; for fp32 the operands' parts, as large as the cache itself and q. */

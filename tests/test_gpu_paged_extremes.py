@@ -4,7 +4,7 @@ that are attended, which give what the formula gives."""
 import numpy as np
 import pytest
 
-from paged_ref import attend, check
+from paged_ref import Pool, attend, check
 from parity import case_seed
 from test_gpu_paged import DTYPES, I, T, f64, q4  # noqa: F401  (q4: the fixture)
 
@@ -358,3 +358,54 @@ def test_paged_pages_that_are_all_gone(q4):  # noqa: F811
     with pytest.raises(q4.Q4Error):
         q4.q4_device_check()
     assert not got[0].any() and float((got[1] - 1).abs().max()) <= 2.0 ** -18
+
+
+# ------------------------------------------------------------------ fp32 prompts of mixed sizes
+
+@pytest.mark.parametrize("H,Hkv,D", [(32, 8, 64), (4, 4, 128), (6, 2, 64), (7, 1, 128), (16, 1, 128)])
+@pytest.mark.parametrize("rows,starts,window,page", [([1], [0], 0, 16), ([33, 0, 1, 130], [0, 4, 77, 0], 0, 48),
+                                                     ([257, 64], [100, 0], 70, 64), ([5], [400], 0, 128), ([300], [0], 1, 256),
+                                                     ([150], [51], 0, 201), ([700, 90, 600], [0, 500, 33], 300, 16)])
+def test_prefill_values_of_mixed_sizes(q4, H, Hkv, D, rows, starts, window, page):  # noqa: F811
+    # fp32: every position's k and v have a size of their own, in some sequences' parts
+    # the usual one, so that each way of taking the factors meets the others in one call
+    rng = np.random.default_rng(case_seed("mixed", H, D, rows, window))
+    lens = [s + r for s, r in zip(starts, rows)]
+    pool = Pool(rng, [max(1, x) for x in lens], Hkv, page, D, torch.float32)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        kv = rng.standard_normal((2, n, Hkv, D)).astype(np.float32)
+        wild = (np.arange(n) // 100 % 2 == 0) if b % 2 == 0 else np.zeros(n, bool)
+        kv[0, wild] *= np.exp2(rng.integers(-30, 3, (int(wild.sum()), Hkv, 1))).astype(np.float32)
+        kv[1, wild] *= np.exp2(rng.integers(-40, 40, (int(wild.sum()), Hkv, 1))).astype(np.float32)
+        kv[:, rng.integers(0, n, 2)] = 0.0
+        pool.put(b, np.arange(n), *kv)
+    dev, used = pool.device(q4), sum(rows)
+    q = rng.standard_normal((used + 2, H, D)).astype(np.float32)
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    outs = []
+    for _ in range(2):
+        out = torch.full((used + 2, H, D), 9.0, device="cuda")
+        outs.append(q4.q4_attn_prefill(T(q), dev, I(cu), I(starts), window=window, out=out))
+    q4.q4_device_check()
+    assert torch.equal(outs[0], outs[1]) and bool((outs[0][used:] == 9.0).all())
+    got = f64(outs[0])
+    sc = D ** -0.5
+    for b, r in enumerate(rows):
+        K, V = (pool.get(x, b, np.arange(lens[b])) for x in (pool.k, pool.v))
+        for i in range(r) if r <= 40 else sorted({0, 1, r - 1, r - 2, *rng.integers(0, r, 24).tolist()}):
+            p = starts[b] + i
+            lo = max(0, p + 1 - window) if window else 0
+            for h in range(H) if H <= 8 else sorted({0, H - 1, *rng.integers(0, H, 4).tolist()}):
+                q1, K1, V1 = q[cu[b] + i, h].astype(np.float64), K[lo:p + 1, h // (H // Hkv)], V[lo:p + 1, h // (H // Hkv)]
+                ref, bound = attend(q1, K1, V1, sc)
+                s = sc * (K1 @ q1)
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                # the parts: of v and of the weights as in test_large_values_of_small_weight; of
+                # k 22 bits or 2^-27 of its row's largest, so a score by 2^-27 |q| max |k|, twice
+                rv, rk = np.abs(V1).max(1), np.abs(K1).max(1)
+                bound = bound + (3 * 2.0 ** -22 + 2 * 2.0 ** -27 * sc * np.abs(q1).sum() * rk.max()) * (w @ np.abs(V1))
+                bound = bound + 2.0 ** -27 * (w @ rv) + len(w) * 2.0 ** -26 * (w * rv).max()
+                check(got[cu[b] + i, h], ref, bound + 1e-30, "mixed b=%d i=%d h=%d" % (b, i, h))
