@@ -17,8 +17,8 @@
 //        fp32: pairs of positions packed, rows of the m tiles permuted so that a
 //        lane's 32 bytes of a V row are rows of its own tiles); P goes through
 //        movmatrix.
-// 64 ragged bf16 contexts up to 8191 (1.03 GB): 173 us, 5.9 TB/s; one of 32768
-// (134 MB): 30.5 us, of which the loop runs at the memory's rate and about 5 us
+// 64 ragged bf16 contexts up to 8191 (1.03 GB): 174 us, 5.9 TB/s; one of 32768
+// (134 MB): 31 us, 4.3 TB/s, whether from HBM or partly from L2, of which about 5 us
 // are the scan, Q, the warps' merge and the joining of the CTAs' shares.
 //
 // Precision: q and p stay fp32-like.  f16 caches: q (scaled per head by a

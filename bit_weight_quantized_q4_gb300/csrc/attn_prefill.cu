@@ -22,16 +22,18 @@
 // An MMA of 128 rows takes about 60 cycles per K = 16 at N = 64 as at N = 128
 // (measured by its issue), so at head size 64 the product runs at half the
 // tensor rate whatever the tiling: 8192 rows took 277 us with two tiles of 128
-// positions, P beside S and S a key tile ahead, and 277 with four of 64 (247 now:
-// 1110 TFLOP/s, the tensor core busy over 90 % of the loop).  At head size 128 (nine
-// ragged prompts, 93 GFLOP: 86 us, 1080 TFLOP/s) a key tile takes 2900 cycles, the
-// time in which shared memory moves what it has to at 128 bytes a cycle: 128 KB of
-// operands for the scores of two row tiles, 128 for their products, 64 of copies, 64
-// of weights written.  (P over its S spares 128 KB of that, but the next scores then
-// wait for the product: 89 us.  The halves' maxima joined a key tile late, with
-// bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 76 us): three
-// products each at 4500 cycles a key tile, 4300 of them tensor work, and about 14 us
-// to write the operands' parts.
+// positions, P beside S and S a key tile ahead, and 277 with four of 64 (249 now:
+// 1100 TFLOP/s, the tensor core busy over 90 % of the loop).  At head size 128 (nine
+// ragged prompts, 93 GFLOP: 86 us, 1080 TFLOP/s) a key tile of two row tiles takes 2900
+// cycles, 1920 of them tensor work.  What takes the rest is not settled: over the
+// launch the tensor pipe is busy 53 % of the active cycles, and of shared memory's
+// wavefronts the tensor core's operands take 48 % and the warps' accesses 21 %, so
+// no unit is full; the chain scores - weights - product and the ends of items are
+// the likely cause.  (P over its S spares a third of the operands' traffic, but the
+// next scores then wait for the product: 89 us.  The halves' maxima joined a key tile
+// late, with bf16's exponents: 87; a warp a row: 89.)  fp32 (2048 rows: 76 us): three
+// products each, of which 4300 cycles a key tile are tensor work, and about 14 us to
+// write the operands' parts; the longest item has 16 key tiles.
 // O is rescaled in tensor memory only when a row's maximum grew by more than 2^8
 // (the sums stay exact: the reference maximum is the row's own, and its factor
 // cancels).

@@ -409,3 +409,22 @@ def test_prefill_values_of_mixed_sizes(q4, H, Hkv, D, rows, starts, window, page
                 bound = bound + (3 * 2.0 ** -22 + 2 * 2.0 ** -27 * sc * np.abs(q1).sum() * rk.max()) * (w @ np.abs(V1))
                 bound = bound + 2.0 ** -27 * (w @ rv) + len(w) * 2.0 ** -26 * (w * rv).max()
                 check(got[cu[b] + i, h], ref, bound + 1e-30, "mixed b=%d i=%d h=%d" % (b, i, h))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_give_up_with_factors_of_their_own(q4, D):  # noqa: F811
+    # a copy that never completes while the positions' factors are looked at: the call
+    # ends and records it, and the next one has its usual bits
+    rng = np.random.default_rng(case_seed("give up", D))
+    k, v = (rng.standard_normal((1, 2, 400, D)).astype(np.float32) for _ in range(2))
+    v[:, :, ::3] *= 2.0 ** 30
+    q = rng.standard_normal((400, 8, D)).astype(np.float32)
+    want = _prefill(q4, k, v, [[0]], q, [0, 400], [0])
+    q4.q4_debug_wait_limits(copy_wait_cycles=200000, copy_extra_bytes=16)
+    try:
+        with pytest.raises(q4.Q4Error) as e:
+            _prefill(q4, k, v, [[0]], q, [0, 400], [0])
+        assert e.value.status == 6
+    finally:
+        q4.q4_debug_wait_limits()
+    assert torch.equal(want, _prefill(q4, k, v, [[0]], q, [0, 400], [0]))
