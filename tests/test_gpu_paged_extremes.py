@@ -428,3 +428,47 @@ def test_waits_give_up_with_factors_of_their_own(q4, D):  # noqa: F811
     finally:
         q4.q4_debug_wait_limits()
     assert torch.equal(want, _prefill(q4, k, v, [[0]], q, [0, 400], [0]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_captured_prompt_follows_the_sizes_of_its_values(q4, D):  # noqa: F811
+    # fp32: one captured call, its values usual, mixed and usual again (the workspace
+    # keeps what the call before left), beside another prompt on a second stream
+    rng = np.random.default_rng(case_seed("captured sizes", D))
+    rows, page, npg = 500, 64, 8
+    kv = [T(rng.standard_normal((2, npg, 2, page, D)).astype(np.float32)) for _ in range(2)]
+    mixed = [x.clone() for x in kv]
+    for x in mixed:
+        x[1] *= torch.exp2(torch.from_numpy(rng.integers(-30, 30, (npg, 2, page, 1))).cuda().float())
+    q = [T(rng.standard_normal((rows, 8, D)).astype(np.float32)) for _ in range(2)]
+    table, cu, st = I([list(range(npg))]), I([0, rows]), I([7])
+    buf = [x.clone() for x in kv]
+    pages = [q4.KVPages(x[0], x[1], table) for x in buf]
+    ws = [q4.q4_attn_prefill_workspace(p, rows, 8) for p in pages]
+    out = [torch.empty_like(x) for x in q]
+    alone = {}
+    for name, vals in (("usual", kv), ("mixed", mixed)):
+        alone[name] = []
+        for i in range(2):
+            p = q4.KVPages(vals[i][0].clone(), vals[i][1].clone(), table)
+            alone[name].append(q4.q4_attn_prefill(q[i], p, cu, st))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        q4.q4_attn_prefill(q[0], pages[0], cu, st, out=out[0], workspace=ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q4.q4_attn_prefill(q[0], pages[0], cu, st, out=out[0], workspace=ws[0])
+    for a, b in (("usual", "mixed"), ("mixed", "usual"), ("mixed", "mixed"), ("usual", "usual")):
+        for i, name in ((0, a), (1, b)):
+            buf[i].copy_(kv[i] if name == "usual" else mixed[i])
+            out[i].zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(side):
+            for _ in range(3):
+                q4.q4_attn_prefill(q[1], pages[1], cu, st, out=out[1], workspace=ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], alone[a][0]) and torch.equal(out[1], alone[b][1])
+    q4.q4_device_check()
