@@ -10,9 +10,10 @@ Entry points (same names as the C ABI in ``include/q4gemv.h``):
 ``q4_gemv``, ``q4_nrm_gemv``, ``q4_dual_gemv``, ``q4_gus_nrm``,
 ``q4_res_gemv``, ``q4_argmax``, ``q4_group_sums``, ``q4_pack_half``,
 ``q4_gemv_half``, ``q4_gemm``, ``q4_decode_step``, ``q4_attn_decode``,
-``q4_kv_append``, ``q4_attn_prefill``, ``q4_attn_paged``, ``q4_logprobs``; plus ``Q4Weight``
-for repacking host weights into the device layout, ``KVPages`` (a paged KV cache)
-and ``rope_table``.
+``q4_kv_append``, ``q4_attn_prefill``, ``q4_attn_paged``, ``q4_logprobs``,
+``q4_mx_quant``, ``q4_mx_dequant``, ``q4_mx_gemm``; plus ``Q4Weight``
+for repacking host weights into the device layout, ``KVPages`` (a paged KV cache),
+``MXMatrix`` (a matrix of microscaled 4-bit values) and ``rope_table``.
 """
 from __future__ import annotations
 
@@ -33,6 +34,8 @@ Q4_FMT_Q8_0 = 2
 Q4_FMT_Q4_K = 3
 Q4_FMT_Q1 = 4
 MAX_NB = 16
+Q4_MX_MXFP4 = 0
+Q4_MX_NVFP4 = 1
 
 STATUS = {0: "Q4_OK", 1: "Q4_ERR_NULL", 2: "Q4_ERR_SHAPE", 3: "Q4_ERR_ALIGN",
           4: "Q4_ERR_UNSUPPORTED", 5: "Q4_ERR_WORKSPACE", 6: "Q4_ERR_CUDA"}
@@ -69,6 +72,16 @@ class _CKvPages(ctypes.Structure):
                 ("width", ctypes.c_int32)]
 
 
+class _CMx(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("rows", ctypes.c_int32), ("k", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("dev", ctypes.c_void_p), ("bytes", ctypes.c_size_t), ("scale", ctypes.c_float)]
+
+
+class _CMxSrc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("up", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("k", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -88,6 +101,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
         W, KV = ctypes.POINTER(_CWeight), ctypes.POINTER(_CKvPages)
+        MX, SRC = ctypes.POINTER(_CMx), ctypes.POINTER(_CMxSrc)
         sig = {
             "q4_packed_bytes": (SZ, [I32, I32, I32]),
             "q4_weight_bytes": (SZ, [I32, I32, I32]),
@@ -131,6 +145,14 @@ def lib() -> ctypes.CDLL:
             "q4_attn_paged_workspace_bytes": (SZ, [KV, I32]),
             "q4_attn_paged": (I32, [KV, P, P, P, P, I32, I32, F, P, P, I32, P, P, SZ, P]),
             "q4_logprobs": (I32, [P, I32, I32, P, I32, P, P, P, P, P]),
+            "q4_mx_bytes": (SZ, [I32, I32, I32]),
+            "q4_mx_quant": (I32, [SRC, MX, P]),
+            "q4_mx_dequant": (I32, [MX, I32, P, P]),
+            "q4_mx_pack": (I32, [P, P, MX, P]),
+            "q4_mx_unpack": (I32, [MX, P, P, P]),
+            "q4_mx_gemm_workspace_bytes": (SZ, [MX, I32]),
+            "q4_mx_gemm": (I32, [MX, MX, P, I32, P, P, SZ, P]),
+            "q4_mx_linear": (I32, [MX, SRC, MX, P, I32, P, P, SZ, P]),
             "q4_status_str": (ctypes.c_char_p, [I32]),
         }
         for name, (res, args) in sig.items():
@@ -990,3 +1012,221 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
     _check(_launch(dev, lib().q4_logprobs, x, rows, n, tok, k, lpp, entp,
                    val.data_ptr() if k > 0 else None, idx.data_ptr() if k > 0 else None), "q4_logprobs")
     return lp, ent, val, idx
+
+
+# ---------------------------------------------------------------- microscaled 4-bit
+
+def _kinds():
+    torch = _torch()
+    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _kind(dtype, name):
+    kind = _kinds().get(dtype)
+    if kind is None:
+        raise TypeError("%s must be float32, float16 or bfloat16" % name)
+    return kind
+
+
+class MXMatrix:
+    """Matrices of microscaled 4-bit values, ``batch`` of them of ``[rows, k]``, in device memory (owns its
+    tensor): E2M1 codes whose blocks of 32 columns share a power of two (``Q4_MX_MXFP4``) or whose blocks of 16
+    share an E4M3 factor, with one fp32 factor ``scale`` for all (``Q4_MX_NVFP4``).  ``q4_mx_quant`` and
+    ``from_codes`` make one with its contents; the constructor alone leaves them undefined."""
+
+    def __init__(self, fmt: int, rows: int, k: int, batch: int = 1, scale: float = 1.0, device="cuda", tensor=None):
+        torch = _torch()
+        self.fmt, self.rows, self.k, self.batch, self.scale = int(fmt), int(rows), int(k), int(batch), float(scale)
+        one = int(lib().q4_mx_bytes(self.fmt, self.rows, self.k))
+        if one == 0 or self.batch < 1:
+            raise ValueError("bad format or shape: fmt=%d rows=%d k=%d batch=%d" % (self.fmt, self.rows, self.k, self.batch))
+        self.nbytes = one * self.batch
+        if tensor is None:
+            tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.tensor = _dev_buf(tensor, "tensor", torch.uint8, None, tensor.device, min_numel=self.nbytes)
+        self.device = tensor.device
+        self._c = _CMx(self.fmt, self.rows, self.k, self.batch, tensor.data_ptr(), self.nbytes, self.scale)
+        self._ref = ctypes.byref(self._c)
+        self._gemm_ws = {}
+
+    @property
+    def block(self) -> int:
+        """Columns that share a scale."""
+        return 32 if self.fmt == Q4_MX_MXFP4 else 16
+
+    @property
+    def weight_bytes(self) -> int:
+        """Algorithmic bytes: 17 (MXFP4) or 18 (NVFP4) per 32 values."""
+        return self.batch * self.rows * (self.k // 2 + self.k // self.block)
+
+    def cref(self):
+        return self._ref
+
+    def _plain_shapes(self):
+        lead = (self.batch,) if self.batch > 1 else ()
+        return lead + (self.rows, self.k // 2), lead + (self.rows, self.k // self.block)
+
+    @classmethod
+    def from_codes(cls, codes, scales, fmt: int, scale: float = 1.0) -> "MXMatrix":
+        """From plain rows on the device: ``codes`` uint8 ``[.., rows, k/2]`` (the even column in the low nibble),
+        ``scales`` uint8 ``[.., rows, k/32]`` (MXFP4) or ``[.., rows, k/16]`` (NVFP4); three dimensions: a batch."""
+        torch = _torch()
+        if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() not in (2, 3):
+            raise TypeError("codes must be a CUDA uint8 tensor [rows, k/2] or [batch, rows, k/2]")
+        batch = codes.shape[0] if codes.dim() == 3 else 1
+        m = cls(fmt, codes.shape[-2], 2 * codes.shape[-1], batch, scale, codes.device)
+        lead = tuple(codes.shape[:-1])
+        cp = _ptr(codes, "codes", torch.uint8, lead + (m.k // 2,), m.device)
+        sp = _ptr(scales, "scales", torch.uint8, lead + (m.k // m.block,), m.device)
+        _check(_launch(m.device, lib().q4_mx_pack, cp, sp, m._ref), "q4_mx_pack")
+        return m
+
+    def codes(self):
+        """``(codes, scales)`` in plain rows, as ``from_codes`` takes them."""
+        torch = _torch()
+        c, s = (torch.empty(shape, dtype=torch.uint8, device=self.device) for shape in self._plain_shapes())
+        _check(_launch(self.device, lib().q4_mx_unpack, self._ref, c.data_ptr(), s.data_ptr()), "q4_mx_unpack")
+        return c, s
+
+
+def _mx(m, name):
+    if not isinstance(m, MXMatrix):
+        raise TypeError("%s must be an MXMatrix" % name)
+    return m
+
+
+def _mx_src(x, gamma, eps, up):
+    """The q4_mx_src of ``x [.., k]`` (rows at an even distance, values next to each other), its rows and k."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a CUDA float32, float16 or bfloat16 tensor")
+    kind = _kind(x.dtype, "x")
+    if x.dim() not in (2, 3) or 0 in x.shape:
+        raise ValueError("x must be [rows, k] or [batch, rows, k], with rows")
+    k = x.shape[-1]
+    if x.dim() == 2:
+        rows, ld = x.shape[0], x.stride(0) if x.shape[0] > 1 else k
+    else:
+        if not x.is_contiguous():
+            raise ValueError("a batch x must be contiguous")
+        rows, ld = x.shape[0] * x.shape[1], k
+    if x.stride(-1) != 1 or ld < k:
+        raise ValueError("the values of a row of x must be next to each other")
+    up_p = gamma_p = None
+    if up is not None:
+        if gamma is not None:
+            raise ValueError("gamma (a norm) and up (a SwiGLU) exclude each other")
+        if not isinstance(up, torch.Tensor) or up.dtype != x.dtype or up.device != x.device or up.shape != x.shape:
+            raise ValueError("up must be like x")
+        if up.stride(-1) != 1 or (x.dim() == 2 and x.shape[0] > 1 and up.stride(0) != ld) or (
+                x.dim() == 3 and not up.is_contiguous()):
+            raise ValueError("up must have the strides of x")
+        up_p = up.data_ptr()
+    if gamma is not None:
+        gamma_p = _ptr(gamma, "gamma", torch.float32, (k,), x.device)
+    return _CMxSrc(x.data_ptr(), up_p, gamma_p, ld, kind, rows, k, float(eps))
+
+
+def q4_mx_quant(x, fmt: int = Q4_MX_MXFP4, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, out=None):
+    """``x`` (float32, float16 or bfloat16, ``[rows, k]`` or ``[batch, rows, k]``) as an ``MXMatrix``: as it is,
+    behind an RMSNorm (``gamma [k]`` float32, ``eps``), or behind a SwiGLU (silu(x) * ``up``).  Rows may be a view
+    (the halves of one projection's output).  ``scale``: NVFP4's factor of the whole matrix, such as
+    amax / (6 * 448).  ``out``: an MXMatrix of the same shape to write into (its scale holds)."""
+    src = _mx_src(x, gamma, eps, up)
+    batch = x.shape[0] if x.dim() == 3 else 1
+    if out is None:
+        out = MXMatrix(fmt, x.shape[-2], x.shape[-1], batch, scale, x.device)
+    elif (_mx(out, "out").rows, out.k, out.batch, out.device) != (x.shape[-2], x.shape[-1], batch, x.device):
+        raise ValueError("out has another shape or device than x")
+    _check(_launch(out.device, lib().q4_mx_quant, ctypes.byref(src), out._ref), "q4_mx_quant")
+    return out
+
+
+def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
+    """The values of ``m``, ``[rows, k]`` (or ``[batch, rows, k]``) of ``dtype`` (float32 by default)."""
+    torch = _torch()
+    m = _mx(m, "m")
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    kind = _kind(dtype, "dtype")
+    shape = ((m.batch,) if m.batch > 1 else ()) + (m.rows, m.k)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=m.device)
+    op = _ptr(out, "out", dtype, shape, m.device)
+    _check(_launch(m.device, lib().q4_mx_dequant, m._ref, kind, op), "q4_mx_dequant")
+    return out
+
+
+def _mx_gemm_ws(W, nb):
+    """Bytes of q4_mx_gemm's workspace (by the shapes alone), rounded up to whole 256s."""
+    n = W._gemm_ws.get(nb)
+    if n is None:
+        with _torch().cuda.device(W.device):
+            n = (int(lib().q4_mx_gemm_workspace_bytes(W._ref, nb)) + 255) // 256 * 256
+        W._gemm_ws[nb] = n
+    return n
+
+
+def q4_mx_gemm_workspace(W: MXMatrix, nb: int):
+    """A (zero-filled) workspace for ``q4_mx_gemm`` with ``nb`` rows, with room for the quantised rows; calls that
+    may run at the same time, captured ones too, need one each."""
+    n = _mx_gemm_ws(_mx(W, "W"), int(nb)) + int(lib().q4_mx_bytes(W.fmt, int(nb), W.k))
+    return _torch().zeros(n, dtype=_torch().uint8, device=W.device)
+
+
+def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, dtype=None,
+               out=None, workspace=None):
+    """``y = x W^T (+ r)`` with both sides in microscaled 4-bit: ``W [n, k]``; ``x`` an ``MXMatrix [nb, k]`` of the
+    same format, or a float tensor ``[nb, k]`` that is quantised to it first as ``q4_mx_quant`` does (``gamma``,
+    ``eps``, ``up``, ``scale``).  ``y`` and ``r`` are ``[nb, n]`` of ``dtype`` (by default x's, float32 for an
+    MXMatrix); ``out`` may be ``r``."""
+    torch = _torch()
+    W = _mx(W, "W")
+    dev, given = W.device, isinstance(x, MXMatrix)
+    if given:
+        if gamma is not None or up is not None:
+            raise ValueError("x is quantised already: gamma and up are q4_mx_quant's")
+        nb, k = x.rows, x.k
+    else:
+        src = _mx_src(x, gamma, eps, up)
+        nb, k = src.rows, src.k
+        if x.dim() != 2:
+            raise ValueError("x must be [nb, %d]" % W.k)
+    if x.device != dev:
+        raise ValueError("x is on %s, W on %s" % (x.device, dev))
+    if k != W.k:
+        raise ValueError("x must be [nb, %d]" % W.k)
+    if dtype is None:
+        dtype = out.dtype if out is not None else torch.float32 if given else x.dtype
+    kind, shape = _kind(dtype, "dtype"), (nb, W.rows)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    op = _ptr(out, "out", dtype, shape, dev)
+    nbytes = nb * W.rows * out.element_size()
+    apart = [(W._c.dev, W.nbytes)]
+    rp = None
+    if r is not None:
+        rp = _ptr(r, "r", dtype, shape, dev)
+        if rp != op:
+            apart.append((rp, nbytes))
+    room = 0 if given else int(lib().q4_mx_bytes(W.fmt, nb, W.k))
+    ws = _mx_gemm_ws(W, nb)
+    if workspace is None:  # zero-filled: its counters start at zero
+        workspace = q4_mx_gemm_workspace(W, nb)
+    else:
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=ws + room)
+    wp = workspace.data_ptr()
+    if given:
+        apart.append((x._c.dev, x.nbytes))
+        _apart(op, nbytes, *apart)
+        _check(_launch(dev, lib().q4_mx_gemm, W._ref, x._ref, rp, kind, op, wp, ws), "q4_mx_gemm")
+        return out
+    span = ((nb - 1) * src.ld + k) * x.element_size()
+    apart.append((src.x, span))
+    if up is not None:
+        apart.append((src.up, span))
+    _apart(op, nbytes, *apart)
+    X = _CMx(W.fmt, nb, k, 1, wp + ws, room, float(scale))
+    _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op, wp, ws),
+           "q4_mx_linear")
+    return out

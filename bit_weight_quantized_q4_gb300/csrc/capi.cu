@@ -1123,6 +1123,177 @@ extern "C" q4_status q4_logprobs(const float *logits, int32_t rows, int32_t n, c
     return Q4_OK;
 }
 
+// ---------------------------------------------------------------- microscaled 4-bit
+
+namespace {
+bool mx_fmt_ok(int32_t fmt) { return fmt == Q4_MX_MXFP4 || fmt == Q4_MX_NVFP4; }
+bool mx_shape_ok(int32_t rows, int32_t k) { return rows >= 1 && rows <= (1 << 24) && k >= 32 && k % 32 == 0 && k <= 65536; }
+bool dtype_ok(int32_t dtype) { return dtype >= Q4_T_F32 && dtype <= Q4_T_BF16; }
+size_t dtype_size(int32_t dtype) { return dtype == Q4_T_F32 ? 4 : 2; }
+constexpr int kMxMaxBatch = 1 << 16;
+
+// format and shape alone (what a workspace size needs), then the memory
+q4_status check_mx_shape(const q4_mx *m) {
+    if (!m) return Q4_ERR_NULL;
+    if (!mx_fmt_ok(m->fmt)) return Q4_ERR_UNSUPPORTED;
+    if (!mx_shape_ok(m->rows, m->k) || m->batch < 1 || m->batch > kMxMaxBatch) return Q4_ERR_SHAPE;
+    if ((long long)m->batch * m->rows > (1ll << 31) - 1) return Q4_ERR_SHAPE;
+    if (m->fmt == Q4_MX_MXFP4 ? m->scale != 1.f : !(m->scale >= 0x1p-60f && m->scale <= 0x1p60f)) return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+q4_status check_mx(const q4_mx *m) {
+    Q4_TRY(check_mx_shape(m));
+    if (!m->dev) return Q4_ERR_NULL;
+    if (m->bytes < q4::mx_bytes(m->fmt, m->rows, m->k) * (size_t)m->batch) return Q4_ERR_SHAPE;
+    return aligned16(m->dev) ? Q4_OK : Q4_ERR_ALIGN;
+}
+q4_status check_mx_src(const q4_mx_src *s) {
+    if (!s) return Q4_ERR_NULL;
+    if (!dtype_ok(s->dtype) || (s->gamma && s->up)) return Q4_ERR_UNSUPPORTED;
+    if (!mx_shape_ok(s->rows, s->k) || s->ld < s->k || s->ld > (1ll << 40)) return Q4_ERR_SHAPE;
+    Q4_TRY(check_act(s->x));
+    if (!aligned16(s->up) || !aligned16(s->gamma)) return Q4_ERR_ALIGN;
+    return (size_t)s->ld * dtype_size(s->dtype) % 16 == 0 ? Q4_OK : Q4_ERR_ALIGN;
+}
+q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
+    q4::MxQuantParams p{};
+    p.x = s->x;
+    p.up = s->up;
+    p.gamma = s->gamma;
+    p.out = (uint8_t *)out->dev;
+    p.ld = s->ld;
+    p.rows = out->rows;
+    p.k = s->k;
+    p.batch = out->batch;
+    p.eps = s->eps;
+    p.scale = out->scale;
+    cudaGetLastError();
+    if (q4::launch_mx_quant(p, out->fmt, s->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+// The multiprocessors a workspace is sized for: the current device's, or a
+// GB300's where there is none.
+int mx_sms() {
+    const int sms = num_sms();
+    return sms > 0 ? sms : 152;
+}
+q4::MxGemmParams mx_gemm_params(const q4_mx *W, int nb, int sms, int *ctas) {
+    q4::MxGemmParams p{};
+    p.n = W->rows;
+    p.nb = nb;
+    p.KS = q4::mx_ktiles(W->k);
+    *ctas = q4::mx_gemm_plan(p, W->fmt, sms);
+    return p;
+}
+constexpr size_t kMxCountBytes = q4::kMxMaxTiles * sizeof(int);
+
+q4_status check_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, const void *y, const void *ws,
+                        size_t ws_bytes) {
+    Q4_TRY(check_mx(W));
+    Q4_TRY(check_mx(X));
+    if (W->fmt != X->fmt || W->batch != 1 || X->batch != 1 || !dtype_ok(dtype)) return Q4_ERR_UNSUPPORTED;
+    if (W->k != X->k || X->rows > (1 << 20)) return Q4_ERR_SHAPE;
+    Q4_TRY(check_act(y));
+    if (!aligned16(r)) return Q4_ERR_ALIGN;
+    if (!ws || ws_bytes < q4_mx_gemm_workspace_bytes(W, X->rows)) return Q4_ERR_WORKSPACE;
+    return aligned16(ws) ? Q4_OK : Q4_ERR_ALIGN;
+}
+q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *ws, bool early,
+                  cudaStream_t stream) {
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
+    int ctas = 0;
+    q4::MxGemmParams p = mx_gemm_params(W, X->rows, sms, &ctas);
+    p.w = (const uint8_t *)W->dev;
+    p.x = (const uint8_t *)X->dev;
+    p.r = r;
+    p.y = y;
+    p.count = (int *)ws;
+    p.part = (float *)((char *)ws + kMxCountBytes);
+    p.alpha = W->scale * X->scale;
+    p.early = early;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    p.wait_cycles = g_wait_cycles;
+    p.extra_tx = g_extra_tx;
+    cudaGetLastError();
+    if (q4::launch_mx_gemm(p, W->fmt, dtype, ctas, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+}  // namespace
+
+extern "C" size_t q4_mx_bytes(int32_t fmt, int32_t rows, int32_t k) {
+    return mx_fmt_ok(fmt) && mx_shape_ok(rows, k) ? q4::mx_bytes(fmt, rows, k) : 0;
+}
+
+extern "C" q4_status q4_mx_quant(const q4_mx_src *src, const q4_mx *out, cudaStream_t stream) {
+    Q4_TRY(check_mx_src(src));
+    Q4_TRY(check_mx(out));
+    if (src->k != out->k || (long long)src->rows != (long long)out->rows * out->batch) return Q4_ERR_SHAPE;
+    return mx_quant(src, out, stream);
+}
+
+extern "C" q4_status q4_mx_dequant(const q4_mx *m, int32_t dtype, void *out, cudaStream_t stream) {
+    Q4_TRY(check_mx(m));
+    if (!dtype_ok(dtype)) return Q4_ERR_UNSUPPORTED;
+    Q4_TRY(check_act(out));
+    q4::MxCopyParams p{};
+    p.mx = (uint8_t *)m->dev;
+    p.out = out;
+    p.rows = m->rows;
+    p.k = m->k;
+    p.batch = m->batch;
+    p.scale = m->scale;
+    cudaGetLastError();
+    if (q4::launch_mx_dequant(p, m->fmt, dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
+static q4_status mx_rows(const q4_mx *m, uint8_t *codes, uint8_t *scales, bool unpack, cudaStream_t stream) {
+    Q4_TRY(check_mx(m));
+    Q4_TRY(check_act(codes));
+    Q4_TRY(check_act(scales));
+    q4::MxCopyParams p{};
+    p.mx = (uint8_t *)m->dev;
+    p.codes = codes;
+    p.scales = scales;
+    p.rows = m->rows;
+    p.k = m->k;
+    p.batch = m->batch;
+    cudaGetLastError();
+    if (q4::launch_mx_pack(p, m->fmt, unpack, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+extern "C" q4_status q4_mx_pack(const uint8_t *codes, const uint8_t *scales, const q4_mx *out, cudaStream_t stream) {
+    return mx_rows(out, const_cast<uint8_t *>(codes), const_cast<uint8_t *>(scales), false, stream);
+}
+extern "C" q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scales, cudaStream_t stream) {
+    return mx_rows(m, codes, scales, true, stream);
+}
+
+extern "C" size_t q4_mx_gemm_workspace_bytes(const q4_mx *W, int32_t nb) {
+    if (check_mx_shape(W) != Q4_OK || W->batch != 1 || nb < 1 || nb > (1 << 20)) return 0;
+    int ctas = 0;
+    const q4::MxGemmParams p = mx_gemm_params(W, nb, mx_sms(), &ctas);
+    return kMxCountBytes + q4::mx_gemm_part_bytes(p, ctas);
+}
+
+extern "C" q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+    Q4_TRY(check_mx_gemm(W, X, r, dtype, y, workspace, workspace_bytes));
+    return mx_gemm(W, X, r, dtype, y, workspace, false, stream);
+}
+
+extern "C" q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype,
+                                  void *y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    Q4_TRY(check_mx_src(src));
+    Q4_TRY(check_mx_gemm(W, X, r, dtype, y, workspace, workspace_bytes));
+    if (src->k != X->k || src->rows != X->rows) return Q4_ERR_SHAPE;
+    int *err = nullptr;  // resolved before anything is launched
+    Q4_TRY(kernel_err_ptr(&err));
+    Q4_TRY(mx_quant(src, X, stream));
+    return mx_gemm(W, X, r, dtype, y, workspace, true, stream);
+}
+
 extern "C" q4_status q4_debug_wait_limits(int64_t barrier_polls, int32_t barrier_extra, int64_t copy_wait_cycles,
                                           int32_t copy_extra_bytes) {
     if (barrier_extra < 0 || barrier_extra > 1 || copy_extra_bytes < 0 || copy_extra_bytes > 4096 ||

@@ -1,0 +1,146 @@
+// mx_common.cuh -- what the kernels of the microscaled 4-bit formats share: the
+// stored forms, and the block-scaled tensor core (tcgen05 kind::mxf4 and
+// kind::mxf4nvf4).
+//
+// A code is E2M1: 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign.  MXFP4: blocks of 32
+// share an E8M0 power of two (255: NaN).  NVFP4: blocks of 16 share an E4M3
+// factor (127: NaN), the matrix an fp32 one.
+#pragma once
+#include "gemv_launch.cuh"
+#include "paged.cuh"
+#include "tc_common.cuh"
+#include "tensor_map.h"
+
+namespace q4 {
+namespace dev {
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// Offset in a record of byte `c` (of 128) of row r's codes, and of row r's scale
+// word w.
+__device__ __forceinline__ uint32_t mx_code_off(int r, int c) {
+    return (uint32_t)(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 15));
+}
+__device__ __forceinline__ uint32_t mx_scale_off(int r, int w) {
+    return (uint32_t)(kMxCodes + w * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
+}
+
+// Eight values as codes, value i in bits 4 i .. (to nearest, ties to the even
+// code, within 6).
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
+}
+__device__ __forceinline__ uint32_t e2m1(float v) {
+    uint16_t w;
+    asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.u16.u8 %0, a;\n\t}"
+        : "=h"(w)
+        : "f"(v), "f"(0.f));
+    return w & 15u;
+}
+// The value of the code in bits 0-3: sign (1 + m / 2) 2^(e - 1), or m / 2 for e = 0.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    // an f32 with the code's exponent and mantissa, 2^-126 subnormals at e = 0,
+    // times 2^126
+    return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(253u << 23);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t b) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(b & 255u));
+    return __half2float(__ushort_as_half((unsigned short)h));
+}
+// 2^(E - 127); E = 255: NaN.
+__device__ __forceinline__ float e8m0_value(uint32_t e) {
+    return __uint_as_float(e == 0u ? 0x00400000u : e == 255u ? 0x7FC00000u : e << 23);
+}
+template <int FMT>
+__device__ __forceinline__ float mx_scale_value(uint32_t b) {
+    return FMT == 0 ? e8m0_value(b) : e4m3_value(b);
+}
+
+// The scale byte of a block whose largest magnitude has the bits `a`, and the
+// factor its values are multiplied with before they are rounded to codes.
+//   MXFP4: the smallest power of two s with a <= 6 s = 1.5 * 2^2 s, 2^-127 at least.
+//   NVFP4: a / (6 g) to the nearest E4M3, 448 at most; six_g = 6 g.
+// A block with an infinity or NaN: a NaN scale (and any finite codes).
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_block_scale(uint32_t a, float g, float six_g, float &mul) {
+    if constexpr (FMT == 0) {
+        const int E = max((int)(a >> 23) - ((a & 0x7FFFFFu) > 0x400000u ? 1 : 2), 0);
+        mul = __uint_as_float((uint32_t)(254 - E) << 23);
+        if (a < kInfBits) return (uint32_t)E;
+        mul = 0.f;
+        return 255u;
+    } else {
+        const float t = fminf(__fdiv_rn(__uint_as_float(a), six_g), 448.f);
+        uint16_t b;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(t));
+        const float sg = e4m3_value(b) * g;
+        mul = (b & 255u) ? __frcp_rn(sg) : 0.f;
+        if (a < kInfBits) return b & 255u;
+        mul = 0.f;
+        return 127u;
+    }
+}
+// Codes of values whose factor is 0: zeros, though a value may be NaN or
+// infinite.
+__device__ __forceinline__ float mx_scaled(float v, float mul) { return mul == 0.f ? 0.f : v * mul; }
+
+// ------------------------------------------------------------------ tensor core
+
+// D[tmem] (+)= sum over blocks of sA sB A B^T, M = 128, N, K = 64, one thread.
+// a, b: lower words of the operands' descriptors (128-byte swizzle, K-major); sa,
+// sb: the scale factors' tensor-memory addresses.  Descriptor of the instruction:
+// bits 4-5 and 29-30 the byte of sb's and sa's word where the blocks' factors
+// begin, 7-9 and 10-11 the types (1: E2M1), 17-22 N / 8, 23 the factors' type (1:
+// E8M0, 0: E4M3), 27-28 M / 128.
+template <int FMT>
+__device__ __forceinline__ constexpr uint32_t mx_idesc(int N, int id) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (FMT == 0 ? 1u << 23 : 0u) | (1u << 27) |
+           ((uint32_t)id << 4) | ((uint32_t)id << 29);
+}
+template <int FMT>
+__device__ __forceinline__ void mx_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                       uint32_t acc) {
+    if constexpr (FMT == 0)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "n"(tc::kSw128Hi)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d),
+            "r"(a), "r"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc), "n"(tc::kSw128Hi)
+            : "memory");
+}
+// One word of 128 rows' scales (512 bytes of shared memory) into four columns of
+// tensor memory, the same in all four quarters of the lanes.  The descriptor: no
+// swizzle, groups of 8 rows of 16 bytes 128 bytes apart.
+__device__ __forceinline__ void mx_copy_scales(uint32_t taddr, uint32_t saddr) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(tc::smem_desc(saddr, 128, 128))
+                 : "memory");
+}
+
+// global -> shared bulk copy without a cache hint.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace dev
+}  // namespace q4

@@ -480,6 +480,74 @@ struct LogprobParams {
 };
 int launch_logprobs(const LogprobParams &p, int sms, void *stream);
 
+// ---------------------------------------------------------------- microscaled 4-bit
+// A microscaled matrix [rows][k] (mx_common.cuh) is stored in records of 128
+// rows x 256 columns, [row tile][column tile]:
+//   bytes [0, 16384)  the codes: 128 bytes a row, two E2M1 codes a byte (the even
+//                     column in the low nibble), as a shared-memory operand in the
+//                     128-byte swizzle: 16-byte part c of row r at part c ^ (r % 8);
+//   then              the scales, 4 blocks a word: word w of row r, 512 w + 16 (r %
+//                     32) + 4 (r / 32), holds blocks 4 w .. 4 w + 3 (of 32 columns
+//                     for MXFP4, 2 words; of 16 for NVFP4, 4 words), as
+//                     tcgen05.cp.32x128b lays them over the tensor memory's lanes.
+// Columns from k on are zero codes with zero scales; what rows behind the last
+// hold is never used (each reaches its own results only).
+constexpr int kMxRows = 128, kMxK = 256, kMxCodes = kMxRows * kMxK / 2;
+Q4_HD constexpr int mx_words(int fmt) { return fmt == 0 ? 2 : 4; }
+Q4_HD constexpr int mx_block(int fmt) { return fmt == 0 ? 32 : 16; }
+Q4_HD constexpr int mx_rec(int fmt) { return kMxCodes + 512 * mx_words(fmt); }
+Q4_HD constexpr int mx_ktiles(int k) { return (k + kMxK - 1) / kMxK; }
+Q4_HD constexpr int mx_rtiles(int rows) { return (rows + kMxRows - 1) / kMxRows; }
+inline size_t mx_bytes(int fmt, int rows, int k) {
+    return (size_t)mx_rtiles(rows) * mx_ktiles(k) * mx_rec(fmt);
+}
+
+// Quantising rows (mx_quant.cu): x [rows][ld], optionally behind an RMSNorm
+// (gamma) or a SwiGLU (up, like x).  batch: matrices of `rows` rows each, one
+// after another in x and in out.
+struct MxQuantParams {
+    const void *x, *up;
+    const float *gamma;
+    uint8_t *out;
+    long long ld;
+    int rows, k, batch;
+    float eps, scale;
+};
+int launch_mx_quant(const MxQuantParams &p, int fmt, int dtype, void *stream);
+// Back into values [batch][rows][k]; and the codes and scales in plain rows
+// ([batch][rows][k / 2], [batch][rows][k / block]), each way.
+struct MxCopyParams {
+    uint8_t *mx;
+    void *out;
+    uint8_t *codes, *scales;
+    int rows, k, batch;
+    float scale;
+};
+int launch_mx_dequant(const MxCopyParams &p, int fmt, int dtype, void *stream);
+int launch_mx_pack(const MxCopyParams &p, int fmt, bool unpack, void *stream);
+
+// The product y[nb][n] = alpha x w^T + r of two microscaled matrices (mx_gemm.cu).
+struct MxGemmParams {
+    const uint8_t *w, *x;
+    const void *r;         // [nb][n] of y's type or nullptr; may be y
+    void *y;
+    int *count;            // a word a tile, zero between calls (split tiles)
+    float *part;           // partial tiles, two a CTA
+    int *err;
+    long long wait_cycles;
+    int extra_tx;          // bytes the first stage expects beyond its copies (0; testing only)
+    int n, nb, MT, CT, NB, KS;  // row tiles of w, column tiles of NB rows of x, column tiles of k
+    int split;             // the CTAs divide the stages of all tiles evenly (else whole tiles)
+    int stages, stage_bytes;
+    int early;             // w is complete before the kernel in front of this one began
+    float alpha;
+};
+// Sets the tiles, the split and the ring of p (n, nb, KS given) and returns the CTAs.
+int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
+constexpr int kMxMaxTiles = 2048;  // tiles of a split product (its counters)
+size_t mx_gemm_part_bytes(const MxGemmParams &p, int ctas);
+int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
+
 int launch_gemv_q4_0(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_affine(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_q8_0(const GemvParams &p, const Plan &plan, void *stream);

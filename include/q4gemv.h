@@ -326,7 +326,7 @@ q4_status q4_decode_check(const void *workspace, cudaStream_t stream);
 /* Synchronises `stream` and reports whether any GEMV-family kernel of this
  * library on the current device (q4_gemv, q4_nrm_gemv, q4_dual_gemv,
  * q4_gus_nrm, q4_res_gemv, q4_argmax, q4_argmax_noalloc, q4_gemm,
- * q4_attn_decode, q4_attn_prefill, q4_attn_paged) gave up waiting for its weight (or K/V)
+ * q4_attn_decode, q4_attn_prefill, q4_attn_paged, q4_mx_gemm, q4_mx_linear) gave up waiting for its weight (or K/V)
  * copies since the last check, or a kernel of the paged cache or of
  * q4_logprobs met a position, page or token out of range (Q4_ERR_CUDA; the
  * flag is then cleared) or not (Q4_OK).  Each kernel bounds every such wait (about a
@@ -546,6 +546,78 @@ q4_status q4_attn_paged(const q4_kv_pages *pages, const float *q, const float *k
  * 0 <= top <= min(32, n) (NULL for top = 0).  1 <= n <= 2^24. */
 q4_status q4_logprobs(const float *logits, int32_t rows, int32_t n, const int32_t *tokens, int32_t top,
                       float *logprob, float *entropy, float *top_val, int32_t *top_idx, cudaStream_t stream);
+
+/* ---------------------------------------------------------------- microscaled 4-bit
+ * Microscaled 4-bit floating point (library-specific; the block formats above
+ * are integers): a value is an E2M1 code -- 0, .5, 1, 1.5, 2, 3, 4, 6 and a sign
+ * -- times the scale of its block of consecutive columns.
+ *   Q4_MX_MXFP4: blocks of 32, the scale a byte E for 2^(E - 127), 255 for NaN;
+ *   Q4_MX_NVFP4: blocks of 16, the scale an E4M3 byte (sign 0, 127 for NaN), and
+ *     an fp32 factor `scale` of the whole matrix.
+ * A q4_mx views `batch` matrices [rows][k] one after another, in a layout of this
+ * library: records of 128 rows x 256 columns that the tensor core takes as they
+ * are, q4_mx_bytes(fmt, rows, k) for each matrix (rows padded to 128, columns to
+ * 256).  k % 32 == 0, k <= 65536, rows <= 2^24; scale in [2^-60, 2^60], and 1
+ * for MXFP4.  Rows of codes may be activations as well as weights. */
+typedef enum { Q4_MX_MXFP4 = 0, Q4_MX_NVFP4 = 1 } q4_mx_format;
+typedef struct {
+    int32_t fmt, rows, k, batch;
+    void *dev;          /* device, 16-byte aligned, batch * q4_mx_bytes(fmt, rows, k) bytes */
+    size_t bytes;
+    float scale;
+} q4_mx;
+
+/* Bytes of one matrix (0 on a bad shape or format). */
+size_t q4_mx_bytes(int32_t fmt, int32_t rows, int32_t k);
+
+/* Rows to be quantised: x [rows][k] of dtype (f32, f16, bf16), row i at x + i * ld
+ * values (ld * size a multiple of 16 bytes, ld >= k).  gamma not NULL: behind an
+ * RMSNorm, x / sqrt(mean x^2 + eps) * gamma ([k] fp32).  up not NULL: behind a
+ * SwiGLU, x / (1 + exp(-x)) * up (up like x, the same ld).  Not both.  The
+ * arithmetic in front of the rounding is fp32. */
+typedef struct {
+    const void *x, *up;
+    const float *gamma;
+    int64_t ld;
+    int32_t dtype, rows, k;
+    float eps;
+} q4_mx_src;
+
+/* Quantises src's rows (batch * rows of them) into out.  A block's scale is, of
+ * its largest magnitude a, for MXFP4 the smallest power of two s >= 2^-127 with a <=
+ * 6 s, so that no value is cut off; for NVFP4 min(a / (6 scale), 448) to the
+ * nearest E4M3 value (6 scale and the quotient in fp32).  A value becomes the
+ * nearest code of x / s, or of x * (1 / (s scale)) with both steps in fp32 (ties
+ * to the even code, at most 6 in magnitude; a scale of 0: zeros).  A block with a
+ * NaN or an infinity gets the NaN scale: it reads back, and multiplies, as NaN. */
+q4_status q4_mx_quant(const q4_mx_src *src, const q4_mx *out, cudaStream_t stream);
+
+/* The values of m, [batch][rows][k] of dtype (rounded once to it). */
+q4_status q4_mx_dequant(const q4_mx *m, int32_t dtype, void *out, cudaStream_t stream);
+
+/* Codes and scales in plain rows, device to device: codes [batch][rows][k / 2],
+ * byte i holding column 2 i in its low nibble and 2 i + 1 in its high one; scales
+ * [batch][rows][k / 32] (MXFP4) or [k / 16] (NVFP4).  Lossless each way. */
+q4_status q4_mx_pack(const uint8_t *codes, const uint8_t *scales, const q4_mx *out, cudaStream_t stream);
+q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scales, cudaStream_t stream);
+
+/* y[t][i] = sum_k w[i][k] x[t][k] (+ r[t][i]) of the stored values, fp32 sums
+ * rounded once to y's type: W [n][k], X [nb][k] of the same format (batch 1 each),
+ * y and r [nb][n] of dtype, r NULL or, in place, y itself; else y must not overlap
+ * an input.  Any nb from 1 to 2^20.
+ * workspace: q4_mx_gemm_workspace_bytes(W, nb) device bytes, zero-filled by the
+ * caller before its first use (every call leaves its counters zero, so calls of
+ * different shapes can share one that is large enough); calls (and captured
+ * graphs) that share one must not run at the same time.  The size goes by the
+ * current device.  Results do not depend on scheduling. */
+size_t q4_mx_gemm_workspace_bytes(const q4_mx *W, int32_t nb);
+q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *workspace,
+                     size_t workspace_bytes, cudaStream_t stream);
+
+/* q4_mx_quant of src into X (W's format, src's rows; the caller's room), then
+ * q4_mx_gemm, whose weight copies run while the rows are quantised. */
+q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype, void *y,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Launch plan the library uses for a GEMV-shaped call (host-only; exposed
  * for tests and tuning).  tiles: 16-row tiles of the launch, chunks: 128-k
