@@ -150,9 +150,8 @@ def lib() -> ctypes.CDLL:
             "q4_mx_dequant": (I32, [MX, I32, P, P]),
             "q4_mx_pack": (I32, [P, P, MX, P]),
             "q4_mx_unpack": (I32, [MX, P, P, P]),
-            "q4_mx_gemm_workspace_bytes": (SZ, [MX, I32]),
-            "q4_mx_gemm": (I32, [MX, MX, P, I32, P, P, SZ, P]),
-            "q4_mx_linear": (I32, [MX, SRC, MX, P, I32, P, P, SZ, P]),
+            "q4_mx_gemm": (I32, [MX, MX, P, I32, P, P]),
+            "q4_mx_linear": (I32, [MX, SRC, MX, P, I32, P, P]),
             "q4_status_str": (ctypes.c_char_p, [I32]),
         }
         for name, (res, args) in sig.items():
@@ -1016,13 +1015,14 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
 
 # ---------------------------------------------------------------- microscaled 4-bit
 
-def _kinds():
-    torch = _torch()
-    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_kinds = {}
 
 
 def _kind(dtype, name):
-    kind = _kinds().get(dtype)
+    if not _kinds:
+        torch = _torch()
+        _kinds.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    kind = _kinds.get(dtype)
     if kind is None:
         raise TypeError("%s must be float32, float16 or bfloat16" % name)
     return kind
@@ -1047,7 +1047,7 @@ class MXMatrix:
         self.device = tensor.device
         self._c = _CMx(self.fmt, self.rows, self.k, self.batch, tensor.data_ptr(), self.nbytes, self.scale)
         self._ref = ctypes.byref(self._c)
-        self._gemm_ws = {}
+        self._room = {}
 
     @property
     def block(self) -> int:
@@ -1157,21 +1157,18 @@ def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
     return out
 
 
-def _mx_gemm_ws(W, nb):
-    """Bytes of q4_mx_gemm's workspace (by the shapes alone), rounded up to whole 256s."""
-    n = W._gemm_ws.get(nb)
+def _mx_room(W, nb):
+    """Bytes of nb quantised rows of W's format and width (by the shapes alone)."""
+    n = W._room.get(nb)
     if n is None:
-        with _torch().cuda.device(W.device):
-            n = (int(lib().q4_mx_gemm_workspace_bytes(W._ref, nb)) + 255) // 256 * 256
-        W._gemm_ws[nb] = n
+        n = W._room[nb] = int(lib().q4_mx_bytes(W.fmt, nb, W.k))
     return n
 
 
 def q4_mx_gemm_workspace(W: MXMatrix, nb: int):
-    """A (zero-filled) workspace for ``q4_mx_gemm`` with ``nb`` rows, with room for the quantised rows; calls that
-    may run at the same time, captured ones too, need one each."""
-    n = _mx_gemm_ws(_mx(W, "W"), int(nb)) + int(lib().q4_mx_bytes(W.fmt, int(nb), W.k))
-    return _torch().zeros(n, dtype=_torch().uint8, device=W.device)
+    """A workspace for ``q4_mx_gemm`` with up to ``nb`` float rows: the room of the quantised rows.  Calls that may
+    run at the same time, captured ones too, need one each."""
+    return _torch().empty(_mx_room(_mx(W, "W"), int(nb)), dtype=_torch().uint8, device=W.device)
 
 
 def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, dtype=None,
@@ -1209,24 +1206,22 @@ def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, sc
         rp = _ptr(r, "r", dtype, shape, dev)
         if rp != op:
             apart.append((rp, nbytes))
-    room = 0 if given else int(lib().q4_mx_bytes(W.fmt, nb, W.k))
-    ws = _mx_gemm_ws(W, nb)
-    if workspace is None:  # zero-filled: its counters start at zero
-        workspace = q4_mx_gemm_workspace(W, nb)
-    else:
-        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=ws + room)
-    wp = workspace.data_ptr()
     if given:
         apart.append((x._c.dev, x.nbytes))
         _apart(op, nbytes, *apart)
-        _check(_launch(dev, lib().q4_mx_gemm, W._ref, x._ref, rp, kind, op, wp, ws), "q4_mx_gemm")
+        _check(_launch(dev, lib().q4_mx_gemm, W._ref, x._ref, rp, kind, op), "q4_mx_gemm")
         return out
+    room = _mx_room(W, nb)
+    if workspace is None:
+        workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+    else:
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=room)
+    wp = workspace.data_ptr()
     span = ((nb - 1) * src.ld + k) * x.element_size()
     apart.append((src.x, span))
     if up is not None:
         apart.append((src.up, span))
     _apart(op, nbytes, *apart)
-    X = _CMx(W.fmt, nb, k, 1, wp + ws, room, float(scale))
-    _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op, wp, ws),
-           "q4_mx_linear")
+    X = _CMx(W.fmt, nb, k, 1, wp, room, float(scale))
+    _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op), "q4_mx_linear")
     return out

@@ -1171,45 +1171,27 @@ q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
     if (q4::launch_mx_quant(p, out->fmt, s->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
     return Q4_OK;
 }
-// The multiprocessors a workspace is sized for: the current device's, or a
-// GB300's where there is none.
-int mx_sms() {
-    const int sms = num_sms();
-    return sms > 0 ? sms : 152;
-}
-q4::MxGemmParams mx_gemm_params(const q4_mx *W, int nb, int sms, int *ctas) {
-    q4::MxGemmParams p{};
-    p.n = W->rows;
-    p.nb = nb;
-    p.KS = q4::mx_ktiles(W->k);
-    *ctas = q4::mx_gemm_plan(p, W->fmt, sms);
-    return p;
-}
-constexpr size_t kMxCountBytes = q4::kMxMaxTiles * sizeof(int);
-
-q4_status check_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, const void *y, const void *ws,
-                        size_t ws_bytes) {
+q4_status check_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, const void *y) {
     Q4_TRY(check_mx(W));
     Q4_TRY(check_mx(X));
     if (W->fmt != X->fmt || W->batch != 1 || X->batch != 1 || !dtype_ok(dtype)) return Q4_ERR_UNSUPPORTED;
     if (W->k != X->k || X->rows > (1 << 20)) return Q4_ERR_SHAPE;
     Q4_TRY(check_act(y));
-    if (!aligned16(r)) return Q4_ERR_ALIGN;
-    if (!ws || ws_bytes < q4_mx_gemm_workspace_bytes(W, X->rows)) return Q4_ERR_WORKSPACE;
-    return aligned16(ws) ? Q4_OK : Q4_ERR_ALIGN;
+    return aligned16(r) ? Q4_OK : Q4_ERR_ALIGN;
 }
-q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *ws, bool early,
+q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, bool early,
                   cudaStream_t stream) {
     const int sms = num_sms();
     if (sms <= 0) return Q4_ERR_CUDA;
-    int ctas = 0;
-    q4::MxGemmParams p = mx_gemm_params(W, X->rows, sms, &ctas);
+    q4::MxGemmParams p{};
+    p.n = W->rows;
+    p.nb = X->rows;
+    p.KS = q4::mx_ktiles(W->k);
+    const int ctas = q4::mx_gemm_plan(p, W->fmt, sms);
     p.w = (const uint8_t *)W->dev;
     p.x = (const uint8_t *)X->dev;
     p.r = r;
     p.y = y;
-    p.count = (int *)ws;
-    p.part = (float *)((char *)ws + kMxCountBytes);
     p.alpha = W->scale * X->scale;
     p.early = early;
     Q4_TRY(kernel_err_ptr(&p.err));
@@ -1270,28 +1252,21 @@ extern "C" q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scale
     return mx_rows(m, codes, scales, true, stream);
 }
 
-extern "C" size_t q4_mx_gemm_workspace_bytes(const q4_mx *W, int32_t nb) {
-    if (check_mx_shape(W) != Q4_OK || W->batch != 1 || nb < 1 || nb > (1 << 20)) return 0;
-    int ctas = 0;
-    const q4::MxGemmParams p = mx_gemm_params(W, nb, mx_sms(), &ctas);
-    return kMxCountBytes + q4::mx_gemm_part_bytes(p, ctas);
-}
-
-extern "C" q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *workspace,
-                                size_t workspace_bytes, cudaStream_t stream) {
-    Q4_TRY(check_mx_gemm(W, X, r, dtype, y, workspace, workspace_bytes));
-    return mx_gemm(W, X, r, dtype, y, workspace, false, stream);
+extern "C" q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y,
+                                cudaStream_t stream) {
+    Q4_TRY(check_mx_gemm(W, X, r, dtype, y));
+    return mx_gemm(W, X, r, dtype, y, false, stream);
 }
 
 extern "C" q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype,
-                                  void *y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+                                  void *y, cudaStream_t stream) {
     Q4_TRY(check_mx_src(src));
-    Q4_TRY(check_mx_gemm(W, X, r, dtype, y, workspace, workspace_bytes));
+    Q4_TRY(check_mx_gemm(W, X, r, dtype, y));
     if (src->k != X->k || src->rows != X->rows) return Q4_ERR_SHAPE;
     int *err = nullptr;  // resolved before anything is launched
     Q4_TRY(kernel_err_ptr(&err));
     Q4_TRY(mx_quant(src, X, stream));
-    return mx_gemm(W, X, r, dtype, y, workspace, true, stream);
+    return mx_gemm(W, X, r, dtype, y, true, stream);
 }
 
 extern "C" q4_status q4_debug_wait_limits(int64_t barrier_polls, int32_t barrier_extra, int64_t copy_wait_cycles,

@@ -18,31 +18,36 @@ namespace q4 {
 namespace dev {
 
 constexpr int kMxgThreads = 192;
-constexpr int kMxgMaxN = 192;      // columns of a tile
+constexpr int kMxgMaxN = 192;       // columns of a tile
+constexpr int kMxgSmallN = 64;      // up to here two CTAs of an SM
 constexpr int kMxgMaxStages = 12;
-constexpr int kMxgSf = 2 * kMxgMaxN;  // tensor memory: two accumulators, then two sets of scales
 constexpr int kMxgBars = 8 * (2 * kMxgMaxStages + 5) + 16;
 
-// CTA c's share of the stages of all tiles, [mx_first(c), mx_first(c + 1)); and
-// the CTA that has unit u.
-__device__ __forceinline__ int mx_first(int c, int units, int ctas) { return (int)((long long)units * c / ctas); }
-__device__ __forceinline__ int mx_cta_of(int u, int units, int ctas) {
-    return (int)((((long long)u + 1) * ctas - 1) / units);
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A value into the shared memory (offset as here) of the cluster's CTA `rank`.
+__device__ __forceinline__ void store_peer(uint32_t saddr, uint32_t rank, float v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(saddr),
+        "r"(rank), "f"(v)
+        : "memory");
 }
 
 template <int FMT, typename T>
-__global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_constant__ MxGemmParams p) {
+__global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_constant__ MxGemmParams p) {
     constexpr int W = mx_words(FMT), REC = mx_rec(FMT);
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int S = p.stages, KS = p.KS, tiles = p.MT * p.CT, ctas = gridDim.x, cta = blockIdx.x;
+    const int S = p.stages, C = p.C, tiles = p.MT * p.CT, rank = C > 1 ? blockIdx.x % C : 0;
+    const int k0 = p.KS * rank / C, k1 = p.KS * (rank + 1) / C;  // this CTA's part of k
+    const uint32_t cols_tm = p.acc == kMxgMaxN ? 512 : 256, sf_tm = 2 * p.acc;  // tensor memory: accumulators, two sets of scales
     const uint32_t ring = smem_u32(sm), bars = ring + S * p.stage_bytes;
     // barriers: a stage has landed, a stage's MMAs are done; of an accumulator: it is
     // complete, it has been read; the last MMAs of all
     const uint32_t b_full = bars, b_empty = b_full + 8 * kMxgMaxStages, b_acc = b_empty + 8 * kMxgMaxStages,
                    b_read = b_acc + 16, b_drain = b_read + 16;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + S * p.stage_bytes + 8 * (2 * kMxgMaxStages + 5));
-    volatile int *last = reinterpret_cast<volatile int *>(tslot + 1);
     if (warp == 0) {
         if (lane < S) {
             mbar_init(b_full + 8 * lane, 1);
@@ -56,7 +61,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        tc::tmem_alloc(smem_u32(tslot), 512);
+        tc::tmem_alloc(smem_u32(tslot), cols_tm);
         tc::tmem_relinquish();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -65,19 +70,10 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
     tc::fence_after_sync();
     const uint32_t tmem = *tslot;
 
-    const int units = tiles * KS, u0 = mx_first(cta, units, ctas), u1 = mx_first(cta + 1, units, ctas);
-    // this CTA's segments (tile, first and last stage): f(tile, k0, k1) until it says no
+    // this CTA's tiles: f(tile) until it says no
     auto walk = [&](auto f) {
-        if (!p.split) {
-            for (int t = cta; t < tiles; t += ctas)
-                if (!f(t, 0, KS)) return;
-        } else {
-            for (int u = u0; u < u1;) {
-                const int t = u / KS, k0 = u - t * KS, k1 = min(KS, k0 + u1 - u);
-                if (!f(t, k0, k1)) return;
-                u += k1 - k0;
-            }
-        }
+        for (int t = blockIdx.x / C; t < tiles; t += gridDim.x / C)
+            if (!f(t)) return;
     };
     // a tile's columns: the first, how many (whole 16s), and how many of them lie in
     // the first of the (two at most) row tiles of x that it covers
@@ -102,22 +98,22 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
                 const uint32_t bar = b_full + 8 * slot;
                 mbar_expect_tx(bar, bytes_of(ct) + extra);
                 extra = 0;
-                bulk_copy(ring + slot * p.stage_bytes, p.w + ((size_t)mt * KS + ks) * REC, REC, bar);
+                bulk_copy(ring + slot * p.stage_bytes, p.w + ((size_t)mt * p.KS + ks) * REC, REC, bar);
             };
             if (p.early) {
                 // the first stages' weights before what is in front of this kernel is done
-                walk([&](int t, int k0, int k1) {
+                walk([&](int t) {
                     const int ct = t / p.MT, mt = t - ct * p.MT;
                     for (int ks = k0; ks < k1 && issued < S; ++ks) copy_w(issued++, mt, ct, ks);
                     return issued < S;
                 });
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            walk([&](int t, int k0, int k1) {
+            walk([&](int t) {
                 const int ct = t / p.MT, mt = t - ct * p.MT;
                 int c0, N, n0;
                 cols(ct, c0, N, n0);
-                const uint8_t *x0 = p.x + (size_t)(c0 / kMxRows) * KS * REC, *x1 = x0 + (size_t)KS * REC;
+                const uint8_t *x0 = p.x + (size_t)(c0 / kMxRows) * p.KS * REC, *x1 = x0 + (size_t)p.KS * REC;
                 for (int ks = k0; ks < k1; ++ks, ++it) {
                     const int slot = it % S;
                     if (it >= issued) {
@@ -147,13 +143,13 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
         // ------------------------------------------------------------ MMAs
         int it = 0, seg = 0;
         bool ok = true;
-        walk([&](int t, int k0, int k1) {
+        walk([&](int t) {
             int c0, N, n0;
             cols(t / p.MT, c0, N, n0);
             const int buf = seg & 1;
             ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
             tc::fence_after_sync();
-            const uint32_t d = tmem + buf * kMxgMaxN, skip = (uint32_t)(c0 & (kMxRows - 1)) / 32;
+            const uint32_t d = tmem + buf * p.acc, skip = (uint32_t)(c0 & (kMxRows - 1)) / 32;
             const bool two = N > n0;
             for (int ks = k0; ok && ks < k1; ++ks, ++it) {
                 const int slot = it % S;
@@ -162,7 +158,7 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
                     const uint32_t a = ring + slot * p.stage_bytes, b = a + REC, sb = b + p.NB * 128;
-                    const uint32_t ta = tmem + kMxgSf + (it & 1) * 64, tb = ta + 16;
+                    const uint32_t ta = tmem + sf_tm + (it & 1) * 64, tb = ta + 16;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         mx_copy_scales(ta + 4 * w, a + kMxCodes + 512 * w);
@@ -195,114 +191,134 @@ __global__ void __launch_bounds__(kMxgThreads, 1) q4mx_gemm_kernel(const __grid_
         bool ok = true;
         T *y = (T *)p.y;
         const T *rs = (const T *)p.r;
-        // Columns c .. c + 15 of the tile: v alpha + r.
-        auto store = [&](int row, int col0, const float (&v)[16]) {
-            if (row >= p.n) return;
-            float add[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                add[i] = rs && col0 + i < p.nb ? to_f32(rs[(size_t)(col0 + i) * p.n + row]) : 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (col0 + i < p.nb) y[(size_t)(col0 + i) * p.n + row] = from_f32<T>(fmaf(v[i], p.alpha, add[i]));
-        };
-        walk([&](int t, int k0, int k1) {
+        walk([&](int t) {
             const int ct = t / p.MT, row = (t - ct * p.MT) * kMxRows + rl, buf = seg & 1;
             int c0, N, n0;
             cols(ct, c0, N, n0);
-            // (a wait that gave up: the counters are kept up, what is stored is undefined)
+            const int live = row < p.n ? min(N, p.nb - c0) : 0;  // columns to write
+            const size_t at = (size_t)c0 * p.n + row;
+            // the residual of 64 columns is under way before the sums are complete, then 48
+            // columns ahead (16 at a time, loaded when they were wanted, took 521 us instead
+            // of 270 for 8192 rows of 4096 x 14336)
+            T add[4][16];
+            auto fetch = [&](int s, int c) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) add[s][i] = c + i < live ? rs[at + (size_t)(c + i) * p.n] : from_f32<T>(0.f);
+            };
+            if (rs && C == 1)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) fetch(s, 16 * s);
             ok = ok && __all_sync(0xffffffffu, mbar_wait(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
             tc::fence_after_sync();
-            const uint32_t d = tmem + buf * kMxgMaxN + ((uint32_t)(32 * q) << 16);
-            const bool whole = k0 == 0 && k1 == KS;
-            float *mine = p.part + ((size_t)cta * 2 + (seg > 0)) * (p.NB * kMxRows) + rl;
-            for (int c = 0; c < N; c += 16) {
-                uint32_t w[16];
-                tc::ld16(d + c, w);
-                tc::wait_ld16(w);
-                float v[16];
+            const uint32_t d = tmem + buf * p.acc + ((uint32_t)(32 * q) << 16);
+            if (C == 1)
+                for (int cb = 0; cb < N; cb += 64)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-                if (whole) {
-                    store(row, c0 + c, v);
-                } else {
+                    for (int s = 0; s < 4; ++s) {
+                        const int c = cb + 16 * s;
+                        if (c >= N) break;
+                        uint32_t w[16];
+                        tc::ld16(d + c, w);
+                        tc::wait_ld16(w);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) __stcg(mine + (c + i) * kMxRows, v[i]);
-                }
-            }
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < live) {
+                                const float v = __uint_as_float(w[i]);
+                                y[at + (size_t)(c + i) * p.n] =
+                                    from_f32<T>(rs ? fmaf(v, p.alpha, to_f32(add[s][i])) : v * p.alpha);
+                            }
+                        if (rs) fetch(s, c + 64);
+                    }
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) bar_arrive(b_read + 8 * buf);
-            if (!whole) {
-                // the last of the tile's CTAs to finish adds their shares in CTA order
-                const int s0 = t * KS, f = mx_cta_of(s0, units, ctas), l = mx_cta_of(s0 + KS - 1, units, ctas);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (warp == 2 && lane == 0) {
-                    int before;
-                    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.count + t) : "memory");
-                    *last = before == l - f;
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (*last) {
-                    const size_t slot = (size_t)p.NB * kMxRows;
-                    const float *first = p.part + ((size_t)f * 2 + (mx_first(f, units, ctas) < s0)) * slot + rl;
-                    for (int c = 0; c < N; c += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __ldcg(first + (c + i) * kMxRows);
-                        for (int x = f + 1; x <= l; ++x) {
-                            const float *other = p.part + (size_t)x * 2 * slot + rl;
-                            float o[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __ldcg(other + (c + i) * kMxRows);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] += o[i];
-                        }
-                        store(row, c0 + c, v);
-                    }
-                    if (warp == 2 && lane == 0) p.count[t] = 0;  // zero again for the next call
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");  // the flag is read before the next tile's
-            }
             ++seg;
             return true;
         });
         if (!ok && lane == 0) atomicExch(p.err, 4);
+    }
+    if (C > 1) {
+        // the parts of k: each CTA sums its share of the columns, in the order of the ranks.
+        // The rings are done in all CTAs behind the first barrier: their room takes the parts.
+        __syncwarp();
+        cluster_sync();
+        int c0, N, n0;
+        const int t = blockIdx.x / C, ct = t / p.MT;
+        cols(ct, c0, N, n0);
+        const int per = (N + C - 1) / C, q = warp & 3, rl = 32 * q + lane, row = (t - ct * p.MT) * kMxRows + rl;
+        if (warp >= 2) {
+            const uint32_t d = tmem + ((uint32_t)(32 * q) << 16);
+            for (int c = 0; c < N; c += 16) {
+                uint32_t w[16];
+                tc::ld16(d + c, w);
+                tc::wait_ld16(w);
+                int to = c / per, left = c - to * per;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    store_peer(ring + 4 * ((rank * per + left) * kMxRows + rl), (uint32_t)to, __uint_as_float(w[i]));
+                    if (++left == per) {
+                        left = 0;
+                        ++to;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2 && row < p.n) {
+            const float *part = reinterpret_cast<const float *>(sm) + rl;
+            const T *rs = (const T *)p.r;
+            for (int i = 0; i < per; ++i) {
+                const int c = c0 + rank * per + i;
+                if (rank * per + i >= N || c >= p.nb) break;
+                const size_t at = (size_t)c * p.n + row;
+                const float add = rs ? to_f32(rs[at]) : 0.f;
+                float v = 0.f;
+                for (int x = 0; x < C; ++x) v += part[(x * per + i) * kMxRows];
+                ((T *)p.y)[at] = from_f32<T>(rs ? fmaf(v, p.alpha, add) : v * p.alpha);
+            }
+        }
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, 512);
+        tc::tmem_dealloc(tmem, cols_tm);
     }
 }
 
 }  // namespace dev
 
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
-    p.MT = mx_rtiles(p.n);
-    // one tile of columns up to 192 rows of x, else tiles of 192 or 128: whichever pads less
-    if (p.nb <= dev::kMxgMaxN) {
-        p.NB = (p.nb + 15) / 16 * 16;
-    } else {
-        const int a = (p.nb + 191) / 192 * 192, b = (p.nb + 127) / 128 * 128;
-        p.NB = b < a - a / 16 ? 128 : 192;
+    // The columns of a tile and the CTAs that share its k by an estimate of the
+    // busiest SM's time: a stage takes about as long as its bytes, (128 + NB) 1.4 ns
+    // (0.46 us at 192 columns), a cluster's sum about a microsecond and 10 ns a column.
+    const int W = mx_words(fmt);
+    double best = 0.0;
+    for (const int NB : {std::min((p.nb + 15) / 16 * 16, dev::kMxgMaxN), 64, 128}) {
+        if (best > 0.0 && NB >= p.nb) break;  // the first: all rows of x in one tile, or 192
+        const int MT = mx_rtiles(p.n), CT = (p.nb + NB - 1) / NB;
+        const long long tiles = (long long)MT * CT;
+        for (int C = 1; C <= 8 && C <= p.KS && (C == 1 || tiles * C <= sms); ++C) {
+            const double cost = (double)((tiles * C + sms - 1) / sms) * ((p.KS + C - 1) / C) * (128 + NB) * 1.4 +
+                                (C > 1 ? 1000.0 + 10.0 * NB : 0.0);
+            if (best > 0.0 && cost >= best) continue;
+            best = cost;
+            p.MT = MT;
+            p.CT = CT;
+            p.NB = NB;
+            p.C = C;
+        }
     }
-    p.CT = (p.nb + p.NB - 1) / p.NB;
-    const int W = mx_words(fmt), blocks = p.NB > 128 || p.CT > 1 ? 2 : 1;
-    p.stage_bytes = mx_rec(fmt) + p.NB * 128 + blocks * 512 * W;
-    p.stage_bytes = (p.stage_bytes + 1023) / 1024 * 1024;
-    p.stages = std::min<int>(dev::kMxgMaxStages, ((int)kSmemMax - dev::kMxgBars) / p.stage_bytes);
+    const int blocks = p.NB > 128 || (p.CT > 1 && p.NB % 128 != 0) ? 2 : 1;
+    p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + blocks * 512 * W + 1023) / 1024 * 1024;
     const long long tiles = (long long)p.MT * p.CT;
-    // whole tiles where the last wave of them is nearly full, else the stages evenly
-    const long long waves = (tiles + sms - 1) / sms;
-    p.split = tiles <= kMxMaxTiles && tiles * 8 < waves * sms * 7;
-    const long long units = tiles * p.KS;
-    return (int)std::min<long long>(p.split ? units : tiles, sms);
-}
-size_t mx_gemm_part_bytes(const MxGemmParams &p, int ctas) {
-    return p.split ? (size_t)ctas * 2 * p.NB * kMxRows * sizeof(float) : 0;
+    const bool two = p.NB <= dev::kMxgSmallN && tiles * p.C > sms;  // two CTAs of an SM
+    const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgBars;
+    p.stages = std::min(dev::kMxgMaxStages, room / p.stage_bytes);
+    p.acc = p.NB <= dev::kMxgSmallN ? dev::kMxgSmallN : dev::kMxgMaxN;
+    return (int)(p.C > 1 ? tiles * p.C : std::min<long long>(tiles, two ? 2 * sms : sms));
 }
 
 template <int FMT, typename T>
@@ -311,8 +327,14 @@ static int launch_mx_gemm_t(const MxGemmParams &p, int ctas, cudaStream_t stream
     static size_t smem_set[64] = {0};
     const size_t smem = (size_t)p.stages * p.stage_bytes + dev::kMxgBars;
     if (!raise_smem(kern, smem, smem_set)) return -1;
-    cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kMxgThreads, smem, stream, &attr);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kMxgThreads, smem, stream, attr);
+    if (p.C > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)p.C;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
 

@@ -531,21 +531,17 @@ struct MxGemmParams {
     const uint8_t *w, *x;
     const void *r;         // [nb][n] of y's type or nullptr; may be y
     void *y;
-    int *count;            // a word a tile, zero between calls (split tiles)
-    float *part;           // partial tiles, two a CTA
     int *err;
     long long wait_cycles;
     int extra_tx;          // bytes the first stage expects beyond its copies (0; testing only)
     int n, nb, MT, CT, NB, KS;  // row tiles of w, column tiles of NB rows of x, column tiles of k
-    int split;             // the CTAs divide the stages of all tiles evenly (else whole tiles)
-    int stages, stage_bytes;
+    int C;                 // CTAs (a cluster) that share a tile's k; 1: a CTA takes every grid-th tile
+    int acc, stages, stage_bytes;  // tensor-memory columns of an accumulator; the ring
     int early;             // w is complete before the kernel in front of this one began
     float alpha;
 };
-// Sets the tiles, the split and the ring of p (n, nb, KS given) and returns the CTAs.
+// Sets the tiles, the cluster and the ring of p (n, nb, KS given) and returns the CTAs.
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
-constexpr int kMxMaxTiles = 2048;  // tiles of a split product (its counters)
-size_t mx_gemm_part_bytes(const MxGemmParams &p, int ctas);
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
 
 int launch_gemv_q4_0(const GemvParams &p, const Plan &plan, void *stream);

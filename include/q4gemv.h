@@ -604,20 +604,13 @@ q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scales, cudaStre
 /* y[t][i] = sum_k w[i][k] x[t][k] (+ r[t][i]) of the stored values, fp32 sums
  * rounded once to y's type: W [n][k], X [nb][k] of the same format (batch 1 each),
  * y and r [nb][n] of dtype, r NULL or, in place, y itself; else y must not overlap
- * an input.  Any nb from 1 to 2^20.
- * workspace: q4_mx_gemm_workspace_bytes(W, nb) device bytes, zero-filled by the
- * caller before its first use (every call leaves its counters zero, so calls of
- * different shapes can share one that is large enough); calls (and captured
- * graphs) that share one must not run at the same time.  The size goes by the
- * current device.  Results do not depend on scheduling. */
-size_t q4_mx_gemm_workspace_bytes(const q4_mx *W, int32_t nb);
-q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, void *workspace,
-                     size_t workspace_bytes, cudaStream_t stream);
+ * an input.  Any nb from 1 to 2^20.  Results do not depend on scheduling. */
+q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, cudaStream_t stream);
 
 /* q4_mx_quant of src into X (W's format, src's rows; the caller's room), then
  * q4_mx_gemm, whose weight copies run while the rows are quantised. */
 q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype, void *y,
-                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+                       cudaStream_t stream);
 
 /* Launch plan the library uses for a GEMV-shaped call (host-only; exposed
  * for tests and tuning).  tiles: 16-row tiles of the launch, chunks: 128-k
