@@ -11,9 +11,10 @@ Entry points (same names as the C ABI in ``include/q4gemv.h``):
 ``q4_res_gemv``, ``q4_argmax``, ``q4_group_sums``, ``q4_pack_half``,
 ``q4_gemv_half``, ``q4_gemm``, ``q4_decode_step``, ``q4_attn_decode``,
 ``q4_kv_append``, ``q4_attn_prefill``, ``q4_attn_paged``, ``q4_logprobs``,
-``q4_mx_quant``, ``q4_mx_dequant``, ``q4_mx_gemm``; plus ``Q4Weight``
+``q4_mx_quant``, ``q4_mx_dequant``, ``q4_mx_gemm``, ``q4_moe``; plus ``Q4Weight``
 for repacking host weights into the device layout, ``KVPages`` (a paged KV cache),
-``MXMatrix`` (a matrix of microscaled 4-bit values) and ``rope_table``.
+``MXMatrix`` (a matrix of microscaled 4-bit values), ``MoELayer`` (a layer of experts)
+and ``rope_table``.
 """
 from __future__ import annotations
 
@@ -82,6 +83,12 @@ class _CMxSrc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("k", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class _CMoELayer(ctypes.Structure):
+    _fields_ = [("gate_up", _CMx), ("down", _CMx), ("router", ctypes.c_void_p), ("experts", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -101,7 +108,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
         W, KV = ctypes.POINTER(_CWeight), ctypes.POINTER(_CKvPages)
-        MX, SRC = ctypes.POINTER(_CMx), ctypes.POINTER(_CMxSrc)
+        MX, SRC, MOE = ctypes.POINTER(_CMx), ctypes.POINTER(_CMxSrc), ctypes.POINTER(_CMoELayer)
         sig = {
             "q4_packed_bytes": (SZ, [I32, I32, I32]),
             "q4_weight_bytes": (SZ, [I32, I32, I32]),
@@ -152,6 +159,9 @@ def lib() -> ctypes.CDLL:
             "q4_mx_unpack": (I32, [MX, P, P, P]),
             "q4_mx_gemm": (I32, [MX, MX, P, I32, P, P]),
             "q4_mx_linear": (I32, [MX, SRC, MX, P, I32, P, P]),
+            "q4_moe_pack": (I32, [MX, MX, MX, P]),
+            "q4_moe_workspace_bytes": (SZ, [MOE, I32]),
+            "q4_moe": (I32, [MOE, SRC, P, P, I32, P, P, P, P, SZ, P]),
             "q4_status_str": (ctypes.c_char_p, [I32]),
         }
         for name, (res, args) in sig.items():
@@ -1225,3 +1235,102 @@ def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, sc
     X = _CMx(W.fmt, nb, k, 1, wp, room, float(scale))
     _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op), "q4_mx_linear")
     return out
+
+
+# ---------------------------------------------------------------- mixture of experts
+
+class MoELayer:
+    """The weights of a mixture-of-experts layer (``q4_moe``): ``router`` float32 ``[experts, hidden]``; ``gate`` and
+    ``up`` ``MXMatrix`` batches ``[experts, inter, hidden]`` and ``down`` ``[experts, hidden, inter]``, all MXFP4.  Each
+    token takes ``top_k`` experts, weighted by the softmax of their logits (``renormalize``) or by their share of the
+    softmax over all.  Keeps a copy of gate and up in turns of 32 rows, and router and down themselves."""
+
+    def __init__(self, router, gate: MXMatrix, up: MXMatrix, down: MXMatrix, top_k: int, renormalize: bool = True):
+        torch = _torch()
+        gate, up, down = _mx(gate, "gate"), _mx(up, "up"), _mx(down, "down")
+        E, inter, hidden = gate.batch, gate.rows, gate.k
+        if (up.batch, up.rows, up.k) != (E, inter, hidden) or (down.batch, down.rows, down.k) != (E, hidden, inter):
+            raise ValueError("gate and up must be [experts, inter, hidden], down [experts, hidden, inter]")
+        if any(m.fmt != Q4_MX_MXFP4 for m in (gate, up, down)):
+            raise ValueError("the experts' weights must be MXFP4")
+        if any(m.device != gate.device for m in (up, down)):
+            raise ValueError("the experts' weights are on different devices")
+        if not 1 <= int(top_k) <= min(16, E) or E > 1024:
+            raise ValueError("top_k must be 1 .. min(16, experts), experts at most 1024")
+        self.router = _dev_buf(router, "router", torch.float32, (E, hidden), gate.device)
+        self.experts, self.hidden, self.inter, self.top_k = E, hidden, inter, int(top_k)
+        self.renormalize, self.down, self.device = bool(renormalize), down, gate.device
+        self.gate_up = MXMatrix(Q4_MX_MXFP4, 2 * inter, hidden, E, 1.0, gate.device)
+        _check(_launch(self.device, lib().q4_moe_pack, gate._ref, up._ref, self.gate_up._ref), "q4_moe_pack")
+        self._c = _CMoELayer(self.gate_up._c, down._c, self.router.data_ptr(), E, hidden, inter, self.top_k,
+                             int(self.renormalize))
+        self._ref = ctypes.byref(self._c)
+        self._ws = {}
+
+    def cref(self):
+        return self._ref
+
+    def workspace_bytes(self, rows: int) -> int:
+        """Workspace bytes of ``q4_moe`` with ``rows`` tokens."""
+        n = self._ws.get(rows)  # by the shapes alone
+        if n is None:
+            n = self._ws[rows] = int(lib().q4_moe_workspace_bytes(self._ref, rows))
+        return n
+
+
+def _moe(layer):
+    if not isinstance(layer, MoELayer):
+        raise TypeError("layer must be a MoELayer")
+    return layer
+
+
+def q4_moe_workspace(layer: MoELayer, rows: int):
+    """A (zero-filled) workspace for ``q4_moe`` with up to ``rows`` tokens; calls that may run at the same time,
+    captured ones too, need one each."""
+    n = _moe(layer).workspace_bytes(int(rows))
+    return _torch().zeros(max(16, n), dtype=_torch().uint8, device=layer.device)
+
+
+def q4_moe(x, layer: MoELayer, gamma=None, eps: float = 0.0, r=None, positions=None, dtype=None, out=None,
+           workspace=None):
+    """A mixture-of-experts layer for 1 to 16 tokens ``x [rows, hidden]`` (float32, float16 or bfloat16): RMSNorm
+    (with ``gamma``), router, top-k, the chosen experts' SwiGLU MLPs with MXFP4 activations, their weighted sum, plus
+    ``r``.  ``positions`` (int32 ``[rows]``): a negative one marks an idle row, which takes no experts.  Returns
+    ``(out [rows, hidden] of dtype (x's by default), experts int32 [rows, top_k], weights float32 [rows, top_k])``;
+    ``out`` may be ``r`` or ``x``."""
+    torch = _torch()
+    layer = _moe(layer)
+    dev = layer.device
+    src = _mx_src(x, gamma, eps, None)
+    rows, hidden = src.rows, layer.hidden
+    if x.dim() != 2 or src.k != hidden:
+        raise ValueError("x must be [rows, %d]" % hidden)
+    if x.device != dev:
+        raise ValueError("x is on %s, the layer on %s" % (x.device, dev))
+    if rows > MAX_NB:
+        raise ValueError("q4_moe takes 1 to %d tokens, not %d" % (MAX_NB, rows))
+    if dtype is None:
+        dtype = out.dtype if out is not None else x.dtype
+    kind, shape = _kind(dtype, "dtype"), (rows, hidden)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    op = _ptr(out, "out", dtype, shape, dev)
+    rp = None if r is None else _ptr(r, "r", dtype, shape, dev)
+    pos = None if positions is None else _ptr(positions, "positions", torch.int32, (rows,), dev)
+    nbytes = rows * hidden * out.element_size()
+    apart = [(layer.gate_up._c.dev, layer.gate_up.nbytes), (layer.down._c.dev, layer.down.nbytes),
+             (layer._c.router, 4 * layer.experts * hidden)]
+    if rp is not None and rp != op:
+        apart.append((rp, nbytes))
+    if src.x != op or x.dtype != dtype or src.ld != hidden:
+        apart.append((src.x, ((rows - 1) * src.ld + hidden) * x.element_size()))
+    _apart(op, nbytes, *apart)
+    idx = torch.empty((rows, layer.top_k), dtype=torch.int32, device=dev)
+    weight = torch.empty((rows, layer.top_k), dtype=torch.float32, device=dev)
+    if workspace is None:  # zero-filled: its counters start at zero
+        workspace = q4_moe_workspace(layer, rows)
+    else:
+        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=layer.workspace_bytes(rows))
+    _check(_launch(dev, lib().q4_moe, layer._ref, ctypes.byref(src), pos, rp, kind, op, idx.data_ptr(),
+                   weight.data_ptr(), workspace.data_ptr(), workspace.numel()), "q4_moe")
+    return out, idx, weight

@@ -1269,6 +1269,101 @@ extern "C" q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4
     return mx_gemm(W, X, r, dtype, y, true, stream);
 }
 
+// ---------------------------------------------------------------- mixture of experts
+
+namespace {
+// The layer's sizes alone (what a workspace size needs), then its memory.
+q4_status check_moe_shape(const q4_moe_layer *L) {
+    if (!L) return Q4_ERR_NULL;
+    if (!mx_shape_ok(L->hidden, L->inter) || !mx_shape_ok(L->inter, L->hidden) || L->inter > 65536 || L->hidden > 65536)
+        return Q4_ERR_SHAPE;
+    if (L->experts < 1 || L->experts > q4::kMoeMaxExperts || L->top_k < 1 || L->top_k > q4::kMoeMaxTop ||
+        L->top_k > L->experts)
+        return Q4_ERR_SHAPE;
+    return Q4_OK;
+}
+q4_status check_moe(const q4_moe_layer *L) {
+    Q4_TRY(check_moe_shape(L));
+    Q4_TRY(check_mx(&L->gate_up));
+    Q4_TRY(check_mx(&L->down));
+    if (L->gate_up.fmt != Q4_MX_MXFP4 || L->down.fmt != Q4_MX_MXFP4) return Q4_ERR_UNSUPPORTED;
+    if (L->gate_up.batch != L->experts || L->down.batch != L->experts || L->gate_up.rows != 2 * L->inter ||
+        L->gate_up.k != L->hidden || L->down.rows != L->hidden || L->down.k != L->inter)
+        return Q4_ERR_SHAPE;
+    return check_act(L->router);
+}
+q4::MoeParams moe_params(const q4_moe_layer *L, int rows) {
+    q4::MoeParams p{};
+    p.nb = rows;
+    p.hidden = L->hidden;
+    p.inter = L->inter;
+    p.E = L->experts;
+    p.top_k = L->top_k;
+    p.renormalize = L->renormalize;
+    return p;
+}
+}  // namespace
+
+extern "C" q4_status q4_moe_pack(const q4_mx *gate, const q4_mx *up, const q4_mx *out, cudaStream_t stream) {
+    Q4_TRY(check_mx(gate));
+    Q4_TRY(check_mx(up));
+    Q4_TRY(check_mx(out));
+    if (gate->fmt != Q4_MX_MXFP4 || up->fmt != Q4_MX_MXFP4 || out->fmt != Q4_MX_MXFP4) return Q4_ERR_UNSUPPORTED;
+    if (gate->rows % 32 != 0 || up->rows != gate->rows || up->k != gate->k || up->batch != gate->batch ||
+        out->rows != 2ll * gate->rows || out->k != gate->k || out->batch != gate->batch)
+        return Q4_ERR_SHAPE;
+    q4::MoePackParams p{(const uint8_t *)gate->dev, (const uint8_t *)up->dev, (uint8_t *)out->dev, gate->rows, gate->k,
+                        gate->batch};
+    cudaGetLastError();
+    if (q4::launch_moe_pack(p, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
+extern "C" size_t q4_moe_workspace_bytes(const q4_moe_layer *L, int32_t rows) {
+    if (check_moe_shape(L) != Q4_OK || rows < 1 || rows > q4::kMaxNb) return 0;
+    q4::MoeParams p = moe_params(L, rows);
+    return q4::moe_workspace(p, nullptr);
+}
+
+extern "C" q4_status q4_moe(const q4_moe_layer *L, const q4_mx_src *src, const int32_t *positions, const void *r,
+                            int32_t dtype, void *y, int32_t *idx, float *weight, void *workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+    Q4_TRY(check_moe(L));
+    Q4_TRY(check_mx_src(src));
+    if (src->up || !dtype_ok(dtype) || src->rows > q4::kMaxNb) return Q4_ERR_UNSUPPORTED;
+    if (src->k != L->hidden) return Q4_ERR_SHAPE;
+    Q4_TRY(check_act(y));
+    Q4_TRY(check_act(idx));
+    Q4_TRY(check_act(weight));
+    if (!aligned16(r) || (positions && !aligned4(positions))) return Q4_ERR_ALIGN;
+    if (!workspace || workspace_bytes < q4_moe_workspace_bytes(L, src->rows)) return Q4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return Q4_ERR_ALIGN;
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
+    q4::MoeParams p = moe_params(L, src->rows);
+    q4::moe_workspace(p, (uint8_t *)workspace);
+    p.x = src->x;
+    p.ldx = src->ld;
+    p.gamma = src->gamma;
+    p.eps = src->eps;
+    p.r = r;
+    p.router = L->router;
+    p.positions = positions;
+    p.gate_up = (const uint8_t *)L->gate_up.dev;
+    p.down = (const uint8_t *)L->down.dev;
+    p.y = y;
+    p.idx = idx;
+    p.weight = weight;
+    Q4_TRY(kernel_err_ptr(&p.err));
+    p.wait_cycles = g_wait_cycles;
+    p.barrier_polls = g_barrier_polls;
+    p.barrier_extra = g_barrier_extra;
+    p.extra_tx = g_extra_tx;
+    cudaGetLastError();
+    if (q4::launch_moe(p, src->dtype, dtype, sms, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    return Q4_OK;
+}
+
 extern "C" q4_status q4_debug_wait_limits(int64_t barrier_polls, int32_t barrier_extra, int64_t copy_wait_cycles,
                                           int32_t copy_extra_bytes) {
     if (barrier_extra < 0 || barrier_extra > 1 || copy_extra_bytes < 0 || copy_extra_bytes > 4096 ||

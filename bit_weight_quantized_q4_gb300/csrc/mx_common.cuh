@@ -141,6 +141,17 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// All threads of the cluster's CTAs (whole warps).
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A value into the shared memory (offset as here) of the cluster's CTA `rank`.
+__device__ __forceinline__ void store_peer(uint32_t saddr, uint32_t rank, float v) {
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(saddr),
+        "r"(rank), "f"(v)
+        : "memory");
+}
 
 }  // namespace dev
 }  // namespace q4

@@ -23,17 +23,6 @@ constexpr int kMxgSmallN = 64;      // up to here two CTAs of an SM
 constexpr int kMxgMaxStages = 12;
 constexpr int kMxgBars = 8 * (2 * kMxgMaxStages + 5) + 16;
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A value into the shared memory (offset as here) of the cluster's CTA `rank`.
-__device__ __forceinline__ void store_peer(uint32_t saddr, uint32_t rank, float v) {
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.f32 [a], %2;\n\t}" ::"r"(saddr),
-        "r"(rank), "f"(v)
-        : "memory");
-}
-
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_constant__ MxGemmParams p) {
     constexpr int W = mx_words(FMT), REC = mx_rec(FMT);

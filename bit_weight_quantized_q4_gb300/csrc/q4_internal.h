@@ -544,6 +544,47 @@ struct MxGemmParams {
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
 
+// A mixture-of-experts layer for up to kMaxNb tokens (moe.cu).  Inside it the few
+// rows of activations lie in records of 16 rows x 256 columns: 2048 bytes of codes
+// and two 512-byte words of scales, as the first 16 rows of an MXFP4 record.
+constexpr int kMoeRec = 2048 + 1024;
+constexpr int kMoeMaxExperts = 1024, kMoeMaxTop = 16;
+constexpr int kMoeMaxActive = kMaxNb * kMoeMaxTop;
+struct MoeParams {
+    const void *x, *r;          // [nb][hidden], rows ldx apart; [nb][hidden] of y's type or nullptr
+    const float *gamma, *router;  // [hidden] or nullptr; [E][hidden]
+    const int32_t *positions;   // [nb] or nullptr; negative: an idle row
+    const uint8_t *gate_up, *down;
+    void *y;
+    int32_t *idx;               // [nb][top_k]
+    float *weight;              // [nb][top_k]
+    // workspace
+    unsigned *arrived;          // CTAs of the routing kernel that are done; zero between calls
+    unsigned *barrier;          // of the experts' kernel; zeroed by the routing kernel
+    int *active;                // experts with a token
+    float *logits;              // [nb][E]
+    int *ids;                   // [active] expert
+    unsigned *mask;             // [active] its tokens
+    float *wtab;                // [active][16] their weights
+    uint8_t *xq, *h;            // records [k tile], [active][k tile]
+    int *err;
+    long long ldx, wait_cycles, barrier_polls;
+    int extra_tx, barrier_extra;
+    int nb, hidden, inter, E, top_k, renormalize;
+    float eps;
+};
+// Sets the workspace pointers of p (nb, hidden, inter, E, top_k given) from `ws`
+// and returns its size.
+size_t moe_workspace(MoeParams &p, uint8_t *ws);
+int launch_moe(const MoeParams &p, int x_dtype, int y_dtype, int sms, void *stream);
+// The rows of gate and up [batch][rows][k] in turns of 32, as [batch][2 rows][k].
+struct MoePackParams {
+    const uint8_t *gate, *up;
+    uint8_t *out;
+    int rows, k, batch;
+};
+int launch_moe_pack(const MoePackParams &p, void *stream);
+
 int launch_gemv_q4_0(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_affine(const GemvParams &p, const Plan &plan, void *stream);
 int launch_gemv_q8_0(const GemvParams &p, const Plan &plan, void *stream);

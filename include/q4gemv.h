@@ -326,7 +326,7 @@ q4_status q4_decode_check(const void *workspace, cudaStream_t stream);
 /* Synchronises `stream` and reports whether any GEMV-family kernel of this
  * library on the current device (q4_gemv, q4_nrm_gemv, q4_dual_gemv,
  * q4_gus_nrm, q4_res_gemv, q4_argmax, q4_argmax_noalloc, q4_gemm,
- * q4_attn_decode, q4_attn_prefill, q4_attn_paged, q4_mx_gemm, q4_mx_linear) gave up waiting for its weight (or K/V)
+ * q4_attn_decode, q4_attn_prefill, q4_attn_paged, q4_mx_gemm, q4_mx_linear, q4_moe) gave up waiting for its weight (or K/V)
  * copies since the last check, or a kernel of the paged cache or of
  * q4_logprobs met a position, page or token out of range (Q4_ERR_CUDA; the
  * flag is then cleared) or not (Q4_OK).  Each kernel bounds every such wait (about a
@@ -611,6 +611,50 @@ q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtyp
  * q4_mx_gemm, whose weight copies run while the rows are quantised. */
 q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype, void *y,
                        cudaStream_t stream);
+
+/* ---------------------------------------------------------------- mixture of experts
+ * A layer of `experts` SwiGLU MLPs of which every token takes top_k, for 1 to 16
+ * tokens (a decode batch), with MXFP4 weights:
+ *   xh = src's row (behind the RMSNorm where gamma is given);  l = router xh (fp32);
+ *   the top_k experts of largest l (ties to the lowest index; NaN behind every
+ *   number), with weights w = softmax of l over them (renormalize != 0) or over all
+ *   experts;
+ *   h_e = silu(gate_e Q(xh)) * (up_e Q(xh)),  silu(t) = t / (1 + exp(-t));
+ *   y = r + sum over its experts of w_e down_e Q(h_e)
+ * with Q the rounding of q4_mx_quant to MXFP4, everything else fp32 until y is
+ * rounded once to dtype.
+ *   gate_up: [experts][2 inter][hidden], rows of gate and up in turns of 32 (gate
+ *     rows 0-31, up rows 0-31, gate rows 32-63, ...: q4_moe_pack);
+ *   down: [experts][hidden][inter];  router: [experts][hidden] fp32, device.
+ * hidden and inter multiples of 32; 1 <= experts <= 1024; 1 <= top_k <= min(16,
+ * experts). */
+typedef struct {
+    q4_mx gate_up, down;
+    const float *router;
+    int32_t experts, hidden, inter, top_k, renormalize;
+} q4_moe_layer;
+
+/* out [batch][2 rows][k] from gate and up [batch][rows][k] (MXFP4, rows % 32 == 0),
+ * device to device, lossless. */
+q4_status q4_moe_pack(const q4_mx *gate, const q4_mx *up, const q4_mx *out, cudaStream_t stream);
+
+/* src: rows = 1..16 tokens, k = hidden; up must be NULL.  positions: [rows] device
+ * int32 (4-byte aligned) or NULL; a negative one marks an idle row (a padded batch):
+ * it takes no experts, its idx are -1, its weights 0 and its y is r.  r: [rows]
+ * [hidden] of dtype or NULL; y: likewise, may be r or src's x (whole), else must not
+ * overlap an input.  idx, weight: [rows][top_k] the experts, largest weight first.
+ * workspace: q4_moe_workspace_bytes(layer, rows) device bytes, zero-filled by the
+ * caller before its first use (every call leaves its counters zero, so calls of
+ * different layers can share one that is large enough); calls (and captured graphs)
+ * that share one must not run at the same time.
+ * Two launches; the second is cooperative, one CTA a multiprocessor, with one
+ * bounded barrier of the grid (q4_device_check reports a wait that gave up).  A
+ * token's last bits may depend on the batch: the sums are split by the experts that
+ * have a token.  They do not depend on scheduling. */
+size_t q4_moe_workspace_bytes(const q4_moe_layer *layer, int32_t rows);
+q4_status q4_moe(const q4_moe_layer *layer, const q4_mx_src *src, const int32_t *positions, const void *r,
+                 int32_t dtype, void *y, int32_t *idx, float *weight, void *workspace, size_t workspace_bytes,
+                 cudaStream_t stream);
 
 /* Launch plan the library uses for a GEMV-shaped call (host-only; exposed
  * for tests and tuning).  tiles: 16-row tiles of the launch, chunks: 128-k
