@@ -1285,10 +1285,10 @@ def _moe(layer):
 
 
 def q4_moe_workspace(layer: MoELayer, rows: int):
-    """A (zero-filled) workspace for ``q4_moe`` with up to ``rows`` tokens; calls that may run at the same time,
-    captured ones too, need one each."""
+    """A workspace for ``q4_moe`` with up to ``rows`` tokens; calls that may run at the same time, captured ones too,
+    need one each."""
     n = _moe(layer).workspace_bytes(int(rows))
-    return _torch().zeros(max(16, n), dtype=_torch().uint8, device=layer.device)
+    return _torch().empty(max(16, n), dtype=_torch().uint8, device=layer.device)
 
 
 def q4_moe(x, layer: MoELayer, gamma=None, eps: float = 0.0, r=None, positions=None, dtype=None, out=None,
@@ -1327,7 +1327,7 @@ def q4_moe(x, layer: MoELayer, gamma=None, eps: float = 0.0, r=None, positions=N
     _apart(op, nbytes, *apart)
     idx = torch.empty((rows, layer.top_k), dtype=torch.int32, device=dev)
     weight = torch.empty((rows, layer.top_k), dtype=torch.float32, device=dev)
-    if workspace is None:  # zero-filled: its counters start at zero
+    if workspace is None:
         workspace = q4_moe_workspace(layer, rows)
     else:
         _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=layer.workspace_bytes(rows))

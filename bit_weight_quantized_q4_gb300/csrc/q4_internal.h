@@ -559,14 +559,11 @@ struct MoeParams {
     int32_t *idx;               // [nb][top_k]
     float *weight;              // [nb][top_k]
     // workspace
-    unsigned *arrived;          // CTAs of the routing kernel that are done; zero between calls
-    unsigned *barrier;          // of the experts' kernel; zeroed by the routing kernel
-    int *active;                // experts with a token
+    unsigned *barrier;          // of the experts' kernel, and
+    unsigned *count;            // [hidden / 128] parts of a tile that are there: zeroed by the routing kernel
     float *logits;              // [nb][E]
-    int *ids;                   // [active] expert
-    unsigned *mask;             // [active] its tokens
-    float *wtab;                // [active][16] their weights
-    uint8_t *xq, *h;            // records [k tile], [active][k tile]
+    uint8_t *xq, *h;            // records [k tile], [expert with a token][k tile]
+    float *part;                // [CTA][2][nb][128] parts of tiles
     int *err;
     long long ldx, wait_cycles, barrier_polls;
     int extra_tx, barrier_extra;

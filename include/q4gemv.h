@@ -643,10 +643,8 @@ q4_status q4_moe_pack(const q4_mx *gate, const q4_mx *up, const q4_mx *out, cuda
  * it takes no experts, its idx are -1, its weights 0 and its y is r.  r: [rows]
  * [hidden] of dtype or NULL; y: likewise, may be r or src's x (whole), else must not
  * overlap an input.  idx, weight: [rows][top_k] the experts, largest weight first.
- * workspace: q4_moe_workspace_bytes(layer, rows) device bytes, zero-filled by the
- * caller before its first use (every call leaves its counters zero, so calls of
- * different layers can share one that is large enough); calls (and captured graphs)
- * that share one must not run at the same time.
+ * workspace: q4_moe_workspace_bytes(layer, rows) device bytes, no initialisation
+ * needed, not shared by calls (or captured graphs) that run at the same time.
  * Two launches; the second is cooperative, one CTA a multiprocessor, with one
  * bounded barrier of the grid (q4_device_check reports a wait that gave up).  A
  * token's last bits may depend on the batch: the sums are split by the experts that
