@@ -1167,8 +1167,10 @@ q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
     p.batch = out->batch;
     p.eps = s->eps;
     p.scale = out->scale;
+    const int sms = num_sms();
+    if (sms <= 0) return Q4_ERR_CUDA;
     cudaGetLastError();
-    if (q4::launch_mx_quant(p, out->fmt, s->dtype, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+    if (q4::launch_mx_quant(p, out->fmt, s->dtype, sms, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
     return Q4_OK;
 }
 q4_status check_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, const void *y) {

@@ -20,23 +20,28 @@ namespace dev {
 
 constexpr int kRouteThreads = 256, kRouteWarps = kRouteThreads / 32;
 
+// Four consecutive values as they are stored.
 template <typename T>
-__device__ __forceinline__ float4 load4(const T *src) {
-    if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float4 *>(src);
-    } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(src);
-        const T *v = reinterpret_cast<const T *>(&w);
-        return make_float4(to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3]));
+struct Raw4 {
+    typename std::conditional<sizeof(T) == 4, uint4, uint2>::type w;
+    __device__ __forceinline__ void load(const T *src) { w = *reinterpret_cast<const decltype(w) *>(src); }
+    __device__ __forceinline__ void zero() { w = {}; }
+    __device__ __forceinline__ float4 values() const {
+        if constexpr (sizeof(T) == 4) {
+            return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+        } else {
+            const T *v = reinterpret_cast<const T *>(&w);
+            return make_float4(to_f32(v[0]), to_f32(v[1]), to_f32(v[2]), to_f32(v[3]));
+        }
     }
-}
+};
 
 // CTAs below E: an expert's logits of all tokens, a warp every eighth 128 columns.
 // The others: a token's row each, its norm and its codes.  (A warp an expert and
 // four tokens, with the choice of the experts by the last CTA: 14 us more for one
-// token.)  Latency bounds it: every load of a warp goes out before the first is used
-// up to 1024 columns.
-template <typename T>
+// token.)  Latency bounds it: the loads of up to 2048 columns of all tokens go out before
+// the first is used (a token at a time, 16 tokens took 12 us).
+template <typename T, int NT>
 __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid_constant__ MoeParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -49,30 +54,58 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
             if (tid == 0) *p.barrier = 0u;
             for (int i = tid; i < mx_rtiles(p.hidden); i += kRouteThreads) p.count[i] = 0u;
         }
-        // dots with the expert's row (0-15) and sums of squares (16-31), a token each
-        float v[32] = {};
+        // dots with the expert's row (below NT) and sums of squares, a token each
+        float v[2 * NT] = {};
         const float *row = p.router + (size_t)e * p.hidden;
-        for (int c = 128 * warp + 4 * lane; c < p.hidden; c += 128 * kRouteWarps) {
-            float4 w = *reinterpret_cast<const float4 *>(row + c);
-            if (p.gamma) {
-                const float4 g = *reinterpret_cast<const float4 *>(p.gamma + c);
-                w = make_float4(w.x * g.x, w.y * g.y, w.z * g.z, w.w * g.w);
-            }
+        constexpr int R = NT < 16 ? 4 : sizeof(T) == 2 ? 2 : 1;  // loads of a row under way
+        for (int c0 = 128 * warp + 4 * lane; c0 < p.hidden; c0 += 128 * kRouteWarps * R) {
+            float4 w[R], g[R];
+            Raw4<T> a[NT][R];
+            auto in = [&](int i) { return i == 0 || c0 + 128 * kRouteWarps * i < p.hidden; };
 #pragma unroll
-            for (int t = 0; t < kMaxNb; ++t)
-                if (t < p.nb) {
-                    const float4 a = load4(x + t * p.ldx + c);
-                    v[t] = fmaf(a.x, w.x, fmaf(a.y, w.y, fmaf(a.z, w.z, fmaf(a.w, w.w, v[t]))));
-                    v[16 + t] = fmaf(a.x, a.x, fmaf(a.y, a.y, fmaf(a.z, a.z, fmaf(a.w, a.w, v[16 + t]))));
+            for (int i = 0; i < R; ++i)
+                if (in(i)) {
+                    const int c = c0 + 128 * kRouteWarps * i;
+                    w[i] = *reinterpret_cast<const float4 *>(row + c);
+                    g[i] = p.gamma ? *reinterpret_cast<const float4 *>(p.gamma + c) : make_float4(1.f, 1.f, 1.f, 1.f);
+                } else {
+                    w[i] = g[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    a[t][i].zero();
+                    if (t < p.nb && in(i)) a[t][i].load(x + t * p.ldx + c0 + 128 * kRouteWarps * i);
+                }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                w[i] = make_float4(w[i].x * g[i].x, w[i].y * g[i].y, w[i].z * g[i].z, w[i].w * g[i].w);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const float4 b = a[t][i].values();
+                    v[t] = fmaf(b.x, w[i].x, fmaf(b.y, w[i].y, fmaf(b.z, w[i].z, fmaf(b.w, w[i].w, v[t]))));
+                    v[NT + t] = fmaf(b.x, b.x, fmaf(b.y, b.y, fmaf(b.z, b.z, fmaf(b.w, b.w, v[NT + t]))));
+                }
+            }
         }
-        sums[warp][lane] = transpose_reduce(v, lane);
+        if constexpr (NT == 16) {
+            sums[warp][lane] = transpose_reduce(v, lane);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * NT; ++i) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+                if (lane == 0) sums[warp][i] = v[i];
+            }
+        }
         __syncthreads();
         if (warp == 0) {
             float s = 0.f;
+            if (lane < 2 * NT)
 #pragma unroll
-            for (int w = 0; w < kRouteWarps; ++w) s += sums[w][lane];
-            const float sq = __shfl_down_sync(0xffffffffu, s, 16);
+                for (int w = 0; w < kRouteWarps; ++w) s += sums[w][lane];
+            const float sq = __shfl_down_sync(0xffffffffu, s, NT);
             if (lane < p.nb)
                 p.logits[(size_t)lane * p.E + e] = p.gamma ? s * (1.f / sqrtf(sq / (float)p.hidden + p.eps)) : s;
         }
@@ -86,7 +119,10 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.f;
         if (c < p.hidden) {
-            const float4 a = load4(src + c), b = load4(src + c + 4);
+            Raw4<T> lo, hi;
+            lo.load(src + c);
+            hi.load(src + c + 4);
+            const float4 a = lo.values(), b = hi.values();
             v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
             v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         }
@@ -119,24 +155,24 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * g[i];
         }
-        uint32_t m = 0;
+        float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        for (int i = 0; i < 8; ++i) m = max_abs(m, v[i]);
+        m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, 2));
         float mul;
-        const uint32_t sc = mx_block_scale<0>(m, 1.f, 6.f, mul);
+        const uint32_t sc = mx_block_scale<0>(m, MxGain{}, mul);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = mx_scaled(v[i], mul);
+        for (int i = 0; i < 8; ++i) v[i] *= mul;
         uint8_t *rec = p.xq + (size_t)kt * kMoeRec;
-        *reinterpret_cast<uint32_t *>(rec + mx_code_off(t, 4 * lane)) = e2m1x8(v);
+        *reinterpret_cast<uint32_t *>(rec + mx_code_off(t, 4 * lane)) = mul == 0.f ? 0u : e2m1x8(v);
         if (lane % 4 == 0) rec[2048 + (lane >> 4) * 512 + t * 16 + ((lane >> 2) & 3)] = (uint8_t)sc;
     }
 }
 
 // ------------------------------------------------------------------ experts
 
-constexpr int kMoeThreads = 192;
+constexpr int kMoeThreads = 32 * kMaxNb;  // a warp a token to choose the experts; then six have roles
 constexpr int kMoeStages = 9;
 constexpr int kMoeStage = mx_rec(0) + kMoeRec;  // a record of weights, one of activations
 constexpr int kMoeExch = 2 * 2 * 2 * 8 * 32 * 4;  // [turn][pair of warps][gate or up][token][row]
@@ -146,60 +182,55 @@ constexpr int kMoeOffExch = kMoeStages * kMoeStage, kMoeOffIds = kMoeOffExch + k
               kMoeOffMask = kMoeOffIds + 4 * kMoeMaxActive, kMoeOffW = kMoeOffMask + 4 * kMoeMaxActive,
               kMoeOffBar = kMoeOffW + 64 * kMoeMaxActive, kMoeSmem = kMoeOffBar + 8 * (2 * kMoeStages + 5) + 16;
 static_assert(kMoeStage % 1024 == 0 && kMoeSmem <= (int)kSmemMax, "shared memory of the experts' kernel");
-// while they are chosen, over the ring: a warp's logits, the choices, an expert's
-// tokens and its place in the list
-constexpr int kMoeOffLogits = 0, kMoeOffChosen = kMoeOffLogits + 6 * 4 * kMoeMaxExperts,
-              kMoeOffChosenW = kMoeOffChosen + 4 * kMoeMaxActive, kMoeOffTok = kMoeOffChosenW + 4 * kMoeMaxActive,
+// while they are chosen, over the ring: the choices, an expert's tokens and its place
+// in the list
+constexpr int kMoeOffChosen = 0, kMoeOffChosenW = kMoeOffChosen + 4 * kMoeMaxActive, kMoeOffTok = kMoeOffChosenW + 4 * kMoeMaxActive,
               kMoeOffSlot = kMoeOffTok + 4 * kMoeMaxExperts;
 static_assert(kMoeOffSlot + 4 * kMoeMaxExperts <= kMoeOffExch, "the ring's room");
 constexpr int kMoeParts = 10;  // CTAs that share a tile of outputs, about
 
-// Order of logits: larger first, NaN behind every number.
+// Order of logits: larger first, NaN (1) behind every number (-inf: 0x7FFFFF).
 __device__ __forceinline__ uint32_t logit_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);  // (-0 is 0)
-    return v != v ? 0u : (u >> 31) ? ~u : u | 0x80000000u;
+    return v != v ? 1u : (u >> 31) ? ~u : u | 0x80000000u;
 }
 
 // One token's choice by a warp: its experts and weights into idx and weight
-// [top_k].  row: room for E logits.  A lane keeps the best of its own experts (lane,
-// lane + 32, ..); a round takes the best of the lanes, whose lane looks again.
-__device__ __forceinline__ void moe_choose(const float *logits, float *row, int E, int top_k, bool renorm, int *idx,
-                                           float *weight, int lane) {
-    uint32_t best = 0;
-    int where = -1;
-    for (int e = lane; e < E; e += 32) {
-        const float v = __ldcg(logits + e);
-        row[e] = v;
-        const uint32_t key = logit_key(v);
-        if (where < 0 || key > best) {
-            best = key;
-            where = e;
-        }
-    }
-    uint32_t taken = 0;  // bit i: expert 32 i + lane is chosen
+// [top_k].  A lane keeps the logits of its experts (lane, lane + 32, ..: NL of them at
+// most) and the best of those not chosen yet; a round takes the best of the lanes.
+template <int NL>
+__device__ __forceinline__ void moe_choose(const float *logits, int E, int top_k, bool renorm, int *idx, float *weight,
+                                           int lane) {
+    float v[NL];
+    uint32_t key[NL];  // 0: none, or chosen
+#pragma unroll
+    for (int i = 0; i < NL; ++i) v[i] = 32 * i + lane < E ? __ldcg(logits + 32 * i + lane) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NL; ++i) key[i] = 32 * i + lane < E ? logit_key(v[i]) : 0u;
     float top = 0.f, mine = 0.f;
     int at = 0;
     for (int j = 0; j < top_k; ++j) {
-        const uint32_t most = __reduce_max_sync(0xffffffffu, where < 0 ? 0u : best);
-        const int first = (int)__reduce_min_sync(0xffffffffu, where >= 0 && best == most ? (uint32_t)where : 0x7FFFFFFFu);
-        __syncwarp();
-        const float v = row[first];
-        if (j == 0) top = v;
-        if (lane == j) {
-            mine = v;
-            at = first;
-        }
-        if (lane == (first & 31)) {
-            taken |= 1u << (first >> 5);
-            where = -1;
-            for (int i = 0; 32 * i + lane < E; ++i) {
-                if ((taken >> i) & 1u) continue;
-                const uint32_t key = logit_key(row[32 * i + lane]);
-                if (where < 0 || key > best) {
-                    best = key;
-                    where = 32 * i + lane;
-                }
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) best = max(best, key[i]);
+        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+        int where = 0x7FFFFFFF;
+        float bv = 0.f;
+#pragma unroll
+        for (int i = NL - 1; i >= 0; --i)
+            if (key[i] == most) {
+                where = 32 * i + lane;
+                bv = v[i];
             }
+        const int first = (int)__reduce_min_sync(0xffffffffu, (uint32_t)where);
+        const float got = __shfl_sync(0xffffffffu, bv, first & 31);
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if (32 * i + lane == first) key[i] = 0u;
+        if (j == 0) top = got;
+        if (lane == j) {
+            mine = got;
+            at = first;
         }
     }
     // softmax with the largest logit as its reference (NaN where one is NaN)
@@ -207,7 +238,9 @@ __device__ __forceinline__ void moe_choose(const float *logits, float *row, int 
     float sum = e;
     if (!renorm) {
         sum = 0.f;
-        for (int i = lane; i < E; i += 32) sum += expf(row[i] - top);
+#pragma unroll
+        for (int i = 0; i < NL; ++i)
+            if (32 * i + lane < E) sum += expf(v[i] - top);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -233,7 +266,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     const uint32_t ring = smem_u32(sm), b_full = ring + kMoeOffBar, b_empty = b_full + 8 * S, b_acc = b_empty + 8 * S,
                    b_read = b_acc + 16, b_drain = b_read + 16;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + kMoeOffBar + 8 * (2 * S + 5));
-    volatile int *info = reinterpret_cast<volatile int *>(tslot + 1);  // experts with a token; a tile's last CTA
+    volatile int *info = reinterpret_cast<volatile int *>(tslot + 1);  // experts with a token; tiles to join
     int *ids = reinterpret_cast<int *>(sm + kMoeOffIds);
     unsigned *masks = reinterpret_cast<unsigned *>(sm + kMoeOffMask);
     float *wtab = reinterpret_cast<float *>(sm + kMoeOffW);
@@ -260,7 +293,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     int *slot = reinterpret_cast<int *>(sm + kMoeOffSlot);
     for (int e = tid; e < p.E; e += kMoeThreads) tokens[e] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int t = warp; t < p.nb; t += kMoeThreads / 32) {
+    if (warp < p.nb) {
+        const int t = warp;
         int *idx = chosen + t * p.top_k;
         float *w = chosen_w + t * p.top_k;
         if (p.positions && p.positions[t] < 0) {  // an idle row: no experts
@@ -269,8 +303,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
                 w[lane] = 0.f;
             }
         } else {
-            moe_choose(p.logits + (size_t)t * p.E, reinterpret_cast<float *>(sm + kMoeOffLogits) + warp * kMoeMaxExperts, p.E,
-                       p.top_k, p.renormalize != 0, idx, w, lane);
+            const float *logits = p.logits + (size_t)t * p.E;
+            if (p.E <= 256)
+                moe_choose<8>(logits, p.E, p.top_k, p.renormalize != 0, idx, w, lane);
+            else
+                moe_choose<kMoeMaxExperts / 32>(logits, p.E, p.top_k, p.renormalize != 0, idx, w, lane);
         }
     }
     __syncthreads();
@@ -297,7 +334,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
             }
             n += __popc(hit);
         }
-        if (lane == 0) info[0] = n;
+        if (lane == 0) {
+            info[0] = n;
+            info[1] = info[2] = -1;
+        }
     }
     __syncthreads();
     for (int i = tid; i < pairs; i += kMoeThreads)
@@ -315,6 +355,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     const int line = nA * KS2, ctas2 = min(grid, T2 * min(kMoeParts, max(line, 1)));
     auto first_of = [&](int c) { return (long long)T2 * line * c / ctas2; };
     const long long g0 = cta < ctas2 ? first_of(cta) : 0, g1 = cta < ctas2 ? first_of(cta + 1) : 0;
+    auto sharers = [&](int m, int &f, int &l) {  // the first and the last CTA with a part of tile m
+        const long long all = (long long)T2 * line, s0 = (long long)m * line;
+        f = (int)(((s0 + 1) * ctas2 - 1) / all);
+        l = (int)(((s0 + line) * ctas2 - 1) / all);
+    };
     // this CTA's segments: f(tile, first stage, end) until it says no
     auto walk = [&](auto f) {
         for (long long g = g0; g < g1;) {
@@ -324,6 +369,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         }
     };
     const long long lim = p.wait_cycles;
+    const size_t slot_floats = (size_t)p.nb * kMxRows;
+    auto store = [&](int row, int t, float v) {
+        if (row >= p.hidden) return;
+        const size_t at = (size_t)t * p.hidden + row;
+        ((T *)p.y)[at] = from_f32<T>(p.r ? v + to_f32(((const T *)p.r)[at]) : v);
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
@@ -439,7 +490,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         if (tc::elect_one()) tc::commit(b_drain);
         __syncwarp();
         mbar_wait(b_drain, 0u, kWaitCycles);
-    } else {
+    } else if (warp < 6) {
         // ------------------------------------------------------------ sums
         const int q = warp & 3, pair = q >> 1, up = q & 1, rl = 32 * q + lane;
         int seg = 0;
@@ -481,11 +532,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
                 if (!((mask >> t) & 1u)) continue;
                 const float o = buf[((1 - up) * 8 + i) * 32 + lane];
                 const float g = up ? o : v[i], w = up ? v[8 + i] : o;
-                const float h = in ? g / (1.f + __expf(-g)) * w : 0.f;
+                const float h = in ? mx_silu(g) * w : 0.f;
                 float mul;
                 const uint32_t sc = mx_block_scale<0>(
-                    __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu), 1.f, 6.f, mul);
-                uint32_t code = e2m1(mx_scaled(h, mul)) << (4 * (lane & 7));
+                    __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7FFFFFFFu)), MxGain{}, mul);
+                uint32_t code = (mul == 0.f ? 0u : e2m1(h * mul)) << (4 * (lane & 7));
 #pragma unroll
                 for (int x = 1; x < 8; x <<= 1) code |= __shfl_xor_sync(0xffffffffu, code, x);
                 if (blk / 8 < KS2)
@@ -497,21 +548,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
                     }
             }
         }
-        __threadfence();
         asm volatile("fence.proxy.async;" ::: "memory");  // h, for the copies of other CTAs
         asm volatile("bar.sync 1, 128;" ::: "memory");
         if (warp == 2 && lane == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.barrier) : "memory");
 
-        auto store = [&](int m, int t, float v) {
-            const int row = m * kMxRows + rl;
-            if (row >= p.hidden) return;
-            const size_t at = (size_t)t * p.hidden + row;
-            ((T *)p.y)[at] = from_f32<T>(p.r ? v + to_f32(((const T *)p.r)[at]) : v);
-        };
-        const size_t slot_floats = (size_t)p.nb * kMxRows;
         if (line == 0)  // only idle rows
             for (int m = cta; m < T2; m += grid)
-                for (int t = 0; t < p.nb; ++t) store(m, t, 0.f);
+                for (int t = 0; t < p.nb; ++t) store(m * kMxRows + rl, t, 0.f);
         int nseg = 0;
         walk([&](int m, int q0, int q1) {
             float sum[16] = {};
@@ -529,42 +572,22 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
             if (q1 - q0 == line) {
 #pragma unroll
                 for (int t = 0; t < 16; ++t)
-                    if (t < p.nb) store(m, t, sum[t]);
+                    if (t < p.nb) store(m * kMxRows + rl, t, sum[t]);
                 return true;
             }
             float *mine = p.part + ((size_t)cta * 2 + slot_of) * slot_floats + rl;
 #pragma unroll
             for (int t = 0; t < 16; ++t)
                 if (t < p.nb) __stcg(mine + t * kMxRows, sum[t]);
-            // the tile's CTAs, and how many of them are done
-            const long long s0 = (long long)m * line, all = (long long)T2 * line;
-            const int f = (int)(((s0 + 1) * ctas2 - 1) / all), l = (int)(((s0 + line) * ctas2 - 1) / all);
+            // the last of the tile's CTAs joins the parts, below
+            int f, l;
+            sharers(m, f, l);
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (warp == 2 && lane == 0) {
                 unsigned before;
                 asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(p.count + m) : "memory");
-                info[1] = (int)before == l - f;
+                if ((int)before == l - f) info[1 + slot_of] = m;
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (info[1]) {
-                // CTA f's part is its second if it began in an earlier tile, the others' their first
-                const float *part0 = p.part + ((size_t)f * 2 + (first_of(f) < s0)) * slot_floats + rl;
-                const float *parts = p.part + rl;
-                for (int t0 = 0; t0 < p.nb; t0 += 4) {
-                    float acc[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = t0 + i < p.nb ? __ldcg(part0 + (t0 + i) * kMxRows) : 0.f;
-#pragma unroll 4
-                    for (int x = f + 1; x <= l; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (t0 + i < p.nb) acc[i] += __ldcg(parts + (size_t)x * 2 * slot_floats + (t0 + i) * kMxRows);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (t0 + i < p.nb) store(m, t0 + i, acc[i]);
-                }
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the flag is read before the next segment's
             return true;
         });
         if (!ok && lane == 0) atomicExch(p.err, 4);
@@ -575,6 +598,30 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     if (warp == 1) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 128);
+    }
+    // Tiles whose last part came from here: a thread a row and every fourth token, the
+    // parts in CTA order, eight at once.  (By the four warps of the sums, a few loads at a
+    // time, 16 tokens took 13 us.)
+    for (int j = 0; j < 2; ++j) {
+        const int m = info[1 + j];
+        if (m < 0) continue;
+        int f, l;
+        sharers(m, f, l);
+        const int rl = tid & (kMxRows - 1);
+        // CTA f's part is its second if it began in an earlier tile, the others' their first
+        const float *part0 = p.part + ((size_t)f * 2 + (first_of(f) < (long long)m * line)) * slot_floats + rl;
+        const float *parts = p.part + rl;
+        for (int t = tid / kMxRows; t < p.nb; t += kMoeThreads / kMxRows) {
+            float v = __ldcg(part0 + t * kMxRows);
+            for (int x = f + 1; x <= l; x += 8) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = x + i <= l ? __ldcg(parts + (size_t)(x + i) * 2 * slot_floats + t * kMxRows) : 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v += o[i];
+            }
+            store(m * kMxRows + rl, t, v);
+        }
     }
 }
 
@@ -617,11 +664,13 @@ size_t moe_workspace(MoeParams &p, uint8_t *ws) {
     return at;
 }
 
+// (a token's sums are straight code: 16 tokens' of it cost one token 1.5 us)
 template <typename T>
 static int launch_route(const MoeParams &p, cudaStream_t stream) {
+    auto kern = p.nb == 1 ? dev::q4moe_route_kernel<T, 1> : p.nb <= 4 ? dev::q4moe_route_kernel<T, 4> : dev::q4moe_route_kernel<T, 16>;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = pdl_config((unsigned)(p.E + p.nb), dev::kRouteThreads, 0, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, dev::q4moe_route_kernel<T>, p) == cudaSuccess ? 0 : -1;
+    return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
 
 template <typename T>

@@ -44,11 +44,20 @@ __device__ __forceinline__ uint32_t e2m1(float v) {
         : "f"(v), "f"(0.f));
     return w & 15u;
 }
-// The value of the code in bits 0-3: sign (1 + m / 2) 2^(e - 1), or m / 2 for e = 0.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    // an f32 with the code's exponent and mantissa, 2^-126 subnormals at e = 0,
-    // times 2^126
-    return __uint_as_float(((c & 8u) << 28) | ((c & 7u) << 22)) * __uint_as_float(253u << 23);
+// The values of a word's eight codes.
+__device__ __forceinline__ void e2m1_values(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 __device__ __forceinline__ float e4m3_value(uint32_t b) {
     uint32_t h;
@@ -64,33 +73,55 @@ __device__ __forceinline__ float mx_scale_value(uint32_t b) {
     return FMT == 0 ? e8m0_value(b) : e4m3_value(b);
 }
 
-// The scale byte of a block whose largest magnitude has the bits `a`, and the
-// factor its values are multiplied with before they are rounded to codes.
-//   MXFP4: the smallest power of two s with a <= 6 s = 1.5 * 2^2 s, 2^-127 at least.
-//   NVFP4: a / (6 g) to the nearest E4M3, 448 at most; six_g = 6 g.
-// A block with an infinity or NaN: a NaN scale (and any finite codes).
+// The larger magnitude, with any sign; NaN where one is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float m;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+// silu(g), g / (1 + exp(-g)), to a few units in the last place; -inf: NaN, as the
+// formula has it.
+__device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+
+// NVFP4's factor g of the whole matrix, 6 g, and 1 / (6 g) to the nearest fp32.
+struct MxGain {
+    float g = 1.f, six_g = 6.f, inv = 0.f;
+};
+
+// The scale byte of a block whose largest magnitude is |a|, and the factor its
+// values are multiplied with before they are rounded to codes.
+//   MXFP4: the smallest power of two s with |a| <= 6 s = 1.5 * 2^2 s, 2^-127 at least.
+//   NVFP4: |a| / (6 g) to the nearest E4M3, 448 at most.  The quotient is the nearest
+//   fp32 one, by Markstein's method (IBM J. Res. Dev. 34, 1990): from the nearest 1 / b,
+//   q + (a - q b) (1 / b) with an exact remainder is the nearest fp32 to a / b once q is
+//   within a unit in the last place of it, which one such step ensures; likewise 1 /
+//   (s g) from the hardware's estimate.  (Divisions of the language took as long as the
+//   rest of the kernel.)
+// A block with an infinity or NaN: a NaN scale, and a factor of 0: its codes are zeros.
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_block_scale(uint32_t a, float g, float six_g, float &mul) {
+__device__ __forceinline__ uint32_t mx_block_scale(float a, const MxGain &gain, float &mul) {
+    const uint32_t bits = __float_as_uint(a) & 0x7FFFFFFFu;
     if constexpr (FMT == 0) {
-        const int E = max((int)(a >> 23) - ((a & 0x7FFFFFu) > 0x400000u ? 1 : 2), 0);
-        mul = __uint_as_float((uint32_t)(254 - E) << 23);
-        if (a < kInfBits) return (uint32_t)E;
-        mul = 0.f;
-        return 255u;
+        const int E = max((int)(bits >> 23) - ((bits & 0x7FFFFFu) > 0x400000u ? 1 : 2), 0);
+        mul = bits < kInfBits ? __uint_as_float((uint32_t)(254 - E) << 23) : 0.f;
+        return bits < kInfBits ? (uint32_t)E : 255u;
     } else {
-        const float t = fminf(__fdiv_rn(__uint_as_float(a), six_g), 448.f);
+        const float x = __uint_as_float(bits);
+        const float q = x * gain.inv;
+        float t = fmaf(fmaf(-q, gain.six_g, x), gain.inv, q);
+        t = fmaf(fmaf(-t, gain.six_g, x), gain.inv, t);
+        t = q < 500.f ? fminf(t, 448.f) : 448.f;  // (beyond, the remainder may overflow)
         uint16_t b;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(0.f), "f"(t));
-        const float sg = e4m3_value(b) * g;
-        mul = (b & 255u) ? __frcp_rn(sg) : 0.f;
-        if (a < kInfBits) return b & 255u;
-        mul = 0.f;
-        return 127u;
+        const uint32_t sc = b & 255u;
+        const float sg = e4m3_value(sc) * gain.g;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sg));
+        r = fmaf(r, fmaf(-sg, r, 1.f), r);
+        mul = sc != 0u && bits < kInfBits ? r : 0.f;
+        return bits < kInfBits ? sc : 127u;
     }
 }
-// Codes of values whose factor is 0: zeros, though a value may be NaN or
-// infinite.
-__device__ __forceinline__ float mx_scaled(float v, float mul) { return mul == 0.f ? 0.f : v * mul; }
 
 // ------------------------------------------------------------------ tensor core
 

@@ -2,9 +2,10 @@
 // optionally behind an RMSNorm (x / rms(x) gamma) or a SwiGLU (silu(x) up);
 // dequantising; codes and scales from and into plain rows.
 //
-// Pure streams.  A warp takes 256 columns of a row, one record row: a lane eight
-// consecutive values, so that a block of 32 (16) is four (two) lanes, its largest
-// magnitude two (one) shuffles, and the warp's codes are one whole 128-byte line.
+// Pure streams.  A lane takes sixteen consecutive values, half a record row a half
+// warp: a block of 32 (16) is two lanes (one), a row's codes of a record one whole
+// 128-byte line.  (Eight values a lane: half the time of the 16-bit forms was the
+// arithmetic of scales and addresses.)
 #include <algorithm>
 
 #include "mx_common.cuh"
@@ -14,26 +15,27 @@ namespace dev {
 
 constexpr int kMxThreads = 256, kMxWarps = kMxThreads / 32;
 
-// Eight consecutive values in 16-byte words of T.
+// Sixteen consecutive values as they are stored.
 template <typename T>
-struct Raw8 {
-    uint4 w[sizeof(T) / 2];
+struct Raw16 {
+    static constexpr int N = (int)sizeof(T);
+    uint4 w[N];
     __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+        for (int i = 0; i < N; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < N; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    __device__ __forceinline__ void values(float (&v)[8]) const {
+    __device__ __forceinline__ void values(float (&v)[16]) const {
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w_of(w[i / 4], i % 4));
+            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w_of(w[i / 4], i % 4));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t x = w_of(w[0], i);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = w_of(w[i / 4], i % 4);
                 if constexpr (std::is_same<T, __half>::value) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
                     v[2 * i] = f.x;
@@ -47,191 +49,209 @@ struct Raw8 {
     }
 };
 
-__device__ __forceinline__ float mx_silu(float g) { return g / (1.f + __expf(-g)); }
-
-// A warp's 256 values (lane: 8 of them) of row `row`, column tile kt, into the
-// matrix at `out`.
+// The sixteen values v f from column c of row `row` into the matrix at `out`; all
+// lanes of a warp, those of a row of a record (16 of them) in order.
 template <int FMT>
-__device__ __forceinline__ void mx_store(uint8_t *out, int row, int kt, int KT, const float (&v)[8], float g, float six_g,
-                                         int lane) {
-    uint32_t a = 0;
+__device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const float (&v)[16], float f,
+                                         const MxGain &gain) {
+    float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 1; o < mx_block(FMT) / 8; o <<= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    for (int i = 0; i < 16; ++i) a = max_abs(a, v[i]);
+    if constexpr (FMT == 0) a = max_abs(a, __shfl_xor_sync(0xffffffffu, a, 1));
     float mul;
-    const uint32_t sc = mx_block_scale<FMT>(a, g, six_g, mul);
-    float u[8];
+    const uint32_t sc = mx_block_scale<FMT>(a * f, gain, mul);
+    const float by = f * mul;
+    float lo[8], hi[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = mx_scaled(v[i], mul);
-    uint8_t *rec = out + ((size_t)(row / kMxRows) * KT + kt) * mx_rec(FMT);
-    const int r = row % kMxRows;
-    *reinterpret_cast<uint32_t *>(rec + mx_code_off(r, 4 * lane)) = e2m1x8(u);
-    // four blocks' scales a word: lanes 0, 16 (MXFP4) or 0, 8, 16, 24 (NVFP4)
-    constexpr int L = mx_block(FMT) / 8;  // lanes of a block
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = v[i] * by;
+        hi[i] = v[8 + i] * by;
+    }
+    const uint2 code = mul == 0.f ? make_uint2(0u, 0u) : make_uint2(e2m1x8(lo), e2m1x8(hi));
+    // four blocks' scales a word
+    constexpr int L = mx_block(FMT) / 16;  // lanes of a block
     uint32_t word = sc;
     word |= __shfl_down_sync(0xffffffffu, word, L) << 8;
     word |= __shfl_down_sync(0xffffffffu, word, 2 * L) << 16;
-    if (lane % (4 * L) == 0) *reinterpret_cast<uint32_t *>(rec + mx_scale_off(r, lane / (4 * L))) = word;
+    if (!live) return;
+    const int r = row % kMxRows, h = (c % kMxK) / 16;  // h: which sixteen of the record's row
+    uint8_t *rec = out + ((size_t)(row / kMxRows) * KT + c / kMxK) * mx_rec(FMT);
+    *reinterpret_cast<uint2 *>(rec + mx_code_off(r, 8 * h)) = code;
+    if (h % (4 * L) == 0) *reinterpret_cast<uint32_t *>(rec + mx_scale_off(r, h / (4 * L))) = word;
 }
 
-// Values as they are, or a SwiGLU of two rows: a warp takes kMxAhead units (row,
-// column tile), their loads issued together.
-constexpr int kMxAhead = 4;
+// A warp's units: two rows (of the whole batch) and a column tile, a half warp each.
+struct MxUnit {
+    int pair, kt;
+    __device__ __forceinline__ MxUnit(long long u, int KT) : pair((int)(u / KT)), kt((int)(u - (long long)pair * KT)) {}
+    __device__ __forceinline__ void next(int KT) {
+        if (++kt == KT) {
+            kt = 0;
+            ++pair;
+        }
+    }
+};
+
+// Values as they are, or a SwiGLU of two rows: a warp takes AH units, their loads
+// issued together.
+template <typename T, bool GLU>
+constexpr int mx_ahead() { return sizeof(T) == 4 || GLU ? 2 : 4; }
 template <typename T, int FMT, bool GLU>
 __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_constant__ MxQuantParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // after the wait: a kernel that starts on this may read what was complete before
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, KT = mx_ktiles(p.k);
-    const long long units = (long long)p.batch * p.rows * KT;
-    const long long u0 = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * kMxAhead;
+    constexpr int AH = mx_ahead<T, GLU>();
+    const int lane = threadIdx.x & 31, half = lane >> 4, KT = mx_ktiles(p.k), rows = p.batch * p.rows;
     const long long mat = (long long)mx_rtiles(p.rows) * KT * mx_rec(FMT);
-    const float six_g = 6.f * p.scale;
-    Raw8<T> x[kMxAhead], y[GLU ? kMxAhead : 1];
-    long long row = u0 / KT;  // over the batch
-    int kt = (int)(u0 - row * KT);
-    const long long row0 = row;
-    const int kt0 = kt;
-    auto next = [&]() {
-        if (++kt == KT) {
-            kt = 0;
-            ++row;
-        }
-    };
+    const MxUnit first((((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * AH), KT);
+    const MxGain gain{p.scale, p.six_g, p.inv};
+    Raw16<T> x[AH], y[GLU ? AH : 1];
+    MxUnit u = first;
 #pragma unroll
-    for (int i = 0; i < kMxAhead; ++i, next()) {
-        const int c = kt * kMxK + 8 * lane;
+    for (int i = 0; i < AH; ++i, u.next(KT)) {
+        const int c = u.kt * kMxK + 16 * (lane & 15);
+        const long long row = 2ll * u.pair + half;
         x[i].zero();
         if constexpr (GLU) y[i].zero();
-        if (u0 + i < units && c < p.k) {
+        if (row < rows && c < p.k) {
             x[i].load((const T *)p.x + row * p.ld + c);
             if constexpr (GLU) y[i].load((const T *)p.up + row * p.ld + c);
         }
     }
-    row = row0;
-    kt = kt0;
+    u = first;
 #pragma unroll
-    for (int i = 0; i < kMxAhead; ++i, next()) {
-        if (u0 + i >= units) break;
-        float v[8];
+    for (int i = 0; i < AH; ++i, u.next(KT)) {
+        if (2ll * u.pair >= rows) break;
+        float v[16];
         x[i].values(v);
         if constexpr (GLU) {
-            float w[8];
+            float w[16];
             y[i].values(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = mx_silu(v[e]) * w[e];
+            for (int e = 0; e < 16; ++e) v[e] = mx_silu(v[e]) * w[e];
         }
-        const long long b = p.batch == 1 ? 0 : row / p.rows;
-        mx_store<FMT>(p.out + b * mat, (int)(row - b * p.rows), kt, KT, v, p.scale, six_g, lane);
+        const int row = 2 * u.pair + half, b = p.batch == 1 ? 0 : row / p.rows;
+        mx_store<FMT>(p.out + b * mat, row < rows, row - b * p.rows, u.kt * kMxK + 16 * (lane & 15), KT, v, 1.f, gain);
     }
 }
 
-// Behind an RMSNorm: WPR warps a row (1 or all eight of the CTA), which keep up to
-// R column tiles each in registers; what a longer row has beyond them is read
-// again after the sum of squares is known.
+// Behind an RMSNorm: WPR warps a row, which keep up to R sixteens a lane of it in
+// registers (what a longer row has beyond is read again once its sum of squares is
+// known); the next row's loads are issued before this one's sum is taken.
 template <typename T, int FMT, int WPR, int R>
 __global__ void __launch_bounds__(kMxThreads) q4mx_quant_norm_kernel(const __grid_constant__ MxQuantParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float sums[kMxWarps];
+    __shared__ float sums[2][kMxWarps];
+    constexpr int RPC = kMxWarps / WPR;  // rows of a CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, KT = mx_ktiles(p.k);
-    const int w = warp % WPR;
-    const long long row = (long long)blockIdx.x * (kMxWarps / WPR) + warp / WPR, rows = (long long)p.batch * p.rows;
-    const bool live = row < rows;
-    const T *src = (const T *)p.x + (live ? row : 0) * p.ld;
-    const float six_g = 6.f * p.scale;
-    Raw8<T> x[R];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int c = (w + i * WPR) * kMxK + 8 * lane;
-        x[i].zero();
-        if (live && c < p.k) x[i].load(src + c);
-    }
-    auto squares = [&](const Raw8<T> &a) {
-        float v[8];
-        a.values(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(v[e], v[e], sum);
-    };
-#pragma unroll
-    for (int i = 0; i < R; ++i) squares(x[i]);
-    for (int t = w + R * WPR; t < KT; t += WPR) {
-        const int c = t * kMxK + 8 * lane;
-        Raw8<T> a;
-        a.zero();
-        if (live && c < p.k) a.load(src + c);
-        squares(a);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if constexpr (WPR > 1) {
-        if (lane == 0) sums[warp] = sum;
-        __syncthreads();
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kMxWarps; ++i) sum += sums[i];
-    }
-    if (!live) return;
-    const float rstd = 1.f / sqrtf(sum / (float)p.k + p.eps);
-    const long long b = p.batch == 1 ? 0 : row / p.rows;
-    uint8_t *out = p.out + b * ((long long)mx_rtiles(p.rows) * KT * mx_rec(FMT));
-    const int r = (int)(row - b * p.rows);
-    auto put = [&](const Raw8<T> &a, int t) {
-        const int c = t * kMxK + 8 * lane;
-        float v[8], gm[8] = {};
-        a.values(v);
-        if (c < p.k) {
-            const float4 g0 = *reinterpret_cast<const float4 *>(p.gamma + c);
-            const float4 g1 = *reinterpret_cast<const float4 *>(p.gamma + c + 4);
-            gm[0] = g0.x, gm[1] = g0.y, gm[2] = g0.z, gm[3] = g0.w;
-            gm[4] = g1.x, gm[5] = g1.y, gm[6] = g1.z, gm[7] = g1.w;
-        }
-        // (columns behind k are zeros even where rstd is infinite or NaN)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = c < p.k ? v[e] * rstd * gm[e] : 0.f;
-        mx_store<FMT>(out, r, t, KT, v, p.scale, six_g, lane);
-    };
+    const int at = 16 * (32 * (warp % WPR) + lane), step = 512 * WPR, kpad = KT * kMxK;
+    const int rows = p.batch * p.rows;
+    const long long mat = (long long)mx_rtiles(p.rows) * KT * mx_rec(FMT);
+    const MxGain gain{p.scale, p.six_g, p.inv};
+    // the lane's columns are the same in every row
+    float gm[R][16];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-        if (w + i * WPR < KT) put(x[i], w + i * WPR);
-    for (int t = w + R * WPR; t < KT; t += WPR) {
-        const int c = t * kMxK + 8 * lane;
-        Raw8<T> a;
-        a.zero();
-        if (c < p.k) a.load(src + c);
-        put(a, t);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const float4 g = at + i * step < p.k ? *reinterpret_cast<const float4 *>(p.gamma + at + i * step + e)
+                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            gm[i][e] = g.x, gm[i][e + 1] = g.y, gm[i][e + 2] = g.z, gm[i][e + 3] = g.w;
+        }
+    Raw16<T> next[R];
+    auto fetch = [&](int row) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            next[i].zero();
+            if (row < rows && at + i * step < p.k) next[i].load((const T *)p.x + row * p.ld + at + i * step);
+        }
+    };
+    int row = blockIdx.x * RPC + warp / WPR, turn = 0;
+    fetch(row);
+    for (; row - warp / WPR < rows; row += gridDim.x * RPC, turn ^= 1) {
+        const bool live = row < rows;
+        const T *src = (const T *)p.x + (live ? row : 0) * p.ld;
+        Raw16<T> x[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = next[i];
+        fetch(row + gridDim.x * RPC);
+        float sum = 0.f;
+        auto squares = [&](const Raw16<T> &a) {
+            float v[16];
+            a.values(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum = fmaf(v[e], v[e], sum);
+        };
+#pragma unroll
+        for (int i = 0; i < R; ++i) squares(x[i]);
+        for (int c = at + R * step; c < p.k; c += step) {
+            Raw16<T> a;
+            a.load(src + c);
+            squares(a);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if constexpr (WPR > 1) {
+            if (lane == 0) sums[turn][warp] = sum;
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) sum += sums[turn][warp / WPR * WPR + i];
+        }
+        const float rstd = 1.f / sqrtf(sum / (float)p.k + p.eps);
+        const int b = p.batch == 1 ? 0 : row / p.rows;
+        auto put = [&](const Raw16<T> &a, const float (&gv)[16], int c) {
+            float v[16];
+            a.values(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] *= gv[e];
+            // (columns behind k are zeros even where rstd is infinite or NaN)
+            mx_store<FMT>(p.out + b * mat, live && c < kpad, row - b * p.rows, c, KT, v, c < p.k ? rstd : 1.f, gain);
+        };
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (at - 16 * lane + i * step < kpad) put(x[i], gm[i], at + i * step);
+        for (int c = at + R * step; c - 16 * lane < kpad; c += step) {
+            Raw16<T> a;
+            float gv[16] = {};
+            a.zero();
+            if (c < p.k) {
+                a.load(src + c);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) gv[e] = p.gamma[c + e];
+            }
+            put(a, gv, c);
+        }
     }
 }
 
-// Back into values: g s e, rounded once to T.
+// Back into values: g s e, rounded once to T.  A warp a record's row, eight values a
+// lane: its stores are whole lines (sixteen a lane: 16 -> 19 us for 8191 x 4096).
+constexpr int kMxAhead = 4;  // units (row, column tile) of a warp
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kMxThreads) q4mx_dequant_kernel(const __grid_constant__ MxCopyParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, KT = mx_ktiles(p.k);
-    const long long units = (long long)p.batch * p.rows * KT;
+    constexpr int L = mx_block(FMT) / 8;
+    const int lane = threadIdx.x & 31, KT = mx_ktiles(p.k), rows = p.batch * p.rows;
     const long long mat = (long long)mx_rtiles(p.rows) * KT * mx_rec(FMT);
     const long long u0 = ((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * kMxAhead;
+    const int row0 = (int)(u0 / KT), kt0 = (int)(u0 - (long long)row0 * KT);
     uint32_t code[kMxAhead], sc[kMxAhead];
-    long long row = u0 / KT;
-    int kt = (int)(u0 - row * KT);
-    const long long row0 = row;
-    const int kt0 = kt;
+    int row = row0, kt = kt0;
     auto next = [&]() {
         if (++kt == KT) {
             kt = 0;
             ++row;
         }
     };
-    constexpr int L = mx_block(FMT) / 8;
 #pragma unroll
     for (int i = 0; i < kMxAhead; ++i, next()) {
         code[i] = sc[i] = 0u;
-        if (u0 + i < units) {
-            const long long b = p.batch == 1 ? 0 : row / p.rows;
-            const int rr = (int)(row - b * p.rows), r = rr % kMxRows;
+        if (row < rows) {
+            const int b = p.batch == 1 ? 0 : row / p.rows, rr = row - b * p.rows, r = rr % kMxRows;
             const uint8_t *rec = p.mx + b * mat + ((size_t)(rr / kMxRows) * KT + kt) * mx_rec(FMT);
             code[i] = *reinterpret_cast<const uint32_t *>(rec + mx_code_off(r, 4 * lane));
             sc[i] = rec[mx_scale_off(r, lane / (4 * L)) + (lane / L) % 4];
@@ -242,12 +262,13 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_dequant_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < kMxAhead; ++i, next()) {
         const int c = kt * kMxK + 8 * lane;
-        if (u0 + i >= units || c >= p.k) continue;
+        if (row >= rows || c >= p.k) continue;
         const float s = mx_scale_value<FMT>(sc[i]);
         float v[8];
+        e2m1_values(code[i], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e2m1_value((code[i] >> (4 * e)) & 15u) * s * p.scale;
-        T *dst = (T *)p.out + row * p.k + c;
+        for (int e = 0; e < 8; ++e) v[e] = FMT == 0 ? v[e] * s : v[e] * s * p.scale;
+        T *dst = (T *)p.out + (size_t)row * p.k + c;
         if constexpr (sizeof(T) == 4) {
             __stcs(reinterpret_cast<float4 *>(dst), make_float4(v[0], v[1], v[2], v[3]));
             __stcs(reinterpret_cast<float4 *>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
@@ -293,11 +314,14 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_pack_kernel(const __grid_cons
 }  // namespace dev
 
 namespace {
-// CTAs of a launch over `units` warps' work
-unsigned mx_grid(long long units) {
-    const long long per = (long long)dev::kMxWarps * dev::kMxAhead;
+// CTAs of a launch over `units` of which a warp takes `ahead`
+unsigned mx_grid(long long units, int ahead) {
+    const long long per = (long long)dev::kMxWarps * ahead;
     return (unsigned)((units + per - 1) / per);
 }
+// units of two rows and a column tile
+long long mx_pairs(int batch, int rows, int k) { return ((long long)batch * rows + 1) / 2 * mx_ktiles(k); }
+
 template <typename Kern, typename P>
 int mx_launch(Kern kern, unsigned grid, const P &p, cudaStream_t stream) {
     cudaLaunchAttribute attr;
@@ -305,43 +329,46 @@ int mx_launch(Kern kern, unsigned grid, const P &p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
 
+template <typename T, int FMT, int WPR, int R>
+int launch_mx_norm(const MxQuantParams &p, int sms, cudaStream_t stream) {
+    const long long ctas = ((long long)p.batch * p.rows * WPR + dev::kMxWarps - 1) / dev::kMxWarps;
+    return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, WPR, R>, (unsigned)std::min<long long>(ctas, 6ll * sms), p, stream);
+}
 template <typename T, int FMT>
-int launch_mx_quant_t(const MxQuantParams &p, cudaStream_t stream) {
-    const int KT = mx_ktiles(p.k);
-    const long long rows = (long long)p.batch * p.rows;
+int launch_mx_quant_t(const MxQuantParams &p, int sms, cudaStream_t stream) {
     if (p.gamma) {
-        // a warp a row up to 2048 columns where there are rows for all SMs, else a CTA a row
-        if (KT <= 2 || (KT <= 8 && rows >= 2048)) {
-            const unsigned grid = (unsigned)((rows + dev::kMxWarps - 1) / dev::kMxWarps);
-            if (KT <= 2) return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, 1, 2>, grid, p, stream);
-            return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, 1, 8>, grid, p, stream);
-        }
-        if (KT <= 8) return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, 8, 1>, (unsigned)rows, p, stream);
-        if (KT <= 16) return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, 8, 2>, (unsigned)rows, p, stream);
-        return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, 8, 8>, (unsigned)rows, p, stream);
+        // as many warps a row as it has 512s, up to eight
+        if (p.k <= 512) return launch_mx_norm<T, FMT, 1, 1>(p, sms, stream);
+        if (p.k <= 1024) return launch_mx_norm<T, FMT, 2, 1>(p, sms, stream);
+        if (p.k <= 2048) return launch_mx_norm<T, FMT, 4, 1>(p, sms, stream);
+        if (p.k <= 4096) return launch_mx_norm<T, FMT, 8, 1>(p, sms, stream);
+        return launch_mx_norm<T, FMT, 8, 2>(p, sms, stream);
     }
-    const unsigned grid = mx_grid(rows * KT);
-    if (p.up) return mx_launch(dev::q4mx_quant_kernel<T, FMT, true>, grid, p, stream);
-    return mx_launch(dev::q4mx_quant_kernel<T, FMT, false>, grid, p, stream);
+    const long long units = mx_pairs(p.batch, p.rows, p.k);
+    if (p.up) return mx_launch(dev::q4mx_quant_kernel<T, FMT, true>, mx_grid(units, dev::mx_ahead<T, true>()), p, stream);
+    return mx_launch(dev::q4mx_quant_kernel<T, FMT, false>, mx_grid(units, dev::mx_ahead<T, false>()), p, stream);
 }
 }  // namespace
 
-int launch_mx_quant(const MxQuantParams &p, int fmt, int dtype, void *stream_) {
+int launch_mx_quant(const MxQuantParams &params, int fmt, int dtype, int sms, void *stream_) {
+    MxQuantParams p = params;
+    p.six_g = 6.f * p.scale;
+    p.inv = 1.f / p.six_g;
     cudaStream_t s = (cudaStream_t)stream_;
     switch (2 * dtype + fmt) {
-        case 0: return launch_mx_quant_t<float, 0>(p, s);
-        case 1: return launch_mx_quant_t<float, 1>(p, s);
-        case 2: return launch_mx_quant_t<__half, 0>(p, s);
-        case 3: return launch_mx_quant_t<__half, 1>(p, s);
-        case 4: return launch_mx_quant_t<__nv_bfloat16, 0>(p, s);
-        case 5: return launch_mx_quant_t<__nv_bfloat16, 1>(p, s);
+        case 0: return launch_mx_quant_t<float, 0>(p, sms, s);
+        case 1: return launch_mx_quant_t<float, 1>(p, sms, s);
+        case 2: return launch_mx_quant_t<__half, 0>(p, sms, s);
+        case 3: return launch_mx_quant_t<__half, 1>(p, sms, s);
+        case 4: return launch_mx_quant_t<__nv_bfloat16, 0>(p, sms, s);
+        case 5: return launch_mx_quant_t<__nv_bfloat16, 1>(p, sms, s);
     }
     return -1;
 }
 
 int launch_mx_dequant(const MxCopyParams &p, int fmt, int dtype, void *stream_) {
     cudaStream_t s = (cudaStream_t)stream_;
-    const unsigned grid = mx_grid((long long)p.batch * p.rows * mx_ktiles(p.k));
+    const unsigned grid = mx_grid((long long)p.batch * p.rows * mx_ktiles(p.k), dev::kMxAhead);
     switch (2 * dtype + fmt) {
         case 0: return mx_launch(dev::q4mx_dequant_kernel<float, 0>, grid, p, s);
         case 1: return mx_launch(dev::q4mx_dequant_kernel<float, 1>, grid, p, s);
@@ -355,7 +382,7 @@ int launch_mx_dequant(const MxCopyParams &p, int fmt, int dtype, void *stream_) 
 
 int launch_mx_pack(const MxCopyParams &p, int fmt, bool unpack, void *stream_) {
     cudaStream_t s = (cudaStream_t)stream_;
-    const unsigned grid = mx_grid((long long)p.batch * p.rows * mx_ktiles(p.k));
+    const unsigned grid = mx_grid((long long)p.batch * p.rows * mx_ktiles(p.k), dev::kMxAhead);
     if (fmt == 0) return unpack ? mx_launch(dev::q4mx_pack_kernel<0, true>, grid, p, s) : mx_launch(dev::q4mx_pack_kernel<0, false>, grid, p, s);
     return unpack ? mx_launch(dev::q4mx_pack_kernel<1, true>, grid, p, s) : mx_launch(dev::q4mx_pack_kernel<1, false>, grid, p, s);
 }

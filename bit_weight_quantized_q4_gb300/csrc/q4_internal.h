@@ -512,8 +512,9 @@ struct MxQuantParams {
     long long ld;
     int rows, k, batch;
     float eps, scale;
+    float six_g, inv;  // 6 scale and 1 / (6 scale), set by the launch
 };
-int launch_mx_quant(const MxQuantParams &p, int fmt, int dtype, void *stream);
+int launch_mx_quant(const MxQuantParams &p, int fmt, int dtype, int sms, void *stream);
 // Back into values [batch][rows][k]; and the codes and scales in plain rows
 // ([batch][rows][k / 2], [batch][rows][k / block]), each way.
 struct MxCopyParams {
