@@ -303,9 +303,15 @@ def plan(fmt: int, tiles: int, chunks: int, nb: int, pairs: bool, num_sms: int) 
 
 # ---------------------------------------------------------------- device side
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 class Q4Weight:
@@ -864,6 +870,16 @@ def _heads3(t, name, head_dim):
     return t.shape[0], t.shape[1]
 
 
+def _room_ptr(t, nbytes, device):
+    """Address of a workspace of at least `nbytes` on `device`."""
+    try:
+        if t.dtype is _torch().uint8 and t.device == device and t.is_contiguous() and t.numel() >= nbytes:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dev_buf(t, "workspace", _torch().uint8, None, device, min_numel=nbytes).data_ptr()
+
+
 def _apart(out, nbytes, *others):
     """The output at address `out` must not share memory with the inputs
     (address, bytes): it is written while they are read."""
@@ -1026,6 +1042,7 @@ def q4_logprobs(logits, tokens=None, top: int = 0, entropy: bool = True):
 # ---------------------------------------------------------------- microscaled 4-bit
 
 _kinds = {}
+_MX_BLOCK = (32, 16)  # columns that share a scale, by format
 
 
 def _kind(dtype, name):
@@ -1038,6 +1055,13 @@ def _kind(dtype, name):
     return kind
 
 
+def _mx_bytes(fmt, rows, k):
+    """q4_mx_bytes of a shape that the library takes (else raises)."""
+    if fmt not in (0, 1) or not 1 <= rows <= 1 << 24 or not 32 <= k <= 65536 or k % 32:
+        raise ValueError("bad format or shape: fmt=%s rows=%s k=%s (k: a multiple of 32, 65536 at most)" % (fmt, rows, k))
+    return (rows + 127) // 128 * ((k + 255) // 256) * (17408 + 1024 * fmt)
+
+
 class MXMatrix:
     """Matrices of microscaled 4-bit values, ``batch`` of them of ``[rows, k]``, in device memory (owns its
     tensor): E2M1 codes whose blocks of 32 columns share a power of two (``Q4_MX_MXFP4``) or whose blocks of 16
@@ -1046,23 +1070,22 @@ class MXMatrix:
 
     def __init__(self, fmt: int, rows: int, k: int, batch: int = 1, scale: float = 1.0, device="cuda", tensor=None):
         torch = _torch()
-        self.fmt, self.rows, self.k, self.batch, self.scale = int(fmt), int(rows), int(k), int(batch), float(scale)
-        one = int(lib().q4_mx_bytes(self.fmt, self.rows, self.k))
-        if one == 0 or self.batch < 1:
-            raise ValueError("bad format or shape: fmt=%d rows=%d k=%d batch=%d" % (self.fmt, self.rows, self.k, self.batch))
-        self.nbytes = one * self.batch
+        if batch < 1:
+            raise ValueError("a batch of %s matrices" % batch)
+        self.fmt, self.rows, self.k, self.batch, self.scale = fmt, rows, k, batch, scale
+        self.nbytes = n = _mx_bytes(fmt, rows, k) * batch
         if tensor is None:
-            tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        self.tensor = _dev_buf(tensor, "tensor", torch.uint8, None, tensor.device, min_numel=self.nbytes)
-        self.device = tensor.device
-        self._c = _CMx(self.fmt, self.rows, self.k, self.batch, tensor.data_ptr(), self.nbytes, self.scale)
-        self._ref = ctypes.byref(self._c)
-        self._room = {}
+            tensor = torch.empty(n, dtype=torch.uint8, device=device)
+        else:
+            _dev_buf(tensor, "tensor", torch.uint8, None, tensor.device, min_numel=n)
+        self.tensor, self.device = tensor, tensor.device
+        self._c = c = _CMx(fmt, rows, k, batch, tensor.data_ptr(), n, scale)
+        self._ref = ctypes.byref(c)
 
     @property
     def block(self) -> int:
         """Columns that share a scale."""
-        return 32 if self.fmt == Q4_MX_MXFP4 else 16
+        return _MX_BLOCK[self.fmt]
 
     @property
     def weight_bytes(self) -> int:
@@ -1106,35 +1129,40 @@ def _mx(m, name):
 
 
 def _mx_src(x, gamma, eps, up):
-    """The q4_mx_src of ``x [.., k]`` (rows at an even distance, values next to each other), its rows and k."""
+    """The q4_mx_src of ``x [.., k]`` (rows at an even distance, values next to each other)."""
     torch = _torch()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise TypeError("x must be a CUDA float32, float16 or bfloat16 tensor")
-    kind = _kind(x.dtype, "x")
-    if x.dim() not in (2, 3) or 0 in x.shape:
-        raise ValueError("x must be [rows, k] or [batch, rows, k], with rows")
-    k = x.shape[-1]
-    if x.dim() == 2:
-        rows, ld = x.shape[0], x.stride(0) if x.shape[0] > 1 else k
-    else:
+    kind = _kinds.get(x.dtype)
+    if kind is None:
+        kind = _kind(x.dtype, "x")
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 2:
+        rows, k = shape
+        ld = stride[0] if rows > 1 else k
+    elif len(shape) == 3:
         if not x.is_contiguous():
             raise ValueError("a batch x must be contiguous")
-        rows, ld = x.shape[0] * x.shape[1], k
-    if x.stride(-1) != 1 or ld < k:
+        rows, k = shape[0] * shape[1], shape[2]
+        ld = k
+    else:
+        raise ValueError("x must be [rows, k] or [batch, rows, k]")
+    if rows == 0 or k == 0:
+        raise ValueError("x must have rows and columns")
+    if stride[-1] != 1 or ld < k:
         raise ValueError("the values of a row of x must be next to each other")
     up_p = gamma_p = None
     if up is not None:
         if gamma is not None:
             raise ValueError("gamma (a norm) and up (a SwiGLU) exclude each other")
-        if not isinstance(up, torch.Tensor) or up.dtype != x.dtype or up.device != x.device or up.shape != x.shape:
+        if not isinstance(up, torch.Tensor) or up.dtype != x.dtype or up.device != x.device or up.shape != shape:
             raise ValueError("up must be like x")
-        if up.stride(-1) != 1 or (x.dim() == 2 and x.shape[0] > 1 and up.stride(0) != ld) or (
-                x.dim() == 3 and not up.is_contiguous()):
+        if up.stride() != stride and (rows > 1 or up.stride(-1) != 1):
             raise ValueError("up must have the strides of x")
         up_p = up.data_ptr()
     if gamma is not None:
         gamma_p = _ptr(gamma, "gamma", torch.float32, (k,), x.device)
-    return _CMxSrc(x.data_ptr(), up_p, gamma_p, ld, kind, rows, k, float(eps))
+    return _CMxSrc(x.data_ptr(), up_p, gamma_p, ld, kind, rows, k, eps)
 
 
 def q4_mx_quant(x, fmt: int = Q4_MX_MXFP4, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, out=None):
@@ -1144,9 +1172,10 @@ def q4_mx_quant(x, fmt: int = Q4_MX_MXFP4, gamma=None, eps: float = 0.0, up=None
     amax / (6 * 448).  ``out``: an MXMatrix of the same shape to write into (its scale holds)."""
     src = _mx_src(x, gamma, eps, up)
     batch = x.shape[0] if x.dim() == 3 else 1
+    rows, k = src.rows // batch, src.k
     if out is None:
-        out = MXMatrix(fmt, x.shape[-2], x.shape[-1], batch, scale, x.device)
-    elif (_mx(out, "out").rows, out.k, out.batch, out.device) != (x.shape[-2], x.shape[-1], batch, x.device):
+        out = MXMatrix(fmt, rows, k, batch, scale, x.device)
+    elif (_mx(out, "out").rows, out.k, out.batch, out.device) != (rows, k, batch, x.device):
         raise ValueError("out has another shape or device than x")
     _check(_launch(out.device, lib().q4_mx_quant, ctypes.byref(src), out._ref), "q4_mx_quant")
     return out
@@ -1167,18 +1196,10 @@ def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
     return out
 
 
-def _mx_room(W, nb):
-    """Bytes of nb quantised rows of W's format and width (by the shapes alone)."""
-    n = W._room.get(nb)
-    if n is None:
-        n = W._room[nb] = int(lib().q4_mx_bytes(W.fmt, nb, W.k))
-    return n
-
-
 def q4_mx_gemm_workspace(W: MXMatrix, nb: int):
     """A workspace for ``q4_mx_gemm`` with up to ``nb`` float rows: the room of the quantised rows.  Calls that may
     run at the same time, captured ones too, need one each."""
-    return _torch().empty(_mx_room(_mx(W, "W"), int(nb)), dtype=_torch().uint8, device=W.device)
+    return _torch().empty(_mx_bytes(_mx(W, "W").fmt, int(nb), W.k), dtype=_torch().uint8, device=W.device)
 
 
 def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, dtype=None,
@@ -1188,51 +1209,48 @@ def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, sc
     ``eps``, ``up``, ``scale``).  ``y`` and ``r`` are ``[nb, n]`` of ``dtype`` (by default x's, float32 for an
     MXMatrix); ``out`` may be ``r``."""
     torch = _torch()
-    W = _mx(W, "W")
-    dev, given = W.device, isinstance(x, MXMatrix)
+    dev, n, k = _mx(W, "W").device, W.rows, W.k
+    given = isinstance(x, MXMatrix)
     if given:
         if gamma is not None or up is not None:
             raise ValueError("x is quantised already: gamma and up are q4_mx_quant's")
-        nb, k = x.rows, x.k
+        nb, got = x.rows, x.k
     else:
         src = _mx_src(x, gamma, eps, up)
-        nb, k = src.rows, src.k
+        nb, got = src.rows, src.k
         if x.dim() != 2:
-            raise ValueError("x must be [nb, %d]" % W.k)
+            raise ValueError("x must be [nb, %d]" % k)
     if x.device != dev:
         raise ValueError("x is on %s, W on %s" % (x.device, dev))
-    if k != W.k:
-        raise ValueError("x must be [nb, %d]" % W.k)
+    if got != k:
+        raise ValueError("x must be [nb, %d]" % k)
     if dtype is None:
         dtype = out.dtype if out is not None else torch.float32 if given else x.dtype
-    kind, shape = _kind(dtype, "dtype"), (nb, W.rows)
+    kind, shape = _kind(dtype, "dtype"), (nb, n)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    op = _ptr(out, "out", dtype, shape, dev)
-    nbytes = nb * W.rows * out.element_size()
-    apart = [(W._c.dev, W.nbytes)]
-    rp = None
-    if r is not None:
-        rp = _ptr(r, "r", dtype, shape, dev)
-        if rp != op:
+        out = torch.empty(shape, dtype=dtype, device=dev)  # apart from everything
+        op = out.data_ptr()
+        rp = None if r is None else _ptr(r, "r", dtype, shape, dev)
+    else:
+        op = _ptr(out, "out", dtype, shape, dev)
+        rp = None if r is None else _ptr(r, "r", dtype, shape, dev)
+        nbytes = nb * n * out.element_size()
+        apart = [(W._c.dev, W.nbytes)]
+        if rp is not None and rp != op:
             apart.append((rp, nbytes))
-    if given:
-        apart.append((x._c.dev, x.nbytes))
+        if given:
+            apart.append((x._c.dev, x.nbytes))
+        else:
+            span = ((nb - 1) * src.ld + k) * x.element_size()
+            apart += [(src.x, span)] + ([(src.up, span)] if up is not None else [])
         _apart(op, nbytes, *apart)
+    if given:
         _check(_launch(dev, lib().q4_mx_gemm, W._ref, x._ref, rp, kind, op), "q4_mx_gemm")
         return out
-    room = _mx_room(W, nb)
+    room = _mx_bytes(W.fmt, nb, k)
     if workspace is None:
         workspace = torch.empty(room, dtype=torch.uint8, device=dev)
-    else:
-        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=room)
-    wp = workspace.data_ptr()
-    span = ((nb - 1) * src.ld + k) * x.element_size()
-    apart.append((src.x, span))
-    if up is not None:
-        apart.append((src.up, span))
-    _apart(op, nbytes, *apart)
-    X = _CMx(W.fmt, nb, k, 1, wp, room, float(scale))
+    X = _CMx(W.fmt, nb, k, 1, _room_ptr(workspace, room, dev), room, scale)
     _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op), "q4_mx_linear")
     return out
 
@@ -1312,25 +1330,27 @@ def q4_moe(x, layer: MoELayer, gamma=None, eps: float = 0.0, r=None, positions=N
     if dtype is None:
         dtype = out.dtype if out is not None else x.dtype
     kind, shape = _kind(dtype, "dtype"), (rows, hidden)
-    if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-    op = _ptr(out, "out", dtype, shape, dev)
     rp = None if r is None else _ptr(r, "r", dtype, shape, dev)
     pos = None if positions is None else _ptr(positions, "positions", torch.int32, (rows,), dev)
-    nbytes = rows * hidden * out.element_size()
-    apart = [(layer.gate_up._c.dev, layer.gate_up.nbytes), (layer.down._c.dev, layer.down.nbytes),
-             (layer._c.router, 4 * layer.experts * hidden)]
-    if rp is not None and rp != op:
-        apart.append((rp, nbytes))
-    if src.x != op or x.dtype != dtype or src.ld != hidden:
-        apart.append((src.x, ((rows - 1) * src.ld + hidden) * x.element_size()))
-    _apart(op, nbytes, *apart)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)  # apart from everything
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", dtype, shape, dev)
+        nbytes = rows * hidden * out.element_size()
+        apart = [(layer.gate_up._c.dev, layer.gate_up.nbytes), (layer.down._c.dev, layer.down.nbytes),
+                 (layer._c.router, 4 * layer.experts * hidden)]
+        if rp is not None and rp != op:
+            apart.append((rp, nbytes))
+        if src.x != op or x.dtype != dtype or src.ld != hidden:
+            apart.append((src.x, ((rows - 1) * src.ld + hidden) * x.element_size()))
+        _apart(op, nbytes, *apart)
     idx = torch.empty((rows, layer.top_k), dtype=torch.int32, device=dev)
     weight = torch.empty((rows, layer.top_k), dtype=torch.float32, device=dev)
+    need = layer.workspace_bytes(rows)
     if workspace is None:
         workspace = q4_moe_workspace(layer, rows)
-    else:
-        _dev_buf(workspace, "workspace", torch.uint8, None, dev, min_numel=layer.workspace_bytes(rows))
+    wp = _room_ptr(workspace, need, dev)
     _check(_launch(dev, lib().q4_moe, layer._ref, ctypes.byref(src), pos, rp, kind, op, idx.data_ptr(),
-                   weight.data_ptr(), workspace.data_ptr(), workspace.numel()), "q4_moe")
+                   weight.data_ptr(), wp, workspace.numel()), "q4_moe")
     return out, idx, weight

@@ -378,87 +378,114 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
+        // (one thread's chain of instructions: what stages share is computed once, slots are counted)
         if (lane == 0) {
-            int it = 0;
             uint32_t extra = (uint32_t)p.extra_tx;
             bool ok = true;
-            // stage i's weights; its activations follow on the same barrier
-            auto weights = [&](const uint8_t *src, int i) {
-                const int s = i % S;
-                if (i >= S && !mbar_wait(b_empty + 8 * s, (uint32_t)(i / S - 1) & 1u, lim)) return false;
-                mbar_expect_tx(b_full + 8 * s, kMoeStage + extra);
+            struct Slot {  // the next slot to fill: of weights, of activations
+                uint32_t dst, bar, par;
+                __device__ __forceinline__ void next(uint32_t ring, uint32_t b_full) {
+                    dst += kMoeStage, bar += 8;
+                    if (bar == b_full + 8 * S) {
+                        dst = ring;
+                        bar = b_full;
+                        par ^= 1;
+                    }
+                }
+            } ws = {ring, b_full, 1}, as = {ring, b_full, 0};  // (a wait for the phase before the first passes)
+            int issued = 0;
+            // a stage's weights; its activations follow on the same barrier
+            auto weights = [&](const uint8_t *src) {
+                if (!mbar_wait(ws.bar + 8 * S, ws.par, lim)) return false;  // b_empty of this slot
+                mbar_expect_tx(ws.bar, kMoeStage + extra);
                 extra = 0;
-                bulk_copy(ring + s * kMoeStage, src, REC, b_full + 8 * s);
+                bulk_copy(ws.dst, src, REC, ws.bar);
+                ws.next(ring, b_full);
                 return true;
             };
-            auto acts = [&](const uint8_t *src, int i) {
-                bulk_copy(ring + (i % S) * kMoeStage + REC, src, kMoeRec, b_full + 8 * (i % S));
+            auto acts = [&](const uint8_t *src) {
+                bulk_copy(as.dst + REC, src, kMoeRec, as.bar);
+                as.next(ring, b_full);
+                ++issued;
             };
             for (int u = cta; ok && u < units; u += grid) {
                 const int a = u / T1, tile = u - a * T1;
-                const uint8_t *w = p.gate_up + ((size_t)ids[a] * T1 + tile) * KS1 * REC;
-                for (int ks = 0; ks < KS1; ++ks) {
-                    ok = weights(w + (size_t)ks * REC, it);
+                const uint8_t *w = p.gate_up + ((size_t)ids[a] * T1 + tile) * KS1 * REC, *x = p.xq;
+                for (int ks = 0; ks < KS1; ++ks, w += REC, x += kMoeRec) {
+                    ok = weights(w);
                     if (!ok) break;
-                    acts(p.xq + (size_t)ks * kMoeRec, it);
-                    ++it;
+                    acts(x);
                 }
             }
-            int ahead = 0;  // stages of the second half with their weights on the way
-            auto down = [&](int m, int q) {
-                const int a = q / KS2;
-                return p.down + (((size_t)ids[a] * T2 + m) * KS2 + (q - a * KS2)) * REC;
+            // the second half: a segment's weights run through the experts' matrices, a tile of KS2
+            // records each
+            int ahead = 0;  // stages with their weights on the way
+            auto segment = [&](int m, int q0, int q1, auto f) {
+                int a = q0 / KS2, k = q0 - a * KS2;
+                const uint8_t *w = p.down + (((size_t)ids[a] * T2 + m) * KS2 + k) * REC;
+                for (int q = q0; q < q1; ++q) {
+                    if (!f(w, q)) return false;
+                    w += REC;
+                    if (++k == KS2 && q + 1 < q1) {
+                        k = 0;
+                        w = p.down + ((size_t)ids[++a] * T2 + m) * KS2 * REC;
+                    }
+                }
+                return true;
             };
             if (ok && g0 < g1) {
                 walk([&](int m, int q0, int q1) {
-                    for (int q = q0; q < q1 && ahead < S; ++q, ++ahead) {
-                        ok = weights(down(m, q), it + ahead);
-                        if (!ok) return false;
-                    }
-                    return ahead < S;
+                    return segment(m, q0, q1, [&](const uint8_t *w, int) {
+                        if (ahead == S) return false;
+                        ok = weights(w);
+                        ahead += ok;
+                        return ok;
+                    });
                 });
                 const unsigned target = (unsigned)grid + (unsigned)p.barrier_extra;
                 for (long long n = 0; ok && ld_acquire_u32(p.barrier) < target; ++n) ok = n < p.barrier_polls;
                 asm volatile("fence.proxy.async;" ::: "memory");  // what others wrote, for this thread's copies
             }
+            int skip = ahead;
             if (ok)
                 walk([&](int m, int q0, int q1) {
-                    for (int q = q0; q < q1; ++q) {
-                        if (ahead > 0) {
-                            --ahead;
+                    return segment(m, q0, q1, [&](const uint8_t *w, int q) {
+                        if (skip > 0) {
+                            --skip;
                         } else {
-                            ok = weights(down(m, q), it);
+                            ok = weights(w);
                             if (!ok) return false;
+                            ++ahead;
                         }
-                        acts(p.h + (size_t)q * kMoeRec, it);
-                        ++it;
-                    }
-                    return true;
+                        acts(p.h + (size_t)q * kMoeRec);
+                        --ahead;
+                        return true;
+                    });
                 });
             if (!ok) atomicExch(p.err, 4);
             // (after a failure: the stages that have their weights get some activations too, so
             // that their barriers complete)
-            for (; ahead > 0; --ahead, ++it) acts(p.h, it);
+            for (; ahead > 0; --ahead) acts(p.h);
             // what is in flight lands before the CTA ends
-            for (int i = max(0, it - S); i < it; ++i) mbar_wait(b_full + 8 * (i % S), (uint32_t)(i / S) & 1u, kWaitCycles);
+            for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(b_full + 8 * (i % S), (uint32_t)(i / S) & 1u, kWaitCycles);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
-        int it = 0, seg = 0;
+        int slot = 0, seg = 0;
+        uint32_t par = 0, sf_set = 0;
         bool ok = true;
         auto run = [&](int n) {  // n stages into the next accumulator
             const int buf = seg & 1;
             ok = ok && (seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim)));
             tc::fence_after_sync();
             const uint32_t d = tmem + 16 * buf;
-            for (int i = 0; ok && i < n; ++i, ++it) {
-                const int s = it % S;
-                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * s, (uint32_t)(it / S) & 1u, lim));
+            for (int i = 0; ok && i < n; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    const uint32_t a = ring + s * kMoeStage, b = a + REC;
-                    const uint32_t ta = tmem + 32 + (it & 1) * 16, tb = ta + 8;
+                    const uint32_t a = ring + slot * kMoeStage, b = a + REC;
+                    const uint32_t ta = tmem + 32 + sf_set, tb = ta + 8;
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         mx_copy_scales(ta + 4 * w, a + kMxCodes + 512 * w);
@@ -468,10 +495,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
                     for (int j = 0; j < 4; ++j)
                         mx_mma<0>(d, tc::desc_sw128(a + 32 * j, 0), tc::desc_sw128(b + 32 * j, 0),
                                   mx_idesc<0>(16, 2 * (j % 2)), ta + 4 * (j / 2), tb + 4 * (j / 2), i | j);
-                    tc::commit(b_empty + 8 * s);
+                    tc::commit(b_empty + 8 * slot);
                     if (i + 1 == n) tc::commit(b_acc + 8 * buf);
                 }
                 __syncwarp();
+                sf_set ^= 16;
+                if (++slot == S) {
+                    slot = 0;
+                    par ^= 1;
+                }
             }
             ++seg;
             return ok;
@@ -507,7 +539,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
             for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(b_read + 8 * buf);
+            if (ok && lane == 0) bar_arrive(b_read + 8 * buf);  // (after a failure a phase could get too many)
             ++seg;
         };
         // a tile's rows: 32 of gate, 32 of up, twice: a warp has the gates or the ups of a

@@ -75,62 +75,73 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
+        // (one thread's chain of instructions: what a tile's stages share is computed once,
+        // and slots are counted, not divided; with that left to every stage the copies, not the
+        // tensor core or the memory, set the pace)
         if (lane == 0) {
-            int it = 0, issued = 0;  // stages with their copies of x, with those of w
             uint32_t extra = (uint32_t)p.extra_tx;
-            auto bytes_of = [&](int ct) {
-                int c0, N, n0;
-                cols(ct, c0, N, n0);
-                return (uint32_t)(REC + N * 128 + (N > n0 ? 2 : 1) * 512 * W);
-            };
-            auto copy_w = [&](int slot, int mt, int ct, int ks) {
-                const uint32_t bar = b_full + 8 * slot;
-                mbar_expect_tx(bar, bytes_of(ct) + extra);
-                extra = 0;
-                bulk_copy(ring + slot * p.stage_bytes, p.w + ((size_t)mt * p.KS + ks) * REC, REC, bar);
-            };
-            if (p.early) {
+            const int t0 = blockIdx.x / C;
+            auto source = [&](int t) { return p.w + ((size_t)(t % p.MT) * p.KS + k0) * REC; };
+            auto bytes_of = [&](int N, int n0) { return (uint32_t)(REC + N * 128 + (N > n0 ? 2 : 1) * 512 * W); };
+            int ahead = 0;  // stages with their copies of w, but not of x
+            if (p.early && t0 < tiles) {
                 // the first stages' weights before what is in front of this kernel is done
-                walk([&](int t) {
-                    const int ct = t / p.MT, mt = t - ct * p.MT;
-                    for (int ks = k0; ks < k1 && issued < S; ++ks) copy_w(issued++, mt, ct, ks);
-                    return issued < S;
-                });
+                int c0, N, n0;
+                cols(t0 / p.MT, c0, N, n0);
+                const uint8_t *w = source(t0);
+                for (; ahead < min(S, k1 - k0); ++ahead) {
+                    mbar_expect_tx(b_full + 8 * ahead, bytes_of(N, n0) + extra);
+                    extra = 0;
+                    bulk_copy(ring + ahead * p.stage_bytes, w + (size_t)ahead * REC, REC, b_full + 8 * ahead);
+                }
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            int slot = 0, issued = 0;
+            uint32_t par = 1, dst = ring, bar = b_full;  // (a wait for the phase before the first passes)
             walk([&](int t) {
-                const int ct = t / p.MT, mt = t - ct * p.MT;
                 int c0, N, n0;
-                cols(ct, c0, N, n0);
-                const uint8_t *x0 = p.x + (size_t)(c0 / kMxRows) * p.KS * REC, *x1 = x0 + (size_t)p.KS * REC;
-                for (int ks = k0; ks < k1; ++ks, ++it) {
-                    const int slot = it % S;
-                    if (it >= issued) {
-                        if (it >= S && !mbar_wait(b_empty + 8 * slot, (uint32_t)(it / S - 1) & 1u, lim)) {
+                cols(t / p.MT, c0, N, n0);
+                const size_t step = (size_t)p.KS * REC;  // a row tile of x
+                const uint8_t *w = source(t), *a = p.x + (size_t)(c0 / kMxRows) * step + (size_t)k0 * REC;
+                const uint8_t *b = a + (c0 & (kMxRows - 1)) * 128, *sf = a + kMxCodes, *b2 = a + step, *sf2 = sf + step;
+                const uint32_t bytes = bytes_of(N, n0), len = n0 * 128, len2 = (N - n0) * 128, osf = REC + p.NB * 128;
+                for (int ks = k0; ks < k1; ++ks) {
+                    if (ahead > 0) {
+                        --ahead;
+                    } else {
+                        if (!mbar_wait(bar + 8 * kMxgMaxStages, par, lim)) {  // b_empty of this slot
                             atomicExch(p.err, 4);
                             return false;
                         }
-                        copy_w(slot, mt, ct, ks);
+                        mbar_expect_tx(bar, bytes + extra);
+                        extra = 0;
+                        bulk_copy(dst, w, REC, bar);
                     }
-                    const uint32_t dst = ring + slot * p.stage_bytes + REC, bar = b_full + 8 * slot;
-                    const uint32_t sf = dst + p.NB * 128;
-                    const uint8_t *a = x0 + (size_t)ks * REC;
-                    bulk_copy(dst, a + (c0 & (kMxRows - 1)) * 128, n0 * 128, bar);
-                    bulk_copy(sf, a + kMxCodes, 512 * W, bar);
-                    if (N > n0) {
-                        const uint8_t *b = x1 + (size_t)ks * REC;
-                        bulk_copy(dst + n0 * 128, b, (N - n0) * 128, bar);
-                        bulk_copy(sf + 512 * W, b + kMxCodes, 512 * W, bar);
+                    bulk_copy(dst + REC, b, len, bar);
+                    bulk_copy(dst + osf, sf, 512 * W, bar);
+                    if (len2) {
+                        bulk_copy(dst + REC + len, b2, len2, bar);
+                        bulk_copy(dst + osf + 512 * W, sf2, 512 * W, bar);
+                    }
+                    w += REC, b += REC, sf += REC, b2 += REC, sf2 += REC;
+                    ++issued;
+                    dst += p.stage_bytes, bar += 8;
+                    if (++slot == S) {
+                        slot = 0;
+                        par ^= 1;
+                        dst = ring;
+                        bar = b_full;
                     }
                 }
                 return true;
             });
             // what is in flight lands before the CTA ends
-            for (int i = max(0, it - S); i < it; ++i) mbar_wait(b_full + 8 * (i % S), (uint32_t)(i / S) & 1u, kWaitCycles);
+            for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(b_full + 8 * (i % S), (uint32_t)(i / S) & 1u, kWaitCycles);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMAs
-        int it = 0, seg = 0;
+        int slot = 0, seg = 0;
+        uint32_t par = 0, sf_set = 0;
         bool ok = true;
         walk([&](int t) {
             int c0, N, n0;
@@ -139,15 +150,15 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
             ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
             tc::fence_after_sync();
             const uint32_t d = tmem + buf * p.acc, skip = (uint32_t)(c0 & (kMxRows - 1)) / 32;
+            const uint32_t idesc0 = mx_idesc<FMT>(N, 0), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0);
             const bool two = N > n0;
-            for (int ks = k0; ok && ks < k1; ++ks, ++it) {
-                const int slot = it % S;
-                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, (uint32_t)(it / S) & 1u, lim));
+            for (int ks = k0; ok && ks < k1; ++ks) {
+                ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
                     const uint32_t a = ring + slot * p.stage_bytes, b = a + REC, sb = b + p.NB * 128;
-                    const uint32_t ta = tmem + sf_tm + (it & 1) * 64, tb = ta + 16;
+                    const uint32_t ta = tmem + sf_tm + sf_set, tb = ta + 16;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         mx_copy_scales(ta + 4 * w, a + kMxCodes + 512 * w);
@@ -156,14 +167,19 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int w = FMT == 0 ? j / 2 : j, id = FMT == 0 ? 2 * (j % 2) : 0;
-                        mx_mma<FMT>(d, tc::desc_sw128(a + 32 * j, 0), tc::desc_sw128(b + 32 * j, 0), mx_idesc<FMT>(N, id),
+                        const int w = FMT == 0 ? j / 2 : j;
+                        mx_mma<FMT>(d, tc::desc_sw128(a + 32 * j, 0), tc::desc_sw128(b + 32 * j, 0), j % 2 ? idesc2 : idesc0,
                                     ta + 4 * w, tb + 8 * w + skip, (ks - k0) | j);
                     }
                     tc::commit(b_empty + 8 * slot);
                     if (ks + 1 == k1) tc::commit(b_acc + 8 * buf);
                 }
                 __syncwarp();
+                sf_set ^= 64;
+                if (++slot == S) {
+                    slot = 0;
+                    par ^= 1;
+                }
             }
             ++seg;
             return ok;
@@ -220,7 +236,7 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
                     }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(b_read + 8 * buf);
+            if (ok && lane == 0) bar_arrive(b_read + 8 * buf);  // (after a failure a phase could get too many)
             ++seg;
             return true;
         });
@@ -289,9 +305,11 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
         if (best > 0.0 && NB >= p.nb) break;  // the first: all rows of x in one tile, or 192
         const int MT = mx_rtiles(p.n), CT = (p.nb + NB - 1) / NB;
         const long long tiles = (long long)MT * CT;
-        for (int C = 1; C <= 8 && C <= p.KS && (C == 1 || tiles * C <= sms); ++C) {
-            const double cost = (double)((tiles * C + sms - 1) / sms) * ((p.KS + C - 1) / C) * (128 + NB) * 1.4 +
-                                (C > 1 ? 1000.0 + 10.0 * NB : 0.0);
+        // (two CTAs of an SM share its time, whole waves of them or not)
+        const int most = NB <= 16 ? 2 * sms : sms;
+        for (int C = 1; C <= 8 && C <= p.KS && (C == 1 || tiles * C <= most); ++C) {
+            const double waves = C > 1 && tiles * C > sms ? (double)(tiles * C) / sms : (double)((tiles * C + sms - 1) / sms);
+            const double cost = waves * ((p.KS + C - 1) / C) * (128 + NB) * 1.4 + (C > 1 ? 1000.0 + 10.0 * NB : 0.0);
             if (best > 0.0 && cost >= best) continue;
             best = cost;
             p.MT = MT;
@@ -299,6 +317,17 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
             p.NB = NB;
             p.C = C;
         }
+    }
+    // a pair of CTAs a tile of 256 x 192 (mx_pair.cu): a stage takes about 0.33 us
+    const int pairs = sms / 2, M2 = (mx_rtiles(p.n) + 1) / 2, CT = (p.nb + dev::kMxgMaxN - 1) / dev::kMxgMaxN;
+    const double pair_cost = (double)(((long long)M2 * CT + pairs - 1) / pairs) * p.KS * 330.0;
+    p.pair = p.nb > dev::kMxgMaxN && pairs > 0 && pair_cost < best;
+    if (p.pair) {
+        p.MT = mx_rtiles(p.n);
+        p.CT = CT;
+        p.NB = dev::kMxgMaxN;
+        p.C = 1;
+        return 2 * (int)std::min<long long>((long long)M2 * CT, pairs);
     }
     const int blocks = p.NB > 128 || (p.CT > 1 && p.NB % 128 != 0) ? 2 : 1;
     p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + blocks * 512 * W + 1023) / 1024 * 1024;
@@ -328,6 +357,7 @@ static int launch_mx_gemm_t(const MxGemmParams &p, int ctas, cudaStream_t stream
 }
 
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream_) {
+    if (p.pair) return launch_mx_pair(p, fmt, dtype, ctas, stream_);
     cudaStream_t s = (cudaStream_t)stream_;
     switch (2 * dtype + fmt) {
         case 0: return launch_mx_gemm_t<0, float>(p, ctas, s);

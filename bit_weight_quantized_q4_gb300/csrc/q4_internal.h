@@ -538,12 +538,14 @@ struct MxGemmParams {
     int n, nb, MT, CT, NB, KS;  // row tiles of w, column tiles of NB rows of x, column tiles of k
     int C;                 // CTAs (a cluster) that share a tile's k; 1: a CTA takes every grid-th tile
     int acc, stages, stage_bytes;  // tensor-memory columns of an accumulator; the ring
+    int pair;              // a pair of CTAs a tile of 256 rows of w and 192 of x (mx_pair.cu)
     int early;             // w is complete before the kernel in front of this one began
     float alpha;
 };
 // Sets the tiles, the cluster and the ring of p (n, nb, KS given) and returns the CTAs.
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
+int launch_mx_pair(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
 
 // A mixture-of-experts layer for up to kMaxNb tokens (moe.cu).  Inside it the few
 // rows of activations lie in records of 16 rows x 256 columns: 2048 bytes of codes
