@@ -1137,7 +1137,7 @@ q4_status check_mx_shape(const q4_mx *m) {
     if (!m) return Q4_ERR_NULL;
     if (!mx_fmt_ok(m->fmt)) return Q4_ERR_UNSUPPORTED;
     if (!mx_shape_ok(m->rows, m->k) || m->batch < 1 || m->batch > kMxMaxBatch) return Q4_ERR_SHAPE;
-    if ((long long)m->batch * m->rows > (1ll << 31) - 1) return Q4_ERR_SHAPE;
+    if ((long long)m->batch * m->rows > (1ll << 30)) return Q4_ERR_SHAPE;
     if (m->fmt == Q4_MX_MXFP4 ? m->scale != 1.f : !(m->scale >= 0x1p-60f && m->scale <= 0x1p60f)) return Q4_ERR_SHAPE;
     return Q4_OK;
 }
@@ -1150,7 +1150,7 @@ q4_status check_mx(const q4_mx *m) {
 q4_status check_mx_src(const q4_mx_src *s) {
     if (!s) return Q4_ERR_NULL;
     if (!dtype_ok(s->dtype) || (s->gamma && s->up)) return Q4_ERR_UNSUPPORTED;
-    if (!mx_shape_ok(s->rows, s->k) || s->ld < s->k || s->ld > (1ll << 40)) return Q4_ERR_SHAPE;
+    if (s->rows < 1 || s->rows > (1 << 30) || !mx_shape_ok(1, s->k) || s->ld < s->k || s->ld > (1ll << 40)) return Q4_ERR_SHAPE;
     Q4_TRY(check_act(s->x));
     if (!aligned16(s->up) || !aligned16(s->gamma)) return Q4_ERR_ALIGN;
     return (size_t)s->ld * dtype_size(s->dtype) % 16 == 0 ? Q4_OK : Q4_ERR_ALIGN;

@@ -318,10 +318,10 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
             p.C = C;
         }
     }
-    // a pair of CTAs a tile of 256 x 192 (mx_pair.cu): a stage takes about 0.33 us
+    // a pair of CTAs a tile of 256 x 192 (mx_pair.cu): a stage takes about (128 + N / 2) 1.05 ns
     const int pairs = sms / 2, M2 = (mx_rtiles(p.n) + 1) / 2, CT = (p.nb + dev::kMxgMaxN - 1) / dev::kMxgMaxN;
-    const double pair_cost = (double)(((long long)M2 * CT + pairs - 1) / pairs) * p.KS * 330.0;
-    p.pair = p.nb > dev::kMxgMaxN && pairs > 0 && pair_cost < best;
+    const double pair_cost = (double)(((long long)M2 * CT + pairs - 1) / pairs) * p.KS * (128 + std::min(p.nb, 192) / 2) * 1.05;
+    p.pair = p.nb > 64 && pairs > 0 && pair_cost < best;
     if (p.pair) {
         p.MT = mx_rtiles(p.n);
         p.CT = CT;

@@ -557,7 +557,7 @@ q4_status q4_logprobs(const float *logits, int32_t rows, int32_t n, const int32_
  * A q4_mx views `batch` matrices [rows][k] one after another, in a layout of this
  * library: records of 128 rows x 256 columns that the tensor core takes as they
  * are, q4_mx_bytes(fmt, rows, k) for each matrix (rows padded to 128, columns to
- * 256).  k % 32 == 0, k <= 65536, rows <= 2^24; scale in [2^-60, 2^60], and 1
+ * 256).  k % 32 == 0, k <= 65536, rows <= 2^24, batch * rows <= 2^30; scale in [2^-60, 2^60], and 1
  * for MXFP4.  Rows of codes may be activations as well as weights. */
 typedef enum { Q4_MX_MXFP4 = 0, Q4_MX_NVFP4 = 1 } q4_mx_format;
 typedef struct {
