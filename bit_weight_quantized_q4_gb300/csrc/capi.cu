@@ -1155,7 +1155,7 @@ q4_status check_mx_src(const q4_mx_src *s) {
     if (!aligned16(s->up) || !aligned16(s->gamma)) return Q4_ERR_ALIGN;
     return (size_t)s->ld * dtype_size(s->dtype) % 16 == 0 ? Q4_OK : Q4_ERR_ALIGN;
 }
-q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
+q4::MxQuantParams mx_quant_params(const q4_mx_src *s, const q4_mx *out) {
     q4::MxQuantParams p{};
     p.x = s->x;
     p.up = s->up;
@@ -1167,6 +1167,11 @@ q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
     p.batch = out->batch;
     p.eps = s->eps;
     p.scale = out->scale;
+    p.set_gain();
+    return p;
+}
+q4_status mx_quant(const q4_mx_src *s, const q4_mx *out, cudaStream_t stream) {
+    const q4::MxQuantParams p = mx_quant_params(s, out);
     const int sms = num_sms();
     if (sms <= 0) return Q4_ERR_CUDA;
     cudaGetLastError();
@@ -1181,7 +1186,9 @@ q4_status check_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t d
     Q4_TRY(check_act(y));
     return aligned16(r) ? Q4_OK : Q4_ERR_ALIGN;
 }
-q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, bool early,
+// src not null: X's rows are quantised first, by the product itself (few rows of y's
+// type) or by a kernel in front of it
+q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const q4_mx_src *src, const void *r, int32_t dtype, void *y,
                   cudaStream_t stream) {
     const int sms = num_sms();
     if (sms <= 0) return Q4_ERR_CUDA;
@@ -1195,10 +1202,15 @@ q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, 
     p.r = r;
     p.y = y;
     p.alpha = W->scale * X->scale;
-    p.early = early;
     Q4_TRY(kernel_err_ptr(&p.err));
     p.wait_cycles = g_wait_cycles;
     p.extra_tx = g_extra_tx;
+    if (src && src->dtype == dtype && !p.pair && q4::mx_gemm_few(X->rows, W->k, src->gamma != nullptr)) {
+        p.src = mx_quant_params(src, X);
+    } else if (src) {
+        Q4_TRY(mx_quant(src, X, stream));
+        p.early = 1;
+    }
     cudaGetLastError();
     if (q4::launch_mx_gemm(p, W->fmt, dtype, ctas, stream) != 0 || cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
     return Q4_OK;
@@ -1257,7 +1269,7 @@ extern "C" q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scale
 extern "C" q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y,
                                 cudaStream_t stream) {
     Q4_TRY(check_mx_gemm(W, X, r, dtype, y));
-    return mx_gemm(W, X, r, dtype, y, false, stream);
+    return mx_gemm(W, X, nullptr, r, dtype, y, stream);
 }
 
 extern "C" q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype,
@@ -1265,10 +1277,7 @@ extern "C" q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4
     Q4_TRY(check_mx_src(src));
     Q4_TRY(check_mx_gemm(W, X, r, dtype, y));
     if (src->k != X->k || src->rows != X->rows) return Q4_ERR_SHAPE;
-    int *err = nullptr;  // resolved before anything is launched
-    Q4_TRY(kernel_err_ptr(&err));
-    Q4_TRY(mx_quant(src, X, stream));
-    return mx_gemm(W, X, r, dtype, y, true, stream);
+    return mx_gemm(W, X, src, r, dtype, y, stream);
 }
 
 // ---------------------------------------------------------------- mixture of experts

@@ -10,21 +10,24 @@
 // MMAs.
 //   warp 0 copies, warp 1 issues MMAs, warps 2-5 write the results, while the
 //   tensor core is at the next tile (two accumulators).
+// A few rows that are not quantised yet are quantised here (QX): warps 6-9 write
+// their codes and scales into the stages, while w's records arrive.
 #include <algorithm>
 
-#include "mx_common.cuh"
+#include "mx_rows.cuh"
 
 namespace q4 {
 namespace dev {
 
-constexpr int kMxgThreads = 192;
+constexpr int kMxgThreads = 192, kMxgQuant = 128;  // and the threads that quantise
 constexpr int kMxgMaxN = 192;       // columns of a tile
 constexpr int kMxgSmallN = 64;      // up to here two CTAs of an SM
 constexpr int kMxgMaxStages = 12;
-constexpr int kMxgBars = 8 * (2 * kMxgMaxStages + 5) + 16;
+constexpr int kMxgBars = (8 * (2 * kMxgMaxStages + 5) + 16 + 15) / 16 * 16, kMxgTail = kMxgBars + 64;  // barriers, 16 rows' factors
 
-template <int FMT, typename T>
-__global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_constant__ MxGemmParams p) {
+template <int FMT, typename T, bool QX>
+__global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
+    q4mx_gemm_kernel(const __grid_constant__ MxGemmParams p) {
     constexpr int W = mx_words(FMT), REC = mx_rec(FMT);
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -39,7 +42,7 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
     uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + S * p.stage_bytes + 8 * (2 * kMxgMaxStages + 5));
     if (warp == 0) {
         if (lane < S) {
-            mbar_init(b_full + 8 * lane, 1);
+            mbar_init(b_full + 8 * lane, QX ? 2 : 1);
             mbar_init(b_empty + 8 * lane, 1);
         }
         if (lane < 2) {
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
             uint32_t extra = (uint32_t)p.extra_tx;
             const int t0 = blockIdx.x / C;
             auto source = [&](int t) { return p.w + ((size_t)(t % p.MT) * p.KS + k0) * REC; };
-            auto bytes_of = [&](int N, int n0) { return (uint32_t)(REC + N * 128 + (N > n0 ? 2 : 1) * 512 * W); };
+            auto bytes_of = [&](int N, int n0) { return (uint32_t)(QX ? REC : REC + N * 128 + (N > n0 ? 2 : 1) * 512 * W); };
             int ahead = 0;  // stages with their copies of w, but not of x
             if (p.early && t0 < tiles) {
                 // the first stages' weights before what is in front of this kernel is done
@@ -117,9 +120,11 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
                         extra = 0;
                         bulk_copy(dst, w, REC, bar);
                     }
-                    bulk_copy(dst + REC, b, len, bar);
-                    bulk_copy(dst + osf, sf, 512 * W, bar);
-                    if (len2) {
+                    if constexpr (!QX) {
+                        bulk_copy(dst + REC, b, len, bar);
+                        bulk_copy(dst + osf, sf, 512 * W, bar);
+                    }
+                    if (!QX && len2) {
                         bulk_copy(dst + REC + len, b2, len2, bar);
                         bulk_copy(dst + osf + 512 * W, sf2, 512 * W, bar);
                     }
@@ -188,6 +193,111 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
         if (tc::elect_one()) tc::commit(b_drain);
         __syncwarp();
         mbar_wait(b_drain, 0u, kWaitCycles);
+    } else if (QX && warp >= 6) {
+        // ------------------------------------------------------------ rows of x into the stages
+        // Every fourth stage a warp, two rows at a time, sixteen values a lane; D such pairs of
+        // rows are under way (all four warps on each stage, its loads a stage ahead: 0.7 us a
+        // stage, the loads' latency).
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        constexpr int NQ = kMxgQuant / 32, D = sizeof(T) == 2 ? 4 : 2;
+        const int w = warp - 6, half = lane >> 4, h = lane & 15, pairs = (p.nb + 1) / 2, len = k1 - k0;
+        const MxGain gain{p.src.scale, p.src.six_g, p.src.inv};
+        const T *x = (const T *)p.src.x, *up = (const T *)p.src.up;
+        float *rs = reinterpret_cast<float *>(sm + S * p.stage_bytes + kMxgBars);  // 1 / rms of the rows
+        if (p.src.gamma) {
+            for (int row = w; row < p.nb; row += NQ) {
+                float sum = 0.f;
+#pragma unroll 4
+                for (int c = 16 * lane; c < p.src.k; c += 512) {
+                    Raw16<T> a;
+                    a.load(x + row * p.src.ld + c);
+                    float v[16];
+                    a.values(v);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum = fmaf(v[e], v[e], sum);
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane == 0) rs[row] = 1.f / sqrtf(sum / (float)p.src.k + p.src.eps);
+            }
+            asm volatile("bar.sync 1, %0;" ::"n"(kMxgQuant) : "memory");
+        }
+        const int mine = (tiles - (int)blockIdx.x / C + (int)gridDim.x / C - 1) / ((int)gridDim.x / C);  // tiles of this CTA
+        const int total = mine * len;                                                                   // stages
+        // the stage and the pair of rows that a step loads, and those it stores
+        struct At {
+            int it, ks, pair;
+        };
+        auto next = [&](At &a) {
+            if (++a.pair == pairs) {
+                a.pair = 0;
+                a.it += NQ;
+                a.ks += NQ;
+                while (a.ks >= len) a.ks -= len;
+            }
+        };
+        At in = {w, w % len, 0};
+        Raw16<T> a[D], b[D];
+        auto fetch = [&](int d) {
+            const int c = (k0 + in.ks) * kMxK + 16 * h, row = 2 * in.pair + half;
+            a[d].zero();
+            b[d].zero();
+            if (in.it < total && row < p.nb && c < p.src.k) {
+                a[d].load(x + row * p.src.ld + c);
+                if (up) b[d].load(up + row * p.src.ld + c);
+            }
+            next(in);
+        };
+#pragma unroll
+        for (int d = 0; d < D; ++d) fetch(d);
+        At out = {w, w % len, 0};
+        int slot = w;  // (a ring has more than four)
+        uint32_t par = 1;
+        bool ok = true;
+        while (ok && out.it < total) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                if (!ok || out.it >= total) break;
+                if (out.pair == 0) ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, par, lim));
+                if (!ok) break;
+                const int c = (k0 + out.ks) * kMxK + 16 * h, row = 2 * out.pair + half;
+                float v[16], f = 1.f;
+                a[d].values(v);
+                if (up) {
+                    float u[16];
+                    b[d].values(u);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = mx_silu(v[e]) * u[e];
+                } else if (p.src.gamma && c < p.src.k) {
+                    if (row < p.nb) f = rs[row];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                        const float4 g = *reinterpret_cast<const float4 *>(p.src.gamma + c + e);
+                        v[e] *= g.x, v[e + 1] *= g.y, v[e + 2] *= g.z, v[e + 3] *= g.w;
+                    }
+                }
+                fetch(d);
+                uint2 code;
+                uint32_t word;
+                mx_codes<FMT>(v, f, gain, code, word);
+                uint8_t *rec = sm + slot * p.stage_bytes + REC;  // 16 rows of codes, then the scales
+                *reinterpret_cast<uint2 *>(rec + mx_code_off(row, 8 * h)) = code;
+                constexpr int L = 4 * mx_block(FMT) / 16;  // lanes of a word
+                if (h % L == 0) *reinterpret_cast<uint32_t *>(rec + p.NB * 128 + h / L * 512 + row * 16) = word;
+                next(out);
+                if (out.pair == 0) {  // the stage is complete
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the codes, for the tensor core
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(b_full + 8 * slot);
+                    slot += NQ;
+                    if (slot >= S) {
+                        slot -= S;
+                        par ^= 1;
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicExch(p.err, 4);
     } else {
         // ------------------------------------------------------------ results
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -251,7 +361,7 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
         const int t = blockIdx.x / C, ct = t / p.MT;
         cols(ct, c0, N, n0);
         const int per = (N + C - 1) / C, q = warp & 3, rl = 32 * q + lane, row = (t - ct * p.MT) * kMxRows + rl;
-        if (warp >= 2) {
+        if (warp >= 2 && warp < 6) {
             const uint32_t d = tmem + ((uint32_t)(32 * q) << 16);
             for (int c = 0; c < N; c += 16) {
                 uint32_t w[16];
@@ -270,7 +380,7 @@ __global__ void __launch_bounds__(kMxgThreads, 2) q4mx_gemm_kernel(const __grid_
         }
         __syncwarp();
         cluster_sync();
-        if (warp >= 2 && row < p.n) {
+        if (warp >= 2 && warp < 6 && row < p.n) {
             const float *part = reinterpret_cast<const float *>(sm) + rl;
             const T *rs = (const T *)p.r;
             for (int i = 0; i < per; ++i) {
@@ -333,20 +443,27 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
     p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + blocks * 512 * W + 1023) / 1024 * 1024;
     const long long tiles = (long long)p.MT * p.CT;
     const bool two = p.NB <= dev::kMxgSmallN && tiles * p.C > sms;  // two CTAs of an SM
-    const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgBars;
+    const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgTail;
     p.stages = std::min(dev::kMxgMaxStages, room / p.stage_bytes);
     p.acc = p.NB <= dev::kMxgSmallN ? dev::kMxgSmallN : dev::kMxgMaxN;
     return (int)(p.C > 1 ? tiles * p.C : std::min<long long>(tiles, two ? 2 * sms : sms));
 }
 
-template <int FMT, typename T>
+bool mx_gemm_few(int nb, int k, bool norm) {
+    // Every CTA quantises the rows of its stages: up to eight in less time than their weights
+    // take (14336 x 4096, one row: 8.8 us, 10.8 with a kernel in front; eight: 11.7 and 11.3;
+    // sixteen: 18.3 and 11.5).  Behind a norm it reads all of them before its first stage.
+    return nb <= 8 && (!norm || (long long)nb * k <= 16384);
+}
+
+template <int FMT, typename T, bool QX>
 static int launch_mx_gemm_t(const MxGemmParams &p, int ctas, cudaStream_t stream) {
-    auto kern = dev::q4mx_gemm_kernel<FMT, T>;
+    auto kern = dev::q4mx_gemm_kernel<FMT, T, QX>;
     static size_t smem_set[64] = {0};
-    const size_t smem = (size_t)p.stages * p.stage_bytes + dev::kMxgBars;
+    const size_t smem = (size_t)p.stages * p.stage_bytes + dev::kMxgTail;
     if (!raise_smem(kern, smem, smem_set)) return -1;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kMxgThreads, smem, stream, attr);
+    cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kMxgThreads + (QX ? dev::kMxgQuant : 0), smem, stream, attr);
     if (p.C > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = (unsigned)p.C;
@@ -355,17 +472,21 @@ static int launch_mx_gemm_t(const MxGemmParams &p, int ctas, cudaStream_t stream
     }
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
+template <int FMT, typename T>
+static int launch_mx_gemm_x(const MxGemmParams &p, int ctas, cudaStream_t stream) {
+    return p.src.x ? launch_mx_gemm_t<FMT, T, true>(p, ctas, stream) : launch_mx_gemm_t<FMT, T, false>(p, ctas, stream);
+}
 
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream_) {
     if (p.pair) return launch_mx_pair(p, fmt, dtype, ctas, stream_);
     cudaStream_t s = (cudaStream_t)stream_;
     switch (2 * dtype + fmt) {
-        case 0: return launch_mx_gemm_t<0, float>(p, ctas, s);
-        case 1: return launch_mx_gemm_t<1, float>(p, ctas, s);
-        case 2: return launch_mx_gemm_t<0, __half>(p, ctas, s);
-        case 3: return launch_mx_gemm_t<1, __half>(p, ctas, s);
-        case 4: return launch_mx_gemm_t<0, __nv_bfloat16>(p, ctas, s);
-        case 5: return launch_mx_gemm_t<1, __nv_bfloat16>(p, ctas, s);
+        case 0: return launch_mx_gemm_x<0, float>(p, ctas, s);
+        case 1: return launch_mx_gemm_x<1, float>(p, ctas, s);
+        case 2: return launch_mx_gemm_x<0, __half>(p, ctas, s);
+        case 3: return launch_mx_gemm_x<1, __half>(p, ctas, s);
+        case 4: return launch_mx_gemm_x<0, __nv_bfloat16>(p, ctas, s);
+        case 5: return launch_mx_gemm_x<1, __nv_bfloat16>(p, ctas, s);
     }
     return -1;
 }

@@ -8,76 +8,27 @@
 // arithmetic of scales and addresses.)
 #include <algorithm>
 
-#include "mx_common.cuh"
+#include "mx_rows.cuh"
 
 namespace q4 {
 namespace dev {
 
 constexpr int kMxThreads = 256, kMxWarps = kMxThreads / 32;
 
-// Sixteen consecutive values as they are stored.
-template <typename T>
-struct Raw16 {
-    static constexpr int N = (int)sizeof(T);
-    uint4 w[N];
-    __device__ __forceinline__ void load(const T *src) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void values(float (&v)[16]) const {
-        if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w_of(w[i / 4], i % 4));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t x = w_of(w[i / 4], i % 4);
-                if constexpr (std::is_same<T, __half>::value) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
-                    v[2 * i] = f.x;
-                    v[2 * i + 1] = f.y;
-                } else {
-                    v[2 * i] = __uint_as_float(x << 16);
-                    v[2 * i + 1] = __uint_as_float(x & 0xFFFF0000u);
-                }
-            }
-        }
-    }
-};
-
 // The sixteen values v f from column c of row `row` into the matrix at `out`; all
 // lanes of a warp, those of a row of a record (16 of them) in order.
 template <int FMT>
 __device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const float (&v)[16], float f,
                                          const MxGain &gain) {
-    float a = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a = max_abs(a, v[i]);
-    if constexpr (FMT == 0) a = max_abs(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    float mul;
-    const uint32_t sc = mx_block_scale<FMT>(a * f, gain, mul);
-    const float by = f * mul;
-    float lo[8], hi[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo[i] = v[i] * by;
-        hi[i] = v[8 + i] * by;
-    }
-    const uint2 code = mul == 0.f ? make_uint2(0u, 0u) : make_uint2(e2m1x8(lo), e2m1x8(hi));
-    // four blocks' scales a word
-    constexpr int L = mx_block(FMT) / 16;  // lanes of a block
-    uint32_t word = sc;
-    word |= __shfl_down_sync(0xffffffffu, word, L) << 8;
-    word |= __shfl_down_sync(0xffffffffu, word, 2 * L) << 16;
+    uint2 code;
+    uint32_t word;
+    mx_codes<FMT>(v, f, gain, code, word);
     if (!live) return;
+    constexpr int L = 4 * mx_block(FMT) / 16;  // lanes of a word
     const int r = row % kMxRows, h = (c % kMxK) / 16;  // h: which sixteen of the record's row
     uint8_t *rec = out + ((size_t)(row / kMxRows) * KT + c / kMxK) * mx_rec(FMT);
     *reinterpret_cast<uint2 *>(rec + mx_code_off(r, 8 * h)) = code;
-    if (h % (4 * L) == 0) *reinterpret_cast<uint32_t *>(rec + mx_scale_off(r, h / (4 * L))) = word;
+    if (h % L == 0) *reinterpret_cast<uint32_t *>(rec + mx_scale_off(r, h / L)) = word;
 }
 
 // A warp's units: two rows (of the whole batch) and a column tile, a half warp each.
@@ -352,8 +303,7 @@ int launch_mx_quant_t(const MxQuantParams &p, int sms, cudaStream_t stream) {
 
 int launch_mx_quant(const MxQuantParams &params, int fmt, int dtype, int sms, void *stream_) {
     MxQuantParams p = params;
-    p.six_g = 6.f * p.scale;
-    p.inv = 1.f / p.six_g;
+    p.set_gain();
     cudaStream_t s = (cudaStream_t)stream_;
     switch (2 * dtype + fmt) {
         case 0: return launch_mx_quant_t<float, 0>(p, sms, s);

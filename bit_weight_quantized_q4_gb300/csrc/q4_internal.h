@@ -512,7 +512,11 @@ struct MxQuantParams {
     long long ld;
     int rows, k, batch;
     float eps, scale;
-    float six_g, inv;  // 6 scale and 1 / (6 scale), set by the launch
+    float six_g, inv;  // 6 scale and 1 / (6 scale)
+    void set_gain() {
+        six_g = 6.f * scale;
+        inv = 1.f / six_g;
+    }
 };
 int launch_mx_quant(const MxQuantParams &p, int fmt, int dtype, int sms, void *stream);
 // Back into values [batch][rows][k]; and the codes and scales in plain rows
@@ -541,7 +545,10 @@ struct MxGemmParams {
     int pair;              // a pair of CTAs a tile of 256 rows of w and 192 of x (mx_pair.cu)
     int early;             // w is complete before the kernel in front of this one began
     float alpha;
+    MxQuantParams src;     // src.x not null: a few rows that the product quantises itself (x unused)
 };
+// Whether the product quantises rows itself.
+bool mx_gemm_few(int nb, int k, bool norm);
 // Sets the tiles, the cluster and the ring of p (n, nb, KS given) and returns the CTAs.
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);

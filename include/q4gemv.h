@@ -608,7 +608,9 @@ q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scales, cudaStre
 q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, cudaStream_t stream);
 
 /* q4_mx_quant of src into X (W's format, src's rows; the caller's room), then
- * q4_mx_gemm, whose weight copies run while the rows are quantised. */
+ * q4_mx_gemm, whose weight copies run while the rows are quantised; the same y.  A
+ * few rows of y's type are quantised by the product itself: X's contents are then
+ * undefined. */
 q4_status q4_mx_linear(const q4_mx *W, const q4_mx_src *src, const q4_mx *X, const void *r, int32_t dtype, void *y,
                        cudaStream_t stream);
 
