@@ -205,19 +205,33 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         const T *x = (const T *)p.src.x, *up = (const T *)p.src.up;
         float *rs = reinterpret_cast<float *>(sm + S * p.stage_bytes + kMxgBars);  // 1 / rms of the rows
         if (p.src.gamma) {
+            // in the order of q4mx_quant_norm_kernel: 512s by eights, then the eight
             for (int row = w; row < p.nb; row += NQ) {
+                float part[8] = {};
+                for (int c0 = 16 * lane; c0 < p.src.k; c0 += 4096)
+#pragma unroll
+                    for (int g = 0; g < 8; g += 4) {
+                        Raw16<T> t[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            t[i].zero();
+                            if (c0 + 512 * (g + i) < p.src.k) t[i].load(x + row * p.src.ld + c0 + 512 * (g + i));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float v[16];
+                            t[i].values(v);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) part[g + i] = fmaf(v[e], v[e], part[g + i]);
+                        }
+                    }
                 float sum = 0.f;
-#pragma unroll 4
-                for (int c = 16 * lane; c < p.src.k; c += 512) {
-                    Raw16<T> a;
-                    a.load(x + row * p.src.ld + c);
-                    float v[16];
-                    a.values(v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) sum = fmaf(v[e], v[e], sum);
+                for (int g = 0; g < 8; ++g) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) part[g] += __shfl_xor_sync(0xffffffffu, part[g], o);
+                    sum += part[g];
                 }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 if (lane == 0) rs[row] = 1.f / sqrtf(sum / (float)p.src.k + p.src.eps);
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kMxgQuant) : "memory");

@@ -225,20 +225,29 @@ def test_product_of_whole_numbers_is_exact(q4, nb):
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
-@pytest.mark.parametrize("nb", [3, 200])
-def test_product_quantises_its_rows_as_the_quantiser_does(q4, fmt, nb):
-    g = gen(5)
-    W = q4.q4_mx_quant(randn(g, 333, 544) * 0.1, fmt, scale=1.0 if fmt == 0 else 1e-3)
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("nb,n,k", [(1, 333, 544), (3, 1200, 1056), (8, 20000, 544), (2, 130, 8224), (1, 640, 16384), (5, 64, 32),
+                                    (7, 40000, 288), (9, 333, 544), (200, 333, 544)])
+def test_product_quantises_its_rows_as_the_quantiser_does(q4, nb, n, k, dtype, fmt):
+    g = gen(5 + nb)
+    W = q4.q4_mx_quant(randn(g, n, k) * 0.1, fmt, scale=1.0 if fmt == 0 else 1e-3)
     sc = 1.0 if fmt == 0 else 0.01
-    x, up, gamma = randn(g, nb, 544).to(BF16), randn(g, nb, 544).to(BF16), 1 + 0.1 * randn(g, 544)
+    x, up, gamma = randn(g, nb, k).to(dtype), randn(g, nb, k).to(dtype), 1 + 0.1 * randn(g, k)
     for kw in ({}, {"gamma": gamma, "eps": 1e-6}, {"up": up}):
         X = q4.q4_mx_quant(x, fmt, scale=sc, **kw)
-        want = q4.q4_mx_gemm(W, X, dtype=BF16)
+        want = q4.q4_mx_gemm(W, X, dtype=dtype)
         assert torch.equal(q4.q4_mx_gemm(W, x, scale=sc, **kw), want)
         ws = q4.q4_mx_gemm_workspace(W, nb)
         ws.fill_(255)  # any contents
         out = torch.empty_like(want)
         assert torch.equal(q4.q4_mx_gemm(W, x, scale=sc, out=out, workspace=ws, **kw), want)
+    # rows of a wider buffer, another output type
+    wide = torch.zeros(nb, 2 * k, dtype=dtype, device="cuda")
+    wide[:, k:] = x
+    assert torch.equal(q4.q4_mx_gemm(W, wide[:, k:], scale=sc), q4.q4_mx_gemm(W, q4.q4_mx_quant(x, fmt, scale=sc), dtype=dtype))
+    other = F16 if dtype == F32 else F32
+    assert torch.equal(q4.q4_mx_gemm(W, x, scale=sc, dtype=other), q4.q4_mx_gemm(W, q4.q4_mx_quant(x, fmt, scale=sc), dtype=other))
+    q4.q4_device_check()
 
 
 @pytest.mark.parametrize("fmt", [0, 1])
@@ -353,10 +362,11 @@ def test_refusals(q4):
     q4.q4_device_check()
 
 
-@pytest.mark.parametrize("nb,n,k", [(1, 512, 4096), (40, 300, 1024), (300, 300, 4096)])
-def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_unchanged(q4, nb, n, k):
+@pytest.mark.parametrize("nb,n,k,inside", [(1, 512, 4096, False), (40, 300, 1024, False), (300, 300, 4096, False), (2, 640, 8192, True)])
+def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_unchanged(q4, nb, n, k, inside):
     g = gen(10)
-    W, X = q4.q4_mx_quant(randn(g, n, k)), q4.q4_mx_quant(randn(g, nb, k))
+    W, X = q4.q4_mx_quant(randn(g, n, k)), randn(g, nb, k)
+    X = X if inside else q4.q4_mx_quant(X)
     y0 = q4.q4_mx_gemm(W, X)
     q4.q4_device_check()
     q4.q4_debug_wait_limits(copy_wait_cycles=200000, copy_extra_bytes=16)
