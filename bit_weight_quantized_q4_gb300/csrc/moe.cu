@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
                 for (int w = 0; w < kRouteWarps; ++w) s += sums[w][lane];
             const float sq = __shfl_down_sync(0xffffffffu, s, NT);
             if (lane < p.nb)
-                p.logits[(size_t)lane * p.E + e] = p.gamma ? s * (1.f / sqrtf(sq / (float)p.hidden + p.eps)) : s;
+                p.logits[(size_t)lane * p.E + e] = p.gamma ? s * rsqrtf(fmaf(sq, 1.f / (float)p.hidden, p.eps)) : s;
         }
         return;
     }
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < kRouteWarps; ++i) sum += sums[i][0];
-        rstd = 1.f / sqrtf(sum / (float)p.hidden + p.eps);
+        rstd = rsqrtf(fmaf(sum, 1.f / (float)p.hidden, p.eps));
     }
     for (int kt = warp; kt < KT; kt += kRouteWarps) {
         const int c = kt * kMxK + 8 * lane;

@@ -37,6 +37,10 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return w;
 }
+__device__ __forceinline__ uint32_t e2m1x8(const uint64_t (&p)[4]) {
+    const float v[8] = {lo_f32(p[0]), hi_f32(p[0]), lo_f32(p[1]), hi_f32(p[1]), lo_f32(p[2]), hi_f32(p[2]), lo_f32(p[3]), hi_f32(p[3])};
+    return e2m1x8(v);
+}
 __device__ __forceinline__ uint32_t e2m1(float v) {
     uint16_t w;
     asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.u16.u8 %0, a;\n\t}"

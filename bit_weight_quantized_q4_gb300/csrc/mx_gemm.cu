@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         if (p.src.gamma) {
             // in the order of q4mx_quant_norm_kernel: 512s by eights, then the eight
             for (int row = w; row < p.nb; row += NQ) {
-                float part[8] = {};
+                uint64_t part[8] = {};
                 for (int c0 = 16 * lane; c0 < p.src.k; c0 += 4096)
 #pragma unroll
                     for (int g = 0; g < 8; g += 4) {
@@ -219,20 +219,21 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
                         }
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            float v[16];
-                            t[i].values(v);
+                            uint64_t v[8];
+                            t[i].pairs(v);
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) part[g + i] = fmaf(v[e], v[e], part[g + i]);
+                            for (int e = 0; e < 8; ++e) part[g + i] = fma_f32x2(v[e], v[e], part[g + i]);
                         }
                     }
                 float sum = 0.f;
 #pragma unroll
                 for (int g = 0; g < 8; ++g) {
+                    float s = lo_f32(part[g]) + hi_f32(part[g]);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) part[g] += __shfl_xor_sync(0xffffffffu, part[g], o);
-                    sum += part[g];
+                    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    sum += s;
                 }
-                if (lane == 0) rs[row] = 1.f / sqrtf(sum / (float)p.src.k + p.src.eps);
+                if (lane == 0) rs[row] = mx_rstd(sum, 1.f / (float)p.src.k, p.src.eps);
             }
             asm volatile("bar.sync 1, %0;" ::"n"(kMxgQuant) : "memory");
         }
@@ -275,20 +276,19 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
                 if (out.pair == 0) ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, par, lim));
                 if (!ok) break;
                 const int c = (k0 + out.ks) * kMxK + 16 * h, row = 2 * out.pair + half;
-                float v[16], f = 1.f;
-                a[d].values(v);
+                uint64_t v[8];
+                float f = 1.f;
+                a[d].pairs(v);
                 if (up) {
-                    float u[16];
-                    b[d].values(u);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = mx_silu(v[e]) * u[e];
+                    uint64_t u[8];
+                    b[d].pairs(u);
+                    mx_glu(v, u);
                 } else if (p.src.gamma && c < p.src.k) {
                     if (row < p.nb) f = rs[row];
+                    uint64_t g[8];
+                    mx_factors(g, p.src.gamma + c);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const float4 g = *reinterpret_cast<const float4 *>(p.src.gamma + c + e);
-                        v[e] *= g.x, v[e + 1] *= g.y, v[e + 2] *= g.z, v[e + 3] *= g.w;
-                    }
+                    for (int e = 0; e < 8; ++e) v[e] = mul_f32x2(v[e], g[e]);
                 }
                 fetch(d);
                 uint2 code;

@@ -18,7 +18,7 @@ constexpr int kMxThreads = 256, kMxWarps = kMxThreads / 32;
 // The sixteen values v f from column c of row `row` into the matrix at `out`; all
 // lanes of a warp, those of a row of a record (16 of them) in order.
 template <int FMT>
-__device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const float (&v)[16], float f,
+__device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const uint64_t (&v)[8], float f,
                                          const MxGain &gain) {
     uint2 code;
     uint32_t word;
@@ -74,13 +74,12 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < AH; ++i, u.next(KT)) {
         if (2ll * u.pair >= rows) break;
-        float v[16];
-        x[i].values(v);
+        uint64_t v[8];
+        x[i].pairs(v);
         if constexpr (GLU) {
-            float w[16];
-            y[i].values(w);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = mx_silu(v[e]) * w[e];
+            uint64_t w[8];
+            y[i].pairs(w);
+            mx_glu(v, w);
         }
         const int row = 2 * u.pair + half, b = p.batch == 1 ? 0 : row / p.rows;
         mx_store<FMT>(p.out + b * mat, row < rows, row - b * p.rows, u.kt * kMxK + 16 * (lane & 15), KT, v, 1.f, gain);
@@ -89,51 +88,50 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_con
 
 // Behind an RMSNorm: WPR warps a row, which keep up to R sixteens a lane of it in
 // registers (what a longer row has beyond is read again once its sum of squares is
-// known); the next row's loads are issued before this one's sum is taken.
+// known).  As many CTAs as are resident take every grid-th rows each, the loads of the
+// next DP rows under way.  Its arithmetic bounds it, not the memory: 8191 x 4096 bf16
+// takes 21 us with three CTAs of an SM and two rows under way (a CTA a row: 30; more
+// CTAs than are resident: 25; four, whose registers spill: 26).
+template <int R>
+constexpr int mx_norm_ctas() { return R == 1 ? 3 : 2; }
 template <typename T, int FMT, int WPR, int R>
-__global__ void __launch_bounds__(kMxThreads) q4mx_quant_norm_kernel(const __grid_constant__ MxQuantParams p) {
+__global__ void __launch_bounds__(kMxThreads, mx_norm_ctas<R>()) q4mx_quant_norm_kernel(const __grid_constant__ MxQuantParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ float sums[2][kMxWarps];
     constexpr int RPC = kMxWarps / WPR;  // rows of a CTA
+    constexpr int DP = sizeof(T) == 2 && R == 1 ? 2 : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, KT = mx_ktiles(p.k);
     const int at = 16 * (32 * (warp % WPR) + lane), step = 512 * WPR, kpad = KT * kMxK;
-    const int rows = p.batch * p.rows;
+    const int rows = p.batch * p.rows, ahead = gridDim.x * RPC;
     const long long mat = (long long)mx_rtiles(p.rows) * KT * mx_rec(FMT);
     const MxGain gain{p.scale, p.six_g, p.inv};
+    const float inv_k = 1.f / (float)p.k;
     // the lane's columns are the same in every row
-    float gm[R][16];
+    uint64_t gm[R][8];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const float4 g = at + i * step < p.k ? *reinterpret_cast<const float4 *>(p.gamma + at + i * step + e)
-                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-            gm[i][e] = g.x, gm[i][e + 1] = g.y, gm[i][e + 2] = g.z, gm[i][e + 3] = g.w;
-        }
-    Raw16<T> next[R];
-    auto fetch = [&](int row) {
+        for (int e = 0; e < 8; ++e) gm[i][e] = 0;
+        if (at + i * step < p.k) mx_factors(gm[i], p.gamma + at + i * step);
+    }
+    Raw16<T> next[DP][R];
+    auto fetch = [&](int d, int row) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            next[i].zero();
-            if (row < rows && at + i * step < p.k) next[i].load((const T *)p.x + row * p.ld + at + i * step);
+            next[d][i].zero();
+            if (row < rows && at + i * step < p.k) next[d][i].load((const T *)p.x + row * p.ld + at + i * step);
         }
     };
-    int row = blockIdx.x * RPC + warp / WPR, turn = 0;
-    fetch(row);
-    for (; row - warp / WPR < rows; row += gridDim.x * RPC, turn ^= 1) {
+    auto one = [&](const Raw16<T> (&x)[R], int row, int turn) {
         const bool live = row < rows;
         const T *src = (const T *)p.x + (live ? row : 0) * p.ld;
-        Raw16<T> x[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) x[i] = next[i];
-        fetch(row + gridDim.x * RPC);
-        float sum = 0.f;
+        uint64_t s2 = 0;
         auto squares = [&](const Raw16<T> &a) {
-            float v[16];
-            a.values(v);
+            uint64_t v[8];
+            a.pairs(v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) sum = fmaf(v[e], v[e], sum);
+            for (int e = 0; e < 8; ++e) s2 = fma_f32x2(v[e], v[e], s2);
         };
 #pragma unroll
         for (int i = 0; i < R; ++i) squares(x[i]);
@@ -142,6 +140,7 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_norm_kernel(const __gri
             a.load(src + c);
             squares(a);
         }
+        float sum = lo_f32(s2) + hi_f32(s2);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if constexpr (WPR > 1) {
@@ -151,13 +150,13 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_norm_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < WPR; ++i) sum += sums[turn][warp / WPR * WPR + i];
         }
-        const float rstd = 1.f / sqrtf(sum / (float)p.k + p.eps);
+        const float rstd = mx_rstd(sum, inv_k, p.eps);
         const int b = p.batch == 1 ? 0 : row / p.rows;
-        auto put = [&](const Raw16<T> &a, const float (&gv)[16], int c) {
-            float v[16];
-            a.values(v);
+        auto put = [&](const Raw16<T> &a, const uint64_t (&gv)[8], int c) {
+            uint64_t v[8];
+            a.pairs(v);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= gv[e];
+            for (int e = 0; e < 8; ++e) v[e] = mul_f32x2(v[e], gv[e]);
             // (columns behind k are zeros even where rstd is infinite or NaN)
             mx_store<FMT>(p.out + b * mat, live && c < kpad, row - b * p.rows, c, KT, v, c < p.k ? rstd : 1.f, gain);
         };
@@ -166,14 +165,29 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_norm_kernel(const __gri
             if (at - 16 * lane + i * step < kpad) put(x[i], gm[i], at + i * step);
         for (int c = at + R * step; c - 16 * lane < kpad; c += step) {
             Raw16<T> a;
-            float gv[16] = {};
+            uint64_t gv[8] = {};
             a.zero();
             if (c < p.k) {
                 a.load(src + c);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) gv[e] = p.gamma[c + e];
+                mx_factors(gv, p.gamma + c);
             }
             put(a, gv, c);
+        }
+    };
+    int row = blockIdx.x * RPC + warp / WPR, turn = 0;
+#pragma unroll
+    for (int d = 0; d < DP; ++d) fetch(d, row + d * ahead);
+    while (row - warp / WPR < rows) {
+#pragma unroll
+        for (int d = 0; d < DP; ++d) {
+            if (row - warp / WPR >= rows) break;
+            Raw16<T> x[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) x[i] = next[d][i];
+            fetch(d, row + DP * ahead);
+            one(x, row, turn);
+            row += ahead;
+            turn ^= 1;
         }
     }
 }
@@ -283,7 +297,7 @@ int mx_launch(Kern kern, unsigned grid, const P &p, cudaStream_t stream) {
 template <typename T, int FMT, int WPR, int R>
 int launch_mx_norm(const MxQuantParams &p, int sms, cudaStream_t stream) {
     const long long ctas = ((long long)p.batch * p.rows * WPR + dev::kMxWarps - 1) / dev::kMxWarps;
-    return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, WPR, R>, (unsigned)std::min<long long>(ctas, 6ll * sms), p, stream);
+    return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, WPR, R>, (unsigned)std::min<long long>(ctas, (long long)dev::mx_norm_ctas<R>() * sms), p, stream);
 }
 template <typename T, int FMT>
 int launch_mx_quant_t(const MxQuantParams &p, int sms, cudaStream_t stream) {
