@@ -10,7 +10,6 @@
 // gathered.
 #include <algorithm>
 
-#include "attn_common.cuh"
 #include "mx_common.cuh"
 
 namespace q4 {
@@ -18,7 +17,7 @@ namespace dev {
 
 // ------------------------------------------------------------------ logits and codes
 
-constexpr int kRouteThreads = 256, kRouteWarps = kRouteThreads / 32;
+constexpr int kRouteSlices = 8;  // warps that share an expert's row
 
 // Four consecutive values as they are stored.
 template <typename T>
@@ -36,36 +35,37 @@ struct Raw4 {
     }
 };
 
-// CTAs below E: an expert's logits of all tokens, a warp every eighth 128 columns.
-// The others: a token's row each, its norm and its codes.  (A warp an expert and
-// four tokens, with the choice of the experts by the last CTA: 14 us more for one
-// token.)  Latency bounds it: the loads of up to 2048 columns of all tokens go out before
-// the first is used (a token at a time, 16 tokens took 12 us).
+// CTAs below E: an expert's logits, eight warps for each NT tokens, a warp every
+// eighth 128 columns.  The others: a token's row each, its norm and its codes.
+// Latency bounds it, of loads and of the code itself: the loads of 4096 (four tokens:
+// 2048) columns of a warp's tokens go out before the first is used, and a warp has one token's or
+// four tokens' sums (eight warps with sixteen tokens' straight code took 6 us longer; a
+// token's loads at a time, 8).
 template <typename T, int NT>
-__global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid_constant__ MoeParams p) {
+__global__ void __launch_bounds__(NT == 1 ? 256 : 1024) q4moe_route_kernel(const __grid_constant__ MoeParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float sums[kRouteWarps][32];
+    __shared__ float sums[NT == 1 ? 8 : 32][2 * NT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const T *x = (const T *)p.x;
     if ((int)blockIdx.x < p.E) {
-        const int e = blockIdx.x;
+        const int e = blockIdx.x, t0 = warp / kRouteSlices * NT;
         if (e == 0) {
-            if (tid == 0) *p.barrier = 0u;
-            for (int i = tid; i < mx_rtiles(p.hidden); i += kRouteThreads) p.count[i] = 0u;
+            if (tid == 0) *p.barrier = 0u, *p.units = 0u;
+            for (int i = tid; i < mx_rtiles(p.hidden); i += blockDim.x) p.count[i] = 0u;
         }
         // dots with the expert's row (below NT) and sums of squares, a token each
         float v[2 * NT] = {};
         const float *row = p.router + (size_t)e * p.hidden;
-        constexpr int R = NT < 16 ? 4 : sizeof(T) == 2 ? 2 : 1;  // loads of a row under way
-        for (int c0 = 128 * warp + 4 * lane; c0 < p.hidden; c0 += 128 * kRouteWarps * R) {
+        constexpr int R = NT == 1 ? 4 : 2, Step = 128 * kRouteSlices;  // loads of a row under way
+        for (int c0 = 128 * (warp % kRouteSlices) + 4 * lane; c0 < p.hidden; c0 += Step * R) {
             float4 w[R], g[R];
             Raw4<T> a[NT][R];
-            auto in = [&](int i) { return i == 0 || c0 + 128 * kRouteWarps * i < p.hidden; };
+            auto in = [&](int i) { return i == 0 || c0 + Step * i < p.hidden; };
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 if (in(i)) {
-                    const int c = c0 + 128 * kRouteWarps * i;
+                    const int c = c0 + Step * i;
                     w[i] = *reinterpret_cast<const float4 *>(row + c);
                     g[i] = p.gamma ? *reinterpret_cast<const float4 *>(p.gamma + c) : make_float4(1.f, 1.f, 1.f, 1.f);
                 } else {
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     a[t][i].zero();
-                    if (t < p.nb && in(i)) a[t][i].load(x + t * p.ldx + c0 + 128 * kRouteWarps * i);
+                    if (t0 + t < p.nb && in(i)) a[t][i].load(x + (t0 + t) * p.ldx + c0 + Step * i);
                 }
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -89,28 +89,25 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
                 }
             }
         }
-        if constexpr (NT == 16) {
-            sums[warp][lane] = transpose_reduce(v, lane);
-        } else {
 #pragma unroll
-            for (int i = 0; i < 2 * NT; ++i) {
+        for (int i = 0; i < 2 * NT; ++i) {
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-                if (lane == 0) sums[warp][i] = v[i];
-            }
+            for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+            if (lane == 0) sums[warp][i] = v[i];
         }
         __syncthreads();
-        if (warp == 0) {
-            float s = 0.f;
-            if (lane < 2 * NT)
+        if (tid < p.nb) {  // a token a thread
+            float dot = 0.f, sq = 0.f;
 #pragma unroll
-                for (int w = 0; w < kRouteWarps; ++w) s += sums[w][lane];
-            const float sq = __shfl_down_sync(0xffffffffu, s, NT);
-            if (lane < p.nb)
-                p.logits[(size_t)lane * p.E + e] = p.gamma ? s * rsqrtf(fmaf(sq, 1.f / (float)p.hidden, p.eps)) : s;
+            for (int w = 0; w < kRouteSlices; ++w) {
+                dot += sums[tid / NT * kRouteSlices + w][tid % NT];
+                sq += sums[tid / NT * kRouteSlices + w][NT + tid % NT];
+            }
+            p.logits[(size_t)tid * p.E + e] = p.gamma ? dot * rsqrtf(fmaf(sq, 1.f / (float)p.hidden, p.eps)) : dot;
         }
         return;
     }
+    const int warps = blockDim.x / 32;
     const int t = blockIdx.x - p.E, KT = mx_ktiles(p.hidden);
     const T *src = x + t * p.ldx;
     float rstd = 1.f;
@@ -129,7 +126,7 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
     };
     if (p.gamma) {
         float sum = 0.f;
-        for (int kt = warp; kt < KT; kt += kRouteWarps) {
+        for (int kt = warp; kt < KT; kt += warps) {
             float v[8];
             load(kt, v);
 #pragma unroll
@@ -140,11 +137,10 @@ __global__ void __launch_bounds__(kRouteThreads) q4moe_route_kernel(const __grid
         if (lane == 0) sums[warp][0] = sum;
         __syncthreads();
         sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kRouteWarps; ++i) sum += sums[i][0];
+        for (int i = 0; i < warps; ++i) sum += sums[i][0];
         rstd = rsqrtf(fmaf(sum, 1.f / (float)p.hidden, p.eps));
     }
-    for (int kt = warp; kt < KT; kt += kRouteWarps) {
+    for (int kt = warp; kt < KT; kt += warps) {
         const int c = kt * kMxK + 8 * lane;
         float v[8];
         load(kt, v);
@@ -180,7 +176,8 @@ constexpr int kMoeExch = 2 * 2 * 2 * 8 * 32 * 4;  // [turn][pair of warps][gate 
 // their tokens (a bit each) and the tokens' weights [expert][16]
 constexpr int kMoeOffExch = kMoeStages * kMoeStage, kMoeOffIds = kMoeOffExch + kMoeExch,
               kMoeOffMask = kMoeOffIds + 4 * kMoeMaxActive, kMoeOffW = kMoeOffMask + 4 * kMoeMaxActive,
-              kMoeOffBar = kMoeOffW + 64 * kMoeMaxActive, kMoeSmem = kMoeOffBar + 8 * (2 * kMoeStages + 5) + 16;
+              kMoeOffBar = kMoeOffW + 64 * kMoeMaxActive, kMoeOffUnit = kMoeOffBar + 8 * (2 * kMoeStages + 5) + 16,
+              kMoeSmem = kMoeOffUnit + 128;
 static_assert(kMoeStage % 1024 == 0 && kMoeSmem <= (int)kSmemMax, "shared memory of the experts' kernel");
 // while they are chosen, over the ring: the choices, an expert's tokens and its place
 // in the list
@@ -252,7 +249,7 @@ __device__ __forceinline__ void moe_choose(const float *logits, int E, int top_k
 
 // Every CTA chooses the experts by itself (the logits are a few kilobytes), then two
 // halves in one kernel: first every (expert with a token, 64 rows of gate and of up)
-// unit, a CTA each in turn; then, behind a barrier of the grid, the down projections,
+// unit, the next one to the CTA that is free first; then, behind a barrier of the grid, the down projections,
 // whose stages (output tile, expert, k) form a line that the CTAs divide evenly: a
 // stream needs all SMs (44 GB/s each; 6.3 of the 6.8 TB/s with all 152).  Parts of
 // a tile are joined by the last of its CTAs to finish, in CTA order: nothing depends on
@@ -269,6 +266,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     volatile int *info = reinterpret_cast<volatile int *>(tslot + 1);  // experts with a token; tiles to join
     int *ids = reinterpret_cast<int *>(sm + kMoeOffIds);
     unsigned *masks = reinterpret_cast<unsigned *>(sm + kMoeOffMask);
+    volatile int *unit_s = reinterpret_cast<volatile int *>(sm + kMoeOffUnit);  // this CTA's last 16 units,
+    volatile int *more_s = unit_s + 16;                                         // and whether others followed
     float *wtab = reinterpret_cast<float *>(sm + kMoeOffW);
     if (warp == 0) {
         if (lane < S) {
@@ -408,14 +407,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
                 as.next(ring, b_full);
                 ++issued;
             };
-            for (int u = cta; ok && u < units; u += grid) {
+            // units of the first half: this CTA's number, then the next that no CTA has.  A
+            // unit's number is there before its first stage is complete, and whether it has a successor
+            // before its last one is.  (The ring and the two accumulators hold fewer than 16 units.)
+            for (int u = cta, count = 0; ok && u < units; ++count) {
+                unit_s[count & 15] = u;
+                const int next = units > grid ? grid + (int)atomicAdd(p.units, 1u) : units;
                 const int a = u / T1, tile = u - a * T1;
                 const uint8_t *w = p.gate_up + ((size_t)ids[a] * T1 + tile) * KS1 * REC, *x = p.xq;
                 for (int ks = 0; ks < KS1; ++ks, w += REC, x += kMoeRec) {
+                    if (ks + 1 == KS1) more_s[count & 15] = next < units;
                     ok = weights(w);
                     if (!ok) break;
                     acts(x);
                 }
+                u = next;
             }
             // the second half: a segment's weights run through the experts' matrices, a tile of KS2
             // records each
@@ -508,7 +514,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
             ++seg;
             return ok;
         };
-        for (int u = cta; ok && u < units; u += grid) run(KS1);
+        bool more = cta < units;
+        for (int count = 0; ok && more; ++count) {
+            run(KS1);
+            more = ok && more_s[count & 15] != 0;
+        }
         if (ok)
             walk([&](int, int q0, int q1) {
                 for (int q = q0; ok && q < q1;) {
@@ -545,11 +555,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         // a tile's rows: 32 of gate, 32 of up, twice: a warp has the gates or the ups of a
         // block of h.  The gates' warp takes tokens 0-7 of it, the ups' 8-15.
         float *exch = reinterpret_cast<float *>(sm + kMoeOffExch) + pair * 512;
-        for (int u = cta; u < units; u += grid) {
-            const int a = u / T1, tile = u - a * T1, blk = 2 * tile + pair;
-            const unsigned mask = masks[a];
+        bool more = cta < units;
+        for (int count = 0; more; ++count) {
             float v[16];
             take(v);
+            if (!ok) break;
+            const int u = unit_s[count & 15];
+            more = more_s[count & 15] != 0;
+            const int a = u / T1, tile = u - a * T1, blk = 2 * tile + pair;
+            const unsigned mask = masks[a];
             float *buf = exch + (seg & 1) * 1024;
 #pragma unroll
             for (int i = 0; i < 8; ++i) buf[(up * 8 + i) * 32 + lane] = up ? v[i] : v[8 + i];
@@ -632,8 +646,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         tc::tmem_dealloc(tmem, 128);
     }
     // Tiles whose last part came from here: a thread a row and every fourth token, the
-    // parts in CTA order, eight at once.  (By the four warps of the sums, a few loads at a
-    // time, 16 tokens took 13 us.)
+    // parts in CTA order, five of all its tokens at once.  (By the four warps of the sums, a
+    // few loads at a time, 16 tokens took 13 us; a token after the other 7.)
     for (int j = 0; j < 2; ++j) {
         const int m = info[1 + j];
         if (m < 0) continue;
@@ -643,17 +657,26 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         // CTA f's part is its second if it began in an earlier tile, the others' their first
         const float *part0 = p.part + ((size_t)f * 2 + (first_of(f) < (long long)m * line)) * slot_floats + rl;
         const float *parts = p.part + rl;
-        for (int t = tid / kMxRows; t < p.nb; t += kMoeThreads / kMxRows) {
-            float v = __ldcg(part0 + t * kMxRows);
-            for (int x = f + 1; x <= l; x += 8) {
-                float o[8];
+        constexpr int TT = kMaxNb * kMxRows / kMoeThreads, X = 5;  // a thread's tokens, parts at once
+        const int t0 = tid / kMxRows;
+        float v[TT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = x + i <= l ? __ldcg(parts + (size_t)(x + i) * 2 * slot_floats + t * kMxRows) : 0.f;
+        for (int i = 0; i < TT; ++i) v[i] = t0 + 4 * i < p.nb ? __ldcg(part0 + (t0 + 4 * i) * kMxRows) : 0.f;
+        for (int x = f + 1; x <= l; x += X) {
+            float o[X][TT];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v += o[i];
-            }
-            store(m * kMxRows + rl, t, v);
+            for (int j = 0; j < X; ++j)
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                    o[j][i] = x + j <= l && t0 + 4 * i < p.nb ? __ldcg(parts + (size_t)(x + j) * 2 * slot_floats + (t0 + 4 * i) * kMxRows) : 0.f;
+#pragma unroll
+            for (int j = 0; j < X; ++j)
+#pragma unroll
+                for (int i = 0; i < TT; ++i) v[i] += o[j][i];
         }
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+            if (t0 + 4 * i < p.nb) store(m * kMxRows + rl, t0 + 4 * i, v[i]);
     }
 }
 
@@ -687,7 +710,9 @@ size_t moe_workspace(MoeParams &p, uint8_t *ws) {
         at += (bytes + 255) / 256 * 256;
         return x;
     };
-    p.barrier = (unsigned *)room(sizeof(unsigned));
+    uint8_t *ctl = room(256);
+    p.barrier = (unsigned *)ctl;
+    p.units = ws ? (unsigned *)(ctl + 128) : nullptr;
     p.count = (unsigned *)room(sizeof(unsigned) * mx_rtiles(p.hidden));
     p.logits = (float *)room(sizeof(float) * p.nb * p.E);
     p.xq = room((size_t)mx_ktiles(p.hidden) * kMoeRec);
@@ -696,12 +721,11 @@ size_t moe_workspace(MoeParams &p, uint8_t *ws) {
     return at;
 }
 
-// (a token's sums are straight code: 16 tokens' of it cost one token 1.5 us)
 template <typename T>
 static int launch_route(const MoeParams &p, cudaStream_t stream) {
-    auto kern = p.nb == 1 ? dev::q4moe_route_kernel<T, 1> : p.nb <= 4 ? dev::q4moe_route_kernel<T, 4> : dev::q4moe_route_kernel<T, 16>;
+    auto kern = p.nb == 1 ? dev::q4moe_route_kernel<T, 1> : dev::q4moe_route_kernel<T, 4>;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(p.E + p.nb), dev::kRouteThreads, 0, stream, &attr);
+    const cudaLaunchConfig_t cfg = pdl_config((unsigned)(p.E + p.nb), 32 * dev::kRouteSlices * ((p.nb + 3) / 4), 0, stream, &attr);
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? 0 : -1;
 }
 

@@ -569,8 +569,9 @@ struct MoeParams {
     int32_t *idx;               // [nb][top_k]
     float *weight;              // [nb][top_k]
     // workspace
-    unsigned *barrier;          // of the experts' kernel, and
-    unsigned *count;            // [hidden / 128] parts of a tile that are there: zeroed by the routing kernel
+    // of the experts' kernel, zeroed by the routing kernel: its barrier, the units of its
+    // first half that are handed out, [hidden / 128] the parts of a tile that are there
+    unsigned *barrier, *units, *count;
     float *logits;              // [nb][E]
     uint8_t *xq, *h;            // records [k tile], [expert with a token][k tile]
     float *part;                // [CTA][2][nb][128] parts of tiles
