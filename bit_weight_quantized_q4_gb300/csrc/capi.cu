@@ -1205,7 +1205,7 @@ q4_status mx_gemm(const q4_mx *W, const q4_mx *X, const q4_mx_src *src, const vo
     Q4_TRY(kernel_err_ptr(&p.err));
     p.wait_cycles = g_wait_cycles;
     p.extra_tx = g_extra_tx;
-    if (src && src->dtype == dtype && !p.pair && q4::mx_gemm_few(X->rows, W->k, src->gamma != nullptr)) {
+    if (src && src->dtype == dtype && !p.pair && q4::mx_gemm_few(X->rows, dtype, src->gamma != nullptr, src->up != nullptr)) {
         p.src = mx_quant_params(src, X);
     } else if (src) {
         Q4_TRY(mx_quant(src, X, stream));

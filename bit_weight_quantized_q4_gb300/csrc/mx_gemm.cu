@@ -23,7 +23,7 @@ constexpr int kMxgThreads = 192, kMxgQuant = 128;  // and the threads that quant
 constexpr int kMxgMaxN = 192;       // columns of a tile
 constexpr int kMxgSmallN = 64;      // up to here two CTAs of an SM
 constexpr int kMxgMaxStages = 12;
-constexpr int kMxgBars = (8 * (2 * kMxgMaxStages + 5) + 16 + 15) / 16 * 16, kMxgTail = kMxgBars + 64;  // barriers, 16 rows' factors
+constexpr int kMxgBars = (8 * (2 * kMxgMaxStages + 5) + 16 + 15) / 16 * 16;
 
 template <int FMT, typename T, bool QX>
 __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
@@ -195,122 +195,99 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         mbar_wait(b_drain, 0u, kWaitCycles);
     } else if (QX && warp >= 6) {
         // ------------------------------------------------------------ rows of x into the stages
-        // Every fourth stage a warp, two rows at a time, sixteen values a lane; D such pairs of
-        // rows are under way (all four warps on each stage, its loads a stage ahead: 0.7 us a
-        // stage, the loads' latency).
+        // Every fourth stage a warp, two rows (a half warp each, sixteen values a lane) or two
+        // such pairs at a time; D steps' loads are under way.  (All four warps on each stage, its
+        // loads a stage ahead: 0.7 us a stage, the loads' latency.)
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        constexpr int NQ = kMxgQuant / 32, D = sizeof(T) == 2 ? 4 : 2;
+        constexpr int NQ = kMxgQuant / 32;
         const int w = warp - 6, half = lane >> 4, h = lane & 15, pairs = (p.nb + 1) / 2, len = k1 - k0;
         const MxGain gain{p.src.scale, p.src.six_g, p.src.inv};
         const T *x = (const T *)p.src.x, *up = (const T *)p.src.up;
-        float *rs = reinterpret_cast<float *>(sm + S * p.stage_bytes + kMxgBars);  // 1 / rms of the rows
-        if (p.src.gamma) {
-            // in the order of q4mx_quant_norm_kernel: 512s by eights, then the eight
-            for (int row = w; row < p.nb; row += NQ) {
-                uint64_t part[8] = {};
-                for (int c0 = 16 * lane; c0 < p.src.k; c0 += 4096)
-#pragma unroll
-                    for (int g = 0; g < 8; g += 4) {
-                        Raw16<T> t[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            t[i].zero();
-                            if (c0 + 512 * (g + i) < p.src.k) t[i].load(x + row * p.src.ld + c0 + 512 * (g + i));
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint64_t v[8];
-                            t[i].pairs(v);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) part[g + i] = fma_f32x2(v[e], v[e], part[g + i]);
-                        }
-                    }
-                float sum = 0.f;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    float s = lo_f32(part[g]) + hi_f32(part[g]);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                    sum += s;
-                }
-                if (lane == 0) rs[row] = mx_rstd(sum, 1.f / (float)p.src.k, p.src.eps);
-            }
-            asm volatile("bar.sync 1, %0;" ::"n"(kMxgQuant) : "memory");
-        }
-        const int mine = (tiles - (int)blockIdx.x / C + (int)gridDim.x / C - 1) / ((int)gridDim.x / C);  // tiles of this CTA
-        const int total = mine * len;                                                                   // stages
-        // the stage and the pair of rows that a step loads, and those it stores
-        struct At {
-            int it, ks, pair;
-        };
-        auto next = [&](At &a) {
-            if (++a.pair == pairs) {
-                a.pair = 0;
-                a.it += NQ;
-                a.ks += NQ;
-                while (a.ks >= len) a.ks -= len;
-            }
-        };
-        At in = {w, w % len, 0};
-        Raw16<T> a[D], b[D];
-        auto fetch = [&](int d) {
-            const int c = (k0 + in.ks) * kMxK + 16 * h, row = 2 * in.pair + half;
-            a[d].zero();
-            b[d].zero();
-            if (in.it < total && row < p.nb && c < p.src.k) {
-                a[d].load(x + row * p.src.ld + c);
-                if (up) b[d].load(up + row * p.src.ld + c);
-            }
-            next(in);
-        };
-#pragma unroll
-        for (int d = 0; d < D; ++d) fetch(d);
-        At out = {w, w % len, 0};
-        int slot = w;  // (a ring has more than four)
-        uint32_t par = 1;
+        const int mine = (tiles - (int)blockIdx.x / C + (int)gridDim.x / C - 1) / ((int)gridDim.x / C);
+        const int total = mine * len;  // tiles of this CTA, their stages
         bool ok = true;
-        while (ok && out.it < total) {
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                if (!ok || out.it >= total) break;
-                if (out.pair == 0) ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, par, lim));
-                if (!ok) break;
-                const int c = (k0 + out.ks) * kMxK + 16 * h, row = 2 * out.pair + half;
-                uint64_t v[8];
-                float f = 1.f;
-                a[d].pairs(v);
-                if (up) {
-                    uint64_t u[8];
-                    b[d].pairs(u);
-                    mx_glu(v, u);
-                } else if (p.src.gamma && c < p.src.k) {
-                    if (row < p.nb) f = rs[row];
-                    uint64_t g[8];
-                    mx_factors(g, p.src.gamma + c);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = mul_f32x2(v[e], g[e]);
+        auto quantise = [&](auto glu) {
+            constexpr bool GLU = decltype(glu)::value;
+            constexpr int P = GLU ? 1 : 2;  // pairs of rows a step
+            constexpr int D = (sizeof(T) == 2 ? 2 : 1) * (GLU ? 2 : 1);
+            struct At {  // the stage and the first pair that a step loads, or stores
+                int it, ks, pair;
+            };
+            auto next = [&](At &a) {
+                a.pair += P;
+                if (a.pair >= pairs) {
+                    a.pair = 0;
+                    a.it += NQ;
+                    a.ks += NQ;
+                    while (a.ks >= len) a.ks -= len;
                 }
-                fetch(d);
-                uint2 code;
-                uint32_t word;
-                mx_codes<FMT>(v, f, gain, code, word);
-                uint8_t *rec = sm + slot * p.stage_bytes + REC;  // 16 rows of codes, then the scales
-                *reinterpret_cast<uint2 *>(rec + mx_code_off(row, 8 * h)) = code;
-                constexpr int L = 4 * mx_block(FMT) / 16;  // lanes of a word
-                if (h % L == 0) *reinterpret_cast<uint32_t *>(rec + p.NB * 128 + h / L * 512 + row * 16) = word;
-                next(out);
-                if (out.pair == 0) {  // the stage is complete
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the codes, for the tensor core
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(b_full + 8 * slot);
-                    slot += NQ;
-                    if (slot >= S) {
-                        slot -= S;
-                        par ^= 1;
+            };
+            At in = {w, w % len, 0};
+            Raw16<T> a[D][P], b[GLU ? D : 1][P];
+            auto fetch = [&](int d) {
+                const int c = (k0 + in.ks) * kMxK + 16 * h;
+#pragma unroll
+                for (int q = 0; q < P; ++q) {
+                    const int row = 2 * (in.pair + q) + half;
+                    a[d][q].zero();
+                    if constexpr (GLU) b[d][q].zero();
+                    if (in.it < total && row < p.nb && c < p.src.k) {
+                        a[d][q].load(x + row * p.src.ld + c);
+                        if constexpr (GLU) b[d][q].load(up + row * p.src.ld + c);
+                    }
+                }
+                next(in);
+            };
+#pragma unroll
+            for (int d = 0; d < D; ++d) fetch(d);
+            At out = {w, w % len, 0};
+            int slot = w;  // (a ring has more than four)
+            uint32_t par = 1;
+            while (ok && out.it < total) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    if (!ok || out.it >= total) break;
+                    if (out.pair == 0) ok = __all_sync(0xffffffffu, mbar_wait(b_empty + 8 * slot, par, lim));
+                    if (!ok) break;
+                    uint64_t v[P][8];
+#pragma unroll
+                    for (int q = 0; q < P; ++q) a[d][q].pairs(v[q]);
+                    if constexpr (GLU) {
+                        uint64_t u[8];
+                        b[d][0].pairs(u);
+                        mx_glu(v[0], u);
+                    }
+                    fetch(d);
+                    uint2 code[P];
+                    uint32_t word[P];
+#pragma unroll
+                    for (int q = 0; q < P; ++q) mx_codes<FMT>(v[q], 1.f, gain, code[q], word[q]);
+                    uint8_t *rec = sm + slot * p.stage_bytes + REC;  // 16 rows of codes, then the scales
+                    constexpr int L = 4 * mx_block(FMT) / 16;        // lanes of a word
+#pragma unroll
+                    for (int q = 0; q < P; ++q) {
+                        const int row = 2 * (out.pair + q) + half;  // (below 16: P divides the pairs of 16 rows)
+                        *reinterpret_cast<uint2 *>(rec + mx_code_off(row, 8 * h)) = code[q];
+                        if (h % L == 0) *reinterpret_cast<uint32_t *>(rec + p.NB * 128 + h / L * 512 + row * 16) = word[q];
+                    }
+                    next(out);
+                    if (out.pair == 0) {  // the stage is complete
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the codes, for the tensor core
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(b_full + 8 * slot);
+                        slot += NQ;
+                        if (slot >= S) {
+                            slot -= S;
+                            par ^= 1;
+                        }
                     }
                 }
             }
-        }
+        };
+        if (up)
+            quantise(std::true_type{});
+        else
+            quantise(std::false_type{});
         if (!ok && lane == 0) atomicExch(p.err, 4);
     } else {
         // ------------------------------------------------------------ results
@@ -457,24 +434,27 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
     p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + blocks * 512 * W + 1023) / 1024 * 1024;
     const long long tiles = (long long)p.MT * p.CT;
     const bool two = p.NB <= dev::kMxgSmallN && tiles * p.C > sms;  // two CTAs of an SM
-    const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgTail;
+    const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgBars;
     p.stages = std::min(dev::kMxgMaxStages, room / p.stage_bytes);
     p.acc = p.NB <= dev::kMxgSmallN ? dev::kMxgSmallN : dev::kMxgMaxN;
     return (int)(p.C > 1 ? tiles * p.C : std::min<long long>(tiles, two ? 2 * sms : sms));
 }
 
-bool mx_gemm_few(int nb, int k, bool norm) {
-    // Every CTA quantises the rows of its stages: up to eight in less time than their weights
-    // take (14336 x 4096, one row: 8.8 us, 10.8 with a kernel in front; eight: 11.7 and 11.3;
-    // sixteen: 18.3 and 11.5).  Behind a norm it reads all of them before its first stage.
-    return nb <= 8 && (!norm || (long long)nb * k <= 16384);
+bool mx_gemm_few(int nb, int dtype, bool norm, bool glu) {
+    // Every CTA quantises the rows of its stages, while the weights arrive: up to this many
+    // rows in less time than a kernel in front of the product takes (us at 14336 x 4096, MXFP4,
+    // here / there: bf16 8.2 / 10.3 for one row, 9.7 / 10.6 for eight, 11.2 / 10.6 for ten; two
+    // inputs 9.2 / 10.5 for four, 10.6 / 10.5 for six; float 9.5 / 10.1 for four, 11.1 / 10.1 for
+    // six).  Behind a norm a CTA would read whole rows before its first stage: 10.1 / 10.1 for
+    // one row, 10.8 / 10.1 for four.
+    return !norm && nb <= (glu || dtype == 0 ? 4 : 8);
 }
 
 template <int FMT, typename T, bool QX>
 static int launch_mx_gemm_t(const MxGemmParams &p, int ctas, cudaStream_t stream) {
     auto kern = dev::q4mx_gemm_kernel<FMT, T, QX>;
     static size_t smem_set[64] = {0};
-    const size_t smem = (size_t)p.stages * p.stage_bytes + dev::kMxgTail;
+    const size_t smem = (size_t)p.stages * p.stage_bytes + dev::kMxgBars;
     if (!raise_smem(kern, smem, smem_set)) return -1;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = pdl_config((unsigned)ctas, dev::kMxgThreads + (QX ? dev::kMxgQuant : 0), smem, stream, attr);

@@ -548,7 +548,7 @@ struct MxGemmParams {
     MxQuantParams src;     // src.x not null: a few rows that the product quantises itself (x unused)
 };
 // Whether the product quantises rows itself.
-bool mx_gemm_few(int nb, int k, bool norm);
+bool mx_gemm_few(int nb, int dtype, bool norm, bool glu);
 // Sets the tiles, the cluster and the ring of p (n, nb, KS given) and returns the CTAs.
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms);
 int launch_mx_gemm(const MxGemmParams &p, int fmt, int dtype, int ctas, void *stream);
