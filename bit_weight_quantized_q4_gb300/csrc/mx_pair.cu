@@ -8,23 +8,24 @@
 // both.  x's scales are in both CTAs, of all columns: each tensor core needs them.  (Four
 // warps of each CTA that wrote the scales to tensor memory, instead of the copies that
 // the first CTA issues for both, took 0.8 us a stage.)
-//   warp 0 copies, warp 1 issues MMAs (first CTA) or tells the first CTA of stages that
-//   have landed (second), warps 2-9 write the results (half of the columns each four).
+//   warps 0, 10 and 11 copy, warp 1 issues MMAs (first CTA) or tells the first CTA of stages
+//   that have landed (second), warps 2-9 write the results (half of the columns each four).
 #include <algorithm>
+#include <type_traits>
 
 #include "mx_common.cuh"
 
 namespace q4 {
 namespace dev {
 
-constexpr int kPairThreads = 320;
+constexpr int kPairThreads = 384;
 constexpr int kPairN = 192, kPairHalf = kPairN / 2;
 template <int FMT>
 struct PairCfg {
     static constexpr int W = mx_words(FMT), REC = mx_rec(FMT);
     static constexpr int OffB = REC, OffSf = OffB + kPairHalf * 128, Stage = OffSf + 2 * 512 * W;
     static constexpr int S = FMT == 0 ? 7 : 6;
-    static constexpr int OffBar = S * Stage, Smem = OffBar + 8 * (3 * S + 5) + 16;
+    static constexpr int OffBar = S * Stage, Smem = OffBar + 8 * (2 * S + 5) + 16;
     static_assert(Stage % 1024 == 0 && Smem <= (int)kSmemMax, "shared memory of a pair's CTA");
 };
 
@@ -74,16 +75,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int rank = blockIdx.x & 1, KS = p.KS, M2 = (p.MT + 1) / 2, tiles = M2 * p.CT;
     const uint32_t ring = smem_u32(sm);
-    // barriers: a stage has landed here, a stage has landed in the second CTA (the first
-    // CTA's), a stage's MMAs are done; of an accumulator: it is complete, both CTAs have read it (the
-    // first CTA's); the last MMAs of all
-    const uint32_t b_full = ring + Cf::OffBar, b_ready = b_full + 8 * S, b_empty = b_ready + 8 * S, b_acc = b_empty + 8 * S,
-                   b_read = b_acc + 16, b_drain = b_read + 16;
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 8 * (3 * S + 5));
+    // barriers: a stage has landed here (the first CTA's: in both), a stage's MMAs are done; of an
+    // accumulator: it is complete, both CTAs have read it (the first CTA's); the last MMAs of all
+    const uint32_t b_full = ring + Cf::OffBar, b_empty = b_full + 8 * S, b_acc = b_empty + 8 * S, b_read = b_acc + 16,
+                   b_drain = b_read + 16;
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + Cf::OffBar + 8 * (2 * S + 5));
     if (warp == 0) {
         if (lane < S) {
-            mbar_init(b_full + 8 * lane, 1);
-            mbar_init(b_ready + 8 * lane, 1);
+            mbar_init(b_full + 8 * lane, rank == 0 ? 4 : 3);  // the three copying warps, the second CTA
             mbar_init(b_empty + 8 * lane, 1);
         }
         if (lane < 2) {
@@ -116,70 +115,65 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     };
     const long long lim = p.wait_cycles;
 
-    if (warp == 0) {
+    if (warp == 0 || warp >= 10) {
         // ------------------------------------------------------------ copies
-        // (one thread's chain of instructions: what a tile's stages share is computed once)
-        if (lane == 0) {
-            uint32_t extra = (uint32_t)p.extra_tx;
-            // the first stages' weights before what is in front of this kernel is done
-            const int t0 = blockIdx.x >> 1;
-            int ahead = 0;
+        // Three warps, one thread each, each with its own share of every stage's bytes: warp 0
+        // w's record, warp 10 x's codes, warp 11 x's scales.  (One thread for all took 560
+        // cycles a stage to issue them.)  What a tile's stages share is computed once.
+        if (tc::elect_one()) {
+            int slot = 0, issued = 0, ahead = 0;
+            uint32_t par = 1, extra = warp == 0 ? (uint32_t)p.extra_tx : 0u;  // (a wait for the phase before the first passes)
             auto source = [&](int t) {
                 // (behind an odd number of row tiles the last one again: its results are not stored)
                 return p.w + (size_t)min(2 * (t % M2) + rank, p.MT - 1) * KS * REC;
             };
-            auto bytes_of = [&](int c0, int N) {
-                return (uint32_t)(REC + N / 2 * 128 + ((c0 & 127) + N > 128 ? 2 : 1) * 512 * W);
-            };
-            if (p.early && t0 < tiles) {
-                int c0, N;
-                cols(t0 / M2, c0, N);
-                const uint8_t *w = source(t0);
-                for (; ahead < min(S, KS); ++ahead) {
-                    mbar_expect_tx(b_full + 8 * ahead, bytes_of(c0, N) + extra);
-                    extra = 0;
-                    bulk_copy(ring + ahead * Cf::Stage, w + (size_t)ahead * REC, REC, b_full + 8 * ahead);
-                }
-            }
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-            int slot = 0, issued = 0;
-            uint32_t par = 1, dst = ring, bar = b_full;  // (a wait for the phase before the first passes)
-            walk([&](int t) {
-                int c0, N;
-                cols(t / M2, c0, N);
-                const int r0 = c0 + rank * (N / 2), off = r0 & 127, n0 = min(N / 2, 128 - off);
-                const size_t step = (size_t)KS * REC;  // a row tile of x
-                const uint8_t *w = source(t), *b = p.x + (r0 >> 7) * step + off * 128, *b2 = p.x + ((r0 >> 7) + 1) * step;
-                const uint8_t *sf = p.x + (c0 >> 7) * step + kMxCodes, *sf2 = sf + step;
-                const uint32_t bytes = bytes_of(c0, N), len = n0 * 128, len2 = (N / 2 - n0) * 128;
-                const bool two = (c0 & 127) + N > 128;
+            // a tile's stages: one or two copies each, KS times, a record further each time
+            auto stages = [&](uint32_t at, const uint8_t *src, uint32_t len, uint32_t at2, const uint8_t *src2, uint32_t len2) {
                 for (int ks = 0; ks < KS; ++ks) {
+                    const uint32_t st = ring + slot * Cf::Stage, bar = b_full + 8 * slot;
                     if (ahead > 0) {
                         --ahead;
                     } else {
-                        if (!mbar_wait(bar + 8 * 2 * S, par, lim)) {  // b_empty of this slot
+                        if (!mbar_wait(b_empty + 8 * slot, par, lim)) {
                             atomicExch(p.err, 4);
                             return false;
                         }
-                        mbar_expect_tx(bar, bytes + extra);
+                        mbar_expect_tx(bar, len + len2 + extra);
                         extra = 0;
-                        bulk_copy(dst, w, REC, bar);
+                        bulk_copy(st + at, src, len, bar);
+                        if (len2) bulk_copy(st + at2, src2, len2, bar);
                     }
-                    bulk_copy(dst + Cf::OffB, b, len, bar);
-                    if (len2) bulk_copy(dst + Cf::OffB + len, b2, len2, bar);
-                    bulk_copy(dst + Cf::OffSf, sf, 512 * W, bar);
-                    if (two) bulk_copy(dst + Cf::OffSf + 512 * W, sf2, 512 * W, bar);
-                    w += REC, b += REC, b2 += REC, sf += REC, sf2 += REC;
+                    src += REC, src2 += REC;
                     ++issued;
-                    dst += Cf::Stage, bar += 8;
                     if (++slot == S) {
                         slot = 0;
                         par ^= 1;
-                        dst = ring;
-                        bar = b_full;
                     }
                 }
                 return true;
+            };
+            if (warp == 0 && p.early && (int)blockIdx.x >> 1 < tiles) {
+                // the first stages' weights before what is in front of this kernel is done
+                const uint8_t *w = source(blockIdx.x >> 1);
+                for (; ahead < min(S, KS); ++ahead, w += REC) {
+                    mbar_expect_tx(b_full + 8 * ahead, REC + extra);
+                    extra = 0;
+                    bulk_copy(ring + ahead * Cf::Stage, w, REC, b_full + 8 * ahead);
+                }
+            }
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            walk([&](int t) {
+                if (warp == 0) return stages(0, source(t), REC, 0, nullptr, 0);
+                int c0, N;
+                cols(t / M2, c0, N);
+                const size_t step = (size_t)KS * REC;  // a row tile of x
+                if (warp == 10) {
+                    const int r0 = c0 + rank * (N / 2), off = r0 & 127, n0 = min(N / 2, 128 - off);
+                    const uint8_t *b = p.x + (r0 >> 7) * step;
+                    return stages(Cf::OffB, b + off * 128, n0 * 128, Cf::OffB + n0 * 128, b + step, (N / 2 - n0) * 128);
+                }
+                const uint8_t *sf = p.x + (c0 >> 7) * step + kMxCodes;
+                return stages(Cf::OffSf, sf, 512 * W, Cf::OffSf + 512 * W, sf + step, (c0 & 127) + N > 128 ? 512 * W : 0);
             });
             // what is in flight lands before the CTA ends
             for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(b_full + 8 * (i % S), (uint32_t)(i / S) & 1u, kWaitCycles);
@@ -195,24 +189,25 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
             }
         };
         if (rank == 0) {
-            int seg = 0;
-            uint32_t sf_set = 0;
-            bool ok = true;
-            walk([&](int t) {
-                int c0, N;
-                cols(t / M2, c0, N);
-                const int buf = seg & 1;
-                ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
-                tc::fence_after_sync();
-                const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
-                const bool two = (c0 & 127) + N > 128;
-                // (M = 256 is bit 28, M = 128 bit 27)
-                const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
-                for (int ks = 0; ok && ks < KS; ++ks) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim) && mbar_wait(b_ready + 8 * slot, par, lim));
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    if (tc::elect_one()) {
+            // (one thread for the whole loop, one barrier a stage: with a vote of the warp and a
+            // barrier for each CTA's bytes a stage took 150 cycles of waits that had long passed)
+            if (tc::elect_one()) {
+                int seg = 0;
+                uint32_t sf_set = 0;
+                bool ok = true;
+                walk([&](int t) {
+                    int c0, N;
+                    cols(t / M2, c0, N);
+                    const int buf = seg & 1;
+                    ok = seg < 2 || mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim);
+                    const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
+                    const bool two = (c0 & 127) + N > 128;
+                    // (M = 256 is bit 28, M = 128 bit 27)
+                    const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
+                    for (int ks = 0; ok && ks < KS; ++ks) {
+                        ok = mbar_wait(b_full + 8 * slot, par, lim);
+                        if (!ok) break;
+                        tc::fence_after_sync();
                         const uint32_t a = ring + slot * Cf::Stage, b = a + Cf::OffB, sb = a + Cf::OffSf;
                         const uint32_t ta = tmem + 2 * kPairN + sf_set, tb = ta + 16;
 #pragma unroll
@@ -228,18 +223,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                                              ta + 4 * w, tb + 8 * w + skip, ks | j);
                         }
                         commit_pair(b_empty + 8 * slot);
-                        if (ks + 1 == KS) commit_pair(b_acc + 8 * buf);
+                        sf_set ^= 64;
+                        next();
                     }
-                    __syncwarp();
-                    sf_set ^= 64;
-                    next();
-                }
-                ++seg;
-                return ok;
-            });
-            if (!ok && lane == 0) atomicExch(p.err, 4);
-            if (tc::elect_one()) commit_pair(b_drain);
-            __syncwarp();
+                    if (ok) commit_pair(b_acc + 8 * buf);
+                    ++seg;
+                    return ok;
+                });
+                if (!ok) atomicExch(p.err, 4);
+                commit_pair(b_drain);
+            }
         } else if (lane == 0) {
             walk([&](int) {
                 for (int ks = 0; ks < KS; ++ks, next()) {
@@ -247,7 +240,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                         atomicExch(p.err, 4);
                         return false;
                     }
-                    arrive_first(b_ready + 8 * slot);
+                    arrive_first(b_full + 8 * slot);
                 }
                 return true;
             });
@@ -257,54 +250,93 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     } else {
         // ------------------------------------------------------------ results
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        const int q = warp & 3, rl = 32 * q + lane, part = (warp - 2) / 4;
-        int seg = 0;
+        // Two types of 16 bits: a lane takes two rows (n) of every second column, its
+        // neighbour the same rows of the others, so that each reads and writes 4 bytes.  (2
+        // bytes a lane: 8500 cycles a tile with a residual, longer than its MMAs.)
+        const int q = warp & 3, part = (warp - 2) / 4;
         bool ok = true;
         const size_t n = p.n;
-        walk([&](int t) {
-            const int row = (2 * (t % M2) + rank) * kMxRows + rl, buf = seg & 1;
-            int c0, N;
-            cols(t / M2, c0, N);
-            c0 += part * (N / 2);
-            N /= 2;
-            const int live = row < p.n ? min(N, p.nb - c0) : 0;  // columns to write
-            T *y = (T *)p.y + c0 * n + row;
-            const T *rs = (const T *)p.r + c0 * n + row;
-            T add[4][16];  // the residual, 64 columns ahead (mx_gemm.cu)
-            auto fetch = [&](int s, int c) {
-                const T *src = rs + c * n;
+        auto results = [&](auto two_rows) {
+            constexpr bool P2 = decltype(two_rows)::value;
+            using V = std::conditional_t<P2, uint32_t, T>;  // what a lane reads and writes at once
+            constexpr int CW = P2 ? 2 : 1, WIN = P2 ? kPairHalf : 64;  // columns of a V of two lanes; of the residual held
+            const int odd = P2 ? lane & 1 : 0, rl = 32 * q + lane - odd;
+            int seg = 0;
+            walk([&](int t) {
+                const int row = (2 * (t % M2) + rank) * kMxRows + rl, buf = seg & 1;
+                int c0, N;
+                cols(t / M2, c0, N);
+                c0 += part * (N / 2);
+                N /= 2;
+                const int live = (row < p.n ? min(N, p.nb - c0) : 0) - odd;  // columns to read and write, from this lane's first
+                const size_t at = (size_t)(c0 + odd) * n + row;
+                T *y = (T *)p.y + at;
+                V add[WIN / CW];  // the residual, before the sums are there
+                auto fetch = [&](int c) {  // 16 columns
+                    const T *src = (const T *)p.r + at + c * n;
 #pragma unroll
-                for (int i = 0; i < 16; ++i, src += n) add[s][i] = c + i < live ? *src : from_f32<T>(0.f);
-            };
-            if (p.r)
+                    for (int i = 0; i < 16 / CW; ++i, src += CW * n) {
+                        V v{};
+                        if (c + CW * i < live) v = *reinterpret_cast<const V *>(src);
+                        add[c % WIN / CW + i] = v;
+                    }
+                };
+                if (p.r)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) fetch(s, 16 * s);
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
-            tc::fence_after_sync();
-            const uint32_t d = tmem + buf * kPairN + part * N + ((uint32_t)(32 * q) << 16);
-            for (int cb = 0; cb < N; cb += 64)
+                    for (int c = 0; c < WIN; c += 16) fetch(c);
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
+                tc::fence_after_sync();
+                const uint32_t d = tmem + buf * kPairN + part * N + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int c = cb + 16 * s;
+                for (int c = 0; c < kPairHalf; c += 16) {
                     if (c >= N) break;
                     uint32_t w[16];
                     tc::ld16(d + c, w);
                     tc::wait_ld16(w);
+                    if (c + 16 >= N) {  // the accumulator has been read
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (ok && lane == 0) arrive_first(b_read + 8 * buf);  // (after a failure a phase could get too many)
+                    }
                     T *dst = y + c * n;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i, dst += n)
-                        if (c + i < live) {
-                            const float v = __uint_as_float(w[i]);
-                            *dst = from_f32<T>(p.r ? fmaf(v, p.alpha, to_f32(add[s][i])) : v * p.alpha);
+                    for (int i = 0; i < 16 / CW; ++i, dst += CW * n) {
+                        float v[CW];
+                        if constexpr (P2) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[2 * i] : w[2 * i + 1], 1);
+                            v[0] = __uint_as_float(odd ? got : w[2 * i]), v[1] = __uint_as_float(odd ? w[2 * i + 1] : got);
+                        } else {
+                            v[0] = __uint_as_float(w[i]);
                         }
-                    if (p.r) fetch(s, c + 64);
+                        if (p.r) {
+                            const T *r = reinterpret_cast<const T *>(&add[c % WIN / CW + i]);
+#pragma unroll
+                            for (int e = 0; e < CW; ++e) v[e] = fmaf(v[e], p.alpha, to_f32(r[e]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < CW; ++e) v[e] *= p.alpha;
+                        }
+                        if (c + CW * i < live) {
+                            if constexpr (P2)
+                                *reinterpret_cast<V *>(dst) = pack2<T>(v[0], v[1]);
+                            else
+                                *dst = from_f32<T>(v[0]);
+                        }
+                    }
+                    if (p.r && c + WIN < N) fetch(c + WIN);
                 }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (ok && lane == 0) arrive_first(b_read + 8 * buf);  // (after a failure a phase could get too many)
-            ++seg;
-            return true;
-        });
+                ++seg;
+                return true;
+            });
+        };
+        if constexpr (sizeof(T) == 2) {
+            if (p.n % 2 == 0)
+                results(std::true_type{});
+            else
+                results(std::false_type{});
+        } else {
+            results(std::false_type{});
+        }
         if (!ok && lane == 0) atomicExch(p.err, 4);
     }
     __syncwarp();
