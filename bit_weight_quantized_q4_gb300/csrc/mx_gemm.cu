@@ -20,8 +20,7 @@ namespace q4 {
 namespace dev {
 
 constexpr int kMxgThreads = 192, kMxgQuant = 128;  // and the threads that quantise
-constexpr int kMxgMaxN = 192;       // columns of a tile
-constexpr int kMxgSmallN = 64;      // up to here two CTAs of an SM
+constexpr int kMxgMaxN = 64;        // columns of a tile
 constexpr int kMxgMaxStages = 12;
 constexpr int kMxgBars = (8 * (2 * kMxgMaxStages + 5) + 16 + 15) / 16 * 16;
 
@@ -31,9 +30,9 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
     constexpr int W = mx_words(FMT), REC = mx_rec(FMT);
     extern __shared__ __align__(1024) uint8_t sm[];  // the swizzle's pattern repeats every 1024 bytes
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int S = p.stages, C = p.C, tiles = p.MT * p.CT, rank = C > 1 ? blockIdx.x % C : 0;
+    const int S = p.stages, C = p.C, tiles = p.MT, rank = C > 1 ? blockIdx.x % C : 0;
     const int k0 = p.KS * rank / C, k1 = p.KS * (rank + 1) / C;  // this CTA's part of k
-    const uint32_t cols_tm = p.acc == kMxgMaxN ? 512 : 256, sf_tm = 2 * p.acc;  // tensor memory: accumulators, two sets of scales
+    constexpr uint32_t cols_tm = 256, sf_tm = 2 * kMxgMaxN;  // tensor memory: two accumulators, two sets of scales
     const uint32_t ring = smem_u32(sm), bars = ring + S * p.stage_bytes;
     // barriers: a stage has landed, a stage's MMAs are done; of an accumulator: it is
     // complete, it has been read; the last MMAs of all
@@ -67,13 +66,7 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         for (int t = blockIdx.x / C; t < tiles; t += gridDim.x / C)
             if (!f(t)) return;
     };
-    // a tile's columns: the first, how many (whole 16s), and how many of them lie in
-    // the first of the (two at most) row tiles of x that it covers
-    auto cols = [&](int ct, int &c0, int &N, int &n0) {
-        c0 = ct * p.NB;
-        N = min(p.NB, (p.nb - c0 + 15) & ~15);
-        n0 = min(N, kMxRows - (c0 & (kMxRows - 1)));
-    };
+    const int N = p.NB;
     const long long lim = p.wait_cycles;
 
     if (warp == 0) {
@@ -84,16 +77,14 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         if (lane == 0) {
             uint32_t extra = (uint32_t)p.extra_tx;
             const int t0 = blockIdx.x / C;
-            auto source = [&](int t) { return p.w + ((size_t)(t % p.MT) * p.KS + k0) * REC; };
-            auto bytes_of = [&](int N, int n0) { return (uint32_t)(QX ? REC : REC + N * 128 + (N > n0 ? 2 : 1) * 512 * W); };
+            auto source = [&](int t) { return p.w + ((size_t)t * p.KS + k0) * REC; };
+            const uint32_t bytes = QX ? REC : REC + N * 128 + 512 * W;
             int ahead = 0;  // stages with their copies of w, but not of x
             if (p.early && t0 < tiles) {
                 // the first stages' weights before what is in front of this kernel is done
-                int c0, N, n0;
-                cols(t0 / p.MT, c0, N, n0);
                 const uint8_t *w = source(t0);
                 for (; ahead < min(S, k1 - k0); ++ahead) {
-                    mbar_expect_tx(b_full + 8 * ahead, bytes_of(N, n0) + extra);
+                    mbar_expect_tx(b_full + 8 * ahead, bytes + extra);
                     extra = 0;
                     bulk_copy(ring + ahead * p.stage_bytes, w + (size_t)ahead * REC, REC, b_full + 8 * ahead);
                 }
@@ -102,12 +93,8 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
             int slot = 0, issued = 0;
             uint32_t par = 1, dst = ring, bar = b_full;  // (a wait for the phase before the first passes)
             walk([&](int t) {
-                int c0, N, n0;
-                cols(t / p.MT, c0, N, n0);
-                const size_t step = (size_t)p.KS * REC;  // a row tile of x
-                const uint8_t *w = source(t), *a = p.x + (size_t)(c0 / kMxRows) * step + (size_t)k0 * REC;
-                const uint8_t *b = a + (c0 & (kMxRows - 1)) * 128, *sf = a + kMxCodes, *b2 = a + step, *sf2 = sf + step;
-                const uint32_t bytes = bytes_of(N, n0), len = n0 * 128, len2 = (N - n0) * 128, osf = REC + p.NB * 128;
+                const uint8_t *w = source(t), *b = p.x + (size_t)k0 * REC, *sf = b + kMxCodes;
+                const uint32_t len = N * 128, osf = REC + len;
                 for (int ks = k0; ks < k1; ++ks) {
                     if (ahead > 0) {
                         --ahead;
@@ -124,11 +111,7 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
                         bulk_copy(dst + REC, b, len, bar);
                         bulk_copy(dst + osf, sf, 512 * W, bar);
                     }
-                    if (!QX && len2) {
-                        bulk_copy(dst + REC + len, b2, len2, bar);
-                        bulk_copy(dst + osf + 512 * W, sf2, 512 * W, bar);
-                    }
-                    w += REC, b += REC, sf += REC, b2 += REC, sf2 += REC;
+                    w += REC, b += REC, sf += REC;
                     ++issued;
                     dst += p.stage_bytes, bar += 8;
                     if (++slot == S) {
@@ -148,33 +131,29 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         int slot = 0, seg = 0;
         uint32_t par = 0, sf_set = 0;
         bool ok = true;
-        walk([&](int t) {
-            int c0, N, n0;
-            cols(t / p.MT, c0, N, n0);
+        walk([&](int) {
             const int buf = seg & 1;
             ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
             tc::fence_after_sync();
-            const uint32_t d = tmem + buf * p.acc, skip = (uint32_t)(c0 & (kMxRows - 1)) / 32;
+            const uint32_t d = tmem + buf * kMxgMaxN;
             const uint32_t idesc0 = mx_idesc<FMT>(N, 0), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0);
-            const bool two = N > n0;
             for (int ks = k0; ok && ks < k1; ++ks) {
                 ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    const uint32_t a = ring + slot * p.stage_bytes, b = a + REC, sb = b + p.NB * 128;
+                    const uint32_t a = ring + slot * p.stage_bytes, b = a + REC, sb = b + N * 128;
                     const uint32_t ta = tmem + sf_tm + sf_set, tb = ta + 16;
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
                         mx_copy_scales(ta + 4 * w, a + kMxCodes + 512 * w);
-                        mx_copy_scales(tb + 8 * w, sb + 512 * w);
-                        if (two) mx_copy_scales(tb + 8 * w + 4, sb + 512 * (W + w));
+                        mx_copy_scales(tb + 4 * w, sb + 512 * w);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int w = FMT == 0 ? j / 2 : j;
                         mx_mma<FMT>(d, tc::desc_sw128(a + 32 * j, 0), tc::desc_sw128(b + 32 * j, 0), j % 2 ? idesc2 : idesc0,
-                                    ta + 4 * w, tb + 8 * w + skip, (ks - k0) | j);
+                                    ta + 4 * w, tb + 4 * w, (ks - k0) | j);
                     }
                     tc::commit(b_empty + 8 * slot);
                     if (ks + 1 == k1) tc::commit(b_acc + 8 * buf);
@@ -298,43 +277,36 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         T *y = (T *)p.y;
         const T *rs = (const T *)p.r;
         walk([&](int t) {
-            const int ct = t / p.MT, row = (t - ct * p.MT) * kMxRows + rl, buf = seg & 1;
-            int c0, N, n0;
-            cols(ct, c0, N, n0);
-            const int live = row < p.n ? min(N, p.nb - c0) : 0;  // columns to write
-            const size_t at = (size_t)c0 * p.n + row;
-            // the residual of 64 columns is under way before the sums are complete, then 48
-            // columns ahead (16 at a time, loaded when they were wanted, took 521 us instead
-            // of 270 for 8192 rows of 4096 x 14336)
-            T add[4][16];
-            auto fetch = [&](int s, int c) {
+            const int row = t * kMxRows + rl, buf = seg & 1;
+            const int live = row < p.n ? p.nb : 0;  // columns to write
+            // the residual is under way before the sums are complete
+            T add[kMxgMaxN / 16][16];
+            auto fetch = [&](int s) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) add[s][i] = c + i < live ? rs[at + (size_t)(c + i) * p.n] : from_f32<T>(0.f);
+                for (int i = 0; i < 16; ++i)
+                    add[s][i] = 16 * s + i < live ? rs[row + (size_t)(16 * s + i) * p.n] : from_f32<T>(0.f);
             };
             if (rs && C == 1)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) fetch(s, 16 * s);
+                for (int s = 0; s < kMxgMaxN / 16; ++s) fetch(s);
             ok = ok && __all_sync(0xffffffffu, mbar_wait(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
             tc::fence_after_sync();
-            const uint32_t d = tmem + buf * p.acc + ((uint32_t)(32 * q) << 16);
+            const uint32_t d = tmem + buf * kMxgMaxN + ((uint32_t)(32 * q) << 16);
             if (C == 1)
-                for (int cb = 0; cb < N; cb += 64)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int c = cb + 16 * s;
-                        if (c >= N) break;
-                        uint32_t w[16];
-                        tc::ld16(d + c, w);
-                        tc::wait_ld16(w);
+                for (int s = 0; s < kMxgMaxN / 16; ++s) {
+                    const int c = 16 * s;
+                    if (c >= N) break;
+                    uint32_t w[16];
+                    tc::ld16(d + c, w);
+                    tc::wait_ld16(w);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < live) {
-                                const float v = __uint_as_float(w[i]);
-                                y[at + (size_t)(c + i) * p.n] =
-                                    from_f32<T>(rs ? fmaf(v, p.alpha, to_f32(add[s][i])) : v * p.alpha);
-                            }
-                        if (rs) fetch(s, c + 64);
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < live) {
+                            const float v = __uint_as_float(w[i]);
+                            y[row + (size_t)(c + i) * p.n] = from_f32<T>(rs ? fmaf(v, p.alpha, to_f32(add[s][i])) : v * p.alpha);
+                        }
+                }
             tc::fence_before_sync();
             __syncwarp();
             if (ok && lane == 0) bar_arrive(b_read + 8 * buf);  // (after a failure a phase could get too many)
@@ -348,10 +320,7 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         // The rings are done in all CTAs behind the first barrier: their room takes the parts.
         __syncwarp();
         cluster_sync();
-        int c0, N, n0;
-        const int t = blockIdx.x / C, ct = t / p.MT;
-        cols(ct, c0, N, n0);
-        const int per = (N + C - 1) / C, q = warp & 3, rl = 32 * q + lane, row = (t - ct * p.MT) * kMxRows + rl;
+        const int per = (N + C - 1) / C, q = warp & 3, rl = 32 * q + lane, row = blockIdx.x / C * kMxRows + rl;
         if (warp >= 2 && warp < 6) {
             const uint32_t d = tmem + ((uint32_t)(32 * q) << 16);
             for (int c = 0; c < N; c += 16) {
@@ -374,14 +343,23 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
         if (warp >= 2 && warp < 6 && row < p.n) {
             const float *part = reinterpret_cast<const float *>(sm) + rl;
             const T *rs = (const T *)p.r;
-            for (int i = 0; i < per; ++i) {
-                const int c = c0 + rank * per + i;
-                if (rank * per + i >= N || c >= p.nb) break;
-                const size_t at = (size_t)c * p.n + row;
-                const float add = rs ? to_f32(rs[at]) : 0.f;
-                float v = 0.f;
-                for (int x = 0; x < C; ++x) v += part[(x * per + i) * kMxRows];
-                ((T *)p.y)[at] = from_f32<T>(rs ? fmaf(v, p.alpha, add) : v * p.alpha);
+            const int first = rank * per, live = min(per, p.nb - first);
+            for (int i = 0; i < live; i += 4) {  // (one column at a time: up to 80 ns each)
+                const size_t at = (size_t)(first + i) * p.n + row;
+                float v[4], add[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j] = 0.f;
+                    add[j] = rs && i + j < live ? to_f32(rs[at + j * (size_t)p.n]) : 0.f;
+                }
+                for (int x = 0; x < C; ++x)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j < live) v[j] += part[(x * per + i + j) * kMxRows];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (i + j < live)
+                        ((T *)p.y)[at + j * (size_t)p.n] = from_f32<T>(rs ? fmaf(v[j], p.alpha, add[j]) : v[j] * p.alpha);
             }
         }
     }
@@ -397,47 +375,55 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
 }  // namespace dev
 
 int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
-    // The columns of a tile and the CTAs that share its k by an estimate of the
-    // busiest SM's time: a stage takes about as long as its bytes, (128 + NB) 1.4 ns
-    // (0.46 us at 192 columns), a cluster's sum about a microsecond and 10 ns a column.
-    const int W = mx_words(fmt);
+    // Up to 64 rows of x: one tile of columns, whose k a cluster may share; or pairs of CTAs
+    // (mx_pair.cu). By estimates in ns of what both took (MXFP4): a launch, its stages, the
+    // results, a cluster's sum.  (us, a cluster / pairs: 64 rows at 4096 x 4096 7.1 / 6.3, at
+    // 4096 x 14336 11.1 / 14.0, at 1024 x 14336 7.5 / 13.2.)
+    const int pairs = sms / 2;
+    p.MT = mx_rtiles(p.n);
     double best = 0.0;
-    for (const int NB : {std::min((p.nb + 15) / 16 * 16, dev::kMxgMaxN), 64, 128}) {
-        if (best > 0.0 && NB >= p.nb) break;  // the first: all rows of x in one tile, or 192
-        const int MT = mx_rtiles(p.n), CT = (p.nb + NB - 1) / NB;
-        const long long tiles = (long long)MT * CT;
-        // (two CTAs of an SM share its time, whole waves of them or not)
-        const int most = NB <= 16 ? 2 * sms : sms;
-        for (int C = 1; C <= 8 && C <= p.KS && (C == 1 || tiles * C <= most); ++C) {
-            const double waves = C > 1 && tiles * C > sms ? (double)(tiles * C) / sms : (double)((tiles * C + sms - 1) / sms);
-            const double cost = waves * ((p.KS + C - 1) / C) * (128 + NB) * 1.4 + (C > 1 ? 1000.0 + 10.0 * NB : 0.0);
+    if (p.nb <= dev::kMxgMaxN) {
+        p.NB = (p.nb + 15) / 16 * 16;
+        for (int C = 1; C <= 8 && C <= p.KS; ++C) {
+            // (Clusters have to find their SMs in one part of the GPU: of 152 SMs 15 clusters of
+            // eight ran at once, not 16, 23 of six, not 25, 32 of four.)
+            if (C > 1 && 8 * p.MT * C > (C > 4 ? 6 : 7) * sms) break;
+            const double stages = (double)((p.MT * C + sms - 1) / sms) * ((p.KS + C - 1) / C);
+            const double cost = 3000.0 + 245.0 * stages + 150.0 * std::min(stages, 4.0) +
+                                (C > 1 ? 300.0 + (22.0 + 36.0 / C) * p.NB : 8.0 * p.NB);
             if (best > 0.0 && cost >= best) continue;
             best = cost;
-            p.MT = MT;
-            p.CT = CT;
-            p.NB = NB;
             p.C = C;
         }
     }
-    // a pair of CTAs a tile of 256 x 192 (mx_pair.cu): a stage takes about (128 + N / 2) 1.05 ns
-    const int pairs = sms / 2, M2 = (mx_rtiles(p.n) + 1) / 2, CT = (p.nb + dev::kMxgMaxN - 1) / dev::kMxgMaxN;
-    const double pair_cost = (double)(((long long)M2 * CT + pairs - 1) / pairs) * p.KS * (128 + std::min(p.nb, 192) / 2) * 1.05;
-    p.pair = p.nb > 64 && pairs > 0 && pair_cost < best;
-    if (p.pair) {
-        p.MT = mx_rtiles(p.n);
-        p.CT = CT;
-        p.NB = dev::kMxgMaxN;
-        p.C = 1;
-        return 2 * (int)std::min<long long>((long long)M2 * CT, pairs);
+    if (p.nb > 16) {
+        const int N = std::min(p.nb, kMxPairN), M2 = (p.MT + 1) / 2, CT = (p.nb + kMxPairN - 1) / kMxPairN;
+        const int whole = M2 * CT, rest = whole % pairs;
+        // The tiles of an incomplete last round are cut, as long as that keeps two thirds of the
+        // pairs at most busy (us, whole / cut: 192 rows at 4096 x 14336, 16 tiles of 76 pairs, 16.3 / 14.4;
+        // 128 at 8192 x 2048, 32 tiles, 5.4 / 5.8).
+        int width = kMxPairN;
+        for (const int to : {128, 64})
+            if (3 * rest * ((N + to - 1) / to) <= 2 * pairs) width = to;
+        const int last = rest ? std::min(width, N) : N;
+        const double cost = 2500.0 + 6.0 * last + p.KS * (whole / pairs * (173 + 0.2 * N) + (rest ? 173 + 0.2 * last : 0.0));
+        if (best == 0.0 || cost < best) {
+            p.pair = 1;
+            p.NB = kMxPairN;
+            p.CT = CT;
+            p.C = 1;
+            p.whole = whole - rest;
+            p.width = width;
+            p.parts = (N + width - 1) / width;
+            p.units = p.whole + rest * p.parts;
+            return 2 * std::min(p.units, pairs);
+        }
     }
-    const int blocks = p.NB > 128 || (p.CT > 1 && p.NB % 128 != 0) ? 2 : 1;
-    p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + blocks * 512 * W + 1023) / 1024 * 1024;
-    const long long tiles = (long long)p.MT * p.CT;
-    const bool two = p.NB <= dev::kMxgSmallN && tiles * p.C > sms;  // two CTAs of an SM
+    p.stage_bytes = (mx_rec(fmt) + p.NB * 128 + 512 * mx_words(fmt) + 1023) / 1024 * 1024;
+    const bool two = p.MT * p.C > sms;  // two CTAs of an SM
     const int room = (two ? (int)kSmemMax / 2 - 1024 : (int)kSmemMax) - dev::kMxgBars;
     p.stages = std::min(dev::kMxgMaxStages, room / p.stage_bytes);
-    p.acc = p.NB <= dev::kMxgSmallN ? dev::kMxgSmallN : dev::kMxgMaxN;
-    return (int)(p.C > 1 ? tiles * p.C : std::min<long long>(tiles, two ? 2 * sms : sms));
+    return p.C > 1 ? p.MT * p.C : std::min(p.MT, two ? 2 * sms : sms);
 }
 
 bool mx_gemm_few(int nb, int dtype, bool norm, bool glu) {

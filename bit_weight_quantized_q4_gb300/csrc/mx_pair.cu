@@ -19,7 +19,7 @@ namespace q4 {
 namespace dev {
 
 constexpr int kPairThreads = 384;
-constexpr int kPairN = 192, kPairHalf = kPairN / 2;
+constexpr int kPairN = kMxPairN, kPairHalf = kPairN / 2;
 template <int FMT>
 struct PairCfg {
     static constexpr int W = mx_words(FMT), REC = mx_rec(FMT);
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     constexpr int W = Cf::W, REC = Cf::REC, S = Cf::S;
     extern __shared__ __align__(1024) uint8_t sm[];
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int rank = blockIdx.x & 1, KS = p.KS, M2 = (p.MT + 1) / 2, tiles = M2 * p.CT;
+    const int rank = blockIdx.x & 1, KS = p.KS, M2 = (p.MT + 1) / 2;
     const uint32_t ring = smem_u32(sm);
     // barriers: a stage has landed here (the first CTA's: in both), a stage's MMAs are done; of an
     // accumulator: it is complete, both CTAs have read it (the first CTA's); the last MMAs of all
@@ -103,15 +103,29 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     tc::fence_after_sync();
     const uint32_t tmem = *tslot;
 
-    // this pair's tiles: f(tile) until it says no
-    auto walk = [&](auto f) {
-        for (int t = blockIdx.x >> 1; t < tiles; t += gridDim.x >> 1)
-            if (!f(t)) return;
+    // unit u of the work: a pair of row tiles of w, the first column and how many (whole 32s).
+    // The tiles of the last, incomplete round may be cut. (A part begins at a multiple of 64
+    // columns: its scales' column in tensor memory has to be even.)
+    auto unit = [&](int u, int &mt, int &c0, int &N) {
+        int t = u, part = 0, width = kPairN;
+        if (u >= p.whole) {
+            t = p.whole + (u - p.whole) / p.parts;
+            part = (u - p.whole) % p.parts;
+            width = p.width;
+        }
+        // the larger matrix is read once, the smaller one again and again (from L2)
+        mt = M2 > p.CT ? t / p.CT : t % M2;
+        const int first = (M2 > p.CT ? t % p.CT : t / M2) * kPairN;
+        c0 = first + part * width;
+        N = min(min(width, first + kPairN - c0), (p.nb - c0 + 31) & ~31);
+        return N > 0;  // (a ragged tile's columns may end before its parts do)
     };
-    // a tile's columns: the first and how many (whole 32s); the row tile of w
-    auto cols = [&](int ct, int &c0, int &N) {
-        c0 = ct * kPairN;
-        N = min(kPairN, (p.nb - c0 + 31) & ~31);
+    // this pair's tiles: f(row tiles, first column, columns) until it says no
+    auto walk = [&](auto f) {
+        for (int u = blockIdx.x >> 1; u < p.units; u += gridDim.x >> 1) {
+            int mt, c0, N;
+            if (unit(u, mt, c0, N) && !f(mt, c0, N)) return;
+        }
     };
     const long long lim = p.wait_cycles;
 
@@ -123,9 +137,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
         if (tc::elect_one()) {
             int slot = 0, issued = 0, ahead = 0;
             uint32_t par = 1, extra = warp == 0 ? (uint32_t)p.extra_tx : 0u;  // (a wait for the phase before the first passes)
-            auto source = [&](int t) {
+            auto source = [&](int mt) {
                 // (behind an odd number of row tiles the last one again: its results are not stored)
-                return p.w + (size_t)min(2 * (t % M2) + rank, p.MT - 1) * KS * REC;
+                return p.w + (size_t)min(2 * mt + rank, p.MT - 1) * KS * REC;
             };
             // a tile's stages: one or two copies each, KS times, a record further each time
             auto stages = [&](uint32_t at, const uint8_t *src, uint32_t len, uint32_t at2, const uint8_t *src2, uint32_t len2) {
@@ -152,9 +166,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                 }
                 return true;
             };
-            if (warp == 0 && p.early && (int)blockIdx.x >> 1 < tiles) {
+            int mt0, first, N0;
+            if (warp == 0 && p.early && unit(blockIdx.x >> 1, mt0, first, N0)) {
                 // the first stages' weights before what is in front of this kernel is done
-                const uint8_t *w = source(blockIdx.x >> 1);
+                const uint8_t *w = source(mt0);
                 for (; ahead < min(S, KS); ++ahead, w += REC) {
                     mbar_expect_tx(b_full + 8 * ahead, REC + extra);
                     extra = 0;
@@ -162,10 +177,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                 }
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            walk([&](int t) {
-                if (warp == 0) return stages(0, source(t), REC, 0, nullptr, 0);
-                int c0, N;
-                cols(t / M2, c0, N);
+            walk([&](int mt, int c0, int N) {
+                if (warp == 0) return stages(0, source(mt), REC, 0, nullptr, 0);
                 const size_t step = (size_t)KS * REC;  // a row tile of x
                 if (warp == 10) {
                     const int r0 = c0 + rank * (N / 2), off = r0 & 127, n0 = min(N / 2, 128 - off);
@@ -191,23 +204,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
         if (rank == 0) {
             // (one thread for the whole loop, one barrier a stage: with a vote of the warp and a
             // barrier for each CTA's bytes a stage took 150 cycles of waits that had long passed)
-            if (tc::elect_one()) {
-                int seg = 0;
+            int seg = 0;
                 uint32_t sf_set = 0;
                 bool ok = true;
-                walk([&](int t) {
-                    int c0, N;
-                    cols(t / M2, c0, N);
+                walk([&](int, int c0, int N) {
                     const int buf = seg & 1;
-                    ok = seg < 2 || mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim);
+                    ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
                     const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
                     const bool two = (c0 & 127) + N > 128;
-                    // (M = 256 is bit 28, M = 128 bit 27)
                     const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
                     for (int ks = 0; ok && ks < KS; ++ks) {
-                        ok = mbar_wait(b_full + 8 * slot, par, lim);
+                        ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
                         if (!ok) break;
                         tc::fence_after_sync();
+                        if (tc::elect_one()) {
                         const uint32_t a = ring + slot * Cf::Stage, b = a + Cf::OffB, sb = a + Cf::OffSf;
                         const uint32_t ta = tmem + 2 * kPairN + sf_set, tb = ta + 16;
 #pragma unroll
@@ -223,18 +233,20 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                                              ta + 4 * w, tb + 8 * w + skip, ks | j);
                         }
                         commit_pair(b_empty + 8 * slot);
+                        if (ks + 1 == KS) commit_pair(b_acc + 8 * buf);
+                        }
+                        __syncwarp();
                         sf_set ^= 64;
                         next();
                     }
-                    if (ok) commit_pair(b_acc + 8 * buf);
                     ++seg;
                     return ok;
                 });
-                if (!ok) atomicExch(p.err, 4);
-                commit_pair(b_drain);
-            }
+                if (!ok && lane == 0) atomicExch(p.err, 4);
+                if (tc::elect_one()) commit_pair(b_drain);
+                __syncwarp();
         } else if (lane == 0) {
-            walk([&](int) {
+            walk([&](int, int, int) {
                 for (int ks = 0; ks < KS; ++ks, next()) {
                     if (!mbar_wait(b_full + 8 * slot, par, lim)) {
                         atomicExch(p.err, 4);
@@ -262,10 +274,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
             constexpr int CW = P2 ? 2 : 1, WIN = P2 ? kPairHalf : 64;  // columns of a V of two lanes; of the residual held
             const int odd = P2 ? lane & 1 : 0, rl = 32 * q + lane - odd;
             int seg = 0;
-            walk([&](int t) {
-                const int row = (2 * (t % M2) + rank) * kMxRows + rl, buf = seg & 1;
-                int c0, N;
-                cols(t / M2, c0, N);
+            walk([&](int mt, int c0, int N) {
+                const int row = (2 * mt + rank) * kMxRows + rl, buf = seg & 1;
                 c0 += part * (N / 2);
                 N /= 2;
                 const int live = (row < p.n ? min(N, p.nb - c0) : 0) - odd;  // columns to read and write, from this lane's first

@@ -493,6 +493,7 @@ int launch_logprobs(const LogprobParams &p, int sms, void *stream);
 // Columns from k on are zero codes with zero scales; what rows behind the last
 // hold is never used (each reaches its own results only).
 constexpr int kMxRows = 128, kMxK = 256, kMxCodes = kMxRows * kMxK / 2;
+constexpr int kMxPairN = 192;  // columns of a tile of a pair of CTAs
 Q4_HD constexpr int mx_words(int fmt) { return fmt == 0 ? 2 : 4; }
 Q4_HD constexpr int mx_block(int fmt) { return fmt == 0 ? 32 : 16; }
 Q4_HD constexpr int mx_rec(int fmt) { return kMxCodes + 512 * mx_words(fmt); }
@@ -539,10 +540,11 @@ struct MxGemmParams {
     int *err;
     long long wait_cycles;
     int extra_tx;          // bytes the first stage expects beyond its copies (0; testing only)
-    int n, nb, MT, CT, NB, KS;  // row tiles of w, column tiles of NB rows of x, column tiles of k
+    int n, nb, MT, CT, NB, KS;  // row tiles of w, column tiles (of a pair) of NB rows of x, column tiles of k
     int C;                 // CTAs (a cluster) that share a tile's k; 1: a CTA takes every grid-th tile
-    int acc, stages, stage_bytes;  // tensor-memory columns of an accumulator; the ring
-    int pair;              // a pair of CTAs a tile of 256 rows of w and 192 of x (mx_pair.cu)
+    int stages, stage_bytes;  // the ring
+    int pair;              // a pair of CTAs a tile of 256 rows of w and 192 of x (mx_pair.cu),
+    int whole, parts, width, units;  // of which so many whole, the others in parts so wide; all of these
     int early;             // w is complete before the kernel in front of this one began
     float alpha;
     MxQuantParams src;     // src.x not null: a few rows that the product quantises itself (x unused)
