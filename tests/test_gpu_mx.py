@@ -214,6 +214,26 @@ def test_product(q4, fmt, nb, n, k):
     q4.q4_device_check()
 
 
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("nb,n,k", [
+    (70, 1500, 96), (129, 333, 288), (150, 2000, 288), (193, 1000, 64), (980, 3900, 256), (1540, 2300, 288),
+    (400, 5000, 512), (2500, 1100, 160), (300, 301, 544), (2000, 1025, 288), (17, 10000, 288), (65, 20000, 32)])
+def test_product_of_whole_and_cut_tiles(q4, fmt, nb, n, k):
+    # columns that end inside a tile's part or before it, rounds that end anywhere, odd rows of results
+    for dtype, residual in ((F32, 1), (BF16, 1), (F16, None)):
+        W, X, r, ref, S = product(q4, gen(nb + n + k + fmt), fmt, nb, n, k, residual, dtype)
+        out = torch.full((nb + 2, n), 7.0, dtype=dtype, device="cuda")
+        y = out[1:-1]
+        if (n * y.element_size()) % 16 == 0:
+            q4.q4_mx_gemm(W, X, r=r, out=y)
+        else:
+            y = q4.q4_mx_gemm(W, X, r=r, dtype=dtype)
+        fine = ref.abs() < torch.finfo(dtype).max * 0.99
+        assert bool(((y.double() - ref).abs() <= bound(ref, S, k, dtype))[fine].all())
+        assert bool((out[0] == 7).all() and (out[-1] == 7).all())
+    q4.q4_device_check()
+
+
 @pytest.mark.parametrize("nb", [1, 40, 300])
 def test_product_of_whole_numbers_is_exact(q4, nb):
     # scales of one: sums of products of halves below 2^24 are fp32 numbers
