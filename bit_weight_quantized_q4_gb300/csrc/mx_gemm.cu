@@ -2,14 +2,17 @@
 // (+ r), w [n][k], x [nb][k], on the block-scaled tensor core: both operands go
 // into tcgen05.mma as they are stored, so that no weight is ever dequantised.
 //
-// w's rows are the instruction's 128 rows and x's its columns, for one token as
-// for thousands: the columns that a few tokens leave empty (16 at least) cost the
-// tensor core less time than the weights take to arrive.  A record of w is one bulk
-// copy, scales and all; x's rows and scales come by bulk copies into the same
-// stage; the scales go from shared to tensor memory (tcgen05.cp) in front of their
-// MMAs.
+// This file: up to 64 rows of x in one tile of columns (mx_pair.cu: more). w's rows are
+// the instruction's 128 rows and x's its columns, for one token too: the columns that a few
+// tokens leave empty (16 at least) cost the tensor core less time than the weights take to
+// arrive.  A record of w is one bulk copy, scales and all; x's rows and scales come by bulk
+// copies into the same stage; the scales go from shared to tensor memory (tcgen05.cp) in
+// front of their MMAs.  Few row tiles: a cluster shares k, its sums meet in shared memory.
 //   warp 0 copies, warp 1 issues MMAs, warps 2-5 write the results, while the
 //   tensor core is at the next tile (two accumulators).
+// The weights' stream bounds it: one row at 65536 x 8192 takes 42.9 us (6.7 TB/s), 64 rows
+// 47; at 14336 x 4096 one row 7.8 (4.0 TB/s: a launch, 16 stages a CTA and the first copies'
+// latency are half of it), at 4096 x 14336 8.8, at 4096 x 4096 4.8.
 // A few rows that are not quantised yet are quantised here (QX): warps 6-9 write
 // their codes and scales into the stages, while w's records arrive.
 #include <algorithm>

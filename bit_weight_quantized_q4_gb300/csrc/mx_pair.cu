@@ -8,6 +8,15 @@
 // both.  x's scales are in both CTAs, of all columns: each tensor core needs them.  (Four
 // warps of each CTA that wrote the scales to tensor memory, instead of the copies that
 // the first CTA issues for both, took 0.8 us a stage.)
+//
+// What bounds it: a stage takes 430 cycles, 355 of them MMAs; the rest are the copies of
+// the scales in front of each stage's MMAs (NVFP4 has twice as many) and stages that are not
+// there yet: an SM draws 74 bytes a cycle from L2.  The results' stores and loads come on
+// top.  8191 x 4096 x 14336 MXFP4 125 us (7.7 PFLOP/s), 8192^3 146 (7.5), NVFP4 162 (6.8);
+// 4096 x 14336 x 4096 NVFP4 81 (5.9), with a residual 92.  (Scales copied a stage ahead, or
+// two stages waited for together: a tenth slower; narrower tiles: w's records take as long
+// to arrive.)
+//
 //   warps 0, 10 and 11 copy, warp 1 issues MMAs (first CTA) or tells the first CTA of stages
 //   that have landed (second), warps 2-9 write the results (half of the columns each four).
 #include <algorithm>
@@ -202,22 +211,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
             }
         };
         if (rank == 0) {
-            // (one thread for the whole loop, one barrier a stage: with a vote of the warp and a
-            // barrier for each CTA's bytes a stage took 150 cycles of waits that had long passed)
+            // (a stage has one barrier; with one for each CTA's bytes it took 80 cycles more)
             int seg = 0;
-                uint32_t sf_set = 0;
-                bool ok = true;
-                walk([&](int, int c0, int N) {
-                    const int buf = seg & 1;
-                    ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
-                    const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
-                    const bool two = (c0 & 127) + N > 128;
-                    const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
-                    for (int ks = 0; ok && ks < KS; ++ks) {
-                        ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        if (tc::elect_one()) {
+            uint32_t sf_set = 0;
+            bool ok = true;
+            walk([&](int, int c0, int N) {
+                const int buf = seg & 1;
+                ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
+                const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
+                const bool two = (c0 & 127) + N > 128;
+                // (M = 256 is bit 28, M = 128 bit 27)
+                const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
+                for (int ks = 0; ok && ks < KS; ++ks) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
                         const uint32_t a = ring + slot * Cf::Stage, b = a + Cf::OffB, sb = a + Cf::OffSf;
                         const uint32_t ta = tmem + 2 * kPairN + sf_set, tb = ta + 16;
 #pragma unroll
@@ -234,17 +243,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                         }
                         commit_pair(b_empty + 8 * slot);
                         if (ks + 1 == KS) commit_pair(b_acc + 8 * buf);
-                        }
-                        __syncwarp();
-                        sf_set ^= 64;
-                        next();
                     }
-                    ++seg;
-                    return ok;
-                });
-                if (!ok && lane == 0) atomicExch(p.err, 4);
-                if (tc::elect_one()) commit_pair(b_drain);
-                __syncwarp();
+                    __syncwarp();
+                    sf_set ^= 64;
+                    next();
+                }
+                ++seg;
+                return ok;
+            });
+            if (!ok && lane == 0) atomicExch(p.err, 4);
+            if (tc::elect_one()) commit_pair(b_drain);
+            __syncwarp();
         } else if (lane == 0) {
             walk([&](int, int, int) {
                 for (int ks = 0; ks < KS; ++ks, next()) {
