@@ -8,9 +8,9 @@
 // core an instruction takes 16 columns at least, so every expert sees all tokens
 // of the batch, and only a token's own experts' columns are used: nothing is
 // gathered.
-//   One token, 8 of 128 experts of 768 x 2048: 19 us for 21 MB (floor 3.1); sixteen: 52 for
-// 208 MB (30.7); four tokens, 2 of 8 experts of 14336 x 4096: 87 for 0.49 GB (72.5); sixteen: 122
-// (107, 0.87 of the copy rate).  The fixed part is a chain of latencies: the logits' kernel 4 us, the
+//   One token, 8 of 128 experts of 768 x 2048: 16.2 us for 21 MB (floor 3.1); sixteen: 49 for
+// 208 MB (30.7); four tokens, 2 of 8 experts of 14336 x 4096: 81 for 0.49 GB (72.5); sixteen:
+// 121.5 (107).  The fixed part is a chain of latencies: the logits' kernel 4 us, the
 // choice 2.4, the grid's barrier 1.2, the first copies of each half, joining 2.
 #include <algorithm>
 
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(NT == 1 ? 256 : 1024) q4moe_route_kernel(const
 // ------------------------------------------------------------------ experts
 
 constexpr int kMoeThreads = 32 * kMaxNb;  // a warp a token to choose the experts; then six have roles
-constexpr int kMoeStages = 9;
+constexpr int kMoeStages = 6;  // (what waits in more of them only delays what is wanted first: nine took 1 to 3 % longer)
 constexpr int kMoeStage = mx_rec(0) + kMoeRec;  // a record of weights, one of activations
 constexpr int kMoeExch = 2 * 2 * 2 * 8 * 32 * 4;  // [turn][pair of warps][gate or up][token][row]
 // what the choice of the experts leaves: the experts with a token in rising order,
@@ -188,7 +188,7 @@ static_assert(kMoeStage % 1024 == 0 && kMoeSmem <= (int)kSmemMax, "shared memory
 constexpr int kMoeOffChosen = 0, kMoeOffChosenW = kMoeOffChosen + 4 * kMoeMaxActive, kMoeOffTok = kMoeOffChosenW + 4 * kMoeMaxActive,
               kMoeOffSlot = kMoeOffTok + 4 * kMoeMaxExperts;
 static_assert(kMoeOffSlot + 4 * kMoeMaxExperts <= kMoeOffExch, "the ring's room");
-constexpr int kMoeParts = 10;  // CTAs that share a tile of outputs, about
+constexpr int kMoeParts = 8;  // CTAs that share a tile of outputs, about (one token of 128 experts 16.2 us; 10: 17.5, 5: 16.7)
 
 // Order of logits: larger first, NaN (1) behind every number (-inf: 0x7FFFFF).
 __device__ __forceinline__ uint32_t logit_key(float v) {
