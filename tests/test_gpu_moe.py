@@ -270,3 +270,23 @@ def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_unchanged(q4, kw)
         q4.q4_debug_wait_limits()
     assert torch.equal(q4.q4_moe(s["x"], s["layer"], gamma=s["gamma"])[0], y0)
     q4.q4_device_check()
+
+
+def test_weights_beyond_32_bits(q4):
+    # 72 experts of 4096 x 14336: 4.5 GB of gate and up; tokens that choose the last eight, against a layer of those alone
+    E, hidden, inter = 72, 4096, 14336
+    g = torch.Generator(device="cuda").manual_seed(7)
+    mats = []
+    for n, k in ((inter, hidden), (inter, hidden), (hidden, inter)):
+        m = q4.MXMatrix(0, n, k, batch=E)
+        m.tensor.random_(100, 118, generator=g)
+        mats.append(m)
+    assert 2 * mats[0].nbytes > 1 << 32
+    router = torch.zeros(E, hidden, device="cuda")
+    router[64:] = torch.randint(1, 5, (8, hidden), generator=g, device="cuda").float() / 64
+    x = torch.randint(1, 4, (3, hidden), generator=g, device="cuda").to(BF16)
+    few = [q4.MXMatrix(0, m.rows, m.k, batch=8, tensor=m.tensor[m.nbytes // E * 64:]) for m in mats]
+    out, idx, w = q4.q4_moe(x, q4.MoELayer(router, *mats, top_k=2))
+    want, widx, ww = q4.q4_moe(x, q4.MoELayer(router[64:].contiguous(), *few, top_k=2))
+    assert torch.equal(idx, widx + 64) and torch.equal(w, ww) and torch.equal(out, want) and bool(out.abs().max() > 0)
+    q4.q4_device_check()

@@ -399,3 +399,57 @@ def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_unchanged(q4, nb,
         q4.q4_debug_wait_limits()
     assert torch.equal(q4.q4_mx_gemm(W, X), y0)
     q4.q4_device_check()
+
+
+def test_offsets_beyond_32_bits(q4):
+    # 2.4e9 values of x and of y, 4.8 GB of records: the last rows against those of a small matrix of the same bytes
+    k = 65536
+    x = torch.empty(37000, k, dtype=BF16, device="cuda").random_(-8, 9)
+    for fmt in (0, 1):
+        m = q4.q4_mx_quant(x, fmt)
+        first = 37000 // 128 * 128
+        part = q4.q4_mx_quant(x[first:], fmt)
+        used = part.nbytes
+        assert torch.equal(q4.q4_mx_dequant(part, BF16), q4.q4_mx_dequant(m, BF16)[first:])
+        gamma = torch.ones(k, device="cuda")
+        behind = q4.q4_mx_quant(x, fmt, gamma=gamma, eps=1e-6)
+        assert torch.equal(q4.q4_mx_dequant(behind, BF16)[first:],
+                           q4.q4_mx_dequant(q4.q4_mx_quant(x[first:], fmt, gamma=gamma, eps=1e-6), BF16))
+        assert used < m.nbytes
+    del x, m, part, behind
+    W = q4.MXMatrix(0, 140000, k)
+    W.tensor.random_(0, 118)
+    last = 140000 // 128
+    w = q4.MXMatrix(0, 140000 - 128 * last, k, tensor=W.tensor[last * 256 * 17408:])
+    for nb in (1, 50, 90):
+        X = q4.MXMatrix(0, nb, k)
+        X.tensor.random_(0, 118)
+        # (the small matrix's k may be shared by more CTAs: against 64 bits)
+        w64, x64 = mx_ref.stored(*w.codes(), 0), mx_ref.stored(*X.codes(), 0)
+        ref, S = x64 @ w64.T, x64.abs() @ w64.abs().T
+        for y in (q4.q4_mx_gemm(W, X)[:, 128 * last:], q4.q4_mx_gemm(w, X)):
+            assert bool(((y.double() - ref).abs() <= bound(ref, S, k, F32)).all())
+    del W, w
+    W, X = q4.MXMatrix(0, 8192, 64), q4.MXMatrix(0, 300000, 64)
+    W.tensor.random_(0, 118), X.tensor.random_(0, 118)
+    first = 300000 // 128
+    tail = q4.MXMatrix(0, 300000 - 128 * first, 64, tensor=X.tensor[first * 17408:])
+    r = torch.zeros(300000, 8192, dtype=F16, device="cuda")
+    y = q4.q4_mx_gemm(W, X, r=r, dtype=F16)
+    assert torch.equal(y[128 * first:], q4.q4_mx_gemm(W, tail, dtype=F16))
+    q4.q4_device_check()
+
+
+@pytest.mark.parametrize("nb", [1, 8, 9, 70])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_float_rows_onto_the_residual_in_place(q4, nb, dtype):
+    g = gen(12)
+    W, x, r = q4.q4_mx_quant(randn(g, 512, 288)), randn(g, nb, 288).to(dtype), randn(g, nb, 512).to(dtype)
+    want = q4.q4_mx_gemm(W, x, r=r)
+    out = r.clone()
+    assert q4.q4_mx_gemm(W, x, r=out, out=out) is out and torch.equal(out, want)
+    # the result of one product as the rows of the next, without anything in between
+    V = q4.q4_mx_quant(randn(g, 288, 512))
+    for _ in range(5):
+        assert torch.equal(q4.q4_mx_gemm(V, q4.q4_mx_gemm(W, x, r=r)), q4.q4_mx_gemm(V, want))
+    q4.q4_device_check()
