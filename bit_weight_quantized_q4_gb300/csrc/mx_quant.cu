@@ -3,9 +3,9 @@
 // dequantising; codes and scales from and into plain rows.
 //
 // Pure streams: HBM bounds the float forms, the arithmetic of scales and codes the 16-bit
-// ones (issue slots 67 % busy behind a norm).  14336 x 4096 float 38.7 us (6.9 TB/s), bf16
-// 25.6 (5.7); 8191 x 4096 bf16 behind a norm 22.1 (3.8); 8191 x 14336 fp16 SwiGLU 83.7 (6.4);
-// back into bf16, 14336 x 4096, 24.3 (6.1).
+// ones.  14336 x 4096 float 39.7 us (6.7 TB/s), bf16 26.2 (5.6); 8191 x 4096 bf16 behind a
+// norm 19.1 (4.5); 8191 x 14336 fp16 SwiGLU 82.9 (6.4); back into bf16, 14336 x 4096, 24.3
+// (6.1).
 // A lane takes sixteen consecutive values, half a record row a half warp: a block of 32
 // (16) is two lanes (one), a row's codes of a record one whole 128-byte line.  (Eight values
 // a lane: half the time of the 16-bit forms was the arithmetic of scales and addresses.)
@@ -48,14 +48,11 @@ struct MxUnit {
 
 // Values as they are, or a SwiGLU of two rows: a warp takes AH units, their loads
 // issued together.
-template <typename T, bool GLU>
-constexpr int mx_ahead() { return sizeof(T) == 4 || GLU ? 2 : 4; }
-template <typename T, int FMT, bool GLU>
+template <typename T, int FMT, bool GLU, int AH>
 __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_constant__ MxQuantParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // after the wait: a kernel that starts on this may read what was complete before
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int AH = mx_ahead<T, GLU>();
     const int lane = threadIdx.x & 31, half = lane >> 4, KT = mx_ktiles(p.k), rows = p.batch * p.rows;
     const long long mat = (long long)mx_rtiles(p.rows) * KT * mx_rec(FMT);
     const MxUnit first((((long long)blockIdx.x * kMxWarps + (threadIdx.x >> 5)) * AH), KT);
@@ -93,8 +90,9 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_con
 // registers (what a longer row has beyond is read again once its sum of squares is
 // known).  As many CTAs as are resident take every grid-th rows each, the loads of the
 // next DP rows under way.  Its arithmetic bounds it, not the memory: 8191 x 4096 bf16
-// takes 21 us with three CTAs of an SM and two rows under way (a CTA a row: 30; more
-// CTAs than are resident: 25; four, whose registers spill: 26).
+// takes 19 us with four warps a row and two CTAs of an SM (three, whose registers spill:
+// 25); with eight, three CTAs and two rows under way 21.5 (a CTA a row: 30; more CTAs than
+// are resident: 25; four, which spill: 26).
 template <int R>
 constexpr int mx_norm_ctas() { return R == 1 ? 3 : 2; }
 template <typename T, int FMT, int WPR, int R>
@@ -302,19 +300,37 @@ int launch_mx_norm(const MxQuantParams &p, int sms, cudaStream_t stream) {
     const long long ctas = ((long long)p.batch * p.rows * WPR + dev::kMxWarps - 1) / dev::kMxWarps;
     return mx_launch(dev::q4mx_quant_norm_kernel<T, FMT, WPR, R>, (unsigned)std::min<long long>(ctas, (long long)dev::mx_norm_ctas<R>() * sms), p, stream);
 }
+template <typename T, int FMT, bool GLU>
+int launch_mx_values(const MxQuantParams &p, int sms, cudaStream_t stream) {
+    // 16-bit types: two units a warp once there are many (us, one / two: 16 x 4096 bf16 1.5 / 1.9,
+    // 8191 x 14336 53.5 / 48.9, SwiGLU 86 / 83); float has as many bytes under way with one
+    const long long units = mx_pairs(p.batch, p.rows, p.k);
+    if constexpr (sizeof(T) == 2)
+        if (units > 64 * sms) return mx_launch(dev::q4mx_quant_kernel<T, FMT, GLU, 2>, mx_grid(units, 2), p, stream);
+    return mx_launch(dev::q4mx_quant_kernel<T, FMT, GLU, 1>, mx_grid(units, 1), p, stream);
+}
 template <typename T, int FMT>
 int launch_mx_quant_t(const MxQuantParams &p, int sms, cudaStream_t stream) {
     if (p.gamma) {
-        // as many warps a row as it has 512s, up to eight
+        // as many warps a row as it has 512s, up to eight; from about a round of the SMs on and for
+        // 16-bit types half as many, of whose work a row's sum is a smaller part (us, 4096 columns of
+        // bf16, eight warps / four: 152 rows 2.3 / 2.6, 304 3.0 / 2.8, 8191 21.5 / 19.1; float
+        // 26.0 / 26.6)
         if (p.k <= 512) return launch_mx_norm<T, FMT, 1, 1>(p, sms, stream);
+        if constexpr (sizeof(T) == 2) {
+            if ((long long)p.batch * p.rows * p.k >= 1 << 20) {
+                if (p.k <= 1024) return launch_mx_norm<T, FMT, 1, 2>(p, sms, stream);
+                if (p.k <= 2048) return launch_mx_norm<T, FMT, 2, 2>(p, sms, stream);
+                if (p.k <= 4096) return launch_mx_norm<T, FMT, 4, 2>(p, sms, stream);
+            }
+        }
         if (p.k <= 1024) return launch_mx_norm<T, FMT, 2, 1>(p, sms, stream);
         if (p.k <= 2048) return launch_mx_norm<T, FMT, 4, 1>(p, sms, stream);
         if (p.k <= 4096) return launch_mx_norm<T, FMT, 8, 1>(p, sms, stream);
         return launch_mx_norm<T, FMT, 8, 2>(p, sms, stream);
     }
-    const long long units = mx_pairs(p.batch, p.rows, p.k);
-    if (p.up) return mx_launch(dev::q4mx_quant_kernel<T, FMT, true>, mx_grid(units, dev::mx_ahead<T, true>()), p, stream);
-    return mx_launch(dev::q4mx_quant_kernel<T, FMT, false>, mx_grid(units, dev::mx_ahead<T, false>()), p, stream);
+    if (p.up) return launch_mx_values<T, FMT, true>(p, sms, stream);
+    return launch_mx_values<T, FMT, false>(p, sms, stream);
 }
 }  // namespace
 
