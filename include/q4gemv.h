@@ -589,7 +589,9 @@ typedef struct {
  * nearest E4M3 value (6 scale and the quotient in fp32).  A value becomes the
  * nearest code of x / s, or of x * (1 / (s scale)) with both steps in fp32 (ties
  * to the even code, at most 6 in magnitude; a scale of 0: zeros).  A block with a
- * NaN or an infinity gets the NaN scale: it reads back, and multiplies, as NaN. */
+ * NaN or an infinity gets the NaN scale: it reads back, and multiplies, as NaN.
+ * Behind a norm a value next to a border of codes may depend on the number of rows
+ * (the order of a row's sum does). */
 q4_status q4_mx_quant(const q4_mx_src *src, const q4_mx *out, cudaStream_t stream);
 
 /* The values of m, [batch][rows][k] of dtype (rounded once to it). */
@@ -604,7 +606,8 @@ q4_status q4_mx_unpack(const q4_mx *m, uint8_t *codes, uint8_t *scales, cudaStre
 /* y[t][i] = sum_k w[i][k] x[t][k] (+ r[t][i]) of the stored values, fp32 sums
  * rounded once to y's type: W [n][k], X [nb][k] of the same format (batch 1 each),
  * y and r [nb][n] of dtype, r NULL or, in place, y itself; else y must not overlap
- * an input.  Any nb from 1 to 2^20.  Results do not depend on scheduling. */
+ * an input.  Any nb from 1 to 2^20.  Results do not depend on scheduling; a row's last
+ * bits may depend on nb (k is split by the number of rows). */
 q4_status q4_mx_gemm(const q4_mx *W, const q4_mx *X, const void *r, int32_t dtype, void *y, cudaStream_t stream);
 
 /* q4_mx_quant of src into X (W's format, src's rows; the caller's room), then

@@ -99,6 +99,14 @@ def test_layer(q4, rows, E, top_k, hidden, inter, renormalize):
     q4.q4_device_check()
 
 
+@pytest.mark.parametrize("rows,E,top_k,hidden,inter", [(2, 2, 1, 65536, 64), (1, 3, 2, 32, 65536), (16, 16, 16, 32, 32), (16, 1024, 16, 64, 32)])
+def test_layer_at_its_limits(q4, rows, E, top_k, hidden, inter):
+    s = draw(q4, rows + E, rows, E, top_k, hidden, inter)
+    r = torch.randn(rows, hidden, generator=s["g"], device="cuda").to(BF16)
+    check(q4.q4_moe(s["x"], s["layer"], gamma=s["gamma"], r=r), reference(s), r, BF16)
+    q4.q4_device_check()
+
+
 def test_other_output_types_and_places(q4):
     s = draw(q4, 1, 5, 8, 2, 256, 96)
     want = reference(s)
