@@ -1191,7 +1191,9 @@ def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
     shape = ((m.batch,) if m.batch > 1 else ()) + (m.rows, m.k)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=m.device)
-    op = _ptr(out, "out", dtype, shape, m.device)
+        op = out.data_ptr()
+    else:
+        op = _ptr(out, "out", dtype, shape, m.device)
     _check(_launch(m.device, lib().q4_mx_dequant, m._ref, kind, op), "q4_mx_dequant")
     return out
 
