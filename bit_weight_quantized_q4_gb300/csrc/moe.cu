@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     if (warp == 1) {
         tc::tmem_alloc(smem_u32(tslot), 128);
         tc::tmem_relinquish();
+        // after the allocation: a kernel that starts on this could hold the columns this one waits for
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int *chosen = reinterpret_cast<int *>(sm + kMoeOffChosen);
     float *chosen_w = reinterpret_cast<float *>(sm + kMoeOffChosenW);
     unsigned *tokens = reinterpret_cast<unsigned *>(sm + kMoeOffTok);

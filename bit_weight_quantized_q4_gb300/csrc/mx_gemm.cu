@@ -57,8 +57,9 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
     if (warp == 1) {
         tc::tmem_alloc(smem_u32(tslot), cols_tm);
         tc::tmem_relinquish();
+        // after the allocation: a kernel that starts on this could hold the columns this one waits for
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

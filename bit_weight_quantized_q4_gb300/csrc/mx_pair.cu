@@ -104,8 +104,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tslot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        // after the allocation: a kernel that starts on this could hold the columns this one waits for
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     cluster_sync();  // the barriers of both CTAs
