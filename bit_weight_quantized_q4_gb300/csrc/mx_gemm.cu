@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kMxgThreads + (QX ? kMxgQuant : 0), 2)
                     uint2 code[P];
                     uint32_t word[P];
 #pragma unroll
-                    for (int q = 0; q < P; ++q) mx_codes<FMT>(v[q], 1.f, gain, code[q], word[q]);
+                    for (int q = 0; q < P; ++q) mx_codes<FMT>(v[q], gain, code[q], word[q]);
                     uint8_t *rec = sm + slot * p.stage_bytes + REC;  // 16 rows of codes, then the scales
                     constexpr int L = 4 * mx_block(FMT) / 16;        // lanes of a word
 #pragma unroll

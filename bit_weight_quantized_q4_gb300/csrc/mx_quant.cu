@@ -18,14 +18,14 @@ namespace dev {
 
 constexpr int kMxThreads = 256, kMxWarps = kMxThreads / 32;
 
-// The sixteen values v f from column c of row `row` into the matrix at `out`; all
+// The sixteen values v from column c of row `row` into the matrix at `out`; all
 // lanes of a warp, those of a row of a record (16 of them) in order.
 template <int FMT>
-__device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const uint64_t (&v)[8], float f,
+__device__ __forceinline__ void mx_store(uint8_t *out, bool live, int row, int c, int KT, const uint64_t (&v)[8],
                                          const MxGain &gain) {
     uint2 code;
     uint32_t word;
-    mx_codes<FMT>(v, f, gain, code, word);
+    mx_codes<FMT>(v, gain, code, word);
     if (!live) return;
     constexpr int L = 4 * mx_block(FMT) / 16;  // lanes of a word
     const int r = row % kMxRows, h = (c % kMxK) / 16;  // h: which sixteen of the record's row
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_con
             mx_glu(v, w);
         }
         const int row = 2 * u.pair + half, b = p.batch == 1 ? 0 : row / p.rows;
-        mx_store<FMT>(p.out + b * mat, row < rows, row - b * p.rows, u.kt * kMxK + 16 * (lane & 15), KT, v, 1.f, gain);
+        mx_store<FMT>(p.out + b * mat, row < rows, row - b * p.rows, u.kt * kMxK + 16 * (lane & 15), KT, v, gain);
     }
 }
 
@@ -156,10 +156,12 @@ __global__ void __launch_bounds__(kMxThreads, mx_norm_ctas<R>()) q4mx_quant_norm
         auto put = [&](const Raw16<T> &a, const uint64_t (&gv)[8], int c) {
             uint64_t v[8];
             a.pairs(v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = mul_f32x2(v[e], gv[e]);
             // (columns behind k are zeros even where rstd is infinite or NaN)
-            mx_store<FMT>(p.out + b * mat, live && c < kpad, row - b * p.rows, c, KT, v, c < p.k ? rstd : 1.f, gain);
+            const float f = c < p.k ? rstd : 1.f;
+            const uint64_t by = pair_f32(f, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = mul_f32x2(mul_f32x2(v[e], by), gv[e]);
+            mx_store<FMT>(p.out + b * mat, live && c < kpad, row - b * p.rows, c, KT, v, gain);
         };
 #pragma unroll
         for (int i = 0; i < R; ++i)

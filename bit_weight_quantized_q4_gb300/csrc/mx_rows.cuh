@@ -56,10 +56,12 @@ __device__ __forceinline__ void mx_factors(uint64_t (&v)[8], const float *src) {
 // 1 / sqrt(mean of squares + eps) of a row, from its sum (inv_k = 1 / k).
 __device__ __forceinline__ float mx_rstd(float sum, float inv_k, float eps) { return rsqrtf(fmaf(sum, inv_k, eps)); }
 
-// The codes of the sixteen values v f of each lane, and in the first lane of four
-// blocks their scales' word; all lanes of a warp, those of a row in order.
+// The codes of the sixteen values v of each lane, and in the first lane of four
+// blocks their scales' word; all lanes of a warp, those of a row in order.  (A row's
+// factor is in v already: its product with a block's, 2^127 for a block of zeros, may
+// be infinite.)
 template <int FMT>
-__device__ __forceinline__ void mx_codes(const uint64_t (&v)[8], float f, const MxGain &gain, uint2 &code, uint32_t &word) {
+__device__ __forceinline__ void mx_codes(const uint64_t (&v)[8], const MxGain &gain, uint2 &code, uint32_t &word) {
     float m[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = max_abs(lo_f32(v[i]), hi_f32(v[i]));
@@ -68,8 +70,8 @@ __device__ __forceinline__ void mx_codes(const uint64_t (&v)[8], float f, const 
     float a = max_abs(max_abs(m[0], m[1]), max_abs(m[2], m[3]));
     if constexpr (FMT == 0) a = max_abs(a, __shfl_xor_sync(0xffffffffu, a, 1));
     float mul;
-    const uint32_t sc = mx_block_scale<FMT>(a * f, gain, mul);
-    const uint64_t by = pair_f32(f * mul, f * mul);
+    const uint32_t sc = mx_block_scale<FMT>(a, gain, mul);
+    const uint64_t by = pair_f32(mul, mul);
     uint64_t u[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) u[i] = mul_f32x2(v[i], by);
