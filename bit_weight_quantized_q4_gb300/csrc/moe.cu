@@ -251,6 +251,17 @@ __device__ __forceinline__ void moe_choose(const float *logits, int E, int top_k
     }
 }
 
+// Named barrier `bar` of n threads (whole warps): whether `v` holds in all of them.
+__device__ __forceinline__ bool bar_all(int bar, int n, bool v) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(bar), "r"(n), "r"((uint32_t)v)
+        : "memory");
+    return all != 0;
+}
+
 // Every CTA chooses the experts by itself (the logits are a few kilobytes), then two
 // halves in one kernel: first every (expert with a token, 64 rows of gate and of up)
 // unit, the next one to the CTA that is free first; then, behind a barrier of the grid, the down projections,
@@ -564,15 +575,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
         for (int count = 0; more; ++count) {
             float v[16];
             take(v);
+            float *buf = exch + (seg & 1) * 1024;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) buf[(up * 8 + i) * 32 + lane] = up ? v[i] : v[8 + i];
+            // (one warp's wait may give up just before the other's passes: both leave, or none)
+            ok = bar_all(2 + pair, 64, ok);
             if (!ok) break;
             const int u = unit_s[count & 15];
             more = more_s[count & 15] != 0;
             const int a = u / T1, tile = u - a * T1, blk = 2 * tile + pair;
             const unsigned mask = masks[a];
-            float *buf = exch + (seg & 1) * 1024;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) buf[(up * 8 + i) * 32 + lane] = up ? v[i] : v[8 + i];
-            asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
             const bool in = blk * 32 < p.inter;
             uint8_t *rec = p.h + ((size_t)a * KS2 + blk / 8) * kMoeRec;
             // this block, and behind the last one the rest of its record as zeros
