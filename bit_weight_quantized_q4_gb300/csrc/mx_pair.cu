@@ -38,12 +38,39 @@ struct PairCfg {
     static_assert(Stage % 1024 == 0 && Smem <= (int)kSmemMax, "shared memory of a pair's CTA");
 };
 
-// An arrival on the first CTA's barrier at this offset.
+// An arrival on the first CTA's barrier at this offset, and a wait for arrivals that may be
+// the other CTA's: both of cluster scope (they are of their own CTA's where they do not say
+// more).  The arrival is relaxed.  It tells of two things, neither of them a store of its
+// thread that a release would have to make visible:
+//  - a stage's bytes in the second CTA's shared memory.  They came by bulk copies, whose
+//    completion the telling thread has waited for, and there is no other copy of that memory
+//    that the second SM's tensor core could read;
+//  - an accumulator that has been read: tcgen05.ld, complete by tcgen05.wait::ld, in front of
+//    tcgen05.fence::before_thread_sync, which orders it before the arrival, as
+//    fence::after_thread_sync orders the MMAs behind the wait.
+// (With a release at cluster scope for every stage 8191 x 4096 x 14336 took 492 us, not 126.)
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar)
         : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, long long limit) {
+    long long t0 = 0;
+    for (int it = 0;; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{ .reg .pred P; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2; selp.b32 %0, 1, 0, P; }"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if (it == 0) {
+            t0 = clock64();
+        } else if (clock64() - t0 > limit) {
+            return false;
+        }
+    }
 }
 __device__ __forceinline__ void commit_pair(uint32_t bar) {
     asm volatile(
@@ -158,7 +185,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                     if (ahead > 0) {
                         --ahead;
                     } else {
-                        if (!mbar_wait(b_empty + 8 * slot, par, lim)) {
+                        if (!mbar_wait_pair(b_empty + 8 * slot, par, lim)) {
                             atomicExch(p.err, 4);
                             return false;
                         }
@@ -218,13 +245,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
             bool ok = true;
             walk([&](int, int c0, int N) {
                 const int buf = seg & 1;
-                ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
+                ok = seg < 2 || __all_sync(0xffffffffu, mbar_wait_pair(b_read + 8 * buf, (uint32_t)(seg / 2 - 1) & 1u, lim));
                 const uint32_t d = tmem + buf * kPairN, skip = (uint32_t)(c0 & 127) / 32;
                 const bool two = (c0 & 127) + N > 128;
                 // (M = 256 is bit 28, M = 128 bit 27)
                 const uint32_t idesc0 = mx_idesc<FMT>(N, 0) + (1u << 27), idesc2 = mx_idesc<FMT>(N, FMT == 0 ? 2 : 0) + (1u << 27);
                 for (int ks = 0; ok && ks < KS; ++ks) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(b_full + 8 * slot, par, lim));
+                    ok = __all_sync(0xffffffffu, mbar_wait_pair(b_full + 8 * slot, par, lim));
                     if (!ok) break;
                     tc::fence_after_sync();
                     if (tc::elect_one()) {
@@ -268,7 +295,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
             });
         }
         __syncwarp();
-        mbar_wait(b_drain, 0u, kWaitCycles);
+        mbar_wait_pair(b_drain, 0u, kWaitCycles);
     } else {
         // ------------------------------------------------------------ results
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -304,7 +331,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) q4mx_pair_kernel(const __grid
                 if (p.r)
 #pragma unroll
                     for (int c = 0; c < WIN; c += 16) fetch(c);
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_pair(b_acc + 8 * buf, (uint32_t)(seg / 2) & 1u, lim));
                 tc::fence_after_sync();
                 const uint32_t d = tmem + buf * kPairN + part * N + ((uint32_t)(32 * q) << 16);
 #pragma unroll
