@@ -1165,18 +1165,22 @@ def _mx_src(x, gamma, eps, up):
     return _CMxSrc(x.data_ptr(), up_p, gamma_p, ld, kind, rows, k, eps)
 
 
-def q4_mx_quant(x, fmt: int = Q4_MX_MXFP4, gamma=None, eps: float = 0.0, up=None, scale: float = 1.0, out=None):
+def q4_mx_quant(x, fmt: int | None = None, gamma=None, eps: float = 0.0, up=None, scale: float | None = None, out=None):
     """``x`` (float32, float16 or bfloat16, ``[rows, k]`` or ``[batch, rows, k]``) as an ``MXMatrix``: as it is,
     behind an RMSNorm (``gamma [k]`` float32, ``eps``), or behind a SwiGLU (silu(x) * ``up``).  Rows may be a view
-    (the halves of one projection's output).  ``scale``: NVFP4's factor of the whole matrix, such as
-    amax / (6 * 448).  ``out``: an MXMatrix of the same shape to write into (its scale holds)."""
+    (the halves of one projection's output).  ``fmt``: MXFP4 by default; ``scale``: NVFP4's factor of the whole matrix,
+    such as amax / (6 * 448), 1 by default.  ``out``: an MXMatrix of the same shape to write into, whose format and scale
+    hold (``fmt`` and ``scale``, where given, must be its own)."""
     src = _mx_src(x, gamma, eps, up)
     batch = x.shape[0] if x.dim() == 3 else 1
     rows, k = src.rows // batch, src.k
     if out is None:
-        out = MXMatrix(fmt, rows, k, batch, scale, x.device)
-    elif (_mx(out, "out").rows, out.k, out.batch, out.device) != (rows, k, batch, x.device):
-        raise ValueError("out has another shape or device than x")
+        out = MXMatrix(Q4_MX_MXFP4 if fmt is None else fmt, rows, k, batch, 1.0 if scale is None else scale, x.device)
+    else:
+        if (_mx(out, "out").rows, out.k, out.batch, out.device) != (rows, k, batch, x.device):
+            raise ValueError("out has another shape or device than x")
+        if fmt not in (None, out.fmt) or scale not in (None, out.scale):
+            raise ValueError("out has another format or scale: fmt=%s scale=%s" % (out.fmt, out.scale))
     _check(_launch(out.device, lib().q4_mx_quant, ctypes.byref(src), out._ref), "q4_mx_quant")
     return out
 

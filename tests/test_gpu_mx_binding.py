@@ -1,0 +1,37 @@
+"""What the Python calls of the microscaled matrices and of the mixture-of-experts layer take and refuse."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import bit_weight_quantized_q4_gb300 as m
+    m.build()
+    m.lib()
+    return m
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def test_a_given_matrix_keeps_its_format_and_factor(q4):
+    x = randn(1, 5, 96)
+    nv, mx = q4.MXMatrix(q4.Q4_MX_NVFP4, 5, 96, scale=0.5), q4.MXMatrix(q4.Q4_MX_MXFP4, 5, 96)
+    # without a word on them they are the matrix's; the same words are fine
+    want = q4.q4_mx_quant(x, q4.Q4_MX_NVFP4, scale=0.5).codes()
+    for kw in ({}, {"fmt": q4.Q4_MX_NVFP4}, {"scale": 0.5}, {"fmt": q4.Q4_MX_NVFP4, "scale": 0.5}):
+        assert q4.q4_mx_quant(x, out=nv, **kw) is nv
+        assert all(torch.equal(a, b) for a, b in zip(nv.codes(), want))
+    assert q4.q4_mx_quant(x, out=mx) is mx and torch.equal(mx.codes()[0], q4.q4_mx_quant(x).codes()[0])
+    # other ones are refused, not passed over
+    before = [t.clone() for t in nv.codes()]
+    for m, kw in ((mx, {"fmt": q4.Q4_MX_NVFP4}), (mx, {"fmt": q4.Q4_MX_NVFP4, "scale": 0.5}), (nv, {"fmt": q4.Q4_MX_MXFP4}),
+                  (nv, {"scale": 0.25}), (nv, {"fmt": q4.Q4_MX_NVFP4, "scale": 1.0}), (mx, {"scale": 2.0})):
+        with pytest.raises(ValueError):
+            q4.q4_mx_quant(2 * x, out=m, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(nv.codes(), before))
+    q4.q4_device_check()
