@@ -1170,7 +1170,7 @@ def q4_mx_quant(x, fmt: int | None = None, gamma=None, eps: float = 0.0, up=None
     behind an RMSNorm (``gamma [k]`` float32, ``eps``), or behind a SwiGLU (silu(x) * ``up``).  Rows may be a view
     (the halves of one projection's output).  ``fmt``: MXFP4 by default; ``scale``: NVFP4's factor of the whole matrix,
     such as amax / (6 * 448), 1 by default.  ``out``: an MXMatrix of the same shape to write into, whose format and scale
-    hold (``fmt`` and ``scale``, where given, must be its own)."""
+    hold (``fmt`` and ``scale``, where given, must be its own), apart from x, up and gamma."""
     src = _mx_src(x, gamma, eps, up)
     batch = x.shape[0] if x.dim() == 3 else 1
     rows, k = src.rows // batch, src.k
@@ -1181,12 +1181,16 @@ def q4_mx_quant(x, fmt: int | None = None, gamma=None, eps: float = 0.0, up=None
             raise ValueError("out has another shape or device than x")
         if fmt not in (None, out.fmt) or scale not in (None, out.scale):
             raise ValueError("out has another format or scale: fmt=%s scale=%s" % (out.fmt, out.scale))
+        span = ((src.rows - 1) * src.ld + k) * x.element_size()
+        apart = [(src.x, span)] + ([(src.up, span)] if up is not None else []) + ([(src.gamma, 4 * k)] if gamma is not None else [])
+        _apart(out._c.dev, out.nbytes, *apart)
     _check(_launch(out.device, lib().q4_mx_quant, ctypes.byref(src), out._ref), "q4_mx_quant")
     return out
 
 
 def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
-    """The values of ``m``, ``[rows, k]`` (or ``[batch, rows, k]``) of ``dtype`` (float32 by default)."""
+    """The values of ``m``, ``[rows, k]`` (or ``[batch, rows, k]``) of ``dtype`` (float32 by default); ``out``: a tensor to
+    write into, apart from m's."""
     torch = _torch()
     m = _mx(m, "m")
     if dtype is None:
@@ -1198,6 +1202,7 @@ def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
         op = out.data_ptr()
     else:
         op = _ptr(out, "out", dtype, shape, m.device)
+        _apart(op, m.batch * m.rows * m.k * out.element_size(), (m._c.dev, m.nbytes))
     _check(_launch(m.device, lib().q4_mx_dequant, m._ref, kind, op), "q4_mx_dequant")
     return out
 

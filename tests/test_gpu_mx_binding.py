@@ -35,3 +35,28 @@ def test_a_given_matrix_keeps_its_format_and_factor(q4):
             q4.q4_mx_quant(2 * x, out=m, **kw)
     assert all(torch.equal(a, b) for a, b in zip(nv.codes(), before))
     q4.q4_device_check()
+
+
+def test_a_quantised_matrix_lies_apart_from_its_rows(q4):
+    # (17408 bytes a matrix of up to 128 rows x 256 columns)
+    buf = torch.zeros(65536, dtype=torch.uint8, device="cuda")
+    x = buf[16384:16384 + 4 * 256 * 4].view(torch.float32).view(4, 256)
+    x.copy_(randn(2, 4, 256))
+    up, gamma = randn(3, 4, 256), torch.ones(256, device="cuda")
+    at = lambda first: q4.MXMatrix(0, 4, 256, tensor=buf[first:first + 17408])  # noqa: E731
+    for first in (0, 1024, 16384, 20464):
+        with pytest.raises(ValueError):
+            q4.q4_mx_quant(x, out=at(first))
+        with pytest.raises(ValueError):
+            q4.q4_mx_quant(up, up=x, out=at(first))
+        with pytest.raises(ValueError):
+            # (the first row ends at 17408, the last one begins at 19456)
+            q4.q4_mx_quant(up, gamma=x[3] if first >= 16384 else x[0], out=at(first))
+    # next to them is fine
+    want = q4.q4_mx_quant(x).codes()
+    m = q4.q4_mx_quant(x, out=at(20480))
+    assert all(torch.equal(a, b) for a, b in zip(m.codes(), want))
+    m = q4.q4_mx_quant(x, gamma=gamma, eps=1e-6, out=q4.MXMatrix(0, 4, 256))
+    with pytest.raises(ValueError):  # nor are values written over the matrix that they are read from
+        q4.q4_mx_dequant(m, out=m.tensor[:4096].view(torch.float32).view(4, 256))
+    q4.q4_device_check()
