@@ -1066,7 +1066,8 @@ class MXMatrix:
     """Matrices of microscaled 4-bit values, ``batch`` of them of ``[rows, k]``, in device memory (owns its
     tensor): E2M1 codes whose blocks of 32 columns share a power of two (``Q4_MX_MXFP4``) or whose blocks of 16
     share an E4M3 factor, with one fp32 factor ``scale`` for all (``Q4_MX_NVFP4``).  ``q4_mx_quant`` and
-    ``from_codes`` make one with its contents; the constructor alone leaves them undefined."""
+    ``from_codes`` make one with its contents, which comes back in as many dimensions as it was made from; the
+    constructor alone leaves them undefined."""
 
     def __init__(self, fmt: int, rows: int, k: int, batch: int = 1, scale: float = 1.0, device="cuda", tensor=None):
         torch = _torch()
@@ -1079,6 +1080,7 @@ class MXMatrix:
         else:
             _dev_buf(tensor, "tensor", torch.uint8, None, tensor.device, min_numel=n)
         self.tensor, self.device = tensor, tensor.device
+        self._lead = (batch,) if batch > 1 else ()  # of its plain shapes; a batch of one: from_codes, q4_mx_quant
         self._c = c = _CMx(fmt, rows, k, batch, tensor.data_ptr(), n, scale)
         self._ref = ctypes.byref(c)
 
@@ -1096,8 +1098,7 @@ class MXMatrix:
         return self._ref
 
     def _plain_shapes(self):
-        lead = (self.batch,) if self.batch > 1 else ()
-        return lead + (self.rows, self.k // 2), lead + (self.rows, self.k // self.block)
+        return self._lead + (self.rows, self.k // 2), self._lead + (self.rows, self.k // self.block)
 
     @classmethod
     def from_codes(cls, codes, scales, fmt: int, scale: float = 1.0) -> "MXMatrix":
@@ -1108,6 +1109,7 @@ class MXMatrix:
             raise TypeError("codes must be a CUDA uint8 tensor [rows, k/2] or [batch, rows, k/2]")
         batch = codes.shape[0] if codes.dim() == 3 else 1
         m = cls(fmt, codes.shape[-2], 2 * codes.shape[-1], batch, scale, codes.device)
+        m._lead = tuple(codes.shape[:-2])
         lead = tuple(codes.shape[:-1])
         cp = _ptr(codes, "codes", torch.uint8, lead + (m.k // 2,), m.device)
         sp = _ptr(scales, "scales", torch.uint8, lead + (m.k // m.block,), m.device)
@@ -1176,6 +1178,8 @@ def q4_mx_quant(x, fmt: int | None = None, gamma=None, eps: float = 0.0, up=None
     rows, k = src.rows // batch, src.k
     if out is None:
         out = MXMatrix(Q4_MX_MXFP4 if fmt is None else fmt, rows, k, batch, 1.0 if scale is None else scale, x.device)
+        if x.dim() == 3:
+            out._lead = (batch,)
     else:
         if (_mx(out, "out").rows, out.k, out.batch, out.device) != (rows, k, batch, x.device):
             raise ValueError("out has another shape or device than x")
@@ -1189,14 +1193,16 @@ def q4_mx_quant(x, fmt: int | None = None, gamma=None, eps: float = 0.0, up=None
 
 
 def q4_mx_dequant(m: MXMatrix, dtype=None, out=None):
-    """The values of ``m``, ``[rows, k]`` (or ``[batch, rows, k]``) of ``dtype`` (float32 by default); ``out``: a tensor to
+    """The values of ``m``, ``[rows, k]`` (a batch: ``[batch, rows, k]``) of ``dtype`` (float32 by default); ``out``: a tensor to
     write into, apart from m's."""
     torch = _torch()
     m = _mx(m, "m")
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     kind = _kind(dtype, "dtype")
-    shape = ((m.batch,) if m.batch > 1 else ()) + (m.rows, m.k)
+    shape = m._lead + (m.rows, m.k)
+    if out is not None and m.batch == 1 and isinstance(out, torch.Tensor):  # with or without a batch's dimension
+        shape = (1,) * (out.dim() - 2) + (m.rows, m.k)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=m.device)
         op = out.data_ptr()

@@ -60,3 +60,28 @@ def test_a_quantised_matrix_lies_apart_from_its_rows(q4):
     with pytest.raises(ValueError):  # nor are values written over the matrix that they are read from
         q4.q4_mx_dequant(m, out=m.tensor[:4096].view(torch.float32).view(4, 256))
     q4.q4_device_check()
+
+
+def test_a_batch_of_one_matrix_is_a_batch(q4):
+    x = randn(4, 1, 40, 96)
+    m = q4.q4_mx_quant(x)
+    assert m.batch == 1 and q4.q4_mx_dequant(m).shape == x.shape
+    c, s = m.codes()
+    assert c.shape == (1, 40, 48) and s.shape == (1, 40, 3)
+    again = q4.MXMatrix.from_codes(c, s, 0)
+    assert all(torch.equal(a, b) for a, b in zip(again.codes(), (c, s)))
+    assert torch.equal(q4.q4_mx_dequant(again, out=torch.empty_like(x)), q4.q4_mx_dequant(m))
+    one = q4.q4_mx_quant(x[0])
+    assert q4.q4_mx_dequant(one).shape == x[0].shape and one.codes()[0].shape == (40, 48)
+    assert torch.equal(q4.q4_mx_dequant(one), q4.q4_mx_dequant(m)[0])
+    # a matrix made for either takes both
+    assert q4.q4_mx_quant(x, out=one) is one and q4.q4_mx_quant(x[0], out=m) is m
+    two = q4.MXMatrix(0, 40, 96, batch=2)
+    assert q4.q4_mx_dequant(q4.q4_mx_quant(x.expand(2, 40, 96).contiguous(), out=two)).shape == (2, 40, 96)
+    assert q4.q4_mx_dequant(q4.MXMatrix(0, 40, 96)).shape == (40, 96)
+    # a single matrix in a product, and a layer of one expert
+    w = q4.q4_mx_quant(randn(5, 1, 64, 96))
+    assert torch.equal(q4.q4_mx_gemm(w, x[0]), q4.q4_mx_gemm(q4.q4_mx_quant(q4.q4_mx_dequant(w)[0]), x[0]))
+    up, down = (q4.q4_mx_quant(randn(i, 1, a, b)) for i, a, b in ((6, 64, 96), (7, 96, 64)))
+    assert q4.q4_moe(x[0, :2], q4.MoELayer(torch.ones(1, 96, device="cuda"), w, up, down, top_k=1))[0].shape == (2, 96)
+    q4.q4_device_check()
