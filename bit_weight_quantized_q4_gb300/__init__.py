@@ -1062,6 +1062,13 @@ def _mx_bytes(fmt, rows, k):
     return (rows + 127) // 128 * ((k + 255) // 256) * (17408 + 1024 * fmt)
 
 
+def _mx_factor(fmt, scale):
+    """NVFP4's factor of a whole matrix (2^-60 .. 2^60), or MXFP4's 1; else raises."""
+    if not (2.0 ** -60 <= scale <= 2.0 ** 60 if fmt == Q4_MX_NVFP4 else scale == 1.0):
+        raise ValueError("scale=%s: NVFP4 takes 2^-60 .. 2^60, MXFP4 1" % scale)
+    return scale
+
+
 class MXMatrix:
     """Matrices of microscaled 4-bit values, ``batch`` of them of ``[rows, k]``, in device memory (owns its
     tensor): E2M1 codes whose blocks of 32 columns share a power of two (``Q4_MX_MXFP4``) or whose blocks of 16
@@ -1073,8 +1080,8 @@ class MXMatrix:
         torch = _torch()
         if batch < 1:
             raise ValueError("a batch of %s matrices" % batch)
-        self.fmt, self.rows, self.k, self.batch, self.scale = fmt, rows, k, batch, scale
         self.nbytes = n = _mx_bytes(fmt, rows, k) * batch
+        self.fmt, self.rows, self.k, self.batch, self.scale = fmt, rows, k, batch, _mx_factor(fmt, scale)
         if tensor is None:
             tensor = torch.empty(n, dtype=torch.uint8, device=device)
         else:
@@ -1267,7 +1274,7 @@ def q4_mx_gemm(W: MXMatrix, x, r=None, gamma=None, eps: float = 0.0, up=None, sc
     room = _mx_bytes(W.fmt, nb, k)
     if workspace is None:
         workspace = torch.empty(room, dtype=torch.uint8, device=dev)
-    X = _CMx(W.fmt, nb, k, 1, _room_ptr(workspace, room, dev), room, scale)
+    X = _CMx(W.fmt, nb, k, 1, _room_ptr(workspace, room, dev), room, _mx_factor(W.fmt, scale))
     _check(_launch(dev, lib().q4_mx_linear, W._ref, ctypes.byref(src), ctypes.byref(X), rp, kind, op), "q4_mx_linear")
     return out
 

@@ -85,3 +85,21 @@ def test_a_batch_of_one_matrix_is_a_batch(q4):
     up, down = (q4.q4_mx_quant(randn(i, 1, a, b)) for i, a, b in ((6, 64, 96), (7, 96, 64)))
     assert q4.q4_moe(x[0, :2], q4.MoELayer(torch.ones(1, 96, device="cuda"), w, up, down, top_k=1))[0].shape == (2, 96)
     q4.q4_device_check()
+
+
+def test_factors_that_a_format_does_not_take_are_named(q4):
+    x = randn(8, 4, 96)
+    W = q4.q4_mx_quant(x)
+    V = q4.q4_mx_quant(x, 1)
+    c, s = W.codes()
+    cn, sn = V.codes()
+    for bad in (lambda: q4.MXMatrix(0, 4, 96, scale=2.0), lambda: q4.q4_mx_quant(x, scale=2.0), lambda: q4.MXMatrix.from_codes(c, s, 0, 0.5),
+                lambda: q4.q4_mx_gemm(W, x, scale=2.0), lambda: q4.q4_mx_quant(x, 1, scale=0.0), lambda: q4.q4_mx_quant(x, 1, scale=-1.0),
+                lambda: q4.q4_mx_quant(x, 1, scale=float("nan")), lambda: q4.q4_mx_gemm(V, x, scale=2.0 ** 61),
+                lambda: q4.MXMatrix.from_codes(cn, sn, 1, float("inf"))):
+        with pytest.raises(ValueError, match="scale"):
+            bad()
+    for ok in (2.0 ** -60, 1.0, 2.0 ** 60):
+        q4.q4_mx_quant(x, 1, scale=ok)
+        q4.q4_mx_gemm(V, x, scale=ok)
+    q4.q4_device_check()
