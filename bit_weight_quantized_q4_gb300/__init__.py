@@ -1313,9 +1313,11 @@ class MoELayer:
         return self._ref
 
     def workspace_bytes(self, rows: int) -> int:
-        """Workspace bytes of ``q4_moe`` with ``rows`` tokens."""
+        """Workspace bytes of ``q4_moe`` with ``rows`` tokens, 1 to 16."""
         n = self._ws.get(rows)  # by the shapes alone
         if n is None:
+            if not 1 <= rows <= MAX_NB:
+                raise ValueError("q4_moe takes 1 to %d tokens, not %s" % (MAX_NB, rows))
             n = self._ws[rows] = int(lib().q4_moe_workspace_bytes(self._ref, rows))
         return n
 
@@ -1330,7 +1332,7 @@ def q4_moe_workspace(layer: MoELayer, rows: int):
     """A workspace for ``q4_moe`` with up to ``rows`` tokens; calls that may run at the same time, captured ones too,
     need one each."""
     n = _moe(layer).workspace_bytes(int(rows))
-    return _torch().empty(max(16, n), dtype=_torch().uint8, device=layer.device)
+    return _torch().empty(n, dtype=_torch().uint8, device=layer.device)
 
 
 def q4_moe(x, layer: MoELayer, gamma=None, eps: float = 0.0, r=None, positions=None, dtype=None, out=None,

@@ -103,3 +103,14 @@ def test_factors_that_a_format_does_not_take_are_named(q4):
         q4.q4_mx_quant(x, 1, scale=ok)
         q4.q4_mx_gemm(V, x, scale=ok)
     q4.q4_device_check()
+
+
+def test_workspaces_of_token_counts_that_a_layer_refuses(q4):
+    mats = [q4.q4_mx_quant(randn(i, 4, a, b)) for i, (a, b) in enumerate(((64, 96), (64, 96), (96, 64)))]
+    layer = q4.MoELayer(torch.ones(4, 96, device="cuda"), *mats, top_k=2)
+    for rows in (0, -1, 17, 1000):
+        with pytest.raises(ValueError):
+            q4.q4_moe_workspace(layer, rows)
+        with pytest.raises(ValueError):
+            layer.workspace_bytes(rows)
+    assert q4.q4_moe_workspace(layer, 16).numel() == layer.workspace_bytes(16) > layer.workspace_bytes(1) > 0
