@@ -1,5 +1,5 @@
 """Microscaled 4-bit matrices on the GPU at their edges: zeros, subnormal numbers, infinities and NaN behind a norm and a
-SwiGLU and in rows that the product quantises."""
+SwiGLU and in rows that the product quantises; NVFP4's reciprocals; and results that are rounded once."""
 import pytest
 
 import mx_ref
@@ -175,4 +175,71 @@ def test_the_product_of_rows_with_zeros_infinities_and_nan(q4, nb, n, k, dtype, 
         odd = torch.tensor([t for t in range(nb - 1) if t % 2 and kinds[t // 2 % 4] != 0.0], dtype=torch.long, device="cuda")
         assert bool(torch.isnan(y[odd]).all())
         assert bool((y[nb - 1] == 0).all())
+    q4.q4_device_check()
+
+
+# ------------------------------------------------------------------ NVFP4's factors
+
+def test_reciprocals_are_the_nearest_ones(q4):
+    # x (1 / (s g)) next to a border: a factor g whose products with every scale have all kinds of significands, those of
+    # ones alone among them, where Newton's step ends at a tie
+    ones = [2.0 - 2.0 ** -23, (2.0 - 2.0 ** -23) * 2.0 ** -7, (2.0 - 2.0 ** -22), 1.0 + 2.0 ** -23]
+    g = gen(3)
+    some = (1.0 + torch.randint(0, 1 << 23, (60,), generator=g, device="cuda").double() / (1 << 23)).tolist()
+    borders = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    for scale in ones + some:
+        gf = torch.tensor(scale, device="cuda", dtype=F32)
+        e = torch.arange(1, 127, device="cuda").to(torch.uint8).view(torch.float8_e4m3fn).float()
+        sg = e * gf
+        # the largest value gives the scale; the others are the fp32 numbers around every border
+        b = borders[None] * sg[:, None]
+        near = (b.view(torch.int32)[:, :, None] + torch.tensor([-2, -1, 0, 1, 2], device="cuda", dtype=torch.int32)).view(F32)
+        near = near.flatten(1)  # 35 for each scale
+        x = torch.zeros(126, 48, device="cuda")
+        x[:, 1:16], x[:, 17:32], x[:, 33:38] = near[:, :15], near[:, 15:30], near[:, 30:]
+        x[:, ::16] = 6.0 * sg[:, None]
+        x = torch.nn.functional.pad(x, (0, 16))
+        m = q4.q4_mx_quant(x, 1, scale=scale)
+        c, s = m.codes()
+        assert torch.equal(s[:, :3].long(), torch.arange(1, 127, device="cuda")[:, None].expand(126, 3))
+        assert torch.equal(mx_ref.stored(c, s, 1, float(gf)), mx_ref.quantise(x, 1, scale))
+    q4.q4_device_check()
+
+
+# ------------------------------------------------------------------ results
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("nb,n", [(1, 515), (1, 20000), (7, 515), (40, 515), (64, 20000), (300, 515), (300, 516), (1000, 130)])
+def test_results_are_rounded_once(q4, nb, n, dtype, fmt):
+    # scales of one, sums of quarters below 2^15 and residuals of eighths: fp32 numbers, so that the output's rounding is
+    # the only one
+    g = gen(nb + n)
+    k = 2080
+    one = 127 if fmt == 0 else 56
+    wc, xc = (torch.randint(0, 256, (rows, k // 2), generator=g, device="cuda", dtype=torch.uint8) for rows in (n, nb))
+    ws, xs = (torch.full((rows, k // mx_ref.BLOCK[fmt]), one, device="cuda", dtype=torch.uint8) for rows in (n, nb))
+    W, X = q4.MXMatrix.from_codes(wc, ws, fmt), q4.MXMatrix.from_codes(xc, xs, fmt)
+    total = mx_ref.stored(xc, xs, fmt) @ mx_ref.stored(wc, ws, fmt).T
+    assert float(total.abs().max()) < 2 ** 15
+    assert torch.equal(q4.q4_mx_gemm(W, X, dtype=dtype), total.float().to(dtype))
+    r = (torch.randint(-64, 65, (nb, n), generator=g, device="cuda").double() / 8)
+    want = (total + r).float().to(dtype)
+    r = r.to(dtype)
+    assert torch.equal(q4.q4_mx_gemm(W, X, r=r, dtype=dtype), want)
+    assert torch.equal(q4.q4_mx_gemm(W, X, r=r, out=r), want)
+    q4.q4_device_check()
+
+
+def test_a_layers_results_are_rounded_once(q4):
+    g = gen(2)
+    mats = [q4.q4_mx_quant(randn(g, 8, a, b) * b ** -0.5) for a, b in ((160, 256), (160, 256), (256, 160))]
+    layer = q4.MoELayer(randn(g, 8, 256) / 16, *mats, top_k=2)
+    for rows in (1, 5, 16):
+        for dtype in (F16, BF16):
+            x, r = randn(g, rows, 256).to(dtype), randn(g, rows, 256).to(dtype)
+            for res in (None, r):
+                fine = q4.q4_moe(x, layer, r=None if res is None else res.float(), dtype=F32)
+                coarse = q4.q4_moe(x, layer, r=res)
+                assert torch.equal(coarse[0], fine[0].to(dtype)) and torch.equal(coarse[1], fine[1])
     q4.q4_device_check()
