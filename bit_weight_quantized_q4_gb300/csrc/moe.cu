@@ -8,10 +8,12 @@
 // core an instruction takes 16 columns at least, so every expert sees all tokens
 // of the batch, and only a token's own experts' columns are used: nothing is
 // gathered.
-//   One token, 8 of 128 experts of 768 x 2048: 16.2 us for 21 MB (floor 3.1); sixteen: 49 for
-// 208 MB (30.7); four tokens, 2 of 8 experts of 14336 x 4096: 81 for 0.49 GB (72.5); sixteen:
-// 121.5 (107).  The fixed part is a chain of latencies: the logits' kernel 4 us, the
-// choice 2.4, the grid's barrier 1.2, the first copies of each half, joining 2.
+//   One token, 8 of 128 experts of 768 x 2048: 16.2 to 17.7 us over machines for 21 MB (floor
+// 3.1); sixteen, which reach 83 experts: 49 to 50 for 208 MB (30.7); four tokens, 2 of 8 experts
+// of 14336 x 4096, which reach five: 82 for 0.47 GB (69.0); sixteen, which reach all: 123 for
+// 0.75 GB (110.4).  The fixed part is a chain of latencies: the logits' kernel 4 us, the choice
+// 2.4, the grid's barrier 1.2, the first copies of each half, joining 2.  (One token's first half
+// is 96 units: 56 SMs have none.)
 #include <algorithm>
 
 #include "mx_common.cuh"
@@ -697,7 +699,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) q4moe_experts_kernel(const __g
     }
 }
 
-// Sixteen bytes of codes, or a word of scales, of a row a thread.
+// Sixteen bytes of codes, or a word of scales, of a row a thread.  When a layer is made: 128
+// experts of 768 x 2048 149 us (2.9 TB/s read and written).
 __global__ void __launch_bounds__(256) q4moe_pack_kernel(const __grid_constant__ MoePackParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

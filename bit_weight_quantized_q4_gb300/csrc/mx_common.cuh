@@ -83,8 +83,9 @@ __device__ __forceinline__ float max_abs(float a, float b) {
     asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
     return m;
 }
-// silu(g), g / (1 + exp(-g)), to a few units in the last place; -inf: NaN, as the
-// formula has it.
+// silu(g), g / (1 + exp(-g)): off by about 4 + 1.17 |g| units in the last place (the fast
+// exponential by 2 + 1.17 |g|, the fast quotient by 2), 27 of them at g = -20; zero below -87.3,
+// where the denominator passes 2^126 (the value: -1e-36); -inf: NaN, as the formula has it.
 __device__ __forceinline__ float mx_silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 // NVFP4's factor g of the whole matrix, 6 g, and 1 / (6 g) to the nearest fp32.
@@ -98,9 +99,10 @@ struct MxGain {
 //   NVFP4: |a| / (6 g) to the nearest E4M3, 448 at most.  The quotient is the nearest
 //   fp32 one, by Markstein's method (IBM J. Res. Dev. 34, 1990): from the nearest 1 / b,
 //   q + (a - q b) (1 / b) with an exact remainder is the nearest fp32 to a / b once q is
-//   within a unit in the last place of it, which one such step ensures; likewise 1 /
-//   (s g) from the hardware's estimate.  (Divisions of the language took as long as the
-//   rest of the kernel.)
+//   within a unit in the last place of it, which one such step ensures.  1 / (s g): one
+//   such step from the hardware's estimate, which is within a unit already; the method
+//   leaves out significands of ones alone, and values beside every border of codes are tested
+//   with those too.  (Divisions of the language took as long as the rest of the kernel.)
 // A block with an infinity or NaN: a NaN scale, and a factor of 0: its codes are zeros.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_block_scale(float a, const MxGain &gain, float &mul) {

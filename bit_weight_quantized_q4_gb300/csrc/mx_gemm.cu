@@ -11,8 +11,9 @@
 //   warp 0 copies, warp 1 issues MMAs, warps 2-5 write the results, while the
 //   tensor core is at the next tile (two accumulators).
 // The weights' stream bounds it: one row at 65536 x 8192 takes 42.9 us (6.7 TB/s), 64 rows
-// 47; at 14336 x 4096 one row 7.8 (4.0 TB/s: a launch, 16 stages a CTA and the first copies'
-// latency are half of it), at 4096 x 14336 8.8, at 4096 x 4096 4.8.
+// 47; at 14336 x 4096 one row 7.8 (4.0 TB/s: 112 row tiles are 112 CTAs, so that 40 SMs have no
+// part, and an SM draws 44 GB/s; a launch and the first copies' latency), at 4096 x 14336 8.8,
+// at 4096 x 4096 4.8.
 // A few rows that are not quantised yet are quantised here (QX): warps 6-9 write
 // their codes and scales into the stages, while w's records arrive.
 #include <algorithm>
@@ -389,8 +390,8 @@ int mx_gemm_plan(MxGemmParams &p, int fmt, int sms) {
     if (p.nb <= dev::kMxgMaxN) {
         p.NB = (p.nb + 15) / 16 * 16;
         for (int C = 1; C <= 8 && C <= p.KS; ++C) {
-            // (Clusters have to find their SMs in one part of the GPU: of 152 SMs 15 clusters of
-            // eight ran at once, not 16, 23 of six, not 25, 32 of four.)
+            // (Clusters have to find their SMs in one part of the GPU: with a CTA an SM 15 of eight
+            // or seven can run at once, 23 of six, 28 of five, 36 of four, 46 of three.)
             if (C > 1 && 8 * p.MT * C > (C > 4 ? 6 : 7) * sms) break;
             const double stages = (double)((p.MT * C + sms - 1) / sms) * ((p.KS + C - 1) / C);
             const double cost = 3000.0 + 245.0 * stages + 150.0 * std::min(stages, 4.0) +

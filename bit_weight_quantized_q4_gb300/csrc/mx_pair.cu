@@ -2,20 +2,21 @@
 // SMs works on one tile (tcgen05 cta_group::2), 256 rows of w by 192 of x.
 //
 // A stage (256 of k) of a 128 x 192 tile is 44 KB that one SM has to bring from L2 and
-// read from shared memory for 364 cycles of tensor work; the pair shares x's rows, so
+// read from shared memory for 355 cycles of tensor work; the pair shares x's rows, so
 // that each SM brings and reads 31 KB for as much.  Each CTA holds its half of w's rows
 // and of x's; the first CTA of the pair issues the MMAs, whose completion is signalled in
 // both.  x's scales are in both CTAs, of all columns: each tensor core needs them.  (Four
 // warps of each CTA that wrote the scales to tensor memory, instead of the copies that
 // the first CTA issues for both, took 0.8 us a stage.)
 //
-// What bounds it: a stage takes 430 cycles, 355 of them MMAs; the rest are the copies of
-// the scales in front of each stage's MMAs (NVFP4 has twice as many) and stages that are not
-// there yet: an SM draws 74 bytes a cycle from L2.  The results' stores and loads come on
-// top.  8191 x 4096 x 14336 MXFP4 125 us (7.7 PFLOP/s), 8192^3 146 (7.5), NVFP4 162 (6.8);
-// 4096 x 14336 x 4096 NVFP4 81 (5.9), with a residual 92.  (Scales copied a stage ahead, or
-// two stages waited for together: a tenth slower; narrower tiles: w's records take as long
-// to arrive.)
+// What bounds it: a stage takes 430 cycles, 355 of them MMAs (of K = 64); the rest are the
+// copies of the scales in front of each stage's MMAs (NVFP4 has twice as many) and stages that are
+// not there yet: 74 bytes a cycle reach an SM from L2, whose queues are at 60 % on average.
+// The results' stores and loads come on top.  8191 x 4096 x 14336 MXFP4 125 us (7.7 PFLOP/s;
+// to 135 on other machines and clocks), 8192^3 146 (7.5; to 155), NVFP4 162 (6.8; to 171); 4096 x
+// 14336 x 4096 NVFP4 81 (5.9; to 92), with a residual 92 (to 97).  (Scales copied a stage ahead,
+// or two stages waited for together: a tenth slower; narrower tiles: w's records take as long to
+// arrive.)
 //
 //   warps 0, 10 and 11 copy, warp 1 issues MMAs (first CTA) or tells the first CTA of stages
 //   that have landed (second), warps 2-9 write the results (half of the columns each four).

@@ -4,8 +4,9 @@
 //
 // Pure streams: HBM bounds the float forms, the arithmetic of scales and codes the 16-bit
 // ones.  14336 x 4096 float 39.7 us (6.7 TB/s), bf16 26.2 (5.6); 8191 x 4096 bf16 behind a
-// norm 19.1 (4.5); 8191 x 14336 fp16 SwiGLU 82.9 (6.4); back into bf16, 14336 x 4096, 24.3
-// (6.1).
+// norm 19.4 (4.4); 8191 x 14336 fp16 SwiGLU 82.9 (6.4); back into bf16, 14336 x 4096, 24.3
+// (6.1).  When a model is loaded: codes and scales of 14336 x 4096 from plain rows 27.6 (2.3
+// TB/s: a record's rows in words of 4 bytes a lane, its scales in single bytes), into them 29.8.
 // A lane takes sixteen consecutive values, half a record row a half warp: a block of 32
 // (16) is two lanes (one), a row's codes of a record one whole 128-byte line.  (Eight values
 // a lane: half the time of the 16-bit forms was the arithmetic of scales and addresses.)
@@ -89,10 +90,10 @@ __global__ void __launch_bounds__(kMxThreads) q4mx_quant_kernel(const __grid_con
 // Behind an RMSNorm: WPR warps a row, which keep up to R sixteens a lane of it in
 // registers (what a longer row has beyond is read again once its sum of squares is
 // known).  As many CTAs as are resident take every grid-th rows each, the loads of the
-// next DP rows under way.  Its arithmetic bounds it, not the memory: 8191 x 4096 bf16
-// takes 19 us with four warps a row and two CTAs of an SM (three, whose registers spill:
-// 25); with eight, three CTAs and two rows under way 21.5 (a CTA a row: 30; more CTAs than
-// are resident: 25; four, which spill: 26).
+// next DP rows under way.  Its arithmetic and the latencies that 16 warps leave uncovered bound
+// it, not the memory: 8191 x 4096 bf16 takes 19 us with four warps a row and two CTAs of an
+// SM (three, whose registers spill: 26); with eight, three CTAs and two rows under way 22 (a
+// CTA a row: 30; more CTAs than are resident: 25; four, which spill: 26).
 template <int R>
 constexpr int mx_norm_ctas() { return R == 1 ? 3 : 2; }
 template <typename T, int FMT, int WPR, int R>
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kMxThreads, mx_norm_ctas<R>()) q4mx_quant_norm
     }
 }
 
-// Back into values: g s e, rounded once to T.  A warp a record's row, eight values a
+// Back into values: g s e in fp32, rounded to T.  A warp a record's row, eight values a
 // lane: its stores are whole lines (sixteen a lane: 16 -> 19 us for 8191 x 4096).
 constexpr int kMxAhead = 4;  // units (row, column tile) of a warp
 template <typename T, int FMT>
@@ -316,8 +317,8 @@ int launch_mx_quant_t(const MxQuantParams &p, int sms, cudaStream_t stream) {
     if (p.gamma) {
         // as many warps a row as it has 512s, up to eight; from about a round of the SMs on and for
         // 16-bit types half as many, of whose work a row's sum is a smaller part (us, 4096 columns of
-        // bf16, eight warps / four: 152 rows 2.3 / 2.6, 304 3.0 / 2.8, 8191 21.5 / 19.1; float
-        // 26.0 / 26.6)
+        // bf16, eight warps / four: 152 rows 2.1 / 2.4, 304 3.0 / 2.7, 8191 21.9 / 18.8; float
+        // 26.3 / 26.8)
         if (p.k <= 512) return launch_mx_norm<T, FMT, 1, 1>(p, sms, stream);
         if constexpr (sizeof(T) == 2) {
             if ((long long)p.batch * p.rows * p.k >= 1 << 20) {

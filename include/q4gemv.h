@@ -594,7 +594,8 @@ typedef struct {
  * (the order of a row's sum does). */
 q4_status q4_mx_quant(const q4_mx_src *src, const q4_mx *out, cudaStream_t stream);
 
-/* The values of m, [batch][rows][k] of dtype (rounded once to it). */
+/* The values of m, [batch][rows][k] of dtype (code, scale and factor multiplied in fp32,
+ * the product rounded to dtype). */
 q4_status q4_mx_dequant(const q4_mx *m, int32_t dtype, void *out, cudaStream_t stream);
 
 /* Codes and scales in plain rows, device to device: codes [batch][rows][k / 2],
